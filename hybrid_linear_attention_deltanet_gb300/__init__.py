@@ -13,6 +13,9 @@ raise when the compiled library is missing.
     x = prepare(qkv, conv_w, a_raw, b_raw, A_log, dt_bias, heads)   # -> q, k, v, alpha, beta
     y = output_norm_gate(out, g, w)                     # Eq. 20 read-out
     y = decode_layer_step(qkv, conv_w, a_raw, b_raw, A_log, dt_bias, conv_state, S, g, w)
+    q, scale, s = residual_norm_fp8(x, w, residual)      # the layer around the mixer:
+    out = linear_fp8(q, scale, wq, w_scale)              # 8-bit projections,
+    h = gated_ffn(x, w_gate, w_up)                       # gated feed-forward
 
 Recurrence (Appendix A.3, Eq. 16-19 of "Long-Context Aware Upcycling"):
 S_t = alpha_t S_{t-1}(I - beta_t k_t k_t^T) + beta_t v_t k_t^T,
@@ -99,6 +102,31 @@ def load():
     lib.gdn_prefill_layer.argtypes = [vp] * 12 + [ctypes.c_float, i32, vp, vp, i32, i64, i32,
                                                   i32, i32, i32, vp]
     lib.gdn_prefill_layer.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.gdn_residual_norm.argtypes = [vp, vp, vp, f32, vp, vp, i64, i32, i32, vp]
+    lib.gdn_residual_norm.restype = ctypes.c_int
+    lib.gdn_residual_norm_fp8.argtypes = [vp, vp, vp, f32, vp, vp, vp, i64, i32, i32, vp]
+    lib.gdn_residual_norm_fp8.restype = ctypes.c_int
+    lib.gdn_residual_norm_backward.argtypes = [vp] * 4 + [f32, vp, vp, i64, i32, i32, vp]
+    lib.gdn_residual_norm_backward.restype = ctypes.c_int
+    lib.gdn_residual_norm_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.gdn_residual_norm_backward_workspace_size.restype = sz
+    lib.gdn_residual_norm_backward_ws.argtypes = [vp] * 4 + [f32, vp, vp, i64, i32, i32, vp, sz,
+                                                             vp]
+    lib.gdn_residual_norm_backward_ws.restype = ctypes.c_int
+    lib.gdn_quantize_fp8.argtypes = [vp, vp, vp, i64, i32, i32, i32, vp]
+    lib.gdn_quantize_fp8.restype = ctypes.c_int
+    lib.gdn_linear_fp8.argtypes = [vp] * 5 + [i64, i32, i32, i32, vp]
+    lib.gdn_linear_fp8.restype = ctypes.c_int
+    lib.gdn_gated_ffn.argtypes = [vp, vp, vp, i32, vp, i64, i32, i32, i32, vp]
+    lib.gdn_gated_ffn.restype = ctypes.c_int
+    lib.gdn_gated_ffn_backward.argtypes = [vp] * 4 + [i32, vp, vp, vp, i64, i32, i32, i32, vp]
+    lib.gdn_gated_ffn_backward.restype = ctypes.c_int
+    lib.gdn_gated_ffn_backward_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.gdn_gated_ffn_backward_workspace_size.restype = sz
+    lib.gdn_gated_ffn_backward_ws.argtypes = [vp] * 4 + [i32, vp, vp, vp, i64, i32, i32, i32, vp,
+                                                         sz, vp]
+    lib.gdn_gated_ffn_backward_ws.restype = ctypes.c_int
     lib.gdn_release_scratch.restype = ctypes.c_int
     lib.gdn_testing_scratch_reserved.argtypes = [vp]
     lib.gdn_testing_scratch_reserved.restype = ctypes.c_int
@@ -588,6 +616,242 @@ def prefill_layer(qkv, conv_w, a_raw, b_raw, A_log, dt_bias, gate, norm_w, heads
     if rc != 0:
         raise GDNError("gdn_prefill_layer", rc)
     return y, S_final
+
+
+# ---------------------------------------------------------------------------
+# The layer around the mixer: residual norm, 8-bit projections, feed-forward.
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def _check_out(t, name, shape, dtype, device):
+    """The caller's output tensor (checked), or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t
+
+
+def _norm_inputs(x, w, residual, s):
+    dev, io = x.device, x.dtype
+    _io_code(io)
+    _check(x, "x", io, dev)
+    if x.dim() < 1:
+        raise ValueError("x must be [.., dim]")
+    _check(w, "w", torch.float32, dev)
+    if tuple(w.shape) != (x.shape[-1],):
+        raise ValueError(f"w must be [{x.shape[-1]}]")
+    if residual is None:
+        if s is not None:
+            raise ValueError("s goes with a residual (without one the sum is x)")
+        return None
+    _check(residual, "residual", io, dev)
+    if residual.shape != x.shape:
+        raise ValueError("residual must be shaped like x")
+    return _check_out(s, "s", x.shape, io, dev)
+
+
+def residual_norm(x, w, residual=None, eps=1e-5, s=None, y=None, stream=None):
+    """Residual addition and root-mean-square norm (``gdn_residual_norm``):
+    s = x + residual (rounded to their dtype), y = s / sqrt(mean(s^2) + eps) * w
+    over the last axis.  x, residual [.., dim] bf16 or fp32; w [dim] fp32.
+    Returns (y, s); s is x itself without a residual.  ``s=residual`` updates
+    the residual stream in place."""
+    lib = load()
+    s_out = _norm_inputs(x, w, residual, s)
+    y = _check_out(y, "y", x.shape, x.dtype, x.device)
+    dim = x.shape[-1]
+    with torch.cuda.device(x.device):
+        rc = lib.gdn_residual_norm(_ptr(x), _ptr(residual), _ptr(w), float(eps), _ptr(s_out),
+                                   _ptr(y), x.numel() // max(dim, 1), dim, _io_code(x.dtype),
+                                   _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_residual_norm", rc)
+    return y, x if s_out is None else s_out
+
+
+def residual_norm_fp8(x, w, residual=None, eps=1e-5, s=None, q=None, scale=None, stream=None):
+    """:func:`residual_norm` with y in 8 bits (``gdn_residual_norm_fp8``).
+    Returns (q, scale, s): q [.., dim] float8_e4m3fn and scale
+    [.., ceil(dim / 128)] fp32, y ~ q * scale per 128 columns, as
+    :func:`linear_fp8` reads them."""
+    lib = load()
+    s_out = _norm_inputs(x, w, residual, s)
+    dim = x.shape[-1]
+    q = _check_out(q, "q", x.shape, FP8, x.device)
+    scale = _check_out(scale, "scale", tuple(x.shape[:-1]) + (_blocks(dim),), torch.float32,
+                       x.device)
+    with torch.cuda.device(x.device):
+        rc = lib.gdn_residual_norm_fp8(_ptr(x), _ptr(residual), _ptr(w), float(eps), _ptr(s_out),
+                                       _ptr(q), _ptr(scale), x.numel() // max(dim, 1), dim,
+                                       _io_code(x.dtype), _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_residual_norm_fp8", rc)
+    return q, scale, x if s_out is None else s_out
+
+
+def residual_norm_backward_workspace_size(tokens, dim, io_dtype=torch.bfloat16) -> int:
+    n = load().gdn_residual_norm_backward_workspace_size(tokens, dim, _io_code(io_dtype))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported residual_norm_backward arguments")
+    return int(n)
+
+
+def residual_norm_backward(dy, s, w, ds=None, eps=1e-5, stream=None, workspace=None):
+    """Gradients of :func:`residual_norm` (``gdn_residual_norm_backward``): dy
+    [.., dim] of y, ds of s from its other uses (or None), s as the forward
+    call returned it.  Returns dict dx (the gradient of x and of residual
+    alike, dtype of s) and dw [dim] fp32."""
+    lib = load()
+    dev, io = s.device, s.dtype
+    _io_code(io)
+    for name, t in (("s", s), ("dy", dy), ("ds", ds)):
+        if t is not None:
+            _check(t, name, io, dev)
+            if t.shape != s.shape:
+                raise ValueError(f"{name} must be shaped like s")
+        elif name != "ds":
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if s.dim() < 1:
+        raise ValueError("s must be [.., dim]")
+    _check(w, "w", torch.float32, dev)
+    dim = s.shape[-1]
+    if tuple(w.shape) != (dim,):
+        raise ValueError(f"w must be [{dim}]")
+    g = dict(dx=torch.empty_like(s), dw=torch.empty_like(w))
+    with torch.cuda.device(dev):
+        args = (_ptr(dy), _ptr(s), _ptr(w), _ptr(ds), float(eps), _ptr(g["dx"]), _ptr(g["dw"]),
+                s.numel() // max(dim, 1), dim, _io_code(io))
+        if workspace is None:
+            rc = lib.gdn_residual_norm_backward(*args, _stream_handle(stream))
+        else:
+            rc = lib.gdn_residual_norm_backward_ws(*args, *_ws_args(workspace),
+                                                   _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_residual_norm_backward", rc)
+    return g
+
+
+def quantize_fp8(x, block_rows=1, q=None, scale=None, stream=None):
+    """x [.., cols] (bf16 or fp32) as e4m3 values with block scales
+    (``gdn_quantize_fp8``): 1 x 128 blocks for activations, with
+    ``block_rows=128`` 128 x 128 blocks for a weight [n, k].  Returns
+    (q, scale)."""
+    lib = load()
+    _io_code(x.dtype)
+    _check(x, "x", x.dtype, x.device)
+    if x.dim() < 1 or (block_rows != 1 and x.dim() != 2):
+        raise ValueError("x must be [.., cols] (a weight [n, k] with block_rows=128)")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    cols = x.shape[-1]
+    rows = x.numel() // max(cols, 1)
+    lead = tuple(x.shape[:-1]) if block_rows == 1 else (_blocks(rows),)
+    q = _check_out(q, "q", x.shape, FP8, x.device)
+    scale = _check_out(scale, "scale", lead + (_blocks(cols),), torch.float32, x.device)
+    with torch.cuda.device(x.device):
+        rc = lib.gdn_quantize_fp8(_ptr(x), _ptr(q), _ptr(scale), rows, cols, block_rows,
+                                  _io_code(x.dtype), _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_quantize_fp8", rc)
+    return q, scale
+
+
+def linear_fp8(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, stream=None):
+    """out = x w^T of 8-bit operands with block scales (``gdn_linear_fp8``):
+    x [.., k] float8_e4m3fn with x_scale [.., ceil(k / 128)], w [n, k] with
+    w_scale [ceil(n / 128), ceil(k / 128)] (as :func:`residual_norm_fp8` and
+    :func:`quantize_fp8` give them).  Returns out [.., n] in ``out_dtype``
+    (bf16 or fp32)."""
+    lib = load()
+    dev = x.device
+    _io_code(out_dtype)
+    _check(x, "x", FP8, dev)
+    _check(w, "w", FP8, dev)
+    _check(x_scale, "x_scale", torch.float32, dev)
+    _check(w_scale, "w_scale", torch.float32, dev)
+    if x.dim() < 1 or w.dim() != 2 or w.shape[1] != x.shape[-1]:
+        raise ValueError("x must be [.., k] and w [n, k]")
+    n, k = w.shape
+    lead = tuple(x.shape[:-1])
+    if tuple(x_scale.shape) != lead + (_blocks(k),):
+        raise ValueError(f"x_scale must be {list(lead + (_blocks(k),))}")
+    if tuple(w_scale.shape) != (_blocks(n), _blocks(k)):
+        raise ValueError(f"w_scale must be [{_blocks(n)}, {_blocks(k)}]")
+    out = _check_out(out, "out", lead + (n,), out_dtype, dev)
+    with torch.cuda.device(dev):
+        rc = lib.gdn_linear_fp8(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out),
+                                x.numel() // max(k, 1), k, n, _io_code(out_dtype),
+                                _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_linear_fp8", rc)
+    return out
+
+
+def _ffn_inputs(x, w_gate, w_up, act):
+    dev, io = x.device, x.dtype
+    if io != torch.bfloat16:
+        raise TypeError("the gated feed-forward takes bf16 tensors")
+    if act not in GATE_ACT:
+        raise ValueError(f"act must be one of {sorted(GATE_ACT)}")
+    for name, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up)):
+        _check(t, name, io, dev)
+    if x.dim() < 1 or w_gate.dim() != 2 or w_gate.shape[1] != x.shape[-1] \
+            or w_up.shape != w_gate.shape:
+        raise ValueError("x must be [.., dim], w_gate and w_up [hidden, dim]")
+    hidden, dim = w_gate.shape
+    return x.numel() // max(dim, 1), dim, hidden
+
+
+def gated_ffn(x, w_gate, w_up, act="silu", h=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T) in one kernel (``gdn_gated_ffn``):
+    x [.., dim], w_gate and w_up [hidden, dim], all bf16.  Returns h
+    [.., hidden]."""
+    lib = load()
+    tokens, dim, hidden = _ffn_inputs(x, w_gate, w_up, act)
+    h = _check_out(h, "h", tuple(x.shape[:-1]) + (hidden,), x.dtype, x.device)
+    with torch.cuda.device(x.device):
+        rc = lib.gdn_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), GATE_ACT[act], _ptr(h), tokens,
+                               dim, hidden, GDN_BF16, _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_gated_ffn", rc)
+    return h
+
+
+def gated_ffn_backward_workspace_size(tokens, dim, hidden, io_dtype=torch.bfloat16) -> int:
+    n = load().gdn_gated_ffn_backward_workspace_size(tokens, dim, hidden, _io_code(io_dtype))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported gated_ffn_backward arguments")
+    return int(n)
+
+
+def gated_ffn_backward(x, w_gate, w_up, dh, act="silu", stream=None, workspace=None):
+    """Gradients of :func:`gated_ffn` from its inputs and dh [.., hidden]
+    (``gdn_gated_ffn_backward``).  Returns dict dx, dw_gate, dw_up (bf16)."""
+    lib = load()
+    tokens, dim, hidden = _ffn_inputs(x, w_gate, w_up, act)
+    _check(dh, "dh", x.dtype, x.device)
+    if tuple(dh.shape) != tuple(x.shape[:-1]) + (hidden,):
+        raise ValueError(f"dh must be {list(x.shape[:-1]) + [hidden]}")
+    g = dict(dx=torch.empty_like(x), dw_gate=torch.empty_like(w_gate),
+             dw_up=torch.empty_like(w_up))
+    with torch.cuda.device(x.device):
+        args = (_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(dh), GATE_ACT[act], _ptr(g["dx"]),
+                _ptr(g["dw_gate"]), _ptr(g["dw_up"]), tokens, dim, hidden, GDN_BF16)
+        if workspace is None:
+            rc = lib.gdn_gated_ffn_backward(*args, _stream_handle(stream))
+        else:
+            rc = lib.gdn_gated_ffn_backward_ws(*args, *_ws_args(workspace),
+                                               _stream_handle(stream))
+    if rc != 0:
+        raise GDNError("gdn_gated_ffn_backward", rc)
+    return g
 
 
 def device_status(stream=None) -> int:

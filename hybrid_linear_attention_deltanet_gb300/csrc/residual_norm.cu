@@ -1,0 +1,636 @@
+// The residual addition with its root-mean-square norm, its gradient, and the
+// 8-bit quantisation of rows and weight blocks (contracts: include/gdn.h).
+//
+//   s = round(x + r);  y = s rs w,  rs = 1 / sqrt(mean_j s_j^2 + eps)
+//   8 bits: per row and 128 columns m = max(|y|, 2^-100), scale = m / 448,
+//           q = e4m3(y (448 / m))
+//   gradient: n = s rs, g = dy w:  dx = (g - n mean_j(g_j n_j)) rs + ds,
+//             dw = sum_t dy n
+//
+// All of it is bound by HBM: nothing is read twice and nothing but the results
+// is written.  A row is held in registers by 1, 2, 4 or 8 warps, 8 elements
+// (16 bytes of bf16) a lane and vector, so that every load of a row is in
+// flight before its first use and the 16 lanes of a half warp hold one
+// 128-column block: a block's largest magnitude is four shuffles.
+#include <cuda_fp8.h>
+
+#include "gdn_internal.cuh"
+#include "hostcheck.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace hostcheck;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxDim = 8 * 8 * 256;   // 8 warps x 8 vectors x 256 columns
+constexpr float kTiny = 0x1p-100f;     // the smallest block maximum: its scale stays normal
+constexpr float kE4m3Max = 448.f;
+
+// ------------------------------------------------------- 8 elements of a row
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    a = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = a;
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void round(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void round(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+__device__ __forceinline__ void load_w(const float* w, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// a NaN wins, so that a block with one shows it
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float amax8(const float (&y)[8]) {
+  float m = fabsf(y[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
+  return m;
+}
+// 8 e4m3 codes of y * inv (round to nearest even; NaN keeps a NaN code)
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv)), __NV_SATFINITE,
+        __NV_E4M3);
+    w[i >> 1] |= (uint32_t)c << (16 * (i & 1));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Sum over the kWPR warps that share a row; every thread of the CTA calls it.
+template <int kWPR, int kN>
+__device__ __forceinline__ void row_sum(float (&x)[kN], float (*part)[kN]) {
+  const int warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) x[i] = warp_sum(x[i]);
+  if (kWPR == 1) return;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) part[warp][i] = x[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    float t = 0.f;
+#pragma unroll
+    for (int j = 0; j < kWPR; ++j) t += part[warp / kWPR * kWPR + j][i];
+    x[i] = t;
+  }
+}
+
+struct NormArgs {
+  const void* x; const void* r; const float* w; float eps;
+  void* s; void* y; uint8_t* q; float* scale;
+  int64_t rows; int32_t dim, blocks;   // blocks: ceil(dim / 128)
+};
+
+// x, r, s and y may be the same memory (each thread reads its elements of a
+// row before it writes them), hence no __restrict__.
+template <typename T, int kVPL, int kWPR, bool kFp8>
+__global__ void __launch_bounds__(kThreads) residual_norm_kernel(NormArgs a) {
+  __shared__ float part[kWarps][1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * (kWarps / kWPR) + warp / kWPR;
+  const bool live = row < a.rows;
+  const size_t base = (size_t)(live ? row : 0) * a.dim;
+  auto col = [&](int j) { return ((j * kWPR + warp % kWPR) * 32 + lane) * 8; };
+  Raw<T> s[kVPL], r[kVPL];
+#pragma unroll
+  for (int j = 0; j < kVPL; ++j) {
+    const int c = col(j);
+    s[j].zero();
+    if (live && c < a.dim) s[j].load((const T*)a.x + base + c);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+      const int c = col(j);
+      r[j].zero();
+      if (live && c < a.dim) r[j].load((const T*)a.r + base + c);
+    }
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+      float f[8], g[8];
+      s[j].widen(f);
+      r[j].widen(g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] += g[i];
+      s[j].round(f);
+    }
+  }
+  float ss[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < kVPL; ++j) {
+    float f[8];
+    s[j].widen(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss[0] = fmaf(f[i], f[i], ss[0]);
+  }
+  row_sum<kWPR>(ss, part);
+  const float rs = rsqrtf(ss[0] / (float)a.dim + a.eps);
+#pragma unroll
+  for (int j = 0; j < kVPL; ++j) {
+    const int c = col(j);
+    const bool in = live && c < a.dim;
+    if (a.r && in && a.s) s[j].store((T*)a.s + base + c);
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in) {
+      float w[8];
+      s[j].widen(f);
+      load_w(a.w + c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * rs * w[i];
+    }
+    if (!kFp8) {
+      if (in) {
+        Raw<T> o;
+        o.round(f);
+        o.store((T*)a.y + base + c);
+      }
+    } else {
+      float m = amax8(f);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = max_nan(m, kTiny);
+      if (in) {
+        *reinterpret_cast<uint2*>(a.q + base + c) = codes8(f, __fdiv_rn(kE4m3Max, m));
+        if ((lane & 15) == 0)
+          a.scale[(size_t)row * a.blocks + c / 128] = __fdiv_rn(m, kE4m3Max);
+      }
+    }
+  }
+}
+
+struct NormBwdArgs {
+  const void* dy; const void* s; const float* w; const void* ds; float eps;
+  void* dx; float* part;   // part: [gridDim.x][dim]
+  int64_t rows; int32_t dim;
+};
+
+// dx, and each CTA's part of dw over the rows it visits: the rows are dealt
+// to a fixed grid, so the sums have a fixed order.
+template <typename T, int kVPL, int kWPR>
+__global__ void __launch_bounds__(kThreads) norm_backward_kernel(NormBwdArgs a) {
+  constexpr int kGroups = kWarps / kWPR;
+  __shared__ float part[2][kWarps][2];
+  __shared__ float acc_s[kGroups > 1 ? kVPL * kWPR * 256 : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto col = [&](int j) { return ((j * kWPR + warp % kWPR) * 32 + lane) * 8; };
+  float dw[kVPL][8];
+#pragma unroll
+  for (int j = 0; j < kVPL; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  int flip = 0;   // alternating buffers: one barrier a row
+  for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows;
+       r0 += (int64_t)gridDim.x * kGroups, flip ^= 1) {
+    const int64_t row = r0 + warp / kWPR;
+    const bool live = row < a.rows;
+    const size_t base = (size_t)(live ? row : 0) * a.dim;
+    Raw<T> s[kVPL], dy[kVPL], ds[kVPL];
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+      const int c = col(j);
+      s[j].zero();
+      dy[j].zero();
+      ds[j].zero();
+      if (live && c < a.dim) {
+        s[j].load((const T*)a.s + base + c);
+        dy[j].load((const T*)a.dy + base + c);
+        if (a.ds) ds[j].load((const T*)a.ds + base + c);
+      }
+    }
+    float t[2] = {0.f, 0.f};   // sum s^2, sum g s
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+      const int c = col(j);
+      if (c < a.dim) {
+        float f[8], d[8], w[8];
+        s[j].widen(f);
+        dy[j].widen(d);
+        load_w(a.w + c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          t[0] = fmaf(f[i], f[i], t[0]);
+          t[1] = fmaf(d[i] * w[i], f[i], t[1]);
+        }
+      }
+    }
+    row_sum<kWPR>(t, part[flip]);
+    const float rs = rsqrtf(t[0] / (float)a.dim + a.eps);
+    const float along = t[1] * rs / (float)a.dim;   // mean(g n)
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+      const int c = col(j);
+      if (live && c < a.dim) {
+        float f[8], d[8], w[8], e[8];
+        s[j].widen(f);
+        dy[j].widen(d);
+        ds[j].widen(e);
+        load_w(a.w + c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float n = f[i] * rs;
+          dw[j][i] = fmaf(d[i], n, dw[j][i]);
+          e[i] = fmaf(fmaf(-n, along, d[i] * w[i]), rs, e[i]);
+        }
+        Raw<T> o;
+        o.round(e);
+        o.store((T*)a.dx + base + c);
+      }
+    }
+  }
+  // the row groups' sums, one group after another
+  if (kGroups > 1) {
+    for (int g = 0; g < kGroups; ++g) {
+      if (warp / kWPR == g) {
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float* p = acc_s + col(j) + i;
+            if (g) dw[j][i] += *p;
+            *p = dw[j][i];
+          }
+      }
+      __syncthreads();
+    }
+  }
+  if (warp / kWPR == kGroups - 1) {
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+      const int c = col(j);
+      if (c < a.dim) {
+        Raw<float> o;
+        o.round(dw[j]);
+        o.store(a.part + (size_t)blockIdx.x * a.dim + c);
+      }
+    }
+  }
+}
+
+// dw[c] = sum_b part[b][c], b in order within each of 8 strided runs, then
+// the runs in order.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int n,
+                                                      int dim, float* __restrict__ dw) {
+  __shared__ float sm[8][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float t = 0.f;
+  if (c < dim)
+#pragma unroll 8
+    for (int b = run; b < n; b += 8) t += part[(size_t)b * dim + c];
+  sm[run][lane] = t;
+  __syncthreads();
+  if (run == 0 && c < dim) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += sm[i][lane];
+    dw[c] = t;
+  }
+}
+
+// ------------------------------------------------------------ quantisation
+struct QuantArgs {
+  const void* x; uint8_t* q; float* scale;
+  int64_t rows; int32_t cols, blocks;
+};
+
+// 1 x 128 blocks: a half warp each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
+  const int64_t units = a.rows * a.blocks;
+  const int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
+  const int l = threadIdx.x & 15;
+  const int64_t row = u / a.blocks;
+  const int b = (int)(u - row * a.blocks), c = b * 128 + l * 8;
+  const bool in = u < units && c < a.cols;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in) {
+    Raw<T> x;
+    x.load((const T*)a.x + (size_t)row * a.cols + c);
+    x.widen(f);
+  }
+  float m = amax8(f);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = max_nan(m, kTiny);
+  if (in) {
+    *reinterpret_cast<uint2*>(a.q + (size_t)row * a.cols + c) = codes8(f, __fdiv_rn(kE4m3Max, m));
+    if (l == 0) a.scale[u] = __fdiv_rn(m, kE4m3Max);
+  }
+}
+
+// 128 x 128 blocks: a CTA each, thread t holding vector t % 16 of rows
+// t / 16 + 16 i.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantArgs a) {
+  __shared__ float wm[kWarps];
+  const int64_t r0 = (int64_t)blockIdx.y * 128 + (threadIdx.x >> 4);
+  const int c = blockIdx.x * 128 + (threadIdx.x & 15) * 8;
+  Raw<T> x[8];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i].zero();
+    if (r0 + 16 * i < a.rows && c < a.cols)
+      x[i].load((const T*)a.x + (size_t)(r0 + 16 * i) * a.cols + c);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    x[i].widen(f);
+    m = max_nan(m, amax8(f));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = kTiny;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) m = max_nan(m, wm[i]);
+  const float inv = __fdiv_rn(kE4m3Max, m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + 16 * i < a.rows && c < a.cols) {
+      float f[8];
+      x[i].widen(f);
+      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = codes8(f, inv);
+    }
+  }
+  if (threadIdx.x == 0)
+    a.scale[(size_t)blockIdx.y * a.blocks + blockIdx.x] = __fdiv_rn(m, kE4m3Max);
+}
+
+// ---------------------------------------------------------------- launchers
+// Calls f(std::integral_constant vectors, warps a row) for the smallest
+// register layout that holds `dim` columns.
+template <int kV, int kW>
+struct Lay {
+  static constexpr int V = kV, W = kW;
+};
+// `few`: at most 4 vectors a lane where 8 warps can hold the row so (the fp32
+// gradient, whose 8-vector form needs more than 255 registers).
+template <typename F>
+void with_layout(int dim, bool few, F&& f) {
+  const int v = (dim + 255) / 256;   // vectors a lane of one warp would hold
+  if (v <= 1) f(Lay<1, 1>{});
+  else if (v <= 2) f(Lay<2, 1>{});
+  else if (v <= 4) f(Lay<4, 1>{});
+  else if (few && v <= 8) f(Lay<4, 2>{});
+  else if (few && v <= 16) f(Lay<4, 4>{});
+  else if (few && v <= 32) f(Lay<4, 8>{});
+  else if (v <= 8) f(Lay<8, 1>{});
+  else if (v <= 16) f(Lay<8, 2>{});
+  else if (v <= 32) f(Lay<8, 4>{});
+  else f(Lay<8, 8>{});
+}
+
+size_t es_of(int32_t io) { return io == GDN_BF16 ? 2 : 4; }
+bool io_ok(int32_t io) { return io == GDN_BF16 || io == GDN_F32; }
+
+int launch_norm(const NormArgs& a, int32_t io, bool fp8, cudaStream_t st) {
+  int rc = GDN_OK;
+  with_layout(a.dim, false, [&](auto lay) {
+    constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
+    const int64_t blocks = (a.rows + kWarps / W - 1) / (kWarps / W);
+    if (blocks > 0x7fffffffLL) {
+      rc = GDN_ERR_UNSUPPORTED;
+      return;
+    }
+    const unsigned g = (unsigned)blocks;
+    if (io == GDN_BF16) {
+      if (fp8) residual_norm_kernel<__nv_bfloat16, V, W, true><<<g, kThreads, 0, st>>>(a);
+      else residual_norm_kernel<__nv_bfloat16, V, W, false><<<g, kThreads, 0, st>>>(a);
+    } else {
+      if (fp8) residual_norm_kernel<float, V, W, true><<<g, kThreads, 0, st>>>(a);
+      else residual_norm_kernel<float, V, W, false><<<g, kThreads, 0, st>>>(a);
+    }
+    count_launches(1);
+    if (cudaGetLastError() != cudaSuccess) rc = GDN_ERR_CUDA;
+  });
+  return rc;
+}
+
+int norm_common(const void* x, const void* residual, const float* w, float eps, void* s, void* y,
+                void* q, float* scale, int64_t tokens, int32_t dim, int32_t io_dtype, bool fp8,
+                cudaStream_t stream) {
+  if (tokens < 0 || dim < 1 || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+  if (!io_ok(io_dtype) || dim % 8 || dim > kMaxDim) return GDN_ERR_UNSUPPORTED;
+  if (tokens == 0) return GDN_OK;
+  if (!x || !w || (fp8 ? !q || !scale : !y) || (residual && !s) || (!residual && s))
+    return GDN_ERR_INVALID_ARG;
+  const void* v16[] = {x, residual, w, s, y};
+  for (const void* p : v16)
+    if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
+  if (!aligned(q, 16) || !aligned(scale, 4)) return GDN_ERR_ALIGNMENT;
+  const size_t n = (size_t)tokens * dim, bytes = n * es_of(io_dtype);
+  const int32_t blocks = (dim + 127) / 128;
+  const Span sx = span_of(x, bytes), sr = span_of(residual, bytes), sw = span_of(w, (size_t)dim * 4);
+  const Span outs[] = {span_of(s, bytes), span_of(y, bytes), span_of(q, n),
+                       span_of(scale, (size_t)tokens * blocks * 4)};
+  for (int i = 0; i < 4; ++i) {
+    // s and y may be x or residual themselves, nothing else overlaps
+    const bool whole = i < 2;
+    const void* o = i == 0 ? s : y;
+    if (intersect(outs[i], sw) || (intersect(outs[i], sx) && !(whole && o == x)) ||
+        (intersect(outs[i], sr) && !(whole && o == residual)))
+      return GDN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (intersect(outs[i], outs[j])) return GDN_ERR_INVALID_ARG;
+  }
+  NormArgs a{x, residual, w, eps, s, y, (uint8_t*)q, scale, tokens, dim, blocks};
+  return launch_norm(a, io_dtype, fp8, stream);
+}
+
+// dw parts of the backward: one row of `dim` a CTA, one CTA an SM at most
+int backward_grid(int64_t tokens, int32_t dim, int32_t io) {
+  int groups = 1;
+  with_layout(dim, io == GDN_F32, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
+  const int64_t want = (tokens + groups - 1) / groups;
+  const int64_t cap = 152;   // the SMs of the device: a constant, so that the sums' order is one
+  return (int)(want < cap ? want : cap);
+}
+bool backward_shape_ok(int64_t tokens, int32_t dim, int32_t io) {
+  return tokens >= 0 && dim >= 1 && io_ok(io) && dim % 8 == 0 && dim <= kMaxDim;
+}
+
+int backward_common(const void* dy, const void* s, const float* w, const void* ds, float eps,
+                    void* dx, float* dw, int64_t tokens, int32_t dim, int32_t io_dtype,
+                    bool use_ws, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (tokens < 0 || dim < 1 || !(eps >= 0.f) || !dw || !w) return GDN_ERR_INVALID_ARG;
+  if (!backward_shape_ok(tokens, dim, io_dtype)) return GDN_ERR_UNSUPPORTED;
+  if (tokens > 0 && (!dy || !s || !dx)) return GDN_ERR_INVALID_ARG;
+  const void* v16[] = {dy, s, w, ds, dx, dw};
+  for (const void* p : v16)
+    if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
+  const size_t bytes = (size_t)tokens * dim * es_of(io_dtype);
+  const int grid = backward_grid(tokens, dim, io_dtype);
+  const size_t need = (size_t)grid * dim * 4;
+  if (use_ws && need) {
+    if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
+    if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
+  }
+  const Span ins[] = {span_of(dy, bytes), span_of(s, bytes), span_of(w, (size_t)dim * 4),
+                      span_of(ds, bytes)};
+  const Span outs[] = {span_of(dx, bytes), span_of(dw, (size_t)dim * 4),
+                       span_of(use_ws ? ws : nullptr, need)};
+  if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
+  if (tokens == 0)
+    return cudaMemsetAsync(dw, 0, (size_t)dim * 4, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  void* part = ws;
+  if (!use_ws && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
+  NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
+  with_layout(dim, io_dtype == GDN_F32, [&](auto lay) {
+    constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
+    if (io_dtype == GDN_BF16)
+      norm_backward_kernel<__nv_bfloat16, V, W><<<grid, kThreads, 0, stream>>>(a);
+    else
+      norm_backward_kernel<float, V, W><<<grid, kThreads, 0, stream>>>(a);
+  });
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    norm_dw_kernel<<<(dim + 31) / 32, 256, 0, stream>>>((const float*)part, grid, dim, dw);
+    e = cudaGetLastError();
+  }
+  count_launches(2);
+  if (!use_ws && scratch_free(part, stream) != cudaSuccess) return GDN_ERR_CUDA;
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+int gdn_residual_norm(const void* x, const void* residual, const float* w, float eps, void* s,
+                      void* y, int64_t tokens, int32_t dim, int32_t io_dtype,
+                      gdn_stream_t stream) {
+  return norm_common(x, residual, w, eps, s, y, nullptr, nullptr, tokens, dim, io_dtype, false,
+                     (cudaStream_t)stream);
+}
+
+int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, float eps, void* s,
+                          void* q, float* scale, int64_t tokens, int32_t dim, int32_t io_dtype,
+                          gdn_stream_t stream) {
+  return norm_common(x, residual, w, eps, s, nullptr, q, scale, tokens, dim, io_dtype, true,
+                     (cudaStream_t)stream);
+}
+
+size_t gdn_residual_norm_backward_workspace_size(int64_t tokens, int32_t dim, int32_t io_dtype) {
+  if (!backward_shape_ok(tokens, dim, io_dtype)) return SIZE_MAX;
+  return (size_t)backward_grid(tokens, dim, io_dtype) * dim * 4;
+}
+
+int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,
+                               float eps, void* dx, float* dw, int64_t tokens, int32_t dim,
+                               int32_t io_dtype, gdn_stream_t stream) {
+  return gdn::backward_common(dy, s, w, ds, eps, dx, dw, tokens, dim, io_dtype, false, nullptr, 0,
+                              (cudaStream_t)stream);
+}
+
+int gdn_residual_norm_backward_ws(const void* dy, const void* s, const float* w, const void* ds,
+                                  float eps, void* dx, float* dw, int64_t tokens, int32_t dim,
+                                  int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                                  gdn_stream_t stream) {
+  return gdn::backward_common(dy, s, w, ds, eps, dx, dw, tokens, dim, io_dtype, true, workspace,
+                              workspace_bytes, (cudaStream_t)stream);
+}
+
+int gdn_quantize_fp8(const void* x, void* q, float* scale, int64_t rows, int32_t cols,
+                     int32_t block_rows, int32_t io_dtype, gdn_stream_t stream_) {
+  cudaStream_t stream = (cudaStream_t)stream_;
+  if (rows < 0 || cols < 1) return GDN_ERR_INVALID_ARG;
+  if (!io_ok(io_dtype) || cols % 8 || (block_rows != 1 && block_rows != 128))
+    return GDN_ERR_UNSUPPORTED;
+  if (rows == 0) return GDN_OK;
+  if (!x || !q || !scale) return GDN_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return GDN_ERR_ALIGNMENT;
+  const int32_t blocks = (cols + 127) / 128;
+  const int64_t row_blocks = (rows + block_rows - 1) / block_rows;
+  const Span ins[] = {span_of(x, (size_t)rows * cols * es_of(io_dtype))};
+  const Span outs[] = {span_of(q, (size_t)rows * cols),
+                       span_of(scale, (size_t)row_blocks * blocks * 4)};
+  if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
+  QuantArgs a{x, (uint8_t*)q, scale, rows, cols, blocks};
+  if (block_rows == 1) {
+    const int64_t grid = (rows * blocks + 15) / 16;
+    if (grid > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (io_dtype == GDN_BF16)
+      quant_rows_kernel<__nv_bfloat16><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+    else
+      quant_rows_kernel<float><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+  } else {
+    if (row_blocks > 65535) return GDN_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, (unsigned)row_blocks);
+    if (io_dtype == GDN_BF16)
+      quant_tiles_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
+    else
+      quant_tiles_kernel<float><<<grid, kThreads, 0, stream>>>(a);
+  }
+  count_launches(1);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -454,6 +454,145 @@ int gdn_prefill_layer(const void* qkv, const float* conv_w, const float* a_raw, 
                       int32_t dv, int32_t io_dtype, gdn_stream_t stream);
 
 /*
+ * Operators around the mixer: the residual stream's norm, the 8-bit
+ * projections and the gated feed-forward of the layer the mixer sits in.
+ * They follow the conventions above (device pointers, contiguous row-major
+ * tensors, asynchronous on `stream`, host-side errors before any launch);
+ * `tokens` counts rows whatever batch shape they come from, and 0 tokens is a
+ * call that writes nothing (the gradients of weights are then zero).  8-bit
+ * values are e4m3 (float8_e4m3fn: 448 largest, no infinity), one byte each.
+ */
+
+/*
+ * gdn_residual_norm -- the residual addition and the root-mean-square norm
+ * that follows it:
+ *
+ *   s = x + residual (rounded to the io dtype; s = x without a residual)
+ *   y = s / sqrt(mean_j s_j^2 + eps) * w
+ *
+ *   x, residual, s, y   [tokens, dim] io dtype (bf16 or fp32)
+ *   w                   [dim] fp32; eps >= 0
+ * residual and s are both given or both NULL (GDN_ERR_INVALID_ARG otherwise).
+ * The norm is that of s as it is stored, so the gradient below, which reads
+ * s, is the gradient of exactly this.  s and y may each be x or residual
+ * itself (in place); no other overlap is allowed.  dim a multiple of 8, at
+ * most 16384 (GDN_ERR_UNSUPPORTED).  Tensors 16-byte aligned.
+ */
+int gdn_residual_norm(const void* x, const void* residual, const float* w, float eps, void* s,
+                      void* y, int64_t tokens, int32_t dim, int32_t io_dtype,
+                      gdn_stream_t stream);
+
+/*
+ * gdn_residual_norm_fp8 -- gdn_residual_norm with y as e4m3 values and a
+ * scale for every 128 columns of a row (the last block may be shorter), the
+ * form gdn_linear_fp8 reads:
+ *
+ *   m = max(max_j |y_j|, 2^-100) over the block,  scale = m / 448,
+ *   q_j = e4m3(y_j * (448 / m))    (round to nearest even), y_j ~ q_j * scale
+ *
+ *   q       [tokens, dim] e4m3, 16-byte aligned
+ *   scale   [tokens, ceil(dim / 128)] fp32, 4-byte aligned
+ * y is in fp32 between the norm and the quantisation.  A NaN or an infinity
+ * leaves NaN in its whole block (q * scale).
+ */
+int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, float eps, void* s,
+                          void* q, float* scale, int64_t tokens, int32_t dim, int32_t io_dtype,
+                          gdn_stream_t stream);
+
+/*
+ * gdn_residual_norm_backward -- gradients of gdn_residual_norm.  With
+ * rs = 1 / sqrt(mean_j s_j^2 + eps), n = s rs and g = dy w:
+ *
+ *   dx = (g - n mean_j(g_j n_j)) rs + ds     (of x and of residual alike)
+ *   dw = sum over the tokens of dy n
+ *
+ *   dy, s, ds, dx   [tokens, dim] io dtype; ds is the gradient that reaches s
+ *                   from its other uses (the residual stream), or NULL
+ *   dw              [dim] fp32, 16-byte aligned, overwritten; the order of
+ *                   its sums is fixed
+ * No output may overlap an input or another output.  Scratch from the
+ * library's pool, or a caller's 256-byte aligned workspace of at least
+ * gdn_residual_norm_backward_workspace_size bytes (SIZE_MAX for unsupported
+ * arguments; rules as gdn_prefill_ws): at most 152 * dim * 4 bytes.
+ */
+int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,
+                               float eps, void* dx, float* dw, int64_t tokens, int32_t dim,
+                               int32_t io_dtype, gdn_stream_t stream);
+size_t gdn_residual_norm_backward_workspace_size(int64_t tokens, int32_t dim, int32_t io_dtype);
+int gdn_residual_norm_backward_ws(const void* dy, const void* s, const float* w, const void* ds,
+                                  float eps, void* dx, float* dw, int64_t tokens, int32_t dim,
+                                  int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                                  gdn_stream_t stream);
+
+/*
+ * gdn_quantize_fp8 -- x [rows, cols] (io dtype) as e4m3 values with a scale
+ * for each block of block_rows x 128 elements, by gdn_residual_norm_fp8's
+ * rule: block_rows = 1 for activations (scale [rows, ceil(cols / 128)]), 128
+ * for weights (scale [ceil(rows / 128), ceil(cols / 128)]).  cols a multiple
+ * of 8; x and q 16-byte aligned, scale 4; no overlap.
+ */
+int gdn_quantize_fp8(const void* x, void* q, float* scale, int64_t rows, int32_t cols,
+                     int32_t block_rows, int32_t io_dtype, gdn_stream_t stream);
+
+/*
+ * gdn_linear_fp8 -- out = x w^T of e4m3 operands with block scales:
+ *
+ *   out[t][n] = sum_b x_scale[t][b] w_scale[n / 128][b]
+ *                     sum_{k in block b of 128} x[t][k] w[n][k]
+ *
+ *   x  [tokens, k] e4m3, x_scale [tokens, ceil(k / 128)] fp32
+ *   w  [n, k] e4m3,      w_scale [ceil(n / 128), ceil(k / 128)] fp32
+ *   out [tokens, n] bf16 or fp32 (out_dtype)
+ * k a multiple of 16 (rows start on 16 bytes); tokens and n are free.  The
+ * sum over a block runs in the tensor cores' fp32 accumulator, the sum over
+ * blocks in fp32.  x, w and out 16-byte aligned, scales 4; out may overlap
+ * no input.
+ */
+int gdn_linear_fp8(const void* x, const float* x_scale, const void* w, const float* w_scale,
+                   void* out, int64_t tokens, int32_t k, int32_t n, int32_t out_dtype,
+                   gdn_stream_t stream);
+
+/*
+ * gdn_gated_ffn -- the gated feed-forward's two projections, activation and
+ * product in one kernel:
+ *
+ *   G = x w_gate^T, U = x w_up^T (fp32),  h = act(G) U
+ *
+ *   x [tokens, dim], w_gate and w_up [hidden, dim], h [tokens, hidden], bf16
+ *   act: GDN_GATE_SILU or GDN_GATE_SIGMOID
+ * bf16 only, dim a multiple of 8 (GDN_ERR_UNSUPPORTED otherwise); tokens and
+ * hidden are free.  Tensors 16-byte aligned; h may overlap no input.
+ */
+int gdn_gated_ffn(const void* x, const void* w_gate, const void* w_up, int32_t act, void* h,
+                  int64_t tokens, int32_t dim, int32_t hidden, int32_t io_dtype,
+                  gdn_stream_t stream);
+
+/*
+ * gdn_gated_ffn_backward -- gradients of gdn_gated_ffn from its inputs and dh
+ * [tokens, hidden] (G and U are recomputed, so the forward pass keeps
+ * nothing):
+ *
+ *   dU = dh act(G), dG = dh U act'(G)
+ *   dx = dG w_gate + dU w_up, dw_gate = dG^T x, dw_up = dU^T x
+ *
+ * all bf16 (products accumulate in fp32; dG and dU are rounded to bf16 where
+ * they enter the products).  dx [tokens, dim], dw_* [hidden, dim],
+ * overwritten.  No output may overlap an input or another output.  Scratch
+ * (dG and dU: 4 bytes a token and feature) from the library's pool, or a
+ * caller's 256-byte aligned workspace of at least
+ * gdn_gated_ffn_backward_workspace_size bytes (rules as gdn_prefill_ws).
+ */
+int gdn_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* dh,
+                           int32_t act, void* dx, void* dw_gate, void* dw_up, int64_t tokens,
+                           int32_t dim, int32_t hidden, int32_t io_dtype, gdn_stream_t stream);
+size_t gdn_gated_ffn_backward_workspace_size(int64_t tokens, int32_t dim, int32_t hidden,
+                                             int32_t io_dtype);
+int gdn_gated_ffn_backward_ws(const void* x, const void* w_gate, const void* w_up, const void* dh,
+                              int32_t act, void* dx, void* dw_gate, void* dw_up, int64_t tokens,
+                              int32_t dim, int32_t hidden, int32_t io_dtype, void* workspace,
+                              size_t workspace_bytes, gdn_stream_t stream);
+
+/*
  * gdn_get_device_status -- synchronises `stream`, then returns and clears the
  * device status word of the current device (GDN_OK when no kernel flagged a
  * problem since the last call; GDN_ERR_CUDA if the synchronisation failed).
