@@ -82,7 +82,6 @@ int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void
   g.act = act;
   g.p[0].out[0] = g.p[0].out[1] = h;
   g.p[0].ldc = hidden;
-  g.wide = aligned(h, 32) && hidden % 16 == 0;
   return gemm::launch_pair<false, gemm::kGate>(g, sms, stream) == cudaSuccess ? GDN_OK
                                                                               : GDN_ERR_CUDA;
 }
@@ -102,7 +101,6 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   g.p[0].out[0] = dG;
   g.p[0].out[1] = dU;
   g.p[0].ldc = pitch;
-  g.wide = 1;
   g.dh = (const __nv_bfloat16*)dh;
   g.ldh = hidden;
   g.dh_wide = hidden % 8 == 0;
@@ -113,7 +111,6 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   g.status = status;
   g.problems = 2;
   g.group_m = 8;
-  g.wide = aligned(dx, 32) && aligned(dwg, 32) && aligned(dwu, 32) && dim % 16 == 0;
   const int32_t kx = (hidden + 63) / 64, kw = (int32_t)((tokens + 63) / 64);
   const int ix = 2 * kx >= kw ? 0 : 1;
   gemm::Problem& px = g.p[ix];

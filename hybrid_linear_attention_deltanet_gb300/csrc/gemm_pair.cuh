@@ -8,21 +8,24 @@
 // even CTA's one MMA thread multiplies all of it: 32 KB into each SM for
 // 512 tensor cycles, half of what two single-CTA 128 x 256 tiles would fetch.
 //
-// Roles (12 warps): warp 0 fetches, warp 1 multiplies (even CTA only), warp 2
-// owns the tensor memory, warps 4..11 take the accumulators out.  The grid is
+// Roles: warp 0 fetches, warp 1 multiplies (even CTA only), warp 2 owns the
+// tensor memory, warps 4 and up take the accumulators out.  The grid is
 // persistent and the tensor memory holds two accumulators, so a tile's
-// epilogue runs while the next tile is multiplied.
+// epilogue runs while the next tile is multiplied.  Results go through shared
+// memory, 32 rows x 128 bytes a warp, and leave as TMA stores.
 //
-// bf16 operands accumulate a whole tile in tensor memory.  8-bit operands
+// bf16 operands (8 epilogue warps, 128 accumulator columns each) accumulate a
+// whole tile in tensor memory.  8-bit operands (16 warps, 64 columns each)
 // carry one scale for every 128 elements of K, so there each K block is an
-// accumulator of its own, which the epilogue warps scale and add into 128
-// fp32 registers a thread while the next block is multiplied.
+// accumulator of its own, which the epilogue warps scale and add into 64 fp32
+// registers a thread while the next block is multiplied.
 //
 // Every wait has a limit: a wait that runs out flags GDN_ERR_TIMEOUT, and the
 // CTA leaves after its copies and products in flight have had time to end.
 #pragma once
 
 #include <string.h>
+#include <type_traits>
 
 #include "gdn_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -43,7 +46,8 @@ enum Epilogue : int {
 // One product.  Its rows of A, or its K, may come in two halves with operands
 // of their own (the two gradients of the weights; dG Wg + dU Wu).
 struct Problem {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[2], b[2], c[2];
+  int32_t c_tma;        // c is valid: rows of the outputs start on 16 bytes
   int32_t m_half;       // tiles of rows in each half of A (all of them: one half)
   int32_t m_tiles, n_tiles;
   int32_t k_half;       // K blocks in each half of K (all of them: one half)
@@ -58,7 +62,6 @@ struct PairArgs {
   Problem p[2];
   int32_t problems;
   int32_t group_m;      // tiles of rows whose columns are visited together (L2 reuse)
-  int32_t wide;         // outputs and row pitches are 32-byte aligned
   int32_t act;
   const __nv_bfloat16* dh;   // kGateGrad: [M][ldh]
   int64_t ldh;
@@ -69,11 +72,22 @@ struct PairArgs {
   unsigned* status;
 };
 
-constexpr int kPairThreads = 384;
-constexpr int kStages = 6;
 constexpr uint32_t kOperand = 128 * 128;             // bytes of A (and of B) a stage
 constexpr uint32_t kStageBytes = 2 * kOperand;
-constexpr uint32_t kPairSmem = kStages * kStageBytes + 1024;
+constexpr int kGroup = 4;                            // K blocks whose scales travel together
+
+template <bool kFp8>
+struct Shape {
+  static constexpr int kEpiWarps = kFp8 ? 16 : 8;
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kStages = kFp8 ? 5 : 6;
+  static constexpr int kRow = kFp8 ? 64 : 128;       // bytes of a row of a warp's staging
+  static constexpr uint32_t kBounce = 32 * kRow;
+  // two groups of scales [kGroup][2 column blocks][128 rows]
+  static constexpr uint32_t kScales = kFp8 ? 2 * kGroup * 256 * 4 : 0;
+  static constexpr uint32_t kSmem =
+      kStages * kStageBytes + kEpiWarps * kBounce + kScales + 1024;
+};
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct Tile {
@@ -104,39 +118,58 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 32 bytes to global memory (one whole sector), 32-byte aligned
-__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// Offset of 16-byte piece `i` of row `r` in a warp's staging image, swizzled
+// as TMA's 128- or 64-byte mode does; lanes that write a piece of each row
+// meet no bank conflicts.
+template <int kRow>
+__device__ __forceinline__ uint32_t stage_piece(uint32_t r, uint32_t i) {
+  return r * kRow + (kRow == 128 ? i ^ (r & 7u) : i ^ ((r >> 1) & 3u)) * 16;
 }
-// 32 consecutive columns of one row, columns past `valid` left out
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[32], int valid,
-                                          bool wide) {
-  if (wide && valid >= 32) {
-    uint32_t w[16];
+// kN columns from `c0` of this lane's row into its warp's staging image.
+template <typename T, int kRow, int kN>
+__device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const float* v) {
+  constexpr int kPer = 16 / (int)sizeof(T);   // elements a piece
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
-    st32(p, w);
-    st32(p + 16, w + 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < valid) p[i] = __float2bfloat16_rn(v[i]);
+  for (int i = 0; i < kN / kPer; ++i) {
+    uint4 w;
+    if constexpr (sizeof(T) == 2)
+      w = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
+                     pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
+    else
+      w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    *reinterpret_cast<uint4*>(buf + stage_piece<kRow>(lane, c0 / kPer + i)) = w;
   }
 }
-__device__ __forceinline__ void store_row(float* p, const float (&v)[32], int valid, bool wide) {
-  if (wide && valid >= 32) {
-    uint32_t w[32];
+// The staged 32 rows to their place, what lies past the edges of the output
+// left out.  stage_free() must return before the next stage_put.
+template <typename T, int kRow>
+__device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Problem& p, int half,
+                                          int row0, int n0) {
+  if (row0 >= p.M || n0 >= p.N) return;
+  if (p.c_tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&p.c[half], buf, n0, row0);
+      bulk_commit();
+    }
+  } else {   // rows that start anywhere: a row at a time, 32 elements a step
+    __syncwarp();
+    constexpr int kCols = kRow / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
+    const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
+    T* out = (T*)p.out[half] + (size_t)row0 * p.ldc + n0;
+    for (int r = 0; r < rows; ++r)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st32(p + 8 * i, w + 8 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < valid) p[i] = v[i];
+      for (int c = lane; c < kCols; c += 32)
+        if (n0 + c < p.N)
+          out[(size_t)r * p.ldc + c] = *reinterpret_cast<const T*>(
+              buf + stage_piece<kRow>(r, c / kPer) + (c % kPer) * sizeof(T));
   }
+}
+__device__ __forceinline__ void stage_free(int lane) {
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
 }
 
 // The gate's activation and its derivative.
@@ -149,13 +182,17 @@ __device__ __forceinline__ float gate_act(float x, int act) {
 }
 
 template <bool kFp8, int kEpi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs g) {
+  using S = Shape<kFp8>;
+  constexpr int kStages = S::kStages, kEpiWarps = S::kEpiWarps, kRow = S::kRow;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t sc_full[2], sc_empty[2];
   __shared__ uint32_t tmem_base;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be uniform
   const uint32_t rank = cluster_ctarank();
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -164,7 +201,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 16);   // both CTAs' epilogue warps
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);   // both CTAs' epilogue warps
+      mbar_init(&sc_full[i], 2);                 // the two warps that fetch scales
+      mbar_init(&sc_empty[i], kEpiWarps);
     }
     fence_barrier_init();
   }
@@ -178,9 +217,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       g.p[0].m_tiles * g.p[0].n_tiles + (g.problems > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   bool ok = true;
+  float* scales = reinterpret_cast<float*>(sm + kStages * kStageBytes + kEpiWarps * S::kBounce);
 
-  if (warp == 0 && lane == 0) {
+  // The fetching and the multiplying warp run their loops whole, with one
+  // elected lane issuing: every address and descriptor then stays in uniform
+  // registers.  (Loops run by one lane alone took 750 cycles a K block against
+  // the 512 of its products.)
+  if (warp == 0) {
     // ---------------------------------------------------------- fetch
+    const bool lead = elect_one();
+    const uint32_t full0 = mapa_smem(&full[0], 0);   // the even CTA's barriers
     int st = 0;
     uint32_t ph = 0;
     for (int t = t0; t < n_tiles && ok; t += step) {
@@ -189,37 +235,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int m0 = tl.m0 + 128 * (int)rank;
       // gated: both CTAs' halves of B are the same 128 features of Wg and Wu
       const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + 128 * (int)rank;
-      for (int kb = 0; kb < p.k_blocks; ++kb) {
-        ok = mbar_wait(&empty[st], ph ^ 1u, kWaitNs);
+      const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
+      const int k_half = p.k_half, k_blocks = p.k_blocks;
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        ok = mbar_wait_warp(&empty[st], ph ^ 1u, kWaitNs);
         if (!ok) break;
-        uint8_t* A = sm + st * kStageBytes;
-        uint8_t* B = A + kOperand;
-        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
-        const uint32_t bar = mapa_smem(&full[st], 0);
-        const int h = kb >= p.k_half;
-        const int k0 = (kb - (h ? p.k_half : 0)) * (kFp8 ? 128 : 64);
-        const CUtensorMap* am = &p.a[h | tl.half];
-        const CUtensorMap* bm = &p.b[kEpi >= kGate ? (int)rank : h];
-        if (!kFp8 && p.a_mn) {
-          tma_load_2d_pair(A, am, m0, k0, bar);
-          tma_load_2d_pair(A + 8192, am, m0 + 64, k0, bar);
-        } else {
-          tma_load_2d_pair(A, am, k0, m0, bar);
+        if (lead) {
+          uint8_t* A = sm + st * kStageBytes;
+          uint8_t* B = A + kOperand;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
+          const uint32_t bar = full0 + 8 * st;
+          const int h = kb >= k_half;
+          const int k0 = (kb - (h ? k_half : 0)) * (kFp8 ? 128 : 64);
+          const CUtensorMap* am = &p.a[h | tl.half];
+          const CUtensorMap* bm = &p.b[kEpi >= kGate ? (int)rank : h];
+          if (a_mn) {
+            tma_load_2d_pair(A, am, m0, k0, bar);
+            tma_load_2d_pair(A + 8192, am, m0 + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(A, am, k0, m0, bar);
+          }
+          if (b_mn) {
+            tma_load_2d_pair(B, bm, n0, k0, bar);
+            tma_load_2d_pair(B + 8192, bm, n0 + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(B, bm, k0, n0, bar);
+          }
         }
-        if (!kFp8 && p.b_mn) {
-          tma_load_2d_pair(B, bm, n0, k0, bar);
-          tma_load_2d_pair(B + 8192, bm, n0 + 64, k0, bar);
-        } else {
-          tma_load_2d_pair(B, bm, k0, n0, bar);
-        }
+        __syncwarp();
         if (++st == kStages) {
           st = 0;
           ph ^= 1u;
         }
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------- multiply
+    const bool lead = elect_one();
+    const uint32_t sm0 = smem_u32(sm);
     int st = 0, buf = 0;
     uint32_t ph = 0, aph = 0;
     for (int t = t0; t < n_tiles && ok; t += step) {
@@ -228,29 +281,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, 256, p.a_mn, p.b_mn);
       // a K-major block advances 32 bytes an instruction inside the swizzled
       // row; one stored by rows advances 16 rows of K (2048 bytes)
-      const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
-      const uint32_t a_lbo = p.a_mn ? 8192 : 16, b_lbo = p.b_mn ? 8192 : 16;
-      for (int kb = 0; kb < p.k_blocks; ++kb) {
-        const bool first = kFp8 || kb == 0, last = kFp8 || kb + 1 == p.k_blocks;
+      const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
+      const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+      const uint64_t a0 = smem_desc(sm0, a_mn ? 8192 : 16, 1024, kSwizzle128B);
+      const uint64_t b0 = smem_desc(sm0 + kOperand, b_mn ? 8192 : 16, 1024, kSwizzle128B);
+      const int k_blocks = p.k_blocks;
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        const bool first = kFp8 || kb == 0, last = kFp8 || kb + 1 == k_blocks;
         if (first) {
-          ok = mbar_wait(&acc_empty[buf], aph ^ 1u, kWaitNs);
+          ok = mbar_wait_warp(&acc_empty[buf], aph ^ 1u, kWaitNs);
           if (!ok) break;
         }
-        ok = mbar_wait(&full[st], ph, kWaitNs);
+        ok = mbar_wait_warp(&full[st], ph, kWaitNs);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t A = smem_u32(sm + st * kStageBytes), B = A + kOperand;
-        const uint32_t d = tmem + 256 * buf;
+        if (lead) {
+          const uint64_t ad = a0 + (uint64_t)(st * (kStageBytes >> 4));
+          const uint64_t bd = b0 + (uint64_t)(st * (kStageBytes >> 4));
+          const uint32_t d = tmem + 256 * buf;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t ad = smem_desc(A + i * a_step, a_lbo, 1024, kSwizzle128B);
-          const uint64_t bd = smem_desc(B + i * b_step, b_lbo, 1024, kSwizzle128B);
-          if (kFp8) mma_f8_pair(d, ad, bd, idesc, i != 0);
-          else mma_bf16_pair(d, ad, bd, idesc, !first || i != 0);
+          for (int i = 0; i < 4; ++i) {
+            if (kFp8) mma_f8_pair(d, ad + i * a_step, bd + i * b_step, idesc, i != 0);
+            else mma_bf16_pair(d, ad + i * a_step, bd + i * b_step, idesc, !first || i != 0);
+          }
+          mma_commit_pair(&empty[st]);
+          if (last) mma_commit_pair(&acc_full[buf]);
         }
-        mma_commit_pair(&empty[st]);
+        __syncwarp();
         if (last) {
-          mma_commit_pair(&acc_full[buf]);
           buf ^= 1;
           if (buf == 0) aph ^= 1u;
         }
@@ -260,91 +318,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-  } else if (warp >= 4) {
-    // -------------------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    const uint32_t free_bar[2] = {mapa_smem(&acc_empty[0], 0), mapa_smem(&acc_empty[1], 0)};
-    int buf = 0;
-    uint32_t aph = 0;
+  } else if (kFp8 && (warp == 2 || warp == 3)) {
+    // ---------------------------------------------------------- scales
+    // s[j][h][r] = sa[row r][k0 + j] sb[column block h][k0 + j] of kGroup K
+    // blocks at a time; a group is in registers while its slot is in use.
+    int slot = 0;
+    uint32_t ph = 0;
     for (int t = t0; t < n_tiles && ok; t += step) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.p];
-      const int row = tl.m0 + 128 * (int)rank + 32 * q + lane;
+      const int r0 = 64 * (warp - 2) + lane, nb = tl.n0 / 128;
+      const float* sb0 = g.sb + (size_t)nb * g.sblocks;
+      const float* sb1 = sb0 + (tl.n0 + 128 < p.N ? g.sblocks : 0);
+      const float* sa[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = tl.m0 + 128 * (int)rank + r0 + 32 * i;
+        sa[i] = g.sa + (size_t)(row < p.M ? row : p.M - 1) * g.sblocks;
+      }
+      for (int kb = 0; kb < p.k_blocks; kb += kGroup) {
+        float a[2][kGroup], b[2][kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+          const int k = kb + j < p.k_blocks ? kb + j : kb;
+          a[0][j] = __ldg(sa[0] + k);
+          a[1][j] = __ldg(sa[1] + k);
+          b[0][j] = __ldg(sb0 + k);
+          b[1][j] = __ldg(sb1 + k);
+        }
+        ok = mbar_wait_warp(&sc_empty[slot], ph ^ 1u, kWaitNs);
+        if (!ok) break;
+        float* d = scales + slot * (kGroup * 256) + r0;
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            d[j * 256 + h * 128] = a[0][j] * b[h][j];
+            d[j * 256 + h * 128 + 32] = a[1][j] * b[h][j];
+          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[slot]);
+        slot ^= 1;
+        if (slot == 0) ph ^= 1u;
+      }
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------- epilogue
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t free0 = mapa_smem(&acc_empty[0], 0);   // the even CTA's barriers
+    uint8_t* bounce = sm + kStages * kStageBytes + (warp - 4) * S::kBounce;
+    int buf = 0, slot = 0;
+    uint32_t aph = 0, sph = 0;
+    // this warp's columns of the accumulator are out of tensor memory
+    auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(free0 + 8 * buf);
+    };
+    auto advance = [&] {
+      buf ^= 1;
+      if (buf == 0) aph ^= 1u;
+    };
+    for (int t = t0; t < n_tiles && ok; t += step) {
+      const Tile tl = tile_at(g, t);
+      const Problem& p = g.p[tl.p];
+      const int row0 = tl.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
       const bool live = row < p.M;
       if constexpr (kFp8) {
-        // this thread's 128 columns belong to one block of the weights' scales
-        const int n0 = tl.n0 + 128 * half;
-        const float* sa = g.sa + (size_t)(live ? row : 0) * g.sblocks;
-        const float* sb = g.sb + (size_t)(n0 < p.N ? n0 / 128 : 0) * g.sblocks;
-        float acc[128];
+        // this thread's 64 columns lie in one column block of the scales
+        const int n0 = tl.n0 + 64 * part;
+        const float* sc = scales + 128 * (part >> 1) + 32 * q + lane;
+        const int k_blocks = p.k_blocks;
+        F2 acc[32];
 #pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        float s = __ldg(sa) * __ldg(sb);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          ok = mbar_wait(&acc_full[buf], aph, kWaitNs);
-          ok = __all_sync(0xffffffffu, ok);
+        for (int i = 0; i < 32; ++i) acc[i] = f2(0.f, 0.f);
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          const int j = kb % kGroup;
+          if (j == 0) {
+            ok = mbar_wait_warp(&sc_full[slot], sph, kWaitNs);
+            if (!ok) break;
+          }
+          const float s = sc[(slot * kGroup + j) * 256];
+          ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          const float sn = kb + 1 < p.k_blocks ? __ldg(sa + kb + 1) * __ldg(sb + kb + 1) : 0.f;
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < 64; c += 32) {
             uint32_t r[32];
-            tmem_ld32(tmem + lanes + 256 * buf + 128 * half + c, r);
+            tmem_ld32(tmem + lanes + 256 * buf + 64 * part + c, r);
             tmem_ld_wait_regs(r);
-            if (c == 96) {   // all of this warp's columns are out
-              tc_fence_before();
-              if (lane == 0) mbar_arrive_cluster(free_bar[buf]);
-            }
+            if (c == 32) release();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(r[i]), s, acc[c + i]);
+            for (int i = 0; i < 16; ++i)
+              acc[c / 2 + i] = f2_fma(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                                      f2(s, s), acc[c / 2 + i]);
           }
-          s = sn;
-          buf ^= 1;
-          if (buf == 0) aph ^= 1u;
+          advance();
+          if (j == kGroup - 1 || kb + 1 == k_blocks) {
+            if (lane == 0) mbar_arrive(&sc_empty[slot]);   // read by the whole warp: release()'s
+            slot ^= 1;                                     // __syncwarp came after
+            if (slot == 0) sph ^= 1u;
+          }
         }
         if (!ok) break;
-        if (live) {
+        using T = typename std::conditional<kEpi == kStoreF32, float, __nv_bfloat16>::type;
+        constexpr int kCols = kRow / (int)sizeof(T);   // 32 bf16 or 16 fp32
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            float v[32];
+        for (int c = 0; c < 64; c += kCols) {
+          float v[kCols];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = acc[c + i];
-            if (n0 + c < p.N) {
-              const size_t o = (size_t)row * p.ldc + n0 + c;
-              if (kEpi == kStoreF32) store_row((float*)p.out[0] + o, v, p.N - n0 - c, g.wide);
-              else store_row((__nv_bfloat16*)p.out[0] + o, v, p.N - n0 - c, g.wide);
-            }
-          }
+          for (int i = 0; i < kCols / 2; ++i) f2_split(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
+          stage_free(lane);
+          stage_put<T, kRow, kCols>(bounce, lane, 0, v);
+          stage_out<T, kRow>(bounce, lane, p, 0, row0, n0 + c);
         }
       } else if constexpr (kEpi == kStore) {
-        ok = mbar_wait(&acc_full[buf], aph, kWaitNs);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
         if (!ok) break;
         tc_fence_after();
+        const int n0 = tl.n0 + 128 * part;
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
-          tmem_ld32(tmem + lanes + 256 * buf + 128 * half + c, r);
+          tmem_ld32(tmem + lanes + 256 * buf + 128 * part + c, r);
           tmem_ld_wait_regs(r);
-          if (c == 96) {
-            tc_fence_before();
-            if (lane == 0) mbar_arrive_cluster(free_bar[buf]);
-          }
-          const int n = tl.n0 + 128 * half + c;
-          if (live && n < p.N) {
-            float v[32];
+          if (c == 96) release();
+          float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            store_row((__nv_bfloat16*)p.out[tl.half] + (size_t)row * p.ldc + n, v, p.N - n,
-                      g.wide);
-          }
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (c % 64 == 0) stage_free(lane);
+          stage_put<__nv_bfloat16, kRow, 32>(bounce, lane, c % 64, v);
+          if (c % 64 == 32)
+            stage_out<__nv_bfloat16, kRow>(bounce, lane, p, tl.half, row0, n0 + c - 32);
         }
-        buf ^= 1;
-        if (buf == 0) aph ^= 1u;
+        advance();
       } else {
         // this thread's 64 features
-        const int f0 = tl.n0 / 2 + 64 * half;
+        const int f0 = tl.n0 / 2 + 64 * part;
         uint32_t dh[kEpi == kGateGrad ? 32 : 1];   // 64 bf16, fetched before the wait
         if constexpr (kEpi == kGateGrad) {
           const __nv_bfloat16* d = g.dh + (size_t)(live ? row : 0) * g.ldh + f0;
@@ -365,51 +476,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
         }
-        ok = mbar_wait(&acc_full[buf], aph, kWaitNs);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t G[32], U[32];
-          tmem_ld32(tmem + lanes + 256 * buf + 64 * half + c, G);
-          tmem_ld32(tmem + lanes + 256 * buf + 128 + 64 * half + c, U);
-          tmem_ld_wait_regs(G);
-          tmem_ld_wait_regs(U);
-          if (c == 32) {
-            tc_fence_before();
-            if (lane == 0) mbar_arrive_cluster(free_bar[buf]);
-          }
-          const int f = f0 + c;
-          if (live && f < p.N) {
-            const size_t o = (size_t)row * p.ldc + f;
+        for (int out = 0; out < (kEpi == kGateGrad ? 2 : 1); ++out) {   // h; or dG, then dU
+          stage_free(lane);
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t G[32], U[32];
+            tmem_ld32(tmem + lanes + 256 * buf + 64 * part + c, G);
+            if (kEpi == kGate || out == 0)
+              tmem_ld32(tmem + lanes + 256 * buf + 128 + 64 * part + c, U);
+            tmem_ld_wait_regs(G);
+            if (kEpi == kGate || out == 0) tmem_ld_wait_regs(U);
+            if (c == 32 && (kEpi == kGate || out == 1)) release();
             float v[32];
-            if constexpr (kEpi == kGate) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                v[i] = gate_act(__uint_as_float(G[i]), g.act) * __uint_as_float(U[i]);
-              store_row((__nv_bfloat16*)p.out[0] + o, v, p.N - f, g.wide);
-            } else {
-              float w[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 32; ++i) {
+              const float x = __uint_as_float(G[i]);
+              if constexpr (kEpi == kGate) {
+                v[i] = gate_act(x, g.act) * __uint_as_float(U[i]);
+              } else {
                 const uint32_t d2 = dh[(c + i) >> 1];
                 const float d = __uint_as_float((i & 1) ? d2 & 0xffff0000u : d2 << 16);
-                const float x = __uint_as_float(G[i]), s = gate_sigmoid(x);
+                const float s = gate_sigmoid(x);
                 const bool silu = g.act == GDN_GATE_SILU;
-                const float slope = silu ? s * fmaf(x, 1.f - s, 1.f) : s * (1.f - s);
-                v[i] = d * __uint_as_float(U[i]) * slope;
-                w[i] = d * (silu ? x * s : s);
+                v[i] = out == 0 ? d * __uint_as_float(U[i]) *
+                                      (silu ? s * fmaf(x, 1.f - s, 1.f) : s * (1.f - s))
+                                : d * (silu ? x * s : s);
               }
-              store_row((__nv_bfloat16*)p.out[0] + o, v, p.N - f, g.wide);
-              store_row((__nv_bfloat16*)p.out[1] + o, w, p.N - f, g.wide);
             }
+            stage_put<__nv_bfloat16, kRow, 32>(bounce, lane, c, v);
           }
+          stage_out<__nv_bfloat16, kRow>(bounce, lane, p, out, row0, f0);
         }
-        buf ^= 1;
-        if (buf == 0) aph ^= 1u;
+        advance();
       }
     }
+    if (lane == 0) bulk_wait_all();   // this warp's stores have left shared memory
   }
   if (!ok) {
     // copies and products in flight end within microseconds; give them longer
@@ -459,16 +564,47 @@ inline bool matrix_map(CUtensorMap* m, const void* base, bool fp8, int64_t inner
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The outputs c[0], c[1] = out[0], out[1], [M][N] with ldc elements a row:
+// TMA stores where rows start on 16 bytes, plain ones elsewhere.
+inline bool output_maps(Problem& p, bool f32, int row_bytes) {
+  const int64_t pitch = p.ldc * (f32 ? 4 : 2);
+  p.c_tma = pitch % 16 == 0;
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  for (int i = 0; p.c_tma && i < 2; ++i) {
+    if (i == 1 && p.out[1] == p.out[0]) {
+      p.c[1] = p.c[0];
+      break;
+    }
+    memset(&p.c[i], 0, sizeof p.c[i]);
+    cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {(cuuint32_t)(row_bytes / (f32 ? 4 : 2)), 32};
+    cuuint32_t es[2] = {1, 1};
+    if (enc(&p.c[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            p.out[i], dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
+}
+
 template <bool kFp8, int kEpi>
-cudaError_t launch_pair(const PairArgs& g, int sms, cudaStream_t st) {
+cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
+  using S = Shape<kFp8>;
   auto kern = pair_gemm_kernel<kFp8, kEpi>;
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
   int64_t tiles = 0;
-  for (int i = 0; i < g.problems; ++i) tiles += (int64_t)g.p[i].m_tiles * g.p[i].n_tiles;
+  for (int i = 0; i < g.problems; ++i) {
+    if (!output_maps(g.p[i], kEpi == kStoreF32, S::kRow)) return cudaErrorUnknown;
+    tiles += (int64_t)g.p[i].m_tiles * g.p[i].n_tiles;
+  }
   const int64_t pairs = sms / 2;
-  kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, kPairSmem, st>>>(g);
+  kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), S::kThreads, S::kSmem, st>>>(g);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -46,7 +46,6 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   p.ldc = n;
   g.problems = 1;
   g.group_m = 8;
-  g.wide = aligned(out, 32) && (size_t)n * es % 32 == 0;
   g.sa = sx;
   g.sb = sw;
   g.sblocks = blocks;
