@@ -620,41 +620,80 @@ def prefill_layer(qkv, conv_w, a_raw, b_raw, A_log, dt_bias, gate, norm_w, heads
 
 # ---------------------------------------------------------------------------
 # The layer around the mixer: residual norm, 8-bit projections, feed-forward.
+# A decoding step makes these calls for single tokens, where the host's time
+# counts: tensors are checked in one pass, addresses go to the library as
+# integers, and the device guard is taken only off the current device.
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _blocks(n):
     return -(-n // FP8_BLOCK)
 
 
-def _check_out(t, name, shape, dtype, device):
-    """The caller's output tensor (checked), or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+def _need(t, name, dtype, index):
+    """t must be a contiguous tensor of this type on this device."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == index
+            and t.is_contiguous()):
+        return
+    _check(t, name, dtype, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
+
+
+def _out(t, name, shape, dtype, index):
+    """The caller's output tensor, checked."""
+    _need(t, name, dtype, index)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     return t
 
 
+def _call(name, index, stream, *args):
+    """lib.name(*args, stream) with device `index` current."""
+    fn = getattr(load(), name)
+    if index < 0:
+        raise ValueError(f"{name} takes CUDA tensors")
+    if index == torch.cuda.current_device():
+        if stream is not None:
+            handle = stream.cuda_stream
+        elif _raw_stream is not None:
+            handle = _raw_stream(index)
+        else:
+            handle = torch.cuda.current_stream().cuda_stream
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _stream_handle(stream))
+    if rc != 0:
+        raise GDNError(name, rc)
+
+
+def _ws(workspace):
+    """(address, bytes) of a caller workspace as integers."""
+    p, n = _ws_args(workspace)
+    return p.value, n
+
+
 def _norm_inputs(x, w, residual, s):
-    dev, io = x.device, x.dtype
-    _io_code(io)
-    _check(x, "x", io, dev)
-    if x.dim() < 1:
+    """(device index, dim, address of residual or None, the sum's tensor)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    index, io, shape = x.get_device(), x.dtype, x.shape
+    if not shape:
         raise ValueError("x must be [.., dim]")
-    _check(w, "w", torch.float32, dev)
-    if tuple(w.shape) != (x.shape[-1],):
-        raise ValueError(f"w must be [{x.shape[-1]}]")
+    _need(x, "x", io, index)
+    _need(w, "w", torch.float32, index)
+    if w.dim() != 1 or w.shape[0] != shape[-1]:
+        raise ValueError(f"w must be [{shape[-1]}]")
     if residual is None:
         if s is not None:
             raise ValueError("s goes with a residual (without one the sum is x)")
-        return None
-    _check(residual, "residual", io, dev)
-    if residual.shape != x.shape:
+        return index, shape, None, None
+    _need(residual, "residual", io, index)
+    if residual.shape != shape:
         raise ValueError("residual must be shaped like x")
-    return _check_out(s, "s", x.shape, io, dev)
+    return index, shape, residual.data_ptr(), (torch.empty_like(x) if s is None else
+                                               _out(s, "s", shape, io, index))
 
 
 def residual_norm(x, w, residual=None, eps=1e-5, s=None, y=None, stream=None):
@@ -663,17 +702,14 @@ def residual_norm(x, w, residual=None, eps=1e-5, s=None, y=None, stream=None):
     over the last axis.  x, residual [.., dim] bf16 or fp32; w [dim] fp32.
     Returns (y, s); s is x itself without a residual.  ``s=residual`` updates
     the residual stream in place."""
-    lib = load()
-    s_out = _norm_inputs(x, w, residual, s)
-    y = _check_out(y, "y", x.shape, x.dtype, x.device)
-    dim = x.shape[-1]
-    with torch.cuda.device(x.device):
-        rc = lib.gdn_residual_norm(_ptr(x), _ptr(residual), _ptr(w), float(eps), _ptr(s_out),
-                                   _ptr(y), x.numel() // max(dim, 1), dim, _io_code(x.dtype),
-                                   _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_residual_norm", rc)
-    return y, x if s_out is None else s_out
+    code = _io_code(x.dtype)
+    index, shape, r, total = _norm_inputs(x, w, residual, s)
+    y = torch.empty_like(x) if y is None else _out(y, "y", shape, x.dtype, index)
+    dim = shape[-1]
+    _call("gdn_residual_norm", index, stream, x.data_ptr(), r, w.data_ptr(), eps,
+          None if total is None else total.data_ptr(), y.data_ptr(), x.numel() // max(dim, 1), dim,
+          code)
+    return y, x if total is None else total
 
 
 def residual_norm_fp8(x, w, residual=None, eps=1e-5, s=None, q=None, scale=None, stream=None):
@@ -681,19 +717,17 @@ def residual_norm_fp8(x, w, residual=None, eps=1e-5, s=None, q=None, scale=None,
     Returns (q, scale, s): q [.., dim] float8_e4m3fn and scale
     [.., ceil(dim / 128)] fp32, y ~ q * scale per 128 columns, as
     :func:`linear_fp8` reads them."""
-    lib = load()
-    s_out = _norm_inputs(x, w, residual, s)
-    dim = x.shape[-1]
-    q = _check_out(q, "q", x.shape, FP8, x.device)
-    scale = _check_out(scale, "scale", tuple(x.shape[:-1]) + (_blocks(dim),), torch.float32,
-                       x.device)
-    with torch.cuda.device(x.device):
-        rc = lib.gdn_residual_norm_fp8(_ptr(x), _ptr(residual), _ptr(w), float(eps), _ptr(s_out),
-                                       _ptr(q), _ptr(scale), x.numel() // max(dim, 1), dim,
-                                       _io_code(x.dtype), _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_residual_norm_fp8", rc)
-    return q, scale, x if s_out is None else s_out
+    code = _io_code(x.dtype)
+    index, shape, r, total = _norm_inputs(x, w, residual, s)
+    dim = shape[-1]
+    q = torch.empty_like(x, dtype=FP8) if q is None else _out(q, "q", shape, FP8, index)
+    sc_shape = (*shape[:-1], -(-dim // FP8_BLOCK))
+    scale = (torch.empty(sc_shape, dtype=torch.float32, device=x.device) if scale is None else
+             _out(scale, "scale", sc_shape, torch.float32, index))
+    _call("gdn_residual_norm_fp8", index, stream, x.data_ptr(), r, w.data_ptr(), eps,
+          None if total is None else total.data_ptr(), q.data_ptr(), scale.data_ptr(),
+          x.numel() // max(dim, 1), dim, code)
+    return q, scale, x if total is None else total
 
 
 def residual_norm_backward_workspace_size(tokens, dim, io_dtype=torch.bfloat16) -> int:
@@ -708,33 +742,23 @@ def residual_norm_backward(dy, s, w, ds=None, eps=1e-5, stream=None, workspace=N
     [.., dim] of y, ds of s from its other uses (or None), s as the forward
     call returned it.  Returns dict dx (the gradient of x and of residual
     alike, dtype of s) and dw [dim] fp32."""
-    lib = load()
-    dev, io = s.device, s.dtype
-    _io_code(io)
-    for name, t in (("s", s), ("dy", dy), ("ds", ds)):
-        if t is not None:
-            _check(t, name, io, dev)
-            if t.shape != s.shape:
-                raise ValueError(f"{name} must be shaped like s")
-        elif name != "ds":
-            raise TypeError(f"{name} must be a torch.Tensor")
-    if s.dim() < 1:
-        raise ValueError("s must be [.., dim]")
-    _check(w, "w", torch.float32, dev)
-    dim = s.shape[-1]
-    if tuple(w.shape) != (dim,):
-        raise ValueError(f"w must be [{dim}]")
+    code = _io_code(s.dtype)
+    index, shape, _, _ = _norm_inputs(s, w, None, None)
+    _need(dy, "dy", s.dtype, index)
+    if dy.shape != shape:
+        raise ValueError("dy must be shaped like s")
+    if ds is not None:
+        _need(ds, "ds", s.dtype, index)
+        if ds.shape != shape:
+            raise ValueError("ds must be shaped like s")
     g = dict(dx=torch.empty_like(s), dw=torch.empty_like(w))
-    with torch.cuda.device(dev):
-        args = (_ptr(dy), _ptr(s), _ptr(w), _ptr(ds), float(eps), _ptr(g["dx"]), _ptr(g["dw"]),
-                s.numel() // max(dim, 1), dim, _io_code(io))
-        if workspace is None:
-            rc = lib.gdn_residual_norm_backward(*args, _stream_handle(stream))
-        else:
-            rc = lib.gdn_residual_norm_backward_ws(*args, *_ws_args(workspace),
-                                                   _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_residual_norm_backward", rc)
+    dim = shape[-1]
+    args = (dy.data_ptr(), s.data_ptr(), w.data_ptr(), None if ds is None else ds.data_ptr(), eps,
+            g["dx"].data_ptr(), g["dw"].data_ptr(), s.numel() // max(dim, 1), dim, code)
+    if workspace is None:
+        _call("gdn_residual_norm_backward", index, stream, *args)
+    else:
+        _call("gdn_residual_norm_backward_ws", index, stream, *args, *_ws(workspace))
     return g
 
 
@@ -743,23 +767,21 @@ def quantize_fp8(x, block_rows=1, q=None, scale=None, stream=None):
     (``gdn_quantize_fp8``): 1 x 128 blocks for activations, with
     ``block_rows=128`` 128 x 128 blocks for a weight [n, k].  Returns
     (q, scale)."""
-    lib = load()
-    _io_code(x.dtype)
-    _check(x, "x", x.dtype, x.device)
-    if x.dim() < 1 or (block_rows != 1 and x.dim() != 2):
+    code = _io_code(x.dtype)
+    index, shape = x.get_device(), x.shape
+    _need(x, "x", x.dtype, index)
+    if not shape or (block_rows != 1 and len(shape) != 2):
         raise ValueError("x must be [.., cols] (a weight [n, k] with block_rows=128)")
     if block_rows not in (1, FP8_BLOCK):
         raise ValueError("block_rows must be 1 or 128")
-    cols = x.shape[-1]
+    cols = shape[-1]
     rows = x.numel() // max(cols, 1)
-    lead = tuple(x.shape[:-1]) if block_rows == 1 else (_blocks(rows),)
-    q = _check_out(q, "q", x.shape, FP8, x.device)
-    scale = _check_out(scale, "scale", lead + (_blocks(cols),), torch.float32, x.device)
-    with torch.cuda.device(x.device):
-        rc = lib.gdn_quantize_fp8(_ptr(x), _ptr(q), _ptr(scale), rows, cols, block_rows,
-                                  _io_code(x.dtype), _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_quantize_fp8", rc)
+    sc_shape = (*(shape[:-1] if block_rows == 1 else (_blocks(rows),)), _blocks(cols))
+    q = torch.empty_like(x, dtype=FP8) if q is None else _out(q, "q", shape, FP8, index)
+    scale = (torch.empty(sc_shape, dtype=torch.float32, device=x.device) if scale is None else
+             _out(scale, "scale", sc_shape, torch.float32, index))
+    _call("gdn_quantize_fp8", index, stream, x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows,
+          cols, block_rows, code)
     return q, scale
 
 
@@ -769,58 +791,58 @@ def linear_fp8(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, strea
     w_scale [ceil(n / 128), ceil(k / 128)] (as :func:`residual_norm_fp8` and
     :func:`quantize_fp8` give them).  Returns out [.., n] in ``out_dtype``
     (bf16 or fp32)."""
-    lib = load()
-    dev = x.device
-    _io_code(out_dtype)
-    _check(x, "x", FP8, dev)
-    _check(w, "w", FP8, dev)
-    _check(x_scale, "x_scale", torch.float32, dev)
-    _check(w_scale, "w_scale", torch.float32, dev)
-    if x.dim() < 1 or w.dim() != 2 or w.shape[1] != x.shape[-1]:
+    code = _io_code(out_dtype)
+    index = x.get_device()
+    _need(x, "x", FP8, index)
+    _need(w, "w", FP8, index)
+    _need(x_scale, "x_scale", torch.float32, index)
+    _need(w_scale, "w_scale", torch.float32, index)
+    shape = x.shape
+    if not shape or w.dim() != 2 or w.shape[1] != shape[-1]:
         raise ValueError("x must be [.., k] and w [n, k]")
     n, k = w.shape
-    lead = tuple(x.shape[:-1])
-    if tuple(x_scale.shape) != lead + (_blocks(k),):
-        raise ValueError(f"x_scale must be {list(lead + (_blocks(k),))}")
-    if tuple(w_scale.shape) != (_blocks(n), _blocks(k)):
-        raise ValueError(f"w_scale must be [{_blocks(n)}, {_blocks(k)}]")
-    out = _check_out(out, "out", lead + (n,), out_dtype, dev)
-    with torch.cuda.device(dev):
-        rc = lib.gdn_linear_fp8(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out),
-                                x.numel() // max(k, 1), k, n, _io_code(out_dtype),
-                                _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_linear_fp8", rc)
+    blocks, lead = -(-k // FP8_BLOCK), shape[:-1]
+    if x_scale.shape != (*lead, blocks):
+        raise ValueError(f"x_scale must be {[*lead, blocks]}")
+    if w_scale.shape != (-(-n // FP8_BLOCK), blocks):
+        raise ValueError(f"w_scale must be [{_blocks(n)}, {blocks}]")
+    if out is None:
+        out = torch.empty((*lead, n), dtype=out_dtype, device=x.device)
+    else:
+        _out(out, "out", (*lead, n), out_dtype, index)
+    _call("gdn_linear_fp8", index, stream, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
+          w_scale.data_ptr(), out.data_ptr(), x.numel() // max(k, 1), k, n, code)
     return out
 
 
 def _ffn_inputs(x, w_gate, w_up, act):
-    dev, io = x.device, x.dtype
-    if io != torch.bfloat16:
+    """(device index, shape of x, hidden)."""
+    io = torch.bfloat16
+    if x.dtype != io:
         raise TypeError("the gated feed-forward takes bf16 tensors")
     if act not in GATE_ACT:
         raise ValueError(f"act must be one of {sorted(GATE_ACT)}")
-    for name, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up)):
-        _check(t, name, io, dev)
-    if x.dim() < 1 or w_gate.dim() != 2 or w_gate.shape[1] != x.shape[-1] \
-            or w_up.shape != w_gate.shape:
+    index, shape, w_shape = x.get_device(), x.shape, w_gate.shape
+    _need(x, "x", io, index)
+    _need(w_gate, "w_gate", io, index)
+    _need(w_up, "w_up", io, index)
+    if not shape or len(w_shape) != 2 or w_shape[1] != shape[-1] or w_up.shape != w_shape:
         raise ValueError("x must be [.., dim], w_gate and w_up [hidden, dim]")
-    hidden, dim = w_gate.shape
-    return x.numel() // max(dim, 1), dim, hidden
+    return index, shape, w_shape[0]
 
 
 def gated_ffn(x, w_gate, w_up, act="silu", h=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T) in one kernel (``gdn_gated_ffn``):
     x [.., dim], w_gate and w_up [hidden, dim], all bf16.  Returns h
     [.., hidden]."""
-    lib = load()
-    tokens, dim, hidden = _ffn_inputs(x, w_gate, w_up, act)
-    h = _check_out(h, "h", tuple(x.shape[:-1]) + (hidden,), x.dtype, x.device)
-    with torch.cuda.device(x.device):
-        rc = lib.gdn_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), GATE_ACT[act], _ptr(h), tokens,
-                               dim, hidden, GDN_BF16, _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_gated_ffn", rc)
+    index, shape, hidden = _ffn_inputs(x, w_gate, w_up, act)
+    dim, h_shape = shape[-1], (*shape[:-1], hidden)
+    if h is None:
+        h = torch.empty(h_shape, dtype=torch.bfloat16, device=x.device)
+    else:
+        _out(h, "h", h_shape, torch.bfloat16, index)
+    _call("gdn_gated_ffn", index, stream, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+          GATE_ACT[act], h.data_ptr(), x.numel() // max(dim, 1), dim, hidden, GDN_BF16)
     return h
 
 
@@ -834,23 +856,20 @@ def gated_ffn_backward_workspace_size(tokens, dim, hidden, io_dtype=torch.bfloat
 def gated_ffn_backward(x, w_gate, w_up, dh, act="silu", stream=None, workspace=None):
     """Gradients of :func:`gated_ffn` from its inputs and dh [.., hidden]
     (``gdn_gated_ffn_backward``).  Returns dict dx, dw_gate, dw_up (bf16)."""
-    lib = load()
-    tokens, dim, hidden = _ffn_inputs(x, w_gate, w_up, act)
-    _check(dh, "dh", x.dtype, x.device)
-    if tuple(dh.shape) != tuple(x.shape[:-1]) + (hidden,):
-        raise ValueError(f"dh must be {list(x.shape[:-1]) + [hidden]}")
+    index, shape, hidden = _ffn_inputs(x, w_gate, w_up, act)
+    _need(dh, "dh", torch.bfloat16, index)
+    if dh.shape != (*shape[:-1], hidden):
+        raise ValueError(f"dh must be {[*shape[:-1], hidden]}")
     g = dict(dx=torch.empty_like(x), dw_gate=torch.empty_like(w_gate),
              dw_up=torch.empty_like(w_up))
-    with torch.cuda.device(x.device):
-        args = (_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(dh), GATE_ACT[act], _ptr(g["dx"]),
-                _ptr(g["dw_gate"]), _ptr(g["dw_up"]), tokens, dim, hidden, GDN_BF16)
-        if workspace is None:
-            rc = lib.gdn_gated_ffn_backward(*args, _stream_handle(stream))
-        else:
-            rc = lib.gdn_gated_ffn_backward_ws(*args, *_ws_args(workspace),
-                                               _stream_handle(stream))
-    if rc != 0:
-        raise GDNError("gdn_gated_ffn_backward", rc)
+    dim = shape[-1]
+    args = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), dh.data_ptr(), GATE_ACT[act],
+            g["dx"].data_ptr(), g["dw_gate"].data_ptr(), g["dw_up"].data_ptr(),
+            x.numel() // max(dim, 1), dim, hidden, GDN_BF16)
+    if workspace is None:
+        _call("gdn_gated_ffn_backward", index, stream, *args)
+    else:
+        _call("gdn_gated_ffn_backward_ws", index, stream, *args, *_ws(workspace))
     return g
 
 

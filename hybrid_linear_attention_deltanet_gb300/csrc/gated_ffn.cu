@@ -17,7 +17,7 @@
 // has the tiles of dx (K runs over dG then dU) and of both weight gradients
 // (rows over dG^T then dU^T), the longer K first, so that the short tiles
 // fill the end of the grid.
-#include "gemm_pair.cuh"
+#include "gemm_split.cuh"
 #include "hostcheck.cuh"
 
 namespace gdn {
@@ -61,6 +61,11 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
   return true;
 }
 
+// Few tokens: the split form.
+bool takes_split(int64_t tokens, int32_t hidden) {
+  return tokens <= 128 && (hidden + 63) / 64 <= 65535;
+}
+
 int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void* h,
                 int64_t tokens, int32_t dim, int32_t hidden, int32_t io, cudaStream_t stream) {
   if (const int rc = shape_check(tokens, dim, hidden, act, io)) return rc;
@@ -73,12 +78,31 @@ int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void
   const Span ins[] = {span_of(x, (size_t)tokens * dim * 2), span_of(wg, wb), span_of(wu, wb)};
   const Span outs[] = {span_of(h, (size_t)tokens * hidden * 2)};
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  unsigned* status = status_ptr();
+  if (sms < 2 || !status) return GDN_ERR_CUDA;
+  if (takes_split(tokens, hidden)) {
+    gemm::SplitArgs a;
+    memset(&a, 0, sizeof a);
+    const int nb = gemm::split_columns(tokens);
+    a.k_blocks = (dim + 63) / 64;
+    a.tokens = (int32_t)tokens;
+    a.n = hidden;
+    a.act = act;
+    a.out = h;
+    a.status = status;
+    if (!gemm::matrix_map(&a.w[0], wg, false, dim, hidden, (int64_t)dim * 2, 64) ||
+        !gemm::matrix_map(&a.w[1], wu, false, dim, hidden, (int64_t)dim * 2, 64) ||
+        !gemm::matrix_map(&a.x, x, false, dim, tokens, (int64_t)dim * 2, nb))
+      return GDN_ERR_CUDA;
+    return gemm::launch_split<false, true, __nv_bfloat16>(a, nb, sms, stream) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+  }
   gemm::PairArgs g;
   memset(&g, 0, sizeof g);
-  const int sms = sm_count();
-  g.status = status_ptr();
-  if (sms < 2 || !g.status || !projections(g, x, wg, wu, tokens, dim, hidden))
-    return GDN_ERR_CUDA;
+  g.status = status;
+  if (!projections(g, x, wg, wu, tokens, dim, hidden)) return GDN_ERR_CUDA;
   g.act = act;
   g.p[0].out[0] = g.p[0].out[1] = h;
   g.p[0].ldc = hidden;

@@ -78,7 +78,7 @@ constexpr int kGroup = 4;                            // K blocks whose scales tr
 
 template <bool kFp8>
 struct Shape {
-  static constexpr int kEpiWarps = kFp8 ? 16 : 8;
+  static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kStages = kFp8 ? 5 : 6;
   static constexpr int kRow = kFp8 ? 64 : 128;       // bytes of a row of a warp's staging
@@ -386,13 +386,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       const int row0 = tl.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
       const bool live = row < p.M;
       if constexpr (kFp8) {
-        // this thread's 64 columns lie in one column block of the scales
-        const int n0 = tl.n0 + 64 * part;
-        const float* sc = scales + 128 * (part >> 1) + 32 * q + lane;
+        // this thread's 128 columns are one column block of the scales
+        const int n0 = tl.n0 + 128 * part;
+        const float* sc = scales + 128 * part + 32 * q + lane;
         const int k_blocks = p.k_blocks;
-        F2 acc[32];
+        F2 acc[64];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] = f2(0.f, 0.f);
+        for (int i = 0; i < 64; ++i) acc[i] = f2(0.f, 0.f);
         for (int kb = 0; kb < k_blocks; ++kb) {
           const int j = kb % kGroup;
           if (j == 0) {
@@ -403,16 +403,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
           ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
           if (!ok) break;
           tc_fence_after();
+          // two 32-column pieces in turn: one is added while the next arrives
+          const uint32_t src = tmem + lanes + 256 * buf + 128 * part;
+          uint32_t r[2][32];
+          tmem_ld32(src, r[0]);
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(tmem + lanes + 256 * buf + 64 * part + c, r);
-            tmem_ld_wait_regs(r);
-            if (c == 32) release();
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait_regs(r[c & 1]);
+            if (c < 3) tmem_ld32(src + 32 * (c + 1), r[(c + 1) & 1]);
+            else release();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              acc[c / 2 + i] = f2_fma(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                                      f2(s, s), acc[c / 2 + i]);
+              acc[16 * c + i] = f2_fma(f2(__uint_as_float(r[c & 1][2 * i]),
+                                          __uint_as_float(r[c & 1][2 * i + 1])),
+                                       f2(s, s), acc[16 * c + i]);
           }
           advance();
           if (j == kGroup - 1 || kb + 1 == k_blocks) {
@@ -425,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         using T = typename std::conditional<kEpi == kStoreF32, float, __nv_bfloat16>::type;
         constexpr int kCols = kRow / (int)sizeof(T);   // 32 bf16 or 16 fp32
 #pragma unroll
-        for (int c = 0; c < 64; c += kCols) {
+        for (int c = 0; c < 128; c += kCols) {
           float v[kCols];
 #pragma unroll
           for (int i = 0; i < kCols / 2; ++i) f2_split(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);

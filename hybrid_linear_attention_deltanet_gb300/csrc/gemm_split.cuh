@@ -1,0 +1,318 @@
+// Matrix products of few tokens on the tensor cores, the K axis split over a
+// thread-block cluster.
+//
+// With few tokens the weights are all there is to read, so they take the
+// MMA's 128 rows and the tokens its columns: a CTA multiplies 128 rows of the
+// weights (gated: 64 of Wg and 64 of Wu, the same features) by kNB tokens
+// over its share of K, and the CTAs of a cluster, one share each, add their
+// fp32 partial products through each other's shared memory, in a fixed order.
+// One launch, whose CTAs (two an SM) hold all of the weights' bytes in
+// flight that their stages allow.
+//
+// Roles (6 warps): warps 0..3 take accumulators out, warp 4 fetches, warp 5
+// multiplies.  8-bit operands: every K block of 128 is an accumulator of its
+// own, scaled (a token's scale times the weight block's) into fp32 registers.
+// Waits are bounded as in gemm_pair.cuh.
+#pragma once
+
+#include "gemm_pair.cuh"
+
+namespace gdn {
+namespace gemm {
+
+struct SplitArgs {
+  CUtensorMap w[2], x;   // weights (gated: Wg, Wu), tokens
+  int32_t k_blocks;      // of 128 bytes
+  int32_t tokens, n;     // n: rows of the weights (gated: features)
+  int32_t act;
+  void* out;             // [tokens][n]
+  const float* sx;       // 8-bit: [tokens][k_blocks]
+  const float* sw;       //        [ceil(n / 128)][k_blocks]
+  unsigned* status;
+};
+
+constexpr int kSplitThreads = 192;
+constexpr int kSplitScaleBytes = 16384;   // of a CTA's staged scales
+
+template <bool kFp8, int kNB>
+struct SplitShape {
+  static constexpr uint32_t kStage = kOperand + kNB * 128;
+  static constexpr int kStages = kNB <= 16 ? 5 : kNB <= 64 ? 4 : 3;
+  static constexpr int kAcc = !kFp8 ? 1 : kNB <= 64 ? 4 : 2;   // accumulators in tensor memory
+  static constexpr uint32_t kCols = kAcc * kNB < 32 ? 32 : kAcc * kNB;
+  static constexpr uint32_t kSmem = kStages * kStage + (kFp8 ? kSplitScaleBytes : 0) + 1024;
+  static_assert(kNB * 128 * 4 <= kStages * kStage, "the partial products reuse the stages");
+};
+
+template <bool kFp8, bool kGated, int kNB, typename T>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    split_gemm_kernel(const __grid_constant__ SplitArgs g) {
+  using S = SplitShape<kFp8, kNB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align_smem_1024(smem_raw);
+  float* scales = reinterpret_cast<float*>(sm + S::kStages * S::kStage);   // [K block][kNB]
+  float* part = reinterpret_cast<float*>(sm);                              // [kNB][128]
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[S::kAcc], acc_empty[S::kAcc];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rank = blockIdx.x, split = gridDim.x;   // the cluster spans x
+  const int kb0 = (int)((int64_t)g.k_blocks * rank / split);
+  const int kbs = (int)((int64_t)g.k_blocks * (rank + 1) / split) - kb0;
+  const int rows = kGated ? 64 : 128;
+  const int f0 = blockIdx.y * rows, t0 = blockIdx.z * kNB;
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < S::kAcc; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 5) tmem_alloc(&tmem_base, S::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  bool ok = true;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- fetch
+    const bool lead = elect_one();
+    int st = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < kbs; ++i) {
+      ok = mbar_wait_warp(&empty[st], ph ^ 1u, kWaitNs);
+      if (!ok) break;
+      if (lead) {
+        uint8_t* W = sm + st * S::kStage;
+        const int k = (kb0 + i) * (kFp8 ? 128 : 64);
+        mbar_arrive_expect_tx(&full[st], S::kStage);
+        if (kGated) {
+          tma_load_2d(W, &g.w[0], k, f0, &full[st]);
+          tma_load_2d(W + 8192, &g.w[1], k, f0, &full[st]);
+        } else {
+          tma_load_2d(W, &g.w[0], k, f0, &full[st]);
+        }
+        tma_load_2d(W + kOperand, &g.x, k, t0, &full[st]);
+      }
+      __syncwarp();
+      if (++st == S::kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  } else if (warp == 5) {
+    // -------------------------------------------------------- multiply
+    const bool lead = elect_one();
+    const uint64_t w0 = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+    constexpr uint32_t idesc = kFp8 ? idesc_e4m3(128, kNB) : idesc_bf16(128, kNB, 0, 0);
+    int st = 0, buf = 0;
+    uint32_t ph = 0, aph = 0;
+    for (int i = 0; i < kbs; ++i) {
+      if (kFp8) {
+        ok = mbar_wait_warp(&acc_empty[buf], aph ^ 1u, kWaitNs);
+        if (!ok) break;
+      }
+      ok = mbar_wait_warp(&full[st], ph, kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      if (lead) {
+        const uint64_t wd = w0 + (uint64_t)(st * (S::kStage >> 4)), xd = wd + (kOperand >> 4);
+        const uint32_t d = tmem + kNB * buf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (kFp8) mma_f8(d, wd + 2 * j, xd + 2 * j, idesc, j != 0);
+          else mma_bf16(d, wd + 2 * j, xd + 2 * j, idesc, (i | j) != 0);
+        }
+        mma_commit(&empty[st]);
+        if (kFp8 || i + 1 == kbs) mma_commit(&acc_full[buf]);
+      }
+      __syncwarp();
+      if (kFp8 && ++buf == S::kAcc) {
+        buf = 0;
+        aph ^= 1u;
+      }
+      if (++st == S::kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  } else {
+    // ------------------------------------- accumulators out of tensor memory
+    const uint32_t src = tmem + ((uint32_t)(32 * warp) << 16);
+    float acc[kNB];
+    if constexpr (kFp8) {
+      const float* sw = g.sw + (size_t)(f0 / 128) * g.k_blocks + kb0;
+      for (int e = tid; e < kbs * kNB; e += 128) {
+        const int c = e / kbs, i = e - c * kbs;   // consecutive threads: one token's blocks
+        scales[i * kNB + c] =
+            t0 + c < g.tokens ? __ldg(g.sx + (size_t)(t0 + c) * g.k_blocks + kb0 + i) * __ldg(sw + i)
+                              : 0.f;
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");   // these four warps
+#pragma unroll
+      for (int c = 0; c < kNB; ++c) acc[c] = 0.f;
+      int buf = 0;
+      uint32_t aph = 0;
+      for (int i = 0; i < kbs; ++i) {
+        ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const float4* s4 = reinterpret_cast<const float4*>(scales + i * kNB);
+        uint32_t r[2][16];   // two 16-column pieces in turn: one arrives while one is added
+        tmem_ld16(src + kNB * buf, r[0]);
+#pragma unroll
+        for (int c = 0; c < kNB; c += 16) {
+          uint32_t(&x)[16] = r[(c / 16) & 1];
+          tmem_ld_wait_regs(x);
+          if (c + 16 < kNB) {
+            tmem_ld16(src + kNB * buf + c + 16, r[(c / 16 + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float4 s = s4[c / 4 + v];
+            acc[c + 4 * v] = fmaf(__uint_as_float(x[4 * v]), s.x, acc[c + 4 * v]);
+            acc[c + 4 * v + 1] = fmaf(__uint_as_float(x[4 * v + 1]), s.y, acc[c + 4 * v + 1]);
+            acc[c + 4 * v + 2] = fmaf(__uint_as_float(x[4 * v + 2]), s.z, acc[c + 4 * v + 2]);
+            acc[c + 4 * v + 3] = fmaf(__uint_as_float(x[4 * v + 3]), s.w, acc[c + 4 * v + 3]);
+          }
+        }
+        if (++buf == S::kAcc) {
+          buf = 0;
+          aph ^= 1u;
+        }
+      }
+    } else {
+      ok = mbar_wait_warp(&acc_full[0], 0, kWaitNs);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kNB; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(src + c, r);
+        tmem_ld_wait_regs(r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c + i] = __uint_as_float(r[i]);
+      }
+      tc_fence_before();
+    }
+    // the last accumulator is complete, so are all products and copies: the
+    // stages are free
+    if (ok) {
+#pragma unroll
+      for (int c = 0; c < kNB; ++c) part[c * 128 + tid] = acc[c];
+    }
+  }
+  if (!ok) {
+    flag_status(g.status, GDN_ERR_TIMEOUT);
+    const uint64_t from = globaltimer_ns();
+    while (globaltimer_ns() - from < 5000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  cluster_sync_all();
+  if (warp < 4) {
+    // four rows a lane: a column of the tile is 32 lanes (gated: 16, G and U
+    // 64 rows apart); the columns are dealt to the cluster's CTAs in turn
+    const uint32_t p0 = smem_u32(part);
+    uint32_t base[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < split) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[s]) : "r"(p0), "r"(s));
+    constexpr int kLanes = kGated ? 16 : 32, kSlots = 128 / kLanes;
+    const int cols = g.tokens - t0 < kNB ? g.tokens - t0 : kNB;
+    const int row = 4 * (tid % kLanes), f = f0 + row;
+    if (f < g.n) {
+#pragma unroll 2
+      for (int c = rank + split * (tid / kLanes); c < cols; c += split * kSlots) {
+        const uint32_t o = (uint32_t)(c * 128 + row) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < split) {
+            const float4 a = ld_shared_cluster4(base[s] + o);
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+            if (kGated) {
+              const float4 b = ld_shared_cluster4(base[s] + o + 256);
+              u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
+            }
+          }
+        if (kGated)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = gate_act(v[i], g.act) * u[i];
+        T* out = (T*)g.out + (size_t)(t0 + c) * g.n + f;
+        if (g.n % 4 == 0) {   // rows start on four elements
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+          else
+            *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (f + i < g.n) st_out(out + i, v[i]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();   // no CTA leaves while another may read its partial products
+  if (warp == 5) tmem_dealloc(tmem, S::kCols);
+}
+
+// Columns of the MMA that hold `tokens`: 16, 32, 64 or 128.
+inline int split_columns(int64_t tokens) {
+  return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
+}
+// CTAs a cluster splits K over: as many as two an SM allow, at least two K
+// blocks each, eight at most.
+inline int split_of(int64_t units, int k_blocks, int sms) {
+  int64_t s = 2 * (int64_t)sms / units;
+  if (s > k_blocks / 2) s = k_blocks / 2;
+  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+}
+
+template <bool kFp8, bool kGated, int kNB, typename T>
+cudaError_t launch_split_nb(const SplitArgs& g, int sms, cudaStream_t st) {
+  using S = SplitShape<kFp8, kNB>;
+  auto kern = split_gemm_kernel<kFp8, kGated, kNB, T>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned ny = (unsigned)((g.n + (kGated ? 63 : 127)) / (kGated ? 64 : 128));
+  const unsigned nz = (unsigned)((g.tokens + kNB - 1) / kNB);
+  const unsigned split = (unsigned)split_of((int64_t)ny * nz, g.k_blocks, sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split, ny, nz);
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, g);
+  count_launches(1);
+  return e;
+}
+
+template <bool kFp8, bool kGated, typename T>
+cudaError_t launch_split(const SplitArgs& g, int nb, int sms, cudaStream_t st) {
+  switch (nb) {
+    case 16: return launch_split_nb<kFp8, kGated, 16, T>(g, sms, st);
+    case 32: return launch_split_nb<kFp8, kGated, 32, T>(g, sms, st);
+    case 64: return launch_split_nb<kFp8, kGated, 64, T>(g, sms, st);
+    default: return launch_split_nb<kFp8, kGated, 128, T>(g, sms, st);
+  }
+}
+
+}  // namespace gemm
+}  // namespace gdn

@@ -6,13 +6,23 @@
 //
 // The inner sums run on the tensor cores (kind::f8f6f4, fp32 accumulation),
 // the outer one in fp32 registers (gemm_pair.cuh).
-#include "gemm_pair.cuh"
+#include "gemm_split.cuh"
 #include "hostcheck.cuh"
 
 namespace gdn {
 namespace {
 
 using namespace hostcheck;
+
+// Few tokens: the split form (its scales must fit their staging).
+bool takes_split(int64_t tokens, int32_t n, int32_t blocks, int sms) {
+  if (tokens > 256) return false;
+  const int nb = gemm::split_columns(tokens);
+  const int64_t units = (int64_t)((n + 127) / 128) * ((tokens + nb - 1) / nb);
+  const int split = gemm::split_of(units, blocks, sms);
+  return (int64_t)((blocks + split - 1) / split) * nb * 4 <= gemm::kSplitScaleBytes &&
+         (n + 127) / 128 <= 65535;
+}
 
 int linear_common(const void* x, const float* sx, const void* w, const float* sw, void* out,
                   int64_t tokens, int32_t k, int32_t n, int32_t out_dtype, cudaStream_t stream) {
@@ -32,6 +42,29 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
                       span_of(sw, (size_t)((n + 127) / 128) * blocks * 4)};
   const Span outs[] = {span_of(out, (size_t)tokens * n * es)};
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  unsigned* status = status_ptr();
+  if (sms < 2 || !status) return GDN_ERR_CUDA;
+  if (takes_split(tokens, n, blocks, sms)) {
+    gemm::SplitArgs a;
+    memset(&a, 0, sizeof a);
+    const int nb = gemm::split_columns(tokens);
+    a.k_blocks = blocks;
+    a.tokens = (int32_t)tokens;
+    a.n = n;
+    a.out = out;
+    a.sx = sx;
+    a.sw = sw;
+    a.status = status;
+    if (!gemm::matrix_map(&a.w[0], w, true, k, n, k, 128) ||
+        !gemm::matrix_map(&a.x, x, true, k, tokens, k, nb))
+      return GDN_ERR_CUDA;
+    const cudaError_t e =
+        out_dtype == GDN_BF16
+            ? gemm::launch_split<true, false, __nv_bfloat16>(a, nb, sms, stream)
+            : gemm::launch_split<true, false, float>(a, nb, sms, stream);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  }
   gemm::PairArgs g;
   memset(&g, 0, sizeof g);
   gemm::Problem& p = g.p[0];
@@ -49,9 +82,7 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   g.sa = sx;
   g.sb = sw;
   g.sblocks = blocks;
-  g.status = status_ptr();
-  const int sms = sm_count();
-  if (!g.status || sms < 2) return GDN_ERR_CUDA;
+  g.status = status;
   if (!gemm::matrix_map(&p.a[0], x, true, k, tokens, k, 128) ||
       !gemm::matrix_map(&p.b[0], w, true, k, n, k, 128))
     return GDN_ERR_CUDA;

@@ -25,6 +25,7 @@ using namespace hostcheck;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDim = 8 * 8 * 256;   // 8 warps x 8 vectors x 256 columns
+constexpr int kFewRows = 304;            // two CTAs an SM of one row each
 constexpr float kTiny = 0x1p-100f;     // the smallest block maximum: its scale stays normal
 constexpr float kE4m3Max = 448.f;
 
@@ -161,6 +162,12 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(NormArgs a) {
     s[j].zero();
     if (live && c < a.dim) s[j].load((const T*)a.x + base + c);
   }
+  constexpr bool kEarlyW = kVPL <= 2;   // w in flight with the row: one latency, not two
+  float w[kEarlyW ? kVPL : 1][8];
+  if (kEarlyW)
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j)
+      if (col(j) < a.dim) load_w(a.w + col(j), w[j]);
   if (a.r) {
 #pragma unroll
     for (int j = 0; j < kVPL; ++j) {
@@ -195,11 +202,11 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(NormArgs a) {
     if (a.r && in && a.s) s[j].store((T*)a.s + base + c);
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (in) {
-      float w[8];
+      float(&wj)[8] = w[kEarlyW ? j : 0];
       s[j].widen(f);
-      load_w(a.w + c, w);
+      if (!kEarlyW) load_w(a.w + c, wj);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * rs * w[i];
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * rs * wj[i];
     }
     if (!kFp8) {
       if (in) {
@@ -429,9 +436,14 @@ struct Lay {
   static constexpr int V = kV, W = kW;
 };
 // `few`: at most 4 vectors a lane where 8 warps can hold the row so (the fp32
-// gradient, whose 8-vector form needs more than 255 registers).
+// gradient, whose 8-vector form needs more than 255 registers).  `spread`: 8
+// warps a row, for calls with fewer rows than warps to run them.
 template <typename F>
-void with_layout(int dim, bool few, F&& f) {
+void with_layout(int dim, bool few, bool spread, F&& f) {
+  const int u = (dim + 2047) / 2048;   // vectors a lane of eight warps would hold
+  if (spread && u <= 1) return f(Lay<1, 8>{});
+  if (spread && u <= 2) return f(Lay<2, 8>{});
+  if (spread && u <= 4) return f(Lay<4, 8>{});
   const int v = (dim + 255) / 256;   // vectors a lane of one warp would hold
   if (v <= 1) f(Lay<1, 1>{});
   else if (v <= 2) f(Lay<2, 1>{});
@@ -450,7 +462,7 @@ bool io_ok(int32_t io) { return io == GDN_BF16 || io == GDN_F32; }
 
 int launch_norm(const NormArgs& a, int32_t io, bool fp8, cudaStream_t st) {
   int rc = GDN_OK;
-  with_layout(a.dim, false, [&](auto lay) {
+  with_layout(a.dim, false, a.rows <= kFewRows, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
     const int64_t blocks = (a.rows + kWarps / W - 1) / (kWarps / W);
     if (blocks > 0x7fffffffLL) {
@@ -505,7 +517,7 @@ int norm_common(const void* x, const void* residual, const float* w, float eps, 
 // dw parts of the backward: one row of `dim` a CTA, one CTA an SM at most
 int backward_grid(int64_t tokens, int32_t dim, int32_t io) {
   int groups = 1;
-  with_layout(dim, io == GDN_F32, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
+  with_layout(dim, io == GDN_F32, false, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
   const int64_t want = (tokens + groups - 1) / groups;
   const int64_t cap = 152;   // the SMs of the device: a constant, so that the sums' order is one
   return (int)(want < cap ? want : cap);
@@ -540,7 +552,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   void* part = ws;
   if (!use_ws && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
   NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
-  with_layout(dim, io_dtype == GDN_F32, [&](auto lay) {
+  with_layout(dim, io_dtype == GDN_F32, false, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
     if (io_dtype == GDN_BF16)
       norm_backward_kernel<__nv_bfloat16, V, W><<<grid, kThreads, 0, stream>>>(a);

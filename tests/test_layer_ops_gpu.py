@@ -267,6 +267,12 @@ def test_linear_fp8(tokens, k, n, out_dtype):
     check_linear(tokens, k, n, out_dtype, tokens + k + n)
 
 
+@pytest.mark.parametrize("tokens", [1, 15, 16, 17, 31, 33, 64, 65, 100, 127, 128, 255, 257])
+@pytest.mark.parametrize("k,n", [(128, 40), (400, 257), (2048, 4608), (5136, 130)])
+def test_linear_fp8_few_tokens(tokens, k, n):
+    check_linear(tokens, k, n, BF16, tokens * k + n)
+
+
 def test_linear_fp8_many_tiles_and_unaligned_rows():
     check_linear(4000, 512, 5000, BF16, 5)           # more tiles than CTA pairs
     check_linear(300, 256, 264, BF16, 6, misaligned=True)
@@ -346,6 +352,19 @@ def test_gated_ffn(tokens, dim, hidden, act):
     G, U, a, da, eU, ea, _ = ffn_terms(x, wg, wu, act)
     ref = a * U
     within(h, ref, (2.0 ** -8 + 2.0 ** -22) * ref.abs() + 1.01 * (ea * U.abs() + a.abs() * eU), "h")
+    b.check()
+    assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 16, 17, 33, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("dim,hidden", [(64, 64), (200, 65), (2048, 6144), (4104, 131)])
+def test_gated_ffn_few_tokens(tokens, dim, hidden):
+    x, wg, wu, _ = ffn_inputs(tokens, dim, hidden, tokens * dim + hidden)
+    b = Guarded((tokens, hidden), BF16)
+    h = gdn.gated_ffn(x, wg, wu, h=b.t)
+    G, U, a, _, eU, ea, _ = ffn_terms(x, wg, wu, "silu")
+    within(h, a * U, (2.0 ** -8 + 2.0 ** -22) * (a * U).abs()
+           + 1.01 * (ea * U.abs() + a.abs() * eU), "h")
     b.check()
     assert gdn.device_status() == 0
 
