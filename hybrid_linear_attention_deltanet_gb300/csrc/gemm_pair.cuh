@@ -159,12 +159,15 @@ __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Pr
     constexpr int kCols = kRow / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
     const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
     T* out = (T*)p.out[half] + (size_t)row0 * p.ldc + n0;
-    for (int r = 0; r < rows; ++r)
 #pragma unroll
-      for (int c = lane; c < kCols; c += 32)
-        if (n0 + c < p.N)
-          out[(size_t)r * p.ldc + c] = *reinterpret_cast<const T*>(
-              buf + stage_piece<kRow>(r, c / kPer) + (c % kPer) * sizeof(T));
+    for (int i = 0; i < (kCols + 31) / 32; ++i) {
+      const int c = lane + 32 * i;
+      if (c >= kCols || n0 + c >= p.N) break;
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r)
+        out[(size_t)r * p.ldc + c] = *reinterpret_cast<const T*>(
+            buf + stage_piece<kRow>(r, c / kPer) + (c % kPer) * sizeof(T));
+    }
   }
 }
 __device__ __forceinline__ void stage_free(int lane) {
@@ -462,22 +465,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         const int f0 = tl.n0 / 2 + 64 * part;
         uint32_t dh[kEpi == kGateGrad ? 32 : 1];   // 64 bf16, fetched before the wait
         if constexpr (kEpi == kGateGrad) {
-          const __nv_bfloat16* d = g.dh + (size_t)(live ? row : 0) * g.ldh + f0;
-          if (live && g.dh_wide && f0 + 64 <= p.N) {
+          if (g.dh_wide) {   // hidden a multiple of 8: whole 16-byte pieces or none
+            const __nv_bfloat16* d = g.dh + (size_t)(live ? row : 0) * g.ldh + f0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const uint4 w = __ldg(reinterpret_cast<const uint4*>(d) + i);
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (live && f0 + 8 * i < p.N) w = __ldg(reinterpret_cast<const uint4*>(d) + i);
               dh[4 * i] = w.x; dh[4 * i + 1] = w.y; dh[4 * i + 2] = w.z; dh[4 * i + 3] = w.w;
             }
-          } else {
-            const unsigned short* u = reinterpret_cast<const unsigned short*>(d);
+          } else {           // rows that start anywhere: a row at a time through the staging
+            stage_free(lane);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              uint32_t lo = 0, hi = 0;
-              if (live && f0 + 2 * i < p.N) lo = __ldg(u + 2 * i);
-              if (live && f0 + 2 * i + 1 < p.N) hi = __ldg(u + 2 * i + 1);
-              dh[i] = lo | (hi << 16);
+            for (int i = 0; i < 2; ++i) {
+              const int c = lane + 32 * i;
+#pragma unroll 8
+              for (int r = 0; r < 32; ++r) {
+                __nv_bfloat16 v = __float2bfloat16_rn(0.f);
+                if (row0 + r < p.M && f0 + c < p.N) v = g.dh[(size_t)(row0 + r) * g.ldh + f0 + c];
+                *reinterpret_cast<__nv_bfloat16*>(bounce + stage_piece<kRow>(r, c / 8) +
+                                                  (c % 8) * 2) = v;
+              }
             }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 w = *reinterpret_cast<const uint4*>(bounce + stage_piece<kRow>(lane, i));
+              dh[4 * i] = w.x; dh[4 * i + 1] = w.y; dh[4 * i + 2] = w.z; dh[4 * i + 3] = w.w;
+            }
+            __syncwarp();   // read before the staging is written again
           }
         }
         ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);

@@ -106,17 +106,37 @@ __device__ __forceinline__ float amax8(const float (&y)[8]) {
   for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
   return m;
 }
-// 8 e4m3 codes of y * inv (round to nearest even; NaN keeps a NaN code)
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+// 8 e4m3 codes of v (round to nearest even, ties in v as they stand; a NaN
+// keeps a NaN code).
+__device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv)), __NV_SATFINITE,
-        __NV_E4M3);
+    const __nv_fp8x2_storage_t c =
+        __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
     w[i >> 1] |= (uint32_t)c << (16 * (i & 1));
   }
   return make_uint2(w[0], w[1]);
+}
+// Is v (an e4m3 value's size, not below its normal range) within 16 units in
+// its last place of the middle between two e4m3 values?  fp32 gets y (448 / m)
+// to about 3, so elsewhere its rounding is that of the real number.
+__device__ __forceinline__ bool near_tie(float v) {
+  return (__float_as_uint(v) & 0xfffffu) - 0x7fff0u <= 0x20u;
+}
+// v, which is near the tie t, moved to where 448 p / m lies: on t or beside it.
+// p = ph + pl and m = mh + ml, magnitudes; t has 5 significant bits.  The
+// products' rounding errors are exact in fp32 (fma), and the leading parts
+// nearly cancel, so the sign of the difference is right.
+__device__ __forceinline__ float settle_tie(float v, float ph, float pl, float mh, float ml) {
+  const uint32_t bits = __float_as_uint(v);
+  const uint32_t tie = ((bits + 0x80000u) & ~0xfffffu) - 0x80000u;   // with v's sign
+  const float t = fabsf(__uint_as_float(tie));
+  const float a = __fmul_rn(kE4m3Max, ph), b = __fmul_rn(t, mh);
+  const float ae = __fmaf_rn(kE4m3Max, ph, -a), be = __fmaf_rn(t, mh, -b);
+  const float low = __fmaf_rn(kE4m3Max, pl, -__fmul_rn(t, ml));
+  const float d = __fadd_rn(__fadd_rn(a, -b), __fadd_rn(__fadd_rn(ae, -be), low));
+  return __uint_as_float(d > 0.f ? tie + 1 : d < 0.f ? tie - 1 : tie);
 }
 
 // Sum over the kWPR warps that share a row; every thread of the CTA calls it.
@@ -148,7 +168,7 @@ struct NormArgs {
 // x, r, s and y may be the same memory (each thread reads its elements of a
 // row before it writes them), hence no __restrict__.
 template <typename T, int kVPL, int kWPR, bool kFp8>
-__global__ void __launch_bounds__(kThreads) residual_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kThreads, kVPL <= 2 ? 4 : 1) residual_norm_kernel(NormArgs a) {
   __shared__ float part[kWarps][1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * (kWarps / kWPR) + warp / kWPR;
@@ -201,8 +221,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(NormArgs a) {
     const bool in = live && c < a.dim;
     if (a.r && in && a.s) s[j].store((T*)a.s + base + c);
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float(&wj)[8] = w[kEarlyW ? j : 0];
     if (in) {
-      float(&wj)[8] = w[kEarlyW ? j : 0];
       s[j].widen(f);
       if (!kEarlyW) load_w(a.w + c, wj);
 #pragma unroll
@@ -219,8 +239,41 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
       m = max_nan(m, kTiny);
+      const float inv = __fdiv_rn(kE4m3Max, m);
+      float v[8];
+      bool near = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = __fmul_rn(f[i], inv);
+        near |= near_tie(v[i]);
+      }
+      if (__any_sync(0xffffffffu, near && m > kTiny)) {
+        // (one in 120 of these) the root cancels in y / m: the codes are those
+        // of 448 s_j w_j / max |s w|, a product being hi + lo exactly
+        float fs[8], mh = 0.f, ml = 0.f;
+        s[j].widen(fs);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!in) fs[i] = 0.f;
+          const float hi = fabsf(__fmul_rn(fs[i], wj[i]));
+          const float lo = __fmaf_rn(fabsf(fs[i]), fabsf(wj[i]), -hi);
+          if (hi > mh || (hi == mh && lo > ml)) mh = hi, ml = lo;
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+          const float hi = __shfl_xor_sync(0xffffffffu, mh, o);
+          const float lo = __shfl_xor_sync(0xffffffffu, ml, o);
+          if (hi > mh || (hi == mh && lo > ml)) mh = hi, ml = lo;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (near_tie(v[i]) && m > kTiny) {
+            const float hi = fabsf(__fmul_rn(fs[i], wj[i]));
+            v[i] = settle_tie(v[i], hi, __fmaf_rn(fabsf(fs[i]), fabsf(wj[i]), -hi), mh, ml);
+          }
+      }
       if (in) {
-        *reinterpret_cast<uint2*>(a.q + base + c) = codes8(f, __fdiv_rn(kE4m3Max, m));
+        *reinterpret_cast<uint2*>(a.q + base + c) = codes8(v);
         if ((lane & 15) == 0)
           a.scale[(size_t)row * a.blocks + c / 128] = __fdiv_rn(m, kE4m3Max);
       }
@@ -235,9 +288,13 @@ struct NormBwdArgs {
 };
 
 // dx, and each CTA's part of dw over the rows it visits: the rows are dealt
-// to a fixed grid, so the sums have a fixed order.
+// to a fixed grid, so the sums have a fixed order.  Rows in flight are what
+// it lives from: two vectors a lane leave registers for four CTAs an SM
+// (8191 rows of 4096 bf16: 49.8 us; 54.5 us with four vectors and two CTAs,
+// 60.8 us with two CTAs that fetch a row ahead).
 template <typename T, int kVPL, int kWPR>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(NormBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, kVPL > 2 ? 1 : sizeof(T) == 2 ? 4 : 2)
+    norm_backward_kernel(NormBwdArgs a) {
   constexpr int kGroups = kWarps / kWPR;
   __shared__ float part[2][kWarps][2];
   __shared__ float acc_s[kGroups > 1 ? kVPL * kWPR * 256 : 1];
@@ -362,6 +419,23 @@ struct QuantArgs {
   int64_t rows; int32_t cols, blocks;
 };
 
+// The codes of x (448 / m) in a block whose largest magnitude is m.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m, float inv) {
+  float v[8];
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = __fmul_rn(x[i], inv);
+    near |= near_tie(v[i]);
+  }
+  if (near && m > kTiny) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);
+  }
+  return codes8(v);
+}
+
 // 1 x 128 blocks: a half warp each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
@@ -382,7 +456,8 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
   for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   m = max_nan(m, kTiny);
   if (in) {
-    *reinterpret_cast<uint2*>(a.q + (size_t)row * a.cols + c) = codes8(f, __fdiv_rn(kE4m3Max, m));
+    *reinterpret_cast<uint2*>(a.q + (size_t)row * a.cols + c) =
+        quantise8(f, m, __fdiv_rn(kE4m3Max, m));
     if (l == 0) a.scale[u] = __fdiv_rn(m, kE4m3Max);
   }
 }
@@ -421,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantArgs a) {
     if (r0 + 16 * i < a.rows && c < a.cols) {
       float f[8];
       x[i].widen(f);
-      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = codes8(f, inv);
+      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = quantise8(f, m, inv);
     }
   }
   if (threadIdx.x == 0)
@@ -429,31 +504,36 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantArgs a) {
 }
 
 // ---------------------------------------------------------------- launchers
-// Calls f(std::integral_constant vectors, warps a row) for the smallest
-// register layout that holds `dim` columns.
+// A register layout for rows of `dim` columns: V vectors a lane, W warps.
 template <int kV, int kW>
 struct Lay {
   static constexpr int V = kV, W = kW;
 };
-// `few`: at most 4 vectors a lane where 8 warps can hold the row so (the fp32
-// gradient, whose 8-vector form needs more than 255 registers).  `spread`: 8
-// warps a row, for calls with fewer rows than warps to run them.
+// Forward: two vectors a lane up to 4096 columns; eight warps a row where
+// there are fewer rows than warps to run them.
 template <typename F>
-void with_layout(int dim, bool few, bool spread, F&& f) {
-  const int u = (dim + 2047) / 2048;   // vectors a lane of eight warps would hold
-  if (spread && u <= 1) return f(Lay<1, 8>{});
-  if (spread && u <= 2) return f(Lay<2, 8>{});
-  if (spread && u <= 4) return f(Lay<4, 8>{});
-  const int v = (dim + 255) / 256;   // vectors a lane of one warp would hold
+void with_forward_layout(int dim, int64_t rows, F&& f) {
+  const int v = (dim + 255) / 256;
+  if (rows <= kFewRows && v <= 8) f(Lay<1, 8>{});
+  else if (rows <= kFewRows && v <= 16) f(Lay<2, 8>{});
+  else if (v <= 1) f(Lay<1, 1>{});
+  else if (v <= 2) f(Lay<2, 1>{});
+  else if (v <= 4) f(Lay<2, 2>{});
+  else if (v <= 8) f(Lay<2, 4>{});
+  else if (v <= 16) f(Lay<2, 8>{});
+  else if (v <= 32) f(Lay<4, 8>{});
+  else f(Lay<8, 8>{});
+}
+// Backward: two vectors a lane up to 4096 columns.
+template <typename F>
+void with_backward_layout(int dim, F&& f) {
+  const int v = (dim + 255) / 256;
   if (v <= 1) f(Lay<1, 1>{});
   else if (v <= 2) f(Lay<2, 1>{});
-  else if (v <= 4) f(Lay<4, 1>{});
-  else if (few && v <= 8) f(Lay<4, 2>{});
-  else if (few && v <= 16) f(Lay<4, 4>{});
-  else if (few && v <= 32) f(Lay<4, 8>{});
-  else if (v <= 8) f(Lay<8, 1>{});
-  else if (v <= 16) f(Lay<8, 2>{});
-  else if (v <= 32) f(Lay<8, 4>{});
+  else if (v <= 4) f(Lay<2, 2>{});
+  else if (v <= 8) f(Lay<2, 4>{});
+  else if (v <= 16) f(Lay<2, 8>{});
+  else if (v <= 32) f(Lay<4, 8>{});
   else f(Lay<8, 8>{});
 }
 
@@ -462,7 +542,7 @@ bool io_ok(int32_t io) { return io == GDN_BF16 || io == GDN_F32; }
 
 int launch_norm(const NormArgs& a, int32_t io, bool fp8, cudaStream_t st) {
   int rc = GDN_OK;
-  with_layout(a.dim, false, a.rows <= kFewRows, [&](auto lay) {
+  with_forward_layout(a.dim, a.rows, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
     const int64_t blocks = (a.rows + kWarps / W - 1) / (kWarps / W);
     if (blocks > 0x7fffffffLL) {
@@ -514,12 +594,12 @@ int norm_common(const void* x, const void* residual, const float* w, float eps, 
   return launch_norm(a, io_dtype, fp8, stream);
 }
 
-// dw parts of the backward: one row of `dim` a CTA, one CTA an SM at most
-int backward_grid(int64_t tokens, int32_t dim, int32_t io) {
+// dw parts of the backward: one row of `dim` a CTA
+int backward_grid(int64_t tokens, int32_t dim) {
   int groups = 1;
-  with_layout(dim, io == GDN_F32, false, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
+  with_backward_layout(dim, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
   const int64_t want = (tokens + groups - 1) / groups;
-  const int64_t cap = 152;   // the SMs of the device: a constant, so that the sums' order is one
+  const int64_t cap = 608;   // four an SM: a constant, so that the sums' order is one
   return (int)(want < cap ? want : cap);
 }
 bool backward_shape_ok(int64_t tokens, int32_t dim, int32_t io) {
@@ -536,7 +616,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   for (const void* p : v16)
     if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
   const size_t bytes = (size_t)tokens * dim * es_of(io_dtype);
-  const int grid = backward_grid(tokens, dim, io_dtype);
+  const int grid = backward_grid(tokens, dim);
   const size_t need = (size_t)grid * dim * 4;
   if (use_ws && need) {
     if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
@@ -552,7 +632,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   void* part = ws;
   if (!use_ws && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
   NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
-  with_layout(dim, io_dtype == GDN_F32, false, [&](auto lay) {
+  with_backward_layout(dim, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
     if (io_dtype == GDN_BF16)
       norm_backward_kernel<__nv_bfloat16, V, W><<<grid, kThreads, 0, stream>>>(a);
@@ -592,7 +672,7 @@ int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, f
 
 size_t gdn_residual_norm_backward_workspace_size(int64_t tokens, int32_t dim, int32_t io_dtype) {
   if (!backward_shape_ok(tokens, dim, io_dtype)) return SIZE_MAX;
-  return (size_t)backward_grid(tokens, dim, io_dtype) * dim * 4;
+  return (size_t)backward_grid(tokens, dim) * dim * 4;
 }
 
 int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,

@@ -513,7 +513,7 @@ int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, f
  * No output may overlap an input or another output.  Scratch from the
  * library's pool, or a caller's 256-byte aligned workspace of at least
  * gdn_residual_norm_backward_workspace_size bytes (SIZE_MAX for unsupported
- * arguments; rules as gdn_prefill_ws): at most 152 * dim * 4 bytes.
+ * arguments; rules as gdn_prefill_ws): at most 608 * dim * 4 bytes.
  */
 int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,
                                float eps, void* dx, float* dw, int64_t tokens, int32_t dim,
