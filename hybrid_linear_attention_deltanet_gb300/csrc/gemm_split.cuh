@@ -265,20 +265,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   if (warp == 5) tmem_dealloc(tmem, S::kCols);
 }
 
-// Columns of the MMA that hold `tokens`: 16, 32, 64 or 128.
-inline int split_columns(int64_t tokens) {
-  return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
-}
-// CTAs a cluster splits K over: as many as two an SM allow, at least two K
-// blocks each, eight at most.
-inline int split_of(int64_t units, int k_blocks, int sms) {
-  int64_t s = 2 * (int64_t)sms / units;
-  if (s > k_blocks / 2) s = k_blocks / 2;
+// CTAs a cluster splits K over: as many as keep the grid within `ctas` and
+// leave each at least `least` K blocks, eight at most.
+inline int split_of(int64_t units, int k_blocks, int ctas, int least) {
+  int64_t s = ctas / units;
+  if (s > k_blocks / least) s = k_blocks / least;
   return s < 1 ? 1 : s > 8 ? 8 : (int)s;
 }
 
 template <bool kFp8, bool kGated, int kNB, typename T>
-cudaError_t launch_split_nb(const SplitArgs& g, int sms, cudaStream_t st) {
+cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st) {
   using S = SplitShape<kFp8, kNB>;
   auto kern = split_gemm_kernel<kFp8, kGated, kNB, T>;
   cudaError_t e =
@@ -286,7 +282,6 @@ cudaError_t launch_split_nb(const SplitArgs& g, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const unsigned ny = (unsigned)((g.n + (kGated ? 63 : 127)) / (kGated ? 64 : 128));
   const unsigned nz = (unsigned)((g.tokens + kNB - 1) / kNB);
-  const unsigned split = (unsigned)split_of((int64_t)ny * nz, g.k_blocks, sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split, ny, nz);
   cfg.blockDim = dim3(kSplitThreads);
@@ -304,13 +299,14 @@ cudaError_t launch_split_nb(const SplitArgs& g, int sms, cudaStream_t st) {
   return e;
 }
 
+// nb columns (16, 32, 64 or 128) a CTA, K split over `split` CTAs.
 template <bool kFp8, bool kGated, typename T>
-cudaError_t launch_split(const SplitArgs& g, int nb, int sms, cudaStream_t st) {
+cudaError_t launch_split(const SplitArgs& g, int nb, int split, cudaStream_t st) {
   switch (nb) {
-    case 16: return launch_split_nb<kFp8, kGated, 16, T>(g, sms, st);
-    case 32: return launch_split_nb<kFp8, kGated, 32, T>(g, sms, st);
-    case 64: return launch_split_nb<kFp8, kGated, 64, T>(g, sms, st);
-    default: return launch_split_nb<kFp8, kGated, 128, T>(g, sms, st);
+    case 16: return launch_split_nb<kFp8, kGated, 16, T>(g, split, st);
+    case 32: return launch_split_nb<kFp8, kGated, 32, T>(g, split, st);
+    case 64: return launch_split_nb<kFp8, kGated, 64, T>(g, split, st);
+    default: return launch_split_nb<kFp8, kGated, 128, T>(g, split, st);
   }
 }
 

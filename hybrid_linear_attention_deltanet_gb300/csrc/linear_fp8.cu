@@ -14,14 +14,23 @@ namespace {
 
 using namespace hostcheck;
 
-// Few tokens: the split form (its scales must fit their staging).
-bool takes_split(int64_t tokens, int32_t n, int32_t blocks, int sms) {
-  if (tokens > 256) return false;
-  const int nb = gemm::split_columns(tokens);
+// The split form's columns and K split for a call, or columns 0 for the pair
+// form.  One wave of CTAs is what pays (their epilogues are the longer part
+// of a K block): 2048 -> 4608, us, split form / pair form: 16 tokens 4.5 / 13,
+// 64 tokens 5.9 / 13, 128 tokens 7.3 / 13, 256 tokens 9.9 / 13.8, 512 tokens
+// 16.0 / 14.
+struct SplitPlan {
+  int columns, split;
+};
+SplitPlan plan_split(int64_t tokens, int32_t n, int32_t blocks, int sms) {
+  if (tokens > 256) return {0, 0};
+  const int nb = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
   const int64_t units = (int64_t)((n + 127) / 128) * ((tokens + nb - 1) / nb);
-  const int split = gemm::split_of(units, blocks, sms);
-  return (int64_t)((blocks + split - 1) / split) * nb * 4 <= gemm::kSplitScaleBytes &&
-         (n + 127) / 128 <= 65535;
+  if (tokens > 64 && units > sms) return {0, 0};
+  const int split = gemm::split_of(units, blocks, sms, 4);
+  const int64_t scales = (int64_t)((blocks + split - 1) / split) * nb * 4;
+  if (scales > gemm::kSplitScaleBytes || (n + 127) / 128 > 65535) return {0, 0};
+  return {nb, split};
 }
 
 int linear_common(const void* x, const float* sx, const void* w, const float* sw, void* out,
@@ -45,10 +54,10 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   const int sms = sm_count();
   unsigned* status = status_ptr();
   if (sms < 2 || !status) return GDN_ERR_CUDA;
-  if (takes_split(tokens, n, blocks, sms)) {
+  const SplitPlan plan = plan_split(tokens, n, blocks, sms);
+  if (plan.columns) {
     gemm::SplitArgs a;
     memset(&a, 0, sizeof a);
-    const int nb = gemm::split_columns(tokens);
     a.k_blocks = blocks;
     a.tokens = (int32_t)tokens;
     a.n = n;
@@ -57,12 +66,12 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
     a.sw = sw;
     a.status = status;
     if (!gemm::matrix_map(&a.w[0], w, true, k, n, k, 128) ||
-        !gemm::matrix_map(&a.x, x, true, k, tokens, k, nb))
+        !gemm::matrix_map(&a.x, x, true, k, tokens, k, plan.columns))
       return GDN_ERR_CUDA;
     const cudaError_t e =
         out_dtype == GDN_BF16
-            ? gemm::launch_split<true, false, __nv_bfloat16>(a, nb, sms, stream)
-            : gemm::launch_split<true, false, float>(a, nb, sms, stream);
+            ? gemm::launch_split<true, false, __nv_bfloat16>(a, plan.columns, plan.split, stream)
+            : gemm::launch_split<true, false, float>(a, plan.columns, plan.split, stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
   }
   gemm::PairArgs g;
