@@ -31,6 +31,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_NAME = "libgdn_gb300.so"
 _lib = None
+_direct = None   # csrc/binding.cpp's module, once the library is loaded
 
 GDN_F32, GDN_BF16 = 0, 1
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "alignment",
@@ -49,7 +50,7 @@ def lib_path() -> str:
 
 def load():
     """Load the compiled library (raises if it has not been built)."""
-    global _lib
+    global _lib, _direct
     if _lib is not None:
         return _lib
     path = lib_path()
@@ -130,8 +131,17 @@ def load():
     lib.gdn_release_scratch.restype = ctypes.c_int
     lib.gdn_testing_scratch_reserved.argtypes = [vp]
     lib.gdn_testing_scratch_reserved.restype = ctypes.c_int
+    from . import _layer_calls
+    _layer_calls.bind(path)
+    _direct = _layer_calls
     _lib = lib
     return lib
+
+
+def _direct_calls():
+    if _lib is None:
+        load()
+    return _direct
 
 
 def _ws_args(workspace):
@@ -621,8 +631,10 @@ def prefill_layer(qkv, conv_w, a_raw, b_raw, A_log, dt_bias, gate, norm_w, heads
 # ---------------------------------------------------------------------------
 # The layer around the mixer: residual norm, 8-bit projections, feed-forward.
 # A decoding step makes these calls for single tokens, where the host's time
-# counts: tensors are checked in one pass, addresses go to the library as
-# integers, and the device guard is taken only off the current device.
+# counts.  The ordinary call (new outputs, the current device and stream) goes
+# through _layer_calls (csrc/binding.cpp), which returns None, having done
+# nothing, where anything is out of the ordinary; the code here then checks,
+# allocates and calls the library itself, and raises what is to be raised.
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -702,6 +714,10 @@ def residual_norm(x, w, residual=None, eps=1e-5, s=None, y=None, stream=None):
     over the last axis.  x, residual [.., dim] bf16 or fp32; w [dim] fp32.
     Returns (y, s); s is x itself without a residual.  ``s=residual`` updates
     the residual stream in place."""
+    if s is None and y is None and stream is None:
+        done = _direct_calls().residual_norm(x, w, residual, eps)
+        if done is not None:
+            return done
     code = _io_code(x.dtype)
     index, shape, r, total = _norm_inputs(x, w, residual, s)
     y = torch.empty_like(x) if y is None else _out(y, "y", shape, x.dtype, index)
@@ -717,6 +733,10 @@ def residual_norm_fp8(x, w, residual=None, eps=1e-5, s=None, q=None, scale=None,
     Returns (q, scale, s): q [.., dim] float8_e4m3fn and scale
     [.., ceil(dim / 128)] fp32, y ~ q * scale per 128 columns, as
     :func:`linear_fp8` reads them."""
+    if s is None and q is None and scale is None and stream is None:
+        done = _direct_calls().residual_norm_fp8(x, w, residual, eps)
+        if done is not None:
+            return done
     code = _io_code(x.dtype)
     index, shape, r, total = _norm_inputs(x, w, residual, s)
     dim = shape[-1]
@@ -742,6 +762,10 @@ def residual_norm_backward(dy, s, w, ds=None, eps=1e-5, stream=None, workspace=N
     [.., dim] of y, ds of s from its other uses (or None), s as the forward
     call returned it.  Returns dict dx (the gradient of x and of residual
     alike, dtype of s) and dw [dim] fp32."""
+    if stream is None and workspace is None:
+        done = _direct_calls().residual_norm_backward(dy, s, w, ds, eps)
+        if done is not None:
+            return dict(dx=done[0], dw=done[1])
     code = _io_code(s.dtype)
     index, shape, _, _ = _norm_inputs(s, w, None, None)
     _need(dy, "dy", s.dtype, index)
@@ -767,6 +791,10 @@ def quantize_fp8(x, block_rows=1, q=None, scale=None, stream=None):
     (``gdn_quantize_fp8``): 1 x 128 blocks for activations, with
     ``block_rows=128`` 128 x 128 blocks for a weight [n, k].  Returns
     (q, scale)."""
+    if q is None and scale is None and stream is None:
+        done = _direct_calls().quantize_fp8(x, block_rows)
+        if done is not None:
+            return done
     code = _io_code(x.dtype)
     index, shape = x.get_device(), x.shape
     _need(x, "x", x.dtype, index)
@@ -792,6 +820,10 @@ def linear_fp8(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, strea
     :func:`quantize_fp8` give them).  Returns out [.., n] in ``out_dtype``
     (bf16 or fp32)."""
     code = _io_code(out_dtype)
+    if out is None and stream is None:
+        done = _direct_calls().linear_fp8(x, x_scale, w, w_scale, code)
+        if done is not None:
+            return done
     index = x.get_device()
     _need(x, "x", FP8, index)
     _need(w, "w", FP8, index)
@@ -835,6 +867,10 @@ def gated_ffn(x, w_gate, w_up, act="silu", h=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T) in one kernel (``gdn_gated_ffn``):
     x [.., dim], w_gate and w_up [hidden, dim], all bf16.  Returns h
     [.., hidden]."""
+    if h is None and stream is None:
+        done = _direct_calls().gated_ffn(x, w_gate, w_up, GATE_ACT.get(act))
+        if done is not None:
+            return done
     index, shape, hidden = _ffn_inputs(x, w_gate, w_up, act)
     dim, h_shape = shape[-1], (*shape[:-1], hidden)
     if h is None:
@@ -856,6 +892,10 @@ def gated_ffn_backward_workspace_size(tokens, dim, hidden, io_dtype=torch.bfloat
 def gated_ffn_backward(x, w_gate, w_up, dh, act="silu", stream=None, workspace=None):
     """Gradients of :func:`gated_ffn` from its inputs and dh [.., hidden]
     (``gdn_gated_ffn_backward``).  Returns dict dx, dw_gate, dw_up (bf16)."""
+    if stream is None and workspace is None:
+        done = _direct_calls().gated_ffn_backward(x, w_gate, w_up, dh, GATE_ACT.get(act))
+        if done is not None:
+            return dict(dx=done[0], dw_gate=done[1], dw_up=done[2])
     index, shape, hidden = _ffn_inputs(x, w_gate, w_up, act)
     _need(dh, "dh", torch.bfloat16, index)
     if dh.shape != (*shape[:-1], hidden):

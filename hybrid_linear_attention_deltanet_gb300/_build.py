@@ -1,12 +1,15 @@
 """Compile the CUDA library (csrc/*.cu) for sm_103a into libgdn_gb300.so in
 this package directory.  Each translation unit compiles in parallel with
-nvcc; the objects are then linked into one shared library (static cudart)."""
+nvcc; the objects are then linked into one shared library (static cudart).
+The layer operators' direct binding (csrc/binding.cpp, against the installed
+PyTorch's headers) becomes _layer_calls.so beside it."""
 from __future__ import annotations
 
 import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,30 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def build_binding() -> str:
+    """Compile csrc/binding.cpp into _layer_calls.so with the host compiler."""
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    out = os.path.join(HERE, "_layer_calls.so")
+    newest = max(os.path.getmtime(p) for p in
+                 [src, torch.__file__] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    libs = os.path.join(root, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(cuda, "include"), src, "-o", out + ".tmp", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def sources():
@@ -49,8 +76,10 @@ def build(verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     lib = os.path.join(HERE, LIB_NAME)
     cmd = [nvcc()] + ARCH + ["-shared", "-o", lib + ".tmp"] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
