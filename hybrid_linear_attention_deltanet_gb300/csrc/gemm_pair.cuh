@@ -76,15 +76,15 @@ constexpr uint32_t kOperand = 128 * 128;             // bytes of A (and of B) a 
 constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr int kGroup = 4;                            // K blocks whose scales travel together
 
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 128 + 32 * kEpiWarps;
+constexpr uint32_t kBounce = 32 * 128;               // a warp's staging: 32 rows x 128 bytes
+
 template <bool kFp8>
 struct Shape {
-  static constexpr int kEpiWarps = 8;
-  static constexpr int kThreads = 128 + 32 * kEpiWarps;
-  static constexpr int kStages = kFp8 ? 5 : 6;
-  static constexpr int kRow = kFp8 ? 64 : 128;       // bytes of a row of a warp's staging
-  static constexpr uint32_t kBounce = 32 * kRow;
   // two groups of scales [kGroup][2 column blocks][128 rows]
   static constexpr uint32_t kScales = kFp8 ? 2 * kGroup * 256 * 4 : 0;
+  static constexpr int kStages = kFp8 ? 5 : 6;       // what 227 KB hold
   static constexpr uint32_t kSmem =
       kStages * kStageBytes + kEpiWarps * kBounce + kScales + 1024;
 };
@@ -119,18 +119,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // Offset of 16-byte piece `i` of row `r` in a warp's staging image, swizzled
-// as TMA's 128- or 64-byte mode does; lanes that write a piece of each row
-// meet no bank conflicts.
-template <int kRow>
+// as TMA's 128-byte mode does; lanes that write a piece of each row meet no
+// bank conflicts.
 __device__ __forceinline__ uint32_t stage_piece(uint32_t r, uint32_t i) {
-  return r * kRow + (kRow == 128 ? i ^ (r & 7u) : i ^ ((r >> 1) & 3u)) * 16;
+  return r * 128 + (i ^ (r & 7u)) * 16;
 }
-// kN columns from `c0` of this lane's row into its warp's staging image.
-template <typename T, int kRow, int kN>
+// 32 columns from `c0` of this lane's row into its warp's staging image.
+template <typename T>
 __device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const float* v) {
   constexpr int kPer = 16 / (int)sizeof(T);   // elements a piece
 #pragma unroll
-  for (int i = 0; i < kN / kPer; ++i) {
+  for (int i = 0; i < 32 / kPer; ++i) {
     uint4 w;
     if constexpr (sizeof(T) == 2)
       w = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
@@ -138,12 +137,12 @@ __device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const 
     else
       w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-    *reinterpret_cast<uint4*>(buf + stage_piece<kRow>(lane, c0 / kPer + i)) = w;
+    *reinterpret_cast<uint4*>(buf + stage_piece(lane, c0 / kPer + i)) = w;
   }
 }
 // The staged 32 rows to their place, what lies past the edges of the output
 // left out.  stage_free() must return before the next stage_put.
-template <typename T, int kRow>
+template <typename T>
 __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Problem& p, int half,
                                           int row0, int n0) {
   if (row0 >= p.M || n0 >= p.N) return;
@@ -156,7 +155,7 @@ __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Pr
     }
   } else {   // rows that start anywhere: a row at a time, 32 elements a step
     __syncwarp();
-    constexpr int kCols = kRow / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
+    constexpr int kCols = 128 / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
     const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
     T* out = (T*)p.out[half] + (size_t)row0 * p.ldc + n0;
 #pragma unroll
@@ -166,7 +165,7 @@ __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Pr
 #pragma unroll 8
       for (int r = 0; r < rows; ++r)
         out[(size_t)r * p.ldc + c] = *reinterpret_cast<const T*>(
-            buf + stage_piece<kRow>(r, c / kPer) + (c % kPer) * sizeof(T));
+            buf + stage_piece(r, c / kPer) + (c % kPer) * sizeof(T));
     }
   }
 }
@@ -185,10 +184,9 @@ __device__ __forceinline__ float gate_act(float x, int act) {
 }
 
 template <bool kFp8, int kEpi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs g) {
-  using S = Shape<kFp8>;
-  constexpr int kStages = S::kStages, kEpiWarps = S::kEpiWarps, kRow = S::kRow;
+  constexpr int kStages = Shape<kFp8>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
@@ -220,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
       g.p[0].m_tiles * g.p[0].n_tiles + (g.problems > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   bool ok = true;
-  float* scales = reinterpret_cast<float*>(sm + kStages * kStageBytes + kEpiWarps * S::kBounce);
+  float* scales = reinterpret_cast<float*>(sm + kStages * kStageBytes + kEpiWarps * kBounce);
 
   // The fetching and the multiplying warp run their loops whole, with one
   // elected lane issuing: every address and descriptor then stays in uniform
@@ -370,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t free0 = mapa_smem(&acc_empty[0], 0);   // the even CTA's barriers
-    uint8_t* bounce = sm + kStages * kStageBytes + (warp - 4) * S::kBounce;
+    uint8_t* bounce = sm + kStages * kStageBytes + (warp - 4) * kBounce;
     int buf = 0, slot = 0;
     uint32_t aph = 0, sph = 0;
     // this warp's columns of the accumulator are out of tensor memory
@@ -430,15 +428,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
         }
         if (!ok) break;
         using T = typename std::conditional<kEpi == kStoreF32, float, __nv_bfloat16>::type;
-        constexpr int kCols = kRow / (int)sizeof(T);   // 32 bf16 or 16 fp32
+        constexpr int kCols = 128 / (int)sizeof(T);   // 64 bf16 or 32 fp32
 #pragma unroll
-        for (int c = 0; c < 128; c += kCols) {
-          float v[kCols];
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < kCols / 2; ++i) f2_split(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
-          stage_free(lane);
-          stage_put<T, kRow, kCols>(bounce, lane, 0, v);
-          stage_out<T, kRow>(bounce, lane, p, 0, row0, n0 + c);
+          for (int i = 0; i < 16; ++i) f2_split(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
+          if (c % kCols == 0) stage_free(lane);
+          stage_put<T>(bounce, lane, c % kCols, v);
+          if ((c + 32) % kCols == 0) stage_out<T>(bounce, lane, p, 0, row0, n0 + c + 32 - kCols);
         }
       } else if constexpr (kEpi == kStore) {
         ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
@@ -455,9 +453,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           if (c % 64 == 0) stage_free(lane);
-          stage_put<__nv_bfloat16, kRow, 32>(bounce, lane, c % 64, v);
+          stage_put<__nv_bfloat16>(bounce, lane, c % 64, v);
           if (c % 64 == 32)
-            stage_out<__nv_bfloat16, kRow>(bounce, lane, p, tl.half, row0, n0 + c - 32);
+            stage_out<__nv_bfloat16>(bounce, lane, p, tl.half, row0, n0 + c - 32);
         }
         advance();
       } else {
@@ -482,14 +480,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
               for (int r = 0; r < 32; ++r) {
                 __nv_bfloat16 v = __float2bfloat16_rn(0.f);
                 if (row0 + r < p.M && f0 + c < p.N) v = g.dh[(size_t)(row0 + r) * g.ldh + f0 + c];
-                *reinterpret_cast<__nv_bfloat16*>(bounce + stage_piece<kRow>(r, c / 8) +
+                *reinterpret_cast<__nv_bfloat16*>(bounce + stage_piece(r, c / 8) +
                                                   (c % 8) * 2) = v;
               }
             }
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const uint4 w = *reinterpret_cast<const uint4*>(bounce + stage_piece<kRow>(lane, i));
+              const uint4 w = *reinterpret_cast<const uint4*>(bounce + stage_piece(lane, i));
               dh[4 * i] = w.x; dh[4 * i + 1] = w.y; dh[4 * i + 2] = w.z; dh[4 * i + 3] = w.w;
             }
             __syncwarp();   // read before the staging is written again
@@ -526,14 +524,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kFp8>::kThread
                                 : d * (silu ? x * s : s);
               }
             }
-            stage_put<__nv_bfloat16, kRow, 32>(bounce, lane, c, v);
+            stage_put<__nv_bfloat16>(bounce, lane, c, v);
           }
-          stage_out<__nv_bfloat16, kRow>(bounce, lane, p, out, row0, f0);
+          stage_out<__nv_bfloat16>(bounce, lane, p, out, row0, f0);
         }
         advance();
       }
     }
-    if (lane == 0) bulk_wait_all();   // this warp's stores have left shared memory
+    stage_free(lane);   // this warp's stores have left shared memory
   }
   if (!ok) {
     // copies and products in flight end within microseconds; give them longer
@@ -585,7 +583,7 @@ inline bool matrix_map(CUtensorMap* m, const void* base, bool fp8, int64_t inner
 
 // The outputs c[0], c[1] = out[0], out[1], [M][N] with ldc elements a row:
 // TMA stores where rows start on 16 bytes, plain ones elsewhere.
-inline bool output_maps(Problem& p, bool f32, int row_bytes) {
+inline bool output_maps(Problem& p, bool f32) {
   const int64_t pitch = p.ldc * (f32 ? 4 : 2);
   p.c_tma = pitch % 16 == 0;
   EncodeFn enc = encoder();
@@ -598,12 +596,11 @@ inline bool output_maps(Problem& p, bool f32, int row_bytes) {
     memset(&p.c[i], 0, sizeof p.c[i]);
     cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
     cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    cuuint32_t box[2] = {(cuuint32_t)(row_bytes / (f32 ? 4 : 2)), 32};
+    cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
     cuuint32_t es[2] = {1, 1};
     if (enc(&p.c[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             p.out[i], dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
   }
@@ -612,18 +609,18 @@ inline bool output_maps(Problem& p, bool f32, int row_bytes) {
 
 template <bool kFp8, int kEpi>
 cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
-  using S = Shape<kFp8>;
+  constexpr uint32_t kSmem = Shape<kFp8>::kSmem;
   auto kern = pair_gemm_kernel<kFp8, kEpi>;
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   int64_t tiles = 0;
   for (int i = 0; i < g.problems; ++i) {
-    if (!output_maps(g.p[i], kEpi == kStoreF32, S::kRow)) return cudaErrorUnknown;
+    if (!output_maps(g.p[i], kEpi == kStoreF32)) return cudaErrorUnknown;
     tiles += (int64_t)g.p[i].m_tiles * g.p[i].n_tiles;
   }
   const int64_t pairs = sms / 2;
-  kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), S::kThreads, S::kSmem, st>>>(g);
+  kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, kSmem, st>>>(g);
   count_launches(1);
   return cudaGetLastError();
 }
