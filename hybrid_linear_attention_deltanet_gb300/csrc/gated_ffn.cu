@@ -52,7 +52,7 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
   p.M = (int32_t)tokens;
   p.N = hidden;
   g.problems = 1;
-  g.group_m = 8;
+  g.group_m = gemm::group_rows((int64_t)dim * 2);
   if (!gemm::matrix_map(&p.a[0], x, false, dim, tokens, (int64_t)dim * 2, 128) ||
       !gemm::matrix_map(&p.b[0], wg, false, dim, hidden, (int64_t)dim * 2, 128) ||
       !gemm::matrix_map(&p.b[1], wu, false, dim, hidden, (int64_t)dim * 2, 128))
@@ -137,7 +137,7 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   memset(&g, 0, sizeof g);
   g.status = status;
   g.problems = 2;
-  g.group_m = 8;
+  g.group_m = 8;   // either operand is read once for the tiles in flight, which are about square
   const int32_t kx = (hidden + 63) / 64, kw = (int32_t)((tokens + 63) / 64);
   const int ix = 2 * kx >= kw ? 0 : 1;
   gemm::Problem& px = g.p[ix];

@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "gdn_internal.cuh"
+#include "hostcheck.cuh"
 #include "sm100_ptx.cuh"
 
 namespace gdn {
@@ -61,7 +62,7 @@ struct Problem {
 struct PairArgs {
   Problem p[2];
   int32_t problems;
-  int32_t group_m;      // tiles of rows whose columns are visited together (L2 reuse)
+  int32_t group_m;      // tiles of rows whose columns are visited together (group_rows)
   int32_t act;
   const __nv_bfloat16* dh;   // kGateGrad: [M][ldh]
   int64_t ldh;
@@ -213,6 +214,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers exist before either uses the other's
   tc_fence_after();
+  grid_release_next();
+  grid_wait();
   const uint32_t tmem = tmem_base;
   const int n_tiles =
       g.p[0].m_tiles * g.p[0].n_tiles + (g.problems > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
@@ -607,6 +610,15 @@ inline bool output_maps(Problem& p, bool f32) {
   return true;
 }
 
+// Tiles of rows in a group: as many as keep their operand rows (256 x pitch
+// bytes each) within 32 MB of the 126 MB L2, from 8, where the tiles in
+// flight (76) are about square, to 32 (32768 x 2048 -> 2 x 6144 bf16: 830 us
+// with 8, 800 with 32, 855 with 64).
+inline int32_t group_rows(int64_t pitch) {
+  const int64_t n = (32 << 20) / (256 * pitch);
+  return n < 8 ? 8 : n > 32 ? 32 : (int32_t)n;
+}
+
 template <bool kFp8, int kEpi>
 cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
   constexpr uint32_t kSmem = Shape<kFp8>::kSmem;
@@ -620,9 +632,10 @@ cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
     tiles += (int64_t)g.p[i].m_tiles * g.p[i].n_tiles;
   }
   const int64_t pairs = sms / 2;
-  kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, kSmem, st>>>(g);
+  e = launch_dependent(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads,
+                       kSmem, 0, st, g);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace gemm

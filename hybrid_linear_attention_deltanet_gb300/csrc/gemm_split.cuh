@@ -76,6 +76,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_release_next();
+  grid_wait();
   const uint32_t tmem = tmem_base;
   bool ok = true;
 
@@ -282,19 +284,7 @@ cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st)
   if (e != cudaSuccess) return e;
   const unsigned ny = (unsigned)((g.n + (kGated ? 63 : 127)) / (kGated ? 64 : 128));
   const unsigned nz = (unsigned)((g.tokens + kNB - 1) / kNB);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(split, ny, nz);
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, g);
+  e = launch_dependent(kern, dim3(split, ny, nz), kSplitThreads, S::kSmem, split, st, g);
   count_launches(1);
   return e;
 }

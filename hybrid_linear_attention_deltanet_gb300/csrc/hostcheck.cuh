@@ -1,5 +1,5 @@
-// Host-side argument checks shared by the entry points of the operators
-// around the mixer.
+// Host-side argument checks and launches shared by the entry points of the
+// operators around the mixer.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -42,4 +42,40 @@ inline int sm_count() {
 }
 
 }  // namespace hostcheck
+
+// The matrix products are launched as programmatic dependents: a grid may
+// start while the one before it in the stream still runs, does what needs no
+// data (barriers, tensor memory), and waits in grid_wait() for that grid's end
+// and memory before its first access to global memory; every kernel launched
+// so calls it.  (About 1 us of a product's 5 to 15 with few tokens; the
+// attribute costs the host 1.5 us a launch, more than the norms would gain.)
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The next grid may start once every CTA of this one has come here.
+__device__ __forceinline__ void grid_release_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// cluster: CTAs of a cluster along x, 0 where the kernel itself says so.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem,
+                             unsigned cluster, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace gdn

@@ -87,7 +87,7 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   p.out[0] = p.out[1] = out;
   p.ldc = n;
   g.problems = 1;
-  g.group_m = 8;
+  g.group_m = gemm::group_rows(k);
   g.sa = sx;
   g.sb = sw;
   g.sblocks = blocks;

@@ -169,6 +169,7 @@ struct NormArgs {
 // row before it writes them), hence no __restrict__.
 template <typename T, int kVPL, int kWPR, bool kFp8>
 __global__ void __launch_bounds__(kThreads, kVPL <= 2 ? 4 : 1) residual_norm_kernel(NormArgs a) {
+  grid_release_next();   // a product that follows may start its prologue
   __shared__ float part[kWarps][1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * (kWarps / kWPR) + warp / kWPR;
@@ -295,6 +296,7 @@ struct NormBwdArgs {
 template <typename T, int kVPL, int kWPR>
 __global__ void __launch_bounds__(kThreads, kVPL > 2 ? 1 : sizeof(T) == 2 ? 4 : 2)
     norm_backward_kernel(NormBwdArgs a) {
+  grid_release_next();
   constexpr int kGroups = kWarps / kWPR;
   __shared__ float part[2][kWarps][2];
   __shared__ float acc_s[kGroups > 1 ? kVPL * kWPR * 256 : 1];
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, kVPL > 2 ? 1 : sizeof(T) == 2 ? 4 : 
 // the runs in order.
 __global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int n,
                                                       int dim, float* __restrict__ dw) {
+  grid_release_next();
   __shared__ float sm[8][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -439,6 +442,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m, float i
 // 1 x 128 blocks: a half warp each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
+  grid_release_next();
   const int64_t units = a.rows * a.blocks;
   const int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
   const int l = threadIdx.x & 15;
@@ -466,6 +470,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
 // t / 16 + 16 i.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantArgs a) {
+  grid_release_next();
   __shared__ float wm[kWarps];
   const int64_t r0 = (int64_t)blockIdx.y * 128 + (threadIdx.x >> 4);
   const int c = blockIdx.x * 128 + (threadIdx.x & 15) * 8;
@@ -549,14 +554,12 @@ int launch_norm(const NormArgs& a, int32_t io, bool fp8, cudaStream_t st) {
       rc = GDN_ERR_UNSUPPORTED;
       return;
     }
-    const unsigned g = (unsigned)blocks;
-    if (io == GDN_BF16) {
-      if (fp8) residual_norm_kernel<__nv_bfloat16, V, W, true><<<g, kThreads, 0, st>>>(a);
-      else residual_norm_kernel<__nv_bfloat16, V, W, false><<<g, kThreads, 0, st>>>(a);
-    } else {
-      if (fp8) residual_norm_kernel<float, V, W, true><<<g, kThreads, 0, st>>>(a);
-      else residual_norm_kernel<float, V, W, false><<<g, kThreads, 0, st>>>(a);
-    }
+    auto kern = io == GDN_BF16
+                    ? (fp8 ? residual_norm_kernel<__nv_bfloat16, V, W, true>
+                           : residual_norm_kernel<__nv_bfloat16, V, W, false>)
+                    : (fp8 ? residual_norm_kernel<float, V, W, true>
+                           : residual_norm_kernel<float, V, W, false>);
+    kern<<<(unsigned)blocks, kThreads, 0, st>>>(a);
     count_launches(1);
     if (cudaGetLastError() != cudaSuccess) rc = GDN_ERR_CUDA;
   });
@@ -634,10 +637,9 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
   with_backward_layout(dim, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
-    if (io_dtype == GDN_BF16)
-      norm_backward_kernel<__nv_bfloat16, V, W><<<grid, kThreads, 0, stream>>>(a);
-    else
-      norm_backward_kernel<float, V, W><<<grid, kThreads, 0, stream>>>(a);
+    auto kern = io_dtype == GDN_BF16 ? norm_backward_kernel<__nv_bfloat16, V, W>
+                                     : norm_backward_kernel<float, V, W>;
+    kern<<<grid, kThreads, 0, stream>>>(a);
   });
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
@@ -709,17 +711,13 @@ int gdn_quantize_fp8(const void* x, void* q, float* scale, int64_t rows, int32_t
   if (block_rows == 1) {
     const int64_t grid = (rows * blocks + 15) / 16;
     if (grid > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
-    if (io_dtype == GDN_BF16)
-      quant_rows_kernel<__nv_bfloat16><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-    else
-      quant_rows_kernel<float><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+    auto kern = io_dtype == GDN_BF16 ? quant_rows_kernel<__nv_bfloat16> : quant_rows_kernel<float>;
+    kern<<<(unsigned)grid, kThreads, 0, stream>>>(a);
   } else {
     if (row_blocks > 65535) return GDN_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks, (unsigned)row_blocks);
-    if (io_dtype == GDN_BF16)
-      quant_tiles_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-    else
-      quant_tiles_kernel<float><<<grid, kThreads, 0, stream>>>(a);
+    auto kern = io_dtype == GDN_BF16 ? quant_tiles_kernel<__nv_bfloat16> : quant_tiles_kernel<float>;
+    kern<<<grid, kThreads, 0, stream>>>(a);
   }
   count_launches(1);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
