@@ -159,6 +159,12 @@ __device__ __forceinline__ void row_sum(float (&x)[kN], float (*part)[kN]) {
   }
 }
 
+// CTAs an SM that the registers of kVPL vectors a lane leave room for.
+constexpr int forward_ctas(int v) { return v <= 2 ? 4 : v <= 3 ? 3 : v <= 4 ? 2 : 1; }
+constexpr int backward_ctas(int v, size_t element) {
+  return element == 2 ? (v <= 2 ? 4 : v <= 3 ? 3 : v <= 4 ? 2 : 1) : v <= 2 ? 2 : 1;
+}
+
 struct NormArgs {
   const void* x; const void* r; const float* w; float eps;
   void* s; void* y; uint8_t* q; float* scale;
@@ -168,7 +174,7 @@ struct NormArgs {
 // x, r, s and y may be the same memory (each thread reads its elements of a
 // row before it writes them), hence no __restrict__.
 template <typename T, int kVPL, int kWPR, bool kFp8>
-__global__ void __launch_bounds__(kThreads, kVPL <= 2 ? 4 : 1) residual_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_kernel(NormArgs a) {
   grid_release_next();   // a product that follows may start its prologue
   __shared__ float part[kWarps][1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -294,7 +300,7 @@ struct NormBwdArgs {
 // (8191 rows of 4096 bf16: 49.8 us; 54.5 us with four vectors and two CTAs,
 // 60.8 us with two CTAs that fetch a row ahead).
 template <typename T, int kVPL, int kWPR>
-__global__ void __launch_bounds__(kThreads, kVPL > 2 ? 1 : sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
     norm_backward_kernel(NormBwdArgs a) {
   grid_release_next();
   constexpr int kGroups = kWarps / kWPR;
@@ -395,23 +401,23 @@ __global__ void __launch_bounds__(kThreads, kVPL > 2 ? 1 : sizeof(T) == 2 ? 4 : 
   }
 }
 
-// dw[c] = sum_b part[b][c], b in order within each of 8 strided runs, then
-// the runs in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int n,
-                                                      int dim, float* __restrict__ dw) {
+// dw[c] = sum_b part[b][c]: 32 strided runs, each in order, then the runs in
+// order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int n,
+                                                       int dim, float* __restrict__ dw) {
   grid_release_next();
-  __shared__ float sm[8][33];
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float t = 0.f;
   if (c < dim)
 #pragma unroll 8
-    for (int b = run; b < n; b += 8) t += part[(size_t)b * dim + c];
+    for (int b = run; b < n; b += 32) t += part[(size_t)b * dim + c];
   sm[run][lane] = t;
   __syncthreads();
   if (run == 0 && c < dim) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += sm[i][lane];
+    for (int i = 1; i < 32; ++i) t += sm[i][lane];
     dw[c] = t;
   }
 }
@@ -514,30 +520,27 @@ template <int kV, int kW>
 struct Lay {
   static constexpr int V = kV, W = kW;
 };
-// Forward: two vectors a lane up to 4096 columns; eight warps a row where
-// there are fewer rows than warps to run them.
-template <typename F>
-void with_forward_layout(int dim, int64_t rows, F&& f) {
-  const int v = (dim + 255) / 256;
-  if (rows <= kFewRows && v <= 8) f(Lay<1, 8>{});
-  else if (rows <= kFewRows && v <= 16) f(Lay<2, 8>{});
-  else if (v <= 1) f(Lay<1, 1>{});
-  else if (v <= 2) f(Lay<2, 1>{});
-  else if (v <= 4) f(Lay<2, 2>{});
-  else if (v <= 8) f(Lay<2, 4>{});
-  else if (v <= 16) f(Lay<2, 8>{});
-  else if (v <= 32) f(Lay<4, 8>{});
-  else f(Lay<8, 8>{});
-}
-// Backward: two vectors a lane up to 4096 columns.
-template <typename F>
-void with_backward_layout(int dim, F&& f) {
-  const int v = (dim + 255) / 256;
+// The fewest warps that hold a row with at most two vectors a lane, from 4096
+// columns eight warps with more.  Forward: three vectors where a third of the
+// lanes would idle otherwise (2560 columns: 94 against 108 us for 67 M
+// elements; the gradient is the faster without, 55.7 against 64.3 us for 34 M:
+// its three vectors leave registers for three CTAs an SM instead of four), and
+// eight warps a row where there are fewer rows than warps to run them.
+template <bool kForward, typename F>
+void with_layout(int dim, int64_t rows, F&& f) {
+  const int v = (dim + 255) / 256;   // vectors a lane of one warp would hold
+  if constexpr (kForward) {
+    if (rows <= kFewRows && v <= 8) return f(Lay<1, 8>{});
+    if (rows <= kFewRows && v <= 16) return f(Lay<2, 8>{});
+    if (v == 5 || v == 6) return f(Lay<3, 2>{});
+    if (v >= 9 && v <= 12) return f(Lay<3, 4>{});
+  }
   if (v <= 1) f(Lay<1, 1>{});
   else if (v <= 2) f(Lay<2, 1>{});
   else if (v <= 4) f(Lay<2, 2>{});
   else if (v <= 8) f(Lay<2, 4>{});
   else if (v <= 16) f(Lay<2, 8>{});
+  else if (v <= 24) f(Lay<3, 8>{});
   else if (v <= 32) f(Lay<4, 8>{});
   else f(Lay<8, 8>{});
 }
@@ -547,7 +550,7 @@ bool io_ok(int32_t io) { return io == GDN_BF16 || io == GDN_F32; }
 
 int launch_norm(const NormArgs& a, int32_t io, bool fp8, cudaStream_t st) {
   int rc = GDN_OK;
-  with_forward_layout(a.dim, a.rows, [&](auto lay) {
+  with_layout<true>(a.dim, a.rows, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
     const int64_t blocks = (a.rows + kWarps / W - 1) / (kWarps / W);
     if (blocks > 0x7fffffffLL) {
@@ -597,11 +600,11 @@ int norm_common(const void* x, const void* residual, const float* w, float eps, 
   return launch_norm(a, io_dtype, fp8, stream);
 }
 
-// dw parts of the backward: one row of `dim` a CTA
+// dw parts of the backward, a row of `dim` a CTA.
 int backward_grid(int64_t tokens, int32_t dim) {
   int groups = 1;
-  with_backward_layout(dim, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
-  const int64_t want = (tokens + groups - 1) / groups;
+  with_layout<false>(dim, tokens, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
+  const int64_t want = (tokens + 2 * groups - 1) / (2 * groups);   // two rows a warp group
   const int64_t cap = 608;   // four an SM: a constant, so that the sums' order is one
   return (int)(want < cap ? want : cap);
 }
@@ -635,7 +638,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   void* part = ws;
   if (!use_ws && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
   NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
-  with_backward_layout(dim, [&](auto lay) {
+  with_layout<false>(dim, tokens, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
     auto kern = io_dtype == GDN_BF16 ? norm_backward_kernel<__nv_bfloat16, V, W>
                                      : norm_backward_kernel<float, V, W>;
@@ -643,7 +646,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   });
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
-    norm_dw_kernel<<<(dim + 31) / 32, 256, 0, stream>>>((const float*)part, grid, dim, dw);
+    norm_dw_kernel<<<(dim + 31) / 32, 1024, 0, stream>>>((const float*)part, grid, dim, dw);
     e = cudaGetLastError();
   }
   count_launches(2);
