@@ -16,7 +16,8 @@
 // fp32 sums round once more to the bf16 results).  One second launch then
 // has the tiles of dx (K runs over dG then dU) and of both weight gradients
 // (rows over dG^T then dU^T), the longer K first, so that the short tiles
-// fill the end of the grid.
+// fill the end of the grid.  Where a product's tiles are few and their K is
+// long, K is cut into parts, whose fp32 sums a third launch adds in order.
 #include "gemm_split.cuh"
 #include "hostcheck.cuh"
 
@@ -29,6 +30,69 @@ using namespace hostcheck;
 int64_t grad_pitch(int32_t hidden) { return ((int64_t)hidden + 15) / 16 * 16; }
 size_t grad_bytes(int64_t tokens, int32_t hidden) {
   return align_up((size_t)tokens * grad_pitch(hidden) * 2, 256);
+}
+
+// Parts of K of the second launch's two products: enough that no tile is
+// longer than the pairs' average load, where that shortens the launch by more
+// than the sums cost (16 K blocks, 5 us).  The pair count is that of the
+// device; a constant, so that a workspace's size needs no device.
+constexpr int kPairs = 76;
+struct Parts {
+  int dx, dw;              // parts of K
+  int64_t dx_rows, dw_rows;   // rows of a part
+  size_t dx_off, dw_off, bytes;   // of the fp32 parts in the scratch, after dG and dU
+};
+int parts_of(int64_t tiles, int64_t blocks, int64_t total) {
+  const int64_t mean = (total + kPairs - 1) / kPairs;
+  if (mean < 1 || tiles * 2 > kPairs || blocks < mean + 16) return 1;
+  int64_t n = (blocks + mean - 1) / mean;
+  if (n > 8) n = 8;
+  return (int)n;
+}
+Parts plan_parts(int64_t tokens, int32_t dim, int32_t hidden) {
+  const int64_t dt = ((int64_t)dim + 255) / 256, tx = (tokens + 255) / 256 * dt;
+  const int64_t tw = 2 * (((int64_t)hidden + 255) / 256) * dt;
+  const int64_t kx = 2 * (((int64_t)hidden + 63) / 64), kw = (tokens + 63) / 64;
+  const int64_t total = tx * kx + tw * kw;
+  Parts p;
+  p.dx = parts_of(tx, kx, total);
+  p.dw = parts_of(tw, kw, total);
+  p.dx_rows = (tokens + 255) / 256 * 256;
+  p.dw_rows = ((int64_t)hidden + 255) / 256 * 256;
+  p.dx_off = 2 * grad_bytes(tokens, hidden);
+  p.dw_off = p.dx_off + (p.dx > 1 ? align_up((size_t)p.dx * p.dx_rows * dim * 4, 256) : 0);
+  p.bytes = p.dw_off + (p.dw > 1 ? align_up(2 * (size_t)p.dw * p.dw_rows * dim * 4, 256) : 0);
+  return p;
+}
+
+// out = the parts' sum, in order, as bf16.
+struct SumArgs {
+  const float* part[3];
+  __nv_bfloat16* out[3];
+  int64_t vecs[3];     // elements / 8
+  int64_t stride[3];   // elements of a part
+  int32_t parts[3];
+};
+__global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ SumArgs a) {
+  grid_release_next();
+  grid_wait();
+  const int64_t all = a.vecs[0] + a.vecs[1] + a.vecs[2];
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all;
+       i += (int64_t)gridDim.x * 256) {
+    const int w = i < a.vecs[0] ? 0 : i < a.vecs[0] + a.vecs[1] ? 1 : 2;
+    const int64_t e = 8 * (i - (w > 0 ? a.vecs[0] : 0) - (w > 1 ? a.vecs[1] : 0));
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = 0; p < a.parts[w]; ++p) {
+      const float4* f = reinterpret_cast<const float4*>(a.part[w] + p * a.stride[w] + e);
+      const float4 x = __ldg(f), y = __ldg(f + 1);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    *reinterpret_cast<uint4*>(a.out[w] + e) =
+        make_uint4(gemm::pack2(v[0], v[1]), gemm::pack2(v[2], v[3]), gemm::pack2(v[4], v[5]),
+                   gemm::pack2(v[6], v[7]));
+  }
 }
 
 int shape_check(int64_t tokens, int32_t dim, int32_t hidden, int32_t act, int32_t io) {
@@ -49,6 +113,7 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
   p.m_half = p.m_tiles = (int32_t)((tokens + 255) / 256);
   p.n_tiles = (hidden + 127) / 128;
   p.k_half = p.k_blocks = (dim + 63) / 64;
+  p.k_parts = 1;
   p.M = (int32_t)tokens;
   p.N = hidden;
   g.problems = 1;
@@ -59,13 +124,6 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
     return false;
   p.a[1] = p.a[0];
   return true;
-}
-
-// Few tokens: the split form, two CTAs an SM to keep the weights coming
-// (2048 -> 6144, us, split form / pair form: 1 token 11.1 / 20, 64 tokens
-// 12.6 / 17, 128 tokens 14.8 / 17, 256 tokens 19.4 / 16.5).
-bool takes_split(int64_t tokens, int32_t hidden) {
-  return tokens <= 128 && (hidden + 63) / 64 <= 65535;
 }
 
 int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void* h,
@@ -83,10 +141,12 @@ int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void
   const int sms = sm_count();
   unsigned* status = status_ptr();
   if (sms < 2 || !status) return GDN_ERR_CUDA;
-  if (takes_split(tokens, hidden)) {
+  // two CTAs an SM keep the weights of few tokens coming
+  const gemm::SplitPlan plan = gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64,
+                                                (dim + 63) / 64, sms, 2 * sms, 8);
+  if (plan.columns) {
     gemm::SplitArgs a;
     memset(&a, 0, sizeof a);
-    const int nb = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
     a.k_blocks = (dim + 63) / 64;
     a.tokens = (int32_t)tokens;
     a.n = hidden;
@@ -95,10 +155,9 @@ int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void
     a.status = status;
     if (!gemm::matrix_map(&a.w[0], wg, false, dim, hidden, (int64_t)dim * 2, 64) ||
         !gemm::matrix_map(&a.w[1], wu, false, dim, hidden, (int64_t)dim * 2, 64) ||
-        !gemm::matrix_map(&a.x, x, false, dim, tokens, (int64_t)dim * 2, nb))
+        !gemm::matrix_map(&a.x, x, false, dim, tokens, (int64_t)dim * 2, plan.columns))
       return GDN_ERR_CUDA;
-    const int split = gemm::split_of((hidden + 63) / 64, a.k_blocks, 2 * sms, 8);
-    return gemm::launch_split<false, true, __nv_bfloat16>(a, nb, split, stream) == cudaSuccess
+    return gemm::launch_split<false, true, __nv_bfloat16>(a, plan, stream) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_CUDA;
   }
@@ -139,7 +198,10 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   g.problems = 2;
   g.group_m = 8;   // either operand is read once for the tiles in flight, which are about square
   const int32_t kx = (hidden + 63) / 64, kw = (int32_t)((tokens + 63) / 64);
-  const int ix = 2 * kx >= kw ? 0 : 1;
+  const Parts parts = plan_parts(tokens, dim, hidden);
+  const int ix = 2 * kx / parts.dx >= kw / parts.dw ? 0 : 1;
+  float* dx_parts = (float*)((char*)scratch + parts.dx_off);
+  float* dw_parts = (float*)((char*)scratch + parts.dw_off);
   gemm::Problem& px = g.p[ix];
   px.m_half = px.m_tiles = (int32_t)((tokens + 255) / 256);
   px.n_tiles = (dim + 255) / 256;
@@ -148,7 +210,9 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   px.b_mn = 1;
   px.M = (int32_t)tokens;
   px.N = dim;
-  px.out[0] = px.out[1] = dx;
+  px.k_parts = parts.dx;
+  px.part_rows = (int32_t)parts.dx_rows;
+  px.out[0] = px.out[1] = parts.dx > 1 ? dx_parts : dx;
   px.ldc = dim;
   gemm::Problem& pw = g.p[1 - ix];
   pw.m_half = (hidden + 255) / 256;
@@ -158,8 +222,11 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   pw.a_mn = pw.b_mn = 1;
   pw.M = hidden;
   pw.N = dim;
-  pw.out[0] = dwg;
-  pw.out[1] = dwu;
+  pw.k_parts = parts.dw;
+  pw.part_rows = (int32_t)parts.dw_rows;
+  const int64_t dw_half = (int64_t)parts.dw * parts.dw_rows * dim;
+  pw.out[0] = parts.dw > 1 ? dw_parts : dwg;
+  pw.out[1] = parts.dw > 1 ? dw_parts + dw_half : dwu;
   pw.ldc = dim;
   const int64_t gp = pitch * 2, dp = (int64_t)dim * 2;
   if (!gemm::matrix_map(&px.a[0], dG, false, hidden, tokens, gp, 128) ||
@@ -171,7 +238,29 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
       !gemm::matrix_map(&pw.b[0], x, false, dim, tokens, dp, 64))
     return cudaErrorUnknown;
   pw.b[1] = pw.b[0];
-  return gemm::launch_pair<false, gemm::kStore>(g, sms, stream);
+  e = gemm::launch_pair<false, gemm::kStore>(g, sms, stream);
+  if (e != cudaSuccess || (parts.dx == 1 && parts.dw == 1)) return e;
+  SumArgs a;
+  memset(&a, 0, sizeof a);
+  if (parts.dx > 1) {
+    a.part[0] = dx_parts;
+    a.out[0] = (__nv_bfloat16*)dx;
+    a.vecs[0] = tokens * dim / 8;
+    a.stride[0] = parts.dx_rows * dim;
+    a.parts[0] = parts.dx;
+  }
+  for (int i = 1; parts.dw > 1 && i < 3; ++i) {
+    a.part[i] = dw_parts + (i - 1) * dw_half;
+    a.out[i] = (__nv_bfloat16*)(i == 1 ? dwg : dwu);
+    a.vecs[i] = (int64_t)hidden * dim / 8;
+    a.stride[i] = parts.dw_rows * dim;
+    a.parts[i] = parts.dw;
+  }
+  const int64_t blocks = (a.vecs[0] + a.vecs[1] + a.vecs[2] + 255) / 256, most = 8 * (int64_t)sms;
+  e = launch_dependent(sum_parts_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 0,
+                       stream, a);
+  count_launches(1);
+  return e;
 }
 
 int ffn_backward(const void* x, const void* wg, const void* wu, const void* dh, int32_t act,
@@ -183,7 +272,7 @@ int ffn_backward(const void* x, const void* wg, const void* wu, const void* dh, 
   const void* v16[] = {x, wg, wu, dh, dx, dwg, dwu};
   for (const void* p : v16)
     if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
-  const size_t need = 2 * grad_bytes(tokens, hidden);
+  const size_t need = plan_parts(tokens, dim, hidden).bytes;
   if (use_ws && need) {
     if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
@@ -227,7 +316,7 @@ int gdn_gated_ffn(const void* x, const void* w_gate, const void* w_up, int32_t a
 size_t gdn_gated_ffn_backward_workspace_size(int64_t tokens, int32_t dim, int32_t hidden,
                                              int32_t io_dtype) {
   if (shape_check(tokens, dim, hidden, GDN_GATE_SILU, io_dtype)) return SIZE_MAX;
-  return 2 * grad_bytes(tokens, hidden);
+  return plan_parts(tokens, dim, hidden).bytes;
 }
 
 int gdn_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* dh,

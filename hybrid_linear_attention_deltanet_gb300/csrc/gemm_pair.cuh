@@ -54,14 +54,20 @@ struct Problem {
   int32_t k_half;       // K blocks in each half of K (all of them: one half)
   int32_t k_blocks;
   int32_t a_mn, b_mn;   // operand stored with its rows contiguous instead of its K
+  int32_t k_parts;      // tiles share K among this many; more than 1: fp32 sums of each
+                        // part at out + part * part_rows * ldc (kStore)
+  int32_t part_rows;
   int32_t M, N;         // valid rows (of each half) and columns
   void* out[2];
   int64_t ldc;
 };
+inline int64_t tiles_of(const Problem& p) {
+  return (int64_t)p.m_tiles * p.n_tiles * p.k_parts;
+}
 
 struct PairArgs {
   Problem p[2];
-  int32_t problems;
+  int32_t problems, tiles;
   int32_t group_m;      // tiles of rows whose columns are visited together (group_rows)
   int32_t act;
   const __nv_bfloat16* dh;   // kGateGrad: [M][ldh]
@@ -93,6 +99,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct Tile {
   int p, half, m0, n0;   // problem, half of its rows, first row of the half, first column
+  int part, k0, k1;      // part of K: its K blocks
 };
 
 // Tile t: groups of group_m row tiles, all columns of a group before the next
@@ -100,12 +107,22 @@ struct Tile {
 __device__ __forceinline__ Tile tile_at(const PairArgs& g, int t) {
   Tile r;
   r.p = 0;
-  const int first = g.p[0].m_tiles * g.p[0].n_tiles;
+  const int first = g.p[0].m_tiles * g.p[0].n_tiles * g.p[0].k_parts;
   if (t >= first) {
     r.p = 1;
     t -= first;
   }
   const Problem& p = g.p[r.p];
+  r.part = 0;
+  r.k0 = 0;
+  r.k1 = p.k_blocks;
+  if (p.k_parts > 1) {
+    const int all = p.m_tiles * p.n_tiles;
+    r.part = t / all;
+    t -= r.part * all;
+    r.k0 = (int)((int64_t)p.k_blocks * r.part / p.k_parts);
+    r.k1 = (int)((int64_t)p.k_blocks * (r.part + 1) / p.k_parts);
+  }
   const int per = g.group_m * p.n_tiles, grp = t / per, in = t - grp * per;
   const int left = p.m_tiles - grp * g.group_m, gm = left < g.group_m ? left : g.group_m;
   const int mt = grp * g.group_m + in % gm, nt = in / gm;
@@ -145,13 +162,13 @@ __device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const 
 // left out.  stage_free() must return before the next stage_put.
 template <typename T>
 __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Problem& p, int half,
-                                          int row0, int n0) {
+                                          int row0, int n0, int shift = 0) {
   if (row0 >= p.M || n0 >= p.N) return;
   if (p.c_tma) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(&p.c[half], buf, n0, row0);
+      tma_store_2d(&p.c[half], buf, n0, row0 + shift);
       bulk_commit();
     }
   } else {   // rows that start anywhere: a row at a time, 32 elements a step
@@ -217,8 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   grid_release_next();
   grid_wait();
   const uint32_t tmem = tmem_base;
-  const int n_tiles =
-      g.p[0].m_tiles * g.p[0].n_tiles + (g.problems > 1 ? g.p[1].m_tiles * g.p[1].n_tiles : 0);
+  const int n_tiles = g.tiles;
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   bool ok = true;
   float* scales = reinterpret_cast<float*>(sm + kStages * kStageBytes + kEpiWarps * kBounce);
@@ -240,8 +256,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // gated: both CTAs' halves of B are the same 128 features of Wg and Wu
       const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + 128 * (int)rank;
       const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
-      const int k_half = p.k_half, k_blocks = p.k_blocks;
-      for (int kb = 0; kb < k_blocks; ++kb) {
+      const int k_half = p.k_half;
+      for (int kb = tl.k0; kb < tl.k1; ++kb) {
         ok = mbar_wait_warp(&empty[st], ph ^ 1u, kWaitNs);
         if (!ok) break;
         if (lead) {
@@ -280,7 +296,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int st = 0, buf = 0;
     uint32_t ph = 0, aph = 0;
     for (int t = t0; t < n_tiles && ok; t += step) {
-      const Problem& p = g.p[tile_at(g, t).p];
+      const Tile tl = tile_at(g, t);
+      const Problem& p = g.p[tl.p];
       const uint32_t idesc =
           kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, 256, p.a_mn, p.b_mn);
       // a K-major block advances 32 bytes an instruction inside the swizzled
@@ -289,9 +306,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
       const uint64_t a0 = smem_desc(sm0, a_mn ? 8192 : 16, 1024, kSwizzle128B);
       const uint64_t b0 = smem_desc(sm0 + kOperand, b_mn ? 8192 : 16, 1024, kSwizzle128B);
-      const int k_blocks = p.k_blocks;
-      for (int kb = 0; kb < k_blocks; ++kb) {
-        const bool first = kFp8 || kb == 0, last = kFp8 || kb + 1 == k_blocks;
+      for (int kb = tl.k0; kb < tl.k1; ++kb) {
+        const bool first = kFp8 || kb == tl.k0, last = kFp8 || kb + 1 == tl.k1;
         if (first) {
           ok = mbar_wait_warp(&acc_empty[buf], aph ^ 1u, kWaitNs);
           if (!ok) break;
@@ -446,6 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int n0 = tl.n0 + 128 * part;
+        const int shift = tl.part * p.part_rows;
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t r[32];
@@ -455,10 +472,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (c % 64 == 0) stage_free(lane);
-          stage_put<__nv_bfloat16>(bounce, lane, c % 64, v);
-          if (c % 64 == 32)
-            stage_out<__nv_bfloat16>(bounce, lane, p, tl.half, row0, n0 + c - 32);
+          if (p.k_parts > 1) {
+            stage_free(lane);
+            stage_put<float>(bounce, lane, 0, v);
+            stage_out<float>(bounce, lane, p, tl.half, row0, n0 + c, shift);
+          } else {
+            if (c % 64 == 0) stage_free(lane);
+            stage_put<__nv_bfloat16>(bounce, lane, c % 64, v);
+            if (c % 64 == 32)
+              stage_out<__nv_bfloat16>(bounce, lane, p, tl.half, row0, n0 + c - 32);
+          }
         }
         advance();
       } else {
@@ -585,8 +608,11 @@ inline bool matrix_map(CUtensorMap* m, const void* base, bool fp8, int64_t inner
 }
 
 // The outputs c[0], c[1] = out[0], out[1], [M][N] with ldc elements a row:
-// TMA stores where rows start on 16 bytes, plain ones elsewhere.
+// TMA stores where rows start on 16 bytes, plain ones elsewhere.  (Parts of K
+// write [k_parts][part_rows][N], whose rows past M no one reads; their rows
+// have to start on 16 bytes.)
 inline bool output_maps(Problem& p, bool f32) {
+  if (p.k_parts > 1) f32 = true;
   const int64_t pitch = p.ldc * (f32 ? 4 : 2);
   p.c_tma = pitch % 16 == 0;
   EncodeFn enc = encoder();
@@ -597,7 +623,8 @@ inline bool output_maps(Problem& p, bool f32) {
       break;
     }
     memset(&p.c[i], 0, sizeof p.c[i]);
-    cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+    cuuint64_t dims[2] = {(cuuint64_t)p.N,
+                          (cuuint64_t)(p.k_parts > 1 ? (int64_t)p.k_parts * p.part_rows : p.M)};
     cuuint64_t strides[1] = {(cuuint64_t)pitch};
     cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
     cuuint32_t es[2] = {1, 1};
@@ -629,8 +656,10 @@ cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
   int64_t tiles = 0;
   for (int i = 0; i < g.problems; ++i) {
     if (!output_maps(g.p[i], kEpi == kStoreF32)) return cudaErrorUnknown;
-    tiles += (int64_t)g.p[i].m_tiles * g.p[i].n_tiles;
+    tiles += tiles_of(g.p[i]);
   }
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  g.tiles = (int32_t)tiles;
   const int64_t pairs = sms / 2;
   e = launch_dependent(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads,
                        kSmem, 0, st, g);

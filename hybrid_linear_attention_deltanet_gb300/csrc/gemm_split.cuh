@@ -37,8 +37,8 @@ constexpr int kSplitScaleBytes = 16384;   // of a CTA's staged scales
 template <bool kFp8, int kNB>
 struct SplitShape {
   static constexpr uint32_t kStage = kOperand + kNB * 128;
-  static constexpr int kStages = kNB <= 16 ? 5 : kNB <= 64 ? 4 : 3;
-  static constexpr int kAcc = !kFp8 ? 1 : kNB <= 64 ? 4 : 2;   // accumulators in tensor memory
+  static constexpr int kStages = kNB <= 16 ? 5 : 4;
+  static constexpr int kAcc = kFp8 ? 4 : 1;   // accumulators in tensor memory
   static constexpr uint32_t kCols = kAcc * kNB < 32 ? 32 : kAcc * kNB;
   static constexpr uint32_t kSmem = kStages * kStage + (kFp8 ? kSplitScaleBytes : 0) + 1024;
   static_assert(kNB * 128 * 4 <= kStages * kStage, "the partial products reuse the stages");
@@ -267,12 +267,30 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   if (warp == 5) tmem_dealloc(tmem, S::kCols);
 }
 
-// CTAs a cluster splits K over: as many as keep the grid within `ctas` and
-// leave each at least `least` K blocks, eight at most.
-inline int split_of(int64_t units, int k_blocks, int ctas, int least) {
+// How a call takes the split form: columns a CTA and CTAs a cluster, or
+// columns 0 for the pair form.
+//
+// Up to 64 tokens are one tile of columns, and K is split until `ctas` CTAs
+// run (each keeping `least` K blocks).  More tokens take tiles of 64 columns
+// while those are within one CTA an SM: fewer, longer chains of K blocks in
+// the pair form would leave most SMs idle.  (us, split / pair.  8 bits, 2048
+// -> 4608: 16 tokens 4.5 / 13, 64 tokens 5.9 / 13, 256 tokens 9.9 / 11.1;
+// 4096 -> 1000: 300 tokens 9.7 / 16.2; 4096 -> 512: 400 tokens 6.7 / 15.8;
+// 2048 -> 2048: 512 tokens, 128 CTAs, 9.8 / 9.9; 1024 -> 4608: 300 tokens, 180
+// CTAs, 12.5 / 7.0.  Gated, 2048 -> 6144: 64 tokens 12.7 / 14.0, 128 tokens,
+// 192 CTAs, 15.6 / 14.3; 1000 -> 1000: 200 tokens 6.9 / 10.1.)
+struct SplitPlan {
+  int columns, split;
+};
+inline SplitPlan plan_split(int64_t tokens, int64_t row_tiles, int k_blocks, int sms, int ctas,
+                            int least) {
+  const int nb = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+  const int64_t units = row_tiles * ((tokens + nb - 1) / nb);
+  if (row_tiles > 65535 || (tokens > 64 && units > sms)) return {0, 0};
+  if (tokens > 64) ctas = sms + sms / 16;
   int64_t s = ctas / units;
   if (s > k_blocks / least) s = k_blocks / least;
-  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+  return {nb, s < 1 ? 1 : s > 8 ? 8 : (int)s};
 }
 
 template <bool kFp8, bool kGated, int kNB, typename T>
@@ -289,14 +307,13 @@ cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st)
   return e;
 }
 
-// nb columns (16, 32, 64 or 128) a CTA, K split over `split` CTAs.
 template <bool kFp8, bool kGated, typename T>
-cudaError_t launch_split(const SplitArgs& g, int nb, int split, cudaStream_t st) {
-  switch (nb) {
+cudaError_t launch_split(const SplitArgs& g, const SplitPlan& plan, cudaStream_t st) {
+  const unsigned split = (unsigned)plan.split;
+  switch (plan.columns) {
     case 16: return launch_split_nb<kFp8, kGated, 16, T>(g, split, st);
     case 32: return launch_split_nb<kFp8, kGated, 32, T>(g, split, st);
-    case 64: return launch_split_nb<kFp8, kGated, 64, T>(g, split, st);
-    default: return launch_split_nb<kFp8, kGated, 128, T>(g, split, st);
+    default: return launch_split_nb<kFp8, kGated, 64, T>(g, split, st);
   }
 }
 

@@ -14,25 +14,6 @@ namespace {
 
 using namespace hostcheck;
 
-// The split form's columns and K split for a call, or columns 0 for the pair
-// form.  One wave of CTAs is what pays (their epilogues are the longer part
-// of a K block): 2048 -> 4608, us, split form / pair form: 16 tokens 4.5 / 13,
-// 64 tokens 5.9 / 13, 128 tokens 7.3 / 13, 256 tokens 9.9 / 13.8, 512 tokens
-// 16.0 / 14.
-struct SplitPlan {
-  int columns, split;
-};
-SplitPlan plan_split(int64_t tokens, int32_t n, int32_t blocks, int sms) {
-  if (tokens > 256) return {0, 0};
-  const int nb = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
-  const int64_t units = (int64_t)((n + 127) / 128) * ((tokens + nb - 1) / nb);
-  if (tokens > 64 && units > sms) return {0, 0};
-  const int split = gemm::split_of(units, blocks, sms, 4);
-  const int64_t scales = (int64_t)((blocks + split - 1) / split) * nb * 4;
-  if (scales > gemm::kSplitScaleBytes || (n + 127) / 128 > 65535) return {0, 0};
-  return {nb, split};
-}
-
 int linear_common(const void* x, const float* sx, const void* w, const float* sw, void* out,
                   int64_t tokens, int32_t k, int32_t n, int32_t out_dtype, cudaStream_t stream) {
   if (tokens < 0 || k < 1 || n < 1) return GDN_ERR_INVALID_ARG;
@@ -54,8 +35,10 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   const int sms = sm_count();
   unsigned* status = status_ptr();
   if (sms < 2 || !status) return GDN_ERR_CUDA;
-  const SplitPlan plan = plan_split(tokens, n, blocks, sms);
-  if (plan.columns) {
+  const gemm::SplitPlan plan =
+      gemm::plan_split(tokens, ((int64_t)n + 127) / 128, blocks, sms, sms, 4);
+  if (plan.columns && (int64_t)((blocks + plan.split - 1) / plan.split) * plan.columns * 4 <=
+                          gemm::kSplitScaleBytes) {
     gemm::SplitArgs a;
     memset(&a, 0, sizeof a);
     a.k_blocks = blocks;
@@ -70,8 +53,8 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
       return GDN_ERR_CUDA;
     const cudaError_t e =
         out_dtype == GDN_BF16
-            ? gemm::launch_split<true, false, __nv_bfloat16>(a, plan.columns, plan.split, stream)
-            : gemm::launch_split<true, false, float>(a, plan.columns, plan.split, stream);
+            ? gemm::launch_split<true, false, __nv_bfloat16>(a, plan, stream)
+            : gemm::launch_split<true, false, float>(a, plan, stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
   }
   gemm::PairArgs g;
@@ -82,6 +65,7 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   p.m_half = p.m_tiles = (int32_t)mt;
   p.n_tiles = (int32_t)nt;
   p.k_half = p.k_blocks = blocks;
+  p.k_parts = 1;
   p.M = (int32_t)tokens;
   p.N = n;
   p.out[0] = p.out[1] = out;

@@ -577,9 +577,10 @@ int gdn_gated_ffn(const void* x, const void* w_gate, const void* w_up, int32_t a
  *
  * all bf16 (products accumulate in fp32; dG and dU are rounded to bf16 where
  * they enter the products).  dx [tokens, dim], dw_* [hidden, dim],
- * overwritten.  No output may overlap an input or another output.  Scratch
- * (dG and dU: 4 bytes a token and feature) from the library's pool, or a
- * caller's 256-byte aligned workspace of at least
+ * overwritten; the order of all sums is fixed.  No output may overlap an input
+ * or another output.  Scratch (dG and dU: 4 bytes a token and feature; for
+ * small products with a long inner axis also fp32 sums of its parts) from the
+ * library's pool, or a caller's 256-byte aligned workspace of at least
  * gdn_gated_ffn_backward_workspace_size bytes (rules as gdn_prefill_ws).
  */
 int gdn_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up, const void* dh,

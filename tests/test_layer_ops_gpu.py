@@ -393,7 +393,10 @@ def check_ffn_backward(tokens, dim, hidden, act, seed):
     return x, wg, wu, dh, r
 
 
-@pytest.mark.parametrize("tokens,dim,hidden", FFN_SHAPES + [(1, 2048, 40), (700, 264, 2731)])
+@pytest.mark.parametrize("tokens,dim,hidden", FFN_SHAPES + [
+    (1, 2048, 40), (700, 264, 2731),
+    # few tiles with a long inner axis: dx, the weight gradients, both in parts
+    (250, 520, 6000), (5000, 264, 300), (1111, 1032, 2731), (3000, 72, 2100)])
 @pytest.mark.parametrize("act", ["silu", "sigmoid"])
 def test_gated_ffn_backward(tokens, dim, hidden, act):
     x, wg, wu, dh, r = check_ffn_backward(tokens, dim, hidden, act, 7 * tokens + dim + hidden)
