@@ -227,6 +227,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fence_barrier_init();
   }
   if (warp == 2) tmem_alloc_pair(&tmem_base, 512);
+  if (warp == 3 && lane == 0) {
+    prefetch_tensormap(&g.p[0].a[0]);
+    prefetch_tensormap(&g.p[0].b[kEpi >= kGate ? rank : 0]);
+    if (g.p[0].c_tma) prefetch_tensormap(&g.p[0].c[0]);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers exist before either uses the other's

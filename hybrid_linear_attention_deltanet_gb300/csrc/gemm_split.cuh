@@ -9,9 +9,11 @@
 // One launch, whose CTAs (two an SM) hold all of the weights' bytes in
 // flight that their stages allow.
 //
-// Roles (6 warps): warps 0..3 take accumulators out, warp 4 fetches, warp 5
-// multiplies.  8-bit operands: every K block of 128 is an accumulator of its
-// own, scaled (a token's scale times the weight block's) into fp32 registers.
+// Roles: the first 4 or 8 warps take accumulators out, then one fetches and
+// one multiplies.  8-bit operands: every K block of 128 is an accumulator of
+// its own, scaled (a token's scale times the weight block's) into fp32
+// registers; with 32 columns or more that takes 8 warps, half the columns
+// each (256 tokens, 2048 -> 4608: 10.3 us with 4).
 // Waits are bounded as in gemm_pair.cuh.
 #pragma once
 
@@ -31,21 +33,23 @@ struct SplitArgs {
   unsigned* status;
 };
 
-constexpr int kSplitThreads = 192;
 constexpr int kSplitScaleBytes = 16384;   // of a CTA's staged scales
 
 template <bool kFp8, int kNB>
 struct SplitShape {
+  static constexpr int kEpi = kFp8 && kNB >= 32 ? 8 : 4;     // warps that take accumulators out
+  static constexpr int kCols = kNB / (kEpi / 4);             // columns of each
+  static constexpr int kThreads = 32 * (kEpi + 2);
   static constexpr uint32_t kStage = kOperand + kNB * 128;
   static constexpr int kStages = kNB <= 16 ? 5 : 4;
   static constexpr int kAcc = kFp8 ? 4 : 1;   // accumulators in tensor memory
-  static constexpr uint32_t kCols = kAcc * kNB < 32 ? 32 : kAcc * kNB;
+  static constexpr uint32_t kTmem = kAcc * kNB < 32 ? 32 : kAcc * kNB;
   static constexpr uint32_t kSmem = kStages * kStage + (kFp8 ? kSplitScaleBytes : 0) + 1024;
   static_assert(kNB * 128 * 4 <= kStages * kStage, "the partial products reuse the stages");
 };
 
 template <bool kFp8, bool kGated, int kNB, typename T>
-__global__ void __launch_bounds__(kSplitThreads, 2)
+__global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
     split_gemm_kernel(const __grid_constant__ SplitArgs g) {
   using S = SplitShape<kFp8, kNB>;
   extern __shared__ uint8_t smem_raw[];
@@ -68,11 +72,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
     for (int i = 0; i < S::kAcc; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], S::kEpi);
     }
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc(&tmem_base, S::kCols);
+  if (warp == S::kEpi + 1) tmem_alloc(&tmem_base, S::kTmem);
+  if (warp == S::kEpi && lane == 0) {
+    prefetch_tensormap(&g.w[0]);
+    prefetch_tensormap(&g.x);
+    if (kGated) prefetch_tensormap(&g.w[1]);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -81,7 +90,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   const uint32_t tmem = tmem_base;
   bool ok = true;
 
-  if (warp == 4) {
+  if (warp == S::kEpi) {
     // ---------------------------------------------------------- fetch
     const bool lead = elect_one();
     int st = 0;
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         ph ^= 1u;
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == S::kEpi + 1) {
     // -------------------------------------------------------- multiply
     const bool lead = elect_one();
     const uint64_t w0 = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
@@ -145,33 +154,35 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
   } else {
     // ------------------------------------- accumulators out of tensor memory
-    const uint32_t src = tmem + ((uint32_t)(32 * warp) << 16);
-    float acc[kNB];
+    constexpr int kCols = S::kCols;
+    const int row = 32 * (warp & 3) + lane, col0 = kCols * (warp >> 2);
+    const uint32_t src = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col0;
+    float acc[kCols];
     if constexpr (kFp8) {
       const float* sw = g.sw + (size_t)(f0 / 128) * g.k_blocks + kb0;
-      for (int e = tid; e < kbs * kNB; e += 128) {
+      for (int e = tid; e < kbs * kNB; e += 32 * S::kEpi) {
         const int c = e / kbs, i = e - c * kbs;   // consecutive threads: one token's blocks
         scales[i * kNB + c] =
             t0 + c < g.tokens ? __ldg(g.sx + (size_t)(t0 + c) * g.k_blocks + kb0 + i) * __ldg(sw + i)
                               : 0.f;
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");   // these four warps
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * S::kEpi) : "memory");   // these warps
 #pragma unroll
-      for (int c = 0; c < kNB; ++c) acc[c] = 0.f;
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
       int buf = 0;
       uint32_t aph = 0;
       for (int i = 0; i < kbs; ++i) {
         ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
         if (!ok) break;
         tc_fence_after();
-        const float4* s4 = reinterpret_cast<const float4*>(scales + i * kNB);
+        const float4* s4 = reinterpret_cast<const float4*>(scales + i * kNB + col0);
         uint32_t r[2][16];   // two 16-column pieces in turn: one arrives while one is added
         tmem_ld16(src + kNB * buf, r[0]);
 #pragma unroll
-        for (int c = 0; c < kNB; c += 16) {
+        for (int c = 0; c < kCols; c += 16) {
           uint32_t(&x)[16] = r[(c / 16) & 1];
           tmem_ld_wait_regs(x);
-          if (c + 16 < kNB) {
+          if (c + 16 < kCols) {
             tmem_ld16(src + kNB * buf + c + 16, r[(c / 16 + 1) & 1]);
           } else {
             tc_fence_before();
@@ -196,7 +207,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       ok = mbar_wait_warp(&acc_full[0], 0, kWaitNs);
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < kNB; c += 16) {
+      for (int c = 0; c < kCols; c += 16) {
         uint32_t r[16];
         tmem_ld16(src + c, r);
         tmem_ld_wait_regs(r);
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     // stages are free
     if (ok) {
 #pragma unroll
-      for (int c = 0; c < kNB; ++c) part[c * 128 + tid] = acc[c];
+      for (int c = 0; c < kCols; ++c) part[(col0 + c) * 128 + row] = acc[c];
     }
   }
   if (!ok) {
@@ -219,7 +230,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
   __syncwarp();
   cluster_sync_all();
-  if (warp < 4) {
+  if (warp < S::kEpi) {
     // four rows a lane: a column of the tile is 32 lanes (gated: 16, G and U
     // 64 rows apart); the columns are dealt to the cluster's CTAs in turn
     const uint32_t p0 = smem_u32(part);
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
     for (int s = 0; s < 8; ++s)
       if (s < split) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[s]) : "r"(p0), "r"(s));
-    constexpr int kLanes = kGated ? 16 : 32, kSlots = 128 / kLanes;
+    constexpr int kLanes = kGated ? 16 : 32, kSlots = 32 * S::kEpi / kLanes;
     const int cols = g.tokens - t0 < kNB ? g.tokens - t0 : kNB;
     const int row = 4 * (tid % kLanes), f = f0 + row;
     if (f < g.n) {
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   }
   __syncwarp();
   cluster_sync_all();   // no CTA leaves while another may read its partial products
-  if (warp == 5) tmem_dealloc(tmem, S::kCols);
+  if (warp == S::kEpi + 1) tmem_dealloc(tmem, S::kTmem);
 }
 
 // How a call takes the split form: columns a CTA and CTAs a cluster, or
@@ -302,7 +313,7 @@ cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st)
   if (e != cudaSuccess) return e;
   const unsigned ny = (unsigned)((g.n + (kGated ? 63 : 127)) / (kGated ? 64 : 128));
   const unsigned nz = (unsigned)((g.tokens + kNB - 1) / kNB);
-  e = launch_dependent(kern, dim3(split, ny, nz), kSplitThreads, S::kSmem, split, st, g);
+  e = launch_dependent(kern, dim3(split, ny, nz), S::kThreads, S::kSmem, split, st, g);
   count_launches(1);
   return e;
 }

@@ -445,30 +445,37 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m, float i
   return codes8(v);
 }
 
-// 1 x 128 blocks: a half warp each.
+// 1 x 128 blocks: a half warp each, kTwo at a time so that both loads are in
+// flight.
+constexpr int kTwo = 2;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
   grid_release_next();
   const int64_t units = a.rows * a.blocks;
-  const int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
+  const int64_t u0 = ((int64_t)blockIdx.x * kTwo * kThreads + threadIdx.x) >> 4;
   const int l = threadIdx.x & 15;
-  const int64_t row = u / a.blocks;
-  const int b = (int)(u - row * a.blocks), c = b * 128 + l * 8;
-  const bool in = u < units && c < a.cols;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (in) {
-    Raw<T> x;
-    x.load((const T*)a.x + (size_t)row * a.cols + c);
-    x.widen(f);
-  }
-  float m = amax8(f);
+  Raw<T> x[kTwo];
+  int64_t at[kTwo];   // the elements' place, -1 past the row's end
 #pragma unroll
-  for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  m = max_nan(m, kTiny);
-  if (in) {
-    *reinterpret_cast<uint2*>(a.q + (size_t)row * a.cols + c) =
-        quantise8(f, m, __fdiv_rn(kE4m3Max, m));
-    if (l == 0) a.scale[u] = __fdiv_rn(m, kE4m3Max);
+  for (int i = 0; i < kTwo; ++i) {
+    const int64_t u = u0 + i * (kThreads / 16), row = u / a.blocks;
+    const int c = (int)(u - row * a.blocks) * 128 + l * 8;
+    at[i] = u < units && c < a.cols ? row * a.cols + c : -1;
+    x[i].zero();
+    if (at[i] >= 0) x[i].load((const T*)a.x + at[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kTwo; ++i) {
+    float f[8];
+    x[i].widen(f);
+    float m = amax8(f);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = max_nan(m, kTiny);
+    if (at[i] >= 0) {
+      *reinterpret_cast<uint2*>(a.q + at[i]) = quantise8(f, m, __fdiv_rn(kE4m3Max, m));
+      if (l == 0) a.scale[u0 + i * (kThreads / 16)] = __fdiv_rn(m, kE4m3Max);
+    }
   }
 }
 
@@ -608,6 +615,11 @@ int backward_grid(int64_t tokens, int32_t dim) {
   const int64_t cap = 608;   // four an SM: a constant, so that the sums' order is one
   return (int)(want < cap ? want : cap);
 }
+// Scratch for them: none where one CTA's part is all of dw.
+size_t parts_bytes(int64_t tokens, int32_t dim) {
+  const int grid = backward_grid(tokens, dim);
+  return grid > 1 ? (size_t)grid * dim * 4 : 0;
+}
 bool backward_shape_ok(int64_t tokens, int32_t dim, int32_t io) {
   return tokens >= 0 && dim >= 1 && io_ok(io) && dim % 8 == 0 && dim <= kMaxDim;
 }
@@ -623,7 +635,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
     if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
   const size_t bytes = (size_t)tokens * dim * es_of(io_dtype);
   const int grid = backward_grid(tokens, dim);
-  const size_t need = (size_t)grid * dim * 4;
+  const size_t need = parts_bytes(tokens, dim);
   if (use_ws && need) {
     if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
@@ -635,8 +647,9 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
   if (tokens == 0)
     return cudaMemsetAsync(dw, 0, (size_t)dim * 4, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-  void* part = ws;
-  if (!use_ws && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
+  void* part = grid == 1 ? dw : ws;
+  const bool own = grid > 1 && !use_ws;
+  if (own && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
   NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
   with_layout<false>(dim, tokens, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
@@ -645,12 +658,12 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
     kern<<<grid, kThreads, 0, stream>>>(a);
   });
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && grid > 1) {
     norm_dw_kernel<<<(dim + 31) / 32, 1024, 0, stream>>>((const float*)part, grid, dim, dw);
     e = cudaGetLastError();
   }
-  count_launches(2);
-  if (!use_ws && scratch_free(part, stream) != cudaSuccess) return GDN_ERR_CUDA;
+  count_launches(grid > 1 ? 2 : 1);
+  if (own && scratch_free(part, stream) != cudaSuccess) return GDN_ERR_CUDA;
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -677,7 +690,7 @@ int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, f
 
 size_t gdn_residual_norm_backward_workspace_size(int64_t tokens, int32_t dim, int32_t io_dtype) {
   if (!backward_shape_ok(tokens, dim, io_dtype)) return SIZE_MAX;
-  return (size_t)backward_grid(tokens, dim) * dim * 4;
+  return parts_bytes(tokens, dim);
 }
 
 int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,
@@ -712,7 +725,7 @@ int gdn_quantize_fp8(const void* x, void* q, float* scale, int64_t rows, int32_t
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
   QuantArgs a{x, (uint8_t*)q, scale, rows, cols, blocks};
   if (block_rows == 1) {
-    const int64_t grid = (rows * blocks + 15) / 16;
+    const int64_t grid = (rows * blocks + 16 * kTwo - 1) / (16 * kTwo);
     if (grid > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     auto kern = io_dtype == GDN_BF16 ? quant_rows_kernel<__nv_bfloat16> : quant_rows_kernel<float>;
     kern<<<(unsigned)grid, kThreads, 0, stream>>>(a);

@@ -66,7 +66,8 @@ def test_residual_norm_backward_refuses(lib):  # noqa: F811
     assert f(dy=MIS) == 3 and f(dw=P(0x7000008)) == 3
     assert f(dx=X) == 1 and f(dw=W) == 1 and f(dx=P(0x2000000 + 16)) == 1
     size = lib.gdn_residual_norm_backward_workspace_size
-    assert size(17, 256, BF16) == 2 * 256 * 4 and size(0, 256, BF16) == 0
+    assert size(17, 256, BF16) == 2 * 256 * 4 and size(16, 256, BF16) == 0
+    assert size(0, 256, BF16) == 0
     assert size(1 << 20, 4096, BF16) == 608 * 4096 * 4
     assert size(16, 12, BF16) == SIZE_MAX and size(-1, 256, BF16) == SIZE_MAX
     ws = P(0x9000000)
