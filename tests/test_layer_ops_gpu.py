@@ -452,3 +452,81 @@ def test_gated_ffn_infinite_and_empty_inputs():
     one = torch.ones(8, 64, dtype=BF16, device=DEV)
     assert bool(torch.isfinite(gdn.gated_ffn(big, one, one)).all())
     assert float(gdn.gated_ffn(-big, one, one).abs().max()) == 0
+
+
+# ------------------------------------------------- graphs, streams, workspaces
+def training_step(t, ws=None):
+    """Norm, feed-forward and both gradients on fixed tensors."""
+    y, s = gdn.residual_norm(t["x"], t["w"], t["r"], EPS)
+    h = gdn.gated_ffn(y, t["wg"], t["wu"])
+    f = gdn.gated_ffn_backward(y, t["wg"], t["wu"], t["dh"],
+                               workspace=None if ws is None else ws[0])
+    n = gdn.residual_norm_backward(f["dx"], s, t["w"], t["r"], EPS,
+                                   workspace=None if ws is None else ws[1])
+    return [y, s, h, *f.values(), *n.values()]
+
+
+def step_tensors(seed, tokens=300, dim=264, hidden=700):
+    g = gen(seed)
+    x, wg, wu, dh = ffn_inputs(tokens, dim, hidden, seed)
+    return dict(x=x, r=randn(g, tokens, dim, dtype=BF16), w=1 + 0.1 * randn(g, dim), wg=wg, wu=wu,
+                dh=dh)
+
+
+@pytest.mark.parametrize("own_workspace", [False, True])
+def test_training_step_in_a_graph(own_workspace):
+    t, other = step_tensors(51), step_tensors(52)
+    want = [training_step(t), training_step(other)]
+    tokens, dim, hidden = 300, 264, 700
+    sizes = (gdn.gated_ffn_backward_workspace_size(tokens, dim, hidden),
+             gdn.residual_norm_backward_workspace_size(tokens, dim))
+    ws = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes] if own_workspace else None
+    live = {k: v.clone() for k, v in t.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = training_step(live, ws)
+    for source, ref in ((t, want[0]), (other, want[1]), (t, want[0])):
+        for k, v in source.items():
+            live[k].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, ref):
+            assert torch.equal(a, b)
+    assert gdn.device_status() == 0
+
+
+def test_streams_side_by_side():
+    """The same calls on two streams at once give each stream's own results."""
+    sets = [step_tensors(61), step_tensors(62, tokens=1500, dim=512, hidden=900)]
+    g = gen(63)
+    q = [gdn.quantize_fp8(randn(g, n, 512, dtype=BF16)) for n in (40, 700)]
+    w = gdn.quantize_fp8(randn(g, 300, 512, dtype=BF16), block_rows=128)
+    want = [training_step(t) + [gdn.linear_fp8(*a, *w)] for t, a in zip(sets, q)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(training_step(sets[i]) + [gdn.linear_fp8(*q[i], *w)])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            for a, b in zip(r, want[i]):
+                assert torch.equal(a, b)
+    assert gdn.device_status() == 0
+
+
+def test_workspace_stays_inside():
+    tokens, dim, hidden = 1111, 264, 2731          # weight gradients and dx in parts
+    x, wg, wu, dh = ffn_inputs(tokens, dim, hidden, 71)
+    n = gdn.gated_ffn_backward_workspace_size(tokens, dim, hidden)
+    b = Guarded((n,), torch.uint8)
+    gdn.gated_ffn_backward(x, wg, wu, dh, workspace=b.t)
+    b.check()
+    n = gdn.residual_norm_backward_workspace_size(tokens, dim)
+    b = Guarded((n,), torch.uint8)
+    gdn.residual_norm_backward(x, x, torch.ones(dim, device=DEV), workspace=b.t)
+    b.check()
+    with pytest.raises(gdn.GDNError):
+        gdn.residual_norm_backward(x, x, torch.ones(dim, device=DEV), workspace=b.t[:-256])
