@@ -126,6 +126,25 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
   return true;
 }
 
+// The same for few tokens (gemm_split.cuh); two CTAs an SM keep the weights
+// coming.
+gemm::SplitPlan plan_projections(int64_t tokens, int32_t dim, int32_t hidden, int sms) {
+  return gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64, (dim + 63) / 64, sms, 2 * sms, 8);
+}
+bool split_projections(gemm::SplitArgs& a, const gemm::SplitPlan& plan, const void* x,
+                       const void* wg, const void* wu, int32_t act, int64_t tokens, int32_t dim,
+                       int32_t hidden) {
+  memset(&a, 0, sizeof a);
+  a.k_blocks = (dim + 63) / 64;
+  a.tokens = (int32_t)tokens;
+  a.n = hidden;
+  a.act = act;
+  const int64_t pitch = (int64_t)dim * 2;
+  return gemm::matrix_map(&a.w[0], wg, false, dim, hidden, pitch, 64) &&
+         gemm::matrix_map(&a.w[1], wu, false, dim, hidden, pitch, 64) &&
+         gemm::matrix_map(&a.x, x, false, dim, tokens, pitch, (uint32_t)plan.columns);
+}
+
 int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void* h,
                 int64_t tokens, int32_t dim, int32_t hidden, int32_t io, cudaStream_t stream) {
   if (const int rc = shape_check(tokens, dim, hidden, act, io)) return rc;
@@ -141,23 +160,14 @@ int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void
   const int sms = sm_count();
   unsigned* status = status_ptr();
   if (sms < 2 || !status) return GDN_ERR_CUDA;
-  // two CTAs an SM keep the weights of few tokens coming
-  const gemm::SplitPlan plan = gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64,
-                                                (dim + 63) / 64, sms, 2 * sms, 8);
+  const gemm::SplitPlan plan = plan_projections(tokens, dim, hidden, sms);
   if (plan.columns) {
     gemm::SplitArgs a;
-    memset(&a, 0, sizeof a);
-    a.k_blocks = (dim + 63) / 64;
-    a.tokens = (int32_t)tokens;
-    a.n = hidden;
-    a.act = act;
+    if (!split_projections(a, plan, x, wg, wu, act, tokens, dim, hidden)) return GDN_ERR_CUDA;
     a.out = h;
+    a.ld = hidden;
     a.status = status;
-    if (!gemm::matrix_map(&a.w[0], wg, false, dim, hidden, (int64_t)dim * 2, 64) ||
-        !gemm::matrix_map(&a.w[1], wu, false, dim, hidden, (int64_t)dim * 2, 64) ||
-        !gemm::matrix_map(&a.x, x, false, dim, tokens, (int64_t)dim * 2, plan.columns))
-      return GDN_ERR_CUDA;
-    return gemm::launch_split<false, true, __nv_bfloat16>(a, plan, stream) == cudaSuccess
+    return gemm::launch_split<false, gemm::kGate, __nv_bfloat16>(a, plan, stream) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_CUDA;
   }
@@ -179,18 +189,31 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   const int64_t pitch = grad_pitch(hidden);
   void* dG = scratch;
   void* dU = (char*)scratch + grad_bytes(tokens, hidden);
+  cudaError_t e;
   gemm::PairArgs g;
-  memset(&g, 0, sizeof g);
-  g.status = status;
-  g.act = act;
-  if (!projections(g, x, wg, wu, tokens, dim, hidden)) return cudaErrorUnknown;
-  g.p[0].out[0] = dG;
-  g.p[0].out[1] = dU;
-  g.p[0].ldc = pitch;
-  g.dh = (const __nv_bfloat16*)dh;
-  g.ldh = hidden;
-  g.dh_wide = hidden % 8 == 0;
-  cudaError_t e = gemm::launch_pair<false, gemm::kGateGrad>(g, sms, stream);
+  const gemm::SplitPlan plan = plan_projections(tokens, dim, hidden, sms);
+  if (plan.columns) {
+    gemm::SplitArgs a;
+    if (!split_projections(a, plan, x, wg, wu, act, tokens, dim, hidden)) return cudaErrorUnknown;
+    a.out = dG;
+    a.out2 = dU;
+    a.ld = pitch;
+    a.dh = (const __nv_bfloat16*)dh;
+    a.status = status;
+    e = gemm::launch_split<false, gemm::kGateGrad, __nv_bfloat16>(a, plan, stream);
+  } else {
+    memset(&g, 0, sizeof g);
+    g.status = status;
+    g.act = act;
+    if (!projections(g, x, wg, wu, tokens, dim, hidden)) return cudaErrorUnknown;
+    g.p[0].out[0] = dG;
+    g.p[0].out[1] = dU;
+    g.p[0].ldc = pitch;
+    g.dh = (const __nv_bfloat16*)dh;
+    g.ldh = hidden;
+    g.dh_wide = hidden % 8 == 0;
+    e = gemm::launch_pair<false, gemm::kGateGrad>(g, sms, stream);
+  }
   if (e != cudaSuccess) return e;
 
   memset(&g, 0, sizeof g);

@@ -201,6 +201,16 @@ __device__ __forceinline__ float gate_act(float x, int act) {
   return act == GDN_GATE_SILU ? x * s : s;
 }
 
+// dG = dh U act'(G) and dU = dh act(G).
+__device__ __forceinline__ void gate_grad(float dh, float G, float U, int act, float& dG,
+                                          float& dU) {
+  const float s = gate_sigmoid(G);
+  const bool silu = act == GDN_GATE_SILU;
+  const float slope = silu ? s * fmaf(G, 1.f - s, 1.f) : s * (1.f - s);
+  dG = dh * U * slope;
+  dU = dh * (silu ? G * s : s);
+}
+
 template <bool kFp8, int kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs g) {
@@ -548,11 +558,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               } else {
                 const uint32_t d2 = dh[(c + i) >> 1];
                 const float d = __uint_as_float((i & 1) ? d2 & 0xffff0000u : d2 << 16);
-                const float s = gate_sigmoid(x);
-                const bool silu = g.act == GDN_GATE_SILU;
-                v[i] = out == 0 ? d * __uint_as_float(U[i]) *
-                                      (silu ? s * fmaf(x, 1.f - s, 1.f) : s * (1.f - s))
-                                : d * (silu ? x * s : s);
+                float dG, dU;
+                gate_grad(d, x, __uint_as_float(U[i]), g.act, dG, dU);
+                v[i] = out == 0 ? dG : dU;
               }
             }
             stage_put<__nv_bfloat16>(bounce, lane, c, v);

@@ -27,7 +27,10 @@ struct SplitArgs {
   int32_t k_blocks;      // of 128 bytes
   int32_t tokens, n;     // n: rows of the weights (gated: features)
   int32_t act;
-  void* out;             // [tokens][n]
+  void* out;             // [tokens][ld]
+  void* out2;            // kGateGrad: dU beside dG in out
+  int64_t ld;
+  const __nv_bfloat16* dh;   // kGateGrad: [tokens][n]
   const float* sx;       // 8-bit: [tokens][k_blocks]
   const float* sw;       //        [ceil(n / 128)][k_blocks]
   unsigned* status;
@@ -48,10 +51,26 @@ struct SplitShape {
   static_assert(kNB * 128 * 4 <= kStages * kStage, "the partial products reuse the stages");
 };
 
-template <bool kFp8, bool kGated, int kNB, typename T>
+// Four columns of a row, those past `valid` left out; whole rows start on four.
+template <typename T>
+__device__ __forceinline__ void store4(T* out, const float (&v)[4], int valid, bool whole) {
+  if (whole && valid >= 4) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    else
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < valid) st_out(out + i, v[i]);
+  }
+}
+
+template <bool kFp8, int kEpi, int kNB, typename T>
 __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
     split_gemm_kernel(const __grid_constant__ SplitArgs g) {
   using S = SplitShape<kFp8, kNB>;
+  constexpr bool kGated = kEpi >= kGate;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
   float* scales = reinterpret_cast<float*>(sm + S::kStages * S::kStage);   // [K block][kNB]
@@ -256,20 +275,18 @@ __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
               u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
             }
           }
-        if (kGated)
+        const int64_t at = (int64_t)(t0 + c) * g.ld + f;
+        if constexpr (kEpi == kGate) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = gate_act(v[i], g.act) * u[i];
-        T* out = (T*)g.out + (size_t)(t0 + c) * g.n + f;
-        if (g.n % 4 == 0) {   // rows start on four elements
-          if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-          else
-            *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
+        } else if constexpr (kEpi == kGateGrad) {
+          const __nv_bfloat16* dh = g.dh + (int64_t)(t0 + c) * g.n + f;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (f + i < g.n) st_out(out + i, v[i]);
+            gate_grad(f + i < g.n ? __bfloat162float(dh[i]) : 0.f, v[i], u[i], g.act, v[i], u[i]);
+          store4((T*)g.out2 + at, u, g.n - f, g.ld % 4 == 0);
         }
+        store4((T*)g.out + at, v, g.n - f, g.ld % 4 == 0);
       }
     }
   }
@@ -304,10 +321,11 @@ inline SplitPlan plan_split(int64_t tokens, int64_t row_tiles, int k_blocks, int
   return {nb, s < 1 ? 1 : s > 8 ? 8 : (int)s};
 }
 
-template <bool kFp8, bool kGated, int kNB, typename T>
+template <bool kFp8, int kEpi, int kNB, typename T>
 cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st) {
   using S = SplitShape<kFp8, kNB>;
-  auto kern = split_gemm_kernel<kFp8, kGated, kNB, T>;
+  constexpr bool kGated = kEpi >= kGate;
+  auto kern = split_gemm_kernel<kFp8, kEpi, kNB, T>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
@@ -318,13 +336,13 @@ cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st)
   return e;
 }
 
-template <bool kFp8, bool kGated, typename T>
+template <bool kFp8, int kEpi, typename T>
 cudaError_t launch_split(const SplitArgs& g, const SplitPlan& plan, cudaStream_t st) {
   const unsigned split = (unsigned)plan.split;
   switch (plan.columns) {
-    case 16: return launch_split_nb<kFp8, kGated, 16, T>(g, split, st);
-    case 32: return launch_split_nb<kFp8, kGated, 32, T>(g, split, st);
-    default: return launch_split_nb<kFp8, kGated, 64, T>(g, split, st);
+    case 16: return launch_split_nb<kFp8, kEpi, 16, T>(g, split, st);
+    case 32: return launch_split_nb<kFp8, kEpi, 32, T>(g, split, st);
+    default: return launch_split_nb<kFp8, kEpi, 64, T>(g, split, st);
   }
 }
 

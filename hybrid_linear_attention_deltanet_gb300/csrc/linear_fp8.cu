@@ -45,6 +45,7 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
     a.tokens = (int32_t)tokens;
     a.n = n;
     a.out = out;
+    a.ld = n;
     a.sx = sx;
     a.sw = sw;
     a.status = status;
@@ -53,8 +54,8 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
       return GDN_ERR_CUDA;
     const cudaError_t e =
         out_dtype == GDN_BF16
-            ? gemm::launch_split<true, false, __nv_bfloat16>(a, plan, stream)
-            : gemm::launch_split<true, false, float>(a, plan, stream);
+            ? gemm::launch_split<true, gemm::kStore, __nv_bfloat16>(a, plan, stream)
+            : gemm::launch_split<true, gemm::kStore, float>(a, plan, stream);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
   }
   gemm::PairArgs g;
