@@ -67,7 +67,9 @@ inline int64_t tiles_of(const Problem& p) {
 
 struct PairArgs {
   Problem p[2];
-  int32_t problems, tiles;
+  int32_t problems;
+  int32_t tiles[2];     // of each problem
+  int32_t ahead;        // see tile_of
   int32_t group_m;      // tiles of rows whose columns are visited together (group_rows)
   int32_t act;
   const __nv_bfloat16* dh;   // kGateGrad: [M][ldh]
@@ -102,15 +104,30 @@ struct Tile {
   int part, k0, k1;      // part of K: its K blocks
 };
 
+// The k-th tile of pair i of `pairs`, or -1.  Problem 0, whose tiles are the
+// longer, is dealt out first; the pairs that got one tile less of it (from r
+// on) then take `ahead` rounds of problem 1 alone, about the time of the tile
+// they were spared, and the last rounds reach everyone, those pairs first.
+// (Dealing all tiles out in turn left 1111 tokens' gradients with pairs of 79
+// and of 36 K blocks; these come to 61 and 54.)
+__device__ __forceinline__ int tile_of(const PairArgs& g, int pairs, int i, int k) {
+  const int r = g.tiles[0] % pairs, n0 = g.tiles[0] / pairs + (i < r);
+  if (k < n0) return k * pairs + i;
+  k -= n0;
+  const int spared = pairs - r, first = g.ahead * spared;
+  const int u = i < r ? first + k * pairs + spared + i
+                      : k < g.ahead ? k * spared + i - r : first + (k - g.ahead) * pairs + i - r;
+  return u < g.tiles[1] ? g.tiles[0] + u : -1;
+}
+
 // Tile t: groups of group_m row tiles, all columns of a group before the next
 // group, so that the tiles in flight share their operands in L2.
 __device__ __forceinline__ Tile tile_at(const PairArgs& g, int t) {
   Tile r;
   r.p = 0;
-  const int first = g.p[0].m_tiles * g.p[0].n_tiles * g.p[0].k_parts;
-  if (t >= first) {
+  if (t >= g.tiles[0]) {
     r.p = 1;
-    t -= first;
+    t -= g.tiles[0];
   }
   const Problem& p = g.p[r.p];
   r.part = 0;
@@ -249,8 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   grid_release_next();
   grid_wait();
   const uint32_t tmem = tmem_base;
-  const int n_tiles = g.tiles;
-  const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   bool ok = true;
   float* scales = reinterpret_cast<float*>(sm + kStages * kStageBytes + kEpiWarps * kBounce);
 
@@ -264,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t full0 = mapa_smem(&full[0], 0);   // the even CTA's barriers
     int st = 0;
     uint32_t ph = 0;
-    for (int t = t0; t < n_tiles && ok; t += step) {
+    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.p];
       const int m0 = tl.m0 + 128 * (int)rank;
@@ -310,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t sm0 = smem_u32(sm);
     int st = 0, buf = 0;
     uint32_t ph = 0, aph = 0;
-    for (int t = t0; t < n_tiles && ok; t += step) {
+    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.p];
       const uint32_t idesc =
@@ -359,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // blocks at a time; a group is in registers while its slot is in use.
     int slot = 0;
     uint32_t ph = 0;
-    for (int t = t0; t < n_tiles && ok; t += step) {
+    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.p];
       const int r0 = 64 * (warp - 2) + lane, nb = tl.n0 / 128;
@@ -415,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       buf ^= 1;
       if (buf == 0) aph ^= 1u;
     };
-    for (int t = t0; t < n_tiles && ok; t += step) {
+    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
       const Tile tl = tile_at(g, t);
       const Problem& p = g.p[tl.p];
       const int row0 = tl.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
@@ -667,12 +683,15 @@ cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   int64_t tiles = 0;
+  int32_t length[2] = {0, 1};   // K blocks of a tile, and about what its end costs
   for (int i = 0; i < g.problems; ++i) {
     if (!output_maps(g.p[i], kEpi == kStoreF32)) return cudaErrorUnknown;
     tiles += tiles_of(g.p[i]);
+    if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    g.tiles[i] = (int32_t)tiles_of(g.p[i]);
+    length[i] = g.p[i].k_blocks / g.p[i].k_parts + 5;
   }
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  g.tiles = (int32_t)tiles;
+  g.ahead = length[0] / length[1];
   const int64_t pairs = sms / 2;
   e = launch_dependent(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads,
                        kSmem, 0, st, g);
