@@ -18,6 +18,8 @@
 // (rows over dG^T then dU^T), the longer K first, so that the short tiles
 // fill the end of the grid.  Where a product's tiles are few and their K is
 // long, K is cut into parts, whose fp32 sums a third launch adds in order.
+#include <utility>
+
 #include "gemm_split.cuh"
 #include "hostcheck.cuh"
 
@@ -32,33 +34,58 @@ size_t grad_bytes(int64_t tokens, int32_t hidden) {
   return align_up((size_t)tokens * grad_pitch(hidden) * 2, 256);
 }
 
-// Parts of K of the second launch's two products: enough that no tile is
-// longer than the pairs' average load, where that shortens the launch by more
-// than the sums cost (16 K blocks, 5 us).  The pair count is that of the
-// device; a constant, so that a workspace's size needs no device.
+// Parts of K of the second launch's two products: those with the shortest
+// estimate of that launch and the sums' together.  The pair count is that of
+// the device; a constant, so that a workspace's size needs no device.
 constexpr int kPairs = 76;
 struct Parts {
-  int dx, dw;              // parts of K
-  int64_t dx_rows, dw_rows;   // rows of a part
+  int dx, dw;                     // parts of K
+  int64_t dx_rows, dw_rows;       // rows of a part
   size_t dx_off, dw_off, bytes;   // of the fp32 parts in the scratch, after dG and dU
 };
-int parts_of(int64_t tiles, int64_t blocks, int64_t total) {
-  const int64_t mean = (total + kPairs - 1) / kPairs;
-  if (mean < 1 || tiles * 2 > kPairs || blocks < mean + 16) return 1;
-  int64_t n = (blocks + mean - 1) / mean;
-  if (n > 8) n = 8;
-  return (int)n;
+struct Work {
+  int64_t tiles, blocks;   // of one product: tiles, and K blocks of a tile (with its end, as 5)
+};
+// K blocks of the longest pair, as gemm_pair.cuh deals the tiles out.
+int64_t longest(Work a, Work b) {
+  if (a.blocks < b.blocks) std::swap(a, b);
+  const int64_t sum = a.tiles + b.tiles, pairs = sum < kPairs ? sum : kPairs;
+  const int64_t r = a.tiles % pairs, n = a.tiles / pairs, spared = pairs - r;
+  const int64_t ahead = a.blocks / b.blocks, rest = b.tiles - ahead * spared;
+  int64_t few = (b.tiles + spared - 1) / spared, many = 0;   // short tiles of either kind of pair
+  if (rest > 0) {
+    few = ahead + rest / pairs + (rest % pairs > 0);
+    many = rest / pairs + (rest % pairs > spared);
+  }
+  const int64_t x = n * a.blocks + few * b.blocks, y = (n + 1) * a.blocks + many * b.blocks;
+  return r && y > x ? y : x;
 }
 Parts plan_parts(int64_t tokens, int32_t dim, int32_t hidden) {
   const int64_t dt = ((int64_t)dim + 255) / 256, tx = (tokens + 255) / 256 * dt;
   const int64_t tw = 2 * (((int64_t)hidden + 255) / 256) * dt;
   const int64_t kx = 2 * (((int64_t)hidden + 63) / 64), kw = (tokens + 63) / 64;
-  const int64_t total = tx * kx + tw * kw;
   Parts p;
-  p.dx = parts_of(tx, kx, total);
-  p.dw = parts_of(tw, kw, total);
+  p.dx = p.dw = 1;
   p.dx_rows = (tokens + 255) / 256 * 256;
   p.dw_rows = ((int64_t)hidden + 255) / 256 * 256;
+  // a part costs its fp32 tiles' way out and back (256 KB each: 0.1 us, a
+  // third of a K block) and the sums one launch (4.5 us, the host's share included)
+  static constexpr int kTry[] = {1, 2, 3, 4, 6, 8};
+  int64_t best = INT64_MAX;
+  for (int a : kTry)
+    for (int b : kTry) {
+      if ((a > 1 && (kx < 4 * a || tx * a > 4 * kPairs)) ||
+          (b > 1 && (kw < 4 * b || tw * b > 4 * kPairs)))
+        continue;
+      const int64_t sums = (a > 1 ? tx * a : 0) + (b > 1 ? tw * b : 0);
+      const int64_t cost = 3 * longest({tx * a, kx / a + 5}, {tw * b, kw / b + 5}) +
+                           (sums ? 45 + sums : 0);
+      if (cost < best) {
+        best = cost;
+        p.dx = a;
+        p.dw = b;
+      }
+    }
   p.dx_off = 2 * grad_bytes(tokens, hidden);
   p.dw_off = p.dx_off + (p.dx > 1 ? align_up((size_t)p.dx * p.dx_rows * dim * 4, 256) : 0);
   p.bytes = p.dw_off + (p.dw > 1 ? align_up(2 * (size_t)p.dw * p.dw_rows * dim * 4, 256) : 0);
@@ -222,7 +249,7 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
   g.group_m = 8;   // either operand is read once for the tiles in flight, which are about square
   const int32_t kx = (hidden + 63) / 64, kw = (int32_t)((tokens + 63) / 64);
   const Parts parts = plan_parts(tokens, dim, hidden);
-  const int ix = 2 * kx / parts.dx >= kw / parts.dw ? 0 : 1;
+  const int ix = 2 * kx / parts.dx >= kw / parts.dw ? 0 : 1;   // the longer tiles first
   float* dx_parts = (float*)((char*)scratch + parts.dx_off);
   float* dw_parts = (float*)((char*)scratch + parts.dw_off);
   gemm::Problem& px = g.p[ix];
