@@ -307,7 +307,7 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
     a.parts[i] = parts.dw;
   }
   const int64_t blocks = (a.vecs[0] + a.vecs[1] + a.vecs[2] + 255) / 256, most = 8 * (int64_t)sms;
-  e = launch_dependent(sum_parts_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 0,
+  e = launch(true, sum_parts_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, 0,
                        stream, a);
   count_launches(1);
   return e;

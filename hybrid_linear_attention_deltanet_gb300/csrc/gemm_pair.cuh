@@ -693,7 +693,7 @@ cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
   }
   g.ahead = length[0] / length[1];
   const int64_t pairs = sms / 2;
-  e = launch_dependent(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads,
+  e = launch(true, kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads,
                        kSmem, 0, st, g);
   count_launches(1);
   return e;

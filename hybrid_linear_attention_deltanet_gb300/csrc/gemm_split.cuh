@@ -331,7 +331,7 @@ cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st)
   if (e != cudaSuccess) return e;
   const unsigned ny = (unsigned)((g.n + (kGated ? 63 : 127)) / (kGated ? 64 : 128));
   const unsigned nz = (unsigned)((g.tokens + kNB - 1) / kNB);
-  e = launch_dependent(kern, dim3(split, ny, nz), S::kThreads, S::kSmem, split, st, g);
+  e = launch(true, kern, dim3(split, ny, nz), S::kThreads, S::kSmem, split, st, g);
   count_launches(1);
   return e;
 }

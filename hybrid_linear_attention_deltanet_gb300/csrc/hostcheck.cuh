@@ -57,24 +57,30 @@ __device__ __forceinline__ void grid_release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// cluster: CTAs of a cluster along x, 0 where the kernel itself says so.
+// dependent: as a programmatic dependent.  cluster: CTAs of a cluster along x,
+// 0 where the kernel itself says so.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem,
-                             unsigned cluster, cudaStream_t st, const A&... args) {
+cudaError_t launch(bool dependent, void (*kern)(P...), dim3 grid, unsigned threads, size_t smem,
+                   unsigned cluster, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
+  unsigned n = 0;
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = cluster ? 2 : 1;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

@@ -16,6 +16,7 @@
 
 #include "gdn_internal.cuh"
 #include "hostcheck.cuh"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -26,6 +27,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDim = 8 * 8 * 256;   // 8 warps x 8 vectors x 256 columns
 constexpr int kFewRows = 304;            // two CTAs an SM of one row each
+constexpr int kClusterCtas = 8;
 constexpr float kTiny = 0x1p-100f;     // the smallest block maximum: its scale stays normal
 constexpr float kE4m3Max = 448.f;
 
@@ -290,16 +292,18 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
 
 struct NormBwdArgs {
   const void* dy; const void* s; const float* w; const void* ds; float eps;
-  void* dx; float* part;   // part: [gridDim.x][dim]
+  void* dx; float* part;   // part: [gridDim.x][dim], or dw
   int64_t rows; int32_t dim;
 };
 
 // dx, and each CTA's part of dw over the rows it visits: the rows are dealt
-// to a fixed grid, so the sums have a fixed order.  Rows in flight are what
+// to a fixed grid, so the sums have a fixed order.  kCluster: the grid is one
+// cluster, whose CTAs add their parts through each other's shared memory, in
+// order, into dw (few rows: one launch and no scratch).  Rows in flight are what
 // it lives from: two vectors a lane leave registers for four CTAs an SM
 // (8191 rows of 4096 bf16: 49.8 us; 54.5 us with four vectors and two CTAs,
 // 60.8 us with two CTAs that fetch a row ahead).
-template <typename T, int kVPL, int kWPR>
+template <typename T, int kVPL, int kWPR, bool kCluster>
 __global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
     norm_backward_kernel(NormBwdArgs a) {
   grid_release_next();
@@ -388,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
       __syncthreads();
     }
   }
+  extern __shared__ __align__(16) float mine[];   // kCluster: [dim]
   if (warp / kWPR == kGroups - 1) {
 #pragma unroll
     for (int j = 0; j < kVPL; ++j) {
@@ -395,9 +400,25 @@ __global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
       if (c < a.dim) {
         Raw<float> o;
         o.round(dw[j]);
-        o.store(a.part + (size_t)blockIdx.x * a.dim + c);
+        o.store(kCluster ? mine + c : a.part + (size_t)blockIdx.x * a.dim + c);
       }
     }
+  }
+  if constexpr (kCluster) {
+    sm100::cluster_sync_all();
+    uint32_t base[kCluster ? kClusterCtas : 1];
+#pragma unroll
+    for (int r = 0; r < kClusterCtas; ++r) base[r] = sm100::mapa_smem(mine, r);
+    for (int v = blockIdx.x * kThreads + threadIdx.x; v < a.dim / 4; v += kClusterCtas * kThreads) {
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < kClusterCtas; ++r) {
+        const float4 x = sm100::ld_shared_cluster4(base[r] + 16 * v);
+        t.x += x.x; t.y += x.y; t.z += x.z; t.w += x.w;
+      }
+      reinterpret_cast<float4*>(a.part)[v] = t;
+    }
+    sm100::cluster_sync_all();   // read before any CTA leaves
   }
 }
 
@@ -607,18 +628,23 @@ int norm_common(const void* x, const void* residual, const float* w, float eps, 
   return launch_norm(a, io_dtype, fp8, stream);
 }
 
-// dw parts of the backward, a row of `dim` a CTA.
-int backward_grid(int64_t tokens, int32_t dim) {
+// How the backward's rows are dealt: to one cluster while each warp group of
+// it gets at most four (1024 columns, us a call, one launch / two: 32 rows 6.2
+// / 10.3, 64 rows 8.2 / 10.8, 128 rows 10.2 / 11.2), else to `grid` CTAs whose
+// parts of dw (a row of `dim` each, in scratch) a second launch adds.
+struct BackwardPlan {
+  bool cluster;
+  int grid;
+  size_t bytes;   // of the parts
+};
+BackwardPlan plan_backward(int64_t tokens, int32_t dim) {
   int groups = 1;
   with_layout<false>(dim, tokens, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
+  if (tokens <= 4 * kClusterCtas * groups && dim <= 8192) return {true, kClusterCtas, 0};
   const int64_t want = (tokens + 2 * groups - 1) / (2 * groups);   // two rows a warp group
   const int64_t cap = 608;   // four an SM: a constant, so that the sums' order is one
-  return (int)(want < cap ? want : cap);
-}
-// Scratch for them: none where one CTA's part is all of dw.
-size_t parts_bytes(int64_t tokens, int32_t dim) {
-  const int grid = backward_grid(tokens, dim);
-  return grid > 1 ? (size_t)grid * dim * 4 : 0;
+  const int grid = (int)(want < cap ? want : cap);
+  return {false, grid, (size_t)grid * dim * 4};
 }
 bool backward_shape_ok(int64_t tokens, int32_t dim, int32_t io) {
   return tokens >= 0 && dim >= 1 && io_ok(io) && dim % 8 == 0 && dim <= kMaxDim;
@@ -634,8 +660,8 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   for (const void* p : v16)
     if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
   const size_t bytes = (size_t)tokens * dim * es_of(io_dtype);
-  const int grid = backward_grid(tokens, dim);
-  const size_t need = parts_bytes(tokens, dim);
+  const BackwardPlan plan = plan_backward(tokens, dim);
+  const size_t need = plan.bytes;
   if (use_ws && need) {
     if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
@@ -647,22 +673,32 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
   if (tokens == 0)
     return cudaMemsetAsync(dw, 0, (size_t)dim * 4, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-  void* part = grid == 1 ? dw : ws;
-  const bool own = grid > 1 && !use_ws;
+  void* part = plan.cluster ? dw : ws;
+  const bool own = need && !use_ws;
   if (own && scratch_alloc(&part, need, stream) != cudaSuccess) return GDN_ERR_CUDA;
-  NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
+  const NormBwdArgs a{dy, s, w, ds, eps, dx, (float*)part, tokens, dim};
+  cudaError_t e = cudaSuccess;
   with_layout<false>(dim, tokens, [&](auto lay) {
     constexpr int V = decltype(lay)::V, W = decltype(lay)::W;
-    auto kern = io_dtype == GDN_BF16 ? norm_backward_kernel<__nv_bfloat16, V, W>
-                                     : norm_backward_kernel<float, V, W>;
-    kern<<<grid, kThreads, 0, stream>>>(a);
+    if constexpr (V <= 4) {
+      if (plan.cluster) {
+        auto kern = io_dtype == GDN_BF16 ? norm_backward_kernel<__nv_bfloat16, V, W, true>
+                                         : norm_backward_kernel<float, V, W, true>;
+        e = launch(false, kern, dim3(plan.grid), kThreads, (size_t)dim * 4, kClusterCtas, stream,
+                   a);
+        return;
+      }
+    }
+    auto kern = io_dtype == GDN_BF16 ? norm_backward_kernel<__nv_bfloat16, V, W, false>
+                                     : norm_backward_kernel<float, V, W, false>;
+    kern<<<plan.grid, kThreads, 0, stream>>>(a);
+    e = cudaGetLastError();
   });
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && grid > 1) {
-    norm_dw_kernel<<<(dim + 31) / 32, 1024, 0, stream>>>((const float*)part, grid, dim, dw);
+  if (e == cudaSuccess && !plan.cluster) {
+    norm_dw_kernel<<<(dim + 31) / 32, 1024, 0, stream>>>((const float*)part, plan.grid, dim, dw);
     e = cudaGetLastError();
   }
-  count_launches(grid > 1 ? 2 : 1);
+  count_launches(plan.cluster ? 1 : 2);
   if (own && scratch_free(part, stream) != cudaSuccess) return GDN_ERR_CUDA;
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -690,7 +726,7 @@ int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, f
 
 size_t gdn_residual_norm_backward_workspace_size(int64_t tokens, int32_t dim, int32_t io_dtype) {
   if (!backward_shape_ok(tokens, dim, io_dtype)) return SIZE_MAX;
-  return parts_bytes(tokens, dim);
+  return plan_backward(tokens, dim).bytes;
 }
 
 int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,

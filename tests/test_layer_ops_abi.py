@@ -66,16 +66,16 @@ def test_residual_norm_backward_refuses(lib):  # noqa: F811
     assert f(dy=MIS) == 3 and f(dw=P(0x7000008)) == 3
     assert f(dx=X) == 1 and f(dw=W) == 1 and f(dx=P(0x2000000 + 16)) == 1
     size = lib.gdn_residual_norm_backward_workspace_size
-    assert size(17, 256, BF16) == 2 * 256 * 4 and size(16, 256, BF16) == 0
+    assert size(300, 256, BF16) == 19 * 256 * 4 and size(256, 256, BF16) == 0
     assert size(0, 256, BF16) == 0
     assert size(1 << 20, 4096, BF16) == 608 * 4096 * 4
     assert size(16, 12, BF16) == SIZE_MAX and size(-1, 256, BF16) == SIZE_MAX
     ws = P(0x9000000)
 
-    def g(ws=ws, n=2 * 256 * 4):
-        return lib.gdn_residual_norm_backward_ws(X, R, W, None, 1e-5, Y, dw, 17, 256, BF16, ws, n,
+    def g(ws=ws, n=19 * 256 * 4):
+        return lib.gdn_residual_norm_backward_ws(X, R, W, None, 1e-5, Y, dw, 300, 256, BF16, ws, n,
                                                  None)
-    assert g(ws=None) == 1 and g(n=2047) == 1 and g(ws=P(0x9000010)) == 3 and g(ws=X) == 1
+    assert g(ws=None) == 1 and g(n=19 * 256 * 4 - 1) == 1 and g(ws=P(0x9000010)) == 3 and g(ws=X) == 1
 
 
 @fake_addresses
