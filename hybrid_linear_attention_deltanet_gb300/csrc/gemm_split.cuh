@@ -100,6 +100,14 @@ __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
     prefetch_tensormap(&g.w[0]);
     prefetch_tensormap(&g.x);
     if (kGated) prefetch_tensormap(&g.w[1]);
+    // the weights' way from HBM to L2 need not wait for the grid before (L2
+    // holds what memory holds, also where that grid still writes): a layer of
+    // one token's six launches 27.6 -> 25.8 us
+    for (int i = 0; i < kbs && i < S::kStages; ++i) {
+      const int k = (kb0 + i) * (kFp8 ? 128 : 64);
+      prefetch_l2_2d(&g.w[0], k, f0);
+      if (kGated) prefetch_l2_2d(&g.w[1], k, f0);
+    }
   }
   tc_fence_before();
   __syncthreads();
