@@ -14,11 +14,22 @@
 // epilogue runs while the next tile is multiplied.  Results go through shared
 // memory, 32 rows x 128 bytes a warp, and leave as TMA stores.
 //
-// bf16 operands (8 epilogue warps, 128 accumulator columns each) accumulate a
-// whole tile in tensor memory.  8-bit operands (16 warps, 64 columns each)
-// carry one scale for every 128 elements of K, so there each K block is an
-// accumulator of its own, which the epilogue warps scale and add into 64 fp32
-// registers a thread while the next block is multiplied.
+// bf16 operands accumulate a whole tile in tensor memory.  8-bit operands carry
+// one scale for every 128 elements of K, so there each K block is an
+// accumulator of its own, which the 8 epilogue warps scale and add into 128
+// fp32 registers a thread while the next block is multiplied.
+//
+// What it measured (GB300).  bf16: 8192 x 2048 against 2 x 6144 rows keeps the
+// tensor pipe 90 % busy (206 us cold); 32768 rows run 890 us at 1.85 PFLOP/s,
+// and over seconds 955 us at the 1400 W limit with the SMs at 1.5 GHz, the rate
+// of a plain library product there.  8 bits: 32768 x 2048 against 4608 rows
+// 243 us, 2.5 PFLOP/s, tensor pipe 47 % busy (1040 cycles a K block; 261 us
+// over seconds, also at the power limit).  A block costs its 512 tensor cycles
+// plus what the epilogue's chain (wait, four loads of 32 columns, 64 packed
+// multiply-adds, release) is not hidden by the other accumulator.  Not kept,
+// same product: 16 epilogue warps of 64 columns 262 us, two 128-column halves
+// with four accumulators 250 us, 16-column loads one block ahead 300 us;
+// without the multiply-adds it would take 207 us, without the loads 247 us.
 //
 // Every wait has a limit: a wait that runs out flags GDN_ERR_TIMEOUT, and the
 // CTA leaves after its copies and products in flight have had time to end.
@@ -692,6 +703,7 @@ cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
     length[i] = g.p[i].k_blocks / g.p[i].k_parts + 5;
   }
   g.ahead = length[0] / length[1];
+  if (g.ahead > 1 << 20) g.ahead = 1 << 20;
   const int64_t pairs = sms / 2;
   e = launch(true, kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads,
                        kSmem, 0, st, g);

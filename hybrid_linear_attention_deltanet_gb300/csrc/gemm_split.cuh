@@ -13,8 +13,13 @@
 // one multiplies.  8-bit operands: every K block of 128 is an accumulator of
 // its own, scaled (a token's scale times the weight block's) into fp32
 // registers; with 32 columns or more that takes 8 warps, half the columns
-// each (256 tokens, 2048 -> 4608: 10.3 us with 4).
+// each (256 tokens, 2048 -> 4608: 8.5 us, 10.3 with 4).
 // Waits are bounded as in gemm_pair.cuh.
+//
+// Bound by HBM, then by the launch's own chain.  One token against 2 x 6144 x
+// 2048 bf16 (50 MB): 10.1 us a call among others, 5.0 TB/s; against 4608 x 2048
+// e4m3 (9.4 MB): 4.4 us, of which an empty launch of this shape takes 1.6 and
+// its tensor memory 0.6.
 #pragma once
 
 #include "gemm_pair.cuh"
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
 // run (each keeping `least` K blocks).  More tokens take tiles of 64 columns
 // while those are within one CTA an SM: fewer, longer chains of K blocks in
 // the pair form would leave most SMs idle.  (us, split / pair.  8 bits, 2048
-// -> 4608: 16 tokens 4.5 / 13, 64 tokens 5.9 / 13, 256 tokens 9.9 / 11.1;
+// -> 4608: 16 tokens 4.1 / 9.9, 64 tokens 5.1 / 9.9, 256 tokens 8.5 / 10;
 // 4096 -> 1000: 300 tokens 9.7 / 16.2; 4096 -> 512: 400 tokens 6.7 / 15.8;
 // 2048 -> 2048: 512 tokens, 128 CTAs, 9.8 / 9.9; 1024 -> 4608: 300 tokens, 180
 // CTAs, 12.5 / 7.0.  Gated, 2048 -> 6144: 64 tokens 12.7 / 14.0, 128 tokens,
