@@ -153,10 +153,9 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
   return true;
 }
 
-// The same for few tokens (gemm_split.cuh); two CTAs an SM keep the weights
-// coming.
+// The same for few tokens (gemm_split.cuh).
 gemm::SplitPlan plan_projections(int64_t tokens, int32_t dim, int32_t hidden, int sms) {
-  return gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64, (dim + 63) / 64, sms, 2 * sms, 8);
+  return gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64, (dim + 63) / 64, sms);
 }
 bool split_projections(gemm::SplitArgs& a, const gemm::SplitPlan& plan, const void* x,
                        const void* wg, const void* wu, int32_t act, int64_t tokens, int32_t dim,

@@ -6,8 +6,8 @@
 // weights (gated: 64 of Wg and 64 of Wu, the same features) by kNB tokens
 // over its share of K, and the CTAs of a cluster, one share each, add their
 // fp32 partial products through each other's shared memory, in a fixed order.
-// One launch, whose CTAs (two an SM) hold all of the weights' bytes in
-// flight that their stages allow.
+// One launch, whose CTAs hold all of the weights' bytes in flight that their
+// stages allow.
 //
 // Roles: the first 4 or 8 warps take accumulators out, then one fetches and
 // one multiplies.  8-bit operands: every K block of 128 is an accumulator of
@@ -41,7 +41,8 @@ struct SplitArgs {
   unsigned* status;
 };
 
-constexpr int kSplitScaleBytes = 16384;   // of a CTA's staged scales
+constexpr uint32_t kSplitAlone = 120 * 1024;   // shared memory that keeps a CTA alone on its SM
+constexpr int kSplitScaleBytes = 65536;   // most of a CTA's staged scales
 
 template <bool kFp8, int kNB>
 struct SplitShape {
@@ -52,7 +53,7 @@ struct SplitShape {
   static constexpr int kStages = kNB <= 16 ? 5 : 4;
   static constexpr int kAcc = kFp8 ? 4 : 1;   // accumulators in tensor memory
   static constexpr uint32_t kTmem = kAcc * kNB < 32 ? 32 : kAcc * kNB;
-  static constexpr uint32_t kSmem = kStages * kStage + (kFp8 ? kSplitScaleBytes : 0) + 1024;
+  static constexpr uint32_t kSmem = kStages * kStage + 1024;   // and the scales, a call's own
   static_assert(kNB * 128 * 4 <= kStages * kStage, "the partial products reuse the stages");
 };
 
@@ -308,43 +309,52 @@ __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
   if (warp == S::kEpi + 1) tmem_dealloc(tmem, S::kTmem);
 }
 
-// How a call takes the split form: columns a CTA and CTAs a cluster, or
-// columns 0 for the pair form.
+// How a call takes the split form: columns a CTA, CTAs a cluster and whether
+// each gets an SM to itself; columns 0: the pair form.
 //
-// Up to 64 tokens are one tile of columns, and K is split until `ctas` CTAs
-// run (each keeping `least` K blocks).  More tokens take tiles of 64 columns
-// while those are within one CTA an SM: fewer, longer chains of K blocks in
-// the pair form would leave most SMs idle.  (us, split / pair.  8 bits, 2048
-// -> 4608: 16 tokens 4.1 / 9.9, 64 tokens 5.1 / 9.9, 256 tokens 8.5 / 10;
-// 4096 -> 1000: 300 tokens 9.7 / 16.2; 4096 -> 512: 400 tokens 6.7 / 15.8;
-// 2048 -> 2048: 512 tokens, 128 CTAs, 9.8 / 9.9; 1024 -> 4608: 300 tokens, 180
-// CTAs, 12.5 / 7.0.  Gated, 2048 -> 6144: 64 tokens 12.7 / 14.0, 128 tokens,
-// 192 CTAs, 15.6 / 14.3; 1000 -> 1000: 200 tokens 6.9 / 10.1.)
+// Up to 64 tokens are one tile of columns; more take tiles of 64 while those
+// are within one CTA an SM (the pair form's fewer, longer chains of K blocks
+// would leave most SMs idle).  K is split (at least four blocks each) while
+// the CTAs are within one an SM, and each is then kept alone there: else the
+// scheduler puts two on some SMs and none on others.  Tiles that leave no room
+// for a split so take two CTAs an SM if K is long.  (us.  8 bits, pair / split:
+// 2048 -> 4608, 16 tokens 9.0 / 4.0, 128 tokens 9.9 / 6.4, 256 tokens 9.9 / 8.2;
+// 4096 -> 1000, 300 tokens, 16.0 / 6.8, with two CTAs an SM 7.5; 4096 -> 2048, 512
+// tokens, 15.7 / 11.1, alone and not split 13.1, not alone 17.7; 1024 -> 4608,
+// 300 tokens, 180 CTAs, 7.0 / 7.9.  Gated: 2048 -> 6144, 64 tokens 14.2 / 11.2, 128
+// tokens, 192 CTAs, 14.4 / 15.7; 1000 -> 1000, 200 tokens, 10.1 / 6.6.  Clusters of
+// eight CTAs alone on their SMs do not find room side by side: 6.1 against 3.6.)
 struct SplitPlan {
   int columns, split;
+  bool alone;
 };
-inline SplitPlan plan_split(int64_t tokens, int64_t row_tiles, int k_blocks, int sms, int ctas,
-                            int least) {
+inline SplitPlan plan_split(int64_t tokens, int64_t row_tiles, int k_blocks, int sms) {
   const int nb = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
   const int64_t units = row_tiles * ((tokens + nb - 1) / nb);
-  if (row_tiles > 65535 || (tokens > 64 && units > sms)) return {0, 0};
-  if (tokens > 64) ctas = sms + sms / 16;
-  int64_t s = ctas / units;
-  if (s > k_blocks / least) s = k_blocks / least;
-  return {nb, s < 1 ? 1 : s > 8 ? 8 : (int)s};
+  if (row_tiles > 65535 || (tokens > 64 && units > sms)) return {0, 0, false};
+  const auto split = [&](int64_t ctas) {
+    int64_t s = ctas / units;
+    if (s > k_blocks / 4) s = k_blocks / 4;
+    return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+  };
+  int s = split(sms);
+  if (s == 1 && k_blocks >= 16) s = split(2 * (int64_t)sms);
+  return {nb, s, units * s <= sms && s < 8};
 }
 
 template <bool kFp8, int kEpi, int kNB, typename T>
-cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, cudaStream_t st) {
+cudaError_t launch_split_nb(const SplitArgs& g, unsigned split, bool alone, cudaStream_t st) {
   using S = SplitShape<kFp8, kNB>;
   constexpr bool kGated = kEpi >= kGate;
   auto kern = split_gemm_kernel<kFp8, kEpi, kNB, T>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  uint32_t smem = S::kSmem + (kFp8 ? (uint32_t)((g.k_blocks + split - 1) / split) * kNB * 4 : 0);
+  if (alone && smem < kSplitAlone) smem = kSplitAlone;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(S::kSmem + kSplitScaleBytes));
   if (e != cudaSuccess) return e;
   const unsigned ny = (unsigned)((g.n + (kGated ? 63 : 127)) / (kGated ? 64 : 128));
   const unsigned nz = (unsigned)((g.tokens + kNB - 1) / kNB);
-  e = launch(true, kern, dim3(split, ny, nz), S::kThreads, S::kSmem, split, st, g);
+  e = launch(true, kern, dim3(split, ny, nz), S::kThreads, smem, split, st, g);
   count_launches(1);
   return e;
 }
@@ -353,9 +363,9 @@ template <bool kFp8, int kEpi, typename T>
 cudaError_t launch_split(const SplitArgs& g, const SplitPlan& plan, cudaStream_t st) {
   const unsigned split = (unsigned)plan.split;
   switch (plan.columns) {
-    case 16: return launch_split_nb<kFp8, kEpi, 16, T>(g, split, st);
-    case 32: return launch_split_nb<kFp8, kEpi, 32, T>(g, split, st);
-    default: return launch_split_nb<kFp8, kEpi, 64, T>(g, split, st);
+    case 16: return launch_split_nb<kFp8, kEpi, 16, T>(g, split, plan.alone, st);
+    case 32: return launch_split_nb<kFp8, kEpi, 32, T>(g, split, plan.alone, st);
+    default: return launch_split_nb<kFp8, kEpi, 64, T>(g, split, plan.alone, st);
   }
 }
 

@@ -36,7 +36,7 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   unsigned* status = status_ptr();
   if (sms < 2 || !status) return GDN_ERR_CUDA;
   const gemm::SplitPlan plan =
-      gemm::plan_split(tokens, ((int64_t)n + 127) / 128, blocks, sms, sms, 4);
+      gemm::plan_split(tokens, ((int64_t)n + 127) / 128, blocks, sms);
   if (plan.columns && (int64_t)((blocks + plan.split - 1) / plan.split) * plan.columns * 4 <=
                           gemm::kSplitScaleBytes) {
     gemm::SplitArgs a;
