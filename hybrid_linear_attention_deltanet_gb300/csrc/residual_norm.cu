@@ -641,13 +641,19 @@ struct BackwardPlan {
   int grid;
   size_t bytes;   // of the parts
 };
-BackwardPlan plan_backward(int64_t tokens, int32_t dim) {
-  int groups = 1;
-  with_layout<false>(dim, tokens, [&](auto lay) { groups = kWarps / decltype(lay)::W; });
+BackwardPlan plan_backward(int64_t tokens, int32_t dim, int32_t io) {
+  int groups = 1, ctas = 1;
+  with_layout<false>(dim, tokens, [&](auto lay) {
+    groups = kWarps / decltype(lay)::W;
+    ctas = backward_ctas(decltype(lay)::V, es_of(io));
+  });
   if (tokens <= 4 * kClusterCtas * groups && dim <= 8192) return {true, kClusterCtas, 0};
-  const int64_t want = (tokens + 2 * groups - 1) / (2 * groups);   // two rows a warp group
-  const int64_t cap = 608;   // four an SM: a constant, so that the sums' order is one
-  const int grid = (int)(want < cap ? want : cap);
+  // one wave of CTAs, of two rows a warp group at least; 152 is the device's
+  // SMs, a constant, so that the sums' order is one
+  const int64_t rounds = (tokens + groups - 1) / groups, most = 152 * ctas;
+  int64_t each = (rounds + most - 1) / most;
+  if (each < 2) each = 2;
+  const int grid = (int)((rounds + each - 1) / each);
   return {false, grid, (size_t)grid * dim * 4};
 }
 bool backward_shape_ok(int64_t tokens, int32_t dim, int32_t io) {
@@ -664,7 +670,7 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
   for (const void* p : v16)
     if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
   const size_t bytes = (size_t)tokens * dim * es_of(io_dtype);
-  const BackwardPlan plan = plan_backward(tokens, dim);
+  const BackwardPlan plan = plan_backward(tokens, dim, io_dtype);
   const size_t need = plan.bytes;
   if (use_ws && need) {
     if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
@@ -730,7 +736,7 @@ int gdn_residual_norm_fp8(const void* x, const void* residual, const float* w, f
 
 size_t gdn_residual_norm_backward_workspace_size(int64_t tokens, int32_t dim, int32_t io_dtype) {
   if (!backward_shape_ok(tokens, dim, io_dtype)) return SIZE_MAX;
-  return plan_backward(tokens, dim).bytes;
+  return plan_backward(tokens, dim, io_dtype).bytes;
 }
 
 int gdn_residual_norm_backward(const void* dy, const void* s, const float* w, const void* ds,
