@@ -136,7 +136,7 @@ __device__ __forceinline__ bool near_tie(float v) {
 // nearly cancel, so the sign of the difference is right.
 __device__ __forceinline__ float settle_tie(float v, float ph, float pl, float mh, float ml) {
   const uint32_t bits = __float_as_uint(v);
-  const uint32_t tie = ((bits + 0x80000u) & ~0xfffffu) - 0x80000u;   // with v's sign
+  const uint32_t tie = (bits & ~0xfffffu) | 0x80000u;   // with v's sign
   const float t = fabsf(__uint_as_float(tie));
   const float a = __fmul_rn(kE4m3Max, ph), b = __fmul_rn(t, mh);
   const float ae = __fmaf_rn(kE4m3Max, ph, -a), be = __fmaf_rn(t, mh, -b);

@@ -229,6 +229,44 @@ def test_quantize_fp8(io, rows, cols):
             within(got, t, (2.0 ** -4 + 2.0 ** -22) * t.abs() + 2.0 ** -10 * m / 448 * (1 + 2.0 ** -22))
 
 
+def e4m3_of(v):
+    """e4m3 value nearest to v (64 bits, |v| <= 448), ties to even; and where it is normal."""
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -6))) - 3)
+    return torch.round(v / step) * step, v.abs() >= 2.0 ** -6
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantised_codes_are_the_real_numbers(io, block_rows):
+    """Every code is the rounding of 448 x / m itself, values that fp32 leaves
+    on or beside the middle between two codes included (among bf16 values the
+    exact middle is common).  64 bits hold 448 x exactly and the quotient to
+    2^-53, exactly where it is such a middle."""
+    g = gen(81)
+    x = randn(g, 1024, 1024, dtype=io)
+    x[:, ::7] = torch.randint(-56, 57, (1024, x[:, ::7].shape[1]), generator=g, device=DEV).to(io)
+    q, scale = gdn.quantize_fp8(x, block_rows=block_rows)
+    b = x.double().view(1024 // block_rows, block_rows, 8, 128)
+    m = b.abs().amax((1, 3), keepdim=True)
+    want, normal = e4m3_of((448 * b / m).view(1024, 1024))
+    assert torch.equal(q.double()[normal], want[normal])
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_norm_codes_are_the_real_numbers(io):
+    """The same for the norm, whose root cancels in y / max |y|: s and w with few
+    bits put many values on the middle between two codes."""
+    g = gen(82)
+    x = torch.randint(-120, 121, (2048, 1024), generator=g, device=DEV).to(io) * 2.0 ** -5
+    x[::2] = randn(g, 1024, 1024, dtype=io)
+    w = torch.randint(1, 29, (1024,), generator=g, device=DEV).float() / 16
+    for rows in (2048, 300):
+        q, scale, _ = gdn.residual_norm_fp8(x[:rows], w, eps=EPS)
+        p = (x[:rows].double() * w.double()).view(rows, 8, 128)
+        want, normal = e4m3_of((448 * p / p.abs().amax(-1, keepdim=True)).view(rows, 1024))
+        assert torch.equal(q.double()[normal], want[normal])
+
+
 # ----------------------------------------------------------- 8-bit product
 def spread(scale, rows, cols, block_rows):
     s = scale.double()
