@@ -23,13 +23,14 @@
 // tensor pipe 90 % busy (206 us cold); 32768 rows run 890 us at 1.85 PFLOP/s,
 // and over seconds 955 us at the 1400 W limit with the SMs at 1.5 GHz, the rate
 // of a plain library product there.  8 bits: 32768 x 2048 against 4608 rows
-// 243 us, 2.5 PFLOP/s, tensor pipe 47 % busy (1040 cycles a K block; 261 us
-// over seconds, also at the power limit).  A block costs its 512 tensor cycles
+// 233 us, 2.65 PFLOP/s, tensor pipe 50 % busy (900 cycles a K block; 254 us over
+// seconds, also at the power limit).  A block costs its 512 tensor cycles
 // plus what the epilogue's chain (wait, four loads of 32 columns, 64 packed
 // multiply-adds, release) is not hidden by the other accumulator.  Not kept,
 // same product: 16 epilogue warps of 64 columns 262 us, two 128-column halves
-// with four accumulators 250 us, 16-column loads one block ahead 300 us;
-// without the multiply-adds it would take 207 us, without the loads 247 us.
+// with four accumulators 250 us, 16-column loads 300 us, each block's first
+// load before the last one's multiply-adds 262 us; without the multiply-adds it
+// would take 207 us, without them and the loads 196 us.
 //
 // Every wait has a limit: a wait that runs out flags GDN_ERR_TIMEOUT, and the
 // CTA leaves after its copies and products in flight have had time to end.
@@ -285,146 +286,154 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   // elected lane issuing: every address and descriptor then stays in uniform
   // registers.  (Loops run by one lane alone took 750 cycles a K block against
   // the 512 of its products.)
-  if (warp == 0) {
-    // ---------------------------------------------------------- fetch
-    const bool lead = elect_one();
-    const uint32_t full0 = mapa_smem(&full[0], 0);   // the even CTA's barriers
-    int st = 0;
-    uint32_t ph = 0;
-    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-      const Tile tl = tile_at(g, t);
-      const Problem& p = g.p[tl.p];
-      const int m0 = tl.m0 + 128 * (int)rank;
-      // gated: both CTAs' halves of B are the same 128 features of Wg and Wu
-      const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + 128 * (int)rank;
-      const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
-      const int k_half = p.k_half;
-      for (int kb = tl.k0; kb < tl.k1; ++kb) {
-        ok = mbar_wait_warp(&empty[st], ph ^ 1u, kWaitNs);
-        if (!ok) break;
-        if (lead) {
-          uint8_t* A = sm + st * kStageBytes;
-          uint8_t* B = A + kOperand;
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
-          const uint32_t bar = full0 + 8 * st;
-          const int h = kb >= k_half;
-          const int k0 = (kb - (h ? k_half : 0)) * (kFp8 ? 128 : 64);
-          const CUtensorMap* am = &p.a[h | tl.half];
-          const CUtensorMap* bm = &p.b[kEpi >= kGate ? (int)rank : h];
-          if (a_mn) {
-            tma_load_2d_pair(A, am, m0, k0, bar);
-            tma_load_2d_pair(A + 8192, am, m0 + 64, k0, bar);
-          } else {
-            tma_load_2d_pair(A, am, k0, m0, bar);
-          }
-          if (b_mn) {
-            tma_load_2d_pair(B, bm, n0, k0, bar);
-            tma_load_2d_pair(B + 8192, bm, n0 + 64, k0, bar);
-          } else {
-            tma_load_2d_pair(B, bm, k0, n0, bar);
-          }
-        }
-        __syncwarp();
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-  } else if (warp == 1 && rank == 0) {
-    // -------------------------------------------------------- multiply
-    const bool lead = elect_one();
-    const uint32_t sm0 = smem_u32(sm);
-    int st = 0, buf = 0;
-    uint32_t ph = 0, aph = 0;
-    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-      const Tile tl = tile_at(g, t);
-      const Problem& p = g.p[tl.p];
-      const uint32_t idesc =
-          kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, 256, p.a_mn, p.b_mn);
-      // a K-major block advances 32 bytes an instruction inside the swizzled
-      // row; one stored by rows advances 16 rows of K (2048 bytes)
-      const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
-      const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
-      const uint64_t a0 = smem_desc(sm0, a_mn ? 8192 : 16, 1024, kSwizzle128B);
-      const uint64_t b0 = smem_desc(sm0 + kOperand, b_mn ? 8192 : 16, 1024, kSwizzle128B);
-      for (int kb = tl.k0; kb < tl.k1; ++kb) {
-        const bool first = kFp8 || kb == tl.k0, last = kFp8 || kb + 1 == tl.k1;
-        if (first) {
-          ok = mbar_wait_warp(&acc_empty[buf], aph ^ 1u, kWaitNs);
+  if (warp < 4) {
+    // 8 bits: 384 threads launch with 168 registers each, 64512 in all, which
+    // is 128 x 72 + 256 x 216; the epilogue's 128 sums and 64 arriving columns
+    // need more than 168 (32768 x 2048 -> 4608: 233 us with them, 243 without).  Both branches say
+    // so themselves: behind a common branch the smaller limit holds for all.
+    if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- fetch
+      const bool lead = elect_one();
+      const uint32_t full0 = mapa_smem(&full[0], 0);   // the even CTA's barriers
+      int st = 0;
+      uint32_t ph = 0;
+      for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
+        const Tile tl = tile_at(g, t);
+        const Problem& p = g.p[tl.p];
+        const int m0 = tl.m0 + 128 * (int)rank;
+        // gated: both CTAs' halves of B are the same 128 features of Wg and Wu
+        const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + 128 * (int)rank;
+        const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
+        const int k_half = p.k_half;
+        for (int kb = tl.k0; kb < tl.k1; ++kb) {
+          ok = mbar_wait_warp(&empty[st], ph ^ 1u, kWaitNs);
           if (!ok) break;
-        }
-        ok = mbar_wait_warp(&full[st], ph, kWaitNs);
-        if (!ok) break;
-        tc_fence_after();
-        if (lead) {
-          const uint64_t ad = a0 + (uint64_t)(st * (kStageBytes >> 4));
-          const uint64_t bd = b0 + (uint64_t)(st * (kStageBytes >> 4));
-          const uint32_t d = tmem + 256 * buf;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (kFp8) mma_f8_pair(d, ad + i * a_step, bd + i * b_step, idesc, i != 0);
-            else mma_bf16_pair(d, ad + i * a_step, bd + i * b_step, idesc, !first || i != 0);
+          if (lead) {
+            uint8_t* A = sm + st * kStageBytes;
+            uint8_t* B = A + kOperand;
+            if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
+            const uint32_t bar = full0 + 8 * st;
+            const int h = kb >= k_half;
+            const int k0 = (kb - (h ? k_half : 0)) * (kFp8 ? 128 : 64);
+            const CUtensorMap* am = &p.a[h | tl.half];
+            const CUtensorMap* bm = &p.b[kEpi >= kGate ? (int)rank : h];
+            if (a_mn) {
+              tma_load_2d_pair(A, am, m0, k0, bar);
+              tma_load_2d_pair(A + 8192, am, m0 + 64, k0, bar);
+            } else {
+              tma_load_2d_pair(A, am, k0, m0, bar);
+            }
+            if (b_mn) {
+              tma_load_2d_pair(B, bm, n0, k0, bar);
+              tma_load_2d_pair(B + 8192, bm, n0 + 64, k0, bar);
+            } else {
+              tma_load_2d_pair(B, bm, k0, n0, bar);
+            }
           }
-          mma_commit_pair(&empty[st]);
-          if (last) mma_commit_pair(&acc_full[buf]);
+          __syncwarp();
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
-        __syncwarp();
-        if (last) {
-          buf ^= 1;
-          if (buf == 0) aph ^= 1u;
+      }
+    } else if (warp == 1 && rank == 0) {
+      // -------------------------------------------------------- multiply
+      const bool lead = elect_one();
+      const uint32_t sm0 = smem_u32(sm);
+      int st = 0, buf = 0;
+      uint32_t ph = 0, aph = 0;
+      for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
+        const Tile tl = tile_at(g, t);
+        const Problem& p = g.p[tl.p];
+        const uint32_t idesc =
+            kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, 256, p.a_mn, p.b_mn);
+        // a K-major block advances 32 bytes an instruction inside the swizzled
+        // row; one stored by rows advances 16 rows of K (2048 bytes)
+        const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
+        const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint64_t a0 = smem_desc(sm0, a_mn ? 8192 : 16, 1024, kSwizzle128B);
+        const uint64_t b0 = smem_desc(sm0 + kOperand, b_mn ? 8192 : 16, 1024, kSwizzle128B);
+        for (int kb = tl.k0; kb < tl.k1; ++kb) {
+          const bool first = kFp8 || kb == tl.k0, last = kFp8 || kb + 1 == tl.k1;
+          if (first) {
+            ok = mbar_wait_warp(&acc_empty[buf], aph ^ 1u, kWaitNs);
+            if (!ok) break;
+          }
+          ok = mbar_wait_warp(&full[st], ph, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+            const uint64_t ad = a0 + (uint64_t)(st * (kStageBytes >> 4));
+            const uint64_t bd = b0 + (uint64_t)(st * (kStageBytes >> 4));
+            const uint32_t d = tmem + 256 * buf;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (kFp8) mma_f8_pair(d, ad + i * a_step, bd + i * b_step, idesc, i != 0);
+              else mma_bf16_pair(d, ad + i * a_step, bd + i * b_step, idesc, !first || i != 0);
+            }
+            mma_commit_pair(&empty[st]);
+            if (last) mma_commit_pair(&acc_full[buf]);
+          }
+          __syncwarp();
+          if (last) {
+            buf ^= 1;
+            if (buf == 0) aph ^= 1u;
+          }
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1u;
+      }
+    } else if (kFp8 && (warp == 2 || warp == 3)) {
+      // ---------------------------------------------------------- scales
+      // s[j][h][r] = sa[row r][k0 + j] sb[column block h][k0 + j] of kGroup K
+      // blocks at a time; a group is in registers while its slot is in use.
+      int slot = 0;
+      uint32_t ph = 0;
+      for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
+        const Tile tl = tile_at(g, t);
+        const Problem& p = g.p[tl.p];
+        const int r0 = 64 * (warp - 2) + lane, nb = tl.n0 / 128;
+        const float* sb0 = g.sb + (size_t)nb * g.sblocks;
+        const float* sb1 = sb0 + (tl.n0 + 128 < p.N ? g.sblocks : 0);
+        const float* sa[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = tl.m0 + 128 * (int)rank + r0 + 32 * i;
+          sa[i] = g.sa + (size_t)(row < p.M ? row : p.M - 1) * g.sblocks;
+        }
+        for (int kb = 0; kb < p.k_blocks; kb += kGroup) {
+          float a[2][kGroup], b[2][kGroup];
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) {
+            const int k = kb + j < p.k_blocks ? kb + j : kb;
+            a[0][j] = __ldg(sa[0] + k);
+            a[1][j] = __ldg(sa[1] + k);
+            b[0][j] = __ldg(sb0 + k);
+            b[1][j] = __ldg(sb1 + k);
+          }
+          ok = mbar_wait_warp(&sc_empty[slot], ph ^ 1u, kWaitNs);
+          if (!ok) break;
+          float* d = scales + slot * (kGroup * 256) + r0;
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              d[j * 256 + h * 128] = a[0][j] * b[h][j];
+              d[j * 256 + h * 128 + 32] = a[1][j] * b[h][j];
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[slot]);
+          slot ^= 1;
+          if (slot == 0) ph ^= 1u;
         }
       }
     }
-  } else if (kFp8 && (warp == 2 || warp == 3)) {
-    // ---------------------------------------------------------- scales
-    // s[j][h][r] = sa[row r][k0 + j] sb[column block h][k0 + j] of kGroup K
-    // blocks at a time; a group is in registers while its slot is in use.
-    int slot = 0;
-    uint32_t ph = 0;
-    for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-      const Tile tl = tile_at(g, t);
-      const Problem& p = g.p[tl.p];
-      const int r0 = 64 * (warp - 2) + lane, nb = tl.n0 / 128;
-      const float* sb0 = g.sb + (size_t)nb * g.sblocks;
-      const float* sb1 = sb0 + (tl.n0 + 128 < p.N ? g.sblocks : 0);
-      const float* sa[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = tl.m0 + 128 * (int)rank + r0 + 32 * i;
-        sa[i] = g.sa + (size_t)(row < p.M ? row : p.M - 1) * g.sblocks;
-      }
-      for (int kb = 0; kb < p.k_blocks; kb += kGroup) {
-        float a[2][kGroup], b[2][kGroup];
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          const int k = kb + j < p.k_blocks ? kb + j : kb;
-          a[0][j] = __ldg(sa[0] + k);
-          a[1][j] = __ldg(sa[1] + k);
-          b[0][j] = __ldg(sb0 + k);
-          b[1][j] = __ldg(sb1 + k);
-        }
-        ok = mbar_wait_warp(&sc_empty[slot], ph ^ 1u, kWaitNs);
-        if (!ok) break;
-        float* d = scales + slot * (kGroup * 256) + r0;
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            d[j * 256 + h * 128] = a[0][j] * b[h][j];
-            d[j * 256 + h * 128 + 32] = a[1][j] * b[h][j];
-          }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sc_full[slot]);
-        slot ^= 1;
-        if (slot == 0) ph ^= 1u;
-      }
-    }
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // -------------------------------------------------------- epilogue
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
