@@ -124,11 +124,28 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
   }
   return make_uint2(w[0], w[1]);
 }
+// 448 / m to a few units in the last place (scaled, so that no m from 2^-100 up
+// has a subnormal reciprocal), and m / 448 rounded to nearest: the product with
+// the rounded reciprocal, corrected by its exact remainder.
+__device__ __forceinline__ float codes_per(float m) { return 1.75f * rcp_sfu(m * 0x1p-8f); }
+__device__ __forceinline__ float scale_of(float m) {
+  constexpr float r = 1.f / kE4m3Max;
+  const float q = __fmul_rn(m, r);
+  return isinf(q) ? q : __fmaf_rn(__fmaf_rn(-kE4m3Max, q, m), r, q);
+}
 // Is v (an e4m3 value's size, not below its normal range) within 16 units in
 // its last place of the middle between two e4m3 values?  fp32 gets y (448 / m)
-// to about 3, so elsewhere its rounding is that of the real number.
-__device__ __forceinline__ bool near_tie(float v) {
-  return (__float_as_uint(v) & 0xfffffu) - 0x7fff0u <= 0x20u;
+// to about 5, so elsewhere its rounding is that of the real number.  tie_gap is
+// at most 0x20 there.
+__device__ __forceinline__ uint32_t tie_gap(float v) {
+  return (__float_as_uint(v) - 0x7fff0u) & 0xfffffu;
+}
+__device__ __forceinline__ bool near_tie(float v) { return tie_gap(v) <= 0x20u; }
+__device__ __forceinline__ bool any_near_tie(const float (&v)[8]) {
+  uint32_t g = tie_gap(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) g = min(g, tie_gap(v[i]));
+  return g <= 0x20u;
 }
 // v, which is near the tie t, moved to where 448 p / m lies: on t or beside it.
 // p = ph + pl and m = mh + ml, magnitudes; t has 5 significant bits.  The
@@ -252,15 +269,11 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
 #pragma unroll
       for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
       m = max_nan(m, kTiny);
-      const float inv = __fdiv_rn(kE4m3Max, m);
+      const float inv = codes_per(m);
       float v[8];
-      bool near = false;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = __fmul_rn(f[i], inv);
-        near |= near_tie(v[i]);
-      }
-      if (__any_sync(0xffffffffu, near && m > kTiny)) {
+      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(f[i], inv);
+      if (__any_sync(0xffffffffu, any_near_tie(v) && m > kTiny)) {
         // (one in 120 of these) the root cancels in y / m: the codes are those
         // of 448 s_j w_j / max |s w|, a product being hi + lo exactly
         float fs[8], mh = 0.f, ml = 0.f;
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
       if (in) {
         *reinterpret_cast<uint2*>(a.q + base + c) = codes8(v);
         if ((lane & 15) == 0)
-          a.scale[(size_t)row * a.blocks + c / 128] = __fdiv_rn(m, kE4m3Max);
+          a.scale[(size_t)row * a.blocks + c / 128] = scale_of(m);
       }
     }
   }
@@ -454,15 +467,12 @@ struct QuantArgs {
 };
 
 // The codes of x (448 / m) in a block whose largest magnitude is m.
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m, float inv) {
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
+  const float inv = codes_per(m);
   float v[8];
-  bool near = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = __fmul_rn(x[i], inv);
-    near |= near_tie(v[i]);
-  }
-  if (near && m > kTiny) {
+  for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inv);
+  if (any_near_tie(v) && m > kTiny) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);
@@ -483,7 +493,8 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
   int64_t at[kTwo];   // the elements' place, -1 past the row's end
 #pragma unroll
   for (int i = 0; i < kTwo; ++i) {
-    const int64_t u = u0 + i * (kThreads / 16), row = u / a.blocks;
+    const int64_t u = u0 + i * (kThreads / 16);
+    const int64_t row = u >> 32 ? u / a.blocks : (uint32_t)u / (uint32_t)a.blocks;
     const int c = (int)(u - row * a.blocks) * 128 + l * 8;
     at[i] = u < units && c < a.cols ? row * a.cols + c : -1;
     x[i].zero();
@@ -498,8 +509,8 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
     for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = max_nan(m, kTiny);
     if (at[i] >= 0) {
-      *reinterpret_cast<uint2*>(a.q + at[i]) = quantise8(f, m, __fdiv_rn(kE4m3Max, m));
-      if (l == 0) a.scale[u0 + i * (kThreads / 16)] = __fdiv_rn(m, kE4m3Max);
+      *reinterpret_cast<uint2*>(a.q + at[i]) = quantise8(f, m);
+      if (l == 0) a.scale[u0 + i * (kThreads / 16)] = scale_of(m);
     }
   }
 }
@@ -533,17 +544,16 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantArgs a) {
   m = kTiny;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) m = max_nan(m, wm[i]);
-  const float inv = __fdiv_rn(kE4m3Max, m);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (r0 + 16 * i < a.rows && c < a.cols) {
       float f[8];
       x[i].widen(f);
-      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = quantise8(f, m, inv);
+      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = quantise8(f, m);
     }
   }
   if (threadIdx.x == 0)
-    a.scale[(size_t)blockIdx.y * a.blocks + blockIdx.x] = __fdiv_rn(m, kE4m3Max);
+    a.scale[(size_t)blockIdx.y * a.blocks + blockIdx.x] = scale_of(m);
 }
 
 // ---------------------------------------------------------------- launchers
