@@ -466,16 +466,30 @@ struct QuantArgs {
   int64_t rows; int32_t cols, blocks;
 };
 
-// The codes of x (448 / m) in a block whose largest magnitude is m.
+// The codes of 448 x / m in a block whose largest magnitude is m.
+template <typename T>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
-  const float inv = codes_per(m);
   float v[8];
+  if constexpr (sizeof(T) == 2) {
+    // bf16: 0.875 x is exact, so one step with the quotient's exact remainder
+    // gives the rounded quotient, and the quotient itself where it has few
+    // bits, as the middle between two codes does (no other is so near one that
+    // fp32 rounds to it: it is apart by 2^-13 at least)
+    const float d = m * 0x1p-9f, r = rcp_sfu(d);   // 448 / m = 0.875 / d
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inv);
-  if (any_near_tie(v) && m > kTiny) {
+    for (int i = 0; i < 8; ++i) {
+      const float a = __fmul_rn(x[i], 0.875f), q = __fmul_rn(a, r);
+      v[i] = __fmaf_rn(__fmaf_rn(-q, d, a), r, q);
+    }
+  } else {
+    const float inv = codes_per(m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inv);
+    if (any_near_tie(v) && m > kTiny) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);
+    }
   }
   return codes8(v);
 }
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantArgs a) {
     for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = max_nan(m, kTiny);
     if (at[i] >= 0) {
-      *reinterpret_cast<uint2*>(a.q + at[i]) = quantise8(f, m);
+      *reinterpret_cast<uint2*>(a.q + at[i]) = quantise8<T>(f, m);
       if (l == 0) a.scale[u0 + i * (kThreads / 16)] = scale_of(m);
     }
   }
@@ -549,7 +563,7 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantArgs a) {
     if (r0 + 16 * i < a.rows && c < a.cols) {
       float f[8];
       x[i].widen(f);
-      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = quantise8(f, m);
+      *reinterpret_cast<uint2*>(a.q + (size_t)(r0 + 16 * i) * a.cols + c) = quantise8<T>(f, m);
     }
   }
   if (threadIdx.x == 0)
