@@ -131,11 +131,21 @@ def load():
     lib.gdn_release_scratch.restype = ctypes.c_int
     lib.gdn_testing_scratch_reserved.argtypes = [vp]
     lib.gdn_testing_scratch_reserved.restype = ctypes.c_int
-    from . import _layer_calls
-    _layer_calls.bind(path)
-    _direct = _layer_calls
+    try:
+        from . import _layer_calls
+        _layer_calls.bind(path)
+        _direct = _layer_calls
+    except ImportError:   # built without Python's headers, or for another PyTorch
+        _direct = _Declines()
     _lib = lib
     return lib
+
+
+class _Declines:
+    """In the place of _layer_calls: every call takes the general path."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
 
 
 def _direct_calls():

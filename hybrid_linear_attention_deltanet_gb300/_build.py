@@ -28,11 +28,16 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def build_binding() -> str:
-    """Compile csrc/binding.cpp into _layer_calls.so with the host compiler."""
+def build_binding() -> str | None:
+    """Compile csrc/binding.cpp into _layer_calls.so with the host compiler
+    (None where Python's headers are not installed: the binding in Python then
+    makes every call itself)."""
     import torch
     src = os.path.join(CSRC, "binding.cpp")
     out = os.path.join(HERE, "_layer_calls.so")
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        print("_layer_calls.so not built: Python.h is missing")
+        return None
     newest = max(os.path.getmtime(p) for p in
                  [src, torch.__file__] + glob.glob(os.path.join(INCLUDE, "*.h")))
     if os.path.exists(out) and os.path.getmtime(out) >= newest:

@@ -81,7 +81,9 @@ cudaError_t launch(bool dependent, void (*kern)(P...), dim3 grid, unsigned threa
   }
   cfg.attrs = at;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();   // reported here, not to the caller's next call
+  return e;
 }
 
 }  // namespace gdn
