@@ -24,13 +24,13 @@
 // and over seconds 955 us at the 1400 W limit with the SMs at 1.5 GHz, the rate
 // of a plain library product there.  8 bits: 32768 x 2048 against 4608 rows
 // 233 us, 2.65 PFLOP/s, tensor pipe 50 % busy (900 cycles a K block; 254 us over
-// seconds, also at the power limit).  A block costs its 512 tensor cycles
-// plus what the epilogue's chain (wait, four loads of 32 columns, 64 packed
-// multiply-adds, release) is not hidden by the other accumulator.  Not kept,
-// same product: 16 epilogue warps of 64 columns 262 us, two 128-column halves
-// with four accumulators 250 us, 16-column loads 300 us, each block's first
-// load before the last one's multiply-adds 262 us; without the multiply-adds it
-// would take 207 us, without them and the loads 196 us.
+// seconds, also at the power limit).  The epilogue's reads of tensor memory
+// bound it: they share it with the products' sums and take twice their time
+// alone.  (Same product, us: products without epilogue 184; loads and
+// multiply-adds running free of any hand-over 254; hand-over without loads and
+// multiply-adds 196, without multiply-adds 207.)  Not kept: 16 epilogue warps of
+// 64 columns 262, two 128-column halves with four accumulators 250, 16-column
+// loads 300, each block's first load before the last one's multiply-adds 262.
 //
 // Every wait has a limit: a wait that runs out flags GDN_ERR_TIMEOUT, and the
 // CTA leaves after its copies and products in flight have had time to end.
