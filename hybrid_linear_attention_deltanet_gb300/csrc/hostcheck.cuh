@@ -43,12 +43,13 @@ inline int sm_count() {
 
 }  // namespace hostcheck
 
-// The matrix products are launched as programmatic dependents: a grid may
-// start while the one before it in the stream still runs, does what needs no
-// data (barriers, tensor memory), and waits in grid_wait() for that grid's end
-// and memory before its first access to global memory; every kernel launched
-// so calls it.  (About 1 us of a product's 5 to 15 with few tokens; the
-// attribute costs the host 1.5 us a launch, more than the norms would gain.)
+// The matrix products and the sums of parts are launched as programmatic
+// dependents: a grid may start while the one before it in the stream still
+// runs, does what needs no data (barriers, tensor memory), and waits in
+// grid_wait() for that grid's end and memory before its first access to global
+// memory; every kernel launched so calls it.  (About 1 us of a product's 5 to
+// 15 with few tokens; the attribute costs the host 1.5 us a launch, more than
+// the norms themselves would gain.)
 __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -440,10 +440,12 @@ __global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
 }
 
 // dw[c] = sum_b part[b][c]: 32 strided runs, each in order, then the runs in
-// order.
+// order.  A programmatic dependent of the kernel above (both for 8191 x 4096:
+// 51.7 us against 54.0 launched plainly).
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int n,
                                                        int dim, float* __restrict__ dw) {
   grid_release_next();
+  grid_wait();
   __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -728,10 +730,9 @@ int backward_common(const void* dy, const void* s, const float* w, const void* d
     kern<<<plan.grid, kThreads, 0, stream>>>(a);
     e = cudaGetLastError();
   });
-  if (e == cudaSuccess && !plan.cluster) {
-    norm_dw_kernel<<<(dim + 31) / 32, 1024, 0, stream>>>((const float*)part, plan.grid, dim, dw);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && !plan.cluster)
+    e = launch(true, norm_dw_kernel, dim3((dim + 31) / 32), 1024, 0, 0, stream,
+               (const float*)part, plan.grid, (int)dim, dw);
   count_launches(plan.cluster ? 1 : 2);
   if (own && scratch_free(part, stream) != cudaSuccess) return GDN_ERR_CUDA;
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
