@@ -134,11 +134,15 @@ int shape_check(int64_t tokens, int32_t dim, int32_t hidden, int32_t act, int32_
 }
 
 // The product with both projections, x [tokens][dim] against Wg and Wu.
-bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* wu, int64_t tokens,
-                 int32_t dim, int32_t hidden) {
+template <int kEpi>
+cudaError_t projections(gemm::PairArgs& g, const void* x, const void* wg, const void* wu,
+                        int64_t tokens, int32_t dim, int32_t hidden, int sms,
+                        cudaStream_t stream) {
+  const bool narrow = gemm::narrow_tiles(tokens, hidden, sms);
+  const int32_t features = narrow ? 96 : 128;   // of each projection a tile
   gemm::Problem& p = g.p[0];
   p.m_half = p.m_tiles = (int32_t)((tokens + 255) / 256);
-  p.n_tiles = (hidden + 127) / 128;
+  p.n_tiles = (hidden + features - 1) / features;
   p.k_half = p.k_blocks = (dim + 63) / 64;
   p.k_parts = 1;
   p.M = (int32_t)tokens;
@@ -146,11 +150,12 @@ bool projections(gemm::PairArgs& g, const void* x, const void* wg, const void* w
   g.problems = 1;
   g.group_m = gemm::group_rows((int64_t)dim * 2);
   if (!gemm::matrix_map(&p.a[0], x, false, dim, tokens, (int64_t)dim * 2, 128) ||
-      !gemm::matrix_map(&p.b[0], wg, false, dim, hidden, (int64_t)dim * 2, 128) ||
-      !gemm::matrix_map(&p.b[1], wu, false, dim, hidden, (int64_t)dim * 2, 128))
-    return false;
+      !gemm::matrix_map(&p.b[0], wg, false, dim, hidden, (int64_t)dim * 2, features) ||
+      !gemm::matrix_map(&p.b[1], wu, false, dim, hidden, (int64_t)dim * 2, features))
+    return cudaErrorUnknown;
   p.a[1] = p.a[0];
-  return true;
+  return narrow ? gemm::launch_pair<false, kEpi, 192>(g, sms, stream)
+                : gemm::launch_pair<false, kEpi>(g, sms, stream);
 }
 
 // The same for few tokens (gemm_split.cuh).
@@ -200,12 +205,12 @@ int ffn_forward(const void* x, const void* wg, const void* wu, int32_t act, void
   gemm::PairArgs g;
   memset(&g, 0, sizeof g);
   g.status = status;
-  if (!projections(g, x, wg, wu, tokens, dim, hidden)) return GDN_ERR_CUDA;
   g.act = act;
   g.p[0].out[0] = g.p[0].out[1] = h;
   g.p[0].ldc = hidden;
-  return gemm::launch_pair<false, gemm::kGate>(g, sms, stream) == cudaSuccess ? GDN_OK
-                                                                              : GDN_ERR_CUDA;
+  const cudaError_t e =
+      projections<gemm::kGate>(g, x, wg, wu, tokens, dim, hidden, sms, stream);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const void* dh,
@@ -231,14 +236,13 @@ cudaError_t launch_backward(const void* x, const void* wg, const void* wu, const
     memset(&g, 0, sizeof g);
     g.status = status;
     g.act = act;
-    if (!projections(g, x, wg, wu, tokens, dim, hidden)) return cudaErrorUnknown;
     g.p[0].out[0] = dG;
     g.p[0].out[1] = dU;
     g.p[0].ldc = pitch;
     g.dh = (const __nv_bfloat16*)dh;
     g.ldh = hidden;
     g.dh_wide = hidden % 8 == 0;
-    e = gemm::launch_pair<false, gemm::kGateGrad>(g, sms, stream);
+    e = projections<gemm::kGateGrad>(g, x, wg, wu, tokens, dim, hidden, sms, stream);
   }
   if (e != cudaSuccess) return e;
 

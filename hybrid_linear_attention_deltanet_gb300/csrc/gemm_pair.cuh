@@ -7,6 +7,7 @@
 // rows of A and its own 128 of B's 256 rows (TMA, 128-byte swizzle) and the
 // even CTA's one MMA thread multiplies all of it: 32 KB into each SM for
 // 512 tensor cycles, half of what two single-CTA 128 x 256 tiles would fetch.
+// (Gated products take tiles of 192 columns where those fill the pairs better.)
 //
 // Roles: warp 0 fetches, warp 1 multiplies (even CTA only), warp 2 owns the
 // tensor memory, warps 4 and up take the accumulators out.  The grid is
@@ -52,7 +53,7 @@ using namespace sm100;
 enum Epilogue : int {
   kStore,      // C as bf16
   kStoreF32,   // C as fp32
-  kGate,       // columns 0..127 are G, 128..255 U of the same 128 features: act(G) U
+  kGate,       // columns of the first half are G, of the second U of the same features: act(G) U
   kGateGrad    // the same G and U with dh: dG = dh U act'(G), dU = dh act(G)
 };
 
@@ -134,6 +135,7 @@ __device__ __forceinline__ int tile_of(const PairArgs& g, int pairs, int i, int 
 
 // Tile t: groups of group_m row tiles, all columns of a group before the next
 // group, so that the tiles in flight share their operands in L2.
+template <int kTileN>
 __device__ __forceinline__ Tile tile_at(const PairArgs& g, int t) {
   Tile r;
   r.p = 0;
@@ -157,7 +159,7 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& g, int t) {
   const int mt = grp * g.group_m + in % gm, nt = in / gm;
   r.half = mt >= p.m_half;
   r.m0 = (mt - (r.half ? p.m_half : 0)) * 256;
-  r.n0 = nt * 256;
+  r.n0 = nt * kTileN;
   return r;
 }
 
@@ -165,14 +167,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Offset of 16-byte piece `i` of row `r` in a warp's staging image, swizzled
-// as TMA's 128-byte mode does; lanes that write a piece of each row meet no
-// bank conflicts.
+// Offset of 16-byte piece `i` of row `r` in a warp's staging image with rows
+// of kRow bytes, swizzled as TMA's mode of that many bytes does; lanes that
+// write a piece of each row meet no bank conflicts.
+template <int kRow = 128>
 __device__ __forceinline__ uint32_t stage_piece(uint32_t r, uint32_t i) {
-  return r * 128 + (i ^ (r & 7u)) * 16;
+  return r * kRow + (kRow == 128 ? i ^ (r & 7u) : i ^ (r >> 1 & 3u)) * 16;
 }
 // 32 columns from `c0` of this lane's row into its warp's staging image.
-template <typename T>
+template <typename T, int kRow = 128>
 __device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const float* v) {
   constexpr int kPer = 16 / (int)sizeof(T);   // elements a piece
 #pragma unroll
@@ -184,12 +187,12 @@ __device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const 
     else
       w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-    *reinterpret_cast<uint4*>(buf + stage_piece(lane, c0 / kPer + i)) = w;
+    *reinterpret_cast<uint4*>(buf + stage_piece<kRow>(lane, c0 / kPer + i)) = w;
   }
 }
 // The staged 32 rows to their place, what lies past the edges of the output
 // left out.  stage_free() must return before the next stage_put.
-template <typename T>
+template <typename T, int kRow = 128>
 __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Problem& p, int half,
                                           int row0, int n0, int shift = 0) {
   if (row0 >= p.M || n0 >= p.N) return;
@@ -202,7 +205,7 @@ __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Pr
     }
   } else {   // rows that start anywhere: a row at a time, 32 elements a step
     __syncwarp();
-    constexpr int kCols = 128 / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
+    constexpr int kCols = kRow / (int)sizeof(T), kPer = 16 / (int)sizeof(T);
     const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
     T* out = (T*)p.out[half] + (size_t)row0 * p.ldc + n0;
 #pragma unroll
@@ -212,7 +215,7 @@ __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Pr
 #pragma unroll 8
       for (int r = 0; r < rows; ++r)
         out[(size_t)r * p.ldc + c] = *reinterpret_cast<const T*>(
-            buf + stage_piece(r, c / kPer) + (c % kPer) * sizeof(T));
+            buf + stage_piece<kRow>(r, c / kPer) + (c % kPer) * sizeof(T));
     }
   }
 }
@@ -240,10 +243,14 @@ __device__ __forceinline__ void gate_grad(float dh, float G, float U, int act, f
   dU = dh * (silu ? G * s : s);
 }
 
-template <bool kFp8, int kEpi>
+// kTileN: 256 columns, or 192 (gated), see narrow_tiles.
+template <bool kFp8, int kEpi, int kTileN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs g) {
   constexpr int kStages = Shape<kFp8>::kStages;
+  static_assert(kTileN == 256 || (kTileN == 192 && kEpi >= kGate && !kFp8), "");
+  // what arrives in both CTAs for a stage
+  constexpr uint32_t kArrive = 2 * (kOperand + kOperand / 256 * kTileN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
@@ -299,10 +306,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int st = 0;
       uint32_t ph = 0;
       for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-        const Tile tl = tile_at(g, t);
+        const Tile tl = tile_at<kTileN>(g, t);
         const Problem& p = g.p[tl.p];
         const int m0 = tl.m0 + 128 * (int)rank;
-        // gated: both CTAs' halves of B are the same 128 features of Wg and Wu
+        // gated: both CTAs' halves of B are the same features of Wg and Wu
         const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + 128 * (int)rank;
         const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
         const int k_half = p.k_half;
@@ -312,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lead) {
             uint8_t* A = sm + st * kStageBytes;
             uint8_t* B = A + kOperand;
-            if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(&full[st], kArrive);
             const uint32_t bar = full0 + 8 * st;
             const int h = kb >= k_half;
             const int k0 = (kb - (h ? k_half : 0)) * (kFp8 ? 128 : 64);
@@ -345,10 +352,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int st = 0, buf = 0;
       uint32_t ph = 0, aph = 0;
       for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-        const Tile tl = tile_at(g, t);
+        const Tile tl = tile_at<kTileN>(g, t);
         const Problem& p = g.p[tl.p];
         const uint32_t idesc =
-            kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, 256, p.a_mn, p.b_mn);
+            kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, kTileN, p.a_mn, p.b_mn);
         // a K-major block advances 32 bytes an instruction inside the swizzled
         // row; one stored by rows advances 16 rows of K (2048 bytes)
         const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
@@ -394,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int slot = 0;
       uint32_t ph = 0;
       for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-        const Tile tl = tile_at(g, t);
+        const Tile tl = tile_at<kTileN>(g, t);
         const Problem& p = g.p[tl.p];
         const int r0 = 64 * (warp - 2) + lane, nb = tl.n0 / 128;
         const float* sb0 = g.sb + (size_t)nb * g.sblocks;
@@ -452,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (buf == 0) aph ^= 1u;
     };
     for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
-      const Tile tl = tile_at(g, t);
+      const Tile tl = tile_at<kTileN>(g, t);
       const Problem& p = g.p[tl.p];
       const int row0 = tl.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
       const bool live = row < p.M;
@@ -536,8 +543,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         advance();
       } else {
-        // this thread's 64 features
+        // this thread's 64 features; of 96 the second warps' 32
+        constexpr bool kNarrow = kTileN == 192;
         const int f0 = tl.n0 / 2 + 64 * part;
+        const bool half = kNarrow && part;
         uint32_t dh[kEpi == kGateGrad ? 32 : 1];   // 64 bf16, fetched before the wait
         if constexpr (kEpi == kGateGrad) {
           if (g.dh_wide) {   // hidden a multiple of 8: whole 16-byte pieces or none
@@ -545,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint4 w = make_uint4(0, 0, 0, 0);
-              if (live && f0 + 8 * i < p.N) w = __ldg(reinterpret_cast<const uint4*>(d) + i);
+              if (live && f0 + 8 * i < p.N && !(half && i >= 4)) w = __ldg(reinterpret_cast<const uint4*>(d) + i);
               dh[4 * i] = w.x; dh[4 * i + 1] = w.y; dh[4 * i + 2] = w.z; dh[4 * i + 3] = w.w;
             }
           } else {           // rows that start anywhere: a row at a time through the staging
@@ -553,6 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int c = lane + 32 * i;
+              if (half && i) break;
 #pragma unroll 8
               for (int r = 0; r < 32; ++r) {
                 __nv_bfloat16 v = __float2bfloat16_rn(0.f);
@@ -578,13 +588,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           stage_free(lane);
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
+            if (half && c) break;
             uint32_t G[32], U[32];
             tmem_ld32(tmem + lanes + 256 * buf + 64 * part + c, G);
             if (kEpi == kGate || out == 0)
-              tmem_ld32(tmem + lanes + 256 * buf + 128 + 64 * part + c, U);
+              tmem_ld32(tmem + lanes + 256 * buf + kTileN / 2 + 64 * part + c, U);
             tmem_ld_wait_regs(G);
             if (kEpi == kGate || out == 0) tmem_ld_wait_regs(U);
-            if (c == 32 && (kEpi == kGate || out == 1)) release();
+            if ((c == 32 || half) && (kEpi == kGate || out == 1)) release();
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -599,9 +610,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 v[i] = out == 0 ? dG : dU;
               }
             }
-            stage_put<__nv_bfloat16>(bounce, lane, c, v);
+            if constexpr (kNarrow) {   // 32 features leave at a time, each from its half
+              uint8_t* own = bounce + c / 32 * (kBounce / 2);
+              stage_put<__nv_bfloat16, 64>(own, lane, 0, v);
+              stage_out<__nv_bfloat16, 64>(own, lane, p, out, row0, f0 + c);
+            } else {
+              stage_put<__nv_bfloat16>(bounce, lane, c, v);
+            }
           }
-          stage_out<__nv_bfloat16>(bounce, lane, p, out, row0, f0);
+          if constexpr (!kNarrow) stage_out<__nv_bfloat16>(bounce, lane, p, out, row0, f0);
         }
         advance();
       }
@@ -660,7 +677,7 @@ inline bool matrix_map(CUtensorMap* m, const void* base, bool fp8, int64_t inner
 // TMA stores where rows start on 16 bytes, plain ones elsewhere.  (Parts of K
 // write [k_parts][part_rows][N], whose rows past M no one reads; their rows
 // have to start on 16 bytes.)
-inline bool output_maps(Problem& p, bool f32) {
+inline bool output_maps(Problem& p, bool f32, int tile_n) {
   if (p.k_parts > 1) f32 = true;
   const int64_t pitch = p.ldc * (f32 ? 4 : 2);
   p.c_tma = pitch % 16 == 0;
@@ -675,11 +692,12 @@ inline bool output_maps(Problem& p, bool f32) {
     cuuint64_t dims[2] = {(cuuint64_t)p.N,
                           (cuuint64_t)(p.k_parts > 1 ? (int64_t)p.k_parts * p.part_rows : p.M)};
     cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+    cuuint32_t box[2] = {f32 || tile_n == 192 ? 32u : 64u, 32};
     cuuint32_t es[2] = {1, 1};
     if (enc(&p.c[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             p.out[i], dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            tile_n == 192 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
   }
@@ -695,17 +713,29 @@ inline int32_t group_rows(int64_t pitch) {
   return n < 8 ? 8 : n > 32 ? 32 : (int32_t)n;
 }
 
-template <bool kFp8, int kEpi>
+// Whether the gated product's tiles have 192 columns and not 256: a round of
+// them takes 5/6 of the time (they read the rows of A for fewer columns), so
+// where that many rounds take less.  (2048 -> 2 x 6144, us with 192 and 256:
+// 256 tokens 14.3 and 15.5, 512 21.0 and 24.0, 4096, where this says 256, 117
+// and 109; 1000 tokens, 1032 -> 2 x 2731: 16.7 and 18.8.)
+inline bool narrow_tiles(int64_t tokens, int32_t features, int sms) {
+  const int64_t pairs = sms / 2, mt = (tokens + 255) / 256;
+  const int64_t wide = mt * (((int64_t)features + 127) / 128);
+  const int64_t narrow = mt * (((int64_t)features + 95) / 96);
+  return 5 * ((narrow + pairs - 1) / pairs) < 6 * ((wide + pairs - 1) / pairs);
+}
+
+template <bool kFp8, int kEpi, int kTileN = 256>
 cudaError_t launch_pair(PairArgs& g, int sms, cudaStream_t st) {
   constexpr uint32_t kSmem = Shape<kFp8>::kSmem;
-  auto kern = pair_gemm_kernel<kFp8, kEpi>;
+  auto kern = pair_gemm_kernel<kFp8, kEpi, kTileN>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   int64_t tiles = 0;
   int32_t length[2] = {0, 1};   // K blocks of a tile, and about what its end costs
   for (int i = 0; i < g.problems; ++i) {
-    if (!output_maps(g.p[i], kEpi == kStoreF32)) return cudaErrorUnknown;
+    if (!output_maps(g.p[i], kEpi == kStoreF32, kTileN)) return cudaErrorUnknown;
     tiles += tiles_of(g.p[i]);
     if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
     g.tiles[i] = (int32_t)tiles_of(g.p[i]);

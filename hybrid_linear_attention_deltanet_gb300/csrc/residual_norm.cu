@@ -14,7 +14,7 @@
 // 128-column block: a block's largest magnitude is four shuffles.
 //
 // Measured (bf16): 32768 x 2048 with residual and 8-bit output 78 us, 6.0 TB/s
-// of a copy's 6.7; the gradient of 8191 x 4096 47 us, 5.7 TB/s; one token 1.8 us
+// of a copy's 6.7; the gradient of 8191 x 4096 48.6 us, 5.5 TB/s; one token 1.8 us
 // on the GPU.
 #include <cuda_fp8.h>
 

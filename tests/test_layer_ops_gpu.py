@@ -454,6 +454,22 @@ def test_gated_ffn_many_tiles():
     assert gdn.device_status() == 0
 
 
+# tiles of 256 columns where they fill the last round, of 192 elsewhere; rows of
+# the result that start on 16 bytes and that do not
+@pytest.mark.parametrize("tokens,dim,hidden", [
+    (777, 64, 8000), (777, 64, 8001), (300, 72, 6000), (300, 72, 6001), (513, 136, 2053),
+    (255, 64, 9700), (255, 64, 9699), (1000, 72, 97), (1000, 72, 33), (1000, 72, 95)])
+def test_gated_ffn_tile_widths(tokens, dim, hidden):
+    x, wg, wu, _ = ffn_inputs(tokens, dim, hidden, 3 * tokens + hidden)
+    b = Guarded((tokens, hidden), BF16)
+    h = gdn.gated_ffn(x, wg, wu, h=b.t)
+    G, U, a, _, eU, ea, _ = ffn_terms(x, wg, wu, "silu")
+    within(h, a * U, (2.0 ** -8 + 2.0 ** -22) * (a * U).abs()
+           + 1.01 * (ea * U.abs() + a.abs() * eU), "h")
+    b.check()
+    check_ffn_backward(tokens, dim, hidden, "silu", 5 * tokens + hidden)
+
+
 @pytest.mark.parametrize("act", ["silu", "sigmoid"])
 def test_gated_ffn_backward_differences(act):
     x, wg, wu, dh = ffn_inputs(33, 64, 48, 31)
