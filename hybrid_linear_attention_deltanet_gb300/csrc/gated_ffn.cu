@@ -138,7 +138,7 @@ template <int kEpi>
 cudaError_t projections(gemm::PairArgs& g, const void* x, const void* wg, const void* wu,
                         int64_t tokens, int32_t dim, int32_t hidden, int sms,
                         cudaStream_t stream) {
-  const bool narrow = gemm::narrow_tiles(tokens, hidden, sms);
+  const bool narrow = gemm::narrow_gated(tokens, hidden, sms);
   const int32_t features = narrow ? 96 : 128;   // of each projection a tile
   gemm::Problem& p = g.p[0];
   p.m_half = p.m_tiles = (int32_t)((tokens + 255) / 256);
@@ -160,7 +160,7 @@ cudaError_t projections(gemm::PairArgs& g, const void* x, const void* wg, const 
 
 // The same for few tokens (gemm_split.cuh).
 gemm::SplitPlan plan_projections(int64_t tokens, int32_t dim, int32_t hidden, int sms) {
-  return gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64, (dim + 63) / 64, sms);
+  return gemm::plan_split(tokens, ((int64_t)hidden + 63) / 64, (dim + 63) / 64, sms, sms);
 }
 bool split_projections(gemm::SplitArgs& a, const gemm::SplitPlan& plan, const void* x,
                        const void* wg, const void* wu, int32_t act, int64_t tokens, int32_t dim,

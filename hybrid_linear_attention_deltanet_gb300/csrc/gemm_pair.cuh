@@ -7,7 +7,8 @@
 // rows of A and its own 128 of B's 256 rows (TMA, 128-byte swizzle) and the
 // even CTA's one MMA thread multiplies all of it: 32 KB into each SM for
 // 512 tensor cycles, half of what two single-CTA 128 x 256 tiles would fetch.
-// (Gated products take tiles of 192 columns where those fill the pairs better.)
+// (Gated products take tiles of 192 columns, 8-bit ones of 128, where those fill
+// the pairs better.)
 //
 // Roles: warp 0 fetches, warp 1 multiplies (even CTA only), warp 2 owns the
 // tensor memory, warps 4 and up take the accumulators out.  The grid is
@@ -243,17 +244,21 @@ __device__ __forceinline__ void gate_grad(float dh, float G, float U, int act, f
   dU = dh * (silu ? G * s : s);
 }
 
-// kTileN: 256 columns, or 192 (gated), see narrow_tiles.
+// kTileN: 256 columns, or 192 (gated) or 128 (8 bits), see narrow_gated and
+// narrow_fp8.
 template <bool kFp8, int kEpi, int kTileN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs g) {
   constexpr int kStages = Shape<kFp8>::kStages;
-  static_assert(kTileN == 256 || (kTileN == 192 && kEpi >= kGate && !kFp8), "");
+  static_assert(kTileN == 256 || (kTileN == 192 && kEpi >= kGate && !kFp8) ||
+                    (kTileN == 128 && kFp8), "");
+  constexpr int kAccs = kTileN == 128 ? 4 : 2;       // accumulators in tensor memory
+  constexpr uint32_t kAccCols = 512 / kAccs;
   // what arrives in both CTAs for a stage
   constexpr uint32_t kArrive = 2 * (kOperand + kOperand / 256 * kTileN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
-  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs];
   __shared__ uint64_t sc_full[2], sc_empty[2];
   __shared__ uint32_t tmem_base;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -264,9 +269,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&full[i], 1);    // the even CTA's expect_tx (both CTAs' bytes)
       mbar_init(&empty[i], 1);   // a commit
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 2 * kEpiWarps);   // both CTAs' epilogue warps
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&sc_full[i], 2);                 // the two warps that fetch scales
       mbar_init(&sc_empty[i], kEpiWarps);
     }
@@ -310,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const Problem& p = g.p[tl.p];
         const int m0 = tl.m0 + 128 * (int)rank;
         // gated: both CTAs' halves of B are the same features of Wg and Wu
-        const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + 128 * (int)rank;
+        const int n0 = kEpi >= kGate ? tl.n0 / 2 : tl.n0 + kTileN / 2 * (int)rank;
         const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
         const int k_half = p.k_half;
         for (int kb = tl.k0; kb < tl.k1; ++kb) {
@@ -355,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const Tile tl = tile_at<kTileN>(g, t);
         const Problem& p = g.p[tl.p];
         const uint32_t idesc =
-            kFp8 ? idesc_e4m3(256, 256) : idesc_bf16(256, kTileN, p.a_mn, p.b_mn);
+            kFp8 ? idesc_e4m3(256, kTileN) : idesc_bf16(256, kTileN, p.a_mn, p.b_mn);
         // a K-major block advances 32 bytes an instruction inside the swizzled
         // row; one stored by rows advances 16 rows of K (2048 bytes)
         const bool a_mn = !kFp8 && p.a_mn, b_mn = !kFp8 && p.b_mn;
@@ -374,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lead) {
             const uint64_t ad = a0 + (uint64_t)(st * (kStageBytes >> 4));
             const uint64_t bd = b0 + (uint64_t)(st * (kStageBytes >> 4));
-            const uint32_t d = tmem + 256 * buf;
+            const uint32_t d = tmem + kAccCols * buf;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (kFp8) mma_f8_pair(d, ad + i * a_step, bd + i * b_step, idesc, i != 0);
@@ -384,9 +391,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (last) mma_commit_pair(&acc_full[buf]);
           }
           __syncwarp();
-          if (last) {
-            buf ^= 1;
-            if (buf == 0) aph ^= 1u;
+          if (last && ++buf == kAccs) {
+            buf = 0;
+            aph ^= 1u;
           }
           if (++st == kStages) {
             st = 0;
@@ -405,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const Problem& p = g.p[tl.p];
         const int r0 = 64 * (warp - 2) + lane, nb = tl.n0 / 128;
         const float* sb0 = g.sb + (size_t)nb * g.sblocks;
-        const float* sb1 = sb0 + (tl.n0 + 128 < p.N ? g.sblocks : 0);
+        const float* sb1 = sb0 + (kTileN > 128 && tl.n0 + 128 < p.N ? g.sblocks : 0);
         const float* sa[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -455,8 +462,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (lane == 0) mbar_arrive_cluster(free0 + 8 * buf);
     };
     auto advance = [&] {
-      buf ^= 1;
-      if (buf == 0) aph ^= 1u;
+      if (++buf == kAccs) {
+        buf = 0;
+        aph ^= 1u;
+      }
     };
     for (int k = 0, t; ok && (t = tile_of(g, pairs, pair, k)) >= 0; ++k) {
       const Tile tl = tile_at<kTileN>(g, t);
@@ -464,13 +473,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int row0 = tl.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
       const bool live = row < p.M;
       if constexpr (kFp8) {
-        // this thread's 128 columns are one column block of the scales
-        const int n0 = tl.n0 + 128 * part;
-        const float* sc = scales + 128 * part + 32 * q + lane;
+        // this thread's 128 or 64 columns are within one column block of the scales
+        constexpr int kMine = kTileN / 2;
+        const int n0 = tl.n0 + kMine * part;
+        const float* sc = scales + (kMine == 128 ? 128 * part : 0) + 32 * q + lane;
         const int k_blocks = p.k_blocks;
-        F2 acc[64];
+        F2 acc[kMine / 2];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = f2(0.f, 0.f);
+        for (int i = 0; i < kMine / 2; ++i) acc[i] = f2(0.f, 0.f);
         for (int kb = 0; kb < k_blocks; ++kb) {
           const int j = kb % kGroup;
           if (j == 0) {
@@ -481,15 +491,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           ok = mbar_wait_warp(&acc_full[buf], aph, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          // two 32-column pieces in turn: one is added while the next arrives
-          const uint32_t src = tmem + lanes + 256 * buf + 128 * part;
+          // two 32-column pieces in turn: one is added while the next arrives;
+          // all 64 columns of a narrow tile at once
+          const uint32_t src = tmem + lanes + kAccCols * buf + kMine * part;
           uint32_t r[2][32];
           tmem_ld32(src, r[0]);
+          if constexpr (kMine == 64) {
+            tmem_ld32(src + 32, r[1]);
+            tmem_ld_wait_regs(r[1]);
+            release();
+          }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kMine / 32; ++c) {
             tmem_ld_wait_regs(r[c & 1]);
-            if (c < 3) tmem_ld32(src + 32 * (c + 1), r[(c + 1) & 1]);
-            else release();
+            if constexpr (kMine == 128) {
+              if (c < 3) tmem_ld32(src + 32 * (c + 1), r[(c + 1) & 1]);
+              else release();
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               acc[16 * c + i] = f2_fma(f2(__uint_as_float(r[c & 1][2 * i]),
@@ -507,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         using T = typename std::conditional<kEpi == kStoreF32, float, __nv_bfloat16>::type;
         constexpr int kCols = 128 / (int)sizeof(T);   // 64 bf16 or 32 fp32
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < kMine; c += 32) {
           float v[32];
 #pragma unroll
           for (int i = 0; i < 16; ++i) f2_split(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
@@ -718,11 +736,22 @@ inline int32_t group_rows(int64_t pitch) {
 // where that many rounds take less.  (2048 -> 2 x 6144, us with 192 and 256:
 // 256 tokens 14.3 and 15.5, 512 21.0 and 24.0, 4096, where this says 256, 117
 // and 109; 1000 tokens, 1032 -> 2 x 2731: 16.7 and 18.8.)
-inline bool narrow_tiles(int64_t tokens, int32_t features, int sms) {
+inline bool narrow_gated(int64_t tokens, int32_t features, int sms) {
   const int64_t pairs = sms / 2, mt = (tokens + 255) / 256;
   const int64_t wide = mt * (((int64_t)features + 127) / 128);
   const int64_t narrow = mt * (((int64_t)features + 95) / 96);
   return 5 * ((narrow + pairs - 1) / pairs) < 6 * ((wide + pairs - 1) / pairs);
+}
+
+// The same for 128 columns of an 8-bit product, where a round takes 3/5 of the
+// time: 500 to 550 cycles a K block, of them 256 for its products, with four
+// accumulators on their way.  (us with 128 and 256: 2048 -> 4608, 512 tokens 8.0
+// and 10.0, 1280 16.6 and 18.4; 4096 -> 2048, 1024 tokens 11.9 and 15.9;
+// 1024 -> 4608, 300 tokens 5.9 and 7.0; 1552 -> 2005, 3001 tokens 18.7 and 20.1.)
+inline bool narrow_fp8(int64_t mt, int32_t n, int sms) {
+  const int64_t pairs = sms / 2;
+  const int64_t wide = mt * (((int64_t)n + 255) / 256), narrow = mt * (((int64_t)n + 127) / 128);
+  return 3 * ((narrow + pairs - 1) / pairs) < 5 * ((wide + pairs - 1) / pairs);
 }
 
 template <bool kFp8, int kEpi, int kTileN = 256>

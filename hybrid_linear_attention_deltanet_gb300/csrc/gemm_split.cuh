@@ -313,25 +313,27 @@ __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
 // each gets an SM to itself; columns 0: the pair form.
 //
 // Up to 64 tokens are one tile of columns; more take tiles of 64 while those
-// are within one CTA an SM (the pair form's fewer, longer chains of K blocks
-// would leave most SMs idle).  K is split (at least four blocks each) while
-// the CTAs are within one an SM, and each is then kept alone there: else the
-// scheduler puts two on some SMs and none on others.  Tiles that leave no room
-// for a split so take two CTAs an SM if K is long.  (us.  8 bits, pair / split:
-// 2048 -> 4608, 16 tokens 9.0 / 4.0, 128 tokens 9.9 / 6.4, 256 tokens 9.9 / 8.2;
-// 4096 -> 1000, 300 tokens, 16.0 / 6.8, with two CTAs an SM 7.5; 4096 -> 2048, 512
-// tokens, 15.7 / 11.1, alone and not split 13.1, not alone 17.7; 1024 -> 4608,
-// 300 tokens, 180 CTAs, 7.0 / 7.9.  Gated: 2048 -> 6144, 64 tokens 14.2 / 11.2, 128
-// tokens, 192 CTAs, 14.4 / 15.7; 1000 -> 1000, 200 tokens, 10.1 / 6.6.  Clusters of
-// eight CTAs alone on their SMs do not find room side by side: 6.1 against 3.6.)
+// are `most` (the pair form's fewer, longer chains of K blocks would leave most
+// SMs idle): one CTA an SM, of 8 bits half of that, where K can be split.  K is
+// split (at least four blocks each) while the CTAs are within one an SM, and
+// each is then kept alone there: else the scheduler puts two on some SMs and
+// none on others.  Tiles that leave no room for a split so take two CTAs an SM
+// if K is long.  (us, pair / split.  8 bits: 2048 -> 4608, 16 tokens 7.0 / 4.0,
+// 128 tokens 7.1 / 6.4, 192 tokens, 108 tiles, 7.1 / 7.9; 4096 -> 1000, 300
+// tokens, 11.1 / 6.9, with two CTAs an SM 7.5; 4096 -> 2048, 256 tokens 10.8 /
+// 8.2, 512 tokens, 128 tiles, 11.0 / 11.3.  Gated: 2048 -> 6144, 64 tokens 14.0 /
+// 11.2, 128 tokens, 192 tiles, 14.0 / 15.7; 2048 -> 4096, 128 tokens, 128 tiles,
+// 12.0 / 10.8; 1000 -> 1000, 200 tokens, 8.9 / 6.6.  Clusters of eight CTAs alone
+// on their SMs do not find room side by side: 6.1 against 3.6.)
 struct SplitPlan {
   int columns, split;
   bool alone;
 };
-inline SplitPlan plan_split(int64_t tokens, int64_t row_tiles, int k_blocks, int sms) {
+inline SplitPlan plan_split(int64_t tokens, int64_t row_tiles, int k_blocks, int sms,
+                            int most) {
   const int nb = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
   const int64_t units = row_tiles * ((tokens + nb - 1) / nb);
-  if (row_tiles > 65535 || (tokens > 64 && units > sms)) return {0, 0, false};
+  if (row_tiles > 65535 || (tokens > 64 && units > most)) return {0, 0, false};
   const auto split = [&](int64_t ctas) {
     int64_t s = ctas / units;
     if (s > k_blocks / 4) s = k_blocks / 4;

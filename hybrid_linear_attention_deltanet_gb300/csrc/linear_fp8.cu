@@ -36,7 +36,7 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   unsigned* status = status_ptr();
   if (sms < 2 || !status) return GDN_ERR_CUDA;
   const gemm::SplitPlan plan =
-      gemm::plan_split(tokens, ((int64_t)n + 127) / 128, blocks, sms);
+      gemm::plan_split(tokens, ((int64_t)n + 127) / 128, blocks, sms, sms / 2);
   if (plan.columns && (int64_t)((blocks + plan.split - 1) / plan.split) * plan.columns * 4 <=
                           gemm::kSplitScaleBytes) {
     gemm::SplitArgs a;
@@ -61,7 +61,10 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   gemm::PairArgs g;
   memset(&g, 0, sizeof g);
   gemm::Problem& p = g.p[0];
-  const int64_t mt = (tokens + 255) / 256, nt = (n + 255) / 256;
+  const int64_t mt = (tokens + 255) / 256;
+  const bool narrow = gemm::narrow_fp8(mt, n, sms);
+  const int32_t columns = narrow ? 128 : 256;
+  const int64_t nt = ((int64_t)n + columns - 1) / columns;
   if (mt * nt > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
   p.m_half = p.m_tiles = (int32_t)mt;
   p.n_tiles = (int32_t)nt;
@@ -78,13 +81,16 @@ int linear_common(const void* x, const float* sx, const void* w, const float* sw
   g.sblocks = blocks;
   g.status = status;
   if (!gemm::matrix_map(&p.a[0], x, true, k, tokens, k, 128) ||
-      !gemm::matrix_map(&p.b[0], w, true, k, n, k, 128))
+      !gemm::matrix_map(&p.b[0], w, true, k, n, k, columns / 2))
     return GDN_ERR_CUDA;
   p.a[1] = p.a[0];
   p.b[1] = p.b[0];
-  const cudaError_t e = out_dtype == GDN_BF16
-                            ? gemm::launch_pair<true, gemm::kStore>(g, sms, stream)
-                            : gemm::launch_pair<true, gemm::kStoreF32>(g, sms, stream);
+  const auto go = out_dtype == GDN_BF16
+                      ? narrow ? gemm::launch_pair<true, gemm::kStore, 128>
+                               : gemm::launch_pair<true, gemm::kStore, 256>
+                      : narrow ? gemm::launch_pair<true, gemm::kStoreF32, 128>
+                               : gemm::launch_pair<true, gemm::kStoreF32, 256>;
+  const cudaError_t e = go(g, sms, stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -317,6 +317,16 @@ def test_linear_fp8_many_tiles_and_unaligned_rows():
     check_linear(300, 256, 264, F32, 6, misaligned=True)
 
 
+# tiles of 256 and of 128 columns, in one round and in several, rows of the
+# result that start on 16 bytes and that do not
+@pytest.mark.parametrize("tokens,k,n", [
+    (1000, 256, 4608), (1000, 144, 4607), (1500, 400, 2001), (520, 256, 4608), (513, 400, 4095),
+    (3001, 144, 2005), (3001, 640, 2008), (9800, 144, 100), (257, 2048, 4500)])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_linear_fp8_tile_widths(tokens, k, n, out_dtype):
+    check_linear(tokens, k, n, out_dtype, tokens + 3 * k + n)
+
+
 def test_linear_fp8_nan_stays_in_its_row():
     g = gen(9)
     x, sx = gdn.quantize_fp8(randn(g, 20, 512, dtype=BF16))
