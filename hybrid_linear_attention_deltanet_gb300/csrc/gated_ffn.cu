@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
 #pragma unroll 4
     for (int p = 0; p < a.parts[w]; ++p) {
       const float4* f = reinterpret_cast<const float4*>(a.part[w] + p * a.stride[w] + e);
-      const float4 x = __ldg(f), y = __ldg(f + 1);
+      const float4 x = ld_waited(f), y = ld_waited(f + 1);
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }

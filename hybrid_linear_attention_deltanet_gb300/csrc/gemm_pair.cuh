@@ -424,10 +424,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < kGroup; ++j) {
             const int k = kb + j < p.k_blocks ? kb + j : kb;
-            a[0][j] = __ldg(sa[0] + k);
-            a[1][j] = __ldg(sa[1] + k);
-            b[0][j] = __ldg(sb0 + k);
-            b[1][j] = __ldg(sb1 + k);
+            a[0][j] = ld_waited(sa[0] + k);
+            a[1][j] = ld_waited(sa[1] + k);
+            b[0][j] = ld_waited(sb0 + k);
+            b[1][j] = ld_waited(sb1 + k);
           }
           ok = mbar_wait_warp(&sc_empty[slot], ph ^ 1u, kWaitNs);
           if (!ok) break;
@@ -572,7 +572,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint4 w = make_uint4(0, 0, 0, 0);
-              if (live && f0 + 8 * i < p.N && !(half && i >= 4)) w = __ldg(reinterpret_cast<const uint4*>(d) + i);
+              if (live && f0 + 8 * i < p.N && !(half && i >= 4))
+                w = ld_waited(reinterpret_cast<const uint4*>(d) + i);
               dh[4 * i] = w.x; dh[4 * i + 1] = w.y; dh[4 * i + 2] = w.z; dh[4 * i + 3] = w.w;
             }
           } else {           // rows that start anywhere: a row at a time through the staging

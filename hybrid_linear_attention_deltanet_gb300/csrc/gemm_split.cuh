@@ -196,8 +196,9 @@ __global__ void __launch_bounds__(SplitShape<kFp8, kNB>::kThreads, 2)
       for (int e = tid; e < kbs * kNB; e += 32 * S::kEpi) {
         const int c = e / kbs, i = e - c * kbs;   // consecutive threads: one token's blocks
         scales[i * kNB + c] =
-            t0 + c < g.tokens ? __ldg(g.sx + (size_t)(t0 + c) * g.k_blocks + kb0 + i) * __ldg(sw + i)
-                              : 0.f;
+            t0 + c < g.tokens
+                ? ld_waited(g.sx + (size_t)(t0 + c) * g.k_blocks + kb0 + i) * ld_waited(sw + i)
+                : 0.f;
       }
       asm volatile("bar.sync 1, %0;" ::"n"(32 * S::kEpi) : "memory");   // these warps
 #pragma unroll

@@ -53,6 +53,29 @@ inline int sm_count() {
 __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Loads of what the grid before may have written, for after grid_wait().  (This
+// grid is resident while that one writes, so the memory is not read-only for its
+// lifetime: a non-coherent load may return what an SM's L1 still holds of it, and
+// the compiler may move one across the wait.)
+__device__ __forceinline__ float ld_waited(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_waited(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_waited(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 // The next grid may start once every CTA of this one has come here.
 __device__ __forceinline__ void grid_release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
 // dw[c] = sum_b part[b][c]: 32 strided runs, each in order, then the runs in
 // order.  A programmatic dependent of the kernel above (both for 8191 x 4096:
 // 51.7 us against 54.0 launched plainly).
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int n,
-                                                       int dim, float* __restrict__ dw) {
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int n, int dim,
+                                                       float* dw) {
   grid_release_next();
   grid_wait();
   __shared__ float sm[32][33];
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   float t = 0.f;
   if (c < dim)
 #pragma unroll 8
-    for (int b = run; b < n; b += 32) t += part[(size_t)b * dim + c];
+    for (int b = run; b < n; b += 32) t += ld_waited(part + (size_t)b * dim + c);
   sm[run][lane] = t;
   __syncthreads();
   if (run == 0 && c < dim) {
