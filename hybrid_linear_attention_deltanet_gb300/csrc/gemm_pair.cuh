@@ -234,12 +234,16 @@ __device__ __forceinline__ float gate_act(float x, int act) {
   return act == GDN_GATE_SILU ? x * s : s;
 }
 
-// dG = dh U act'(G) and dU = dh act(G).
+// dG = dh U act'(G) and dU = dh act(G).  With e = exp(-|G|) and r = 1 / (1 + e)
+// the sigmoids of G and of -G are r and e r, either way round: 1 - sigmoid(G)
+// taken as a difference has lost a bf16's bits from G = 11 on.
 __device__ __forceinline__ void gate_grad(float dh, float G, float U, int act, float& dG,
                                           float& dU) {
-  const float s = gate_sigmoid(G);
+  const float e = ex2_sfu(__fmul_rn(fabsf(G), kNegLog2e));
+  const float r = rcp_sfu(__fadd_rn(e, 1.f)), er = e * r;
+  const float s = G < 0.f ? er : r, c = G < 0.f ? r : er;
   const bool silu = act == GDN_GATE_SILU;
-  const float slope = silu ? s * fmaf(G, 1.f - s, 1.f) : s * (1.f - s);
+  const float slope = silu ? s * fmaf(G, c, 1.f) : s * c;
   dG = dh * U * slope;
   dU = dh * (silu ? G * s : s);
 }
