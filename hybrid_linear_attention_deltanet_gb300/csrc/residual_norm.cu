@@ -95,6 +95,19 @@ __device__ __forceinline__ void load_w(const float* w, float (&f)[8]) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// x times one factor, or element by element, two at a time (rounded as scalar
+// products are).
+__device__ __forceinline__ void mul8(const float (&x)[8], float c, float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    f2_split(f2_mul(f2(x[i], x[i + 1]), f2(c, c)), y[i], y[i + 1]);
+}
+__device__ __forceinline__ void mul8(const float (&x)[8], const float (&c)[8], float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    f2_split(f2_mul(f2(x[i], x[i + 1]), f2(c[i], c[i + 1])), y[i], y[i + 1]);
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -133,33 +146,51 @@ __device__ __forceinline__ float scale_of(float m) {
   const float q = __fmul_rn(m, r);
   return isinf(q) ? q : __fmaf_rn(__fmaf_rn(-kE4m3Max, q, m), r, q);
 }
-// Is v (an e4m3 value's size, not below its normal range) within 16 units in
-// its last place of the middle between two e4m3 values?  fp32 gets y (448 / m)
-// to about 5, so elsewhere its rounding is that of the real number.  tie_gap is
-// at most 0x20 there.
+// Is v (of an e4m3 value's size) within 16 units in its last place of the middle
+// between two e4m3 values?  fp32 gets y (448 / m) to about 5, so elsewhere its
+// rounding is that of the real number.  tie_gap, of v's low 20 bits, is at most
+// kNearTie there.  Below the normal range, 2^-6, the codes are 2^-9 apart, as they
+// are from 2^-6 to 2^-5: |v| + 2^-6 is looked at in its place, whose units there
+// are 2^-29 and v's errors still less than 5 of them.
+constexpr float kLeastNormal = 0x1p-6f;
+constexpr uint32_t kNearTie = 0x20u << 12;
 __device__ __forceinline__ uint32_t tie_gap(float v) {
-  return (__float_as_uint(v) - 0x7fff0u) & 0xfffffu;
+  return __float_as_uint(v) * 4096u - (0x7fff0u << 12);
 }
-__device__ __forceinline__ bool near_tie(float v) { return tie_gap(v) <= 0x20u; }
+__device__ __forceinline__ float on_normal_grid(float v) {
+  const float a = fabsf(v);
+  return a < kLeastNormal ? a + kLeastNormal : a;
+}
+__device__ __forceinline__ bool near_tie(float v) { return tie_gap(on_normal_grid(v)) <= kNearTie; }
 __device__ __forceinline__ bool any_near_tie(const float (&v)[8]) {
   uint32_t g = tie_gap(v[0]);
+  float least = fabsf(v[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) g = min(g, tie_gap(v[i]));
-  return g <= 0x20u;
+  for (int i = 1; i < 8; ++i) {
+    g = min(g, tie_gap(v[i]));
+    least = fminf(least, fabsf(v[i]));
+  }
+  if (least < kLeastNormal) {   // few have one
+    g = tie_gap(on_normal_grid(v[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) g = min(g, tie_gap(on_normal_grid(v[i])));
+  }
+  return g <= kNearTie;
 }
 // v, which is near the tie t, moved to where 448 p / m lies: on t or beside it.
 // p = ph + pl and m = mh + ml, magnitudes; t has 5 significant bits.  The
 // products' rounding errors are exact in fp32 (fma), and the leading parts
 // nearly cancel, so the sign of the difference is right.
 __device__ __forceinline__ float settle_tie(float v, float ph, float pl, float mh, float ml) {
-  const uint32_t bits = __float_as_uint(v);
-  const uint32_t tie = (bits & ~0xfffffu) | 0x80000u;   // with v's sign
-  const float t = fabsf(__uint_as_float(tie));
+  const uint32_t tie_z = (__float_as_uint(on_normal_grid(v)) & ~0xfffffu) | 0x80000u;
+  const float z = __uint_as_float(tie_z);
+  const float t = fabsf(v) < kLeastNormal ? z - kLeastNormal : z;
   const float a = __fmul_rn(kE4m3Max, ph), b = __fmul_rn(t, mh);
   const float ae = __fmaf_rn(kE4m3Max, ph, -a), be = __fmaf_rn(t, mh, -b);
   const float low = __fmaf_rn(kE4m3Max, pl, -__fmul_rn(t, ml));
   const float d = __fadd_rn(__fadd_rn(a, -b), __fadd_rn(__fadd_rn(ae, -be), low));
-  return __uint_as_float(d > 0.f ? tie + 1 : d < 0.f ? tie - 1 : tie);
+  const uint32_t tie = __float_as_uint(t);   // at least 2^-10
+  return copysignf(__uint_as_float(d > 0.f ? tie + 1 : d < 0.f ? tie - 1 : tie), v);
 }
 
 // Sum over the kWPR warps that share a row; every thread of the CTA calls it.
@@ -231,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
       s[j].widen(f);
       r[j].widen(g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] += g[i];
+      for (int i = 0; i < 8; i += 2)
+        f2_split(f2_add(f2(f[i], f[i + 1]), f2(g[i], g[i + 1])), f[i], f[i + 1]);
       s[j].round(f);
     }
   }
@@ -255,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
     if (in) {
       s[j].widen(f);
       if (!kEarlyW) load_w(a.w + c, wj);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * rs * wj[i];
+      mul8(f, rs, f);
+      mul8(f, wj, f);
     }
     if (!kFp8) {
       if (in) {
@@ -271,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
       m = max_nan(m, kTiny);
       const float inv = codes_per(m);
       float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(f[i], inv);
+      mul8(f, inv, v);
       if (__any_sync(0xffffffffu, any_near_tie(v) && m > kTiny)) {
         // (one in 120 of these) the root cancels in y / m: the codes are those
         // of 448 s_j w_j / max |s w|, a product being hi + lo exactly
