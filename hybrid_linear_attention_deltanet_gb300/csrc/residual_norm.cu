@@ -179,15 +179,17 @@ __device__ __forceinline__ bool any_near_tie(const float (&v)[8]) {
 }
 // v, which is near the tie t, moved to where 448 p / m lies: on t or beside it.
 // p = ph + pl and m = mh + ml, magnitudes; t has 5 significant bits.  The
-// products' rounding errors are exact in fp32 (fma), and the leading parts
-// nearly cancel, so the sign of the difference is right.
+// products (of 448 / 512 and t / 512, which overflow for no p and m) have
+// rounding errors that are exact in fp32 (fma), and the leading parts nearly
+// cancel, so the sign of the difference is right.
 __device__ __forceinline__ float settle_tie(float v, float ph, float pl, float mh, float ml) {
+  constexpr float k448 = kE4m3Max * 0x1p-9f;
   const uint32_t tie_z = (__float_as_uint(on_normal_grid(v)) & ~0xfffffu) | 0x80000u;
   const float z = __uint_as_float(tie_z);
-  const float t = fabsf(v) < kLeastNormal ? z - kLeastNormal : z;
-  const float a = __fmul_rn(kE4m3Max, ph), b = __fmul_rn(t, mh);
-  const float ae = __fmaf_rn(kE4m3Max, ph, -a), be = __fmaf_rn(t, mh, -b);
-  const float low = __fmaf_rn(kE4m3Max, pl, -__fmul_rn(t, ml));
+  const float t = fabsf(v) < kLeastNormal ? z - kLeastNormal : z, ts = t * 0x1p-9f;
+  const float a = __fmul_rn(k448, ph), b = __fmul_rn(ts, mh);
+  const float ae = __fmaf_rn(k448, ph, -a), be = __fmaf_rn(ts, mh, -b);
+  const float low = __fmaf_rn(k448, pl, -__fmul_rn(ts, ml));
   const float d = __fadd_rn(__fadd_rn(a, -b), __fadd_rn(__fadd_rn(ae, -be), low));
   const uint32_t tie = __float_as_uint(t);   // at least 2^-10
   return copysignf(__uint_as_float(d > 0.f ? tie + 1 : d < 0.f ? tie - 1 : tie), v);

@@ -1,6 +1,6 @@
 """Values of the layer operators where fp32 arithmetic loses what the result
 still shows: the gate's slope far out, and 8-bit codes on and beside the middle
-between two codes below e4m3's normal range.
+between two codes below e4m3's normal range and near fp32's largest numbers.
 
 Tolerances, from the arithmetic.  A one-hot row of x makes G, U and every
 product behind them exact, so a weight gradient is the rounding of dG or dU to
@@ -90,6 +90,12 @@ def check_codes_about_middles(io, block_rows, exponent):
 @pytest.mark.parametrize("exponent", [0, -100])
 def test_quantised_codes_on_and_beside_the_middles(io, block_rows, exponent):
     check_codes_about_middles(io, block_rows, exponent)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantised_codes_near_the_largest_numbers(block_rows):
+    """448 x passes fp32's largest number here: block maxima to 1.8e6 2^107."""
+    check_codes_about_middles(F32, block_rows, 107)
 
 
 @pytest.mark.parametrize("io", [BF16, F32])
