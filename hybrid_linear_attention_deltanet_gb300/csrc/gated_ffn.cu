@@ -124,7 +124,9 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
 
 int shape_check(int64_t tokens, int32_t dim, int32_t hidden, int32_t act, int32_t io) {
   if (tokens < 0 || dim < 1 || hidden < 1) return GDN_ERR_INVALID_ARG;
-  if (io != GDN_BF16 || dim % 8 || tokens > 0x7fffff00LL || hidden > 0x7fffff00 ||
+  // (a tile of the projections has two columns for each feature)
+  if (io != GDN_BF16 || dim % 8 || tokens > kLongestAxis || dim > kLongestAxis ||
+      hidden > kLongestAxis / 2 ||
       (act != GDN_GATE_SILU && act != GDN_GATE_SIGMOID))
     return GDN_ERR_UNSUPPORTED;
   const int64_t mt = (tokens + 255) / 256, ft = (hidden + 127) / 128, dt = (dim + 255) / 256;

@@ -8,6 +8,9 @@
 namespace gdn {
 namespace hostcheck {
 
+// The longest axis that 32-bit coordinates of tiles up to 256 wide hold.
+constexpr int32_t kLongestAxis = 0x7fffff00;
+
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 struct Span {

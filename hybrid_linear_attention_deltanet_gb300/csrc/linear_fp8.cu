@@ -17,8 +17,8 @@ using namespace hostcheck;
 int linear_common(const void* x, const float* sx, const void* w, const float* sw, void* out,
                   int64_t tokens, int32_t k, int32_t n, int32_t out_dtype, cudaStream_t stream) {
   if (tokens < 0 || k < 1 || n < 1) return GDN_ERR_INVALID_ARG;
-  if (k % 16 || (out_dtype != GDN_BF16 && out_dtype != GDN_F32) || tokens > 0x7fffff00LL ||
-      n > 0x7fffff00)
+  if (k % 16 || (out_dtype != GDN_BF16 && out_dtype != GDN_F32) || tokens > kLongestAxis ||
+      k > kLongestAxis || n > kLongestAxis)
     return GDN_ERR_UNSUPPORTED;
   if (tokens == 0) return GDN_OK;
   if (!x || !sx || !w || !sw || !out) return GDN_ERR_INVALID_ARG;

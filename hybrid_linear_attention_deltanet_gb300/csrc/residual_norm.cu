@@ -816,7 +816,8 @@ int gdn_quantize_fp8(const void* x, void* q, float* scale, int64_t rows, int32_t
                      int32_t block_rows, int32_t io_dtype, gdn_stream_t stream_) {
   cudaStream_t stream = (cudaStream_t)stream_;
   if (rows < 0 || cols < 1) return GDN_ERR_INVALID_ARG;
-  if (!io_ok(io_dtype) || cols % 8 || (block_rows != 1 && block_rows != 128))
+  if (!io_ok(io_dtype) || cols % 8 || cols > kLongestAxis ||
+      (block_rows != 1 && block_rows != 128))
     return GDN_ERR_UNSUPPORTED;
   if (rows == 0) return GDN_OK;
   if (!x || !q || !scale) return GDN_ERR_INVALID_ARG;

@@ -461,6 +461,7 @@ int gdn_prefill_layer(const void* qkv, const float* conv_w, const float* a_raw, 
  * `tokens` counts rows whatever batch shape they come from, and 0 tokens is a
  * call that writes nothing (the gradients of weights are then zero).  8-bit
  * values are e4m3 (float8_e4m3fn: 448 largest, no infinity), one byte each.
+ * Axes longer than 0x7fffff00 (hidden: 0x3fffff80) are GDN_ERR_UNSUPPORTED.
  */
 
 /*
