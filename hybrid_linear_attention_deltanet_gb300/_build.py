@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -28,16 +29,22 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _no_binding(out, why) -> None:
+    """The binding is left out, and no older one stays in its place."""
+    if os.path.exists(out):
+        os.remove(out)
+    warnings.warn(f"_layer_calls.so is not built, calls go through ctypes: {why}", RuntimeWarning)
+
+
 def build_binding() -> str | None:
     """Compile csrc/binding.cpp into _layer_calls.so with the host compiler
-    (None where Python's headers are not installed: the binding in Python then
-    makes every call itself)."""
+    (None, with a warning, where that fails, as it does without Python's
+    headers: the binding in Python then makes every call itself)."""
     import torch
     src = os.path.join(CSRC, "binding.cpp")
     out = os.path.join(HERE, "_layer_calls.so")
     if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
-        print("_layer_calls.so not built: Python.h is missing")
-        return None
+        return _no_binding(out, "Python.h is missing")
     newest = max(os.path.getmtime(p) for p in
                  [src, torch.__file__] + glob.glob(os.path.join(INCLUDE, "*.h")))
     if os.path.exists(out) and os.path.getmtime(out) >= newest:
@@ -50,9 +57,12 @@ def build_binding() -> str | None:
            "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(cuda, "include"), src, "-o", out + ".tmp", "-L", libs,
            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return _no_binding(out, str(e))
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+        return _no_binding(out, f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(out + ".tmp", out)
     return out
 
