@@ -520,7 +520,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
     const float inv = codes_per(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inv);
-    if (any_near_tie(v) && m > kTiny) {
+    if (any_near_tie(v)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);

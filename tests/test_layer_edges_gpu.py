@@ -98,6 +98,19 @@ def test_quantised_codes_near_the_largest_numbers(block_rows):
     check_codes_about_middles(F32, block_rows, 107)
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantised_codes_below_the_least_maximum(block_rows):
+    """Blocks whose maximum is below 2^-100 take that in its place: 448 x 2^100 is
+    beside a middle (7 divides no power of two)."""
+    g = gen(block_rows + 300)
+    x = (middles(g, (512, 1024)) * 2.0 ** -106 / 7).float()
+    way = torch.randint(-1, 2, x.shape, generator=g, device=DEV)
+    x = torch.where(way == 0, x, torch.nextafter(x, torch.where(way > 0, 1.0, -1.0)))
+    q, scale = gdn.quantize_fp8(x, block_rows=block_rows)
+    assert bool((scale == torch.tensor(2.0 ** -100, device=DEV) / 448).all())
+    assert torch.equal(q.double(), e4m3_of(448 * x.double() * 2.0 ** 100))
+
+
 @pytest.mark.parametrize("io", [BF16, F32])
 @pytest.mark.parametrize("rows", [2048, 300, 1])
 def test_norm_codes_below_the_normal_range(io, rows):
