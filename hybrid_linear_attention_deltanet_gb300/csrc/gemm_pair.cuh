@@ -22,7 +22,7 @@
 // fp32 registers a thread while the next block is multiplied.
 //
 // What it measured (GB300).  bf16: 8192 x 2048 against 2 x 6144 rows keeps the
-// tensor pipe 90 % busy (206 us cold); 32768 rows run 890 us at 1.85 PFLOP/s,
+// tensor pipe 88 % busy (209 us cold); 32768 rows run 890 us at 1.85 PFLOP/s,
 // and over seconds 955 us at the 1400 W limit with the SMs at 1.5 GHz, the rate
 // of a plain library product there.  8 bits: 32768 x 2048 against 4608 rows
 // 233 us, 2.65 PFLOP/s, tensor pipe 50 % busy (900 cycles a K block; 254 us over
@@ -192,7 +192,10 @@ __device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c0, const 
   }
 }
 // The staged 32 rows to their place, what lies past the edges of the output
-// left out.  stage_free() must return before the next stage_put.
+// left out.  stage_free() must return before the next stage_put.  Rows that do
+// not start on 16 bytes leave by single stores (32768 tokens, us, beside a width
+// that starts on them: 8-bit product, 2048 -> 4609 301 and 4616 251; gated, 2048 ->
+// 2 x 6145 930 and 6152 912).
 template <typename T, int kRow = 128>
 __device__ __forceinline__ void stage_out(const uint8_t* buf, int lane, const Problem& p, int half,
                                           int row0, int n0, int shift = 0) {

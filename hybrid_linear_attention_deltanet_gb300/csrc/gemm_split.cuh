@@ -13,7 +13,8 @@
 // one multiplies.  8-bit operands: every K block of 128 is an accumulator of
 // its own, scaled (a token's scale times the weight block's) into fp32
 // registers; with 32 columns or more that takes 8 warps, half the columns
-// each (256 tokens, 2048 -> 4608: 8.5 us, 10.3 with 4).
+// each (64 tokens, 2048 -> 4608: 5.4 us, 5.9 with 4; 256 tokens, 4096 -> 2048: 8.6
+// and 9.6).
 // Waits are bounded as in gemm_pair.cuh.
 //
 // Bound by HBM, then by the launch's own chain.  One token against 2 x 6144 x

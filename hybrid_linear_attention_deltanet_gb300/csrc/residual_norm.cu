@@ -13,9 +13,10 @@
 // flight before its first use and the 16 lanes of a half warp hold one
 // 128-column block: a block's largest magnitude is four shuffles.
 //
-// Measured (bf16): 32768 x 2048 with residual and 8-bit output 78 us, 6.0 TB/s
-// of a copy's 6.7; the gradient of 8191 x 4096 48.6 us, 5.5 TB/s; one token 1.8 us
-// on the GPU.
+// Measured (bf16): 32768 x 2048 with residual and 8-bit output 82 us, 5.7 TB/s
+// of a copy's 6.7 (88 us with weights that are bf16 numbers, 109 with weights of 1:
+// the more values lie on the middle between two codes, the more are settled); the
+// gradient of 8191 x 4096 51.8 us, 5.2 TB/s; one token 1.8 us on the GPU.
 #include <cuda_fp8.h>
 
 #include "gdn_internal.cuh"
@@ -139,7 +140,9 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
 }
 // 448 / m to a few units in the last place (scaled, so that no m from 2^-100 up
 // has a subnormal reciprocal), and m / 448 rounded to nearest: the product with
-// the rounded reciprocal, corrected by its exact remainder.
+// the rounded reciprocal, corrected by its exact remainder (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Dev. 34, 1990).
 __device__ __forceinline__ float codes_per(float m) { return 1.75f * rcp_sfu(m * 0x1p-8f); }
 __device__ __forceinline__ float scale_of(float m) {
   constexpr float r = 1.f / kE4m3Max;
@@ -351,8 +354,7 @@ struct NormBwdArgs {
 // cluster, whose CTAs add their parts through each other's shared memory, in
 // order, into dw (few rows: one launch and no scratch).  Rows in flight are what
 // it lives from: two vectors a lane leave registers for four CTAs an SM
-// (8191 rows of 4096 bf16: 49.8 us; 54.5 us with four vectors and two CTAs,
-// 60.8 us with two CTAs that fetch a row ahead).
+// (8191 rows of 4096 bf16: 51.9 us, 57.4 with four vectors and two CTAs).
 template <typename T, int kVPL, int kWPR, bool kCluster>
 __global__ void __launch_bounds__(kThreads, backward_ctas(kVPL, sizeof(T)))
     norm_backward_kernel(NormBwdArgs a) {
@@ -506,7 +508,7 @@ template <typename T>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
   float v[8];
   if constexpr (sizeof(T) == 2) {
-    // bf16: 0.875 x is exact, so one step with the quotient's exact remainder
+    // bf16: 0.875 x is exact, so one step with the quotient's exact remainder (scale_of's)
     // gives the rounded quotient, and the quotient itself where it has few
     // bits, as the middle between two codes does (no other is so near one that
     // fp32 rounds to it: it is apart by 2^-13 at least)
@@ -613,10 +615,9 @@ struct Lay {
 };
 // The fewest warps that hold a row with at most two vectors a lane, from 4096
 // columns eight warps with more.  Forward: three vectors where a third of the
-// lanes would idle otherwise (2560 columns: 94 against 108 us for 67 M
-// elements; the gradient is the faster without, 55.7 against 64.3 us for 34 M:
-// its three vectors leave registers for three CTAs an SM instead of four), and
-// eight warps a row where there are fewer rows than warps to run them.
+// lanes would idle otherwise (2560 columns: 92 against 109 us for 67 M
+// elements; the gradient takes 57.3 us for 34 M either way), and eight warps a
+// row where there are fewer rows than warps to run them.
 template <bool kForward, typename F>
 void with_layout(int dim, int64_t rows, F&& f) {
   const int v = (dim + 255) / 256;   // vectors a lane of one warp would hold
