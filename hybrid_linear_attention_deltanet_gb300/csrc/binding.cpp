@@ -1,7 +1,7 @@
 // The layer operators' calls from Python for the ordinary case: tensors in,
 // new tensors out, on the current stream.  A decoding step makes these calls
 // for single tokens, where the interpreter's checks and allocations took
-// longer than the kernels (8-bit norm of one token: 14.8 us a call through
+// longer than the kernels (8-bit norm of one token: 17.7 us a call through
 // ctypes).  Each function checks its arguments, allocates the outputs and
 // calls the C ABI; where anything is not as it expects (another type, shape,
 // stride or device, a refusal by the library) it returns None and has done

@@ -22,7 +22,7 @@
 // fp32 registers a thread while the next block is multiplied.
 //
 // What it measured (GB300).  bf16: 8192 x 2048 against 2 x 6144 rows keeps the
-// tensor pipe 88 % busy (209 us cold); 32768 rows run 890 us at 1.85 PFLOP/s,
+// tensor pipe 90 % busy (208 us cold); 32768 rows run 890 us at 1.85 PFLOP/s,
 // and over seconds 955 us at the 1400 W limit with the SMs at 1.5 GHz, the rate
 // of a plain library product there.  8 bits: 32768 x 2048 against 4608 rows
 // 233 us, 2.65 PFLOP/s, tensor pipe 50 % busy (900 cycles a K block; 254 us over

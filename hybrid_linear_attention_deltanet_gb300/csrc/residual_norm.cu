@@ -13,8 +13,8 @@
 // flight before its first use and the 16 lanes of a half warp hold one
 // 128-column block: a block's largest magnitude is four shuffles.
 //
-// Measured (bf16): 32768 x 2048 with residual and 8-bit output 82 us, 5.7 TB/s
-// of a copy's 6.7 (88 us with weights that are bf16 numbers, 109 with weights of 1:
+// Measured (bf16): 32768 x 2048 with residual and 8-bit output 80 us, 5.9 TB/s
+// of a copy's 6.7 (86 us with weights that are bf16 numbers, 105 with weights of 1:
 // the more values lie on the middle between two codes, the more are settled); the
 // gradient of 8191 x 4096 51.8 us, 5.2 TB/s; one token 1.8 us on the GPU.
 #include <cuda_fp8.h>
@@ -162,22 +162,29 @@ __device__ __forceinline__ uint32_t tie_gap(float v) {
 }
 __device__ __forceinline__ float on_normal_grid(float v) {
   const float a = fabsf(v);
-  return a < kLeastNormal ? a + kLeastNormal : a;
+  float below;   // 1 or 0: one instruction, and one more with the product
+  asm("set.lt.f32.f32 %0, %1, %2;" : "=f"(below) : "f"(a), "f"(kLeastNormal));
+  return __fmaf_rn(below, kLeastNormal, a);
 }
 __device__ __forceinline__ bool near_tie(float v) { return tie_gap(on_normal_grid(v)) <= kNearTie; }
+// kSmallest: the smallest value tells first whether any is below the normal range
+// (32768 x 2048: the fp32 quantisation 54.6 us, 59.1 without; the norm 81.9, 80.1
+// without).
+template <bool kSmallest>
 __device__ __forceinline__ bool any_near_tie(const float (&v)[8]) {
-  uint32_t g = tie_gap(v[0]);
-  float least = fabsf(v[0]);
+  uint32_t g = 0xffffffffu;
+  if constexpr (kSmallest) {
+    float least = fabsf(v[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    g = min(g, tie_gap(v[i]));
-    least = fminf(least, fabsf(v[i]));
+    for (int i = 0; i < 8; ++i) {
+      g = min(g, tie_gap(v[i]));
+      least = fminf(least, fabsf(v[i]));
+    }
+    if (least >= kLeastNormal) return g <= kNearTie;
+    g = 0xffffffffu;
   }
-  if (least < kLeastNormal) {   // few have one
-    g = tie_gap(on_normal_grid(v[0]));
 #pragma unroll
-    for (int i = 1; i < 8; ++i) g = min(g, tie_gap(on_normal_grid(v[i])));
-  }
+  for (int i = 0; i < 8; ++i) g = min(g, tie_gap(on_normal_grid(v[i])));
   return g <= kNearTie;
 }
 // v, which is near the tie t, moved to where 448 p / m lies: on t or beside it.
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, forward_ctas(kVPL)) residual_norm_ke
       const float inv = codes_per(m);
       float v[8];
       mul8(f, inv, v);
-      if (__any_sync(0xffffffffu, any_near_tie(v) && m > kTiny)) {
+      if (__any_sync(0xffffffffu, any_near_tie<false>(v) && m > kTiny)) {
         // (one in 120 of these) the root cancels in y / m: the codes are those
         // of 448 s_j w_j / max |s w|, a product being hi + lo exactly
         float fs[8], mh = 0.f, ml = 0.f;
@@ -522,7 +529,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
     const float inv = codes_per(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inv);
-    if (any_near_tie(v)) {
+    if (any_near_tie<true>(v)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);
@@ -615,7 +622,7 @@ struct Lay {
 };
 // The fewest warps that hold a row with at most two vectors a lane, from 4096
 // columns eight warps with more.  Forward: three vectors where a third of the
-// lanes would idle otherwise (2560 columns: 92 against 109 us for 67 M
+// lanes would idle otherwise (2560 columns: 91 against 109 us for 67 M
 // elements; the gradient takes 57.3 us for 34 M either way), and eight warps a
 // row where there are fewer rows than warps to run them.
 template <bool kForward, typename F>
