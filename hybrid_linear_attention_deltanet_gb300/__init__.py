@@ -16,6 +16,9 @@ raise when the compiled library is missing.
     q, scale, s = residual_norm_fp8(x, w, residual)      # the layer around the mixer:
     out = linear_fp8(q, scale, wq, w_scale)              # 8-bit projections,
     h = gated_ffn(x, w_gate, w_up)                       # gated feed-forward
+    cache = kv_cache(layers, pages, kv_heads, rows, max_pages)   # a hybrid's attention layers:
+    start = cache_reserve(cache, counts); cache_append(cache, k, v, start, layer=i)
+    out = attention_decode_step(q, cache, layer=i)
 
 Recurrence (Appendix A.3, Eq. 16-19 of "Long-Context Aware Upcycling"):
 S_t = alpha_t S_{t-1}(I - beta_t k_t k_t^T) + beta_t v_t k_t^T,
@@ -34,9 +37,10 @@ LIB_NAME = "libgdn_gb300.so"
 _lib = None
 _direct = None   # csrc/binding.cpp's module, once the library is loaded
 
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_E4M3 = 0, 1, 2
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "alignment",
-           4: "CUDA error", 5: "device timeout", 6: "malformed cu_seqlens"}
+           4: "CUDA error", 5: "device timeout", 6: "malformed cu_seqlens",
+           8: "no page of the attention cache left", 9: "outside the attention cache"}
 
 
 class GDNError(RuntimeError):
@@ -129,6 +133,22 @@ def load():
     lib.gdn_gated_ffn_backward_ws.argtypes = [vp] * 4 + [i32, vp, vp, vp, i64, i32, i32, i32, vp,
                                                          sz, vp]
     lib.gdn_gated_ffn_backward_ws.restype = ctypes.c_int
+    lib.gdn_attention_decode_step.argtypes = [vp, vp, i32, i32, f32, vp, vp]
+    lib.gdn_attention_decode_step.restype = ctypes.c_int
+    lib.gdn_attention_decode_step_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.gdn_attention_decode_step_workspace_size.restype = sz
+    lib.gdn_attention_decode_step_ws.argtypes = [vp, vp, i32, i32, f32, vp, vp, sz, vp]
+    lib.gdn_attention_decode_step_ws.restype = ctypes.c_int
+    lib.gdn_cache_reserve.argtypes = [vp] * 4
+    lib.gdn_cache_reserve.restype = ctypes.c_int
+    lib.gdn_cache_append.argtypes = [vp, i32, vp, vp, vp, vp, i64, i64, i64, vp]
+    lib.gdn_cache_append.restype = ctypes.c_int
+    lib.gdn_cache_free.argtypes = [vp, vp, i32, vp]
+    lib.gdn_cache_free.restype = ctypes.c_int
+    lib.gdn_cache_fork.argtypes = [vp, vp, vp, i32, vp]
+    lib.gdn_cache_fork.restype = ctypes.c_int
+    lib.gdn_cache_compact.argtypes = [vp, vp, vp]
+    lib.gdn_cache_compact.restype = ctypes.c_int
     lib.gdn_release_scratch.restype = ctypes.c_int
     lib.gdn_testing_scratch_reserved.argtypes = [vp]
     lib.gdn_testing_scratch_reserved.restype = ctypes.c_int
@@ -924,6 +944,205 @@ def gated_ffn_backward(x, w_gate, w_up, dh, act="silu", stream=None, workspace=N
     else:
         _call("gdn_gated_ffn_backward_ws", index, stream, *args, *_ws(workspace))
     return g
+
+
+# ---------------------------------------------------------------------------
+# The attention layers that a hybrid keeps among its Gated DeltaNet layers, and
+# the paged cache that they share.
+def _token_rows(t, name, index):
+    """(heads, d, elements from one token to the next) of bf16 t [.., T, heads, d],
+    whose tokens may be rows of a wider tensor (a slice of a packed projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bf16")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on another device")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [B, T, heads, d] or [T, heads, d]")
+    heads, d = t.shape[-2:]
+    step = heads * d
+    if t.numel() == 0:
+        return heads, d, step
+    batch, tokens = (t.shape[0] if t.dim() == 4 else 1), t.shape[-3]
+    if tokens > 1:
+        step = t.stride(-3)
+    elif batch > 1:
+        step = t.stride(0)
+    if ((d > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != d) or step < heads * d
+            or (batch > 1 and tokens > 1 and t.stride(0) != tokens * step)):
+        raise ValueError(f"{name}'s heads must be contiguous and its tokens evenly spaced")
+    return heads, d, step
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table", "lengths",
+                                               "refs")] + \
+               [(n, ctypes.c_int32) for n in ("layers", "pages", "kv_heads", "page", "d", "rows",
+                                              "max_pages", "dtype")]
+
+
+class KVCache:
+    """A paged cache of keys and values (``gdn_kv_cache``) over the caller's
+    tensors: k and v [layers, pages, kv_heads, page, d] bf16, or float8_e4m3fn
+    with k_scale and v_scale [layers, pages, kv_heads, page] fp32; table
+    [rows, max_pages], lengths [rows] and refs [pages] int32.  The tensors are
+    its attributes and do not change; their contents are the cache.  (A new,
+    empty one: :func:`kv_cache`.)"""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lengths", "refs", "index", "struct",
+                 "address")
+
+    def __init__(self, k, v, table, lengths, refs, k_scale=None, v_scale=None):
+        if not isinstance(k, torch.Tensor) or k.dim() != 5:
+            raise ValueError("k must be [layers, pages, kv_heads, page, d]")
+        if k.dtype not in (torch.bfloat16, FP8):
+            raise TypeError("a cache holds bf16 or float8_e4m3fn")
+        layers, pages, kv_heads, page, d = k.shape
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be [rows, max_pages]")
+        rows, max_pages = table.shape
+        index, eight = k.get_device(), k.dtype == FP8
+        if (k_scale is not None) != eight or (v_scale is not None) != eight:
+            raise ValueError("k_scale and v_scale go with an 8-bit cache")
+        shapes = dict(k=k.shape, v=k.shape, table=(rows, max_pages), lengths=(rows,),
+                      refs=(pages,), k_scale=k.shape[:-1], v_scale=k.shape[:-1])
+        given = dict(k=k, v=v, table=table, lengths=lengths, refs=refs, k_scale=k_scale,
+                     v_scale=v_scale)
+        c = _CacheStruct(layers=layers, pages=pages, kv_heads=kv_heads, page=page, d=d, rows=rows,
+                         max_pages=max_pages, dtype=GDN_E4M3 if eight else GDN_BF16)
+        for name, t in given.items():
+            if t is not None:
+                io = (k.dtype if name in ("k", "v") else
+                      torch.float32 if name.endswith("scale") else torch.int32)
+                _out(t, name, shapes[name], io, index)
+                setattr(c, name, t.data_ptr())
+            object.__setattr__(self, name, t)
+        object.__setattr__(self, "index", index)
+        object.__setattr__(self, "struct", c)
+        object.__setattr__(self, "address", ctypes.addressof(c))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a KVCache's tensors are fixed")
+
+
+def kv_cache(layers, pages, kv_heads, rows, max_pages, page=64, d=128, dtype=torch.bfloat16,
+             device="cuda") -> KVCache:
+    """A new, empty paged cache for ``rows`` sequences of up to ``max_pages``
+    pages of ``page`` tokens each, out of a pool of ``pages``, shared by
+    ``layers`` layers; dtype bf16 or float8_e4m3fn."""
+    new = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device=device)  # noqa: E731
+    if dtype not in (torch.bfloat16, FP8):
+        raise TypeError("a cache holds bf16 or float8_e4m3fn")
+    shape = (layers, pages, kv_heads, page, d)
+    pool = lambda: (new(*shape, t=torch.uint8).view(FP8) if dtype == FP8 else  # noqa: E731
+                    new(*shape, t=dtype))
+    scale = lambda: new(*shape[:-1], t=torch.float32) if dtype == FP8 else None  # noqa: E731
+    return KVCache(pool(), pool(), new(rows, max_pages).fill_(-1), new(rows), new(pages), scale(),
+                   scale())
+
+
+def _cache(cache):
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    return cache.index, cache.address
+
+
+def _row_numbers(t, name, index):
+    _need(t, name, torch.int32, index)
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be a vector of row numbers")
+    return t.shape[0]
+
+
+def cache_reserve(cache, counts, start=None, stream=None):
+    """Places for counts [rows] new tokens of every row (``gdn_cache_reserve``):
+    takes pages, advances the lengths, and returns start [rows] int32, each
+    row's first new position (-1 where the pool or the row's table had no
+    room; :func:`device_status` then says so)."""
+    index, at = _cache(cache)
+    _out(counts, "counts", cache.lengths.shape, torch.int32, index)
+    start = (torch.empty_like(counts) if start is None else
+             _out(start, "start", counts.shape, torch.int32, index))
+    _call("gdn_cache_reserve", index, stream, at, counts.data_ptr(), start.data_ptr())
+    return start
+
+
+def cache_append(cache, k, v, start, cu_seqlens=None, layer=0, stream=None):
+    """Writes one layer's new keys and values [tokens, kv_heads, d] (bf16; rows
+    of a wider tensor allowed) to the places that :func:`cache_reserve` gave
+    (``gdn_cache_append``): one token a row, or row r's tokens
+    cu_seqlens[r] .. cu_seqlens[r + 1]."""
+    index, at = _cache(cache)
+    heads, d, ks = _token_rows(k, "k", index)
+    _, _, vs = _token_rows(v, "v", index)
+    if k.dim() != 3 or k.shape != v.shape or (heads, d) != (cache.k.shape[2], cache.k.shape[4]):
+        raise ValueError(f"k and v must be [tokens, {cache.k.shape[2]}, {cache.k.shape[4]}]")
+    rows = cache.lengths.shape[0]
+    _out(start, "start", (rows,), torch.int32, index)
+    if cu_seqlens is not None:
+        _out(cu_seqlens, "cu_seqlens", (rows + 1,), torch.int32, index)
+    elif k.shape[0] != rows:
+        raise ValueError(f"k and v must have a token for each of the {rows} rows (or cu_seqlens)")
+    _call("gdn_cache_append", index, stream, at, layer, k.data_ptr(), v.data_ptr(),
+          start.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), k.shape[0], ks, vs)
+
+
+def cache_free(cache, rows, stream=None):
+    """Empties the named rows (int32) and gives their pages back
+    (``gdn_cache_free``)."""
+    index, at = _cache(cache)
+    n = _row_numbers(rows, "rows", index)
+    _call("gdn_cache_free", index, stream, at, rows.data_ptr(), n)
+
+
+def cache_fork(cache, src, dst, stream=None):
+    """The empty rows dst [n] (int32) become copies of rows src [n]
+    (``gdn_cache_fork``): full pages are shared, a last page that is not full is
+    copied, in all layers."""
+    index, at = _cache(cache)
+    n = _row_numbers(src, "src", index)
+    if _row_numbers(dst, "dst", index) != n:
+        raise ValueError("src and dst must name as many rows")
+    _call("gdn_cache_fork", index, stream, at, src.data_ptr(), dst.data_ptr(), n)
+
+
+def cache_compact(cache, into, stream=None):
+    """Moves a cache's rows to ``into``, their pages in order at the front of its
+    pool (``gdn_cache_compact``), which may be larger or smaller; ``cache``
+    stays as it is.  Returns ``into``."""
+    index, at = _cache(cache)
+    other, to = _cache(into)
+    if other != index:
+        raise ValueError("the two caches are on different devices")
+    _call("gdn_cache_compact", index, stream, at, to)
+    return into
+
+
+def attention_decode_step_workspace_size(rows, q_heads, kv_heads, d) -> int:
+    n = load().gdn_attention_decode_step_workspace_size(rows, q_heads, kv_heads, d)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported attention_decode_step arguments")
+    return int(n)
+
+
+def attention_decode_step(q, cache, layer=0, scale=None, out=None, stream=None, workspace=None):
+    """Attention of one new token of every row over the row's cached keys and
+    values of one layer (``gdn_attention_decode_step``): q [rows, q_heads, d]
+    bf16.  Returns out like q; 0 for an empty row."""
+    index, at = _cache(cache)
+    _need(q, "q", torch.bfloat16, index)
+    rows, d = cache.lengths.shape[0], cache.k.shape[4]
+    if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d:
+        raise ValueError(f"q must be [{rows}, q_heads, {d}]")
+    out = torch.empty_like(q) if out is None else _out(out, "out", q.shape, q.dtype, index)
+    args = (q.data_ptr(), at, layer, q.shape[1], d ** -0.5 if scale is None else float(scale),
+            out.data_ptr())
+    if workspace is None:
+        _call("gdn_attention_decode_step", index, stream, *args)
+    else:
+        _call("gdn_attention_decode_step_ws", index, stream, *args, *_ws(workspace))
+    return out
 
 
 def device_status(stream=None) -> int:

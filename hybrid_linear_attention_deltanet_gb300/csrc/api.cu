@@ -619,6 +619,8 @@ const char* gdn_status_string(int s) {
     case GDN_ERR_TIMEOUT: return "device: bounded wait timed out";
     case GDN_ERR_BAD_SEQLENS: return "device: malformed cu_seqlens";
     case GDN_ERR_SCRATCH_LIMIT: return "problem needs more than the 64 MiB static no-allocation scratch";
+    case GDN_ERR_CACHE_FULL: return "device: no page of the attention cache was left";
+    case GDN_ERR_BAD_CACHE: return "device: row, page, length or count outside the attention cache";
     default: return "unknown status";
   }
 }

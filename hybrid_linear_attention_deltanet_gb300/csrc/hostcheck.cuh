@@ -79,6 +79,11 @@ __device__ __forceinline__ uint4 ld_waited(const uint4* p) {
                : "l"(p));
   return v;
 }
+__device__ __forceinline__ int32_t ld_waited(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 // The next grid may start once every CTA of this one has come here.
 __device__ __forceinline__ void grid_release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

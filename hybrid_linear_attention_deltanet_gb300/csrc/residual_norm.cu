@@ -17,8 +17,7 @@
 // of a copy's 6.7 (86 us with weights that are bf16 numbers, 105 with weights of 1:
 // the more values lie on the middle between two codes, the more are settled); the
 // gradient of 8191 x 4096 51.8 us, 5.2 TB/s; one token 1.8 us on the GPU.
-#include <cuda_fp8.h>
-
+#include "fp8_codes.cuh"
 #include "gdn_internal.cuh"
 #include "hostcheck.cuh"
 #include "sm100_ptx.cuh"
@@ -33,8 +32,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDim = 8 * 8 * 256;   // 8 warps x 8 vectors x 256 columns
 constexpr int kFewRows = 304;            // two CTAs an SM of one row each
 constexpr int kClusterCtas = 8;
-constexpr float kTiny = 0x1p-100f;     // the smallest block maximum: its scale stays normal
-constexpr float kE4m3Max = 448.f;
 
 // ------------------------------------------------------- 8 elements of a row
 template <typename T>
@@ -113,41 +110,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
-}
-// a NaN wins, so that a block with one shows it
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float amax8(const float (&y)[8]) {
-  float m = fabsf(y[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
-  return m;
-}
-// 8 e4m3 codes of v (round to nearest even, ties in v as they stand; a NaN
-// keeps a NaN code).
-__device__ __forceinline__ uint2 codes8(const float (&v)[8]) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_fp8x2_storage_t c =
-        __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    w[i >> 1] |= (uint32_t)c << (16 * (i & 1));
-  }
-  return make_uint2(w[0], w[1]);
-}
-// 448 / m to a few units in the last place (scaled, so that no m from 2^-100 up
-// has a subnormal reciprocal), and m / 448 rounded to nearest: the product with
-// the rounded reciprocal, corrected by its exact remainder (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// IBM J. Res. Dev. 34, 1990).
-__device__ __forceinline__ float codes_per(float m) { return 1.75f * rcp_sfu(m * 0x1p-8f); }
-__device__ __forceinline__ float scale_of(float m) {
-  constexpr float r = 1.f / kE4m3Max;
-  const float q = __fmul_rn(m, r);
-  return isinf(q) ? q : __fmaf_rn(__fmaf_rn(-kE4m3Max, q, m), r, q);
 }
 // Is v (of an e4m3 value's size) within 16 units in its last place of the middle
 // between two e4m3 values?  fp32 gets y (448 / m) to about 5, so elsewhere its
@@ -513,19 +475,10 @@ struct QuantArgs {
 // The codes of 448 x / m in a block whose largest magnitude is m.
 template <typename T>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
-  float v[8];
   if constexpr (sizeof(T) == 2) {
-    // bf16: 0.875 x is exact, so one step with the quotient's exact remainder (scale_of's)
-    // gives the rounded quotient, and the quotient itself where it has few
-    // bits, as the middle between two codes does (no other is so near one that
-    // fp32 rounds to it: it is apart by 2^-13 at least)
-    const float d = m * 0x1p-9f, r = rcp_sfu(d);   // 448 / m = 0.875 / d
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = __fmul_rn(x[i], 0.875f), q = __fmul_rn(a, r);
-      v[i] = __fmaf_rn(__fmaf_rn(-q, d, a), r, q);
-    }
+    return quantise8_bf16(x, m);
   } else {
+    float v[8];
     const float inv = codes_per(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(x[i], inv);
@@ -534,8 +487,8 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m) {
       for (int i = 0; i < 8; ++i)
         if (near_tie(v[i])) v[i] = settle_tie(v[i], fabsf(x[i]), 0.f, m, 0.f);
     }
+    return codes8(v);
   }
-  return codes8(v);
 }
 
 // 1 x 128 blocks: a half warp each, kTwo at a time so that both loads are in

@@ -51,7 +51,8 @@ extern "C" {
 /* same object as cudaStream_t; spelled out so that this header needs no CUDA header */
 typedef struct CUstream_st* gdn_stream_t;
 
-enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
+/* GDN_E4M3: the attention cache only */
+enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 };
 
 enum gdn_status {
   GDN_OK = 0,
@@ -61,8 +62,11 @@ enum gdn_status {
   GDN_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
   GDN_ERR_TIMEOUT = 5,       /* device: a bounded wait inside a kernel gave up */
   GDN_ERR_BAD_SEQLENS = 6,   /* device: cu_seqlens not 0 = cu[0] <= ... <= cu[N] = T_total */
-  GDN_ERR_SCRATCH_LIMIT = 7  /* gdn_prefill_noalloc: the problem needs more scratch than its
+  GDN_ERR_SCRATCH_LIMIT = 7, /* gdn_prefill_noalloc: the problem needs more scratch than its
                                 static buffer holds */
+  GDN_ERR_CACHE_FULL = 8,    /* device: no page was left, or a row's table was full */
+  GDN_ERR_BAD_CACHE = 9      /* device: a row, page number, length or count of the attention
+                                cache outside its range */
 };
 
 /*
@@ -593,6 +597,127 @@ int gdn_gated_ffn_backward_ws(const void* x, const void* w_gate, const void* w_u
                               int32_t act, void* dx, void* dw_gate, void* dw_up, int64_t tokens,
                               int32_t dim, int32_t hidden, int32_t io_dtype, void* workspace,
                               size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The attention layers that a hybrid keeps among its Gated DeltaNet layers
+ * (grouped heads, causal), for training and serving, with the paged cache of
+ * keys and values that serving reads.  The conventions above hold; in
+ * addition d = 64 or 128, q_heads a multiple of kv_heads (query head h reads
+ * kv head h / group, group = q_heads / kv_heads <= 128), bf16 tensors
+ * (GDN_ERR_UNSUPPORTED otherwise).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * The paged cache of keys and values, shared by `layers` attention layers.
+ * A row is a sequence: lengths[row] tokens on the pages that table[row][0],
+ * table[row][1], ... name, page tokens each; entries behind the last page are
+ * -1.  refs[p] counts the rows that hold page p; a page with 0 is free.  An
+ * empty cache has lengths and refs 0 and table -1.  The caller owns all of
+ * it; the calls below change it in the stream's order, and calls on the same
+ * cache from several streams are the caller's to order.
+ */
+typedef struct gdn_kv_cache {
+  void *k, *v;                /* [layers, pages, kv_heads, page, d], 16-byte aligned */
+  float *k_scale, *v_scale;   /* GDN_E4M3: [layers, pages, kv_heads, page], 16; GDN_BF16: NULL */
+  int32_t* table;             /* [rows, max_pages] */
+  int32_t* lengths;           /* [rows] */
+  int32_t* refs;              /* [pages], 16-byte aligned */
+  int32_t layers, pages, kv_heads, page, d, rows, max_pages;
+  int32_t dtype;              /* GDN_BF16, or GDN_E4M3: codes with a scale a token and head by
+                                 gdn_quantize_fp8's rule over the d values */
+} gdn_kv_cache;
+/* page is 16, 32, 64, 128 or 256; all other sizes >= 1; max_pages * page < 2^31. */
+
+/*
+ * gdn_cache_reserve -- places for counts[row] >= 0 new tokens of every row:
+ * start[row] = lengths[row], lengths[row] += counts[row], and the pages that
+ * this needs are taken in the order of their numbers, for the rows in order
+ * (refs 1).  A row whose table is too narrow, or whose need together with
+ * that of the rows before it is more than the free pages, is left as it is:
+ * start -1 and the device status GDN_ERR_CACHE_FULL (a negative count, or a
+ * length out of range: start -1 and GDN_ERR_BAD_CACHE).
+ *   counts, start [rows] int32
+ */
+int gdn_cache_reserve(const gdn_kv_cache* cache, const int32_t* counts, int32_t* start,
+                      gdn_stream_t stream);
+
+/*
+ * gdn_cache_append -- writes new keys and values of one layer to the places
+ * that gdn_cache_reserve gave: row r's tokens cu_seqlens[r] .. cu_seqlens[r+1]
+ * of k and v (or, with NULL, its one token r) go to positions start[r],
+ * start[r] + 1, ...  A row with start -1 writes nothing.
+ *   k, v [tokens, kv_heads, d] bf16, rows k_stride, v_stride elements apart
+ *   cu_seqlens [rows + 1] with cu_seqlens[rows] = tokens, or NULL (tokens = rows)
+ * What lies at or behind lengths[row] is not reserved and is not written (so
+ * a row with count 0 needs no place for its token).  A token whose place is
+ * outside its row's table or whose page number is outside the pool is skipped
+ * (GDN_ERR_BAD_CACHE), one outside its cu_seqlens too (GDN_ERR_BAD_SEQLENS).
+ */
+int gdn_cache_append(const gdn_kv_cache* cache, int32_t layer, const void* k, const void* v,
+                     const int32_t* start, const int32_t* cu_seqlens, int64_t tokens,
+                     int64_t k_stride, int64_t v_stride, gdn_stream_t stream);
+
+/*
+ * gdn_cache_free -- empties rows[0 .. n): their pages lose a reference, their
+ * table entries become -1, their lengths 0.  A row named twice is emptied
+ * once; an empty row stays so; a number outside [0, cache rows) is skipped
+ * (GDN_ERR_BAD_CACHE).
+ */
+int gdn_cache_free(const gdn_kv_cache* cache, const int32_t* rows, int32_t n,
+                   gdn_stream_t stream);
+
+/*
+ * gdn_cache_fork -- row dst[i] becomes a copy of row src[i] for i in 0 .. n:
+ * it shares the full pages (refs + 1) and gets a page of its own, taken as
+ * gdn_cache_reserve takes them in the order of the pairs, for the tokens on
+ * the last page if that is not full; those tokens are copied in every layer.
+ * All pairs read the rows as they were before the call.  A pair is skipped,
+ * with GDN_ERR_BAD_CACHE, where a number is outside [0, rows), dst[i] is not
+ * empty, or an earlier pair names the same dst; with GDN_ERR_CACHE_FULL where
+ * its page, together with those of the pairs before it, is more than the
+ * free pages.
+ */
+int gdn_cache_fork(const gdn_kv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
+                   gdn_stream_t stream);
+
+/*
+ * gdn_cache_compact -- copies the pages of `cache` that are not free to the
+ * first pages of `into`, in the order of their numbers, and its rows with
+ * them; into's table, lengths and refs are overwritten, its pages behind the
+ * copied ones are left as they were.  `into` has the same layers, kv_heads,
+ * page, d, dtype and rows; pages may differ (a pool to grow or to shrink to)
+ * and max_pages may be larger.  More live pages than `into` has:
+ * GDN_ERR_CACHE_FULL and nothing is written.  The two may not overlap.
+ */
+int gdn_cache_compact(const gdn_kv_cache* cache, const gdn_kv_cache* into, gdn_stream_t stream);
+
+/*
+ * gdn_attention_decode_step -- attention of one new token of each row over
+ * the row's cached keys and values of one layer (its own among them, once
+ * gdn_cache_reserve and gdn_cache_append have placed them):
+ *
+ *   out[r] = softmax_j(scale q[r] . k_j) v_j   over the lengths[r] tokens of row r
+ *
+ *   q, out [rows, q_heads, d] bf16, contiguous; an empty row's out is 0
+ * The rows' lengths are read on the device; the work is cut into equal parts
+ * over all rows and heads whatever they are, and parts of a row are joined in
+ * a fixed order.  Scores, sums and the join are fp32; probabilities (8-bit
+ * cache: times the value's scale) enter the second product rounded to bf16.
+ * A length outside [0, max_pages * page] counts as 0, a page number outside
+ * the pool reads as zeros, both with GDN_ERR_BAD_CACHE.  out may not overlap
+ * q or the cache.  Scratch from the library's pool, or a caller's 256-byte
+ * aligned workspace of at least gdn_attention_decode_step_workspace_size
+ * bytes (rules as gdn_prefill_ws).
+ */
+int gdn_attention_decode_step(const void* q, const gdn_kv_cache* cache, int32_t layer,
+                              int32_t q_heads, float scale, void* out, gdn_stream_t stream);
+size_t gdn_attention_decode_step_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                                int32_t d);
+int gdn_attention_decode_step_ws(const void* q, const gdn_kv_cache* cache, int32_t layer,
+                                 int32_t q_heads, float scale, void* out, void* workspace,
+                                 size_t workspace_bytes, gdn_stream_t stream);
 
 /*
  * gdn_get_device_status -- synchronises `stream`, then returns and clears the
