@@ -16,7 +16,8 @@ raise when the compiled library is missing.
     q, scale, s = residual_norm_fp8(x, w, residual)      # the layer around the mixer:
     out = linear_fp8(q, scale, wq, w_scale)              # 8-bit projections,
     h = gated_ffn(x, w_gate, w_up)                       # gated feed-forward
-    cache = kv_cache(layers, pages, kv_heads, rows, max_pages)   # a hybrid's attention layers:
+    out, lse = attention_prefill(q, k, v, cu_seqlens, cu_seqlens_k)   # a hybrid's attention layers
+    cache = kv_cache(layers, pages, kv_heads, rows, max_pages)        # and their paged cache:
     start = cache_reserve(cache, counts); cache_append(cache, k, v, start, layer=i)
     out = attention_decode_step(q, cache, layer=i)
 
@@ -133,6 +134,9 @@ def load():
     lib.gdn_gated_ffn_backward_ws.argtypes = [vp] * 4 + [i32, vp, vp, vp, i64, i32, i32, i32, vp,
                                                          sz, vp]
     lib.gdn_gated_ffn_backward_ws.restype = ctypes.c_int
+    lib.gdn_attention_prefill.argtypes = [vp] * 5 + [f32, vp, vp, i32, i64, i64, i32, i32, i32,
+                                                     i64, i64, i64, vp]
+    lib.gdn_attention_prefill.restype = ctypes.c_int
     lib.gdn_attention_decode_step.argtypes = [vp, vp, i32, i32, f32, vp, vp]
     lib.gdn_attention_decode_step.restype = ctypes.c_int
     lib.gdn_attention_decode_step_workspace_size.argtypes = [i32, i32, i32, i32]
@@ -973,6 +977,59 @@ def _token_rows(t, name, index):
             or (batch > 1 and tokens > 1 and t.stride(0) != tokens * step)):
         raise ValueError(f"{name}'s heads must be contiguous and its tokens evenly spaced")
     return heads, d, step
+
+
+def _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, scale):
+    """(device index, the C ABI's sizes and strides, cu pointers, scale)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    index = q.get_device()
+    H, d, qs = _token_rows(q, "q", index)
+    kv, dk, ks = _token_rows(k, "k", index)
+    kv2, dv, vs = _token_rows(v, "v", index)
+    if dk != d or dv != d or kv2 != kv or k.shape != v.shape or q.dim() != k.dim():
+        raise ValueError("q [.., T, q_heads, d], k and v [.., T_k, kv_heads, d]")
+    if cu_seqlens is None and cu_seqlens_k is None:
+        N = q.shape[0] if q.dim() == 4 else 1
+        if q.dim() == 4 and k.shape[0] != N:
+            raise ValueError("q and k have different batch sizes")
+        cu_q = cu_k = None
+    else:
+        if cu_seqlens is None:
+            raise ValueError("cu_seqlens_k goes with cu_seqlens")
+        if cu_seqlens_k is None:
+            if q.shape[:-2] != k.shape[:-2]:
+                raise ValueError("cu_seqlens_k is needed where k has other tokens than q")
+            cu_seqlens_k = cu_seqlens
+        for name, t in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_seqlens_k)):
+            _need(t, name, torch.int32, index)
+            if t.dim() != 1 or t.shape[0] < 2 or t.shape != cu_seqlens.shape:
+                raise ValueError("cu_seqlens and cu_seqlens_k must be [N + 1]")
+        if q.dim() == 4 and (q.shape[0] != 1 or k.shape[0] != 1):
+            raise ValueError("varlen input must have batch axis 1")
+        N, cu_q, cu_k = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr()
+    scale = d ** -0.5 if scale is None else float(scale)
+    return index, (N, q.shape[-3], k.shape[-3], H, kv, d, qs, ks, vs), (cu_q, cu_k), scale
+
+
+def attention_prefill(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None, out=None, lse=None,
+                      stream=None):
+    """Causal attention with grouped heads over whole sequences
+    (``gdn_attention_prefill``): q [B, T, q_heads, d] or packed [T, q_heads, d],
+    k and v [.., T_k, kv_heads, d], bf16; d 64 or 128.  ``cu_seqlens`` [N + 1]
+    packs the queries, ``cu_seqlens_k`` the keys (the same when None).  A
+    sequence's mask ends at both last tokens, so longer keys are a stored
+    context.  q, k and v may be slices of a packed projection (heads
+    contiguous, tokens evenly spaced).  Returns (out like q, contiguous; lse
+    [.., T, q_heads] fp32); a row that sees no key has out 0 and lse -inf."""
+    index, sizes, cu, scale = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+    out = (torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else
+           _out(out, "out", q.shape, q.dtype, index))
+    lse = (torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else
+           _out(lse, "lse", q.shape[:-1], torch.float32, index))
+    _call("gdn_attention_prefill", index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), *cu,
+          scale, out.data_ptr(), lse.data_ptr(), *sizes)
+    return out, lse
 
 
 class _CacheStruct(ctypes.Structure):

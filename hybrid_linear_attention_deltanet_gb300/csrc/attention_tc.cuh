@@ -1,0 +1,177 @@
+// What the tensor-core kernels of the attention over prompts share: where a
+// tile of queries or keys lies, its tensor maps, its shared-memory images.
+//
+// The queries of a kv head's group are packed into the rows of a tile: row r
+// is query r / group, head r % group, and a 128-row tile holds the largest
+// whole number of queries, so that a group's heads read a key once and sum its
+// gradients in one accumulator.
+#pragma once
+
+#include <string.h>
+
+#include "gdn_internal.cuh"
+#include "hostcheck.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gdn {
+namespace attn {
+
+using namespace hostcheck;
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kRows = 128;           // of a tile: queries x group, or keys
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// The call's sequences; dense batches are cu == nullptr.
+struct Seqs {
+  const int32_t *cu_q, *cu_k;
+  int32_t n;
+  int64_t len_q, len_k;        // dense: of each; packed: of all
+  int32_t group, kv_heads;
+};
+// One sequence: its first query and key, their numbers.
+struct Seq {
+  int64_t q0, k0;
+  int32_t lq, lk;
+  int32_t tile;                // the tile's number in the sequence, -1: none
+};
+
+// The sequence and the tile of job `job` (of one kv head), tiles of `per` tokens of
+// the queries (or keys); the last tile of a sequence first where `down`, as it
+// sees the most keys.  Every thread of the CTA calls it; sm holds 2 + kThreads
+// words.  false: no such job, or malformed sequences (the first CTA says so).
+template <int kThreads>
+__device__ bool locate(const Seqs& s, int64_t job, int per, bool keys, bool down, int64_t* sm,
+                       unsigned* status, Seq& out) {
+  if (!s.cu_q) {
+    // all sequences' last tiles, then all the tiles before them
+    const int64_t len = keys ? s.len_k : s.len_q, tiles = (len + per - 1) / per;
+    const int64_t t = job / s.n, i = job - t * s.n;
+    if (t >= tiles) return false;
+    out = {i * s.len_q, i * s.len_k, (int32_t)s.len_q, (int32_t)s.len_k,
+           (int32_t)(down ? tiles - 1 - t : t)};
+    return true;
+  }
+  const int tid = threadIdx.x;
+  const int64_t chunk = ((int64_t)s.n + kThreads - 1) / kThreads;
+  const int64_t i0 = tid * chunk, i1 = i0 + chunk < s.n ? i0 + chunk : s.n;
+  int64_t mine = 0;
+  bool bad = tid == 0 && (s.cu_q[0] != 0 || s.cu_k[0] != 0 || s.cu_q[s.n] != s.len_q ||
+                          s.cu_k[s.n] != s.len_k);
+  for (int64_t i = i0; i < i1; ++i) {
+    const int32_t lq = s.cu_q[i + 1] - s.cu_q[i], lk = s.cu_k[i + 1] - s.cu_k[i];
+    bad |= lq < 0 || lk < 0 || s.cu_q[i] < 0 || s.cu_k[i] < 0;
+    mine += ((int64_t)(keys ? lk : lq) + per - 1) / per;
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0 && blockIdx.x == 0) flag_status(status, GDN_ERR_BAD_SEQLENS);
+    return false;
+  }
+  // exclusive prefix of the threads' tiles
+  sm[1 + tid] = mine;
+  if (tid == 0) sm[0] = 0;
+  __syncthreads();
+  if (tid < 32) {
+    int64_t carry = 0;
+    for (int b = 0; b < kThreads; b += 32) {
+      int64_t x = sm[1 + b + tid];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (tid >= o) x += y;
+      }
+      sm[1 + b + tid] = x + carry;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  if (job >= sm[kThreads]) return false;
+  __shared__ Seq found;
+  if (job >= sm[tid] && job < sm[tid + 1]) {
+    int64_t left = job - sm[tid];
+    for (int64_t i = i0; i < i1; ++i) {
+      const int32_t a = s.cu_q[i], b = s.cu_k[i];
+      const int32_t lq = s.cu_q[i + 1] - a, lk = s.cu_k[i + 1] - b;
+      const int64_t t = ((int64_t)(keys ? lk : lq) + per - 1) / per;
+      if (left < t) {
+        found = {a, b, lq, lk, (int32_t)(down ? t - 1 - left : left)};
+        break;
+      }
+      left -= t;
+    }
+  }
+  __syncthreads();
+  out = found;
+  return true;
+}
+
+// ---------------------------------------------------------------- host side
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+// x [tokens][heads][d] bf16, tokens `stride` elements apart, read in boxes of 64
+// columns x box_heads heads x box_tokens tokens with the 128-byte swizzle; what
+// lies past the last token reads as zeros.
+inline bool heads_map(CUtensorMap* m, const void* x, int64_t tokens, int32_t heads, int32_t d,
+                      int64_t stride, uint32_t box_heads, uint32_t box_tokens) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  memset(m, 0, sizeof *m);
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)(tokens > 0 ? tokens : 1)};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The checks that the prompt kernels share: sizes, strides, alignment.
+struct Shape {
+  int32_t batch;
+  int64_t seqlen_q, seqlen_k;
+  int32_t q_heads, kv_heads, d;
+  int64_t q_stride, k_stride, v_stride;
+  bool packed;
+  int64_t tq() const { return packed ? seqlen_q : batch * seqlen_q; }
+  int64_t tk() const { return packed ? seqlen_k : batch * seqlen_k; }
+  size_t q_bytes() const { return tq() ? (size_t)((tq() - 1) * q_stride + q_heads * d) * 2 : 0; }
+  size_t k_bytes(int64_t stride) const {
+    return tk() ? (size_t)((tk() - 1) * stride + kv_heads * d) * 2 : 0;
+  }
+  size_t rows() const { return (size_t)tq() * q_heads; }      // of out and lse
+};
+inline int check_shape(const Shape& s, const int32_t* cu_q, const int32_t* cu_k, float scale) {
+  if (s.batch < 1 || s.seqlen_q < 0 || s.seqlen_k < 0 || s.q_heads < 1 || s.kv_heads < 1)
+    return GDN_ERR_INVALID_ARG;
+  if ((cu_q == nullptr) != (cu_k == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > 3e38f) return GDN_ERR_INVALID_ARG;
+  if ((s.d != 64 && s.d != 128) || s.q_heads % s.kv_heads || s.q_heads / s.kv_heads > kRows)
+    return GDN_ERR_UNSUPPORTED;
+  // 32-bit token coordinates, with room for a tile; sequences counted in 32 bits
+  if (s.seqlen_q > kLongestAxis || s.seqlen_k > kLongestAxis || s.tq() > kLongestAxis ||
+      s.tk() > kLongestAxis || (int64_t)s.q_heads * s.d > kLongestAxis)
+    return GDN_ERR_UNSUPPORTED;
+  const int64_t wq = (int64_t)s.q_heads * s.d, wk = (int64_t)s.kv_heads * s.d;
+  if (s.q_stride < wq || s.k_stride < wk || s.v_stride < wk) return GDN_ERR_INVALID_ARG;
+  if (s.q_stride > kLongestAxis || s.k_stride > kLongestAxis || s.v_stride > kLongestAxis)
+    return GDN_ERR_UNSUPPORTED;
+  if (s.q_stride % 8 || s.k_stride % 8 || s.v_stride % 8) return GDN_ERR_ALIGNMENT;
+  return GDN_OK;
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -610,6 +610,37 @@ int gdn_gated_ffn_backward_ws(const void* x, const void* w_gate, const void* w_u
  */
 
 /*
+ * gdn_attention_prefill -- causal attention over whole sequences:
+ *
+ *   s_ij = scale q_i . k_j   for the keys j <= i + len_k - len_q of a row i
+ *   lse_i = log sum_j exp(s_ij),   out_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ * The mask ends at both last tokens: len_k > len_q are new tokens behind a
+ * stored context; the first rows of a sequence with len_k < len_q see no key,
+ * and such a row has out = 0, lse = -inf.
+ *
+ *   q    [T_q, q_heads, d], rows q_stride elements apart (>= q_heads * d)
+ *   k, v [T_k, kv_heads, d], rows k_stride, v_stride elements apart
+ *   out  [T_q, q_heads, d] contiguous; lse [T_q, q_heads] fp32
+ * Dense batch (cu_q == cu_k == NULL): batch sequences of seqlen_q queries and
+ * seqlen_k keys.  Packed: batch sequences, seqlen_q = T_q and seqlen_k = T_k
+ * tokens in all, cu_q and cu_k [batch + 1] (both or neither) as in
+ * gdn_prefill; where either is malformed nothing is written and the device
+ * status is GDN_ERR_BAD_SEQLENS.
+ * Scores, the softmax's sums and the sum over keys are fp32; the
+ * probabilities enter the second product rounded to bf16.  A key or value
+ * that is not finite reaches, besides the rows that see it, the rows of its
+ * own sequence whose 128-key tile holds it.
+ * Strides are multiples of 8; tensors 16-byte aligned, lse and cu 4; scale
+ * finite and > 0.  out and lse may overlap no input or each other.
+ */
+int gdn_attention_prefill(const void* q, const void* k, const void* v, const int32_t* cu_q,
+                          const int32_t* cu_k, float scale, void* out, float* lse, int32_t batch,
+                          int64_t seqlen_q, int64_t seqlen_k, int32_t q_heads, int32_t kv_heads,
+                          int32_t d, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          gdn_stream_t stream);
+
+/*
  * The paged cache of keys and values, shared by `layers` attention layers.
  * A row is a sequence: lengths[row] tokens on the pages that table[row][0],
  * table[row][1], ... name, page tokens each; entries behind the last page are
