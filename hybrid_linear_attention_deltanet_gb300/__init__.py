@@ -137,6 +137,15 @@ def load():
     lib.gdn_attention_prefill.argtypes = [vp] * 5 + [f32, vp, vp, i32, i64, i64, i32, i32, i32,
                                                      i64, i64, i64, vp]
     lib.gdn_attention_prefill.restype = ctypes.c_int
+    lib.gdn_attention_prefill_backward.argtypes = [vp] * 8 + [f32, vp, vp, vp, i32, i64, i64, i32,
+                                                              i32, i32, i64, i64, i64, vp]
+    lib.gdn_attention_prefill_backward.restype = ctypes.c_int
+    lib.gdn_attention_prefill_backward_workspace_size.argtypes = [i32, i64, i32, i32, i32, i32]
+    lib.gdn_attention_prefill_backward_workspace_size.restype = sz
+    lib.gdn_attention_prefill_backward_ws.argtypes = [vp] * 8 + [f32, vp, vp, vp, i32, i64, i64,
+                                                                 i32, i32, i32, i64, i64, i64, vp,
+                                                                 sz, vp]
+    lib.gdn_attention_prefill_backward_ws.restype = ctypes.c_int
     lib.gdn_attention_decode_step.argtypes = [vp, vp, i32, i32, f32, vp, vp]
     lib.gdn_attention_decode_step.restype = ctypes.c_int
     lib.gdn_attention_decode_step_workspace_size.argtypes = [i32, i32, i32, i32]
@@ -1030,6 +1039,36 @@ def attention_prefill(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None, o
     _call("gdn_attention_prefill", index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), *cu,
           scale, out.data_ptr(), lse.data_ptr(), *sizes)
     return out, lse
+
+
+def attention_prefill_backward_workspace_size(batch, seqlen, q_heads, kv_heads, d,
+                                              varlen=False) -> int:
+    n = load().gdn_attention_prefill_backward_workspace_size(batch, seqlen, int(bool(varlen)),
+                                                             q_heads, kv_heads, d)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported attention_prefill_backward arguments")
+    return int(n)
+
+
+def attention_prefill_backward(q, k, v, out, lse, dout, cu_seqlens=None, cu_seqlens_k=None,
+                               scale=None, stream=None, workspace=None):
+    """Gradients of :func:`attention_prefill` from its inputs, its results and
+    dout (``gdn_attention_prefill_backward``).  Returns dict dq, dk, dv (bf16,
+    contiguous)."""
+    index, sizes, cu, scale = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+    for name, t in (("out", out), ("dout", dout)):
+        _out(t, name, q.shape, torch.bfloat16, index)
+    _out(lse, "lse", q.shape[:-1], torch.float32, index)
+    g = {n: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+         for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            dout.data_ptr(), *cu, scale, g["dq"].data_ptr(), g["dk"].data_ptr(),
+            g["dv"].data_ptr(), *sizes)
+    if workspace is None:
+        _call("gdn_attention_prefill_backward", index, stream, *args)
+    else:
+        _call("gdn_attention_prefill_backward_ws", index, stream, *args, *_ws(workspace))
+    return g
 
 
 class _CacheStruct(ctypes.Structure):

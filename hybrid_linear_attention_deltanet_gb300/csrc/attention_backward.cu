@@ -1,0 +1,808 @@
+// Gradients of the causal attention over whole sequences (contract:
+// include/gdn.h):
+//
+//   P_ij = exp(s_ij - lse_i), D_i = dout_i . out_i, dS_ij = P_ij (dout_i . v_j - D_i)
+//   dV = P^T dO, dK = scale dS^T Q, dQ = scale dS K
+//
+// P is computed again from lse, so that no pass before it keeps anything of the
+// size of P.  One kernel holds a tile of keys and goes over the queries that
+// see it (S^T, dP^T, dV, dK), one a tile of queries and goes over its keys (S,
+// dP, dQ): seven products where five would do, but every sum is one tensor-
+// memory accumulator with one order, and nothing is added in memory.  Both are
+// bound by the tensor cores; the order of their products is such that the
+// cores work on the next tile's scores while P and dS of this one are made:
+//   keys:     dV(i), S(i+1), dK(i), dP(i+1), ...
+//   queries:  S(j+1), dQ(j), dP(j+1), ...
+// P and dS go back to tensor memory as bf16, over the scores that they came
+// from, and are the A operand there.
+#include "attention_tc.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace attn;
+using namespace sm100;
+
+constexpr int kThreads = 384;   // two warpgroups for P and dS; a third with the issuing warps
+constexpr uint32_t kHalfTile = 16384;   // 128 rows x 64 columns bf16
+
+struct BwdArgs {
+  CUtensorMap q, k, v, dout;
+  Seqs s;
+  const float *nlse, *nd;      // [kv_heads][T_q][group]: -lse log2 e and -D
+  __nv_bfloat16 *dq, *dk, *dv;
+  float c, scale;              // scale log2 e, scale
+  int64_t tq;
+  int32_t q_heads, per;        // per: queries of a 128-row tile
+  unsigned* status;
+};
+
+// ------------------------------------------------------------ row sums
+struct RowArgs {
+  const __nv_bfloat16 *out, *dout;
+  const float* lse;
+  float *nlse, *nd;
+  int64_t tq;
+  int32_t q_heads, group;
+};
+// D / 8 lanes a row, 16 bytes of each tensor a lane; bound by HBM.
+template <int D>
+__global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
+  grid_release_next();
+  constexpr int kLanes = D / 8;
+  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int l = threadIdx.x % kLanes;
+  const bool on = r < a.tq * a.q_heads;
+  float sum = 0.f;
+  if (on) {
+    const uint4 x = *reinterpret_cast<const uint4*>(a.out + r * D + l * 8);
+    const uint4 y = *reinterpret_cast<const uint4*>(a.dout + r * D + l * 8);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), sum);
+      sum = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), sum);
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (on && l == 0) {
+    const int64_t t = r / a.q_heads;
+    const int head = (int)(r - t * a.q_heads), h = head / a.group;
+    const int64_t to = ((int64_t)h * a.tq + t) * a.group + head - h * a.group;
+    const float lse = a.lse[r];
+    // a row that sees no key: P = 2^-inf
+    a.nlse[to] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    a.nd[to] = -sum;
+  }
+}
+
+// ------------------------------------------------------------ the two loops
+// Shared memory: two resident tiles, three slots of the operand that is used
+// again a product later (Q; K) and two of the other (dO; V), then the
+// statistics and the barriers.  D = 128: 224 KB of tiles.
+template <int D>
+struct Bwd {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kTile = kHalves * kHalfTile;
+  static constexpr uint32_t kA = 2 * kTile, kB = 5 * kTile;   // the slots of the two operands
+  static constexpr int kNA = 3, kNB = 2;
+  static constexpr uint32_t kStats = 7 * kTile;               // [2][2][128] fp32
+  static constexpr uint32_t kBars = kStats + 2048;
+  static constexpr uint32_t kSmem = kBars + 256;
+};
+struct Bars {
+  uint64_t own, a_full[3], a_empty[3], b_full[2], b_empty[2], s_full[2], dp_full, p_ready, ds_ready,
+      done;
+  uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 256, "");
+
+__device__ __forceinline__ uint32_t kstep(int s) { return (s >> 2) * kHalfTile + (s & 3) * 32; }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Rows [from, 128) of a tile in shared memory become zeros, by one warp.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h) {
+    uint4* z = reinterpret_cast<uint4*>(tile + h * kHalfTile);
+    for (int i = from * 8 + lane; i < kRows * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// This lane's row of an accumulator's columns as bf16 (times f) to memory.
+template <int kCols>
+__device__ __forceinline__ void store_row(uint32_t at, float f, __nv_bfloat16* to, bool live, bool zero) {
+#pragma unroll
+  for (int i = 0; i < kCols / 32; ++i) {
+    uint32_t o[32];
+    if (!zero) {
+      tmem_ld32(at + 32 * i, o);
+      tmem_ld_wait_regs(o);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t y[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        y[z] = zero ? 0u
+                    : pack(__uint_as_float(o[8 * x + 2 * z]) * f, __uint_as_float(o[8 * x + 2 * z + 1]) * f);
+      if (live) *reinterpret_cast<uint4*>(to + 32 * i + 8 * x) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
+// The common part of both kernels: the job's place, barriers, tensor memory.
+template <int D>
+__device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, int per, bool keys, Seq& seq,
+                                      int& head) {
+  using C = Bwd<D>;
+  Bars& b = *reinterpret_cast<Bars*>(sm + C::kBars);
+  const int tid = threadIdx.x, lane = tid & 31;
+  // the swizzled tiles' pattern repeats every 1024 bytes (without static shared
+  // memory the dynamic part starts on one)
+  if (smem_u32(sm) & 1023u) {
+    if (tid == 0) flag_status(a.status, GDN_ERR_UNSUPPORTED);
+    return false;
+  }
+  head = blockIdx.x % a.s.kv_heads;
+  if (!locate<kThreads>(a.s, blockIdx.x / a.s.kv_heads, per, keys, !keys,
+                        reinterpret_cast<int64_t*>(sm), a.status, seq))
+    return false;
+  if (tid == 0) {
+    mbar_init(&b.own, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&b.a_full[i], 1);
+      mbar_init(&b.a_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.b_full[i], 1);
+      mbar_init(&b.b_empty[i], 1);
+      mbar_init(&b.s_full[i], 1);
+    }
+    mbar_init(&b.dp_full, 1);
+    mbar_init(&b.p_ready, 8);
+    mbar_init(&b.ds_ready, 8);
+    mbar_init(&b.done, 1);
+    fence_barrier_init();
+  }
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (warp == 8) tmem_alloc(&b.tmem, 512);
+  if (warp == 9 && lane == 0) {
+    prefetch_tensormap(&a.q);
+    prefetch_tensormap(&a.k);
+    prefetch_tensormap(&a.v);
+    prefetch_tensormap(&a.dout);
+  }
+  return true;
+}
+__device__ __forceinline__ void finish(bool ok, uint32_t tmem, unsigned* status) {
+  if (!ok) {
+    // copies and products in flight end within microseconds; give them longer
+    flag_status(status, GDN_ERR_TIMEOUT);
+    const uint64_t from = globaltimer_ns();
+    while (globaltimer_ns() - from < 5000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x >> 5 == 8) tmem_dealloc(tmem, 512);
+}
+
+// A tile of 128 keys of a kv head: dK and dV.  Rows of all products are keys,
+// so P^T and dS^T are A operands as they come; a column is a packed query row,
+// whose statistics are read from shared memory.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+keys_kernel(const __grid_constant__ BwdArgs a) {
+  using C = Bwd<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw;
+  Bars& b = *reinterpret_cast<Bars*>(sm + C::kBars);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  Seq seq;
+  int head;
+  if (!begin<D>(a, sm, kRows, true, seq, head)) return;
+  const int32_t group = a.s.group, shift = seq.lk - seq.lq;
+  const int32_t k0 = seq.tile * kRows;                       // the tile's first key
+  const int32_t used = a.per * group;                        // rows of a tile of queries
+  // tiles of queries: from that of the first query that sees key k0
+  const int32_t sees = k0 - shift > 0 ? k0 - shift : 0;
+  const int32_t t0 = sees / a.per, t1 = (seq.lq + a.per - 1) / a.per;
+  const int32_t n = sees < seq.lq ? t1 - t0 : 0;
+  // rows that no query fills take part in the products with P = dS = 0: zeros,
+  // so that the products are
+  if (used < kRows && warp < 5)
+    zero_rows<D>(sm + (2 + warp) * C::kTile, used, lane);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_wait();
+  const uint32_t tmem = b.tmem;
+  constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 256 + D;
+  bool ok = true;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 9) {
+      // ----------------------------------------------------------- load
+      const bool lead = elect_one();
+      if (lead && n > 0) {
+        mbar_arrive_expect_tx(&b.own, 2 * C::kTile);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          tma_load_3d(sm + h * kHalfTile, &a.k, 64 * h, head, (int32_t)(seq.k0 + k0), &b.own);
+          tma_load_3d(sm + C::kTile + h * kHalfTile, &a.v, 64 * h, head, (int32_t)(seq.k0 + k0), &b.own);
+        }
+      }
+      for (int32_t i = 0; ok && i < n; ++i) {
+        const int32_t t = (int32_t)(seq.q0 + (int64_t)(t0 + i) * a.per);
+        const int sa = i % C::kNA, sb = i % C::kNB;
+        ok = mbar_wait_warp(&b.a_empty[sa], (uint32_t)((i / C::kNA) & 1) ^ 1u, kWaitNs);
+        if (ok && lead) {
+          mbar_arrive_expect_tx(&b.a_full[sa], (uint32_t)used * 128 * C::kHalves);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(sm + C::kA + sa * C::kTile + h * kHalfTile, &a.q, 64 * h, head * group, t,
+                        &b.a_full[sa]);
+        }
+        __syncwarp();
+        ok = ok && mbar_wait_warp(&b.b_empty[sb], (uint32_t)((i / C::kNB) & 1) ^ 1u, kWaitNs);
+        if (ok && lead) {
+          mbar_arrive_expect_tx(&b.b_full[sb], (uint32_t)used * 128 * C::kHalves);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(sm + C::kB + sb * C::kTile + h * kHalfTile, &a.dout, 64 * h, head * group, t,
+                        &b.b_full[sb]);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------- multiply
+      const bool lead = elect_one();
+      const uint32_t base = smem_u32(sm);
+      constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kGrad = idesc_bf16(128, D, 0, 1);
+      const uint64_t own = smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t own2 = smem_desc(base + C::kTile, 16, 1024, kSwizzle128B);
+      const uint64_t ak = smem_desc(base + C::kA, 16, 1024, kSwizzle128B);
+      const uint64_t bk = smem_desc(base + C::kB, 16, 1024, kSwizzle128B);
+      const uint64_t an = smem_desc(base + C::kA, kHalfTile, 1024, kSwizzle128B);
+      const uint64_t bn = smem_desc(base + C::kB, kHalfTile, 1024, kSwizzle128B);
+      // queries behind the sequence's last are another's: their rows become zeros
+      auto clean = [&](uint8_t* slots, int slot, int32_t i) {
+        const int64_t rows = ((int64_t)seq.lq - (int64_t)(t0 + i) * a.per) * group;
+        if (rows < used) {
+          zero_rows<D>(slots + slot * C::kTile, (int)rows, lane);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+      };
+      auto scores = [&](int32_t i) {   // S^T = K Q^T
+        const int sa = i % C::kNA;
+        ok = ok && mbar_wait_warp(&b.a_full[sa], (uint32_t)((i / C::kNA) & 1), kWaitNs);
+        if (!ok) return;
+        clean(sm + C::kA, sa, i);
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_bf16(tmem + kS, own + (uint64_t)(kstep(s) >> 4),
+                     ak + (uint64_t)((sa * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+          mma_commit(&b.s_full[0]);
+        }
+        __syncwarp();
+      };
+      auto dprobs = [&](int32_t i) {   // dP^T = V dO^T
+        const int sb = i % C::kNB;
+        ok = ok && mbar_wait_warp(&b.b_full[sb], (uint32_t)((i / C::kNB) & 1), kWaitNs);
+        if (!ok) return;
+        clean(sm + C::kB, sb, i);
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_bf16(tmem + kDP, own2 + (uint64_t)(kstep(s) >> 4),
+                     bk + (uint64_t)((sb * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+          mma_commit(&b.dp_full);
+        }
+        __syncwarp();
+      };
+      if (n > 0) {
+        ok = mbar_wait_warp(&b.own, 0, kWaitNs);
+        scores(0);
+        dprobs(0);
+      }
+      for (int32_t i = 0; ok && i < n; ++i) {
+        const int sa = i % C::kNA, sb = i % C::kNB;
+        ok = mbar_wait_warp(&b.p_ready, (uint32_t)(i & 1), kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {   // dV += P^T dO
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_bf16_ts(tmem + kDV, tmem + kS + (s >> 2) * 64 + (s & 3) * 8,
+                        bn + (uint64_t)((sb * C::kTile + s * 2048) >> 4), kGrad, i > 0 || s > 0);
+          mma_commit(&b.b_empty[sb]);
+        }
+        __syncwarp();
+        if (i + 1 < n) scores(i + 1);
+        ok = ok && mbar_wait_warp(&b.ds_ready, (uint32_t)(i & 1), kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {   // dK += dS^T Q
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_bf16_ts(tmem + kDK, tmem + kDP + (s >> 2) * 64 + (s & 3) * 8,
+                        an + (uint64_t)((sa * C::kTile + s * 2048) >> 4), kGrad, i > 0 || s > 0);
+          mma_commit(&b.a_empty[sa]);
+          if (i + 1 == n) mma_commit(&b.done);
+        }
+        __syncwarp();
+        if (i + 1 < n) dprobs(i + 1);
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- P and dS
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int w = warp >> 2, row = tid & 127;             // the columns' half, the key
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t s_at = tmem + lanes + kS + 64 * w, dp_at = tmem + lanes + kDP + 64 * w;
+    float* stats = reinterpret_cast<float*>(sm + C::kStats) + 128 * w;   // [2 buffers: + 256][64 | 64]
+    const int64_t stat0 = ((int64_t)head * a.tq + seq.q0) * group;
+    const bool fetch = row < 64;
+    // column `row` of this half of tile i: its statistics, 0 where there is none
+    auto read = [&](int32_t i, float& x, float& y) {
+      const int col = 64 * w + row;
+      const int64_t at = (int64_t)(t0 + i) * used + col;
+      const bool on = fetch && i < n && col < used && at < (int64_t)seq.lq * group;
+      x = on ? ld_waited(a.nlse + stat0 + at) : 0.f;
+      y = on ? ld_waited(a.nd + stat0 + at) : 0.f;
+    };
+    float nl, nd;
+    read(0, nl, nd);
+    const F2 cc = f2(a.c, a.c);
+    for (int32_t i = 0; i < n; ++i) {
+      float* st = stats + 256 * (i & 1);
+      if (fetch) {
+        st[row] = nl;
+        st[64 + row] = nd;
+      }
+      bar_sync(1 + w, 128);
+      read(i + 1, nl, nd);
+      // the columns that see this key: [lo, hi)
+      const int32_t q0 = (t0 + i) * a.per;
+      const int64_t lo64 = ((int64_t)k0 + row - shift - q0) * group - 64 * w;
+      const int64_t hi64 = ((int64_t)seq.lq - q0) * group;
+      const int32_t lo = lo64 < 0 ? 0 : lo64 > 64 ? 64 : (int32_t)lo64;
+      const int32_t hi = (hi64 < used ? (int32_t)hi64 : kRows) - 64 * w;   // (behind `used`: zeros)
+      const bool masked = (int64_t)k0 + kRows - 1 - shift > q0 || hi64 < used;
+      ok = mbar_wait_warp(&b.s_full[0], (uint32_t)(i & 1), kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld32(s_at + 32 * h, s[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(s[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(st + 32 * h + x);
+          float y[4];
+          f2_split(f2_fma(f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1])), cc, f2(l4.x, l4.y)),
+                   y[0], y[1]);
+          f2_split(f2_fma(f2(__uint_as_float(s[h][x + 2]), __uint_as_float(s[h][x + 3])), cc,
+                          f2(l4.z, l4.w)),
+                   y[2], y[3]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            float e = ex2_sfu(y[z]);
+            if (masked && (32 * h + x + z < lo || 32 * h + x + z >= hi)) e = 0.f;
+            s[h][x + z] = __float_as_uint(e);
+          }
+          p[x / 2] = pack(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1]));
+          p[x / 2 + 1] = pack(__uint_as_float(s[h][x + 2]), __uint_as_float(s[h][x + 3]));
+        }
+        tmem_st16(s_at + 16 * h, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.p_ready);
+      ok = mbar_wait_warp(&b.dp_full, (uint32_t)(i & 1), kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t g[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld32(dp_at + 32 * h, g[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(g[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(st + 64 + 32 * h + x);
+          float y[4];
+          f2_split(f2_mul(f2_add(f2(__uint_as_float(g[h][x]), __uint_as_float(g[h][x + 1])), f2(d4.x, d4.y)),
+                          f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1]))),
+                   y[0], y[1]);
+          f2_split(f2_mul(f2_add(f2(__uint_as_float(g[h][x + 2]), __uint_as_float(g[h][x + 3])),
+                                 f2(d4.z, d4.w)),
+                          f2(__uint_as_float(s[h][x + 2]), __uint_as_float(s[h][x + 3]))),
+                   y[2], y[3]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (masked && (32 * h + x + z < lo || 32 * h + x + z >= hi)) y[z] = 0.f;
+          p[x / 2] = pack(y[0], y[1]);
+          p[x / 2 + 1] = pack(y[2], y[3]);
+        }
+        tmem_st16(dp_at + 16 * h, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.ds_ready);
+    }
+    if (ok && n > 0) ok = mbar_wait_warp(&b.done, 0, kWaitNs);
+    tc_fence_after();
+    if (ok) {
+      // one warpgroup dV, the other dK
+      const bool live = (int64_t)k0 + row < seq.lk;
+      const int64_t to = ((seq.k0 + k0 + row) * a.s.kv_heads + head) * D;
+      store_row<D>(tmem + lanes + (w ? kDK : kDV), w ? a.scale : 1.f, (w ? a.dk : a.dv) + to, live, n == 0);
+    }
+  }
+  finish(ok, tmem, a.status);
+}
+
+// A tile of packed query rows: dQ.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+queries_kernel(const __grid_constant__ BwdArgs a) {
+  using C = Bwd<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw;
+  Bars& b = *reinterpret_cast<Bars*>(sm + C::kBars);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  Seq seq;
+  int head;
+  if (!begin<D>(a, sm, a.per, false, seq, head)) return;
+  const int32_t group = a.s.group, shift = seq.lk - seq.lq;
+  const int32_t used = a.per * group;
+  const int32_t first = seq.tile * a.per;                    // the tile's first query
+  const int32_t rows = seq.lq - first < a.per ? seq.lq - first : a.per;
+  const int32_t seen = first + rows + shift;                 // keys that the last row sees
+  const int32_t n = seen > 0 ? (seen + kRows - 1) / kRows : 0;
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_wait();
+  const uint32_t tmem = b.tmem;
+  constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;           // two buffers of scores
+  bool ok = true;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 9) {
+      // ----------------------------------------------------------- load
+      const bool lead = elect_one();
+      if (lead && n > 0) {
+        mbar_arrive_expect_tx(&b.own, 2 * (uint32_t)used * 128 * C::kHalves);
+        const int32_t t = (int32_t)(seq.q0 + first);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          tma_load_3d(sm + h * kHalfTile, &a.q, 64 * h, head * group, t, &b.own);
+          tma_load_3d(sm + C::kTile + h * kHalfTile, &a.dout, 64 * h, head * group, t, &b.own);
+        }
+      }
+      for (int32_t j = 0; ok && j < n; ++j) {
+        const int32_t t = (int32_t)(seq.k0 + (int64_t)j * kRows);
+        const int sa = j % C::kNA, sb = j % C::kNB;
+        ok = mbar_wait_warp(&b.a_empty[sa], (uint32_t)((j / C::kNA) & 1) ^ 1u, kWaitNs);
+        if (ok && lead) {
+          mbar_arrive_expect_tx(&b.a_full[sa], C::kTile);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(sm + C::kA + sa * C::kTile + h * kHalfTile, &a.k, 64 * h, head, t, &b.a_full[sa]);
+        }
+        __syncwarp();
+        ok = ok && mbar_wait_warp(&b.b_empty[sb], (uint32_t)((j / C::kNB) & 1) ^ 1u, kWaitNs);
+        if (ok && lead) {
+          mbar_arrive_expect_tx(&b.b_full[sb], C::kTile);
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_3d(sm + C::kB + sb * C::kTile + h * kHalfTile, &a.v, 64 * h, head, t, &b.b_full[sb]);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------- multiply
+      const bool lead = elect_one();
+      const uint32_t base = smem_u32(sm);
+      constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kGrad = idesc_bf16(128, D, 0, 1);
+      const uint64_t own = smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t own2 = smem_desc(base + C::kTile, 16, 1024, kSwizzle128B);
+      const uint64_t ak = smem_desc(base + C::kA, 16, 1024, kSwizzle128B);
+      const uint64_t bk = smem_desc(base + C::kB, 16, 1024, kSwizzle128B);
+      const uint64_t an = smem_desc(base + C::kA, kHalfTile, 1024, kSwizzle128B);
+      auto scores = [&](int32_t j) {   // S = Q K^T
+        const int sa = j % C::kNA;
+        ok = ok && mbar_wait_warp(&b.a_full[sa], (uint32_t)((j / C::kNA) & 1), kWaitNs);
+        if (!ok) return;
+        // keys behind the sequence's last are another's: their rows become
+        // zeros, so that the products with dS = 0 are
+        const int64_t valid = seq.lk - (int64_t)j * kRows;
+        if (valid < kRows) {
+          zero_rows<D>(sm + C::kA + sa * C::kTile, (int)valid, lane);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_bf16(tmem + kS + 128 * (j & 1), own + (uint64_t)(kstep(s) >> 4),
+                     ak + (uint64_t)((sa * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+          mma_commit(&b.s_full[j & 1]);
+        }
+        __syncwarp();
+      };
+      auto dprobs = [&](int32_t j) {   // dP = dO V^T
+        const int sb = j % C::kNB;
+        ok = ok && mbar_wait_warp(&b.b_full[sb], (uint32_t)((j / C::kNB) & 1), kWaitNs);
+        if (!ok) return;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_bf16(tmem + kDP, own2 + (uint64_t)(kstep(s) >> 4),
+                     bk + (uint64_t)((sb * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+          mma_commit(&b.dp_full);
+          mma_commit(&b.b_empty[sb]);
+        }
+        __syncwarp();
+      };
+      if (n > 0) {
+        ok = mbar_wait_warp(&b.own, 0, kWaitNs);
+        scores(0);
+        dprobs(0);
+      }
+      for (int32_t j = 0; ok && j < n; ++j) {
+        const int sa = j % C::kNA;
+        if (j + 1 < n) scores(j + 1);
+        ok = ok && mbar_wait_warp(&b.ds_ready, (uint32_t)(j & 1), kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        if (lead) {   // dQ += dS K
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_bf16_ts(tmem + kDQ, tmem + kS + 128 * (j & 1) + (s >> 2) * 64 + (s & 3) * 8,
+                        an + (uint64_t)((sa * C::kTile + s * 2048) >> 4), kGrad, j > 0 || s > 0);
+          mma_commit(&b.a_empty[sa]);
+          if (j + 1 == n) mma_commit(&b.done);
+        }
+        __syncwarp();
+        if (j + 1 < n) dprobs(j + 1);
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- P and dS
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const int qi = row / group;
+    const bool live = qi < rows;
+    const int64_t stat = ((int64_t)head * a.tq + seq.q0 + first) * group + row;
+    const float nl = live ? ld_waited(a.nlse + stat) : 0.f, nd = live ? ld_waited(a.nd + stat) : 0.f;
+    const int32_t last = first + qi + shift;               // the last key that the row sees
+    const F2 cc = f2(a.c, a.c), ll = f2(nl, nl), dd = f2(nd, nd);
+    for (int32_t j = 0; j < n; ++j) {
+      const uint32_t s_at = tmem + lanes + kS + 128 * (j & 1) + 64 * w, dp_at = tmem + lanes + kDP + 64 * w;
+      const int32_t k0 = j * kRows;
+      const bool masked = k0 + kRows - 1 > first + shift;
+      const int32_t see = last - k0 - 64 * w;
+      ok = mbar_wait_warp(&b.s_full[j & 1], (uint32_t)((j >> 1) & 1), kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld32(s_at + 32 * h, s[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(s[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          float y0, y1;
+          f2_split(f2_fma(f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1])), cc, ll), y0, y1);
+          s[h][x] = __float_as_uint(ex2_sfu(y0));
+          s[h][x + 1] = __float_as_uint(ex2_sfu(y1));
+        }
+      ok = mbar_wait_warp(&b.dp_full, (uint32_t)(j & 1), kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t g[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld32(dp_at + 32 * h, g[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(g[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          float y0, y1;
+          f2_split(f2_mul(f2_add(f2(__uint_as_float(g[h][x]), __uint_as_float(g[h][x + 1])), dd),
+                          f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1]))),
+                   y0, y1);
+          if (masked && 32 * h + x > see) y0 = 0.f;
+          if (masked && 32 * h + x + 1 > see) y1 = 0.f;
+          p[x / 2] = pack(y0, y1);
+        }
+        tmem_st16(s_at + 16 * h, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.ds_ready);
+    }
+    if (ok && n > 0) ok = mbar_wait_warp(&b.done, 0, kWaitNs);
+    tc_fence_after();
+    if (ok) {
+      // half the columns each
+      const int64_t r = (seq.q0 + first + qi) * a.q_heads + (int64_t)head * group + row % group;
+      store_row<D / 2>(tmem + lanes + kDQ + D / 2 * w, a.scale, a.dq + r * D + D / 2 * w, live, n == 0);
+    }
+  }
+  finish(ok, tmem, a.status);
+}
+
+size_t stat_bytes(int64_t tq, int32_t q_heads) { return align_up((size_t)tq * q_heads * 4, 256); }
+
+int backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
+             const void* dout, const int32_t* cu_q, const int32_t* cu_k, float scale, void* dq,
+             void* dk, void* dv, const Shape& s, bool use_ws, void* ws, size_t ws_bytes,
+             cudaStream_t st) {
+  if (const int rc = check_shape(s, cu_q, cu_k, scale)) return rc;
+  const int64_t tq = s.tq(), tk = s.tk();
+  if (tq > 0 && (!q || !out || !lse || !dout || !dq)) return GDN_ERR_INVALID_ARG;
+  if (tk > 0 && (!k || !v || !dk || !dv)) return GDN_ERR_INVALID_ARG;
+  const void* v16[] = {q, k, v, out, dout, dq, dk, dv};
+  for (const void* p : v16)
+    if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
+  if (!aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return GDN_ERR_ALIGNMENT;
+  const size_t stat = stat_bytes(tq, s.q_heads), need = 2 * stat;
+  if (use_ws && need) {
+    if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
+    if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
+  }
+  const size_t cu_bytes = ((size_t)s.batch + 1) * 4, io = s.rows() * s.d * 2,
+               kio = (size_t)tk * s.kv_heads * s.d * 2;
+  const Span ins[] = {span_of(q, s.q_bytes()), span_of(k, s.k_bytes(s.k_stride)),
+                      span_of(v, s.k_bytes(s.v_stride)), span_of(cu_q, cu_bytes),
+                      span_of(cu_k, cu_bytes), span_of(out, io), span_of(dout, io),
+                      span_of(lse, s.rows() * 4)};
+  const Span outs[] = {span_of(dq, io), span_of(dk, kio), span_of(dv, kio),
+                       span_of(use_ws ? ws : nullptr, need)};
+  if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
+  if (tq == 0 && tk == 0) return GDN_OK;
+  if (tq == 0)   // keys that no query sees
+    return cudaMemsetAsync(dk, 0, kio, st) == cudaSuccess && cudaMemsetAsync(dv, 0, kio, st) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+  BwdArgs a;
+  memset(&a, 0, sizeof a);
+  a.status = status_ptr();
+  if (!a.status) return GDN_ERR_CUDA;
+  const int32_t group = s.q_heads / s.kv_heads;
+  a.s = {cu_q, cu_k, s.batch, s.seqlen_q, s.seqlen_k, group, s.kv_heads};
+  a.dq = (__nv_bfloat16*)dq;
+  a.dk = (__nv_bfloat16*)dk;
+  a.dv = (__nv_bfloat16*)dv;
+  a.c = scale * kLog2e;
+  a.scale = scale;
+  a.tq = tq;
+  a.q_heads = s.q_heads;
+  a.per = kRows / group;
+  // (no keys: nothing is loaded through their maps)
+  const int64_t width = (int64_t)s.kv_heads * s.d;
+  if (!heads_map(&a.q, q, tq, s.q_heads, s.d, s.q_stride, group, a.per) ||
+      !heads_map(&a.dout, dout, tq, s.q_heads, s.d, (int64_t)s.q_heads * s.d, group, a.per) ||
+      !heads_map(&a.k, tk ? k : q, tk, s.kv_heads, s.d, tk ? s.k_stride : width, 1, kRows) ||
+      !heads_map(&a.v, tk ? v : q, tk, s.kv_heads, s.d, tk ? s.v_stride : width, 1, kRows))
+    return GDN_ERR_CUDA;
+  // packed: upper bounds, sum_n ceil(len_n / per) <= T / per + N
+  const int64_t kt = s.packed ? tk / kRows + s.batch : (s.seqlen_k + kRows - 1) / kRows * s.batch;
+  const int64_t qt = s.packed ? tq / a.per + s.batch : (s.seqlen_q + a.per - 1) / a.per * s.batch;
+  const int64_t row_ctas = ((int64_t)s.rows() * (s.d / 8) + 255) / 256;
+  if (kt * s.kv_heads > 0x7fffffffLL || qt * s.kv_heads > 0x7fffffffLL || row_ctas > 0x7fffffffLL)
+    return GDN_ERR_UNSUPPORTED;
+  void* scratch = ws;
+  if (!use_ws && scratch_alloc(&scratch, need, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  a.nlse = (float*)scratch;
+  a.nd = (float*)((char*)scratch + stat);
+  const RowArgs r = {(const __nv_bfloat16*)out, (const __nv_bfloat16*)dout, lse, (float*)scratch,
+                     (float*)((char*)scratch + stat), tq, s.q_heads, group};
+  cudaError_t e = launch(false, s.d == 128 ? rows_kernel<128> : rows_kernel<64>,
+                         dim3((unsigned)row_ctas), 256, 0, 0, st, r);
+  auto run = [&](auto shape, auto kern, int64_t tiles) {
+    using C = decltype(shape);
+    if (e != cudaSuccess || tiles == 0) return;
+    e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess)
+      e = launch(true, kern, dim3((unsigned)(tiles * s.kv_heads)), kThreads, C::kSmem, 0, st, a);
+    count_launches(1);
+  };
+  if (s.d == 128) {
+    run(Bwd<128>{}, keys_kernel<128>, tk ? kt : 0);
+    run(Bwd<128>{}, queries_kernel<128>, qt);
+  } else {
+    run(Bwd<64>{}, keys_kernel<64>, tk ? kt : 0);
+    run(Bwd<64>{}, queries_kernel<64>, qt);
+  }
+  count_launches(1);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  const cudaError_t f = use_ws ? cudaSuccess : scratch_free(scratch, st);
+  return e == cudaSuccess && f == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+int gdn_attention_prefill_backward(const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const void* dout, const int32_t* cu_q,
+                                   const int32_t* cu_k, float scale, void* dq, void* dk, void* dv,
+                                   int32_t batch, int64_t seqlen_q, int64_t seqlen_k,
+                                   int32_t q_heads, int32_t kv_heads, int32_t d, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, gdn_stream_t stream) {
+  const attn::Shape s = {batch, seqlen_q, seqlen_k, q_heads, kv_heads, d, q_stride, k_stride,
+                         v_stride, cu_q != nullptr};
+  return backward(q, k, v, out, lse, dout, cu_q, cu_k, scale, dq, dk, dv, s, false, nullptr, 0,
+                  (cudaStream_t)stream);
+}
+
+size_t gdn_attention_prefill_backward_workspace_size(int32_t batch, int64_t seqlen_q,
+                                                     int32_t varlen, int32_t q_heads,
+                                                     int32_t kv_heads, int32_t d) {
+  const int32_t some = 0;
+  const int64_t width = (int64_t)q_heads * d;
+  const attn::Shape s = {batch, seqlen_q, 1, q_heads, kv_heads, d, width, width, width, varlen != 0};
+  if (attn::check_shape(s, varlen ? &some : nullptr, varlen ? &some : nullptr, 1.f)) return SIZE_MAX;
+  return 2 * stat_bytes(s.tq(), q_heads);
+}
+
+int gdn_attention_prefill_backward_ws(const void* q, const void* k, const void* v,
+                                      const void* out, const float* lse, const void* dout,
+                                      const int32_t* cu_q, const int32_t* cu_k, float scale,
+                                      void* dq, void* dk, void* dv, int32_t batch,
+                                      int64_t seqlen_q, int64_t seqlen_k, int32_t q_heads,
+                                      int32_t kv_heads, int32_t d, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, void* workspace,
+                                      size_t workspace_bytes, gdn_stream_t stream) {
+  const attn::Shape s = {batch, seqlen_q, seqlen_k, q_heads, kv_heads, d, q_stride, k_stride,
+                         v_stride, cu_q != nullptr};
+  return backward(q, k, v, out, lse, dout, cu_q, cu_k, scale, dq, dk, dv, s, true, workspace,
+                  workspace_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -59,7 +59,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ uint64_t q_full, kv_full[C::kStages], kv_empty[C::kStages], s_full[2], p_half[2],
       p_full[2], o_full[2];
   __shared__ uint32_t tmem_base;
-  __shared__ int64_t scratch[kThreads + 2];
+  __shared__ int64_t scratch[kThreads + 6];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const Seqs& sq = a.s;

@@ -39,7 +39,7 @@ struct Seq {
 
 // The sequence and the tile of job `job` (of one kv head), tiles of `per` tokens of
 // the queries (or keys); the last tile of a sequence first where `down`, as it
-// sees the most keys.  Every thread of the CTA calls it; sm holds 2 + kThreads
+// sees the most keys.  Every thread of the CTA calls it; sm holds kThreads + 6
 // words.  false: no such job, or malformed sequences (the first CTA says so).
 template <int kThreads>
 __device__ bool locate(const Seqs& s, int64_t job, int per, bool keys, bool down, int64_t* sm,
@@ -87,7 +87,8 @@ __device__ bool locate(const Seqs& s, int64_t job, int per, bool keys, bool down
   }
   __syncthreads();
   if (job >= sm[kThreads]) return false;
-  __shared__ Seq found;
+  Seq& found = *reinterpret_cast<Seq*>(sm + kThreads + 2);
+  static_assert(sizeof(Seq) <= 32, "");
   if (job >= sm[tid] && job < sm[tid + 1]) {
     int64_t left = job - sm[tid];
     for (int64_t i = i0; i < i1; ++i) {

@@ -641,6 +641,40 @@ int gdn_attention_prefill(const void* q, const void* k, const void* v, const int
                           gdn_stream_t stream);
 
 /*
+ * gdn_attention_prefill_backward -- gradients of gdn_attention_prefill from
+ * its inputs, its results and dout (the gradient of out):
+ *
+ *   P_ij = exp(s_ij - lse_i), D_i = dout_i . out_i, dS_ij = P_ij (dout_i . v_j - D_i)
+ *   dq_i = scale sum_j dS_ij k_j
+ *   dk_j = scale sum_i dS_ij q_i, dv_j = sum_i P_ij dout_i  (over the group's query heads too)
+ *
+ * out, dout and dq [T_q, q_heads, d], dk and dv [T_k, kv_heads, d], bf16 and
+ * contiguous; q, k, v with strides as above; the rest as above.  P and dS
+ * enter the products rounded to bf16, all sums are fp32 and their order is
+ * fixed.  No output may overlap an input or another output.  Scratch (8 bytes
+ * a token and query head) from the library's pool, or a caller's 256-byte
+ * aligned workspace of at least gdn_attention_prefill_backward_workspace_size
+ * bytes (rules as gdn_prefill_ws).
+ */
+int gdn_attention_prefill_backward(const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const void* dout, const int32_t* cu_q,
+                                   const int32_t* cu_k, float scale, void* dq, void* dk, void* dv,
+                                   int32_t batch, int64_t seqlen_q, int64_t seqlen_k,
+                                   int32_t q_heads, int32_t kv_heads, int32_t d, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, gdn_stream_t stream);
+size_t gdn_attention_prefill_backward_workspace_size(int32_t batch, int64_t seqlen_q,
+                                                     int32_t varlen, int32_t q_heads,
+                                                     int32_t kv_heads, int32_t d);
+int gdn_attention_prefill_backward_ws(const void* q, const void* k, const void* v,
+                                      const void* out, const float* lse, const void* dout,
+                                      const int32_t* cu_q, const int32_t* cu_k, float scale,
+                                      void* dq, void* dk, void* dv, int32_t batch,
+                                      int64_t seqlen_q, int64_t seqlen_k, int32_t q_heads,
+                                      int32_t kv_heads, int32_t d, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, void* workspace,
+                                      size_t workspace_bytes, gdn_stream_t stream);
+
+/*
  * The paged cache of keys and values, shared by `layers` attention layers.
  * A row is a sequence: lengths[row] tokens on the pages that table[row][0],
  * table[row][1], ... name, page tokens each; entries behind the last page are
