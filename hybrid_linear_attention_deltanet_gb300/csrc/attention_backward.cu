@@ -138,6 +138,37 @@ __device__ __forceinline__ void store_row(uint32_t at, float f, __nv_bfloat16* t
   }
 }
 
+// Two elements: 2^(x c + l); (x + d) p; and 64 columns' masks and their way back
+// to tensor memory.  (The masks apart, behind a branch: selects in the loops above
+// were half of their instructions.)
+__device__ __forceinline__ void exp_pair(uint32_t& x0, uint32_t& x1, F2 c, F2 l) {
+  float y0, y1;
+  f2_split(f2_fma(f2(__uint_as_float(x0), __uint_as_float(x1)), c, l), y0, y1);
+  x0 = __float_as_uint(ex2_sfu(y0));
+  x1 = __float_as_uint(ex2_sfu(y1));
+}
+__device__ __forceinline__ void times_less(uint32_t& x0, uint32_t& x1, F2 d, uint32_t p0, uint32_t p1) {
+  float y0, y1;
+  f2_split(f2_mul(f2_add(f2(__uint_as_float(x0), __uint_as_float(x1)), d),
+                  f2(__uint_as_float(p0), __uint_as_float(p1))),
+           y0, y1);
+  x0 = __float_as_uint(y0);
+  x1 = __float_as_uint(y1);
+}
+__device__ __forceinline__ void keep_columns(uint32_t (&x)[2][32], int lo, int hi) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (32 * h + i < lo || 32 * h + i >= hi) x[h][i] = 0;
+}
+__device__ __forceinline__ void put_bf16(uint32_t at, const uint32_t (&x)[32]) {
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+  tmem_st16(at, p);
+}
+
 // The common part of both kernels: the job's place, barriers, tensor memory.
 template <int D>
 __device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, int per, bool keys, Seq& seq,
@@ -393,28 +424,16 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(s[h]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[16];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 l4 = *reinterpret_cast<const float4*>(st + 32 * h + x);
-          float y[4];
-          f2_split(f2_fma(f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1])), cc, f2(l4.x, l4.y)),
-                   y[0], y[1]);
-          f2_split(f2_fma(f2(__uint_as_float(s[h][x + 2]), __uint_as_float(s[h][x + 3])), cc,
-                          f2(l4.z, l4.w)),
-                   y[2], y[3]);
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            float e = ex2_sfu(y[z]);
-            if (masked && (32 * h + x + z < lo || 32 * h + x + z >= hi)) e = 0.f;
-            s[h][x + z] = __float_as_uint(e);
-          }
-          p[x / 2] = pack(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1]));
-          p[x / 2 + 1] = pack(__uint_as_float(s[h][x + 2]), __uint_as_float(s[h][x + 3]));
+          exp_pair(s[h][x], s[h][x + 1], cc, f2(l4.x, l4.y));
+          exp_pair(s[h][x + 2], s[h][x + 3], cc, f2(l4.z, l4.w));
         }
-        tmem_st16(s_at + 16 * h, p);
-      }
+      if (masked) keep_columns(s, lo, hi);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) put_bf16(s_at + 16 * h, s[h]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -428,27 +447,16 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(g[h]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[16];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 d4 = *reinterpret_cast<const float4*>(st + 64 + 32 * h + x);
-          float y[4];
-          f2_split(f2_mul(f2_add(f2(__uint_as_float(g[h][x]), __uint_as_float(g[h][x + 1])), f2(d4.x, d4.y)),
-                          f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1]))),
-                   y[0], y[1]);
-          f2_split(f2_mul(f2_add(f2(__uint_as_float(g[h][x + 2]), __uint_as_float(g[h][x + 3])),
-                                 f2(d4.z, d4.w)),
-                          f2(__uint_as_float(s[h][x + 2]), __uint_as_float(s[h][x + 3]))),
-                   y[2], y[3]);
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            if (masked && (32 * h + x + z < lo || 32 * h + x + z >= hi)) y[z] = 0.f;
-          p[x / 2] = pack(y[0], y[1]);
-          p[x / 2 + 1] = pack(y[2], y[3]);
+          times_less(g[h][x], g[h][x + 1], f2(d4.x, d4.y), s[h][x], s[h][x + 1]);
+          times_less(g[h][x + 2], g[h][x + 3], f2(d4.z, d4.w), s[h][x + 2], s[h][x + 3]);
         }
-        tmem_st16(dp_at + 16 * h, p);
-      }
+      if (masked) keep_columns(g, lo, hi);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) put_bf16(dp_at + 16 * h, g[h]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -625,12 +633,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float y0, y1;
-          f2_split(f2_fma(f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1])), cc, ll), y0, y1);
-          s[h][x] = __float_as_uint(ex2_sfu(y0));
-          s[h][x + 1] = __float_as_uint(ex2_sfu(y1));
-        }
+        for (int x = 0; x < 32; x += 2) exp_pair(s[h][x], s[h][x + 1], cc, ll);
       ok = mbar_wait_warp(&b.dp_full, (uint32_t)(j & 1), kWaitNs);
       if (!ok) break;
       tc_fence_after();
@@ -640,20 +643,13 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(g[h]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[16];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float y0, y1;
-          f2_split(f2_mul(f2_add(f2(__uint_as_float(g[h][x]), __uint_as_float(g[h][x + 1])), dd),
-                          f2(__uint_as_float(s[h][x]), __uint_as_float(s[h][x + 1]))),
-                   y0, y1);
-          if (masked && 32 * h + x > see) y0 = 0.f;
-          if (masked && 32 * h + x + 1 > see) y1 = 0.f;
-          p[x / 2] = pack(y0, y1);
-        }
-        tmem_st16(s_at + 16 * h, p);
-      }
+        for (int x = 0; x < 32; x += 2)
+          times_less(g[h][x], g[h][x + 1], dd, s[h][x], s[h][x + 1]);
+      if (masked) keep_columns(g, 0, see + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) put_bf16(s_at + 16 * h, g[h]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
