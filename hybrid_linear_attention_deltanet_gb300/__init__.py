@@ -960,6 +960,7 @@ def gated_ffn_backward(x, w_gate, w_up, dh, act="silu", stream=None, workspace=N
 
 
 # ---------------------------------------------------------------------------
+# (Calls go through _layer_calls first, as above.)
 # The attention layers that a hybrid keeps among its Gated DeltaNet layers, and
 # the paged cache that they share.
 def _token_rows(t, name, index):
@@ -1031,6 +1032,10 @@ def attention_prefill(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None, o
     context.  q, k and v may be slices of a packed projection (heads
     contiguous, tokens evenly spaced).  Returns (out like q, contiguous; lse
     [.., T, q_heads] fp32); a row that sees no key has out 0 and lse -inf."""
+    if out is None and lse is None and stream is None:
+        done = _direct_calls().attention_prefill(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+        if done is not None:
+            return done
     index, sizes, cu, scale = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, scale)
     out = (torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else
            _out(out, "out", q.shape, q.dtype, index))
@@ -1055,6 +1060,11 @@ def attention_prefill_backward(q, k, v, out, lse, dout, cu_seqlens=None, cu_seql
     """Gradients of :func:`attention_prefill` from its inputs, its results and
     dout (``gdn_attention_prefill_backward``).  Returns dict dq, dk, dv (bf16,
     contiguous)."""
+    if stream is None and workspace is None:
+        done = _direct_calls().attention_prefill_backward(q, k, v, cu_seqlens, cu_seqlens_k, scale,
+                                                          out, lse, dout)
+        if done is not None:
+            return dict(dq=done[0], dk=done[1], dv=done[2])
     index, sizes, cu, scale = _attention_inputs(q, k, v, cu_seqlens, cu_seqlens_k, scale)
     for name, t in (("out", out), ("dout", dout)):
         _out(t, name, q.shape, torch.bfloat16, index)
@@ -1157,6 +1167,10 @@ def cache_reserve(cache, counts, start=None, stream=None):
     row's first new position (-1 where the pool or the row's table had no
     room; :func:`device_status` then says so)."""
     index, at = _cache(cache)
+    if start is None and stream is None:
+        done = _direct_calls().cache_reserve(at, index, counts)
+        if done is not None:
+            return done
     _out(counts, "counts", cache.lengths.shape, torch.int32, index)
     start = (torch.empty_like(counts) if start is None else
              _out(start, "start", counts.shape, torch.int32, index))
@@ -1170,6 +1184,8 @@ def cache_append(cache, k, v, start, cu_seqlens=None, layer=0, stream=None):
     (``gdn_cache_append``): one token a row, or row r's tokens
     cu_seqlens[r] .. cu_seqlens[r + 1]."""
     index, at = _cache(cache)
+    if stream is None and _direct_calls().cache_append(at, index, k, v, start, cu_seqlens, layer):
+        return
     heads, d, ks = _token_rows(k, "k", index)
     _, _, vs = _token_rows(v, "v", index)
     if k.dim() != 3 or k.shape != v.shape or (heads, d) != (cache.k.shape[2], cache.k.shape[4]):
@@ -1188,6 +1204,8 @@ def cache_free(cache, rows, stream=None):
     """Empties the named rows (int32) and gives their pages back
     (``gdn_cache_free``)."""
     index, at = _cache(cache)
+    if stream is None and _direct_calls().cache_free(at, index, rows):
+        return
     n = _row_numbers(rows, "rows", index)
     _call("gdn_cache_free", index, stream, at, rows.data_ptr(), n)
 
@@ -1197,6 +1215,8 @@ def cache_fork(cache, src, dst, stream=None):
     (``gdn_cache_fork``): full pages are shared, a last page that is not full is
     copied, in all layers."""
     index, at = _cache(cache)
+    if stream is None and _direct_calls().cache_fork(at, index, src, dst):
+        return
     n = _row_numbers(src, "src", index)
     if _row_numbers(dst, "dst", index) != n:
         raise ValueError("src and dst must name as many rows")
@@ -1209,6 +1229,8 @@ def cache_compact(cache, into, stream=None):
     stays as it is.  Returns ``into``."""
     index, at = _cache(cache)
     other, to = _cache(into)
+    if stream is None and _direct_calls().cache_compact(at, index, to, other):
+        return into
     if other != index:
         raise ValueError("the two caches are on different devices")
     _call("gdn_cache_compact", index, stream, at, to)
@@ -1227,6 +1249,10 @@ def attention_decode_step(q, cache, layer=0, scale=None, out=None, stream=None, 
     values of one layer (``gdn_attention_decode_step``): q [rows, q_heads, d]
     bf16.  Returns out like q; 0 for an empty row."""
     index, at = _cache(cache)
+    if out is None and stream is None and workspace is None:
+        done = _direct_calls().attention_decode_step(at, index, q, layer, scale)
+        if done is not None:
+            return done
     _need(q, "q", torch.bfloat16, index)
     rows, d = cache.lengths.shape[0], cache.k.shape[4]
     if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d:

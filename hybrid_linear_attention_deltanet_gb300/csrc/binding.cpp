@@ -1,4 +1,4 @@
-// The layer operators' calls from Python for the ordinary case: tensors in,
+// The layer operators' and the attention's calls from Python for the ordinary case: tensors in,
 // new tensors out, on the current stream.  A decoding step makes these calls
 // for single tokens, where the interpreter's checks and allocations took
 // longer than the kernels (8-bit norm of one token: 17.7 us a call through
@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
+#include <cmath>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -28,6 +29,14 @@ struct Library {
   decltype(&gdn_linear_fp8) linear_fp8 = nullptr;
   decltype(&gdn_gated_ffn) gated_ffn = nullptr;
   decltype(&gdn_gated_ffn_backward) gated_ffn_backward = nullptr;
+  decltype(&gdn_attention_prefill) attention_prefill = nullptr;
+  decltype(&gdn_attention_prefill_backward) attention_prefill_backward = nullptr;
+  decltype(&gdn_attention_decode_step) attention_decode_step = nullptr;
+  decltype(&gdn_cache_reserve) cache_reserve = nullptr;
+  decltype(&gdn_cache_append) cache_append = nullptr;
+  decltype(&gdn_cache_free) cache_free = nullptr;
+  decltype(&gdn_cache_fork) cache_fork = nullptr;
+  decltype(&gdn_cache_compact) cache_compact = nullptr;
   bool ready = false;
 } lib;
 
@@ -322,6 +331,249 @@ PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------- attention
+// bf16 [.., T, heads, d] whose heads are contiguous and whose tokens are evenly
+// spaced, on the current device, not empty
+struct Tokens {
+  const at::Tensor* t = nullptr;
+  int64_t batch = 0, tokens = 0, heads = 0, d = 0, step = 0;
+};
+bool tokens_in(PyObject* o, c10::DeviceIndex index, Tokens& v) {
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != index ||
+      t.scalar_type() != at::kBFloat16 || (t.dim() != 3 && t.dim() != 4) || t.numel() < 1)
+    return false;
+  const int n = (int)t.dim();
+  v = {&t, n == 4 ? t.size(0) : 1, t.size(n - 3), t.size(n - 2), t.size(n - 1), 0};
+  v.step = v.heads * v.d;
+  if (v.tokens > 1) v.step = t.stride(n - 3);
+  else if (v.batch > 1) v.step = t.stride(0);
+  return t.stride(n - 1) == 1 && (v.heads == 1 || t.stride(n - 2) == v.d) &&
+         v.step >= v.heads * v.d &&
+         (v.batch == 1 || v.tokens == 1 || t.stride(0) == v.tokens * v.step);
+}
+bool number(PyObject* o, double& v) {
+  v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    return false;
+  }
+  return true;
+}
+
+// (q, k, v, cu_seqlens or None, cu_seqlens_k or None, scale or None)
+struct AttnIn {
+  Tokens q, k, v;
+  const int32_t *cu_q = nullptr, *cu_k = nullptr;
+  int32_t batch = 0;
+  double scale = 0;
+  c10::DeviceIndex index = 0;
+};
+bool attn_in(PyObject* const* a, AttnIn& v) {
+  if (!lib.ready) return false;
+  v.index = device_of(a[0]);
+  if (v.index < 0) return false;
+  if (!tokens_in(a[0], v.index, v.q) || !tokens_in(a[1], v.index, v.k) ||
+      !tokens_in(a[2], v.index, v.v))
+    return false;
+  if (v.q.t->dim() != v.k.t->dim() || v.k.t->sizes() != v.v.t->sizes() || v.k.d != v.q.d ||
+      v.q.batch != v.k.batch || v.q.d > INT32_MAX || v.q.heads > INT32_MAX)
+    return false;
+  int64_t n = v.q.batch;
+  if (a[3] != Py_None) {
+    const at::Tensor* cq = plain(a[3], at::kInt, v.index);
+    const at::Tensor* ck = a[4] == Py_None ? cq : plain(a[4], at::kInt, v.index);
+    if (!cq || !ck || cq->dim() != 1 || cq->size(0) < 2 || cq->sizes() != ck->sizes() || n != 1)
+      return false;
+    if (a[4] == Py_None && v.q.tokens != v.k.tokens) return false;
+    n = cq->size(0) - 1;
+    v.cu_q = (const int32_t*)cq->data_ptr();
+    v.cu_k = (const int32_t*)ck->data_ptr();
+  } else if (a[4] != Py_None) {
+    return false;
+  }
+  if (n > INT32_MAX) return false;
+  v.batch = (int32_t)n;
+  if (a[5] == Py_None) v.scale = 1.0 / std::sqrt((double)v.q.d);
+  else if (!number(a[5], v.scale)) return false;
+  return true;
+}
+
+PyObject* attention_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  AttnIn v;
+  if (n != 6 || !attn_in(a, v)) return none();
+  const at::Tensor& q = *v.q.t;
+  at::Tensor out = like(q);
+  at::Tensor lse = make(q, q.sizes().slice(0, q.dim() - 1), at::kFloat);
+  const gdn_stream_t st = stream_of(v.index);
+  if (!call([&] {
+        return lib.attention_prefill(ptr(v.q.t), ptr(v.k.t), ptr(v.v.t), v.cu_q, v.cu_k,
+                                     (float)v.scale, out.data_ptr(), (float*)lse.data_ptr(),
+                                     v.batch, v.q.tokens, v.k.tokens, (int32_t)v.q.heads,
+                                     (int32_t)v.k.heads, (int32_t)v.q.d, v.q.step, v.k.step,
+                                     v.v.step, st);
+      }))
+    return none();
+  return pack({wrap(out), wrap(lse)});
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, cu_seqlens, cu_seqlens_k, scale, out, lse, dout) -> (dq, dk, dv)
+PyObject* attention_prefill_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  AttnIn v;
+  if (n != 9 || !attn_in(a, v)) return none();
+  const at::Tensor *out = plain(a[6], at::kBFloat16, v.index),
+                   *lse = plain(a[7], at::kFloat, v.index),
+                   *dout = plain(a[8], at::kBFloat16, v.index);
+  const at::Tensor& q = *v.q.t;
+  if (!out || !lse || !dout || out->sizes() != q.sizes() || dout->sizes() != q.sizes() ||
+      lse->sizes() != q.sizes().slice(0, q.dim() - 1))
+    return none();
+  at::Tensor dq = like(q);
+  at::Tensor dk = like(*v.k.t);
+  at::Tensor dv = like(*v.v.t);
+  const gdn_stream_t st = stream_of(v.index);
+  if (!call([&] {
+        return lib.attention_prefill_backward(
+            ptr(v.q.t), ptr(v.k.t), ptr(v.v.t), ptr(out), (const float*)ptr(lse), ptr(dout),
+            v.cu_q, v.cu_k, (float)v.scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), v.batch,
+            v.q.tokens, v.k.tokens, (int32_t)v.q.heads, (int32_t)v.k.heads, (int32_t)v.q.d,
+            v.q.step, v.k.step, v.v.step, st);
+      }))
+    return none();
+  return pack({wrap(dq), wrap(dk), wrap(dv)});
+  END_HANDLE_TH_ERRORS
+}
+
+// A KVCache as (address of its gdn_kv_cache, its device), the current device's.
+const gdn_kv_cache* cache_in(PyObject* address, PyObject* device, c10::DeviceIndex& index) {
+  if (!lib.ready || !PyLong_CheckExact(address)) return nullptr;
+  const long d = int_arg(device, -1);
+  if (d < 0 || d != c10::cuda::current_device()) return nullptr;
+  index = (c10::DeviceIndex)d;
+  void* p = PyLong_AsVoidPtr(address);
+  if (!p) PyErr_Clear();
+  return (const gdn_kv_cache*)p;
+}
+const int32_t* row_ints(PyObject* o, c10::DeviceIndex index, int64_t n) {
+  const at::Tensor* t = plain(o, at::kInt, index);
+  return t && is_vector(*t, n) ? (const int32_t*)t->data_ptr() : nullptr;
+}
+PyObject* done(bool ok) { return PyBool_FromLong(ok); }
+
+// (cache, device, q, layer, scale or None) -> out
+PyObject* attention_decode_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index;
+  const gdn_kv_cache* c = n == 5 ? cache_in(a[0], a[1], index) : nullptr;
+  if (!c) return none();
+  const at::Tensor* q = plain(a[2], at::kBFloat16, index);
+  const long layer = int_arg(a[3], -1);
+  if (!q || q->dim() != 3 || q->size(0) != c->rows || q->size(2) != c->d || layer < 0 ||
+      layer >= c->layers || q->size(1) > INT32_MAX)
+    return none();
+  double scale = 1.0 / std::sqrt((double)c->d);
+  if (a[4] != Py_None && !number(a[4], scale)) return none();
+  at::Tensor out = like(*q);
+  const gdn_stream_t st = stream_of(index);
+  if (!call([&] {
+        return lib.attention_decode_step(ptr(q), c, (int32_t)layer, (int32_t)q->size(1),
+                                         (float)scale, out.data_ptr(), st);
+      }))
+    return none();
+  return wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, device, counts) -> start
+PyObject* cache_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index;
+  const gdn_kv_cache* c = n == 3 ? cache_in(a[0], a[1], index) : nullptr;
+  const int32_t* counts = c ? row_ints(a[2], index, c->rows) : nullptr;
+  if (!counts) return none();
+  at::Tensor start = like(THPVariable_Unpack(a[2]));
+  const gdn_stream_t st = stream_of(index);
+  if (!call([&] { return lib.cache_reserve(c, counts, (int32_t*)start.data_ptr(), st); }))
+    return none();
+  return wrap(start);
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, device, k, v, start, cu_seqlens or None, layer) -> True
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index;
+  const gdn_kv_cache* c = n == 7 ? cache_in(a[0], a[1], index) : nullptr;
+  if (!c) return none();
+  Tokens k, v;
+  const int32_t* start = row_ints(a[4], index, c->rows);
+  const int32_t* cu = a[5] == Py_None ? nullptr : row_ints(a[5], index, (int64_t)c->rows + 1);
+  const long layer = int_arg(a[6], -1);
+  if (!start || (a[5] != Py_None && !cu) || layer < 0 || layer >= c->layers ||
+      !tokens_in(a[2], index, k) || !tokens_in(a[3], index, v) || k.t->dim() != 3 ||
+      k.t->sizes() != v.t->sizes() || k.heads != c->kv_heads || k.d != c->d ||
+      (!cu && k.tokens != c->rows))
+    return none();
+  const gdn_stream_t st = stream_of(index);
+  return call([&] {
+           return lib.cache_append(c, (int32_t)layer, ptr(k.t), ptr(v.t), start, cu, k.tokens,
+                                   k.step, v.step, st);
+         })
+             ? done(true)
+             : none();
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, device, rows) -> True
+PyObject* cache_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index;
+  const gdn_kv_cache* c = n == 3 ? cache_in(a[0], a[1], index) : nullptr;
+  const at::Tensor* rows = c ? plain(a[2], at::kInt, index) : nullptr;
+  if (!rows || rows->dim() != 1 || rows->size(0) > INT32_MAX) return none();
+  const gdn_stream_t st = stream_of(index);
+  return call([&] {
+           return lib.cache_free(c, (const int32_t*)ptr(rows), (int32_t)rows->size(0), st);
+         })
+             ? done(true)
+             : none();
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, device, src, dst) -> True
+PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index;
+  const gdn_kv_cache* c = n == 4 ? cache_in(a[0], a[1], index) : nullptr;
+  const at::Tensor* src = c ? plain(a[2], at::kInt, index) : nullptr;
+  if (!src || src->dim() != 1 || src->size(0) > INT32_MAX) return none();
+  const int32_t* dst = row_ints(a[3], index, src->size(0));
+  if (!dst) return none();
+  const gdn_stream_t st = stream_of(index);
+  return call([&] {
+           return lib.cache_fork(c, (const int32_t*)ptr(src), dst, (int32_t)src->size(0), st);
+         })
+             ? done(true)
+             : none();
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, device, into, its device) -> True
+PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index, other;
+  const gdn_kv_cache* c = n == 4 ? cache_in(a[0], a[1], index) : nullptr;
+  const gdn_kv_cache* d = c ? cache_in(a[2], a[3], other) : nullptr;
+  if (!d) return none();
+  const gdn_stream_t st = stream_of(index);
+  return call([&] { return lib.cache_compact(c, d, st); }) ? done(true) : none();
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(path of the library, already loaded): looks its functions up
 PyObject* bind(PyObject*, PyObject* path) {
   const char* p = PyUnicode_AsUTF8(path);
@@ -343,6 +595,14 @@ PyObject* bind(PyObject*, PyObject* path) {
   find(lib.linear_fp8, "gdn_linear_fp8");
   find(lib.gated_ffn, "gdn_gated_ffn");
   find(lib.gated_ffn_backward, "gdn_gated_ffn_backward");
+  find(lib.attention_prefill, "gdn_attention_prefill");
+  find(lib.attention_prefill_backward, "gdn_attention_prefill_backward");
+  find(lib.attention_decode_step, "gdn_attention_decode_step");
+  find(lib.cache_reserve, "gdn_cache_reserve");
+  find(lib.cache_append, "gdn_cache_append");
+  find(lib.cache_free, "gdn_cache_free");
+  find(lib.cache_fork, "gdn_cache_fork");
+  find(lib.cache_compact, "gdn_cache_compact");
   lib.ready = ok;
   if (!ok) {
     PyErr_Format(PyExc_ImportError, "%s lacks an entry point", p);
@@ -362,10 +622,18 @@ PyMethodDef methods[] = {
     GDN_CALL(linear_fp8),
     GDN_CALL(gated_ffn),
     GDN_CALL(gated_ffn_backward),
+    GDN_CALL(attention_prefill),
+    GDN_CALL(attention_prefill_backward),
+    GDN_CALL(attention_decode_step),
+    GDN_CALL(cache_reserve),
+    GDN_CALL(cache_append),
+    GDN_CALL(cache_free),
+    GDN_CALL(cache_fork),
+    GDN_CALL(cache_compact),
     {nullptr, nullptr, 0, nullptr}};
 #undef GDN_CALL
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_calls",
-                      "Direct calls of the layer operators (None: take the general path).", -1,
+                      "Direct calls of the operators (None: take the general path).", -1,
                       methods};
 
 }  // namespace
