@@ -35,8 +35,20 @@ struct FwdArgs {
   float* lse;
   float c;                 // scale log2 e
   int32_t q_heads, per;    // per: queries of a 128-row tile
+  // kListed: the jobs
+  const int32_t* count;
+  uint32_t* next;
+  const Job* jobs;
+  // kParts: what the parts of a job leave for join_kernel, [jobs][parts][256 rows]
+  int32_t parts;
+  float2* ml;              // maximum (in powers of two) and sum, 0 where the part saw no key
+  float* o;                // [..][D]
   unsigned* status;
 };
+
+// How a CTA comes to its work: kOnce, one job each; kParts, blockIdx.y's part of
+// a job's keys; kListed, persistent CTAs take the next job of a list.
+enum Mode { kOnce, kParts, kListed };
 
 template <int D>
 struct Fwd {
@@ -50,25 +62,69 @@ struct Fwd {
 // 128 rows x 64 columns a half, K-major: 16 columns a step
 __device__ __forceinline__ uint32_t kstep(int s) { return (s >> 2) * kTileBytes + (s & 3) * 32; }
 
-template <int D>
+// What every warp derives from a job: two tiles' first queries, their numbers,
+// and the blocks of 128 keys [begin, end) that this CTA goes over.
+struct Place {
+  int64_t q0, k0;
+  int32_t lk, shift, first[2], rows[2], blocks[2], begin, most;
+  // (indexed by selection: a tile's number is no constant in the softmax warps)
+  __device__ __forceinline__ int32_t first_of(int w) const { return w ? first[1] : first[0]; }
+  __device__ __forceinline__ int32_t rows_of(int w) const { return w ? rows[1] : rows[0]; }
+  __device__ __forceinline__ int32_t blocks_of(int w) const { return w ? blocks[1] : blocks[0]; }
+  __device__ __forceinline__ Place(const Seq& s, int per, int part, int parts) {
+    q0 = s.q0;
+    k0 = s.k0;
+    lk = s.lk;
+    shift = s.lk - s.lq;
+    int32_t n[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      first[w] = s.tile * 2 * per + w * per;
+      const int32_t left = s.lq - first[w];
+      rows[w] = left < 0 ? 0 : left < per ? left : per;
+      const int32_t seen = rows[w] ? first[w] + rows[w] + shift : 0;   // keys that the last row sees
+      n[w] = seen > 0 ? (seen + kRows - 1) / kRows : 0;
+    }
+    const int32_t all = n[1] > n[0] ? n[1] : n[0];
+    begin = parts > 1 ? (int32_t)((int64_t)all * part / parts) : 0;
+    const int32_t end = parts > 1 ? (int32_t)((int64_t)all * (part + 1) / parts) : all;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int32_t e = n[w] < end ? n[w] : end;
+      blocks[w] = e > begin ? e - begin : 0;
+    }
+    most = end - begin;
+  }
+};
+
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ FwdArgs a) {
   using C = Fwd<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
-  __shared__ uint64_t q_full, kv_full[C::kStages], kv_empty[C::kStages], s_full[2], p_half[2],
-      p_full[2], o_full[2];
+  __shared__ uint64_t q_full, q_empty, kv_full[C::kStages], kv_empty[C::kStages], s_full[2],
+      p_half[2], p_full[2], o_full[2], job_full[2], job_empty[2];
   __shared__ uint32_t tmem_base;
-  __shared__ int64_t scratch[kThreads + 6];
+  __shared__ int64_t scratch[kMode == kListed ? 1 : kThreads + 6];
+  __shared__ Seq slots[2];
+  __shared__ int32_t slot_head[2];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const Seqs& sq = a.s;
-  const int head = blockIdx.x % sq.kv_heads;
-  Seq seq;
-  if (!locate<kThreads>(sq, blockIdx.x / sq.kv_heads, 2 * a.per, false, true, scratch, a.status, seq))
-    return;
+  grid_release_next();
+  if constexpr (kMode != kListed) {
+    Seq seq;
+    if (!locate<kThreads>(sq, blockIdx.x / sq.kv_heads, 2 * a.per, false, true, scratch, a.status, seq))
+      return;
+    if (tid == 0) {
+      slots[0] = seq;
+      slot_head[0] = blockIdx.x % sq.kv_heads;
+    }
+  }
   if (tid == 0) {
     mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
@@ -78,6 +134,8 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
+      mbar_init(&job_full[i], 1);
+      mbar_init(&job_empty[i], 9);
     }
     fence_barrier_init();
   }
@@ -90,122 +148,179 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (kMode == kListed) grid_wait();
   const uint32_t tmem = tmem_base;
-
-  // a tile's first query, its queries, and its blocks of 128 keys
-  const int32_t shift = seq.lk - seq.lq;
-  int32_t first[2], rows[2], blocks[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    first[w] = seq.tile * 2 * a.per + w * a.per;
-    const int32_t left = seq.lq - first[w];
-    rows[w] = left < 0 ? 0 : left < a.per ? left : a.per;
-    const int32_t seen = rows[w] ? first[w] + rows[w] + shift : 0;   // keys that the last row sees
-    blocks[w] = seen > 0 ? (seen + kRows - 1) / kRows : 0;
-  }
-  const int32_t most = blocks[1] > blocks[0] ? blocks[1] : blocks[0];
+  const int part = kMode == kParts ? blockIdx.y : 0, parts = kMode == kParts ? a.parts : 1;
   bool ok = true;
+
+  // The next job for a warp that multiplies or takes exponentials (`n` counts
+  // them): false when there is none.  It stays in its slot until release().
+  auto take = [&](uint32_t n, Seq& s) {
+    if constexpr (kMode != kListed) {
+      if (n > 0) return false;
+      s = slots[0];
+      return true;
+    } else {
+      ok = mbar_wait_warp(&job_full[n & 1], (n >> 1) & 1, kWaitNs);
+      if (!ok) return false;
+      s = slots[n & 1];
+      return s.tile >= 0;
+    }
+  };
+  auto release = [&](uint32_t n) {
+    if constexpr (kMode == kListed) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&job_empty[n & 1]);
+    }
+  };
 
   // 384 threads launch with 168 registers each, 64512 in all, which is 256 x 216
   // + 128 x 72: a softmax thread holds a row's 128 scores
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 9) {
-    // ------------------------------------------------------------- load
-    const bool lead = elect_one();
-    if (lead && most > 0) {
-      const uint32_t box = (uint32_t)(a.per * sq.group) * 128 * C::kHalves;
-      mbar_arrive_expect_tx(&q_full, 2 * box);
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          tma_load_3d(sm + w * C::kTile + h * kTileBytes, &a.q, 64 * h, head * sq.group,
-                      (int32_t)(seq.q0 + first[w]), &q_full);
-    }
-    int st = 0;
-    uint32_t ph = 0;
-    for (int32_t j = 0; ok && j < most; ++j) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        ok = ok && mbar_wait_warp(&kv_empty[st], ph ^ 1u, kWaitNs);
-        if (ok && lead) {
-          uint8_t* to = sm + (2 + st) * C::kTile;
-          mbar_arrive_expect_tx(&kv_full[st], C::kTile);
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_3d(to + h * kTileBytes, x ? &a.v : &a.k, 64 * h, head,
-                        (int32_t)(seq.k0 + (int64_t)j * kRows), &kv_full[st]);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 9) {
+      // ----------------------------------------------------------- load
+      const bool lead = elect_one();
+      uint32_t kv = 0, jobs_done = 0;     // loads so far; jobs with keys so far
+      for (uint32_t n = 0; ok; ++n) {
+        Seq seq;
+        int head;
+        if constexpr (kMode == kListed) {
+          int64_t at = 0;
+          if (lane == 0) at = atomicAdd(a.next, 1u);
+          at = __shfl_sync(0xffffffffu, at, 0);
+          ok = mbar_wait_warp(&job_empty[n & 1], ((n >> 1) & 1) ^ 1u, kWaitNs);
+          if (!ok) break;
+          int32_t count;
+          asm volatile("ld.global.s32 %0, [%1];" : "=r"(count) : "l"(a.count));
+          const bool more = at < (int64_t)count * sq.kv_heads;
+          seq.tile = -1;
+          head = 0;
+          if (more) {
+            const int64_t i = at / sq.kv_heads;
+            head = (int)(at - i * sq.kv_heads);
+            const uint4 x = ld_waited(reinterpret_cast<const uint4*>(a.jobs + i));
+            const int32_t tile = ld_waited(&a.jobs[i].tile);
+            seq = {(int32_t)x.x, (int32_t)x.y, (int32_t)x.z, (int32_t)x.w, tile};
+          }
+          if (lane == 0) {
+            slots[n & 1] = seq;
+            slot_head[n & 1] = head;
+            mbar_arrive(&job_full[n & 1]);
+          }
+          __syncwarp();
+          if (!more) break;
+        } else {
+          if (!take(n, seq)) break;
+          head = slot_head[0];
         }
-        __syncwarp();
-        if (++st == C::kStages) {
-          st = 0;
-          ph ^= 1u;
+        const Place pl(seq, a.per, part, parts);
+        if (pl.most == 0) continue;
+        ok = mbar_wait_warp(&q_empty, (jobs_done & 1) ^ 1u, kWaitNs);
+        if (!ok) break;
+        ++jobs_done;
+        if (lead) {
+          const uint32_t box = (uint32_t)(a.per * sq.group) * 128 * C::kHalves;
+          mbar_arrive_expect_tx(&q_full, 2 * box);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_3d(sm + w * C::kTile + h * kTileBytes, &a.q, 64 * h, head * sq.group,
+                          (int32_t)(pl.q0 + pl.first[w]), &q_full);
+        }
+        for (int32_t j = 0; ok && j < pl.most; ++j) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t st = kv % C::kStages;
+            ok = ok && mbar_wait_warp(&kv_empty[st], ((kv / C::kStages) & 1) ^ 1u, kWaitNs);
+            if (ok && lead) {
+              uint8_t* to = sm + (2 + st) * C::kTile;
+              mbar_arrive_expect_tx(&kv_full[st], C::kTile);
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_3d(to + h * kTileBytes, x ? &a.v : &a.k, 64 * h, head,
+                            (int32_t)(pl.k0 + (int64_t)(pl.begin + j) * kRows), &kv_full[st]);
+            }
+            __syncwarp();
+            ++kv;
+          }
         }
       }
-    }
-  } else if (warp == 8) {
-    // --------------------------------------------------------- multiply
-    const bool lead = elect_one();
-    const uint32_t base = smem_u32(sm);
-    constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kOut = idesc_bf16(128, D, 0, 1);
-    const uint64_t qd = smem_desc(base, 16, 1024, kSwizzle128B);
-    const uint64_t kd = smem_desc(base + 2 * C::kTile, 16, 1024, kSwizzle128B);
-    const uint64_t vd = smem_desc(base + 2 * C::kTile, kTileBytes, 1024, kSwizzle128B);
-    if (most > 0) ok = mbar_wait_warp(&q_full, 0, kWaitNs);
-    // step j: P V of block j - 1, then Q K^T of block j; a block's K is loaded
-    // one stage before its V
-    for (int32_t j = 0; ok && j <= most; ++j) {
-      const int k_st = (int)((2 * (int64_t)j) % C::kStages);
-      const int v_st = (int)((2 * (int64_t)j - 1 + C::kStages) % C::kStages);
-      if (j < most) ok = mbar_wait_warp(&kv_full[k_st], (uint32_t)((2 * (int64_t)j / C::kStages) & 1), kWaitNs);
-      if (ok && j > 0) {
-        ok = mbar_wait_warp(&kv_full[v_st], (uint32_t)(((2 * (int64_t)j - 1) / C::kStages) & 1), kWaitNs);
-        // values behind the sequence's last one are another's: a product
-        // with a zero probability has to be zero
-        const int64_t valid = seq.lk - (int64_t)(j - 1) * kRows;
-        if (ok && valid < kRows) {
-          for (int h = 0; h < C::kHalves; ++h) {
-            uint4* z = reinterpret_cast<uint4*>(sm + (2 + v_st) * C::kTile + h * kTileBytes);
-            for (int i = (int)valid * 8 + lane; i < kRows * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+    } else if (warp == 8) {
+      // ------------------------------------------------------- multiply
+      const bool lead = elect_one();
+      const uint32_t base = smem_u32(sm);
+      constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kOut = idesc_bf16(128, D, 0, 1);
+      uint64_t qd = smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t kd = smem_desc(base + 2 * C::kTile, 16, 1024, kSwizzle128B);
+      const uint64_t vd = smem_desc(base + 2 * C::kTile, kTileBytes, 1024, kSwizzle128B);
+      uint32_t kv = 0, jobs_done = 0, probs[2] = {0, 0};   // a tile's blocks so far
+      Seq seq;
+      for (uint32_t n = 0; ok && take(n, seq); ++n) {
+        const Place pl(seq, a.per, part, parts);
+        release(n);
+        if (pl.most == 0) continue;
+        ok = mbar_wait_warp(&q_full, jobs_done & 1, kWaitNs);
+        ++jobs_done;
+        // step j: P V of block j - 1, then Q K^T of block j; a block's K is loaded
+        // one stage before its V
+        for (int32_t j = 0; ok && j <= pl.most; ++j) {
+          asm volatile("" : "+l"(qd));   // (else all descriptors of the loop are kept, and spilled)
+          const uint32_t ki = kv + 2 * j, vi = kv + 2 * j - 1;
+          const uint32_t k_st = ki % C::kStages, v_st = vi % C::kStages;
+          if (j < pl.most) ok = mbar_wait_warp(&kv_full[k_st], (ki / C::kStages) & 1, kWaitNs);
+          if (ok && j > 0) {
+            ok = mbar_wait_warp(&kv_full[v_st], (vi / C::kStages) & 1, kWaitNs);
+            // values behind the sequence's last one are another's: a product
+            // with a zero probability has to be zero
+            const int64_t valid = pl.lk - (int64_t)(pl.begin + j - 1) * kRows;
+            if (ok && valid < kRows) {
+              for (int h = 0; h < C::kHalves; ++h) {
+                uint4* z = reinterpret_cast<uint4*>(sm + (2 + v_st) * C::kTile + h * kTileBytes);
+                for (int i = (int)valid * 8 + lane; i < kRows * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
           }
-          fence_proxy_async_smem();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t s_at = tmem + C::kS + 128 * w, o_at = tmem + C::kO + 128 * w;
+            if (ok && j > 0 && j <= pl.blocks[w]) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                ok = ok && mbar_wait_warp(half ? &p_full[w] : &p_half[w], probs[w] & 1, kWaitNs);
+                tc_fence_after();
+                if (ok && lead)
+#pragma unroll
+                  for (int s = 4 * half; s < 4 * half + 4; ++s)
+                    mma_bf16_ts(o_at, s_at + 8 * s, vd + (uint64_t)((v_st * C::kTile + s * 2048) >> 4),
+                                kOut, j > 1 || s > 0);
+              }
+              ++probs[w];
+              if (ok && lead && j == pl.blocks[w]) mma_commit(&o_full[w]);
+            }
+            if (ok && lead && j < pl.blocks[w]) {
+              tc_fence_after();
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s)
+                mma_bf16(s_at, qd + (uint64_t)((w * C::kTile + kstep(s)) >> 4),
+                         kd + (uint64_t)((k_st * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+              mma_commit(&s_full[w]);
+            }
+            __syncwarp();
+          }
+          if (ok && lead) {
+            if (j > 0) mma_commit(&kv_empty[v_st]);
+            if (j < pl.most) mma_commit(&kv_empty[k_st]);
+            if (j + 1 == pl.most) mma_commit(&q_empty);
+          }
           __syncwarp();
         }
+        kv += 2 * pl.most;
       }
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const uint32_t s_at = tmem + C::kS + 128 * w, o_at = tmem + C::kO + 128 * w;
-        if (ok && j > 0 && j <= blocks[w]) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && mbar_wait_warp(half ? &p_full[w] : &p_half[w], (uint32_t)((j - 1) & 1), kWaitNs);
-            tc_fence_after();
-            if (ok && lead)
-#pragma unroll
-              for (int s = 4 * half; s < 4 * half + 4; ++s)
-                mma_bf16_ts(o_at, s_at + 8 * s, vd + (uint64_t)((v_st * C::kTile + s * 2048) >> 4), kOut,
-                            j > 1 || s > 0);
-          }
-          if (ok && lead && j == blocks[w]) mma_commit(&o_full[w]);
-        }
-        if (ok && lead && j < blocks[w]) {
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_bf16(s_at, qd + (uint64_t)((w * C::kTile + kstep(s)) >> 4),
-                     kd + (uint64_t)((k_st * C::kTile + kstep(s)) >> 4), kScores, s > 0);
-          mma_commit(&s_full[w]);
-        }
-        __syncwarp();
-      }
-      if (ok && lead) {
-        if (j > 0) mma_commit(&kv_empty[v_st]);
-        if (j < most) mma_commit(&kv_empty[k_st]);
-      }
-      __syncwarp();
     }
-  }
   } else {
     // ---------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -213,117 +328,147 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     const int row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // 32 lanes, in the address's upper half
     const uint32_t s_at = tmem + lanes + C::kS + 128 * w, o_at = tmem + lanes + C::kO + 128 * w;
-    const int32_t n = blocks[w];
     const int qi = row / sq.group;                         // the row's query in its tile
-    const bool live = qi < rows[w];
-    // the last key that the row sees
-    const int32_t last = first[w] + qi + shift;
     const float c = a.c;
-    float m = 0.f, l = 0.f;
-    for (int32_t j = 0; j < n; ++j) {
-      ok = mbar_wait_warp(&s_full[w], (uint32_t)(j & 1), kWaitNs);
-      if (!ok) break;
+    uint32_t scores = 0, outs = 0;                         // blocks and jobs of this tile so far
+    Seq seq;
+    for (uint32_t job = 0; ok && take(job, seq); ++job) {
+      int32_t n, first, begin;
+      {
+        const Place pl(seq, a.per, part, parts);
+        n = pl.blocks_of(w);
+        first = pl.first_of(w) + pl.shift;                   // the last key that the first row sees
+        begin = pl.begin;
+      }
+      float m = 0.f, l = 0.f;
+      for (int32_t j = 0; j < n; ++j, ++scores) {
+        ok = mbar_wait_warp(&s_full[w], scores & 1, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_wait_regs(s[i]);
+        // keys that the tile's first row does not see are in the block?
+        const int32_t k0 = (begin + j) * kRows;
+        if (k0 + kRows - 1 > first) {
+          const int32_t see = first + qi - k0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (32 * i + x > see) s[i][x] = 0xff800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+          for (int x = 1; x < 31; x += 2)
+            mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])));
+          mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (j == 0) {
+          m = top == -INFINITY ? 0.f : top;
+        } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+          // (the scores' commit covers the products before them: O is at rest)
+          // a row's bits depend on no other row of its warp: the others get a factor of 1
+          const bool grows = top > m + kGrow;
+          const float f = grows ? ex2_sfu(m - top) : 1.f;
+          l *= f;
+          m = grows ? top : m;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            tmem_ld16(o_at + 16 * i, o);
+            tmem_ld_wait_regs(o);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_st16(o_at + 16 * i, o);
+          }
+        }
+        const F2 cc = f2(c, c), mm = f2(-m, -m);
+        F2 sum[2] = {f2(l, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float lo, hi;
+            f2_split(f2_fma(f2(__uint_as_float(s[i][2 * x]), __uint_as_float(s[i][2 * x + 1])), cc, mm),
+                     lo, hi);
+            lo = ex2_sfu(lo);
+            hi = ex2_sfu(hi);
+            sum[x & 1] = f2_add(sum[x & 1], f2(lo, hi));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x]) : "f"(hi), "f"(lo));
+          }
+          tmem_st16(s_at + 16 * i, p);
+          if (i & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(i == 1 ? &p_half[w] : &p_full[w]);
+          }
+        }
+        float x0, x1;
+        f2_split(f2_add(sum[0], sum[1]), x0, x1);
+        l = x0 + x1;
+      }
+      // the row's results.  (The next job's first product into O waits for this
+      // warpgroup's next probabilities, so these loads come before it.)
+      if (ok && n > 0) ok = mbar_wait_warp(&o_full[w], outs++ & 1, kWaitNs);
       tc_fence_after();
-      uint32_t s[4][32];
+      if (!ok) break;
+      const int slot = kMode == kListed ? job & 1 : 0;
+      const Place pl(slots[slot], a.per, part, parts);       // (again: it took registers)
+      const bool live = qi < pl.rows_of(w);
+      const int64_t r = (pl.q0 + pl.first_of(w) + qi) * a.q_heads +
+                        (int64_t)slot_head[slot] * sq.group + row % sq.group;
+      release(job);
+      if constexpr (kMode == kParts) {
+        const int64_t at = ((int64_t)blockIdx.x * parts + part) * 256 + 128 * w + row;
+        if (live) a.ml[at] = make_float2(m, n > 0 ? l : 0.f);
+        if (n > 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * i, o);
+            tmem_ld_wait_regs(o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld_wait_regs(s[i]);
-      // keys that the tile's first row does not see are in the block?
-      const int32_t k0 = j * kRows;
-      if (k0 + kRows - 1 > first[w] + shift) {
-        const int32_t see = last - k0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (32 * i + x > see) s[i][x] = 0xff800000u;   // -inf
-      }
-      float mx[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mx[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-        for (int x = 1; x < 31; x += 2)
-          mx[i] = fmaxf(mx[i], fmaxf(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])));
-        mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      if (j == 0) {
-        m = top == -INFINITY ? 0.f : top;
-      } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
-        // (the scores' commit covers the products before them: O is at rest)
-        // a row's bits depend on no other row of its warp: the others get a factor of 1
-        const bool grows = top > m + kGrow;
-        const float f = grows ? ex2_sfu(m - top) : 1.f;
-        l *= f;
-        m = grows ? top : m;
+            for (int x = 0; x < 8; ++x)
+              if (live)
+                *reinterpret_cast<uint4*>(a.o + at * D + 32 * i + 4 * x) =
+                    make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+      } else {
+        const bool none = n == 0 || l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
-          tmem_ld32(o_at + 32 * i, o);
-          tmem_ld_wait_regs(o);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-          tmem_st32(o_at + 32 * i, o);
-        }
-      }
-      const F2 cc = f2(c, c), mm = f2(-m, -m);
-      F2 sum[2] = {f2(l, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t p[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float lo, hi;
-          f2_split(f2_fma(f2(__uint_as_float(s[i][2 * x]), __uint_as_float(s[i][2 * x + 1])), cc, mm),
-                   lo, hi);
-          lo = ex2_sfu(lo);
-          hi = ex2_sfu(hi);
-          sum[x & 1] = f2_add(sum[x & 1], f2(lo, hi));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x]) : "f"(hi), "f"(lo));
-        }
-        tmem_st16(s_at + 16 * i, p);
-        if (i & 1) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(i == 1 ? &p_half[w] : &p_full[w]);
-        }
-      }
-      float x0, x1;
-      f2_split(f2_add(sum[0], sum[1]), x0, x1);
-      l = x0 + x1;
-    }
-    // the row's results
-    if (ok && n > 0) ok = mbar_wait_warp(&o_full[w], 0, kWaitNs);
-    tc_fence_after();
-    if (ok && rows[w] > 0) {
-      const int64_t r = (seq.q0 + first[w] + qi) * a.q_heads + (int64_t)head * sq.group + row % sq.group;
-      const bool none = n == 0 || l == 0.f;
-      const float inv = none ? 0.f : 1.f / l;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(o_at + 32 * i, o);
-          tmem_ld_wait_regs(o);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t y[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const float lo = none ? 0.f : __uint_as_float(o[8 * x + 2 * z]) * inv;
-            const float hi = none ? 0.f : __uint_as_float(o[8 * x + 2 * z + 1]) * inv;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[z]) : "f"(hi), "f"(lo));
+          if (n > 0) {
+            tmem_ld32(o_at + 32 * i, o);
+            tmem_ld_wait_regs(o);
           }
-          if (live)
-            *reinterpret_cast<uint4*>(a.out + r * D + 32 * i + 8 * x) =
-                make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t y[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float lo = none ? 0.f : __uint_as_float(o[8 * x + 2 * z]) * inv;
+              const float hi = none ? 0.f : __uint_as_float(o[8 * x + 2 * z + 1]) * inv;
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[z]) : "f"(hi), "f"(lo));
+            }
+            if (live)
+              *reinterpret_cast<uint4*>(a.out + r * D + 32 * i + 8 * x) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
+        if (live) a.lse[r] = none ? -INFINITY : (m + log2f(l)) * kLn2;
       }
-      if (live) a.lse[r] = none ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   }
   if (!ok) {
@@ -336,6 +481,93 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   tc_fence_before();
   __syncthreads();
   if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+__global__ void __launch_bounds__(kListThreads) prefill_list_kernel(ListArgs a) {
+  grid_release_next();
+  list_jobs(a);
+}
+
+// The parts of a job, joined in their order: a warp takes every eighth packed
+// row, a lane 4 columns (2 of 64).
+constexpr int kJoinThreads = 256;
+constexpr int kMostParts = 32;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ FwdArgs a) {
+  constexpr int kV = D / 32;
+  __shared__ int64_t scratch[kJoinThreads + 6];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int head = blockIdx.x % a.s.kv_heads;
+  Seq seq;
+  if (!locate<kJoinThreads>(a.s, blockIdx.x / a.s.kv_heads, 2 * a.per, false, true, scratch, nullptr, seq))
+    return;
+  grid_wait();
+  const Place pl(seq, a.per, 0, 1);
+  // blockIdx.y: 32 rows of the job's 256
+  for (int row = 32 * blockIdx.y + warp; row < 32 * blockIdx.y + 32; row += kJoinThreads / 32) {
+    const int w = row >> 7, in = row & 127, qi = in / a.s.group;
+    if (qi >= pl.rows_of(w)) continue;
+    const int64_t base = (int64_t)blockIdx.x * a.parts * 256 + row;
+    float m = -INFINITY, l = 0.f;
+    if (lane < a.parts) {
+      const float* p = reinterpret_cast<const float*>(a.ml + base + (int64_t)lane * 256);
+      m = ld_waited(p);
+      l = ld_waited(p + 1);
+    }
+    const bool on = !(l == 0.f);     // (a NaN counts)
+    float top = on ? m : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = on ? ex2_sfu(m - top) : 0.f;
+    float all = on ? l * f : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    const unsigned some = __ballot_sync(0xffffffffu, on);
+    float acc[kV] = {};
+#pragma unroll 8
+    for (int p = 0; p < a.parts; ++p) {
+      const float fp = __shfl_sync(0xffffffffu, f, p);
+      if (some >> p & 1) {
+        const float* src = a.o + (base + (int64_t)p * 256) * D + lane * kV;
+        float x[kV];
+        if constexpr (kV == 4) {
+          const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
+          x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+        } else {
+          x[0] = ld_waited(src);
+          x[1] = ld_waited(src + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] = fmaf(x[i], fp, acc[i]);
+      }
+    }
+    const int64_t r =
+        (pl.q0 + pl.first_of(w) + qi) * a.q_heads + (int64_t)head * a.s.group + in % a.s.group;
+    const float inv = some ? 1.f / all : 0.f;
+    uint32_t y[kV / 2];
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(acc[2 * i + 1] * inv), "f"(acc[2 * i] * inv));
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.out + r * D) + lane * (kV / 2);
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) to[i] = y[i];
+    if (lane == 0) a.lse[r] = some ? (top + log2f(all)) * kLn2 : -INFINITY;
+  }
+}
+
+// Jobs that the GPU's SMs take in one turn or less: a part of a job's keys each
+// where there are SMs for two parts and more, of at least `kPartBlocks` blocks.
+// More jobs than `kTurns` turns: from a list.
+constexpr int kPartBlocks = 1, kTurns = 2;
+Mode mode_of(int64_t jobs, int64_t blocks, int sms, int32_t& parts) {
+  parts = 1;
+  if (jobs > (int64_t)kTurns * sms) return kListed;
+  int64_t p = sms / jobs;
+  if (p > blocks / kPartBlocks) p = blocks / kPartBlocks;
+  if (p > kMostParts) p = kMostParts;
+  if (p < 2 || blocks < 4) return kOnce;
+  parts = (int32_t)p;
+  return kParts;
 }
 
 int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, const int32_t* cu_k,
@@ -357,7 +589,8 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   FwdArgs a;
   memset(&a, 0, sizeof a);
   a.status = status_ptr();
-  if (!a.status) return GDN_ERR_CUDA;
+  const int sms = sm_count();
+  if (!a.status || sms < 1) return GDN_ERR_CUDA;
   const int32_t group = s.q_heads / s.kv_heads;
   a.s = {cu_q, cu_k, s.batch, s.seqlen_q, s.seqlen_k, group, s.kv_heads};
   a.out = (__nv_bfloat16*)out;
@@ -373,19 +606,61 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   // packed: an upper bound, sum_n ceil(len_n / per) <= T / per + N
   const int64_t per = 2 * a.per;
   const int64_t tiles = s.packed ? tq / per + s.batch : (s.seqlen_q + per - 1) / per * s.batch;
-  const int64_t grid = tiles * s.kv_heads;
-  if (grid > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
-  cudaError_t e;
-  auto run = [&](auto shape, auto kern) {
+  const int64_t jobs = tiles * s.kv_heads, blocks = (s.seqlen_k + kRows - 1) / kRows;
+  if (jobs > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+  const Mode mode = mode_of(jobs, blocks, sms, a.parts);
+  size_t need = 0, at_jobs = 256, at_o = 0;
+  if (mode == kListed) need = at_jobs + (size_t)tiles * sizeof(Job);
+  if (mode == kParts) {
+    at_o = align_up((size_t)jobs * a.parts * 256 * sizeof(float2), 256);
+    need = at_o + (size_t)jobs * a.parts * 256 * s.d * 4;
+  }
+  void* scratch = nullptr;
+  if (need && scratch_alloc(&scratch, need, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  cudaError_t e = cudaSuccess;
+  dim3 grid((unsigned)jobs);
+  if (mode == kListed) {
+    a.count = (const int32_t*)scratch;
+    a.next = (uint32_t*)scratch + 1;
+    a.jobs = (const Job*)((char*)scratch + at_jobs);
+    const int64_t longest = (s.seqlen_q + per - 1) / per;
+    const ListArgs list = {a.s, (int32_t)per, (int32_t)((longest + kLevels - 1) / kLevels), false,
+                           (int32_t*)scratch, a.next, (Job*)((char*)scratch + at_jobs), a.status};
+    e = launch(false, prefill_list_kernel, dim3(1), kListThreads, 0, 0, st, list);
+    count_launches(1);
+    grid = dim3((unsigned)sms);
+  } else if (mode == kParts) {
+    a.ml = (float2*)scratch;
+    a.o = (float*)((char*)scratch + at_o);
+    grid.y = (unsigned)a.parts;
+  }
+  auto run = [&](auto shape, auto kern, std::atomic<uint64_t>& on) {
     using C = decltype(shape);
-    e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e == cudaSuccess) e = launch(false, kern, dim3((unsigned)grid), kThreads, C::kSmem, 0, st, a);
+    if (e == cudaSuccess) e = allow_smem((const void*)kern, C::kSmem, on);
+    if (e == cudaSuccess) e = launch(mode == kListed, kern, grid, kThreads, C::kSmem, 0, st, a);
   };
-  if (s.d == 128) run(Fwd<128>{}, prefill_kernel<128>);
-  else run(Fwd<64>{}, prefill_kernel<64>);
+  static std::atomic<uint64_t> on[6];
+  if (s.d == 128) {
+    if (mode == kListed) run(Fwd<128>{}, prefill_kernel<128, kListed>, on[0]);
+    else if (mode == kParts) run(Fwd<128>{}, prefill_kernel<128, kParts>, on[1]);
+    else run(Fwd<128>{}, prefill_kernel<128, kOnce>, on[2]);
+  } else {
+    if (mode == kListed) run(Fwd<64>{}, prefill_kernel<64, kListed>, on[3]);
+    else if (mode == kParts) run(Fwd<64>{}, prefill_kernel<64, kParts>, on[4]);
+    else run(Fwd<64>{}, prefill_kernel<64, kOnce>, on[5]);
+  }
   count_launches(1);
+  if (mode == kParts && e == cudaSuccess) {
+    e = launch(true, s.d == 128 ? prefill_join_kernel<128> : prefill_join_kernel<64>,
+               dim3((unsigned)jobs, 8), kJoinThreads, 0, 0, st, a);
+    count_launches(1);
+  }
   if (e != cudaSuccess) (void)cudaGetLastError();
-  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  const cudaError_t f = scratch_free(scratch, st);
+  return e == cudaSuccess && f == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace

@@ -107,6 +107,118 @@ __device__ bool locate(const Seqs& s, int64_t job, int per, bool keys, bool down
   return true;
 }
 
+// ------------------------------------------------------------- job lists
+// Where a call has more jobs than the GPU has SMs, one CTA lists them first,
+// those that see the most tiles first whatever their sequence, and persistent
+// CTAs take the next one when they are done with one.  (Sequence by sequence
+// the long jobs of the last sequence start late; and a persistent CTA loads its
+// next job while the last one ends.)  The order among jobs of equal length, that
+// of atomics, does not matter: jobs share nothing.
+struct Job {
+  int32_t q0, k0, lq, lk, tile, unused[3];
+};
+constexpr int kListThreads = 1024;
+constexpr int kLevels = 2048;     // lengths told apart, in `unit` tiles
+struct ListArgs {
+  Seqs s;
+  int32_t per, unit;     // tokens of a tile; tiles of a level
+  bool keys;             // tiles of keys: the first ones see the most
+  int32_t* count;        // jobs of a kv head, 0 for malformed sequences
+  uint32_t* next;        // the CTAs' place in the list
+  Job* jobs;
+  unsigned* status;
+};
+inline __device__ void list_jobs(const ListArgs& a) {
+  __shared__ int32_t level[kLevels];
+  __shared__ int32_t warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Seqs& s = a.s;
+  bool bad = tid == 0 && s.cu_q && (s.cu_q[0] != 0 || s.cu_k[0] != 0 || s.cu_q[s.n] != s.len_q ||
+                                    s.cu_k[s.n] != s.len_k);
+  if (s.cu_q)
+    for (int i = tid; i < s.n; i += kListThreads)
+      bad |= s.cu_q[i] < 0 || s.cu_k[i] < 0 || s.cu_q[i + 1] < s.cu_q[i] || s.cu_k[i + 1] < s.cu_k[i];
+  for (int i = tid; i < kLevels; i += kListThreads) level[i] = 0;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      *a.count = 0;
+      *a.next = 0;
+      flag_status(a.status, GDN_ERR_BAD_SEQLENS);
+    }
+    return;
+  }
+  auto seq = [&](int i) {
+    Job j = {};
+    if (s.cu_q) {
+      j.q0 = s.cu_q[i];
+      j.k0 = s.cu_k[i];
+      j.lq = s.cu_q[i + 1] - j.q0;
+      j.lk = s.cu_k[i + 1] - j.k0;
+    } else {
+      j.lq = (int32_t)s.len_q;
+      j.lk = (int32_t)s.len_k;
+      j.q0 = (int32_t)(i * s.len_q);
+      j.k0 = (int32_t)(i * s.len_k);
+    }
+    return j;
+  };
+  // a tile's level: the longest job is level 0
+  auto level_of = [&](int64_t t, int64_t tiles) {
+    const int64_t longer = (a.keys ? tiles - 1 - t : t) / a.unit;
+    return (int)(kLevels - 1 - (longer < kLevels ? longer : kLevels - 1));
+  };
+  // a warp takes a sequence, its lanes the tiles
+  for (int i = warp; i < s.n; i += kListThreads / 32) {
+    const Job j = seq(i);
+    const int64_t tiles = ((int64_t)(a.keys ? j.lk : j.lq) + a.per - 1) / a.per;
+    for (int64_t t = lane; t < tiles; t += 32) atomicAdd(&level[level_of(t, tiles)], 1);
+  }
+  __syncthreads();
+  // where each level begins
+  int32_t sum = 0;
+  int32_t mine[kLevels / kListThreads];
+#pragma unroll
+  for (int i = 0; i < kLevels / kListThreads; ++i) {
+    mine[i] = sum;
+    sum += level[tid * (kLevels / kListThreads) + i];
+  }
+  int32_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int32_t w = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  const int32_t before = (warp ? warp_sum[warp - 1] : 0) + x - sum;
+#pragma unroll
+  for (int i = 0; i < kLevels / kListThreads; ++i)
+    level[tid * (kLevels / kListThreads) + i] = before + mine[i];
+  if (tid == 0) {
+    *a.count = warp_sum[31];
+    *a.next = 0;
+  }
+  __syncthreads();
+  for (int i = warp; i < s.n; i += kListThreads / 32) {
+    Job j = seq(i);
+    const int64_t tiles = ((int64_t)(a.keys ? j.lk : j.lq) + a.per - 1) / a.per;
+    for (int64_t t = lane; t < tiles; t += 32) {
+      j.tile = (int32_t)t;
+      a.jobs[atomicAdd(&level[level_of(t, tiles)], 1)] = j;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host side
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

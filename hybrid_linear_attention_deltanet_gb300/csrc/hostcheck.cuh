@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gdn {
 namespace hostcheck {
 
@@ -42,6 +44,18 @@ inline int sm_count() {
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return n;
+}
+
+// Allows a kernel its dynamic shared memory, once a device (a bit each in `on`).
+inline cudaError_t allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& on) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (on.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) on.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 }  // namespace hostcheck

@@ -93,8 +93,8 @@ def test_dense_batches(gdn_lib, B, tq, tk, d):
     out, lse = gdn.attention_prefill(q.view(B, tq, 6, d), k.view(B, tk, 2, d), v.view(B, tk, 2, d))
     assert out.shape == (B, tq, 6, d) and lse.shape == (B, tq, 6)
     verify(q, k, v, out.flatten(0, 1), lse.flatten(0, 1), [tq] * B, [tk] * B)
-    again = gdn.attention_prefill(q, k, v, cu([tq] * B), cu([tk] * B))
-    assert torch.equal(again[0], out.flatten(0, 1)) and torch.equal(again[1], lse.flatten(0, 1))
+    # (packed, a sequence's keys may be cut into other parts)
+    verify(q, k, v, *gdn.attention_prefill(q, k, v, cu([tq] * B), cu([tk] * B)), [tq] * B, [tk] * B)
 
 
 @pytest.mark.parametrize("d", [64, 128])
