@@ -5,16 +5,18 @@
 //
 // Every key and value is used once by each of a group's query heads, so the
 // cache's bytes through HBM bound it, whatever the rows' lengths.  The tiles of
-// all rows and kv heads (64 tokens; 128 in 8 bits) form one list; CTA c of n
-// takes the c-th n-th of it, so that no CTA has more than a tile more than
-// another.  A CTA walks its part with three stages of asynchronous 16-byte loads
-// (the next tiles' page numbers and lengths a step ahead of them), its four
-// warps taking a quarter of a tile each, with softmax statistics of their own.
-// The heads of a group (up to 16, then in parts) are the rows of the matrix
-// instructions: with one token there is nothing else to fill them, and these
-// kernels' products are far from bounding anything.  Where a (row, head) ends,
-// the warps' sums are joined; one that is cut over several CTAs is joined from
-// their partial sums by a second kernel, in the order of the CTAs.
+// all rows and kv heads (64 tokens of 256 bytes, 128 of fewer) form one list; CTA
+// c of n takes the c-th n-th of it, so that no CTA has more than a tile more than
+// another.  One warp walks the CTA's part and has TMA bring the tiles, page by
+// page, into a ring; four warps take a quarter of a tile each, with softmax
+// statistics of their own.  (With the loads' addresses computed by all threads
+// these took more instructions than the attention: heads of 64 ran at 3.8 TB/s,
+// 8 bits at 1.4 to 3.)  The heads of a group (up to 16, then in parts) are the rows
+// of the matrix instructions: with one token there is nothing else to fill them.
+// Where a (row, head) ends, the warps' sums are joined; one that is cut over
+// several CTAs is joined from their partial sums by a second kernel, in the order
+// of the CTAs.
+#include "attention_tc.cuh"
 #include "gdn_internal.cuh"
 #include "hostcheck.cuh"
 #include "kv_cache.cuh"
@@ -24,46 +26,66 @@ namespace gdn {
 namespace {
 
 using namespace hostcheck;
-using sm100::smem_u32;
+using namespace sm100;
 
-constexpr int kThreads = 128;
-constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kWarps = 4;                       // that compute
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kHeads = 16;          // rows of a matrix instruction
 constexpr int kSms = 152;
+constexpr int kCtas = 2 * kSms;     // two resident ones an SM
 constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <int D, bool kFp8>
 struct Shape {
-  static constexpr int kTile = kFp8 ? 128 : 64;             // tokens
   static constexpr int kRow = D * (kFp8 ? 1 : 2);           // bytes of a token's head
-  static constexpr int kChunks = kRow / 16;
-  static constexpr int kPool = kTile * kRow;
-  static constexpr int kScales = kFp8 ? kTile * 4 : 0;
-  static constexpr int kQ = 2 * kPool + 2 * kScales;        // where the queries lie
-  static constexpr int kStage = kQ + kHeads * D * 2;
+  static constexpr int kTile = kRow == 256 ? 64 : 128;      // tokens
+  static constexpr int kSub = kRow < 128 ? kRow : 128;      // bytes of a row of an image
+  static constexpr int kHalves = kRow / kSub;               // images side by side
+  static constexpr uint32_t kImage = kTile * kSub;
+  static constexpr uint32_t kPool = kHalves * kImage;       // of keys or values
+  static constexpr uint32_t kScales = kFp8 ? kTile * 4 : 0;
+  static constexpr uint32_t kQ = 2 * kPool;                 // where the queries lie
+  static constexpr uint32_t kQBytes = kHeads * D * 2;
+  static constexpr uint32_t kScaleAt = kQ + kQBytes;
+  static constexpr uint32_t kStage = kScaleAt + (kFp8 ? 1024 : 0);
+  static constexpr int kStages = kRow == 64 ? 5 : 3;
   static constexpr int kPitch = D + 8;                      // floats of a row of the join
-  static constexpr int kSmem = kStages * kStage;
+  static constexpr uint32_t kSmall = kStages * kStage;      // where Small lies
+  static constexpr uint32_t kSmem = kSmall + 768;
   static_assert(kWarps * kHeads * kPitch * 4 <= kStage, "the join uses a consumed stage");
+  static_assert(2 * kScales <= 1024 && kStage % 1024 == 0, "");
 };
+
+// One tile of the list.
+struct Tile {
+  int32_t row, hh, at, n, len;   // row, its (kv head, part of the group), tile, tiles, tokens
+};
+// (8 bits, heads of 128: two CTAs' shared memory is all of an SM's but 2.5 KB, so
+// there is no static part, and the dynamic one starts on 1024 bytes.)
+struct Small {
+  uint64_t full[5], empty[5];
+  Tile meta[5];
+  float ml[kWarps][kHeads][2];
+};
+static_assert(sizeof(Small) <= 768, "");
 
 // What is left of a cut (row, head)'s parts: slot 2c of CTA c if the part
 // continues one, 2c + 1 if it begins one.
 struct Work {
-  int64_t total;      // tiles in all
   int64_t* begin;     // [items] first tile of a cut item, ...
   int64_t* end;       // ... and behind its last; 0: the item is not cut
   float* ml;          // [slots][16][2] maximum (of scores in powers of two), sum
   float* o;           // [slots][16][D]
 };
 struct Args {
-  const __nv_bfloat16* q;
+  CUtensorMap q, k, v;
   __nv_bfloat16* out;
   gdn_kv_cache c;
   int32_t layer, q_heads, group, parts, items_per_row, page_log2;
   float scale_log2;
-  int64_t* total;     // Work::total in memory
+  int64_t* total;     // tiles in all
   Work w;
   unsigned* status;
 };
@@ -80,57 +102,61 @@ __device__ __forceinline__ void ldmatrix4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// 16 x 8 += 16 x 16 times 16 x 8, bf16 or (kHalf) fp16 operands
+template <bool kHalf>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (kHalf)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two e4m3 codes of w, chosen by the permutation that puts each in the upper
-// byte of a half, as bf16: the exponent's four bits and the fraction's three
-// move to their places, and the product with 2^120 (127 - 7) makes the
-// exponent's bias bf16's, subnormal codes included.  Exact; a NaN code becomes
-// a number, but then the scale is NaN.
-template <uint32_t kSel>
-__device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t w) {
-  const uint32_t x = __byte_perm(w, 0, kSel);
-  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Four e4m3 codes as fp16, two a register (exact: 4 exponent bits in 5, 3 in 10).
+__device__ __forceinline__ void e4m3_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
-// Byte of 16-byte chunk `c` of row `r` in a swizzled image of rows of kRow bytes:
-// eight consecutive rows' chunks of one column lie in different bank groups.
-template <int kRow>
+// base-2 logarithm by the special-function unit (2^-22 absolute near 1)
+__device__ __forceinline__ float lg2_sfu(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Byte of 16-byte chunk `c` of row `r` in TMA's swizzled image of rows of 128 or
+// 64 bytes: eight consecutive rows' chunks of one column lie in different bank
+// groups.
+template <int kSub>
 __device__ __forceinline__ uint32_t image(int r, int c) {
-  return (uint32_t)(r * kRow + ((c ^ (kRow >= 128 ? r & 7 : (r >> 1) & 3)) << 4));
+  return (uint32_t)(r * kSub + ((c ^ (kSub == 128 ? r & 7 : (r >> 1) & 3)) << 4));
 }
-
-// One tile of the list.
-struct Tile {
-  int32_t row, hh, at, n, len;   // row, its (kv head, part of the group), tile, tiles, tokens
-};
+// Chunk `c` of row `r` where rows are cut into images of kSub bytes, kRows rows each.
+template <int kSub, int kRows>
+__device__ __forceinline__ uint32_t place(int r, int c) {
+  constexpr int kPer = kSub / 16;
+  return (uint32_t)(c / kPer * kRows * kSub) + image<kSub>(r, c % kPer);
+}
 
 // tokens of a row, 0 where its length is out of range
 __device__ __forceinline__ int32_t row_tokens(const gdn_kv_cache& c, int64_t row, unsigned* status) {
@@ -142,17 +168,39 @@ __device__ __forceinline__ int32_t row_tokens(const gdn_kv_cache& c, int64_t row
 }
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) decode_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ Args a) {
   using S = Shape<D, kFp8>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sums[kThreads + 1];
-  __shared__ int64_t where[2];
-  __shared__ Tile meta[kStages];
-  __shared__ float ml[kWarps][kHeads][2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small& small = *reinterpret_cast<Small*>(smem + S::kSmall);
+  uint64_t* full = small.full;
+  uint64_t* empty = small.empty;
+  Tile* meta = small.meta;
+  auto& ml = small.ml;
+  // (in the stages, before anything is loaded)
+  int64_t* sums = reinterpret_cast<int64_t*>(smem);
+  int64_t* warp_sums = sums + kThreads + 1;
+  int64_t* where = warp_sums + kWarps + 1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const gdn_kv_cache& c = a.c;
   const int HH = a.items_per_row;
   grid_release_next();
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) flag_status(a.status, GDN_ERR_UNSUPPORTED);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    fence_barrier_init();
+  }
+  if (tid == kThreads - 1) {
+    prefetch_tensormap(&a.q);
+    prefetch_tensormap(&a.k);
+    prefetch_tensormap(&a.v);
+  }
 
   // the list's length, and where this CTA's part begins
   const int64_t per = ((int64_t)c.rows + kThreads - 1) / kThreads;
@@ -160,13 +208,18 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) decode_kernel(Args
   int64_t mine = 0;
   for (int64_t r = r0; r < r1; ++r)
     mine += (row_tokens(c, r, a.status) + S::kTile - 1) / S::kTile;
-  sums[tid + 1] = mine;
-  if (tid == 0) sums[0] = 0;
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {
-    const int64_t t = tid >= o ? sums[tid + 1 - o] : 0;
+  {
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    sums[tid + 1] += t;
+    for (int w = 0; w < warp; ++w) x += warp_sums[w];
+    sums[tid + 1] = x;
+    if (tid == 0) sums[0] = 0;
     __syncthreads();
   }
   const int64_t total = sums[kThreads] * HH;
@@ -178,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) decode_kernel(Args
   if (lo >= sums[tid] * HH && lo < sums[tid + 1] * HH) {
     int64_t left = lo - sums[tid] * HH;
     for (int64_t r = r0; r < r1; ++r) {
-      const int64_t n = (row_tokens(c, r, nullptr) + S::kTile - 1) / S::kTile * HH;
+      const int64_t n = (int64_t)((row_tokens(c, r, nullptr) + S::kTile - 1) / S::kTile) * HH;
       if (left < n) {
         where[0] = r;
         where[1] = left;
@@ -188,359 +241,448 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) decode_kernel(Args
     }
   }
   __syncthreads();
-  // the loads' place in the list, with the next row's tokens and the next
-  // tile's pages read ahead
-  Tile ld;
-  ld.row = (int32_t)where[0];
-  ld.len = row_tokens(c, ld.row, nullptr);
-  ld.n = (ld.len + S::kTile - 1) / S::kTile;
-  ld.hh = (int32_t)(where[1] / ld.n);
-  ld.at = (int32_t)(where[1] - (int64_t)ld.hh * ld.n);
-  int32_t next_len = row_tokens(c, ld.row + 1, nullptr);
-  const int page = c.page, lg = a.page_log2;
-  constexpr int kIds = S::kTile / 16;   // pages of a tile at most
-  int32_t ids[kIds];
-  auto read_ids = [&]() {
-    const int32_t* t = c.table + (int64_t)ld.row * c.max_pages;
-    const int first = (ld.at * S::kTile) >> lg;
-#pragma unroll
-    for (int i = 0; i < kIds; ++i) {
-      ids[i] = -1;
-      if (i == 0 || (i << lg) < S::kTile)
-        if (((int64_t)(first + i) << lg) < ld.len) {
-          ids[i] = t[first + i];
-          if (ids[i] < 0 || ids[i] >= c.pages) {
-            flag_status(a.status, GDN_ERR_BAD_CACHE);
-            ids[i] = -1;
-          }
-        }
-    }
-  };
-  read_ids();
-  int64_t left = hi - lo;   // tiles to load
-  bool fresh = true;        // the next tile is the first of its part
-  const int64_t layer_pages = (int64_t)a.layer * c.pages;
+  const int64_t row0 = where[0], in_row = where[1];
+  fence_proxy_async_smem();
+  __syncthreads();
+  bool ok = true;
 
-  auto issue = [&](int stage) {
-    if (left > 0) {
-      const uint32_t base = smem_u32(smem) + stage * S::kStage;
-      const int h = ld.hh / a.parts, part = ld.hh - h * a.parts;
-      const int64_t pos0 = (int64_t)ld.at * S::kTile;
-      constexpr int kRowsStep = kThreads / S::kChunks;   // tokens a round of loads covers
-      const int ch = tid % S::kChunks, tr = tid / S::kChunks;
-#pragma unroll
-      for (int i = 0; i < S::kTile / kRowsStep; ++i) {
-        const int tok = i * kRowsStep + tr;
-        // (up to 16 tokens from a multiple of their number lie on one page)
-        const int at = kRowsStep <= 16 ? i * kRowsStep : tok;
-        int32_t id = ids[0];
-#pragma unroll
-        for (int j = 1; j < kIds; ++j)
-          if ((at >> lg) == j) id = ids[j];
-        const bool on = pos0 + tok < ld.len && id >= 0;
-        const int64_t e =
-            ((layer_pages + (on ? id : 0)) * c.kv_heads + h) * page + ((pos0 + tok) & (page - 1));
-        const uint32_t to = image<S::kRow>(tok, ch);
-        const int64_t off = e * S::kRow + ch * 16;
-        cp_async16(base + to, (const uint8_t*)c.k + off, on ? 16 : 0);
-        cp_async16(base + S::kPool + to, (const uint8_t*)c.v + off, on ? 16 : 0);
+  if (warp == kWarps) {
+    // --------------------------------------------------------------- load
+    const bool lead = elect_one();
+    const int lg = a.page_log2;
+    const int box = c.page < S::kTile ? c.page : S::kTile;   // tokens of one copy
+    constexpr int kIds = S::kTile / 16;                      // copies of a tile at most
+    Tile t;
+    t.row = (int32_t)row0;
+    t.len = row_tokens(c, t.row, nullptr);
+    int32_t next_len = row_tokens(c, t.row + 1, nullptr);
+    t.n = (t.len + S::kTile - 1) / S::kTile;
+    t.hh = (int32_t)(in_row / t.n);
+    t.at = (int32_t)(in_row - (int64_t)t.hh * t.n);
+    // lane i reads the page of the tile's i-th copy, one tile ahead
+    auto read_id = [&]() {
+      const int64_t pos = (int64_t)t.at * S::kTile + lane * box;
+      int32_t id = 0;
+      if (lane < kIds && lane * box < S::kTile && pos < t.len)
+        id = c.table[(int64_t)t.row * c.max_pages + (pos >> lg)];
+      return id;
+    };
+    int32_t id = read_id();
+    bool fresh = true;                                       // the first tile of its part
+    for (int64_t i = lo; i < hi; ++i) {
+      const int stage = (int)((i - lo) % S::kStages);
+      const Tile now = t;
+      const bool first = fresh;
+      if (id < 0 || id >= c.pages) {                         // some page of the pool in its place
+        flag_status(a.status, GDN_ERR_BAD_CACHE);
+        id = 0;
       }
-      if constexpr (kFp8) {
-        const int tok = tid;   // kTile == kThreads
-        int32_t id = ids[0];
-#pragma unroll
-        for (int j = 1; j < kIds; ++j)
-          if ((tok >> lg) == j) id = ids[j];
-        const bool on = pos0 + tok < ld.len && id >= 0;
-        const int64_t e =
-            ((layer_pages + (on ? id : 0)) * c.kv_heads + h) * page + ((pos0 + tok) & (page - 1));
-        cp_async4(base + 2 * S::kPool + tok * 4, c.k_scale + e, on ? 4 : 0);
-        cp_async4(base + 2 * S::kPool + S::kScales + tok * 4, c.v_scale + e, on ? 4 : 0);
-      }
-      if (fresh) {
-        // the queries of the part's heads, missing ones as zeros
-        constexpr int kQChunks = D / 8;
-        for (int i = tid; i < kHeads * kQChunks; i += kThreads) {
-          const int hr = i / kQChunks, cc = i % kQChunks, head = part * kHeads + hr;
-          const bool on = head < a.group;
-          const __nv_bfloat16* src =
-              a.q + ((int64_t)ld.row * a.q_heads + (int64_t)h * a.group + (on ? head : 0)) * D + cc * 8;
-          cp_async16(base + S::kQ + image<D * 2>(hr, cc), src, on ? 16 : 0);
-        }
-      }
-      if (tid == 0) meta[stage] = ld;
+      const int32_t ids = id;
       // on to the next tile
       fresh = false;
-      --left;
-      if (++ld.at == ld.n) {
-        ld.at = 0;
+      if (++t.at == t.n) {
+        t.at = 0;
         fresh = true;
-        if (++ld.hh == HH) {
-          ld.hh = 0;
+        if (++t.hh == HH) {
+          t.hh = 0;
           do {
-            ++ld.row;
-            ld.len = next_len;
-            ld.n = (ld.len + S::kTile - 1) / S::kTile;
-            next_len = row_tokens(c, (int64_t)ld.row + 1, nullptr);
-          } while (ld.n == 0 && ld.row < c.rows);
+            ++t.row;
+            t.len = next_len;
+            t.n = (t.len + S::kTile - 1) / S::kTile;
+            next_len = row_tokens(c, (int64_t)t.row + 1, nullptr);
+          } while (t.n == 0 && t.row < c.rows);
         }
       }
-      if (left > 0) read_ids();
-    }
-    cp_async_commit();
-  };
-
-  const int g = lane >> 2, t4 = lane & 3;
-  constexpr int kSteps = D / 16;
-  constexpr int kTok = S::kTile / kWarps;   // a warp's tokens of a tile
-  uint32_t qa[kSteps][4];
-  float o[D / 8][4];
-  float m[2], l[2];
-  bool start = true;
-  int64_t first_of_part = lo;
+      if (i + 1 < hi) id = read_id();
+      ok = mbar_wait_warp(&empty[stage], (uint32_t)(((i - lo) / S::kStages) & 1) ^ 1u, kWaitNs);
+      if (!ok) break;
+      const int64_t pos = (int64_t)now.at * S::kTile;
+      const int64_t tokens = now.len - pos < S::kTile ? now.len - pos : S::kTile;
+      const int copies = (int)((tokens + box - 1) / box);
+      const int h = now.hh / a.parts, part = now.hh - h * a.parts;
+      uint8_t* base = smem + stage * S::kStage;
+      if (lead) {
+        meta[stage] = now;
+        mbar_arrive_expect_tx(&full[stage], copies * box * (2 * S::kRow + (kFp8 ? 8 : 0)) +
+                                                (first ? S::kQBytes : 0));
+        if (first)
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
-  for (int64_t i = lo; i < hi; ++i) {
-    const int stage = (int)((i - lo) % kStages);
-    cp_async_wait<kStages - 2>();
-    __syncthreads();
-    issue((int)((i - lo + kStages - 1) % kStages));
-    const Tile tile = meta[stage];
-    const uint32_t base = smem_u32(smem) + stage * S::kStage;
-    if (start) {
-      first_of_part = i;
-      start = false;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if constexpr (!kFp8) {
-          // rows 0-7 and 8-15 of the first eight columns, then of the second
-          ldmatrix4(qa[s], base + S::kQ +
-                               image<D * 2>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * s + (lane >> 4)));
-        } else {
-          // the order in which four consecutive codes of a key arrive: columns
-          // 4t, 4t + 1 in the place of 2t, 2t + 1 and the next two in that of
-          // 2t + 8, 2t + 9 (a sum over columns may take them in any order)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t p = base + S::kQ + image<D * 2>(g + 8 * x, 2 * s + (t4 >> 1)) + (t4 & 1) * 8;
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(qa[s][x]), "=r"(qa[s][2 + x])
-                         : "r"(p));
-          }
-        }
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_2d(base + S::kQ + x * kHeads * 128, &a.q, 64 * x,
+                        now.row * a.q_heads + h * a.group + part * kHeads, &full[stage]);
       }
-    }
-    const int valid = tile.len - tile.at * S::kTile;   // tokens of the tile (or more)
+      const int32_t off = (int32_t)(pos & (c.page - 1));     // (pages longer than a tile)
+      for (int x = 0; x < copies; ++x) {
+        const int32_t p = __shfl_sync(0xffffffffu, ids, x);
+        if (!lead) continue;
 #pragma unroll
-    for (int sub = 0; sub < kTok / 16; ++sub) {
-      const int tok0 = warp * kTok + sub * 16;
-      if (tok0 >= valid) break;
-      // scores of 16 heads and 16 tokens
-      float s[2][4] = {};
-      if constexpr (!kFp8) {
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t b[4];
-          ldmatrix4(b, base + image<S::kRow>(tok0 + (lane >> 4) * 8 + (lane & 7),
-                                             2 * k + ((lane >> 3) & 1)));
-          mma16816(s[0], qa[k], b[0], b[1]);
-          mma16816(s[1], qa[k], b[2], b[3]);
+        for (int y = 0; y < S::kHalves; ++y) {
+          uint8_t* to = base + y * S::kImage + x * box * S::kSub;
+          const int32_t col = y * (S::kSub / (kFp8 ? 1 : 2));
+          tma_load_3d(to, &a.k, col, h * c.page + off, a.layer * c.pages + p, &full[stage]);
+          tma_load_3d(to + S::kPool, &a.v, col, h * c.page + off, a.layer * c.pages + p, &full[stage]);
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kSteps; k += 2) {
-          uint32_t b[4];
-          ldmatrix4(b, base + image<S::kRow>(tok0 + (lane >> 4) * 8 + (lane & 7),
-                                             k + ((lane >> 3) & 1)));
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma16816(s[x >> 1], qa[k + (x & 1)], e4m3_to_bf16<0x1404>(b[x]),
-                     e4m3_to_bf16<0x3424>(b[x]));
-        }
-      }
-      float vs[2][2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int col = tok0 + n * 8 + 2 * t4;
-        float f0 = a.scale_log2, f1 = a.scale_log2;
         if constexpr (kFp8) {
-          const float* sc = reinterpret_cast<const float*>(smem + stage * S::kStage + 2 * S::kPool);
-          f0 *= sc[col];
-          f1 *= sc[col + 1];
-          vs[n][0] = sc[S::kTile + col];
-          vs[n][1] = sc[S::kTile + col + 1];
-        }
-        const bool v0 = col < valid, v1 = col + 1 < valid;
-        s[n][0] = v0 ? s[n][0] * f0 : -INFINITY;
-        s[n][1] = v1 ? s[n][1] * f1 : -INFINITY;
-        s[n][2] = v0 ? s[n][2] * f0 : -INFINITY;
-        s[n][3] = v1 ? s[n][3] * f1 : -INFINITY;
-      }
-      // running maximum and sum of rows g and g + 8
-      float sub_m[2];
-      bool grew = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        sub_m[x] = fmaxf(m[x], mx);
-        grew |= sub_m[x] > m[x];
-      }
-      if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float f = sub_m[x] > m[x] ? ex2_sfu(m[x] - sub_m[x]) : 1.f;
-          l[x] *= f;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][2 * x] *= f;
-            o[j][2 * x + 1] *= f;
-          }
-          m[x] = sub_m[x];
+          const int64_t e = (((int64_t)a.layer * c.pages + p) * c.kv_heads + h) * c.page + off;
+          uint8_t* to = base + S::kScaleAt + x * box * 4;
+          tma_load_1d(to, c.k_scale + e, box * 4, &full[stage]);
+          tma_load_1d(to + S::kScales, c.v_scale + e, box * 4, &full[stage]);
         }
       }
-      uint32_t p[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float z = m[x] == -INFINITY ? 0.f : m[x];
-          float p0 = ex2_sfu(s[n][2 * x] - z), p1 = ex2_sfu(s[n][2 * x + 1] - z);
-          l[x] += p0 + p1;
-          if constexpr (kFp8) {
-            p0 *= vs[n][0];
-            p1 *= vs[n][1];
-          }
-          p[2 * n + x] = pack_bf16(p0, p1);
-        }
-      // out of 16 heads, the warp's tokens added
-      const uint32_t vb = base + S::kPool;
-      if constexpr (!kFp8) {
-#pragma unroll
-        for (int j = 0; j < D / 8; j += 2) {
-          uint32_t b[4];
-          ldmatrix4t(b, vb + image<S::kRow>(tok0 + ((lane >> 3) & 1) * 8 + (lane & 7), j + (lane >> 4)));
-          mma16816(o[j], p, b[0], b[1]);
-          mma16816(o[j + 1], p, b[2], b[3]);
-        }
-      } else {
-        // a transposed pair of codes is two columns: even ones to o[2j], odd to
-        // o[2j + 1], so that a lane ends with four consecutive columns of 16
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 2) {
-          uint32_t b[4];
-          ldmatrix4t(b, vb + image<S::kRow>(tok0 + ((lane >> 3) & 1) * 8 + (lane & 7), j + (lane >> 4)));
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            mma16816(o[2 * (j + x)], p, e4m3_to_bf16<0x2404>(b[2 * x]), e4m3_to_bf16<0x2404>(b[2 * x + 1]));
-            mma16816(o[2 * (j + x) + 1], p, e4m3_to_bf16<0x3414>(b[2 * x]),
-                     e4m3_to_bf16<0x3414>(b[2 * x + 1]));
-          }
-        }
-      }
+      __syncwarp();
     }
-    const bool item_ends = tile.at == tile.n - 1;
-    if (!item_ends && i + 1 < hi) continue;
-
-    // the part ends: join the warps' sums, in the consumed stage
-    start = true;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      if (t4 == 0) {
-        ml[warp][g + 8 * x][0] = m[x];
-        ml[warp][g + 8 * x][1] = l[x];
-      }
-    }
-    __syncthreads();
-    float* js = reinterpret_cast<float*>(smem + stage * S::kStage);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][g + 8 * x][0]);
-      const float f = m[x] == -INFINITY ? 0.f : ex2_sfu(m[x] - top);
-      float* r = js + (warp * kHeads + g + 8 * x) * S::kPitch;
-      if constexpr (!kFp8) {
+  } else {
+    // ---------------------------------------------------------- attention
+    const int g = lane >> 2, t4 = lane & 3;
+    constexpr int kSteps = D / 16;
+    constexpr int kTok = S::kTile / kWarps;   // a warp's tokens of a tile
+    // 8 bits: a weight is the probability times the value's scale.  In powers of
+    // two its exponent is the score's plus the scale's logarithm; with a running
+    // maximum of its own, fp16 holds all weights that matter (the largest is
+    // 2^8, what is lost of small ones 2^-33 of that).
+    constexpr float kRoom = 8.f;
+    uint32_t qa[kSteps][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+    float unit[2];        // scores' factor of rows g and g + 8
+    float wm[2];          // 8 bits: the weights' running maxima
+    bool start = true;
+    int64_t first_of_part = lo;
+    for (int64_t i = lo; i < hi; ++i) {
+      const int stage = (int)((i - lo) % S::kStages);
+      ok = mbar_wait_warp(&full[stage], (uint32_t)(((i - lo) / S::kStages) & 1), kWaitNs);
+      if (!ok) break;
+      const Tile tile = meta[stage];
+      uint8_t* bytes = smem + stage * S::kStage;
+      const uint32_t base = smem_u32(bytes);
+      if (start) {
+        first_of_part = i;
+        start = false;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2*>(r + j * 8 + 2 * t4) =
-              make_float2(o[j][2 * x] * f, o[j][2 * x + 1] * f);
-      } else {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-          *reinterpret_cast<float4*>(r + j * 16 + 4 * t4) =
-              make_float4(o[2 * j][2 * x] * f, o[2 * j + 1][2 * x] * f, o[2 * j][2 * x + 1] * f,
-                          o[2 * j + 1][2 * x + 1] * f);
-      }
-    }
-    __syncthreads();
-    const int h = tile.hh / a.parts, part = tile.hh - h * a.parts;
-    const int64_t item_begin = i - tile.at;
-    const bool from_begin = first_of_part == item_begin, whole = from_begin && item_ends;
-    const int64_t item = (int64_t)tile.row * HH + tile.hh;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + from_begin;
-    if (tid == 0 && from_begin) {
-      a.w.begin[item] = item_begin;
-      a.w.end[item] = whole ? 0 : item_begin + tile.n;
-    }
-    const int heads = a.group - part * kHeads < kHeads ? a.group - part * kHeads : kHeads;
+          for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+        unit[0] = unit[1] = a.scale_log2;
+        wm[0] = wm[1] = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < kHeads * D / 4 / kThreads; ++v) {
-      const int e = v * kThreads + tid, row = e / (D / 4), col = e % (D / 4) * 4;
-      if (row >= heads) break;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      float top = -INFINITY, all = 0.f;
+        for (int s = 0; s < kSteps; ++s) {
+          if constexpr (!kFp8) {
+            // rows 0-7 and 8-15 of the first eight columns, then of the second
+            ldmatrix4(qa[s], base + S::kQ + place<128, kHeads>((lane & 7) + ((lane >> 3) & 1) * 8,
+                                                               2 * s + (lane >> 4)));
+          } else {
+            // the order in which four consecutive codes of a key arrive: columns
+            // 4t, 4t + 1 in the place of 2t, 2t + 1 and the next two in that of
+            // 2t + 8, 2t + 9 (a sum over columns may take them in any order)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][row][0]);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t p =
+                  base + S::kQ + place<128, kHeads>(g + 8 * x, 2 * s + (t4 >> 1)) + (t4 & 1) * 8;
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                           : "=r"(qa[s][x]), "=r"(qa[s][2 + x])
+                           : "r"(p));
+            }
+          }
+        }
+        if constexpr (kFp8) {
+          // queries as fp16, a row times a power of two that puts its largest
+          // between 2^8 and 2^9: fp16 holds bf16's digits down to 2^-22 of that,
+          // and what it loses below is 2^-33 of it
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(js + (w * kHeads + row) * S::kPitch + col);
-        sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
-        const float mw = ml[w][row][0];
-        all += mw == -INFINITY ? 0.f : ml[w][row][1] * ex2_sfu(mw - top);
-      }
-      // (a warp whose scores were all NaN kept the maximum -inf: its sum is NaN)
+          for (int x = 0; x < 2; ++x) {
+            uint32_t top = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (isnan(ml[w][row][1])) all = ml[w][row][1];
-      if (whole) {
-        const float inv = 1.f / all;
-        const int64_t to =
-            ((int64_t)tile.row * a.q_heads + (int64_t)h * a.group + part * kHeads + row) * D + col;
-        *reinterpret_cast<uint2*>(a.out + to) =
-            make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-      } else {
-        *reinterpret_cast<float4*>(a.w.o + (slot * kHeads + row) * D + col) = sum;
-        if (col == 0) {
-          a.w.ml[(slot * kHeads + row) * 2] = top;
-          a.w.ml[(slot * kHeads + row) * 2 + 1] = all;
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+              for (int y = x; y < 4; y += 2) {
+                top = max(top, qa[s][y] << 16 & 0x7fffffffu);
+                top = max(top, qa[s][y] & 0x7fff0000u);
+              }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(8 - exponent), its size kept within fp32's normal numbers
+            int e = 8 + 127 - (int)(top >> 23);
+            e = top == 0 || top >= 0x7f800000u ? 0 : e > 126 ? 126 : e < -126 ? -126 : e;
+            const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+            unit[x] *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+              for (int y = x; y < 4; y += 2)
+                qa[s][y] = pack_half(__uint_as_float(qa[s][y] << 16) * f,
+                                     __uint_as_float(qa[s][y] & 0xffff0000u) * f);
+          }
         }
       }
+      const int valid = tile.len - tile.at * S::kTile;   // tokens of the tile (or more)
+      if (valid < S::kTile) {
+        // values behind the last token are whatever the page holds: a product
+        // with a zero probability has to be zero
+        for (int tok = warp * kTok + lane / (S::kSub / 16); tok < (warp + 1) * kTok;
+             tok += 32 / (S::kSub / 16))
+          if (tok >= valid)
+#pragma unroll
+            for (int y = 0; y < S::kHalves; ++y)
+              *reinterpret_cast<uint4*>(bytes + S::kPool + y * S::kImage + tok * S::kSub +
+                                        lane % (S::kSub / 16) * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int sub = 0; sub < kTok / 16; ++sub) {
+        const int tok0 = warp * kTok + sub * 16;
+        if (tok0 >= valid) break;
+        // scores of 16 heads and 16 tokens
+        float s[2][4] = {};
+        const int kr = tok0 + (lane >> 4) * 8 + (lane & 7);
+        if constexpr (!kFp8) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t b[4];
+            ldmatrix4(b, base + place<S::kSub, S::kTile>(kr, 2 * k + ((lane >> 3) & 1)));
+            mma16816<false>(s[0], qa[k], b[0], b[1]);
+            mma16816<false>(s[1], qa[k], b[2], b[3]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            uint32_t b[4];
+            ldmatrix4(b, base + place<S::kSub, S::kTile>(kr, k + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t b0, b1;
+              e4m3_to_half(b[x], b0, b1);
+              mma16816<true>(s[x >> 1], qa[k + (x & 1)], b0, b1);
+            }
+          }
+        }
+        float vs[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int col = tok0 + n * 8 + 2 * t4;
+          const bool v0 = col < valid, v1 = col + 1 < valid;
+          float k0 = 1.f, k1 = 1.f;
+          if constexpr (kFp8) {
+            const float2 ks = *reinterpret_cast<const float2*>(bytes + S::kScaleAt + col * 4);
+            const float2 v2 = *reinterpret_cast<const float2*>(bytes + S::kScaleAt + S::kScales + col * 4);
+            k0 = ks.x;
+            k1 = ks.y;
+            vs[n][0] = lg2_sfu(v2.x);
+            vs[n][1] = lg2_sfu(v2.y);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            s[n][2 * x] = v0 ? s[n][2 * x] * (kFp8 ? unit[x] * k0 : unit[x]) : -INFINITY;
+            s[n][2 * x + 1] = v1 ? s[n][2 * x + 1] * (kFp8 ? unit[x] * k1 : unit[x]) : -INFINITY;
+          }
+        }
+        // running maximum and sum of rows g and g + 8
+        float sub_m[2];
+        bool grew = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          sub_m[x] = fmaxf(m[x], mx);
+          grew |= sub_m[x] > m[x];
+        }
+        float u[2][4], sub_w[2];
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)   // (behind the last token the scale may be anything)
+              u[n][x] = s[n][x] == -INFINITY ? -INFINITY : s[n][x] + vs[n][x & 1];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = fmaxf(fmaxf(u[0][2 * x], u[0][2 * x + 1]), fmaxf(u[1][2 * x], u[1][2 * x + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            sub_w[x] = fmaxf(wm[x], mx);
+            grew |= sub_w[x] > wm[x];
+          }
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float f = sub_m[x] > m[x] ? ex2_sfu(m[x] - sub_m[x]) : 1.f;
+            float fo = f;
+            l[x] *= f;
+            m[x] = sub_m[x];
+            if constexpr (kFp8) {
+              fo = sub_w[x] > wm[x] ? ex2_sfu(wm[x] - sub_w[x]) : 1.f;
+              wm[x] = sub_w[x];
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+              o[j][2 * x] *= fo;
+              o[j][2 * x + 1] *= fo;
+            }
+          }
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float z = m[x] == -INFINITY ? 0.f : m[x];
+            const float p0 = ex2_sfu(s[n][2 * x] - z), p1 = ex2_sfu(s[n][2 * x + 1] - z);
+            l[x] += p0 + p1;
+            if constexpr (kFp8) {
+              const float zw = wm[x] == -INFINITY ? 0.f : kRoom - wm[x];
+              p[2 * n + x] = pack_half(ex2_sfu(u[n][2 * x] + zw), ex2_sfu(u[n][2 * x + 1] + zw));
+            } else {
+              p[2 * n + x] = pack_bf16(p0, p1);
+            }
+          }
+        // out of 16 heads, the warp's tokens added
+        const uint32_t vb = base + S::kPool;
+        const int vr = tok0 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        if constexpr (!kFp8) {
+#pragma unroll
+          for (int j = 0; j < D / 8; j += 2) {
+            uint32_t b[4];
+            ldmatrix4t(b, vb + place<S::kSub, S::kTile>(vr, j + (lane >> 4)));
+            mma16816<false>(o[j], p, b[0], b[1]);
+            mma16816<false>(o[j + 1], p, b[2], b[3]);
+          }
+        } else {
+          // a transposed pair of codes is two columns: even ones to o[2j], odd to
+          // o[2j + 1], so that a lane ends with four consecutive columns of 16
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 2) {
+            uint32_t b[4];
+            ldmatrix4t(b, vb + place<S::kSub, S::kTile>(vr, j + (lane >> 4)));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t e0, d0, e1, d1;
+              e4m3_to_half(__byte_perm(b[2 * x], 0, 0x3120), e0, d0);
+              e4m3_to_half(__byte_perm(b[2 * x + 1], 0, 0x3120), e1, d1);
+              mma16816<true>(o[2 * (j + x)], p, e0, e1);
+              mma16816<true>(o[2 * (j + x) + 1], p, d0, d1);
+            }
+          }
+        }
+      }
+      const bool item_ends = tile.at == tile.n - 1;
+      if (!item_ends && i + 1 < hi) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        continue;
+      }
+
+      // the part ends: join the warps' sums, in the consumed stage
+      start = true;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        if (t4 == 0) {
+          ml[warp][g + 8 * x][0] = m[x];
+          ml[warp][g + 8 * x][1] = l[x];
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      float* js = reinterpret_cast<float*>(bytes);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][g + 8 * x][0]);
+        const float f = m[x] == -INFINITY ? 0.f
+                        : !kFp8           ? ex2_sfu(m[x] - top)
+                        : wm[x] == -INFINITY ? 0.f
+                                             : ex2_sfu(wm[x] - kRoom - top);
+        float* r = js + (warp * kHeads + g + 8 * x) * S::kPitch;
+        if constexpr (!kFp8) {
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2*>(r + j * 8 + 2 * t4) =
+                make_float2(o[j][2 * x] * f, o[j][2 * x + 1] * f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+            *reinterpret_cast<float4*>(r + j * 16 + 4 * t4) =
+                make_float4(o[2 * j][2 * x] * f, o[2 * j + 1][2 * x] * f, o[2 * j][2 * x + 1] * f,
+                            o[2 * j + 1][2 * x + 1] * f);
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      const int h = tile.hh / a.parts, part = tile.hh - h * a.parts;
+      const int64_t item_begin = i - tile.at;
+      const bool from_begin = first_of_part == item_begin, whole = from_begin && item_ends;
+      const int64_t item = (int64_t)tile.row * HH + tile.hh;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + from_begin;
+      if (tid == 0 && from_begin) {
+        a.w.begin[item] = item_begin;
+        a.w.end[item] = whole ? 0 : item_begin + tile.n;
+      }
+      const int heads = a.group - part * kHeads < kHeads ? a.group - part * kHeads : kHeads;
+#pragma unroll
+      for (int v = 0; v < kHeads * D / 4 / (32 * kWarps); ++v) {
+        const int e = v * 32 * kWarps + tid, row = e / (D / 4), col = e % (D / 4) * 4;
+        if (row >= heads) break;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = -INFINITY, all = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][row][0]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(js + (w * kHeads + row) * S::kPitch + col);
+          sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
+          const float mw = ml[w][row][0];
+          all += mw == -INFINITY ? 0.f : ml[w][row][1] * ex2_sfu(mw - top);
+        }
+        // (a warp whose scores were all NaN kept the maximum -inf: its sum is NaN)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (isnan(ml[w][row][1])) all = ml[w][row][1];
+        if (whole) {
+          const float inv = 1.f / all;
+          const int64_t to =
+              ((int64_t)tile.row * a.q_heads + (int64_t)h * a.group + part * kHeads + row) * D + col;
+          *reinterpret_cast<uint2*>(a.out + to) =
+              make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(a.w.o + (slot * kHeads + row) * D + col) = sum;
+          if (col == 0) {
+            a.w.ml[(slot * kHeads + row) * 2] = top;
+            a.w.ml[(slot * kHeads + row) * 2 + 1] = all;
+          }
+        }
+      }
+      // TMA writes the stage next; ml is written again only by warps that all
+      // others have passed here for
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      if (lane == 0) mbar_arrive(&empty[stage]);
     }
+  }
+  if (!ok) {
+    // copies in flight end within microseconds; give them longer
+    flag_status(a.status, GDN_ERR_TIMEOUT);
+    const uint64_t from = globaltimer_ns();
+    while (globaltimer_ns() - from < 5000000ull) __nanosleep(1000);
   }
 }
 
 // The cut (row, head)s: a CTA takes one query head at a time, its warps every
-// eighth part, then the warps' sums in order.  Rows without tokens get zeros.
+// eighth part, then the warps' sums in order.  (Every load of a step in flight at
+// once: parts one after another took 11 us for the 76 of a row of 32768 tokens.)
+// Rows without tokens get zeros.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
   constexpr int kN = kJoinThreads / 32, kV = D / 32;
-  __shared__ float sm[kN][D + 2];
+  __shared__ float sm[kN][D + 2], weight[kCtas], sum[kCtas];
   const gdn_kv_cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_wait();
   int64_t total;
   asm volatile("ld.global.s64 %0, [%1];" : "=l"(total) : "l"(a.total));
-  const int64_t ctas = total < grid ? total : grid;
+  const int64_t ctas = total < kCtas ? total : kCtas;
   const int64_t jobs = (int64_t)c.rows * a.q_heads;
   for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
     const int64_t row = job / a.q_heads;
@@ -560,41 +702,69 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a, int grid) {
     auto owner = [&](int64_t t) {
       return (int64_t)(((unsigned __int128)(t + 1) * ctas - 1) / total);
     };
-    const int64_t first = owner(b), last = owner(e - 1);
-    float m = -INFINITY, l = 0.f, o[kV] = {};
-    for (int64_t p = first + warp; p <= last; p += kN) {
-      const int64_t slot = 2 * p + (p == first);
-      const float mp = ld_waited(a.w.ml + (slot * kHeads + r) * 2);
-      const float lp = ld_waited(a.w.ml + (slot * kHeads + r) * 2 + 1);
-      const float* src = a.w.o + (slot * kHeads + r) * D + lane * kV;
-      float x[kV];
-#pragma unroll
-      for (int i = 0; i < kV; ++i) x[i] = ld_waited(src + i);
-      const float top = fmaxf(m, mp);
-      const float fa = m == -INFINITY ? 0.f : ex2_sfu(m - top);
-      const float fb = mp == -INFINITY ? (isnan(lp) ? 1.f : 0.f) : ex2_sfu(mp - top);
-      l = l * fa + lp * fb;
-#pragma unroll
-      for (int i = 0; i < kV; ++i) o[i] = o[i] * fa + x[i] * fb;
-      m = top;
+    const int64_t first = owner(b);
+    const int parts = (int)(owner(e - 1) - first + 1);      // up to the CTAs
+    auto slot = [&](int p) { return ((2 * (first + p) + (p == 0)) * kHeads + r); };
+    // the parts' maxima and sums, then every part's factor
+    float m = -INFINITY;
+    for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
+      const float mp = ld_waited(a.w.ml + slot(p) * 2);
+      weight[p] = mp;
+      sum[p] = ld_waited(a.w.ml + slot(p) * 2 + 1);
+      m = fmaxf(m, mp);
     }
-    if (lane == 0) {
-      sm[warp][D] = m;
-      sm[warp][D + 1] = l;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) sm[warp][D] = m;
+    __syncthreads();
+    m = sm[0][D];
+#pragma unroll
+    for (int w = 1; w < kN; ++w) m = fmaxf(m, sm[w][D]);
+    float l = 0.f;
+    for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
+      const float mp = weight[p], lp = sum[p];
+      // (scores that are all NaN leave the maximum -inf and a NaN sum)
+      const float f = mp == -INFINITY ? (isnan(lp) ? 1.f : 0.f) : ex2_sfu(mp - m);
+      weight[p] = f;
+      l += lp * f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) sm[warp][D + 1] = l;
+    __syncthreads();
+    // a warp adds every eighth part, four in flight
+    float o[kV] = {};
+    for (int p = warp; p < parts; p += 4 * kN) {
+      float x[4][kV];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool on = p + i * kN < parts;
+        const float* src = a.w.o + slot(on ? p + i * kN : p) * D + lane * kV;
+        if constexpr (kV == 4) {
+          const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
+          x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+        } else {
+          x[i][0] = ld_waited(src);
+          x[i][1] = ld_waited(src + 1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p + i * kN < parts) {
+          const float f = weight[p + i * kN];
+#pragma unroll
+          for (int j = 0; j < kV; ++j) o[j] = f == 0.f ? o[j] : fmaf(x[i][j], f, o[j]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kV; ++i) sm[warp][lane * kV + i] = o[i];
     __syncthreads();
     if (threadIdx.x < D) {
-      float top = -INFINITY, all = 0.f, x = 0.f;
-#pragma unroll
-      for (int w = 0; w < kN; ++w) top = fmaxf(top, sm[w][D]);
+      float all = 0.f, x = 0.f;
 #pragma unroll
       for (int w = 0; w < kN; ++w) {
-        const float mw = sm[w][D], lw = sm[w][D + 1];
-        const float f = mw == -INFINITY ? (isnan(lw) ? 1.f : 0.f) : ex2_sfu(mw - top);
-        all += lw * f;
-        x += sm[w][threadIdx.x] * f;
+        all += sm[w][D + 1];
+        x += sm[w][threadIdx.x];
       }
       out[threadIdx.x] = __float2bfloat16_rn(x / all);
     }
@@ -605,10 +775,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a, int grid) {
 struct Layout {
   size_t begin, end, ml, o, bytes;
 };
-int ctas_of(int32_t d) { return kSms * (d == 128 ? 2 : 4); }
 Layout layout_of(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t d) {
   const int32_t group = q_heads / kv_heads, parts = (group + kHeads - 1) / kHeads;
-  const size_t items = (size_t)rows * kv_heads * parts, slots = 2 * (size_t)ctas_of(d);
+  const size_t items = (size_t)rows * kv_heads * parts, slots = 2 * (size_t)kCtas;
   Layout l;
   l.begin = 256;
   l.end = l.begin + align_up(items * 8, 256);
@@ -620,7 +789,26 @@ Layout layout_of(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t d) {
 int heads_check(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t d) {
   if (rows < 1 || q_heads < 1 || kv_heads < 1) return GDN_ERR_INVALID_ARG;
   if (q_heads % kv_heads || q_heads / kv_heads > 128 || !kv::dim_ok(d)) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)rows * q_heads > kLongestAxis) return GDN_ERR_UNSUPPORTED;   // 32-bit coordinates
   return GDN_OK;
+}
+
+// A pool of keys or values as [layers * pages][kv heads * page][row bytes], read in
+// boxes of 128 (64) bytes x the smaller of a page and a tile, swizzled.
+bool pool_map(CUtensorMap* m, const void* pool, const gdn_kv_cache& c, int32_t row, int32_t tile) {
+  attn::EncodeFn enc = attn::encoder();
+  if (!enc) return false;
+  memset(m, 0, sizeof *m);
+  const bool fp8 = c.dtype == GDN_E4M3;
+  cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)c.kv_heads * c.page,
+                        (cuuint64_t)c.layers * c.pages};
+  cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)row * c.kv_heads * c.page};
+  cuuint32_t box[3] = {fp8 ? (cuuint32_t)c.d : 64u, (cuuint32_t)(c.page < tile ? c.page : tile), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_heads, float scale,
@@ -628,6 +816,8 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
   if (const int rc = kv::check_cache(cache)) return rc;
   const gdn_kv_cache c = *cache;
   if (const int rc = heads_check(c.rows, q_heads, c.kv_heads, c.d)) return rc;
+  if ((int64_t)c.layers * c.pages > kLongestAxis || (int64_t)c.kv_heads * c.page > kLongestAxis)
+    return GDN_ERR_UNSUPPORTED;
   if (!q || !out || layer < 0 || layer >= c.layers || !(scale > 0.f) || scale > 3e38f)
     return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return GDN_ERR_ALIGNMENT;
@@ -642,15 +832,10 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
                       own.s[4],       own.s[5], own.s[6]};
   const Span outs[] = {span_of(out, io), span_of(use_ws ? ws : nullptr, lay.bytes)};
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
-  Args a = {};
+  Args a;
+  memset(&a, 0, sizeof a);
   a.status = status_ptr();
   if (!a.status) return GDN_ERR_CUDA;
-  void* scratch = ws;
-  if (!use_ws && scratch_alloc(&scratch, lay.bytes, st) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
-  a.q = (const __nv_bfloat16*)q;
   a.out = (__nv_bfloat16*)out;
   a.c = c;
   a.layer = layer;
@@ -658,33 +843,41 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
   a.group = q_heads / c.kv_heads;
   a.parts = (a.group + kHeads - 1) / kHeads;
   a.items_per_row = c.kv_heads * a.parts;
-  while ((1 << a.page_log2) < c.page) ++a.page_log2;
+  a.page_log2 = kv::log2_of(c.page);
   a.scale_log2 = scale * kLog2e;
+  const bool fp8 = c.dtype == GDN_E4M3;
+  const int32_t row = c.d * (fp8 ? 1 : 2), tile = row == 256 ? 64 : 128;
+  if (!pool_map(&a.k, c.k, c, row, tile) || !pool_map(&a.v, c.v, c, row, tile) ||
+      !attn::heads_map(&a.q, q, (int64_t)c.rows * q_heads, c.d, kHeads))
+    return GDN_ERR_CUDA;
+  void* scratch = ws;
+  if (!use_ws && scratch_alloc(&scratch, lay.bytes, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
   char* p = (char*)scratch;
   a.total = (int64_t*)p;
   a.w.begin = (int64_t*)(p + lay.begin);
   a.w.end = (int64_t*)(p + lay.end);
   a.w.ml = (float*)(p + lay.ml);
   a.w.o = (float*)(p + lay.o);
-  const bool fp8 = c.dtype == GDN_E4M3;
-  const int ctas = ctas_of(c.d);
   cudaError_t e;
-  auto run = [&](auto shape, auto kern) {
+  static std::atomic<uint64_t> on[4];
+  auto run = [&](auto shape, auto kern, std::atomic<uint64_t>& allowed) {
     using S = decltype(shape);
-    e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e == cudaSuccess)
-      e = launch(false, kern, dim3(ctas), kThreads, S::kSmem, 0, st, a);
+    e = allow_smem((const void*)kern, S::kSmem, allowed);
+    if (e == cudaSuccess) e = launch(false, kern, dim3(kCtas), kThreads, S::kSmem, 0, st, a);
   };
   if (c.d == 128)
-    fp8 ? run(Shape<128, true>{}, decode_kernel<128, true>)
-        : run(Shape<128, false>{}, decode_kernel<128, false>);
+    fp8 ? run(Shape<128, true>{}, decode_kernel<128, true>, on[0])
+        : run(Shape<128, false>{}, decode_kernel<128, false>, on[1]);
   else
-    fp8 ? run(Shape<64, true>{}, decode_kernel<64, true>)
-        : run(Shape<64, false>{}, decode_kernel<64, false>);
+    fp8 ? run(Shape<64, true>{}, decode_kernel<64, true>, on[2])
+        : run(Shape<64, false>{}, decode_kernel<64, false>, on[3]);
   if (e == cudaSuccess) {
     const int64_t jobs = (int64_t)c.rows * q_heads, most = 8 * kSms;
     e = launch(true, c.d == 128 ? join_kernel<128> : join_kernel<64>,
-               dim3((unsigned)(jobs < most ? jobs : most)), kJoinThreads, 0, 0, st, a, ctas);
+               dim3((unsigned)(jobs < most ? jobs : most)), kJoinThreads, 0, 0, st, a);
   }
   count_launches(2);
   if (e != cudaSuccess) (void)cudaGetLastError();

@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(kListThreads) prefill_list_kernel(ListArgs a) 
   list_jobs(a);
 }
 
-// The parts of a job, joined in their order: a warp takes every eighth packed
-// row, a lane 4 columns (2 of 64).
+// The parts of a job, joined in their order: a warp takes a packed row, a lane 4
+// columns (2 of 64), with the loads of eight parts in flight.
 constexpr int kJoinThreads = 256;
 constexpr int kMostParts = 32;
 template <int D>
@@ -503,10 +503,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
     return;
   grid_wait();
   const Place pl(seq, a.per, 0, 1);
-  // blockIdx.y: 32 rows of the job's 256
-  for (int row = 32 * blockIdx.y + warp; row < 32 * blockIdx.y + 32; row += kJoinThreads / 32) {
+  // blockIdx.y: 8 rows of the job's 256
+  {
+    const int row = 8 * blockIdx.y + warp;
     const int w = row >> 7, in = row & 127, qi = in / a.s.group;
-    if (qi >= pl.rows_of(w)) continue;
+    if (qi >= pl.rows_of(w)) return;
     const int64_t base = (int64_t)blockIdx.x * a.parts * 256 + row;
     float m = -INFINITY, l = 0.f;
     if (lane < a.parts) {
@@ -524,21 +525,29 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     const unsigned some = __ballot_sync(0xffffffffu, on);
     float acc[kV] = {};
-#pragma unroll 8
-    for (int p = 0; p < a.parts; ++p) {
-      const float fp = __shfl_sync(0xffffffffu, f, p);
-      if (some >> p & 1) {
-        const float* src = a.o + (base + (int64_t)p * 256) * D + lane * kV;
-        float x[kV];
-        if constexpr (kV == 4) {
-          const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
-          x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-        } else {
-          x[0] = ld_waited(src);
-          x[1] = ld_waited(src + 1);
-        }
+    for (int p0 = 0; p0 < a.parts; p0 += 8) {
+      float x[8][kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] = fmaf(x[i], fp, acc[i]);
+      for (int i = 0; i < 8; ++i) {
+        const bool in_use = p0 + i < a.parts && (some >> (p0 + i) & 1);
+        const float* src = a.o + (base + (int64_t)(p0 + i) * 256) * D + lane * kV;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) x[i][j] = 0.f;
+        if constexpr (kV == 4) {
+          if (in_use) {
+            const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
+            x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+          }
+        } else {
+          if (in_use) x[i][0] = ld_waited(src);
+          if (in_use) x[i][1] = ld_waited(src + 1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float fp = __shfl_sync(0xffffffffu, f, (p0 + i) & 31);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) acc[j] = fmaf(x[i][j], p0 + i < a.parts ? fp : 0.f, acc[j]);
       }
     }
     const int64_t r =
@@ -655,7 +664,7 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   count_launches(1);
   if (mode == kParts && e == cudaSuccess) {
     e = launch(true, s.d == 128 ? prefill_join_kernel<128> : prefill_join_kernel<64>,
-               dim3((unsigned)jobs, 8), kJoinThreads, 0, 0, st, a);
+               dim3((unsigned)jobs, 32), kJoinThreads, 0, 0, st, a);
     count_launches(1);
   }
   if (e != cudaSuccess) (void)cudaGetLastError();

@@ -252,6 +252,20 @@ inline bool heads_map(CUtensorMap* m, const void* x, int64_t tokens, int32_t hea
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// x [rows][d] bf16, contiguous, read in boxes of 64 columns x box_rows rows.
+inline bool heads_map(CUtensorMap* m, const void* x, int64_t rows, int32_t d, uint32_t box_rows) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  memset(m, 0, sizeof *m);
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The checks that the prompt kernels share: sizes, strides, alignment.
 struct Shape {
   int32_t batch;

@@ -107,10 +107,12 @@ reserve_kernel(gdn_kv_cache c, const int32_t* counts, int32_t* start, int32_t* l
     now = to;
     return 0;
   };
-  int64_t want = 0, step, old, now, len;
+  int64_t want = 0, step, old, now, len, first;
+  int bad = 0;
+  const bool one = c.rows <= kPlan;   // then what the first round found is kept
   for (int base = 0; base < c.rows; base += kPlan) {
-    ask(base + threadIdx.x, old, now, len);
-    scan(now - old, sm, step);
+    bad = ask(base + threadIdx.x, old, now, len);
+    first = scan(now - old, sm, step);
     want += step;
   }
   if (want > c.pages) want = c.pages;
@@ -118,10 +120,12 @@ reserve_kernel(gdn_kv_cache c, const int32_t* counts, int32_t* start, int32_t* l
   int64_t before = 0;
   for (int base = 0; base < c.rows; base += kPlan) {
     const int row = base + threadIdx.x;
-    const int bad = ask(row, old, now, len);
+    if (!one) {
+      bad = ask(row, old, now, len);
+      first = before + scan(now - old, sm, step);
+      before += step;
+    }
     const int64_t need = now - old;
-    const int64_t first = before + scan(need, sm, step);
-    before += step;
     const bool ok = bad == 0 && (need == 0 || first + need <= found);
     if (row < c.rows) {
       start[row] = ok ? (int32_t)len : -1;
@@ -151,50 +155,69 @@ struct AppendArgs {
   const __nv_bfloat16 *k, *v;
   const int32_t *start, *cu;
   int64_t tokens, k_stride, v_stride;
-  int32_t layer;
+  int32_t layer, page_log2;
   unsigned* status;
 };
 
 // d / 8 lanes hold one head of one token, 16 bytes of its key and of its value
-// each.  Bound by HBM for prompts (4 rows of up to 8192 tokens into 8 bits: see
-// the measurements below), by latency for a decoding step's tokens.
-template <int D, bool kFp8>
+// each, for kUnits tokens in turn whose loads are all in flight.  Prompts are
+// bound by HBM: four tokens' loads cover the chain of small ones (sequence,
+// start, page) that each place takes.  A decoding step's few tokens are bound by
+// that chain: one each.
+template <int D, bool kFp8, int kUnits>
 __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8;
+  constexpr int kSpan = kCopy / kLanes;   // heads of tokens that the CTA holds at a time
   const gdn_kv_cache& c = a.c;
-  const int64_t unit = ((int64_t)blockIdx.x * kCopy + threadIdx.x) / kLanes;
+  const int64_t units = a.tokens * c.kv_heads;
+  const int64_t unit0 = (int64_t)blockIdx.x * kSpan * kUnits + threadIdx.x / kLanes;
   const int l = threadIdx.x % kLanes;
-  const int64_t t = unit / c.kv_heads;
-  const int h = (int)(unit - t * c.kv_heads);
-  const bool there = t < a.tokens;
-  uint4 x[2] = {};
-  if (there) {
-    x[0] = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + l * 8);
-    x[1] = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + l * 8);
+  int64_t t[kUnits];
+  int h[kUnits];
+  uint4 x[kUnits][2];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int64_t unit = unit0 + u * kSpan;
+    // (64-bit divisions were most of the kernel's instructions)
+    t[u] = unit >= units ? -1
+           : units >> 32 ? unit / c.kv_heads
+                         : (int64_t)((uint32_t)unit / (uint32_t)c.kv_heads);
+    h[u] = (int)(unit - t[u] * c.kv_heads);
+    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+    if (t[u] >= 0) {
+      x[u][0] = *reinterpret_cast<const uint4*>(a.k + t[u] * a.k_stride + h[u] * D + l * 8);
+      x[u][1] = *reinterpret_cast<const uint4*>(a.v + t[u] * a.v_stride + h[u] * D + l * 8);
+    }
   }
-  // the token's row and place
-  int64_t at = -1;   // first element of its head in the pool, -1: nowhere
-  if (there) {
-    int64_t row = t, i = 0;
+  // the tokens' rows and places
+  int64_t at[kUnits];   // first element of its head in the pool, -1: nowhere
+  int64_t seen = 0;     // the last row found: later tokens lie in it or behind it
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    at[u] = -1;
+    if (t[u] < 0) continue;
+    int64_t row = t[u], i = 0;
     bool ok = true;
     if (a.cu) {
-      int lo = 0, hi = c.rows - 1;   // last row with cu[row] <= t
+      int64_t lo = seen, hi = c.rows - 1;   // last row with cu[row] <= t
+      if (a.cu[seen + 1] > t[u]) hi = seen;
       while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (a.cu[mid] <= t[u]) lo = mid; else hi = mid - 1;
       }
-      row = lo;
-      i = t - a.cu[lo];
-      ok = i >= 0 && t < a.cu[lo + 1];
+      row = seen = lo;
+      i = t[u] - a.cu[lo];
+      ok = i >= 0 && t[u] < a.cu[lo + 1];
       if (!ok) flag_status(a.status, GDN_ERR_BAD_SEQLENS);
     }
     const int64_t s = ok ? a.start[row] : -1;
     if (ok && s >= 0 && s + i < c.lengths[row]) {
-      const int64_t pos = s + i, n = pos / c.page;
+      const int64_t pos = s + i, n = pos >> a.page_log2;
       int32_t p = -1;
       if (n < c.max_pages) p = c.table[row * c.max_pages + n];
       if (p >= 0 && p < c.pages)
-        at = ((((int64_t)a.layer * c.pages + p) * c.kv_heads + h) * c.page + (pos - n * c.page));
+        at[u] = ((((int64_t)a.layer * c.pages + p) * c.kv_heads + h[u]) << a.page_log2) +
+                (pos & (c.page - 1));
       else
         flag_status(a.status, GDN_ERR_BAD_CACHE);
     } else if (ok && s < -1) {
@@ -202,29 +225,31 @@ __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    void* pool = i ? c.v : c.k;
-    if constexpr (!kFp8) {
-      if (at >= 0)
-        *reinterpret_cast<uint4*>((__nv_bfloat16*)pool + at * D + l * 8) = x[i];
-    } else {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      float f[8];
+  for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-      float m = amax8(f);
+    for (int i = 0; i < 2; ++i) {
+      void* pool = i ? c.v : c.k;
+      if constexpr (!kFp8) {
+        if (at[u] >= 0)
+          *reinterpret_cast<uint4*>((__nv_bfloat16*)pool + at[u] * D + l * 8) = x[u][i];
+      } else {
+        const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+        float f[8];
 #pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = max_nan(m, kTiny);
-      if (at >= 0) {
-        *reinterpret_cast<uint2*>((uint8_t*)pool + at * D + l * 8) = quantise8_bf16(f, m);
-        if (l == 0) (i ? c.v_scale : c.k_scale)[at] = scale_of(m);
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = __uint_as_float(w[j] << 16);
+          f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+        float m = amax8(f);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = max_nan(m, kTiny);
+        if (at[u] >= 0) {
+          *reinterpret_cast<uint2*>((uint8_t*)pool + at[u] * D + l * 8) = quantise8_bf16(f, m);
+          if (l == 0) (i ? c.v_scale : c.k_scale)[at[u]] = scale_of(m);
+        }
       }
     }
-  }
 }
 
 // --------------------------------------------------------------- freeing
@@ -301,20 +326,24 @@ fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t
     const int32_t t = __ldcg(c.lengths + s);
     return t <= 0 ? 0 : t > c.max_pages * c.page ? -1 : t;
   };
-  int64_t want = 0, step;
+  int64_t want = 0, step, at = 0;
+  int32_t t = 0;
+  const bool one = n <= kPlan;   // then what the first round found is kept
   for (int base = 0; base < n; base += kPlan) {
-    const int32_t t = tokens(base + threadIdx.x);
-    scan(t > 0 && t % c.page != 0, sm, step);
+    t = tokens(base + threadIdx.x);
+    at = scan(t > 0 && t % c.page != 0, sm, step);
     want += step;
   }
   const int64_t found = want ? find_free(c.refs, c.pages, want, list, sm) : 0;
   int64_t before = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + threadIdx.x;
-    int32_t t = tokens(i);
+    if (!one) {
+      t = tokens(i);
+      at = before + scan(t > 0 && t % c.page != 0, sm, step);
+      before += step;
+    }
     const bool need = t > 0 && t % c.page != 0;
-    const int64_t at = before + scan(need, sm, step);
-    before += step;
     if (i >= n) continue;
     if (t < 0) flag_status(status, GDN_ERR_BAD_CACHE);
     Pair p = {t, -1};
@@ -534,13 +563,19 @@ int gdn_cache_append(const gdn_kv_cache* cache, int32_t layer, const void* k, co
                       span_of(cu_seqlens, (size_t)(c.rows + 1) * 4)};
   if (any_overlap(ins, own.s)) return GDN_ERR_INVALID_ARG;
   AppendArgs a = {c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, start, cu_seqlens, tokens,
-                  k_stride, v_stride, layer, status_ptr()};
+                  k_stride, v_stride, layer, kv::log2_of(c.page), status_ptr()};
   if (!a.status) return GDN_ERR_CUDA;
-  const int64_t ctas = (tokens * c.kv_heads * (c.d / 8) + kCopy - 1) / kCopy;
+  // four tokens a thread where that still fills the GPU (152 SMs x 8 CTAs)
+  const int64_t one = (tokens * c.kv_heads * (c.d / 8) + kCopy - 1) / kCopy;
+  const bool four = one >= 1216;
+  const int64_t ctas = four ? (one + 3) / 4 : one;
   if (ctas > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
   const bool fp8 = c.dtype == GDN_E4M3;
-  auto* kern = c.d == 128 ? (fp8 ? append_kernel<128, true> : append_kernel<128, false>)
-                          : (fp8 ? append_kernel<64, true> : append_kernel<64, false>);
+  auto pick = [&](auto* k1, auto* k4) { return four ? k4 : k1; };
+  auto* kern = c.d == 128 ? (fp8 ? pick(append_kernel<128, true, 1>, append_kernel<128, true, 4>)
+                                 : pick(append_kernel<128, false, 1>, append_kernel<128, false, 4>))
+                          : (fp8 ? pick(append_kernel<64, true, 1>, append_kernel<64, true, 4>)
+                                 : pick(append_kernel<64, false, 1>, append_kernel<64, false, 4>));
   count_launches(1);
   return launch(false, kern, dim3((unsigned)ctas), kCopy, 0, 0, (cudaStream_t)stream, a) ==
                  cudaSuccess

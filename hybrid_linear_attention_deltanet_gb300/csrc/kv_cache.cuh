@@ -11,6 +11,11 @@ namespace kv {
 using namespace hostcheck;
 
 inline bool page_ok(int32_t page) { return page >= 16 && page <= 256 && (page & (page - 1)) == 0; }
+inline int32_t log2_of(int32_t page) {
+  int32_t n = 0;
+  while ((1 << n) < page) ++n;
+  return n;
+}
 inline bool dim_ok(int32_t d) { return d == 64 || d == 128; }
 
 inline size_t pool_bytes(const gdn_kv_cache& c) {
