@@ -140,7 +140,8 @@ def load():
     lib.gdn_attention_prefill_backward.argtypes = [vp] * 8 + [f32, vp, vp, vp, i32, i64, i64, i32,
                                                               i32, i32, i64, i64, i64, vp]
     lib.gdn_attention_prefill_backward.restype = ctypes.c_int
-    lib.gdn_attention_prefill_backward_workspace_size.argtypes = [i32, i64, i32, i32, i32, i32]
+    lib.gdn_attention_prefill_backward_workspace_size.argtypes = [i32, i64, i64, i32, i32, i32,
+                                                                  i32]
     lib.gdn_attention_prefill_backward_workspace_size.restype = sz
     lib.gdn_attention_prefill_backward_ws.argtypes = [vp] * 8 + [f32, vp, vp, vp, i32, i64, i64,
                                                                  i32, i32, i32, i64, i64, i64, vp,
@@ -1046,10 +1047,13 @@ def attention_prefill(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None, o
     return out, lse
 
 
-def attention_prefill_backward_workspace_size(batch, seqlen, q_heads, kv_heads, d,
-                                              varlen=False) -> int:
-    n = load().gdn_attention_prefill_backward_workspace_size(batch, seqlen, int(bool(varlen)),
-                                                             q_heads, kv_heads, d)
+def attention_prefill_backward_workspace_size(batch, seqlen, q_heads, kv_heads, d, varlen=False,
+                                              seqlen_k=None) -> int:
+    """Bytes of ``attention_prefill_backward``'s workspace for batch sequences of
+    seqlen queries (varlen: seqlen in all) and seqlen_k keys (as many when None)."""
+    n = load().gdn_attention_prefill_backward_workspace_size(
+        batch, seqlen, seqlen if seqlen_k is None else seqlen_k, int(bool(varlen)), q_heads,
+        kv_heads, d)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("unsupported attention_prefill_backward arguments")
     return int(n)

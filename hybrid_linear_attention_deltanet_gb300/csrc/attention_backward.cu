@@ -34,6 +34,12 @@ struct BwdArgs {
   float c, scale;              // scale log2 e, scale
   int64_t tq;
   int32_t q_heads, per;        // per: queries of a 128-row tile
+  // the order of the jobs, longest first (nullptr: that of the sequences)
+  const int32_t* count[2];     // [tiles of keys, of queries]
+  const Job* jobs[2];
+  // parts of a key tile's queries, and their sums of dV and dK, [jobs][parts][2][128][D]
+  int32_t parts;
+  float* part;
   unsigned* status;
 };
 
@@ -48,7 +54,8 @@ struct RowArgs {
 // D / 8 lanes a row, 16 bytes of each tensor a lane; bound by HBM.
 template <int D>
 __global__ void __launch_bounds__(256) rows_kernel(RowArgs a) {
-  grid_release_next();
+  grid_wait();
+  grid_release_next();   // (the next kernels read the sequences before they wait)
   constexpr int kLanes = D / 8;
   const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
   const int l = threadIdx.x % kLanes;
@@ -169,6 +176,14 @@ __device__ __forceinline__ void put_bf16(uint32_t at, const uint32_t (&x)[32]) {
   tmem_st16(at, p);
 }
 
+// A row's statistic as it stands in L2 (the queries' kernel may start beside the
+// keys' one, without waiting for it, but after that has waited for the rows').
+__device__ __forceinline__ float ld_stat(const float* p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // The common part of both kernels: the job's place, barriers, tensor memory.
 template <int D>
 __device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, int per, bool keys, Seq& seq,
@@ -183,9 +198,17 @@ __device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, int per, bo
     return false;
   }
   head = blockIdx.x % a.s.kv_heads;
-  if (!locate<kThreads>(a.s, blockIdx.x / a.s.kv_heads, per, keys, !keys,
-                        reinterpret_cast<int64_t*>(sm), a.status, seq))
+  const int64_t job = blockIdx.x / a.s.kv_heads;
+  const Job* list = a.jobs[keys ? 0 : 1];
+  if (list) {
+    if (job >= (int64_t)ld_relaxed_gpu((const uint32_t*)a.count[keys ? 0 : 1])) return false;
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(list + job);
+    seq = {(int32_t)ld_relaxed_gpu(x), (int32_t)ld_relaxed_gpu(x + 1), (int32_t)ld_relaxed_gpu(x + 2),
+           (int32_t)ld_relaxed_gpu(x + 3), (int32_t)ld_relaxed_gpu(x + 4)};
+  } else if (!locate<kThreads>(a.s, job, per, keys, !keys, reinterpret_cast<int64_t*>(sm), a.status,
+                               seq)) {
     return false;
+  }
   if (tid == 0) {
     mbar_init(&b.own, 1);
     for (int i = 0; i < 3; ++i) {
@@ -240,14 +263,18 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   Seq seq;
   int head;
+  grid_wait();
+  grid_release_next();   // the queries' kernel starts where SMs are left: it needs nothing of this one
   if (!begin<D>(a, sm, kRows, true, seq, head)) return;
   const int32_t group = a.s.group, shift = seq.lk - seq.lq;
   const int32_t k0 = seq.tile * kRows;                       // the tile's first key
   const int32_t used = a.per * group;                        // rows of a tile of queries
   // tiles of queries: from that of the first query that sees key k0
   const int32_t sees = k0 - shift > 0 ? k0 - shift : 0;
-  const int32_t t0 = sees / a.per, t1 = (seq.lq + a.per - 1) / a.per;
-  const int32_t n = sees < seq.lq ? t1 - t0 : 0;
+  const int32_t f0 = sees / a.per, f1 = sees < seq.lq ? (seq.lq + a.per - 1) / a.per : f0;
+  // this CTA's part of them
+  const int32_t t0 = f0 + (int32_t)((int64_t)(f1 - f0) * blockIdx.y / a.parts);
+  const int32_t n = f0 + (int32_t)((int64_t)(f1 - f0) * (blockIdx.y + 1) / a.parts) - t0;
   // rows that no query fills take part in the products with P = dS = 0: zeros,
   // so that the products are
   if (used < kRows && warp < 5)
@@ -256,7 +283,6 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_wait();
   const uint32_t tmem = b.tmem;
   constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 256 + D;
   bool ok = true;
@@ -394,8 +420,8 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       const int col = 64 * w + row;
       const int64_t at = (int64_t)(t0 + i) * used + col;
       const bool on = fetch && i < n && col < used && at < (int64_t)seq.lq * group;
-      x = on ? ld_waited(a.nlse + stat0 + at) : 0.f;
-      y = on ? ld_waited(a.nd + stat0 + at) : 0.f;
+      x = on ? ld_stat(a.nlse + stat0 + at) : 0.f;
+      y = on ? ld_stat(a.nd + stat0 + at) : 0.f;
     };
     float nl, nd;
     read(0, nl, nd);
@@ -467,8 +493,27 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
     if (ok) {
       // one warpgroup dV, the other dK
       const bool live = (int64_t)k0 + row < seq.lk;
-      const int64_t to = ((seq.k0 + k0 + row) * a.s.kv_heads + head) * D;
-      store_row<D>(tmem + lanes + (w ? kDK : kDV), w ? a.scale : 1.f, (w ? a.dk : a.dv) + to, live, n == 0);
+      const uint32_t from = tmem + lanes + (w ? kDK : kDV);
+      if (a.parts == 1) {
+        const int64_t to = ((seq.k0 + k0 + row) * a.s.kv_heads + head) * D;
+        store_row<D>(from, w ? a.scale : 1.f, (w ? a.dk : a.dv) + to, live, n == 0);
+      } else {
+        float* to = a.part + ((((int64_t)blockIdx.x * a.parts + blockIdx.y) * 2 + w) * kRows + row) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(from + 32 * i, o);
+            tmem_ld_wait_regs(o);
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (live)
+              *reinterpret_cast<uint4*>(to + 32 * i + 4 * x) =
+                  n > 0 ? make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3])
+                        : make_uint4(0, 0, 0, 0);
+        }
+      }
     }
   }
   finish(ok, tmem, a.status);
@@ -497,7 +542,6 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_wait();
   const uint32_t tmem = b.tmem;
   constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;           // two buffers of scores
   bool ok = true;
@@ -614,7 +658,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
     const int qi = row / group;
     const bool live = qi < rows;
     const int64_t stat = ((int64_t)head * a.tq + seq.q0 + first) * group + row;
-    const float nl = live ? ld_waited(a.nlse + stat) : 0.f, nd = live ? ld_waited(a.nd + stat) : 0.f;
+    const float nl = live ? ld_stat(a.nlse + stat) : 0.f, nd = live ? ld_stat(a.nd + stat) : 0.f;
     const int32_t last = first + qi + shift;               // the last key that the row sees
     const F2 cc = f2(a.c, a.c), ll = f2(nl, nl), dd = f2(nd, nd);
     for (int32_t j = 0; j < n; ++j) {
@@ -664,9 +708,79 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
     }
   }
   finish(ok, tmem, a.status);
+  grid_wait();   // the keys' kernel, beside which this one ran, is part of the call
 }
 
-size_t stat_bytes(int64_t tq, int32_t q_heads) { return align_up((size_t)tq * q_heads * 4, 256); }
+__global__ void __launch_bounds__(kListThreads) backward_list_kernel(ListArgs keys, ListArgs queries) {
+  grid_wait();
+  grid_release_next();
+  list_jobs(blockIdx.x ? queries : keys);
+}
+
+// The parts of a key tile's dV and dK, added in their order: 4 columns a thread.
+template <int D>
+__global__ void __launch_bounds__(kThreads) keys_sum_kernel(const __grid_constant__ BwdArgs a) {
+  __shared__ int64_t scratch[kThreads + 6];
+  Seq seq;
+  const int head = blockIdx.x % a.s.kv_heads;
+  grid_wait();
+  grid_release_next();
+  if (!locate<kThreads>(a.s, blockIdx.x / a.s.kv_heads, kRows, true, false, scratch, nullptr, seq)) return;
+  const int64_t k0 = (int64_t)seq.tile * kRows;
+  constexpr int kVecs = kRows * D / 4;
+  for (int i = blockIdx.y * kThreads + threadIdx.x; i < 2 * kVecs; i += gridDim.y * kThreads) {
+    const int w = i / kVecs, row = i % kVecs / (D / 4), col = i % (D / 4) * 4;
+    if (k0 + row >= seq.lk) continue;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* from = a.part + (((int64_t)blockIdx.x * a.parts * 2 + w) * kRows + row) * D + col;
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p) {
+      const float4 x = ld_waited(reinterpret_cast<const float4*>(from + (int64_t)p * 2 * kRows * D));
+      sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+    }
+    const float f = w ? a.scale : 1.f;
+    *reinterpret_cast<uint2*>((w ? a.dk : a.dv) + ((seq.k0 + k0 + row) * a.s.kv_heads + head) * D + col) =
+        make_uint2(pack(sum.x * f, sum.y * f), pack(sum.z * f, sum.w * f));
+  }
+}
+
+// How a call is launched, and its scratch.
+struct Plan {
+  int64_t key_tiles, query_tiles;   // packed: upper bounds, sum_n ceil(len_n / per) <= T / per + N
+  bool listed;
+  int32_t parts;
+  size_t stat, key_jobs, query_jobs, part, bytes;   // statistics, then where the others lie
+};
+Plan plan_of(const Shape& s, int sms) {
+  const int32_t per = kRows / (s.q_heads / s.kv_heads);
+  Plan p = {};
+  const int64_t tq = s.tq(), tk = s.tk(), iters = (s.seqlen_q + per - 1) / per;
+  p.key_tiles = s.packed ? tk / kRows + s.batch : (s.seqlen_k + kRows - 1) / kRows * s.batch;
+  p.query_tiles = s.packed ? tq / per + s.batch : iters * s.batch;
+  if (tk == 0) p.key_tiles = 0;
+  const int64_t jobs = p.key_tiles * s.kv_heads;
+  // a list where either kernel has more than two turns of jobs; where the keys'
+  // jobs leave SMs empty and are long, a part of their queries each
+  p.listed = jobs > 2 * sms || p.query_tiles * s.kv_heads > 2 * sms;
+  p.parts = 1;
+  if (!p.listed && jobs > 0 && jobs <= sms / 2 && iters >= 8) {
+    int64_t n = sms / jobs;
+    if (n > iters / 4) n = iters / 4;
+    p.parts = (int32_t)(n > 16 ? 16 : n);
+  }
+  p.stat = align_up(s.rows() * 4, 256);
+  p.bytes = 2 * p.stat;
+  if (p.listed) {
+    p.key_jobs = p.bytes + 256;       // counts before
+    p.query_jobs = p.key_jobs + align_up((size_t)p.key_tiles * sizeof(Job), 256);
+    p.bytes = p.query_jobs + align_up((size_t)p.query_tiles * sizeof(Job), 256);
+  }
+  if (p.parts > 1) {
+    p.part = p.bytes;
+    p.bytes += (size_t)jobs * p.parts * 2 * kRows * s.d * 4;
+  }
+  return p;
+}
 
 int backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
              const void* dout, const int32_t* cu_q, const int32_t* cu_k, float scale, void* dq,
@@ -680,7 +794,9 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
   for (const void* p : v16)
     if (!aligned(p, 16)) return GDN_ERR_ALIGNMENT;
   if (!aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return GDN_ERR_ALIGNMENT;
-  const size_t stat = stat_bytes(tq, s.q_heads), need = 2 * stat;
+  const int sms = sm_count();
+  const Plan plan = plan_of(s, sms > 0 ? sms : 152);
+  const size_t need = tq ? plan.bytes : 0;
   if (use_ws && need) {
     if (!ws || ws_bytes < need) return GDN_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
@@ -702,7 +818,7 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
   BwdArgs a;
   memset(&a, 0, sizeof a);
   a.status = status_ptr();
-  if (!a.status) return GDN_ERR_CUDA;
+  if (!a.status || sms < 1) return GDN_ERR_CUDA;
   const int32_t group = s.q_heads / s.kv_heads;
   a.s = {cu_q, cu_k, s.batch, s.seqlen_q, s.seqlen_k, group, s.kv_heads};
   a.dq = (__nv_bfloat16*)dq;
@@ -720,37 +836,62 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
       !heads_map(&a.k, tk ? k : q, tk, s.kv_heads, s.d, tk ? s.k_stride : width, 1, kRows) ||
       !heads_map(&a.v, tk ? v : q, tk, s.kv_heads, s.d, tk ? s.v_stride : width, 1, kRows))
     return GDN_ERR_CUDA;
-  // packed: upper bounds, sum_n ceil(len_n / per) <= T / per + N
-  const int64_t kt = s.packed ? tk / kRows + s.batch : (s.seqlen_k + kRows - 1) / kRows * s.batch;
-  const int64_t qt = s.packed ? tq / a.per + s.batch : (s.seqlen_q + a.per - 1) / a.per * s.batch;
   const int64_t row_ctas = ((int64_t)s.rows() * (s.d / 8) + 255) / 256;
-  if (kt * s.kv_heads > 0x7fffffffLL || qt * s.kv_heads > 0x7fffffffLL || row_ctas > 0x7fffffffLL)
+  if (plan.key_tiles * s.kv_heads > 0x7fffffffLL || plan.query_tiles * s.kv_heads > 0x7fffffffLL || row_ctas > 0x7fffffffLL)
     return GDN_ERR_UNSUPPORTED;
   void* scratch = ws;
   if (!use_ws && scratch_alloc(&scratch, need, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  a.nlse = (float*)scratch;
-  a.nd = (float*)((char*)scratch + stat);
-  const RowArgs r = {(const __nv_bfloat16*)out, (const __nv_bfloat16*)dout, lse, (float*)scratch,
-                     (float*)((char*)scratch + stat), tq, s.q_heads, group};
-  cudaError_t e = launch(false, s.d == 128 ? rows_kernel<128> : rows_kernel<64>,
-                         dim3((unsigned)row_ctas), 256, 0, 0, st, r);
-  auto run = [&](auto shape, auto kern, int64_t tiles) {
+  char* base = (char*)scratch;
+  a.nlse = (float*)base;
+  a.nd = (float*)(base + plan.stat);
+  a.parts = plan.parts;
+  a.part = (float*)(base + plan.part);
+  cudaError_t e = cudaSuccess;
+  if (plan.listed) {
+    int32_t* head = (int32_t*)(base + plan.key_jobs - 256);
+    auto unit = [](int64_t len, int64_t per) {
+      return (int32_t)(((len + per - 1) / per + kLevels - 1) / kLevels);
+    };
+    const ListArgs keys = {a.s, kRows, unit(s.seqlen_k, kRows) > 0 ? unit(s.seqlen_k, kRows) : 1, true,
+                           head, (uint32_t*)head + 1, (Job*)(base + plan.key_jobs), a.status};
+    const ListArgs queries = {a.s, a.per, unit(s.seqlen_q, a.per), false,
+                              head + 2, (uint32_t*)head + 3, (Job*)(base + plan.query_jobs), a.status};
+    a.count[0] = head;
+    a.count[1] = head + 2;
+    a.jobs[0] = (const Job*)(base + plan.key_jobs);
+    a.jobs[1] = (const Job*)(base + plan.query_jobs);
+    e = launch(true, backward_list_kernel, dim3(2), kListThreads, 0, 0, st, keys, queries);
+    count_launches(1);
+  }
+  const RowArgs r = {(const __nv_bfloat16*)out, (const __nv_bfloat16*)dout, lse, (float*)a.nlse,
+                     (float*)a.nd, tq, s.q_heads, group};
+  if (e == cudaSuccess)
+    e = launch(true, s.d == 128 ? rows_kernel<128> : rows_kernel<64>, dim3((unsigned)row_ctas), 256, 0, 0,
+               st, r);
+  auto run = [&](auto shape, auto kern, int64_t tiles, int parts, std::atomic<uint64_t>& on) {
     using C = decltype(shape);
     if (e != cudaSuccess || tiles == 0) return;
-    e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = allow_smem((const void*)kern, C::kSmem, on);
     if (e == cudaSuccess)
-      e = launch(true, kern, dim3((unsigned)(tiles * s.kv_heads)), kThreads, C::kSmem, 0, st, a);
+      e = launch(true, kern, dim3((unsigned)(tiles * s.kv_heads), (unsigned)parts), kThreads, C::kSmem,
+                 0, st, a);
     count_launches(1);
   };
+  static std::atomic<uint64_t> on[4];
   if (s.d == 128) {
-    run(Bwd<128>{}, keys_kernel<128>, tk ? kt : 0);
-    run(Bwd<128>{}, queries_kernel<128>, qt);
+    run(Bwd<128>{}, keys_kernel<128>, plan.key_tiles, plan.parts, on[0]);
+    run(Bwd<128>{}, queries_kernel<128>, plan.query_tiles, 1, on[1]);
   } else {
-    run(Bwd<64>{}, keys_kernel<64>, tk ? kt : 0);
-    run(Bwd<64>{}, queries_kernel<64>, qt);
+    run(Bwd<64>{}, keys_kernel<64>, plan.key_tiles, plan.parts, on[2]);
+    run(Bwd<64>{}, queries_kernel<64>, plan.query_tiles, 1, on[3]);
+  }
+  if (plan.parts > 1 && e == cudaSuccess) {
+    e = launch(true, s.d == 128 ? keys_sum_kernel<128> : keys_sum_kernel<64>,
+               dim3((unsigned)(plan.key_tiles * s.kv_heads), 4), kThreads, 0, 0, st, a);
+    count_launches(1);
   }
   count_launches(1);
   if (e != cudaSuccess) (void)cudaGetLastError();
@@ -778,13 +919,15 @@ int gdn_attention_prefill_backward(const void* q, const void* k, const void* v, 
 }
 
 size_t gdn_attention_prefill_backward_workspace_size(int32_t batch, int64_t seqlen_q,
-                                                     int32_t varlen, int32_t q_heads,
-                                                     int32_t kv_heads, int32_t d) {
+                                                     int64_t seqlen_k, int32_t varlen,
+                                                     int32_t q_heads, int32_t kv_heads, int32_t d) {
   const int32_t some = 0;
   const int64_t width = (int64_t)q_heads * d;
-  const attn::Shape s = {batch, seqlen_q, 1, q_heads, kv_heads, d, width, width, width, varlen != 0};
+  const attn::Shape s = {batch, seqlen_q, seqlen_k, q_heads, kv_heads, d, width, width, width,
+                         varlen != 0};
   if (attn::check_shape(s, varlen ? &some : nullptr, varlen ? &some : nullptr, 1.f)) return SIZE_MAX;
-  return 2 * stat_bytes(s.tq(), q_heads);
+  const int sms = hostcheck::sm_count();
+  return s.tq() ? plan_of(s, sms > 0 ? sms : 152).bytes : 0;
 }
 
 int gdn_attention_prefill_backward_ws(const void* q, const void* k, const void* v,

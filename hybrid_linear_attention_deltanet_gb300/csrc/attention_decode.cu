@@ -74,8 +74,8 @@ static_assert(sizeof(Small) <= 768, "");
 // What is left of a cut (row, head)'s parts: slot 2c of CTA c if the part
 // continues one, 2c + 1 if it begins one.
 struct Work {
-  int64_t* begin;     // [items] first tile of a cut item, ...
-  int64_t* end;       // ... and behind its last; 0: the item is not cut
+  int2* cut;          // [items] the first CTA that has a part of it, and its parts (0: one CTA
+                      // has all of it)
   float* ml;          // [slots][16][2] maximum (of scores in powers of two), sum
   float* o;           // [slots][16][D]
 };
@@ -85,7 +85,6 @@ struct Args {
   gdn_kv_cache c;
   int32_t layer, q_heads, group, parts, items_per_row, page_log2;
   float scale_log2;
-  int64_t* total;     // tiles in all
   Work w;
   unsigned* status;
 };
@@ -158,6 +157,17 @@ __device__ __forceinline__ uint32_t place(int r, int c) {
   return (uint32_t)(c / kPer * kRows * kSub) + image<kSub>(r, c % kPer);
 }
 
+// The first tile of CTA i of n.
+__device__ __forceinline__ int64_t begin_of(int64_t total, int64_t i, int64_t n) {
+  const uint64_t x = (uint64_t)total * (uint64_t)i;
+  return x >> 32 ? (int64_t)(x / (uint64_t)n) : (int64_t)((uint32_t)x / (uint32_t)n);
+}
+// The CTA of n that has tile t.
+__device__ __forceinline__ int64_t owner_of(int64_t total, int64_t t, int64_t n) {
+  const uint64_t x = (uint64_t)(t + 1) * (uint64_t)n - 1;
+  return x >> 32 ? (int64_t)(x / (uint64_t)total) : (int64_t)((uint32_t)x / (uint32_t)total);
+}
+
 // tokens of a row, 0 where its length is out of range
 __device__ __forceinline__ int32_t row_tokens(const gdn_kv_cache& c, int64_t row, unsigned* status) {
   if (row >= c.rows) return 0;
@@ -180,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
   int64_t* warp_sums = sums + kThreads + 1;
   int64_t* where = warp_sums + kWarps + 1;
+  int32_t* lens = reinterpret_cast<int32_t*>(where + 2);   // a thread's only row, with few rows
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const gdn_kv_cache& c = a.c;
@@ -202,12 +213,20 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     prefetch_tensormap(&a.v);
   }
 
+  grid_wait();
   // the list's length, and where this CTA's part begins
   const int64_t per = ((int64_t)c.rows + kThreads - 1) / kThreads;
   const int64_t r0 = tid * per, r1 = r0 + per < c.rows ? r0 + per : c.rows;
+  const bool few = per == 1;
   int64_t mine = 0;
-  for (int64_t r = r0; r < r1; ++r)
-    mine += (row_tokens(c, r, a.status) + S::kTile - 1) / S::kTile;
+  if (few) {
+    const int32_t n = row_tokens(c, tid, a.status);
+    lens[tid] = n;
+    mine = (n + S::kTile - 1) / S::kTile;
+  } else {
+    for (int64_t r = r0; r < r1; ++r)
+      mine += (row_tokens(c, r, a.status) + S::kTile - 1) / S::kTile;
+  }
   {
     int64_t x = mine;
 #pragma unroll
@@ -223,14 +242,17 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     __syncthreads();
   }
   const int64_t total = sums[kThreads] * HH;
-  if (blockIdx.x == 0 && tid == 0) *a.total = total;
+  // (the table that fits the GPU's memory bounds total below 2^50: 64 bits do)
   const int64_t ctas = total < gridDim.x ? total : gridDim.x;   // none has no tile
   if (blockIdx.x >= ctas) return;
-  const int64_t lo = (int64_t)((unsigned __int128)total * blockIdx.x / ctas);
-  const int64_t hi = (int64_t)((unsigned __int128)total * (blockIdx.x + 1) / ctas);
+  const int64_t lo = begin_of(total, blockIdx.x, ctas), hi = begin_of(total, blockIdx.x + 1, ctas);
   if (lo >= sums[tid] * HH && lo < sums[tid + 1] * HH) {
     int64_t left = lo - sums[tid] * HH;
-    for (int64_t r = r0; r < r1; ++r) {
+    if (few) {
+      where[0] = tid;
+      where[1] = left;
+    }
+    for (int64_t r = few ? r1 : r0; r < r1; ++r) {
       const int64_t n = (int64_t)((row_tokens(c, r, nullptr) + S::kTile - 1) / S::kTile) * HH;
       if (left < n) {
         where[0] = r;
@@ -242,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   }
   __syncthreads();
   const int64_t row0 = where[0], in_row = where[1];
+  const int32_t len0 = few ? lens[row0] : row_tokens(c, row0, nullptr);
+  const int32_t len1 = few && row0 + 1 < kThreads ? lens[row0 + 1] : row_tokens(c, row0 + 1, nullptr);
   fence_proxy_async_smem();
   __syncthreads();
   bool ok = true;
@@ -254,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     constexpr int kIds = S::kTile / 16;                      // copies of a tile at most
     Tile t;
     t.row = (int32_t)row0;
-    t.len = row_tokens(c, t.row, nullptr);
-    int32_t next_len = row_tokens(c, t.row + 1, nullptr);
+    t.len = len0;
+    int32_t next_len = len1;
     t.n = (t.len + S::kTile - 1) / S::kTile;
     t.hh = (int32_t)(in_row / t.n);
     t.at = (int32_t)(in_row - (int64_t)t.hh * t.n);
@@ -617,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       const int64_t item = (int64_t)tile.row * HH + tile.hh;
       const int64_t slot = 2 * (int64_t)blockIdx.x + from_begin;
       if (tid == 0 && from_begin) {
-        a.w.begin[item] = item_begin;
-        a.w.end[item] = whole ? 0 : item_begin + tile.n;
+        a.w.cut[item] = make_int2(
+            blockIdx.x, whole ? 0 : (int)(owner_of(total, item_begin + tile.n - 1, ctas) - blockIdx.x + 1));
       }
       const int heads = a.group - part * kHeads < kHeads ? a.group - part * kHeads : kHeads;
 #pragma unroll
@@ -679,33 +703,40 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ float sm[kN][D + 2], weight[kCtas], sum[kCtas];
   const gdn_kv_cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_release_next();
   grid_wait();
-  int64_t total;
-  asm volatile("ld.global.s64 %0, [%1];" : "=l"(total) : "l"(a.total));
-  const int64_t ctas = total < kCtas ? total : kCtas;
   const int64_t jobs = (int64_t)c.rows * a.q_heads;
   for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
     const int64_t row = job / a.q_heads;
     const int head = (int)(job - row * a.q_heads);
     const int h = head / a.group, in = head - h * a.group, part = in / kHeads, r = in % kHeads;
     __nv_bfloat16* out = a.out + job * D;
+    const int32_t* cut = reinterpret_cast<const int32_t*>(a.w.cut + row * a.items_per_row + h * a.parts + part);
+    const int32_t first = ld_waited(cut), parts = ld_waited(cut + 1);   // (unset for empty rows)
     if (row_tokens(c, row, nullptr) == 0) {
       for (int i = threadIdx.x; i < D; i += kJoinThreads) out[i] = __float2bfloat16_rn(0.f);
       continue;
     }
-    const int64_t item = row * a.items_per_row + h * a.parts + part;
-    int64_t b, e;
-    asm volatile("ld.global.s64 %0, [%1];" : "=l"(b) : "l"(a.w.begin + item));
-    asm volatile("ld.global.s64 %0, [%1];" : "=l"(e) : "l"(a.w.end + item));
-    if (e == 0) continue;
-    // the CTA that has tile t: part c of n begins at floor(c total / n)
-    auto owner = [&](int64_t t) {
-      return (int64_t)(((unsigned __int128)(t + 1) * ctas - 1) / total);
+    if (parts == 0) continue;
+    auto slot = [&](int p) { return (int64_t)((2 * (first + p) + (p == 0)) * kHeads + r); };
+    // the parts' maxima and sums, then every part's factor; a warp's first four
+    // parts are on their way by then
+    float x[4][kV];
+    auto read = [&](int p) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* src = a.w.o + slot(p + i * kN) * D + lane * kV;
+        if (p + i * kN >= parts) continue;
+        if constexpr (kV == 4) {
+          const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
+          x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+        } else {
+          x[i][0] = ld_waited(src);
+          x[i][1] = ld_waited(src + 1);
+        }
+      }
     };
-    const int64_t first = owner(b);
-    const int parts = (int)(owner(e - 1) - first + 1);      // up to the CTAs
-    auto slot = [&](int p) { return ((2 * (first + p) + (p == 0)) * kHeads + r); };
-    // the parts' maxima and sums, then every part's factor
+    read(warp);
     float m = -INFINITY;
     for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
       const float mp = ld_waited(a.w.ml + slot(p) * 2);
@@ -735,19 +766,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     // a warp adds every eighth part, four in flight
     float o[kV] = {};
     for (int p = warp; p < parts; p += 4 * kN) {
-      float x[4][kV];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool on = p + i * kN < parts;
-        const float* src = a.w.o + slot(on ? p + i * kN : p) * D + lane * kV;
-        if constexpr (kV == 4) {
-          const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
-          x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
-        } else {
-          x[i][0] = ld_waited(src);
-          x[i][1] = ld_waited(src + 1);
-        }
-      }
+      if (p != warp) read(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (p + i * kN < parts) {
@@ -773,15 +792,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 struct Layout {
-  size_t begin, end, ml, o, bytes;
+  size_t cut, ml, o, bytes;
 };
 Layout layout_of(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t d) {
   const int32_t group = q_heads / kv_heads, parts = (group + kHeads - 1) / kHeads;
   const size_t items = (size_t)rows * kv_heads * parts, slots = 2 * (size_t)kCtas;
   Layout l;
-  l.begin = 256;
-  l.end = l.begin + align_up(items * 8, 256);
-  l.ml = l.end + align_up(items * 8, 256);
+  l.cut = 0;
+  l.ml = align_up(items * sizeof(int2), 256);
   l.o = l.ml + slots * kHeads * 2 * 4;
   l.bytes = l.o + slots * kHeads * d * 4;
   return l;
@@ -856,9 +874,7 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
     return GDN_ERR_CUDA;
   }
   char* p = (char*)scratch;
-  a.total = (int64_t*)p;
-  a.w.begin = (int64_t*)(p + lay.begin);
-  a.w.end = (int64_t*)(p + lay.end);
+  a.w.cut = (int2*)(p + lay.cut);
   a.w.ml = (float*)(p + lay.ml);
   a.w.o = (float*)(p + lay.o);
   cudaError_t e;
@@ -866,7 +882,7 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
   auto run = [&](auto shape, auto kern, std::atomic<uint64_t>& allowed) {
     using S = decltype(shape);
     e = allow_smem((const void*)kern, S::kSmem, allowed);
-    if (e == cudaSuccess) e = launch(false, kern, dim3(kCtas), kThreads, S::kSmem, 0, st, a);
+    if (e == cudaSuccess) e = launch(true, kern, dim3(kCtas), kThreads, S::kSmem, 0, st, a);
   };
   if (c.d == 128)
     fp8 ? run(Shape<128, true>{}, decode_kernel<128, true>, on[0])

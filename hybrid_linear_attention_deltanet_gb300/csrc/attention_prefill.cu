@@ -112,16 +112,6 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const Seqs& sq = a.s;
-  grid_release_next();
-  if constexpr (kMode != kListed) {
-    Seq seq;
-    if (!locate<kThreads>(sq, blockIdx.x / sq.kv_heads, 2 * a.per, false, true, scratch, a.status, seq))
-      return;
-    if (tid == 0) {
-      slots[0] = seq;
-      slot_head[0] = blockIdx.x % sq.kv_heads;
-    }
-  }
   if (tid == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
@@ -145,11 +135,25 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     prefetch_tensormap(&a.k);
     prefetch_tensormap(&a.v);
   }
+  grid_wait();
+  grid_release_next();   // (the join reads the sequences before it waits)
+  bool here = true;
+  if constexpr (kMode != kListed) {
+    Seq seq;
+    here = locate<kThreads>(sq, blockIdx.x / sq.kv_heads, 2 * a.per, false, true, scratch, a.status, seq);
+    if (here && tid == 0) {
+      slots[0] = seq;
+      slot_head[0] = blockIdx.x % sq.kv_heads;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (kMode == kListed) grid_wait();
   const uint32_t tmem = tmem_base;
+  if (!here) {
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    return;
+  }
   const int part = kMode == kParts ? blockIdx.y : 0, parts = kMode == kParts ? a.parts : 1;
   bool ok = true;
 
@@ -485,6 +489,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
 
 __global__ void __launch_bounds__(kListThreads) prefill_list_kernel(ListArgs a) {
   grid_release_next();
+  grid_wait();
   list_jobs(a);
 }
 
@@ -498,6 +503,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
   __shared__ int64_t scratch[kJoinThreads + 6];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int head = blockIdx.x % a.s.kv_heads;
+  grid_release_next();
+  // (the sequences are inputs: the kernel before this one has waited for them)
   Seq seq;
   if (!locate<kJoinThreads>(a.s, blockIdx.x / a.s.kv_heads, 2 * a.per, false, true, scratch, nullptr, seq))
     return;
@@ -638,7 +645,7 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
     const int64_t longest = (s.seqlen_q + per - 1) / per;
     const ListArgs list = {a.s, (int32_t)per, (int32_t)((longest + kLevels - 1) / kLevels), false,
                            (int32_t*)scratch, a.next, (Job*)((char*)scratch + at_jobs), a.status};
-    e = launch(false, prefill_list_kernel, dim3(1), kListThreads, 0, 0, st, list);
+    e = launch(true, prefill_list_kernel, dim3(1), kListThreads, 0, 0, st, list);
     count_launches(1);
     grid = dim3((unsigned)sms);
   } else if (mode == kParts) {
@@ -649,7 +656,7 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   auto run = [&](auto shape, auto kern, std::atomic<uint64_t>& on) {
     using C = decltype(shape);
     if (e == cudaSuccess) e = allow_smem((const void*)kern, C::kSmem, on);
-    if (e == cudaSuccess) e = launch(mode == kListed, kern, grid, kThreads, C::kSmem, 0, st, a);
+    if (e == cudaSuccess) e = launch(true, kern, grid, kThreads, C::kSmem, 0, st, a);
   };
   static std::atomic<uint64_t> on[6];
   if (s.d == 128) {

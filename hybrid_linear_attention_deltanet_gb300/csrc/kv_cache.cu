@@ -6,7 +6,11 @@
 // captured.  Everything about them is decided by one CTA, which takes pages in
 // the order of their numbers: a scan of the reference counts, 4096 a step (a
 // step is one load, two warp scans and two barriers, about 1 us), that ends as
-// soon as it has found enough.  Copies are split over the GPU, 64 KB a CTA, 16
+// soon as it has found enough.  The kernels are short and come in chains (free,
+// reserve; free, fork), so they are programmatic dependents: each waits for the
+// one before it first, but is on the GPU by then.  (append_kernel is not: a
+// decoding step's is over before the attribute has cost the host its 1.5 us.)
+// Copies are split over the GPU, 64 KB a CTA, 16
 // bytes a lane; they are bound by HBM.
 #include "fp8_codes.cuh"
 #include "gdn_internal.cuh"
@@ -89,6 +93,8 @@ reserve_kernel(gdn_kv_cache c, const int32_t* counts, int32_t* start, int32_t* l
                unsigned* status) {
   __shared__ ScanMem sm;
   const int lane = threadIdx.x & 31;
+  grid_release_next();
+  grid_wait();
   // pages a row holds and will hold; what is asked of it in bad: 1 out of range, 2 no room
   auto ask = [&](int row, int64_t& old, int64_t& now, int64_t& len) {
     if (row >= c.rows) {
@@ -168,6 +174,7 @@ template <int D, bool kFp8, int kUnits>
 __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8;
   constexpr int kSpan = kCopy / kLanes;   // heads of tokens that the CTA holds at a time
+  grid_release_next();
   const gdn_kv_cache& c = a.c;
   const int64_t units = a.tokens * c.kv_heads;
   const int64_t unit0 = (int64_t)blockIdx.x * kSpan * kUnits + threadIdx.x / kLanes;
@@ -256,6 +263,8 @@ __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
 __global__ void __launch_bounds__(128)
 free_kernel(gdn_kv_cache c, const int32_t* rows, unsigned* status) {
   __shared__ int32_t len;
+  grid_release_next();
+  grid_wait();
   const int32_t r = rows[blockIdx.x];
   if (r < 0 || r >= c.rows) {
     if (threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_CACHE);
@@ -310,6 +319,7 @@ fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t
                  int32_t* list, unsigned* status) {
   __shared__ ScanMem sm;
   grid_release_next();
+  grid_wait();
   for (int i = threadIdx.x; i < n; i += kPlan) {
     const int32_t s = src[i], d = dst[i];
     const bool in = s >= 0 && s < c.rows && d >= 0 && d < c.rows;
@@ -373,6 +383,7 @@ template <bool kFp8>
 __global__ void __launch_bounds__(kCopy)
 fork_copy_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, const Pair* plan,
                  unsigned* status) {
+  grid_release_next();
   grid_wait();
   const int i = blockIdx.x;
   const int32_t len = ld_waited(&plan[i].len), fresh = ld_waited(&plan[i].page);
@@ -427,6 +438,7 @@ compact_plan_kernel(gdn_kv_cache c, gdn_kv_cache into, int32_t* count, int32_t* 
                     int32_t* number, unsigned* status) {
   __shared__ ScanMem sm;
   grid_release_next();
+  grid_wait();
   int64_t live = 0, step;
   for (int64_t base = 0; base < c.pages; base += 4 * kPlan) {
     const int64_t p = base + 4 * (int64_t)threadIdx.x;
@@ -463,6 +475,7 @@ template <bool kFp8>
 __global__ void __launch_bounds__(kCopy)
 compact_copy_kernel(gdn_kv_cache c, gdn_kv_cache into, const int32_t* count, const int32_t* order,
                     const int32_t* number, int64_t jobs, unsigned* status) {
+  grid_release_next();
   grid_wait();
   const int32_t live = ld_waited(count);
   if (live < 0) return;
@@ -537,7 +550,7 @@ int gdn_cache_reserve(const gdn_kv_cache* cache, const int32_t* counts, int32_t*
   const int64_t most = least(c.pages, (int64_t)c.rows * c.max_pages);
   if (!status || scratch_alloc(&list, (size_t)most * 4, st) != cudaSuccess) return GDN_ERR_CUDA;
   count_launches(1);
-  return finish(launch(false, reserve_kernel, dim3(1), kPlan, 0, 0, st, c, counts, start,
+  return finish(launch(true, reserve_kernel, dim3(1), kPlan, 0, 0, st, c, counts, start,
                        (int32_t*)list, status),
                 list, st);
 }
@@ -595,7 +608,7 @@ int gdn_cache_free(const gdn_kv_cache* cache, const int32_t* rows, int32_t n,
   unsigned* status = status_ptr();
   if (!status) return GDN_ERR_CUDA;
   count_launches(1);
-  return launch(false, free_kernel, dim3((unsigned)n), 128, 0, 0, (cudaStream_t)stream, *cache,
+  return launch(true, free_kernel, dim3((unsigned)n), 128, 0, 0, (cudaStream_t)stream, *cache,
                 rows, status) == cudaSuccess
              ? GDN_OK
              : GDN_ERR_CUDA;
@@ -620,7 +633,7 @@ int gdn_cache_fork(const gdn_kv_cache* cache, const int32_t* src, const int32_t*
   if (!status || scratch_alloc(&scratch, plan_bytes + (size_t)n * 4, st) != cudaSuccess)
     return GDN_ERR_CUDA;
   Pair* plan = (Pair*)scratch;
-  cudaError_t e = launch(false, fork_plan_kernel, dim3(1), kPlan, 0, 0, st, c, src, dst, n, plan,
+  cudaError_t e = launch(true, fork_plan_kernel, dim3(1), kPlan, 0, 0, st, c, src, dst, n, plan,
                          (int32_t*)((char*)scratch + plan_bytes), status);
   if (e == cudaSuccess)
     e = launch(true, c.dtype == GDN_E4M3 ? fork_copy_kernel<true> : fork_copy_kernel<false>,
@@ -649,7 +662,7 @@ int gdn_cache_compact(const gdn_kv_cache* cache, const gdn_kv_cache* into, gdn_s
   int32_t* count = (int32_t*)scratch;
   int32_t* order = (int32_t*)((char*)scratch + 256);
   int32_t* number = (int32_t*)((char*)order + order_bytes);
-  cudaError_t e = launch(false, compact_plan_kernel, dim3(1), kPlan, 0, 0, st, c, d, count, order,
+  cudaError_t e = launch(true, compact_plan_kernel, dim3(1), kPlan, 0, 0, st, c, d, count, order,
                          number, status);
   const int64_t jobs = 2 * (int64_t)c.layers * least(c.pages, d.pages);
   if (e == cudaSuccess)

@@ -652,7 +652,8 @@ int gdn_attention_prefill(const void* q, const void* k, const void* v, const int
  * contiguous; q, k, v with strides as above; the rest as above.  P and dS
  * enter the products rounded to bf16, all sums are fp32 and their order is
  * fixed.  No output may overlap an input or another output.  Scratch (8 bytes
- * a token and query head) from the library's pool, or a caller's 256-byte
+ * a token and query head; 32 bytes a tile for long calls, up to 40 MB of
+ * partial sums for short ones) from the library's pool, or a caller's 256-byte
  * aligned workspace of at least gdn_attention_prefill_backward_workspace_size
  * bytes (rules as gdn_prefill_ws).
  */
@@ -663,8 +664,8 @@ int gdn_attention_prefill_backward(const void* q, const void* k, const void* v, 
                                    int32_t q_heads, int32_t kv_heads, int32_t d, int64_t q_stride,
                                    int64_t k_stride, int64_t v_stride, gdn_stream_t stream);
 size_t gdn_attention_prefill_backward_workspace_size(int32_t batch, int64_t seqlen_q,
-                                                     int32_t varlen, int32_t q_heads,
-                                                     int32_t kv_heads, int32_t d);
+                                                     int64_t seqlen_k, int32_t varlen,
+                                                     int32_t q_heads, int32_t kv_heads, int32_t d);
 int gdn_attention_prefill_backward_ws(const void* q, const void* k, const void* v,
                                       const void* out, const float* lse, const void* dout,
                                       const int32_t* cu_q, const int32_t* cu_k, float scale,

@@ -114,7 +114,8 @@ def test_dense_batches(gdn_lib, B, tq, tk, d):
     out, lse, dout = (t.flatten(0, 1) for t in (out, lse, dout))
     verify(q, k, v, out, lse, dout, flat, [tq] * B, [tk] * B)
     packed = gdn.attention_prefill_backward(q, k, v, out, lse, dout, cu([tq] * B), cu([tk] * B))
-    assert all(torch.equal(flat[n], packed[n]) for n in flat)
+    # (packed, a key's queries may be cut into other parts)
+    verify(q, k, v, out, lse, dout, packed, [tq] * B, [tk] * B)
 
 
 @pytest.mark.parametrize("d", [64, 128])
