@@ -37,9 +37,10 @@ struct BwdArgs {
   // the order of the jobs, longest first (nullptr: that of the sequences)
   const int32_t* count[2];     // [tiles of keys, of queries]
   const Job* jobs[2];
-  // parts of a key tile's queries, and their sums of dV and dK, [jobs][parts][2][128][D]
-  int32_t parts;
-  float* part;
+  // parts of a key tile's queries, and their sums of dV and dK, [jobs][parts][2][128][D];
+  // parts of a query tile's keys, and their sums of dQ, [jobs][parts][128][D]
+  int32_t parts, q_parts;
+  float *part, *q_part;
   unsigned* status;
 };
 
@@ -120,9 +121,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
     for (int i = from * 8 + lane; i < kRows * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
   }
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 // This lane's row of an accumulator's columns as bf16 (times f) to memory.
 template <int kCols>
 __device__ __forceinline__ void store_row(uint32_t at, float f, __nv_bfloat16* to, bool live, bool zero) {
@@ -142,6 +140,25 @@ __device__ __forceinline__ void store_row(uint32_t at, float f, __nv_bfloat16* t
                     : pack(__uint_as_float(o[8 * x + 2 * z]) * f, __uint_as_float(o[8 * x + 2 * z + 1]) * f);
       if (live) *reinterpret_cast<uint4*>(to + 32 * i + 8 * x) = make_uint4(y[0], y[1], y[2], y[3]);
     }
+  }
+}
+
+// The same row as it is, a part's sum: four columns of all rows together, then the
+// next four, so that a warp's store is contiguous (rows one after another took a
+// CTA 5 us).
+template <int kCols>
+__device__ __forceinline__ void store_part(uint32_t at, float* to, int row, bool zero) {
+#pragma unroll
+  for (int i = 0; i < kCols / 32; ++i) {
+    uint32_t o[32];
+    if (!zero) {
+      tmem_ld32(at + 32 * i, o);
+      tmem_ld_wait_regs(o);
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      *reinterpret_cast<uint4*>(to + ((8 * i + x) * kRows + row) * 4) =
+          zero ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
   }
 }
 
@@ -184,10 +201,24 @@ __device__ __forceinline__ float ld_stat(const float* p) {
   return v;
 }
 
+// This CTA's job, from the list or the sequences; sm as locate() wants it.
+template <int kN>
+__device__ __forceinline__ bool find_job(const BwdArgs& a, bool keys, int64_t* sm, unsigned* status,
+                                         Seq& seq, int& head) {
+  head = blockIdx.x % a.s.kv_heads;
+  const int64_t job = blockIdx.x / a.s.kv_heads;
+  const Job* list = a.jobs[keys ? 0 : 1];
+  if (!list) return locate<kN>(a.s, job, keys ? kRows : a.per, keys, !keys, sm, status, seq);
+  if (job >= (int64_t)ld_relaxed_gpu((const uint32_t*)a.count[keys ? 0 : 1])) return false;
+  const uint32_t* x = reinterpret_cast<const uint32_t*>(list + job);
+  seq = {(int32_t)ld_relaxed_gpu(x), (int32_t)ld_relaxed_gpu(x + 1), (int32_t)ld_relaxed_gpu(x + 2),
+         (int32_t)ld_relaxed_gpu(x + 3), (int32_t)ld_relaxed_gpu(x + 4)};
+  return true;
+}
+
 // The common part of both kernels: the job's place, barriers, tensor memory.
 template <int D>
-__device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, int per, bool keys, Seq& seq,
-                                      int& head) {
+__device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, bool keys, Seq& seq, int& head) {
   using C = Bwd<D>;
   Bars& b = *reinterpret_cast<Bars*>(sm + C::kBars);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -197,18 +228,7 @@ __device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, int per, bo
     if (tid == 0) flag_status(a.status, GDN_ERR_UNSUPPORTED);
     return false;
   }
-  head = blockIdx.x % a.s.kv_heads;
-  const int64_t job = blockIdx.x / a.s.kv_heads;
-  const Job* list = a.jobs[keys ? 0 : 1];
-  if (list) {
-    if (job >= (int64_t)ld_relaxed_gpu((const uint32_t*)a.count[keys ? 0 : 1])) return false;
-    const uint32_t* x = reinterpret_cast<const uint32_t*>(list + job);
-    seq = {(int32_t)ld_relaxed_gpu(x), (int32_t)ld_relaxed_gpu(x + 1), (int32_t)ld_relaxed_gpu(x + 2),
-           (int32_t)ld_relaxed_gpu(x + 3), (int32_t)ld_relaxed_gpu(x + 4)};
-  } else if (!locate<kThreads>(a.s, job, per, keys, !keys, reinterpret_cast<int64_t*>(sm), a.status,
-                               seq)) {
-    return false;
-  }
+  if (!find_job<kThreads>(a, keys, reinterpret_cast<int64_t*>(sm), a.status, seq, head)) return false;
   if (tid == 0) {
     mbar_init(&b.own, 1);
     for (int i = 0; i < 3; ++i) {
@@ -265,7 +285,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
   int head;
   grid_wait();
   grid_release_next();   // the queries' kernel starts where SMs are left: it needs nothing of this one
-  if (!begin<D>(a, sm, kRows, true, seq, head)) return;
+  if (!begin<D>(a, sm, true, seq, head)) return;
   const int32_t group = a.s.group, shift = seq.lk - seq.lq;
   const int32_t k0 = seq.tile * kRows;                       // the tile's first key
   const int32_t used = a.per * group;                        // rows of a tile of queries
@@ -498,21 +518,8 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
         const int64_t to = ((seq.k0 + k0 + row) * a.s.kv_heads + head) * D;
         store_row<D>(from, w ? a.scale : 1.f, (w ? a.dk : a.dv) + to, live, n == 0);
       } else {
-        float* to = a.part + ((((int64_t)blockIdx.x * a.parts + blockIdx.y) * 2 + w) * kRows + row) * D;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld32(from + 32 * i, o);
-            tmem_ld_wait_regs(o);
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (live)
-              *reinterpret_cast<uint4*>(to + 32 * i + 4 * x) =
-                  n > 0 ? make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3])
-                        : make_uint4(0, 0, 0, 0);
-        }
+        float* to = a.part + (((int64_t)blockIdx.x * a.parts + blockIdx.y) * 2 + w) * kRows * D;
+        store_part<D>(from, to, row, n == 0);
       }
     }
   }
@@ -531,13 +538,16 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   Seq seq;
   int head;
-  if (!begin<D>(a, sm, a.per, false, seq, head)) return;
+  if (!begin<D>(a, sm, false, seq, head)) return;
   const int32_t group = a.s.group, shift = seq.lk - seq.lq;
   const int32_t used = a.per * group;
   const int32_t first = seq.tile * a.per;                    // the tile's first query
   const int32_t rows = seq.lq - first < a.per ? seq.lq - first : a.per;
   const int32_t seen = first + rows + shift;                 // keys that the last row sees
-  const int32_t n = seen > 0 ? (seen + kRows - 1) / kRows : 0;
+  const int32_t all = seen > 0 ? (seen + kRows - 1) / kRows : 0;
+  // this CTA's part of their blocks
+  const int32_t j0 = (int32_t)((int64_t)all * blockIdx.y / a.q_parts);
+  const int32_t n = (int32_t)((int64_t)all * (blockIdx.y + 1) / a.q_parts) - j0;
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -561,7 +571,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
         }
       }
       for (int32_t j = 0; ok && j < n; ++j) {
-        const int32_t t = (int32_t)(seq.k0 + (int64_t)j * kRows);
+        const int32_t t = (int32_t)(seq.k0 + (int64_t)(j0 + j) * kRows);
         const int sa = j % C::kNA, sb = j % C::kNB;
         ok = mbar_wait_warp(&b.a_empty[sa], (uint32_t)((j / C::kNA) & 1) ^ 1u, kWaitNs);
         if (ok && lead) {
@@ -596,7 +606,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
         if (!ok) return;
         // keys behind the sequence's last are another's: their rows become
         // zeros, so that the products with dS = 0 are
-        const int64_t valid = seq.lk - (int64_t)j * kRows;
+        const int64_t valid = seq.lk - (int64_t)(j0 + j) * kRows;
         if (valid < kRows) {
           zero_rows<D>(sm + C::kA + sa * C::kTile, (int)valid, lane);
           fence_proxy_async_smem();
@@ -663,7 +673,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
     const F2 cc = f2(a.c, a.c), ll = f2(nl, nl), dd = f2(nd, nd);
     for (int32_t j = 0; j < n; ++j) {
       const uint32_t s_at = tmem + lanes + kS + 128 * (j & 1) + 64 * w, dp_at = tmem + lanes + kDP + 64 * w;
-      const int32_t k0 = j * kRows;
+      const int32_t k0 = (j0 + j) * kRows;
       const bool masked = k0 + kRows - 1 > first + shift;
       const int32_t see = last - k0 - 64 * w;
       ok = mbar_wait_warp(&b.s_full[j & 1], (uint32_t)((j >> 1) & 1), kWaitNs);
@@ -704,7 +714,14 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
     if (ok) {
       // half the columns each
       const int64_t r = (seq.q0 + first + qi) * a.q_heads + (int64_t)head * group + row % group;
-      store_row<D / 2>(tmem + lanes + kDQ + D / 2 * w, a.scale, a.dq + r * D + D / 2 * w, live, n == 0);
+      const uint32_t from = tmem + lanes + kDQ + D / 2 * w;
+      if (a.q_parts == 1)
+        store_row<D / 2>(from, a.scale, a.dq + r * D + D / 2 * w, live, n == 0);
+      else
+        store_part<D / 2>(from,
+                          a.q_part + ((int64_t)blockIdx.x * a.q_parts + blockIdx.y) * kRows * D +
+                              D / 2 * w * kRows,
+                          row, n == 0);
     }
   }
   finish(ok, tmem, a.status);
@@ -717,30 +734,40 @@ __global__ void __launch_bounds__(kListThreads) backward_list_kernel(ListArgs ke
   list_jobs(blockIdx.x ? queries : keys);
 }
 
-// The parts of a key tile's dV and dK, added in their order: 4 columns a thread.
-template <int D>
-__global__ void __launch_bounds__(kThreads) keys_sum_kernel(const __grid_constant__ BwdArgs a) {
+// The parts of a tile's dV and dK, or dQ, added in their order: 8 columns of a row a
+// thread.
+template <int D, bool kKeys>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ int64_t scratch[kThreads + 6];
   Seq seq;
-  const int head = blockIdx.x % a.s.kv_heads;
+  int head;
   grid_wait();
   grid_release_next();
-  if (!locate<kThreads>(a.s, blockIdx.x / a.s.kv_heads, kRows, true, false, scratch, nullptr, seq)) return;
-  const int64_t k0 = (int64_t)seq.tile * kRows;
-  constexpr int kVecs = kRows * D / 4;
-  for (int i = blockIdx.y * kThreads + threadIdx.x; i < 2 * kVecs; i += gridDim.y * kThreads) {
-    const int w = i / kVecs, row = i % kVecs / (D / 4), col = i % (D / 4) * 4;
-    if (k0 + row >= seq.lk) continue;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* from = a.part + (((int64_t)blockIdx.x * a.parts * 2 + w) * kRows + row) * D + col;
+  if (!find_job<kThreads>(a, kKeys, scratch, nullptr, seq, head)) return;
+  constexpr int kVecs = kRows * D / 8, kTensors = kKeys ? 2 : 1;
+  const int group = a.s.group;
+  const int64_t first = (int64_t)seq.tile * (kKeys ? kRows : a.per);
+  const float* part = kKeys ? a.part : a.q_part;
+  const int parts = kKeys ? a.parts : a.q_parts;
+  for (int i = blockIdx.y * kThreads + threadIdx.x; i < kTensors * kVecs; i += gridDim.y * kThreads) {
+    const int row = i % kRows, col = i / kRows % (D / 8) * 8, w = i / kVecs;
+    const int64_t t = first + (kKeys ? row : row / group);
+    if (t >= (kKeys ? seq.lk : seq.lq) || (!kKeys && row >= a.per * group)) continue;
+    const float* from = part + (((int64_t)blockIdx.x * parts * kTensors + w) * D + col) * kRows + row * 4;
+    float sum[8] = {};
 #pragma unroll 4
-    for (int p = 0; p < a.parts; ++p) {
-      const float4 x = ld_waited(reinterpret_cast<const float4*>(from + (int64_t)p * 2 * kRows * D));
-      sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
-    }
-    const float f = w ? a.scale : 1.f;
-    *reinterpret_cast<uint2*>((w ? a.dk : a.dv) + ((seq.k0 + k0 + row) * a.s.kv_heads + head) * D + col) =
-        make_uint2(pack(sum.x * f, sum.y * f), pack(sum.z * f, sum.w * f));
+    for (int p = 0; p < parts; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = ld_waited(reinterpret_cast<const float4*>(
+            from + (int64_t)p * kTensors * kRows * D + h * 4 * kRows));
+        sum[4 * h] += x.x; sum[4 * h + 1] += x.y; sum[4 * h + 2] += x.z; sum[4 * h + 3] += x.w;
+      }
+    const float f = kKeys && w == 0 ? 1.f : a.scale;
+    __nv_bfloat16* to = kKeys ? (w ? a.dk : a.dv) + ((seq.k0 + t) * a.s.kv_heads + head) * D + col
+                              : a.dq + ((seq.q0 + t) * a.q_heads + (int64_t)head * group + row % group) * D + col;
+    *reinterpret_cast<uint4*>(to) = make_uint4(pack(sum[0] * f, sum[1] * f), pack(sum[2] * f, sum[3] * f),
+                                               pack(sum[4] * f, sum[5] * f), pack(sum[6] * f, sum[7] * f));
   }
 }
 
@@ -748,26 +775,43 @@ __global__ void __launch_bounds__(kThreads) keys_sum_kernel(const __grid_constan
 struct Plan {
   int64_t key_tiles, query_tiles;   // packed: upper bounds, sum_n ceil(len_n / per) <= T / per + N
   bool listed;
-  int32_t parts;
-  size_t stat, key_jobs, query_jobs, part, bytes;   // statistics, then where the others lie
+  int32_t parts, q_parts;
+  size_t stat, key_jobs, query_jobs, part, q_part, bytes;   // statistics, then where the others lie
 };
+// Parts of a loop of `iters` steps (about 1.2 us each) for `jobs` of them: as many
+// as minimise the longest's time and that of the parts' sums, of `bytes` each, out
+// and in again (at about 4 TB/s), where that is not less than what the SMs have to do
+// meanwhile anyway.
+int32_t parts_of(int64_t jobs, int64_t iters, int least, int sms, int64_t bytes) {
+  if (jobs == 0 || iters < 2 * least) return 1;
+  const float sums = (float)jobs * (float)bytes * 2.f / 4e6f, loop = (float)iters * 1.2f;
+  const float share = (float)jobs * (float)iters * 0.9f / (float)sms;   // of both kernels, us
+  int32_t best = 1;
+  float least_time = fmaxf(loop, share);
+  for (int32_t p = 2; p <= 16 && p * least <= iters; ++p) {
+    const float t = fmaxf(loop / (float)p, share) + (float)p * sums + 4.f;
+    if (t < least_time) {
+      least_time = t;
+      best = p;
+    }
+  }
+  return best;
+}
 Plan plan_of(const Shape& s, int sms) {
   const int32_t per = kRows / (s.q_heads / s.kv_heads);
   Plan p = {};
-  const int64_t tq = s.tq(), tk = s.tk(), iters = (s.seqlen_q + per - 1) / per;
-  p.key_tiles = s.packed ? tk / kRows + s.batch : (s.seqlen_k + kRows - 1) / kRows * s.batch;
+  const int64_t tq = s.tq(), tk = s.tk(), iters = (s.seqlen_q + per - 1) / per,
+                blocks = (s.seqlen_k + kRows - 1) / kRows;
+  p.key_tiles = s.packed ? tk / kRows + s.batch : blocks * s.batch;
   p.query_tiles = s.packed ? tq / per + s.batch : iters * s.batch;
   if (tk == 0) p.key_tiles = 0;
-  const int64_t jobs = p.key_tiles * s.kv_heads;
-  // a list where either kernel has more than two turns of jobs; where the keys'
-  // jobs leave SMs empty and are long, a part of their queries each
-  p.listed = jobs > 2 * sms || p.query_tiles * s.kv_heads > 2 * sms;
-  p.parts = 1;
-  if (!p.listed && jobs > 0 && jobs <= sms / 2 && iters >= 8) {
-    int64_t n = sms / jobs;
-    if (n > iters / 4) n = iters / 4;
-    p.parts = (int32_t)(n > 16 ? 16 : n);
-  }
+  const int64_t key_jobs = p.key_tiles * s.kv_heads, query_jobs = p.query_tiles * s.kv_heads;
+  p.listed = key_jobs > 2 * sms || query_jobs > 2 * sms;
+  const int64_t tile = (int64_t)kRows * s.d * 4;
+  // (packed: no sequence is taken to be longer than four average ones)
+  const int64_t few = s.packed && s.batch > 4 ? s.batch : 4;
+  p.parts = parts_of(key_jobs, s.packed ? iters * 4 / few : iters, 6, sms, 2 * tile);
+  p.q_parts = parts_of(query_jobs, s.packed ? blocks * 4 / few : blocks, 6, sms, tile);
   p.stat = align_up(s.rows() * 4, 256);
   p.bytes = 2 * p.stat;
   if (p.listed) {
@@ -775,10 +819,10 @@ Plan plan_of(const Shape& s, int sms) {
     p.query_jobs = p.key_jobs + align_up((size_t)p.key_tiles * sizeof(Job), 256);
     p.bytes = p.query_jobs + align_up((size_t)p.query_tiles * sizeof(Job), 256);
   }
-  if (p.parts > 1) {
-    p.part = p.bytes;
-    p.bytes += (size_t)jobs * p.parts * 2 * kRows * s.d * 4;
-  }
+  p.part = p.bytes;
+  if (p.parts > 1) p.bytes += (size_t)key_jobs * p.parts * 2 * tile;
+  p.q_part = p.bytes;
+  if (p.q_parts > 1) p.bytes += (size_t)query_jobs * p.q_parts * tile;
   return p;
 }
 
@@ -848,7 +892,9 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
   a.nlse = (float*)base;
   a.nd = (float*)(base + plan.stat);
   a.parts = plan.parts;
+  a.q_parts = plan.q_parts;
   a.part = (float*)(base + plan.part);
+  a.q_part = (float*)(base + plan.q_part);
   cudaError_t e = cudaSuccess;
   if (plan.listed) {
     int32_t* head = (int32_t*)(base + plan.key_jobs - 256);
@@ -883,16 +929,18 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
   static std::atomic<uint64_t> on[4];
   if (s.d == 128) {
     run(Bwd<128>{}, keys_kernel<128>, plan.key_tiles, plan.parts, on[0]);
-    run(Bwd<128>{}, queries_kernel<128>, plan.query_tiles, 1, on[1]);
+    run(Bwd<128>{}, queries_kernel<128>, plan.query_tiles, plan.q_parts, on[1]);
   } else {
     run(Bwd<64>{}, keys_kernel<64>, plan.key_tiles, plan.parts, on[2]);
-    run(Bwd<64>{}, queries_kernel<64>, plan.query_tiles, 1, on[3]);
+    run(Bwd<64>{}, queries_kernel<64>, plan.query_tiles, plan.q_parts, on[3]);
   }
-  if (plan.parts > 1 && e == cudaSuccess) {
-    e = launch(true, s.d == 128 ? keys_sum_kernel<128> : keys_sum_kernel<64>,
-               dim3((unsigned)(plan.key_tiles * s.kv_heads), 4), kThreads, 0, 0, st, a);
+  auto join = [&](bool on_, auto kern, int64_t tiles) {
+    if (!on_ || e != cudaSuccess) return;
+    e = launch(true, kern, dim3((unsigned)(tiles * s.kv_heads), 4), kThreads, 0, 0, st, a);
     count_launches(1);
-  }
+  };
+  join(plan.parts > 1, s.d == 128 ? sum_kernel<128, true> : sum_kernel<64, true>, plan.key_tiles);
+  join(plan.q_parts > 1, s.d == 128 ? sum_kernel<128, false> : sum_kernel<64, false>, plan.query_tiles);
   count_launches(1);
   if (e != cudaSuccess) (void)cudaGetLastError();
   const cudaError_t f = use_ws ? cudaSuccess : scratch_free(scratch, st);

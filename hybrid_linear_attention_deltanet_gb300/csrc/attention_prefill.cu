@@ -41,8 +41,9 @@ struct FwdArgs {
   const Job* jobs;
   // kParts: what the parts of a job leave for join_kernel, [jobs][parts][256 rows]
   int32_t parts;
+  int64_t* dest;           // [jobs][256] the row's place in lse, -1: none
   float2* ml;              // maximum (in powers of two) and sum, 0 where the part saw no key
-  float* o;                // [..][D]
+  float* o;                // [jobs][parts][D / 4][256][4]
   unsigned* status;
 };
 
@@ -135,8 +136,8 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     prefetch_tensormap(&a.k);
     prefetch_tensormap(&a.v);
   }
+  grid_release_next();
   grid_wait();
-  grid_release_next();   // (the join reads the sequences before it waits)
   bool here = true;
   if constexpr (kMode != kListed) {
     Seq seq;
@@ -152,6 +153,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   const uint32_t tmem = tmem_base;
   if (!here) {
     if (warp == 8) tmem_dealloc(tmem, 512);
+    if (kMode == kParts && blockIdx.y == 0 && tid < 256) a.dest[(int64_t)blockIdx.x * 256 + tid] = -1;
     return;
   }
   const int part = kMode == kParts ? blockIdx.y : 0, parts = kMode == kParts ? a.parts : 1;
@@ -433,6 +435,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       release(job);
       if constexpr (kMode == kParts) {
         const int64_t at = ((int64_t)blockIdx.x * parts + part) * 256 + 128 * w + row;
+        if (part == 0) a.dest[(int64_t)blockIdx.x * 256 + 128 * w + row] = live ? r : -1;
         if (live) a.ml[at] = make_float2(m, n > 0 ? l : 0.f);
         if (n > 0) {
 #pragma unroll
@@ -443,7 +446,9 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               if (live)
-                *reinterpret_cast<uint4*>(a.o + at * D + 32 * i + 4 * x) =
+                // (four columns of all rows together: a warp's store is contiguous)
+                *reinterpret_cast<uint4*>(a.o + (at - 128 * w - row) * D +
+                                          ((8 * i + x) * 256 + 128 * w + row) * 4) =
                     make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
         }
@@ -493,95 +498,87 @@ __global__ void __launch_bounds__(kListThreads) prefill_list_kernel(ListArgs a) 
   list_jobs(a);
 }
 
-// The parts of a job, joined in their order: a warp takes a packed row, a lane 4
-// columns (2 of 64), with the loads of eight parts in flight.
+// The parts of a job, joined in their order: a lane holds a packed row, a warp an
+// eighth of its columns, so that loads and stores are contiguous.
 constexpr int kJoinThreads = 256;
 constexpr int kMostParts = 32;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ FwdArgs a) {
-  constexpr int kV = D / 32;
-  __shared__ int64_t scratch[kJoinThreads + 6];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int head = blockIdx.x % a.s.kv_heads;
+  constexpr int kV = D / 32;   // groups of four columns
+  __shared__ float2 ml[kMostParts][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = 32 * blockIdx.y + lane;      // blockIdx.y: 32 rows of the job's 256
   grid_release_next();
-  // (the sequences are inputs: the kernel before this one has waited for them)
-  Seq seq;
-  if (!locate<kJoinThreads>(a.s, blockIdx.x / a.s.kv_heads, 2 * a.per, false, true, scratch, nullptr, seq))
-    return;
   grid_wait();
-  const Place pl(seq, a.per, 0, 1);
-  // blockIdx.y: 8 rows of the job's 256
-  {
-    const int row = 8 * blockIdx.y + warp;
-    const int w = row >> 7, in = row & 127, qi = in / a.s.group;
-    if (qi >= pl.rows_of(w)) return;
-    const int64_t base = (int64_t)blockIdx.x * a.parts * 256 + row;
-    float m = -INFINITY, l = 0.f;
-    if (lane < a.parts) {
-      const float* p = reinterpret_cast<const float*>(a.ml + base + (int64_t)lane * 256);
-      m = ld_waited(p);
-      l = ld_waited(p + 1);
+  int64_t r;
+  asm volatile("ld.global.s64 %0, [%1];" : "=l"(r) : "l"(a.dest + (int64_t)blockIdx.x * 256 + row));
+  const float* o = a.o + (int64_t)blockIdx.x * a.parts * 256 * D + (warp * kV * 256 + row) * 4;
+  // (rows that are no one's have unset statistics, which no one uses)
+#pragma unroll
+  for (int i = 0; i < kMostParts / 8; ++i) {
+    const int p = warp + 8 * i;
+    if (p < a.parts) {
+      const float* from =
+          reinterpret_cast<const float*>(a.ml + ((int64_t)blockIdx.x * a.parts + p) * 256 + row);
+      ml[p][lane] = make_float2(ld_waited(from), ld_waited(from + 1));
     }
-    const bool on = !(l == 0.f);     // (a NaN counts)
-    float top = on ? m : -INFINITY;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = on ? ex2_sfu(m - top) : 0.f;
-    float all = on ? l * f : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    const unsigned some = __ballot_sync(0xffffffffu, on);
-    float acc[kV] = {};
-    for (int p0 = 0; p0 < a.parts; p0 += 8) {
-      float x[8][kV];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in_use = p0 + i < a.parts && (some >> (p0 + i) & 1);
-        const float* src = a.o + (base + (int64_t)(p0 + i) * 256) * D + lane * kV;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) x[i][j] = 0.f;
-        if constexpr (kV == 4) {
-          if (in_use) {
-            const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
-            x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
-          }
-        } else {
-          if (in_use) x[i][0] = ld_waited(src);
-          if (in_use) x[i][1] = ld_waited(src + 1);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float fp = __shfl_sync(0xffffffffu, f, (p0 + i) & 31);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) acc[j] = fmaf(x[i][j], p0 + i < a.parts ? fp : 0.f, acc[j]);
-      }
-    }
-    const int64_t r =
-        (pl.q0 + pl.first_of(w) + qi) * a.q_heads + (int64_t)head * a.s.group + in % a.s.group;
-    const float inv = some ? 1.f / all : 0.f;
-    uint32_t y[kV / 2];
-#pragma unroll
-    for (int i = 0; i < kV / 2; ++i)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(acc[2 * i + 1] * inv), "f"(acc[2 * i] * inv));
-    uint32_t* to = reinterpret_cast<uint32_t*>(a.out + r * D) + lane * (kV / 2);
-#pragma unroll
-    for (int i = 0; i < kV / 2; ++i) to[i] = y[i];
-    if (lane == 0) a.lse[r] = some ? (top + log2f(all)) * kLn2 : -INFINITY;
   }
+  __syncthreads();
+  if (r < 0) return;
+  float top = -INFINITY;
+  for (int p = 0; p < a.parts; ++p) top = ml[p][lane].y == 0.f ? top : fmaxf(top, ml[p][lane].x);
+  float all = 0.f, acc[kV][4] = {};
+  bool some = false;
+  for (int p0 = 0; p0 < a.parts; p0 += 4) {
+    float4 x[4][kV];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const int p = p0 + i < a.parts ? p0 + i : p0;
+        x[i][v] = ld_waited(reinterpret_cast<const float4*>(o + (int64_t)p * 256 * D + v * 1024));
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p0 + i >= a.parts) break;
+      const float2 s = ml[p0 + i][lane];
+      if (s.y == 0.f) continue;                // (a part without keys left nothing; a NaN counts)
+      const float f = ex2_sfu(s.x - top);
+      some = true;
+      all += s.y * f;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        acc[v][0] = fmaf(x[i][v].x, f, acc[v][0]);
+        acc[v][1] = fmaf(x[i][v].y, f, acc[v][1]);
+        acc[v][2] = fmaf(x[i][v].z, f, acc[v][2]);
+        acc[v][3] = fmaf(x[i][v].w, f, acc[v][3]);
+      }
+    }
+  }
+  const float inv = some ? 1.f / all : 0.f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    uint32_t y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+          : "=r"(y[i])
+          : "f"(acc[v][2 * i + 1] * inv), "f"(acc[v][2 * i] * inv));
+    *reinterpret_cast<uint2*>(a.out + r * D + (warp * kV + v) * 4) = make_uint2(y[0], y[1]);
+  }
+  if (warp == 0) a.lse[r] = some ? (top + log2f(all)) * kLn2 : -INFINITY;
 }
 
-// Jobs that the GPU's SMs take in one turn or less: a part of a job's keys each
-// where there are SMs for two parts and more, of at least `kPartBlocks` blocks.
-// More jobs than `kTurns` turns: from a list.
-constexpr int kPartBlocks = 1, kTurns = 2;
+// Where the SMs hold two jobs each or more: a part of a job's keys, if that takes
+// four blocks (a block is 1.1 to 1.7 us) off the longest: the join costs about as
+// much as two.  More jobs than two turns of the SMs: from a list.
 Mode mode_of(int64_t jobs, int64_t blocks, int sms, int32_t& parts) {
   parts = 1;
-  if (jobs > (int64_t)kTurns * sms) return kListed;
+  if (jobs > 2 * (int64_t)sms) return kListed;
   int64_t p = sms / jobs;
-  if (p > blocks / kPartBlocks) p = blocks / kPartBlocks;
+  if (p > blocks) p = blocks;
   if (p > kMostParts) p = kMostParts;
-  if (p < 2 || blocks < 4) return kOnce;
+  if (p < 2 || blocks - (blocks + p - 1) / p < 4) return kOnce;
   parts = (int32_t)p;
   return kParts;
 }
@@ -625,10 +622,11 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   const int64_t jobs = tiles * s.kv_heads, blocks = (s.seqlen_k + kRows - 1) / kRows;
   if (jobs > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
   const Mode mode = mode_of(jobs, blocks, sms, a.parts);
-  size_t need = 0, at_jobs = 256, at_o = 0;
+  size_t need = 0, at_jobs = 256, at_ml = 0, at_o = 0;
   if (mode == kListed) need = at_jobs + (size_t)tiles * sizeof(Job);
   if (mode == kParts) {
-    at_o = align_up((size_t)jobs * a.parts * 256 * sizeof(float2), 256);
+    at_ml = (size_t)jobs * 256 * sizeof(int64_t);
+    at_o = at_ml + (size_t)jobs * a.parts * 256 * sizeof(float2);
     need = at_o + (size_t)jobs * a.parts * 256 * s.d * 4;
   }
   void* scratch = nullptr;
@@ -649,7 +647,8 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
     count_launches(1);
     grid = dim3((unsigned)sms);
   } else if (mode == kParts) {
-    a.ml = (float2*)scratch;
+    a.dest = (int64_t*)scratch;
+    a.ml = (float2*)((char*)scratch + at_ml);
     a.o = (float*)((char*)scratch + at_o);
     grid.y = (unsigned)a.parts;
   }
@@ -671,7 +670,7 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   count_launches(1);
   if (mode == kParts && e == cudaSuccess) {
     e = launch(true, s.d == 128 ? prefill_join_kernel<128> : prefill_join_kernel<64>,
-               dim3((unsigned)jobs, 32), kJoinThreads, 0, 0, st, a);
+               dim3((unsigned)jobs, 8), kJoinThreads, 0, 0, st, a);
     count_launches(1);
   }
   if (e != cudaSuccess) (void)cudaGetLastError();

@@ -23,6 +23,10 @@ constexpr int kRows = 128;           // of a tile: queries x group, or keys
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // The call's sequences; dense batches are cu == nullptr.
 struct Seqs {
   const int32_t *cu_q, *cu_k;

@@ -652,8 +652,8 @@ int gdn_attention_prefill(const void* q, const void* k, const void* v, const int
  * contiguous; q, k, v with strides as above; the rest as above.  P and dS
  * enter the products rounded to bf16, all sums are fp32 and their order is
  * fixed.  No output may overlap an input or another output.  Scratch (8 bytes
- * a token and query head; 32 bytes a tile for long calls, up to 40 MB of
- * partial sums for short ones) from the library's pool, or a caller's 256-byte
+ * a token and query head, 32 bytes a tile, up to 192 MB of partial sums where
+ * there are few long tiles) from the library's pool, or a caller's 256-byte
  * aligned workspace of at least gdn_attention_prefill_backward_workspace_size
  * bytes (rules as gdn_prefill_ws).
  */
