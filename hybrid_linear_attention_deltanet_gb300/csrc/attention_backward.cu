@@ -323,7 +323,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       for (int32_t i = 0; ok && i < n; ++i) {
         const int32_t t = (int32_t)(seq.q0 + (int64_t)(t0 + i) * a.per);
         const int sa = i % C::kNA, sb = i % C::kNB;
-        ok = mbar_wait_warp(&b.a_empty[sa], (uint32_t)((i / C::kNA) & 1) ^ 1u, kWaitNs);
+        ok = mbar_wait_warp_cycles(&b.a_empty[sa], (uint32_t)((i / C::kNA) & 1) ^ 1u, kWaitCycles);
         if (ok && lead) {
           mbar_arrive_expect_tx(&b.a_full[sa], (uint32_t)used * 128 * C::kHalves);
 #pragma unroll
@@ -332,7 +332,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
                         &b.a_full[sa]);
         }
         __syncwarp();
-        ok = ok && mbar_wait_warp(&b.b_empty[sb], (uint32_t)((i / C::kNB) & 1) ^ 1u, kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.b_empty[sb], (uint32_t)((i / C::kNB) & 1) ^ 1u, kWaitCycles);
         if (ok && lead) {
           mbar_arrive_expect_tx(&b.b_full[sb], (uint32_t)used * 128 * C::kHalves);
 #pragma unroll
@@ -364,7 +364,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       };
       auto scores = [&](int32_t i) {   // S^T = K Q^T
         const int sa = i % C::kNA;
-        ok = ok && mbar_wait_warp(&b.a_full[sa], (uint32_t)((i / C::kNA) & 1), kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.a_full[sa], (uint32_t)((i / C::kNA) & 1), kWaitCycles);
         if (!ok) return;
         clean(sm + C::kA, sa, i);
         tc_fence_after();
@@ -379,7 +379,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       };
       auto dprobs = [&](int32_t i) {   // dP^T = V dO^T
         const int sb = i % C::kNB;
-        ok = ok && mbar_wait_warp(&b.b_full[sb], (uint32_t)((i / C::kNB) & 1), kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.b_full[sb], (uint32_t)((i / C::kNB) & 1), kWaitCycles);
         if (!ok) return;
         clean(sm + C::kB, sb, i);
         tc_fence_after();
@@ -393,13 +393,13 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
         __syncwarp();
       };
       if (n > 0) {
-        ok = mbar_wait_warp(&b.own, 0, kWaitNs);
+        ok = mbar_wait_warp_cycles(&b.own, 0, kWaitCycles);
         scores(0);
         dprobs(0);
       }
       for (int32_t i = 0; ok && i < n; ++i) {
         const int sa = i % C::kNA, sb = i % C::kNB;
-        ok = mbar_wait_warp(&b.p_ready, (uint32_t)(i & 1), kWaitNs);
+        ok = mbar_wait_warp_cycles(&b.p_ready, (uint32_t)(i & 1), kWaitCycles);
         if (!ok) break;
         tc_fence_after();
         if (lead) {   // dV += P^T dO
@@ -411,7 +411,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
         }
         __syncwarp();
         if (i + 1 < n) scores(i + 1);
-        ok = ok && mbar_wait_warp(&b.ds_ready, (uint32_t)(i & 1), kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.ds_ready, (uint32_t)(i & 1), kWaitCycles);
         if (!ok) break;
         tc_fence_after();
         if (lead) {   // dK += dS^T Q
@@ -461,7 +461,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       const int32_t lo = lo64 < 0 ? 0 : lo64 > 64 ? 64 : (int32_t)lo64;
       const int32_t hi = (hi64 < used ? (int32_t)hi64 : kRows) - 64 * w;   // (behind `used`: zeros)
       const bool masked = (int64_t)k0 + kRows - 1 - shift > q0 || hi64 < used;
-      ok = mbar_wait_warp(&b.s_full[0], (uint32_t)(i & 1), kWaitNs);
+      ok = mbar_wait_warp_cycles(&b.s_full[0], (uint32_t)(i & 1), kWaitCycles);
       if (!ok) break;
       tc_fence_after();
       uint32_t s[2][32];
@@ -484,7 +484,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.p_ready);
-      ok = mbar_wait_warp(&b.dp_full, (uint32_t)(i & 1), kWaitNs);
+      ok = mbar_wait_warp_cycles(&b.dp_full, (uint32_t)(i & 1), kWaitCycles);
       if (!ok) break;
       tc_fence_after();
       uint32_t g[2][32];
@@ -508,7 +508,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.ds_ready);
     }
-    if (ok && n > 0) ok = mbar_wait_warp(&b.done, 0, kWaitNs);
+    if (ok && n > 0) ok = mbar_wait_warp_cycles(&b.done, 0, kWaitCycles);
     tc_fence_after();
     if (ok) {
       // one warpgroup dV, the other dK
@@ -573,7 +573,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       for (int32_t j = 0; ok && j < n; ++j) {
         const int32_t t = (int32_t)(seq.k0 + (int64_t)(j0 + j) * kRows);
         const int sa = j % C::kNA, sb = j % C::kNB;
-        ok = mbar_wait_warp(&b.a_empty[sa], (uint32_t)((j / C::kNA) & 1) ^ 1u, kWaitNs);
+        ok = mbar_wait_warp_cycles(&b.a_empty[sa], (uint32_t)((j / C::kNA) & 1) ^ 1u, kWaitCycles);
         if (ok && lead) {
           mbar_arrive_expect_tx(&b.a_full[sa], C::kTile);
 #pragma unroll
@@ -581,7 +581,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
             tma_load_3d(sm + C::kA + sa * C::kTile + h * kHalfTile, &a.k, 64 * h, head, t, &b.a_full[sa]);
         }
         __syncwarp();
-        ok = ok && mbar_wait_warp(&b.b_empty[sb], (uint32_t)((j / C::kNB) & 1) ^ 1u, kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.b_empty[sb], (uint32_t)((j / C::kNB) & 1) ^ 1u, kWaitCycles);
         if (ok && lead) {
           mbar_arrive_expect_tx(&b.b_full[sb], C::kTile);
 #pragma unroll
@@ -602,7 +602,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       const uint64_t an = smem_desc(base + C::kA, kHalfTile, 1024, kSwizzle128B);
       auto scores = [&](int32_t j) {   // S = Q K^T
         const int sa = j % C::kNA;
-        ok = ok && mbar_wait_warp(&b.a_full[sa], (uint32_t)((j / C::kNA) & 1), kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.a_full[sa], (uint32_t)((j / C::kNA) & 1), kWaitCycles);
         if (!ok) return;
         // keys behind the sequence's last are another's: their rows become
         // zeros, so that the products with dS = 0 are
@@ -624,7 +624,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       };
       auto dprobs = [&](int32_t j) {   // dP = dO V^T
         const int sb = j % C::kNB;
-        ok = ok && mbar_wait_warp(&b.b_full[sb], (uint32_t)((j / C::kNB) & 1), kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.b_full[sb], (uint32_t)((j / C::kNB) & 1), kWaitCycles);
         if (!ok) return;
         tc_fence_after();
         if (lead) {
@@ -638,14 +638,14 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
         __syncwarp();
       };
       if (n > 0) {
-        ok = mbar_wait_warp(&b.own, 0, kWaitNs);
+        ok = mbar_wait_warp_cycles(&b.own, 0, kWaitCycles);
         scores(0);
         dprobs(0);
       }
       for (int32_t j = 0; ok && j < n; ++j) {
         const int sa = j % C::kNA;
         if (j + 1 < n) scores(j + 1);
-        ok = ok && mbar_wait_warp(&b.ds_ready, (uint32_t)(j & 1), kWaitNs);
+        ok = ok && mbar_wait_warp_cycles(&b.ds_ready, (uint32_t)(j & 1), kWaitCycles);
         if (!ok) break;
         tc_fence_after();
         if (lead) {   // dQ += dS K
@@ -676,7 +676,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       const int32_t k0 = (j0 + j) * kRows;
       const bool masked = k0 + kRows - 1 > first + shift;
       const int32_t see = last - k0 - 64 * w;
-      ok = mbar_wait_warp(&b.s_full[j & 1], (uint32_t)((j >> 1) & 1), kWaitNs);
+      ok = mbar_wait_warp_cycles(&b.s_full[j & 1], (uint32_t)((j >> 1) & 1), kWaitCycles);
       if (!ok) break;
       tc_fence_after();
       uint32_t s[2][32];
@@ -688,7 +688,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 32; x += 2) exp_pair(s[h][x], s[h][x + 1], cc, ll);
-      ok = mbar_wait_warp(&b.dp_full, (uint32_t)(j & 1), kWaitNs);
+      ok = mbar_wait_warp_cycles(&b.dp_full, (uint32_t)(j & 1), kWaitCycles);
       if (!ok) break;
       tc_fence_after();
       uint32_t g[2][32];
@@ -709,7 +709,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.ds_ready);
     }
-    if (ok && n > 0) ok = mbar_wait_warp(&b.done, 0, kWaitNs);
+    if (ok && n > 0) ok = mbar_wait_warp_cycles(&b.done, 0, kWaitCycles);
     tc_fence_after();
     if (ok) {
       // half the columns each

@@ -35,7 +35,7 @@ constexpr int kSms = 152;
 constexpr int kCtas = 2 * kSms;     // two resident ones an SM
 constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr long long kWaitCycles = 4000000000ll;   // about two seconds
 
 template <int D, bool kFp8>
 struct Shape {
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         }
       }
       if (i + 1 < hi) id = read_id();
-      ok = mbar_wait_warp(&empty[stage], (uint32_t)(((i - lo) / S::kStages) & 1) ^ 1u, kWaitNs);
+      ok = mbar_wait_warp_cycles(&empty[stage], (uint32_t)(((i - lo) / S::kStages) & 1) ^ 1u, kWaitCycles);
       if (!ok) break;
       const int64_t pos = (int64_t)now.at * S::kTile;
       const int64_t tokens = now.len - pos < S::kTile ? now.len - pos : S::kTile;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     int64_t first_of_part = lo;
     for (int64_t i = lo; i < hi; ++i) {
       const int stage = (int)((i - lo) % S::kStages);
-      ok = mbar_wait_warp(&full[stage], (uint32_t)(((i - lo) / S::kStages) & 1), kWaitNs);
+      ok = mbar_wait_warp_cycles(&full[stage], (uint32_t)(((i - lo) / S::kStages) & 1), kWaitCycles);
       if (!ok) break;
       const Tile tile = meta[stage];
       uint8_t* bytes = smem + stage * S::kStage;

@@ -105,7 +105,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
   __shared__ uint64_t q_full, q_empty, kv_full[C::kStages], kv_empty[C::kStages], s_full[2],
-      p_half[2], p_full[2], o_full[2], job_full[2], job_empty[2];
+      p_half[2], p_full[2], o_full[2], job_full[2], job_empty[2], turn[2];
   __shared__ uint32_t tmem_base;
   __shared__ int64_t scratch[kMode == kListed ? 1 : kThreads + 6];
   __shared__ Seq slots[2];
@@ -115,18 +115,19 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   const Seqs& sq = a.s;
   if (tid == 0) {
     mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
+    mbar_init(&q_empty, 2);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
+      mbar_init(&turn[i], 1);
       mbar_init(&job_full[i], 1);
-      mbar_init(&job_empty[i], 9);
+      mbar_init(&job_empty[i], 10);
     }
     fence_barrier_init();
   }
@@ -167,7 +168,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       s = slots[0];
       return true;
     } else {
-      ok = mbar_wait_warp(&job_full[n & 1], (n >> 1) & 1, kWaitNs);
+      ok = mbar_wait_warp_cycles(&job_full[n & 1], (n >> 1) & 1, kWaitCycles);
       if (!ok) return false;
       s = slots[n & 1];
       return s.tile >= 0;
@@ -195,7 +196,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
           int64_t at = 0;
           if (lane == 0) at = atomicAdd(a.next, 1u);
           at = __shfl_sync(0xffffffffu, at, 0);
-          ok = mbar_wait_warp(&job_empty[n & 1], ((n >> 1) & 1) ^ 1u, kWaitNs);
+          ok = mbar_wait_warp_cycles(&job_empty[n & 1], ((n >> 1) & 1) ^ 1u, kWaitCycles);
           if (!ok) break;
           int32_t count;
           asm volatile("ld.global.s32 %0, [%1];" : "=r"(count) : "l"(a.count));
@@ -222,7 +223,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
         }
         const Place pl(seq, a.per, part, parts);
         if (pl.most == 0) continue;
-        ok = mbar_wait_warp(&q_empty, (jobs_done & 1) ^ 1u, kWaitNs);
+        ok = mbar_wait_warp_cycles(&q_empty, (jobs_done & 1) ^ 1u, kWaitCycles);
         if (!ok) break;
         ++jobs_done;
         if (lead) {
@@ -239,7 +240,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t st = kv % C::kStages;
-            ok = ok && mbar_wait_warp(&kv_empty[st], ((kv / C::kStages) & 1) ^ 1u, kWaitNs);
+            ok = ok && mbar_wait_warp_cycles(&kv_empty[st], ((kv / C::kStages) & 1) ^ 1u, kWaitCycles);
             if (ok && lead) {
               uint8_t* to = sm + (2 + st) * C::kTile;
               mbar_arrive_expect_tx(&kv_full[st], C::kTile);
@@ -253,78 +254,87 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
           }
         }
       }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 10) {
       // ------------------------------------------------------- multiply
+      // A warp for each tile: waiting and issuing for both took one warp 3200
+      // cycles a block, half as long again as the products.  They take turns, so that
+      // one tile's products run while the other's probabilities are made; left to
+      // themselves both wait for these at the same time.
+      const int w = warp == 10;
       const bool lead = elect_one();
       const uint32_t base = smem_u32(sm);
       constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kOut = idesc_bf16(128, D, 0, 1);
-      uint64_t qd = smem_desc(base, 16, 1024, kSwizzle128B);
+      const uint64_t qd = smem_desc(base + w * C::kTile, 16, 1024, kSwizzle128B);
       const uint64_t kd = smem_desc(base + 2 * C::kTile, 16, 1024, kSwizzle128B);
       const uint64_t vd = smem_desc(base + 2 * C::kTile, kTileBytes, 1024, kSwizzle128B);
-      uint32_t kv = 0, jobs_done = 0, probs[2] = {0, 0};   // a tile's blocks so far
+      const uint32_t s_at = tmem + C::kS + 128 * w, o_at = tmem + C::kO + 128 * w;
+      uint32_t kv = 0, jobs_done = 0, steps = 0, probs = 0;   // (probs: the tile's blocks so far)
       Seq seq;
       for (uint32_t n = 0; ok && take(n, seq); ++n) {
-        const Place pl(seq, a.per, part, parts);
+        int32_t most, blocks, last;      // last: keys of the last block
+        {
+          const Place pl(seq, a.per, part, parts);
+          most = pl.most;
+          blocks = pl.blocks_of(w);
+          const int64_t valid = pl.lk - (int64_t)(pl.begin + most - 1) * kRows;
+          last = valid < kRows ? (int32_t)valid : kRows;
+        }
         release(n);
-        if (pl.most == 0) continue;
-        ok = mbar_wait_warp(&q_full, jobs_done & 1, kWaitNs);
+        if (most == 0) continue;
+        ok = mbar_wait_warp_cycles(&q_full, jobs_done & 1, kWaitCycles);
         ++jobs_done;
         // step j: P V of block j - 1, then Q K^T of block j; a block's K is loaded
         // one stage before its V
-        for (int32_t j = 0; ok && j <= pl.most; ++j) {
-          asm volatile("" : "+l"(qd));   // (else all descriptors of the loop are kept, and spilled)
+        for (int32_t j = 0; ok && j <= most; ++j, ++steps) {
           const uint32_t ki = kv + 2 * j, vi = kv + 2 * j - 1;
           const uint32_t k_st = ki % C::kStages, v_st = vi % C::kStages;
-          if (j < pl.most) ok = mbar_wait_warp(&kv_full[k_st], (ki / C::kStages) & 1, kWaitNs);
-          if (ok && j > 0) {
-            ok = mbar_wait_warp(&kv_full[v_st], (vi / C::kStages) & 1, kWaitNs);
+          if (j > 0) {
+            ok = mbar_wait_warp_cycles(&kv_full[v_st], (vi / C::kStages) & 1, kWaitCycles);
             // values behind the sequence's last one are another's: a product
             // with a zero probability has to be zero
-            const int64_t valid = pl.lk - (int64_t)(pl.begin + j - 1) * kRows;
-            if (ok && valid < kRows) {
+            if (ok && j == most && last < kRows) {
               for (int h = 0; h < C::kHalves; ++h) {
                 uint4* z = reinterpret_cast<uint4*>(sm + (2 + v_st) * C::kTile + h * kTileBytes);
-                for (int i = (int)valid * 8 + lane; i < kRows * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+                for (int i = last * 8 + lane; i < kRows * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
               }
               fence_proxy_async_smem();
               __syncwarp();
             }
           }
+          if (j < most)
+            ok = ok && mbar_wait_warp_cycles(&kv_full[k_st], (ki / C::kStages) & 1, kWaitCycles);
+          ok = ok && mbar_wait_warp_cycles(&turn[w], (steps & 1) ^ (w ? 0u : 1u), kWaitCycles);
+          if (ok && j > 0 && j <= blocks) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t s_at = tmem + C::kS + 128 * w, o_at = tmem + C::kO + 128 * w;
-            if (ok && j > 0 && j <= pl.blocks[w]) {
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && mbar_wait_warp_cycles(half ? &p_full[w] : &p_half[w], probs & 1, kWaitCycles);
+              tc_fence_after();
+              if (ok && lead)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                ok = ok && mbar_wait_warp(half ? &p_full[w] : &p_half[w], probs[w] & 1, kWaitNs);
-                tc_fence_after();
-                if (ok && lead)
-#pragma unroll
-                  for (int s = 4 * half; s < 4 * half + 4; ++s)
-                    mma_bf16_ts(o_at, s_at + 8 * s, vd + (uint64_t)((v_st * C::kTile + s * 2048) >> 4),
-                                kOut, j > 1 || s > 0);
-              }
-              ++probs[w];
-              if (ok && lead && j == pl.blocks[w]) mma_commit(&o_full[w]);
+                for (int s = 4 * half; s < 4 * half + 4; ++s)
+                  mma_bf16_ts(o_at, s_at + 8 * s, vd + (uint64_t)((v_st * C::kTile + s * 2048) >> 4),
+                              kOut, j > 1 || s > 0);
             }
-            if (ok && lead && j < pl.blocks[w]) {
+            ++probs;
+          }
+          if (ok && lead) {
+            if (j > 0 && j == blocks) mma_commit(&o_full[w]);
+            if (j < blocks) {
               tc_fence_after();
 #pragma unroll
               for (int s = 0; s < D / 16; ++s)
-                mma_bf16(s_at, qd + (uint64_t)((w * C::kTile + kstep(s)) >> 4),
+                mma_bf16(s_at, qd + (uint64_t)(kstep(s) >> 4),
                          kd + (uint64_t)((k_st * C::kTile + kstep(s)) >> 4), kScores, s > 0);
               mma_commit(&s_full[w]);
             }
-            __syncwarp();
-          }
-          if (ok && lead) {
+            mbar_arrive(&turn[w ^ 1]);
             if (j > 0) mma_commit(&kv_empty[v_st]);
-            if (j < pl.most) mma_commit(&kv_empty[k_st]);
-            if (j + 1 == pl.most) mma_commit(&q_empty);
+            if (j < most) mma_commit(&kv_empty[k_st]);
+            if (j + 1 == most) mma_commit(&q_empty);
           }
           __syncwarp();
         }
-        kv += 2 * pl.most;
+        kv += 2 * most;
       }
     }
   } else {
@@ -348,7 +358,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       }
       float m = 0.f, l = 0.f;
       for (int32_t j = 0; j < n; ++j, ++scores) {
-        ok = mbar_wait_warp(&s_full[w], scores & 1, kWaitNs);
+        ok = mbar_wait_warp_cycles(&s_full[w], scores & 1, kWaitCycles);
         if (!ok) break;
         tc_fence_after();
         uint32_t s[4][32];
@@ -424,7 +434,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       }
       // the row's results.  (The next job's first product into O waits for this
       // warpgroup's next probabilities, so these loads come before it.)
-      if (ok && n > 0) ok = mbar_wait_warp(&o_full[w], outs++ & 1, kWaitNs);
+      if (ok && n > 0) ok = mbar_wait_warp_cycles(&o_full[w], outs++ & 1, kWaitCycles);
       tc_fence_after();
       if (!ok) break;
       const int slot = kMode == kListed ? job & 1 : 0;

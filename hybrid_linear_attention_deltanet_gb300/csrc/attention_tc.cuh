@@ -18,7 +18,7 @@ namespace attn {
 
 using namespace hostcheck;
 
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr long long kWaitCycles = 4000000000ll;   // about two seconds
 constexpr int kRows = 128;           // of a tile: queries x group, or keys
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
