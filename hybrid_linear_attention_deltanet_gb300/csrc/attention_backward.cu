@@ -12,7 +12,7 @@
 // bound by the tensor cores; the order of their products is such that the
 // cores work on the next tile's scores while P and dS of this one are made:
 //   keys:     dV(i), S(i+1), dK(i), dP(i+1), ...
-//   queries:  S(j+1), dQ(j), dP(j+1), ...
+//   queries:  dP(j+1), dQ(j), S(j+2), ...
 // P and dS go back to tensor memory as bf16, over the scores that they came
 // from, and are the A operand there.
 #include "attention_tc.cuh"
@@ -100,8 +100,8 @@ struct Bwd {
   static constexpr uint32_t kSmem = kBars + 256;
 };
 struct Bars {
-  uint64_t own, a_full[3], a_empty[3], b_full[2], b_empty[2], s_full[2], dp_full, p_ready, ds_ready,
-      done;
+  uint64_t own, a_full[3], a_empty[3], b_full[2], b_empty[2], s_full[2], dp_full, p_ready,
+      ds_ready[2], done, turn[2];
   uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 256, "");
@@ -237,13 +237,14 @@ __device__ __forceinline__ bool begin(const BwdArgs& a, uint8_t* sm, bool keys, 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.b_full[i], 1);
-      mbar_init(&b.b_empty[i], 1);
+      mbar_init(&b.b_empty[i], keys ? 2 : 1);
+      mbar_init(&b.turn[i], 1);
+      mbar_init(&b.ds_ready[i], 8);
       mbar_init(&b.s_full[i], 1);
     }
     mbar_init(&b.dp_full, 1);
     mbar_init(&b.p_ready, 8);
-    mbar_init(&b.ds_ready, 8);
-    mbar_init(&b.done, 1);
+    mbar_init(&b.done, keys ? 2 : 1);
     fence_barrier_init();
   }
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -342,88 +343,72 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
         }
         __syncwarp();
       }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 10) {
       // ------------------------------------------------------- multiply
+      // One warp dV(i - 1) and S(i), one dK(i - 1) and dP(i), in turns: while one's
+      // products run, the other waits for the operands that the first one's last
+      // results become.  (All of it by one warp took its waits and commits besides
+      // the products.)
+      const int w = warp == 10;
       const bool lead = elect_one();
       const uint32_t base = smem_u32(sm);
       constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kGrad = idesc_bf16(128, D, 0, 1);
-      const uint64_t own = smem_desc(base, 16, 1024, kSwizzle128B);
-      const uint64_t own2 = smem_desc(base + C::kTile, 16, 1024, kSwizzle128B);
-      const uint64_t ak = smem_desc(base + C::kA, 16, 1024, kSwizzle128B);
-      const uint64_t bk = smem_desc(base + C::kB, 16, 1024, kSwizzle128B);
-      const uint64_t an = smem_desc(base + C::kA, kHalfTile, 1024, kSwizzle128B);
-      const uint64_t bn = smem_desc(base + C::kB, kHalfTile, 1024, kSwizzle128B);
+      // w: K (V) and the slots of Q (dO) for the scores, those of dO (Q) for the gradient
+      const uint32_t mine = w ? C::kB : C::kA, other = w ? C::kA : C::kB;
+      const uint64_t own = smem_desc(base + w * C::kTile, 16, 1024, kSwizzle128B);
+      const uint64_t sd = smem_desc(base + mine, 16, 1024, kSwizzle128B);
+      const uint64_t gd = smem_desc(base + other, kHalfTile, 1024, kSwizzle128B);
+      const uint32_t s_at = tmem + (w ? kDP : kS), g_at = tmem + (w ? kDK : kDV);
+      uint64_t* const s_done = w ? &b.dp_full : &b.s_full[0];
       // queries behind the sequence's last are another's: their rows become zeros
-      auto clean = [&](uint8_t* slots, int slot, int32_t i) {
+      auto clean = [&](uint32_t slots, int slot, int32_t i) {
         const int64_t rows = ((int64_t)seq.lq - (int64_t)(t0 + i) * a.per) * group;
         if (rows < used) {
-          zero_rows<D>(slots + slot * C::kTile, (int)rows, lane);
+          zero_rows<D>(sm + slots + slot * C::kTile, (int)rows, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();
       };
-      auto scores = [&](int32_t i) {   // S^T = K Q^T
-        const int sa = i % C::kNA;
-        ok = ok && mbar_wait_warp_cycles(&b.a_full[sa], (uint32_t)((i / C::kNA) & 1), kWaitCycles);
-        if (!ok) return;
-        clean(sm + C::kA, sa, i);
-        tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_bf16(tmem + kS, own + (uint64_t)(kstep(s) >> 4),
-                     ak + (uint64_t)((sa * C::kTile + kstep(s)) >> 4), kScores, s > 0);
-          mma_commit(&b.s_full[0]);
+      if (n > 0) ok = mbar_wait_warp_cycles(&b.own, 0, kWaitCycles);
+      for (int32_t i = 0; ok && i <= n && n > 0; ++i) {
+        const int sa = i % C::kNA, sb = i % C::kNB;                   // slots of step i ...
+        const int ga = (i + C::kNA - 1) % C::kNA, gb = (i + C::kNB - 1) % C::kNB;   // ... and i - 1
+        const int s_slot = w ? sb : sa, g_slot = w ? ga : gb;
+        if (i < n) {
+          ok = w ? mbar_wait_warp_cycles(&b.b_full[sb], (uint32_t)((i / C::kNB) & 1), kWaitCycles)
+                 : mbar_wait_warp_cycles(&b.a_full[sa], (uint32_t)((i / C::kNA) & 1), kWaitCycles);
+          if (ok) clean(mine, s_slot, i);
         }
-        __syncwarp();
-      };
-      auto dprobs = [&](int32_t i) {   // dP^T = V dO^T
-        const int sb = i % C::kNB;
-        ok = ok && mbar_wait_warp_cycles(&b.b_full[sb], (uint32_t)((i / C::kNB) & 1), kWaitCycles);
-        if (!ok) return;
-        clean(sm + C::kB, sb, i);
-        tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_bf16(tmem + kDP, own2 + (uint64_t)(kstep(s) >> 4),
-                     bk + (uint64_t)((sb * C::kTile + kstep(s)) >> 4), kScores, s > 0);
-          mma_commit(&b.dp_full);
+        if (ok && i > 0 && !w) {   // (Q's slot: its scores are done, so it is there)
+          ok = mbar_wait_warp_cycles(&b.b_full[gb], (uint32_t)(((i - 1) / C::kNB) & 1), kWaitCycles);
+          if (ok) clean(other, gb, i - 1);
         }
-        __syncwarp();
-      };
-      if (n > 0) {
-        ok = mbar_wait_warp_cycles(&b.own, 0, kWaitCycles);
-        scores(0);
-        dprobs(0);
-      }
-      for (int32_t i = 0; ok && i < n; ++i) {
-        const int sa = i % C::kNA, sb = i % C::kNB;
-        ok = mbar_wait_warp_cycles(&b.p_ready, (uint32_t)(i & 1), kWaitCycles);
+        ok = ok && mbar_wait_warp_cycles(&b.turn[w], (uint32_t)(i & 1) ^ (w ? 0u : 1u), kWaitCycles);
+        if (ok && i > 0)
+          ok = mbar_wait_warp_cycles(w ? &b.ds_ready[0] : &b.p_ready, (uint32_t)((i - 1) & 1), kWaitCycles);
         if (!ok) break;
         tc_fence_after();
-        if (lead) {   // dV += P^T dO
+        if (lead) {
+          if (i > 0) {   // dV += P^T dO, dK += dS^T Q
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_bf16_ts(tmem + kDV, tmem + kS + (s >> 2) * 64 + (s & 3) * 8,
-                        bn + (uint64_t)((sb * C::kTile + s * 2048) >> 4), kGrad, i > 0 || s > 0);
-          mma_commit(&b.b_empty[sb]);
+            for (int s = 0; s < 8; ++s)
+              mma_bf16_ts(g_at, s_at + (s >> 2) * 64 + (s & 3) * 8,
+                          gd + (uint64_t)((g_slot * C::kTile + s * 2048) >> 4), kGrad, i > 1 || s > 0);
+            if (w) mma_commit(&b.a_empty[ga]);
+            else mma_commit(&b.b_empty[gb]);
+          }
+          if (i < n) {   // S^T = K Q^T, dP^T = V dO^T
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              mma_bf16(s_at, own + (uint64_t)(kstep(s) >> 4),
+                       sd + (uint64_t)((s_slot * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+            mma_commit(s_done);
+          }
+          mbar_arrive(&b.turn[w ^ 1]);
+          if (w && i < n) mma_commit(&b.b_empty[sb]);
+          if (i == n) mma_commit(&b.done);
         }
         __syncwarp();
-        if (i + 1 < n) scores(i + 1);
-        ok = ok && mbar_wait_warp_cycles(&b.ds_ready, (uint32_t)(i & 1), kWaitCycles);
-        if (!ok) break;
-        tc_fence_after();
-        if (lead) {   // dK += dS^T Q
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_bf16_ts(tmem + kDK, tmem + kDP + (s >> 2) * 64 + (s & 3) * 8,
-                        an + (uint64_t)((sa * C::kTile + s * 2048) >> 4), kGrad, i > 0 || s > 0);
-          mma_commit(&b.a_empty[sa]);
-          if (i + 1 == n) mma_commit(&b.done);
-        }
-        __syncwarp();
-        if (i + 1 < n) dprobs(i + 1);
       }
     }
   } else {
@@ -506,7 +491,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b.ds_ready);
+      if (lane == 0) mbar_arrive(&b.ds_ready[0]);
     }
     if (ok && n > 0) ok = mbar_wait_warp_cycles(&b.done, 0, kWaitCycles);
     tc_fence_after();
@@ -590,74 +575,80 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
         }
         __syncwarp();
       }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 10) {
       // ------------------------------------------------------- multiply
+      // One warp dP(j + 1), as soon as dS(j) is there; then the other dQ(j) and
+      // S(j + 2), while dS(j + 1) is made.  (Two barriers each for dS and for the
+      // turn: either may be a step further than this warp, but not two, as S(j + 2)
+      // comes from here.)
       const bool lead = elect_one();
       const uint32_t base = smem_u32(sm);
       constexpr uint32_t kScores = idesc_bf16(128, 128, 0, 0), kGrad = idesc_bf16(128, D, 0, 1);
-      const uint64_t own = smem_desc(base, 16, 1024, kSwizzle128B);
-      const uint64_t own2 = smem_desc(base + C::kTile, 16, 1024, kSwizzle128B);
-      const uint64_t ak = smem_desc(base + C::kA, 16, 1024, kSwizzle128B);
-      const uint64_t bk = smem_desc(base + C::kB, 16, 1024, kSwizzle128B);
-      const uint64_t an = smem_desc(base + C::kA, kHalfTile, 1024, kSwizzle128B);
-      auto scores = [&](int32_t j) {   // S = Q K^T
-        const int sa = j % C::kNA;
-        ok = ok && mbar_wait_warp_cycles(&b.a_full[sa], (uint32_t)((j / C::kNA) & 1), kWaitCycles);
-        if (!ok) return;
-        // keys behind the sequence's last are another's: their rows become
-        // zeros, so that the products with dS = 0 are
-        const int64_t valid = seq.lk - (int64_t)(j0 + j) * kRows;
-        if (valid < kRows) {
-          zero_rows<D>(sm + C::kA + sa * C::kTile, (int)valid, lane);
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        tc_fence_after();
-        if (lead) {
+      if (n > 0) ok = mbar_wait_warp_cycles(&b.own, 0, kWaitCycles);
+      if (warp == 10) {
+        const uint64_t own2 = smem_desc(base + C::kTile, 16, 1024, kSwizzle128B);
+        const uint64_t bk = smem_desc(base + C::kB, 16, 1024, kSwizzle128B);
+        for (int32_t j = 0; ok && j < n; ++j) {   // dP = dO V^T
+          const int sb = j % C::kNB;
+          ok = mbar_wait_warp_cycles(&b.b_full[sb], (uint32_t)((j / C::kNB) & 1), kWaitCycles);
+          if (ok && j > 0)
+            ok = mbar_wait_warp_cycles(&b.ds_ready[(j - 1) & 1], (uint32_t)(((j - 1) >> 1) & 1), kWaitCycles);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_bf16(tmem + kS + 128 * (j & 1), own + (uint64_t)(kstep(s) >> 4),
-                     ak + (uint64_t)((sa * C::kTile + kstep(s)) >> 4), kScores, s > 0);
-          mma_commit(&b.s_full[j & 1]);
+            for (int s = 0; s < D / 16; ++s)
+              mma_bf16(tmem + kDP, own2 + (uint64_t)(kstep(s) >> 4),
+                       bk + (uint64_t)((sb * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+            mma_commit(&b.dp_full);
+            if (j > 0) mbar_arrive(&b.turn[j & 1]);
+            mma_commit(&b.b_empty[sb]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      };
-      auto dprobs = [&](int32_t j) {   // dP = dO V^T
-        const int sb = j % C::kNB;
-        ok = ok && mbar_wait_warp_cycles(&b.b_full[sb], (uint32_t)((j / C::kNB) & 1), kWaitCycles);
-        if (!ok) return;
-        tc_fence_after();
-        if (lead) {
+      } else {
+        const uint64_t own = smem_desc(base, 16, 1024, kSwizzle128B);
+        const uint64_t ak = smem_desc(base + C::kA, 16, 1024, kSwizzle128B);
+        const uint64_t an = smem_desc(base + C::kA, kHalfTile, 1024, kSwizzle128B);
+        // step j: dQ(j - 2) += dS K, then S(j) = Q K^T in the buffer of dS(j - 2)
+        for (int32_t j = 0; ok && j < n + 2 && n > 0; ++j) {
+          const int sa = j % C::kNA, ga = (j + 2 * C::kNA - 2) % C::kNA;
+          if (j >= 2) {
+            ok = mbar_wait_warp_cycles(&b.ds_ready[j & 1], (uint32_t)(((j - 2) >> 1) & 1), kWaitCycles);
+            if (ok && j - 1 < n)   // dP(j - 1) goes first: turn[1] for odd ones, from 1; [0] from 2
+              ok = mbar_wait_warp_cycles(&b.turn[(j - 1) & 1], (uint32_t)(((j - 2) >> 1) & 1), kWaitCycles);
+            tc_fence_after();
+            if (ok && lead) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_bf16(tmem + kDP, own2 + (uint64_t)(kstep(s) >> 4),
-                     bk + (uint64_t)((sb * C::kTile + kstep(s)) >> 4), kScores, s > 0);
-          mma_commit(&b.dp_full);
-          mma_commit(&b.b_empty[sb]);
-        }
-        __syncwarp();
-      };
-      if (n > 0) {
-        ok = mbar_wait_warp_cycles(&b.own, 0, kWaitCycles);
-        scores(0);
-        dprobs(0);
-      }
-      for (int32_t j = 0; ok && j < n; ++j) {
-        const int sa = j % C::kNA;
-        if (j + 1 < n) scores(j + 1);
-        ok = ok && mbar_wait_warp_cycles(&b.ds_ready, (uint32_t)(j & 1), kWaitCycles);
-        if (!ok) break;
-        tc_fence_after();
-        if (lead) {   // dQ += dS K
+              for (int s = 0; s < 8; ++s)
+                mma_bf16_ts(tmem + kDQ, tmem + kS + 128 * (j & 1) + (s >> 2) * 64 + (s & 3) * 8,
+                            an + (uint64_t)((ga * C::kTile + s * 2048) >> 4), kGrad, j > 2 || s > 0);
+              mma_commit(&b.a_empty[ga]);
+              if (j == n + 1) mma_commit(&b.done);
+            }
+            __syncwarp();
+          }
+          if (j < n) {
+            ok = ok && mbar_wait_warp_cycles(&b.a_full[sa], (uint32_t)((j / C::kNA) & 1), kWaitCycles);
+            // keys behind the sequence's last are another's: their rows become
+            // zeros, so that the products with dS = 0 are
+            const int64_t valid = seq.lk - (int64_t)(j0 + j) * kRows;
+            if (ok && valid < kRows) {
+              zero_rows<D>(sm + C::kA + sa * C::kTile, (int)valid, lane);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            tc_fence_after();
+            if (ok && lead) {
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_bf16_ts(tmem + kDQ, tmem + kS + 128 * (j & 1) + (s >> 2) * 64 + (s & 3) * 8,
-                        an + (uint64_t)((sa * C::kTile + s * 2048) >> 4), kGrad, j > 0 || s > 0);
-          mma_commit(&b.a_empty[sa]);
-          if (j + 1 == n) mma_commit(&b.done);
+              for (int s = 0; s < D / 16; ++s)
+                mma_bf16(tmem + kS + 128 * (j & 1), own + (uint64_t)(kstep(s) >> 4),
+                         ak + (uint64_t)((sa * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+              mma_commit(&b.s_full[j & 1]);
+            }
+            __syncwarp();
+          }
         }
-        __syncwarp();
-        if (j + 1 < n) dprobs(j + 1);
       }
     }
   } else {
@@ -707,7 +698,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b.ds_ready);
+      if (lane == 0) mbar_arrive(&b.ds_ready[j & 1]);
     }
     if (ok && n > 0) ok = mbar_wait_warp_cycles(&b.done, 0, kWaitCycles);
     tc_fence_after();
