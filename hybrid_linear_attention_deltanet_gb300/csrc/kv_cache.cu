@@ -165,56 +165,45 @@ struct AppendArgs {
   unsigned* status;
 };
 
-// d / 8 lanes hold one head of one token, 16 bytes of its key and of its value
-// each, for kUnits tokens in turn whose loads are all in flight.  Prompts are
-// bound by HBM: four tokens' loads cover the chain of small ones (sequence,
-// start, page) that each place takes.  A decoding step's few tokens are bound by
-// that chain: one each.
-template <int D, bool kFp8, int kUnits>
+// d / 16 lanes hold one head of one token, 32 bytes of its key and of its value
+// each.  A decoding step's few tokens are bound by the chain of small loads
+// (sequence, start, page) that their places take, prompts by HBM and, in 8 bits, by
+// instructions as much (64-bit divisions, and 16 bytes a lane, made them half as
+// long again).
+template <int D, bool kFp8>
 __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
-  constexpr int kLanes = D / 8;
-  constexpr int kSpan = kCopy / kLanes;   // heads of tokens that the CTA holds at a time
+  constexpr int kLanes = D / 16;
   grid_release_next();
   const gdn_kv_cache& c = a.c;
   const int64_t units = a.tokens * c.kv_heads;
-  const int64_t unit0 = (int64_t)blockIdx.x * kSpan * kUnits + threadIdx.x / kLanes;
+  const int64_t unit = ((int64_t)blockIdx.x * kCopy + threadIdx.x) / kLanes;
   const int l = threadIdx.x % kLanes;
-  int64_t t[kUnits];
-  int h[kUnits];
-  uint4 x[kUnits][2];
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int64_t unit = unit0 + u * kSpan;
-    // (64-bit divisions were most of the kernel's instructions)
-    t[u] = unit >= units ? -1
-           : units >> 32 ? unit / c.kv_heads
-                         : (int64_t)((uint32_t)unit / (uint32_t)c.kv_heads);
-    h[u] = (int)(unit - t[u] * c.kv_heads);
-    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-    if (t[u] >= 0) {
-      x[u][0] = *reinterpret_cast<const uint4*>(a.k + t[u] * a.k_stride + h[u] * D + l * 8);
-      x[u][1] = *reinterpret_cast<const uint4*>(a.v + t[u] * a.v_stride + h[u] * D + l * 8);
-    }
+  const bool there = unit < units;
+  const int64_t t = units >> 32 ? unit / c.kv_heads : (int64_t)((uint32_t)unit / (uint32_t)c.kv_heads);
+  const int h = (int)(unit - t * c.kv_heads);
+  uint4 x[2][2] = {};
+  if (there) {
+    const uint4* k = reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + l * 16);
+    const uint4* v = reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + l * 16);
+    x[0][0] = k[0];
+    x[0][1] = k[1];
+    x[1][0] = v[0];
+    x[1][1] = v[1];
   }
-  // the tokens' rows and places
-  int64_t at[kUnits];   // first element of its head in the pool, -1: nowhere
-  int64_t seen = 0;     // the last row found: later tokens lie in it or behind it
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    at[u] = -1;
-    if (t[u] < 0) continue;
-    int64_t row = t[u], i = 0;
+  // the token's row and place
+  int64_t at = -1;   // first element of its head in the pool, -1: nowhere
+  if (there) {
+    int64_t row = t, i = 0;
     bool ok = true;
     if (a.cu) {
-      int64_t lo = seen, hi = c.rows - 1;   // last row with cu[row] <= t
-      if (a.cu[seen + 1] > t[u]) hi = seen;
+      int lo = 0, hi = c.rows - 1;   // last row with cu[row] <= t
       while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] <= t[u]) lo = mid; else hi = mid - 1;
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
       }
-      row = seen = lo;
-      i = t[u] - a.cu[lo];
-      ok = i >= 0 && t[u] < a.cu[lo + 1];
+      row = lo;
+      i = t - a.cu[lo];
+      ok = i >= 0 && t < a.cu[lo + 1];
       if (!ok) flag_status(a.status, GDN_ERR_BAD_SEQLENS);
     }
     const int64_t s = ok ? a.start[row] : -1;
@@ -223,8 +212,7 @@ __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
       int32_t p = -1;
       if (n < c.max_pages) p = c.table[row * c.max_pages + n];
       if (p >= 0 && p < c.pages)
-        at[u] = ((((int64_t)a.layer * c.pages + p) * c.kv_heads + h[u]) << a.page_log2) +
-                (pos & (c.page - 1));
+        at = ((((int64_t)a.layer * c.pages + p) * c.kv_heads + h) << a.page_log2) + (pos & (c.page - 1));
       else
         flag_status(a.status, GDN_ERR_BAD_CACHE);
     } else if (ok && s < -1) {
@@ -232,31 +220,36 @@ __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
     }
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u)
+  for (int i = 0; i < 2; ++i) {
+    void* pool = i ? c.v : c.k;
+    if constexpr (!kFp8) {
+      if (at >= 0) {
+        uint4* to = reinterpret_cast<uint4*>((__nv_bfloat16*)pool + at * D + l * 16);
+        to[0] = x[i][0];
+        to[1] = x[i][1];
+      }
+    } else {
+      float f[2][8];
+      float m = kTiny;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      void* pool = i ? c.v : c.k;
-      if constexpr (!kFp8) {
-        if (at[u] >= 0)
-          *reinterpret_cast<uint4*>((__nv_bfloat16*)pool + at[u] * D + l * 8) = x[u][i];
-      } else {
-        const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
-        float f[8];
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t w[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[2 * j] = __uint_as_float(w[j] << 16);
-          f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int k = 0; k < 4; ++k) {
+          f[j][2 * k] = __uint_as_float(w[k] << 16);
+          f[j][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
         }
-        float m = amax8(f);
+        m = max_nan(m, amax8(f[j]));
+      }
 #pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m = max_nan(m, kTiny);
-        if (at[u] >= 0) {
-          *reinterpret_cast<uint2*>((uint8_t*)pool + at[u] * D + l * 8) = quantise8_bf16(f, m);
-          if (l == 0) (i ? c.v_scale : c.k_scale)[at[u]] = scale_of(m);
-        }
+      for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (at >= 0) {
+        const uint2 q0 = quantise8_bf16(f[0], m), q1 = quantise8_bf16(f[1], m);
+        *reinterpret_cast<uint4*>((uint8_t*)pool + at * D + l * 16) = make_uint4(q0.x, q0.y, q1.x, q1.y);
+        if (l == 0) (i ? c.v_scale : c.k_scale)[at] = scale_of(m);
       }
     }
+  }
 }
 
 // --------------------------------------------------------------- freeing
@@ -309,7 +302,8 @@ __device__ __forceinline__ void copy_vectors(const uint4* src, uint4* dst, int64
 
 // --------------------------------------------------------------- forking
 struct Pair {
-  int32_t len, page;   // tokens of the row (-1: the pair is skipped), the new page or -1
+  int32_t len, page, old;   // tokens of the row (-1: the pair is skipped), the new page and the one
+                            // that it copies, or -1
 };
 
 // Which pairs are valid is decided by marking dst's length (0) with i - n < 0:
@@ -356,10 +350,11 @@ fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t
     const bool need = t > 0 && t % c.page != 0;
     if (i >= n) continue;
     if (t < 0) flag_status(status, GDN_ERR_BAD_CACHE);
-    Pair p = {t, -1};
+    Pair p = {t, -1, -1};
     if (need) {
       if (at < found) {
         p.page = list[at];
+        p.old = c.table[(int64_t)src[i] * c.max_pages + t / c.page];
         c.refs[p.page] = 1;
       } else {
         p.len = -2;   // no page: the mark is taken off below
@@ -386,7 +381,8 @@ fork_copy_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, const P
   grid_release_next();
   grid_wait();
   const int i = blockIdx.x;
-  const int32_t len = ld_waited(&plan[i].len), fresh = ld_waited(&plan[i].page);
+  const int32_t len = ld_waited(&plan[i].len), fresh = ld_waited(&plan[i].page),
+                old = ld_waited(&plan[i].old);
   if (len <= 0) return;
   const int32_t* from = c.table + (int64_t)src[i] * c.max_pages;
   const int32_t full = len / c.page, tail = len % c.page;
@@ -402,7 +398,6 @@ fork_copy_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, const P
     return;
   }
   if (!tail) return;
-  const int32_t old = ld_waited(from + full);
   if (old < 0 || old >= c.pages) {
     if (threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_CACHE);
     return;
@@ -578,17 +573,11 @@ int gdn_cache_append(const gdn_kv_cache* cache, int32_t layer, const void* k, co
   AppendArgs a = {c, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, start, cu_seqlens, tokens,
                   k_stride, v_stride, layer, kv::log2_of(c.page), status_ptr()};
   if (!a.status) return GDN_ERR_CUDA;
-  // four tokens a thread where that still fills the GPU (152 SMs x 8 CTAs)
-  const int64_t one = (tokens * c.kv_heads * (c.d / 8) + kCopy - 1) / kCopy;
-  const bool four = one >= 1216;
-  const int64_t ctas = four ? (one + 3) / 4 : one;
+  const int64_t ctas = (tokens * c.kv_heads * (c.d / 16) + kCopy - 1) / kCopy;
   if (ctas > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
   const bool fp8 = c.dtype == GDN_E4M3;
-  auto pick = [&](auto* k1, auto* k4) { return four ? k4 : k1; };
-  auto* kern = c.d == 128 ? (fp8 ? pick(append_kernel<128, true, 1>, append_kernel<128, true, 4>)
-                                 : pick(append_kernel<128, false, 1>, append_kernel<128, false, 4>))
-                          : (fp8 ? pick(append_kernel<64, true, 1>, append_kernel<64, true, 4>)
-                                 : pick(append_kernel<64, false, 1>, append_kernel<64, false, 4>));
+  auto* kern = c.d == 128 ? (fp8 ? append_kernel<128, true> : append_kernel<128, false>)
+                          : (fp8 ? append_kernel<64, true> : append_kernel<64, false>);
   count_launches(1);
   return launch(false, kern, dim3((unsigned)ctas), kCopy, 0, 0, (cudaStream_t)stream, a) ==
                  cudaSuccess
