@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const int g = lane >> 2, t4 = lane & 3;
     constexpr int kSteps = D / 16;
     constexpr int kTok = S::kTile / kWarps;   // a warp's tokens of a tile
+    constexpr int kGroups = kTok / 16;
     // 8 bits: a weight is the probability times the value's scale.  In powers of
     // two its exponent is the score's plus the scale's logarithm; with a running
     // maximum of its own, fp16 holds all weights that matter (the largest is
@@ -454,37 +455,40 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         fence_proxy_async_smem();
         __syncwarp();
       }
-#pragma unroll
-      for (int sub = 0; sub < kTok / 16; ++sub) {
-        const int tok0 = warp * kTok + sub * 16;
-        if (tok0 >= valid) break;
-        // scores of 16 heads and 16 tokens
-        float s[2][4] = {};
-        const int kr = tok0 + (lane >> 4) * 8 + (lane & 7);
+      const int tok0 = warp * kTok;
+      if (tok0 < valid) {
+        // scores of 16 heads and the warp's 16 or 32 tokens
+        float s[2 * kGroups][4] = {};
         if constexpr (!kFp8) {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            uint32_t b[4];
-            ldmatrix4(b, base + place<S::kSub, S::kTile>(kr, 2 * k + ((lane >> 3) & 1)));
-            mma16816<false>(s[0], qa[k], b[0], b[1]);
-            mma16816<false>(s[1], qa[k], b[2], b[3]);
-          }
+          for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+              uint32_t b[4];
+              ldmatrix4(b, base + place<S::kSub, S::kTile>(tok0 + 16 * i + (lane >> 4) * 8 + (lane & 7),
+                                                           2 * k + ((lane >> 3) & 1)));
+              mma16816<false>(s[2 * i], qa[k], b[0], b[1]);
+              mma16816<false>(s[2 * i + 1], qa[k], b[2], b[3]);
+            }
         } else {
 #pragma unroll
-          for (int k = 0; k < kSteps; k += 2) {
-            uint32_t b[4];
-            ldmatrix4(b, base + place<S::kSub, S::kTile>(kr, k + ((lane >> 3) & 1)));
+          for (int k = 0; k < kSteps; k += 2)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t b0, b1;
-              e4m3_to_half(b[x], b0, b1);
-              mma16816<true>(s[x >> 1], qa[k + (x & 1)], b0, b1);
+            for (int i = 0; i < kGroups; ++i) {
+              uint32_t b[4];
+              ldmatrix4(b, base + place<S::kSub, S::kTile>(tok0 + 16 * i + (lane >> 4) * 8 + (lane & 7),
+                                                           k + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t b0, b1;
+                e4m3_to_half(b[x], b0, b1);
+                mma16816<true>(s[2 * i + (x >> 1)], qa[k + (x & 1)], b0, b1);
+              }
             }
-          }
         }
-        float vs[2][2];
+        float vs[2 * kGroups][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 2 * kGroups; ++n) {
           const int col = tok0 + n * 8 + 2 * t4;
           const bool v0 = col < valid, v1 = col + 1 < valid;
           float k0 = 1.f, k1 = 1.f;
@@ -502,43 +506,44 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             s[n][2 * x + 1] = v1 ? s[n][2 * x + 1] * (kFp8 ? unit[x] * k1 : unit[x]) : -INFINITY;
           }
         }
-        // running maximum and sum of rows g and g + 8
-        float sub_m[2];
+        // running maximum and sum of rows g and g + 8; 8 bits: the weights' too, whose
+        // exponents are the scores' plus the scales' (behind the last token the
+        // scale may be anything)
+        float top[2][2];
         bool grew = false;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          sub_m[x] = fmaxf(m[x], mx);
-          grew |= sub_m[x] > m[x];
+          float mx = -INFINITY, mw = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2 * kGroups; ++n)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float v = s[n][2 * x + y];
+              mx = fmaxf(mx, v);
+              if constexpr (kFp8) mw = fmaxf(mw, v == -INFINITY ? -INFINITY : v + vs[n][y]);
+            }
+          top[x][0] = mx;
+          top[x][1] = mw;
         }
-        float u[2][4], sub_w[2];
-        if constexpr (kFp8) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)   // (behind the last token the scale may be anything)
-              u[n][x] = s[n][x] == -INFINITY ? -INFINITY : s[n][x] + vs[n][x & 1];
+        for (int d = 1; d < 4; d <<= 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mx = fmaxf(fmaxf(u[0][2 * x], u[0][2 * x + 1]), fmaxf(u[1][2 * x], u[1][2 * x + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            sub_w[x] = fmaxf(wm[x], mx);
-            grew |= sub_w[x] > wm[x];
+            top[x][0] = fmaxf(top[x][0], __shfl_xor_sync(0xffffffffu, top[x][0], d));
+            if constexpr (kFp8) top[x][1] = fmaxf(top[x][1], __shfl_xor_sync(0xffffffffu, top[x][1], d));
           }
-        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) grew |= top[x][0] > m[x] || (kFp8 && top[x][1] > wm[x]);
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float f = sub_m[x] > m[x] ? ex2_sfu(m[x] - sub_m[x]) : 1.f;
+            const float f = top[x][0] > m[x] ? ex2_sfu(m[x] - top[x][0]) : 1.f;
             float fo = f;
             l[x] *= f;
-            m[x] = sub_m[x];
+            m[x] = fmaxf(m[x], top[x][0]);
             if constexpr (kFp8) {
-              fo = sub_w[x] > wm[x] ? ex2_sfu(wm[x] - sub_w[x]) : 1.f;
-              wm[x] = sub_w[x];
+              fo = top[x][1] > wm[x] ? ex2_sfu(wm[x] - top[x][1]) : 1.f;
+              wm[x] = fmaxf(wm[x], top[x][1]);
             }
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
@@ -547,46 +552,53 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             }
           }
         }
-        uint32_t p[4];
+        uint32_t p[kGroups][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int x = 0; x < 2; ++x) {
+          const float z = m[x] == -INFINITY ? 0.f : m[x];
+          const float zw = !kFp8 || wm[x] == -INFINITY ? 0.f : kRoom - wm[x];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float z = m[x] == -INFINITY ? 0.f : m[x];
-            const float p0 = ex2_sfu(s[n][2 * x] - z), p1 = ex2_sfu(s[n][2 * x + 1] - z);
+          for (int n = 0; n < 2 * kGroups; ++n) {
+            const float s0 = s[n][2 * x], s1 = s[n][2 * x + 1];
+            const float p0 = ex2_sfu(s0 - z), p1 = ex2_sfu(s1 - z);
             l[x] += p0 + p1;
             if constexpr (kFp8) {
-              const float zw = wm[x] == -INFINITY ? 0.f : kRoom - wm[x];
-              p[2 * n + x] = pack_half(ex2_sfu(u[n][2 * x] + zw), ex2_sfu(u[n][2 * x + 1] + zw));
+              const float u0 = s0 == -INFINITY ? -INFINITY : s0 + vs[n][0];
+              const float u1 = s1 == -INFINITY ? -INFINITY : s1 + vs[n][1];
+              p[n >> 1][2 * (n & 1) + x] = pack_half(ex2_sfu(u0 + zw), ex2_sfu(u1 + zw));
             } else {
-              p[2 * n + x] = pack_bf16(p0, p1);
+              p[n >> 1][2 * (n & 1) + x] = pack_bf16(p0, p1);
             }
           }
+        }
         // out of 16 heads, the warp's tokens added
         const uint32_t vb = base + S::kPool;
-        const int vr = tok0 + ((lane >> 3) & 1) * 8 + (lane & 7);
-        if constexpr (!kFp8) {
 #pragma unroll
-          for (int j = 0; j < D / 8; j += 2) {
-            uint32_t b[4];
-            ldmatrix4t(b, vb + place<S::kSub, S::kTile>(vr, j + (lane >> 4)));
-            mma16816<false>(o[j], p, b[0], b[1]);
-            mma16816<false>(o[j + 1], p, b[2], b[3]);
-          }
-        } else {
-          // a transposed pair of codes is two columns: even ones to o[2j], odd to
-          // o[2j + 1], so that a lane ends with four consecutive columns of 16
+        for (int i = 0; i < kGroups; ++i) {
+          const int vr = tok0 + 16 * i + ((lane >> 3) & 1) * 8 + (lane & 7);
+          if constexpr (!kFp8) {
 #pragma unroll
-          for (int j = 0; j < D / 16; j += 2) {
-            uint32_t b[4];
-            ldmatrix4t(b, vb + place<S::kSub, S::kTile>(vr, j + (lane >> 4)));
+            for (int j = 0; j < D / 8; j += 2) {
+              uint32_t b[4];
+              ldmatrix4t(b, vb + place<S::kSub, S::kTile>(vr, j + (lane >> 4)));
+              mma16816<false>(o[j], p[i], b[0], b[1]);
+              mma16816<false>(o[j + 1], p[i], b[2], b[3]);
+            }
+          } else {
+            // a transposed pair of codes is two columns: even ones to o[2j], odd to
+            // o[2j + 1], so that a lane ends with four consecutive columns of 16
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t e0, d0, e1, d1;
-              e4m3_to_half(__byte_perm(b[2 * x], 0, 0x3120), e0, d0);
-              e4m3_to_half(__byte_perm(b[2 * x + 1], 0, 0x3120), e1, d1);
-              mma16816<true>(o[2 * (j + x)], p, e0, e1);
-              mma16816<true>(o[2 * (j + x) + 1], p, d0, d1);
+            for (int j = 0; j < D / 16; j += 2) {
+              uint32_t b[4];
+              ldmatrix4t(b, vb + place<S::kSub, S::kTile>(vr, j + (lane >> 4)));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t e0, d0, e1, d1;
+                e4m3_to_half(__byte_perm(b[2 * x], 0, 0x3120), e0, d0);
+                e4m3_to_half(__byte_perm(b[2 * x + 1], 0, 0x3120), e1, d1);
+                mma16816<true>(o[2 * (j + x)], p[i], e0, e1);
+                mma16816<true>(o[2 * (j + x) + 1], p[i], d0, d1);
+              }
             }
           }
         }
