@@ -221,3 +221,45 @@ def test_nothing_to_do(gdn_lib):
     out, lse = gdn.attention_prefill(q, k, v, cu([5]), cu([0]))
     assert (out == 0).all() and lse.isneginf().all()
     assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [300, 3000])
+def test_scores_of_minus_infinity(gdn_lib, n):
+    """Keys whose scores are -inf count for nothing, however many come before the first finite one."""
+    d, m = 128, n - 20
+    q = torch.ones(n, 2, d, device="cuda", dtype=BF16)
+    k = torch.full((n, 1, d), -10.0, device="cuda", dtype=BF16)
+    k[:m] = -float("inf")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    v = torch.randn(n, 1, d, generator=g, device="cuda").to(BF16)
+    out, lse = gdn_lib.attention_prefill(q, k, v)
+    assert lse[:m].isneginf().all() and (out[:m] == 0).all()
+    o, want = gdn_lib.attention_prefill(q[m:], k[m:], v[m:])
+    # (all finite scores are equal: the probabilities are 1, the sums' order apart)
+    assert (out[m:].float() - o.float()).abs().max() <= 2.0 ** -7 * v.abs().max()
+    assert (lse[m:] - want).abs().max() <= 2.0 ** -16 * (1 + want.abs().max())
+    assert gdn_lib.device_status() == 0
+
+
+def test_more_tiles_than_levels(gdn_lib):
+    """128 heads on one: tiles of two queries, more of them than the list tells apart."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    n, d = 5000, 64
+    q, k, v = (torch.randn(n, h, d, generator=g, device="cuda").to(BF16) for h in (128, 1, 1))
+    out, lse = gdn_lib.attention_prefill(q, k, v)
+    for a, b in ((0, 200), (2500, 2540), (n - 40, n)):
+        verify(q[a:b], k[:b], v[:b], out[a:b], lse[a:b], [b - a], [b])
+    assert gdn_lib.device_status() == 0
+
+
+def test_tensors_of_more_than_2_31_elements(gdn_lib):
+    g = torch.Generator(device="cuda").manual_seed(22)
+    H, d, lens = 64, 128, [64] * 4200 + [200]
+    T = sum(lens)
+    q, k, v = (torch.randn(T, H, d, generator=g, device="cuda", dtype=BF16) for _ in range(3))
+    c = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    out, lse = gdn_lib.attention_prefill(q, k, v, c)
+    assert q.numel() > 2 ** 31
+    for a, b in ((0, 64), (64 * 4100, 64 * 4101), (T - 200, T)):
+        verify(q[a:b], k[a:b], v[a:b], out[a:b], lse[a:b], [b - a], [b - a])
+    assert gdn_lib.device_status() == 0
