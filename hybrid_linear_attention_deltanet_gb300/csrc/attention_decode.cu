@@ -16,6 +16,11 @@
 // Where a (row, head) ends, the warps' sums are joined; one that is cut over
 // several CTAs is joined from their partial sums by a second kernel, in the order
 // of the CTAs.
+//
+// 20 query and 4 kv heads of 128: 256 rows of up to 8192 tokens 319 us (6.6 TB/s), in
+// 8 bits 209 (5.2; widening the codes); one row of 32768 tokens in 8 bits 17 us, of which
+// the bytes are 5.  Heads of 64 in 8 bits: 3.2 TB/s, a tile's 128 tokens of 64 bytes
+// being too little for the steps that follow one another in it.
 #include "attention_tc.cuh"
 #include "gdn_internal.cuh"
 #include "hostcheck.cuh"

@@ -235,3 +235,35 @@ def test_a_training_step_in_a_graph(gdn_lib):
         assert torch.equal(o, out) and torch.equal(s, lse)
         assert all(torch.equal(want[x], got[x]) for x in want)
     assert gdn.device_status() == 0
+
+
+def test_more_tiles_than_levels(gdn_lib):
+    """128 heads on one: tiles of a query, more of them than the list tells apart."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    n, d, H = 5000, 64, 128
+    q, k, v = (torch.randn(n, h, d, generator=g, device="cuda").to(BF16) for h in (H, 1, 1))
+    out, lse, dout, got = step(gdn_lib, q, k, v, None)
+    dk, dk_off, dv, dv_off = (torch.zeros(n, 1, d, device="cuda").double() for _ in range(4))
+    for h in range(H):
+        x = slice(h, h + 1)
+        (dq, tol), *kv = formula(q[:, x], k, v, out[:, x], lse[:, x], dout[:, x], d ** -0.5)
+        assert ((got["dq"][:, x].double() - dq).abs() <= tol).all(), h
+        for total, part in zip((dk, dk_off, dv, dv_off), (t for pair in kv for t in pair)):
+            total += part
+    assert ((got["dk"].double() - dk).abs() <= dk_off).all()
+    assert ((got["dv"].double() - dv).abs() <= dv_off).all()
+    assert gdn_lib.device_status() == 0
+
+
+def test_tensors_of_more_than_2_31_elements(gdn_lib):
+    g = torch.Generator(device="cuda").manual_seed(22)
+    H, d, lens = 64, 128, [64] * 4200 + [200]
+    T = sum(lens)
+    q, k, v, dout = (torch.randn(T, H, d, generator=g, device="cuda", dtype=BF16) for _ in range(4))
+    c = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    out, lse = gdn_lib.attention_prefill(q, k, v, c)
+    got = gdn_lib.attention_prefill_backward(q, k, v, out, lse, dout, c)
+    for a, b in ((0, 64), (64 * 4100, 64 * 4101), (T - 200, T)):
+        verify(q[a:b], k[a:b], v[a:b], out[a:b], lse[a:b], dout[a:b], {n: t[a:b] for n, t in got.items()},
+               [b - a], [b - a])
+    assert gdn_lib.device_status() == 0
