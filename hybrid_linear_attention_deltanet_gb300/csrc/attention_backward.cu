@@ -183,12 +183,10 @@ __device__ __forceinline__ void times_less(uint32_t& x0, uint32_t& x1, F2 d, uin
   x0 = __float_as_uint(y0);
   x1 = __float_as_uint(y1);
 }
-__device__ __forceinline__ void keep_columns(uint32_t (&x)[2][32], int lo, int hi) {
+__device__ __forceinline__ void keep_columns(uint32_t (&x)[32], int lo, int hi) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (32 * h + i < lo || 32 * h + i >= hi) x[h][i] = 0;
+  for (int i = 0; i < 32; ++i)
+    if (i < lo || i >= hi) x[i] = 0;
 }
 __device__ __forceinline__ void put_bf16(uint32_t at, const uint32_t (&x)[32]) {
   uint32_t p[16];
@@ -453,22 +451,24 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       ok = mbar_wait_warp_cycles(&b.s_full[0], (uint32_t)(i & 1), kWaitCycles);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[2][32];
+      // half of the columns at a time: one half's loads and stores pass while the
+      // other is computed
+      uint32_t s[2][32], g[2][32];
+      tmem_ld32(s_at, s[0]);
+      tmem_ld_wait_regs(s[0]);
+      tmem_ld32(s_at + 32, s[1]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) tmem_ld32(s_at + 32 * h, s[h]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(s[h]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (h) tmem_ld_wait_regs(s[1]);
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 l4 = *reinterpret_cast<const float4*>(st + 32 * h + x);
           exp_pair(s[h][x], s[h][x + 1], cc, f2(l4.x, l4.y));
           exp_pair(s[h][x + 2], s[h][x + 3], cc, f2(l4.z, l4.w));
         }
-      if (masked) keep_columns(s, lo, hi);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) put_bf16(s_at + 16 * h, s[h]);
+        if (masked) keep_columns(s[h], lo - 32 * h, hi - 32 * h);
+        put_bf16(s_at + 16 * h, s[h]);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -476,22 +476,21 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       ok = mbar_wait_warp_cycles(&b.dp_full, (uint32_t)(i & 1), kWaitCycles);
       if (!ok) break;
       tc_fence_after();
-      uint32_t g[2][32];
+      tmem_ld32(dp_at, g[0]);
+      tmem_ld_wait_regs(g[0]);
+      tmem_ld32(dp_at + 32, g[1]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) tmem_ld32(dp_at + 32 * h, g[h]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) tmem_ld_wait_regs(g[h]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (h) tmem_ld_wait_regs(g[1]);
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 d4 = *reinterpret_cast<const float4*>(st + 64 + 32 * h + x);
           times_less(g[h][x], g[h][x + 1], f2(d4.x, d4.y), s[h][x], s[h][x + 1]);
           times_less(g[h][x + 2], g[h][x + 3], f2(d4.z, d4.w), s[h][x + 2], s[h][x + 3]);
         }
-      if (masked) keep_columns(g, lo, hi);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) put_bf16(dp_at + 16 * h, g[h]);
+        if (masked) keep_columns(g[h], lo - 32 * h, hi - 32 * h);
+        put_bf16(dp_at + 16 * h, g[h]);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -696,7 +695,10 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
 #pragma unroll
         for (int x = 0; x < 32; x += 2)
           times_less(g[h][x], g[h][x + 1], dd, s[h][x], s[h][x + 1]);
-      if (masked) keep_columns(g, 0, see + 1);
+      if (masked) {
+        keep_columns(g[0], 0, see + 1);
+        keep_columns(g[1], 0, see - 31);
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) put_bf16(s_at + 16 * h, g[h]);
       tmem_st_wait();

@@ -64,7 +64,12 @@ struct Fwd {
   static constexpr uint32_t kTile = kHalves * kTileBytes;     // of Q, K or V
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kSmem = 2 * kTile + kStages * kTile + 1024;
-  static constexpr uint32_t kS = 0, kO = 256;                 // tensor-memory columns, + tile * 128
+  // Tensor-memory columns: scores, + tile * 128; probabilities and outputs.  Heads of
+  // 64 leave room for probabilities of their own: the next block's scores come as
+  // soon as this one's are in registers.
+  static constexpr bool kEarly = D == 64;
+  static constexpr uint32_t kS = 0, kP = kEarly ? 256 : 0, kPStep = kEarly ? 64 : 128;
+  static constexpr uint32_t kO = kEarly ? 384 : 256, kOStep = D;
 };
 
 // 128 rows x 64 columns a half, K-major: 16 columns a step
@@ -112,7 +117,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_smem_1024(smem_raw);
   __shared__ uint64_t q_full, q_empty, kv_full[C::kStages], kv_empty[C::kStages], s_full[2],
-      p_half[2], p_full[2], o_full[2], job_full[2], job_empty[2], turn[2];
+      p_half[2], p_full[2], o_full[2], job_full[2], job_empty[2], turn[2], s_free[2];
   __shared__ uint32_t tmem_base;
   __shared__ int64_t scratch[kMode == kListed ? 1 : kThreads + 6];
   __shared__ Seq slots[2];
@@ -133,6 +138,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&turn[i], 1);
+      mbar_init(&s_free[i], 4);
       mbar_init(&job_full[i], 1);
       mbar_init(&job_empty[i], 10);
     }
@@ -274,8 +280,10 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       const uint64_t qd = smem_desc(base + w * C::kTile, 16, 1024, kSwizzle128B);
       const uint64_t kd = smem_desc(base + 2 * C::kTile, 16, 1024, kSwizzle128B);
       const uint64_t vd = smem_desc(base + 2 * C::kTile, kTileBytes, 1024, kSwizzle128B);
-      const uint32_t s_at = tmem + C::kS + 128 * w, o_at = tmem + C::kO + 128 * w;
+      const uint32_t s_at = tmem + C::kS + 128 * w, o_at = tmem + C::kO + C::kOStep * w;
+      const uint32_t p_at = tmem + C::kP + C::kPStep * w;
       uint32_t kv = 0, jobs_done = 0, steps = 0, probs = 0;   // (probs: the tile's blocks so far)
+      uint32_t scored = 0;                                    // (scores of it so far)
       Seq seq;
       for (uint32_t n = 0; ok && take(n, seq); ++n) {
         int32_t most, blocks, last;      // last: keys of the last block
@@ -290,13 +298,14 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
         if (most == 0) continue;
         ok = mbar_wait_warp_cycles(&q_full, jobs_done & 1, kWaitCycles);
         ++jobs_done;
-        // step j: P V of block j - 1, then Q K^T of block j; a block's K is loaded
-        // one stage before its V
+        // step j: P V of block j - 1 and Q K^T of block j, in this order where their
+        // probabilities and scores share a place; a block's K is loaded one stage
+        // before its V
         for (int32_t j = 0; ok && j <= most; ++j, ++steps) {
           const uint32_t ki = kv + 2 * j, vi = kv + 2 * j - 1;
           const uint32_t k_st = ki % C::kStages, v_st = vi % C::kStages;
-          if (j > 0) {
-            ok = mbar_wait_warp_cycles(&kv_full[v_st], (vi / C::kStages) & 1, kWaitCycles);
+          auto values_there = [&] {
+            ok = ok && mbar_wait_warp_cycles(&kv_full[v_st], (vi / C::kStages) & 1, kWaitCycles);
             // values behind the sequence's last one are another's: a product
             // with a zero probability has to be zero
             if (ok && j == most && last < kRows) {
@@ -307,11 +316,13 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
               fence_proxy_async_smem();
               __syncwarp();
             }
-          }
-          if (j < most)
-            ok = ok && mbar_wait_warp_cycles(&kv_full[k_st], (ki / C::kStages) & 1, kWaitCycles);
-          ok = ok && mbar_wait_warp_cycles(&turn[w], (steps & 1) ^ (w ? 0u : 1u), kWaitCycles);
-          if (ok && j > 0 && j <= blocks) {
+          };
+          auto keys_there = [&] {
+            if (j < most)
+              ok = ok && mbar_wait_warp_cycles(&kv_full[k_st], (ki / C::kStages) & 1, kWaitCycles);
+          };
+          auto add_values = [&] {
+            if (!ok || j == 0 || j > blocks) return;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               ok = ok && mbar_wait_warp_cycles(half ? &p_full[w] : &p_half[w], probs & 1, kWaitCycles);
@@ -319,25 +330,48 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
               if (ok && lead)
 #pragma unroll
                 for (int s = 4 * half; s < 4 * half + 4; ++s)
-                  mma_bf16_ts(o_at, s_at + 8 * s, vd + (uint64_t)((v_st * C::kTile + s * 2048) >> 4),
+                  mma_bf16_ts(o_at, p_at + 8 * s, vd + (uint64_t)((v_st * C::kTile + s * 2048) >> 4),
                               kOut, j > 1 || s > 0);
             }
             ++probs;
-          }
-          if (ok && lead) {
-            if (j > 0 && j == blocks) mma_commit(&o_full[w]);
-            if (j < blocks) {
-              tc_fence_after();
+          };
+          auto score_keys = [&] {
+            if (!ok || !lead || j >= blocks) return;
+            tc_fence_after();
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s)
-                mma_bf16(s_at, qd + (uint64_t)(kstep(s) >> 4),
-                         kd + (uint64_t)((k_st * C::kTile + kstep(s)) >> 4), kScores, s > 0);
-              mma_commit(&s_full[w]);
+            for (int s = 0; s < D / 16; ++s)
+              mma_bf16(s_at, qd + (uint64_t)(kstep(s) >> 4),
+                       kd + (uint64_t)((k_st * C::kTile + kstep(s)) >> 4), kScores, s > 0);
+            mma_commit(&s_full[w]);
+          };
+          if constexpr (C::kEarly) {
+            keys_there();
+            if (ok && j < blocks) {
+              if (scored > 0) ok = mbar_wait_warp_cycles(&s_free[w], (scored - 1) & 1, kWaitCycles);
+              ++scored;
             }
-            mbar_arrive(&turn[w ^ 1]);
-            if (j > 0) mma_commit(&kv_empty[v_st]);
-            if (j < most) mma_commit(&kv_empty[k_st]);
-            if (j + 1 == most) mma_commit(&q_empty);
+            score_keys();
+            if (ok && lead && j < most) mma_commit(&kv_empty[k_st]);
+            if (ok && lead && j + 1 == most) mma_commit(&q_empty);
+            if (j > 0) values_there();
+            add_values();
+            if (ok && lead && j > 0) {
+              if (j <= blocks) mma_commit(&o_full[w]);
+              mma_commit(&kv_empty[v_st]);
+            }
+          } else {
+            if (j > 0) values_there();
+            keys_there();
+            ok = ok && mbar_wait_warp_cycles(&turn[w], (steps & 1) ^ (w ? 0u : 1u), kWaitCycles);
+            add_values();
+            if (ok && lead && j > 0 && j == blocks) mma_commit(&o_full[w]);
+            score_keys();
+            if (ok && lead) {
+              mbar_arrive(&turn[w ^ 1]);
+              if (j > 0) mma_commit(&kv_empty[v_st]);
+              if (j < most) mma_commit(&kv_empty[k_st]);
+              if (j + 1 == most) mma_commit(&q_empty);
+            }
           }
           __syncwarp();
         }
@@ -350,10 +384,11 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     const int w = warp >> 2;
     const int row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // 32 lanes, in the address's upper half
-    const uint32_t s_at = tmem + lanes + C::kS + 128 * w, o_at = tmem + lanes + C::kO + 128 * w;
+    const uint32_t s_at = tmem + lanes + C::kS + 128 * w, o_at = tmem + lanes + C::kO + C::kOStep * w;
+    const uint32_t p_at = tmem + lanes + C::kP + C::kPStep * w;
     const int qi = row / sq.group;                         // the row's query in its tile
     const float c = a.c;
-    uint32_t scores = 0, outs = 0;                         // blocks and jobs of this tile so far
+    uint32_t scores = 0, outs = 0;       // blocks of this tile so far, and outputs waited for
     Seq seq;
     for (uint32_t job = 0; ok && take(job, seq); ++job) {
       int32_t n, first, begin;
@@ -373,6 +408,11 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
         for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_wait_regs(s[i]);
+        if constexpr (C::kEarly) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[w]);
+        }
         // keys that the tile's first row does not see are in the block?
         const int32_t k0 = (begin + j) * kRows;
         if (k0 + kRows - 1 > first) {
@@ -393,10 +433,16 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
           mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (C::kEarly && j > 0) {
+          // the last block's product is done with its probabilities' place, and O at rest
+          ok = mbar_wait_warp_cycles(&o_full[w], outs++ & 1, kWaitCycles);
+          if (!ok) break;
+          tc_fence_after();
+        }
         if (j == 0) {
           m = fmaxf(top, kLowest);   // (all -inf: the first finite score replaces it)
         } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
-          // (the scores' commit covers the products before them: O is at rest)
+          // (one place for both: the scores' commit covers the products before them)
           // a row's bits depend on no other row of its warp: the others get a factor of 1
           const bool grows = top > m + kGrow;
           const float f = grows ? ex2_sfu(m - top) : 1.f;
@@ -427,7 +473,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
             sum[x & 1] = f2_add(sum[x & 1], f2(lo, hi));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[x]) : "f"(hi), "f"(lo));
           }
-          tmem_st16(s_at + 16 * i, p);
+          tmem_st16(p_at + 16 * i, p);
           if (i & 1) {
             tmem_st_wait();
             tc_fence_before();
