@@ -17,8 +17,13 @@
 // from, and are the A operand there.
 //
 // 16 query and 4 kv heads of 128: 2 x 8192 tokens 1125 us (580 and 509 in the two
-// kernels, the tensor pipe 82% and 70% busy), 8192 547, 4096 179; one kernel that
-// adds dQ in memory would save two products in seven, but not keep the sums' order.
+// kernels), 8192 550, 4096 179; heads of 64: 2 x 8192 864.  What holds the products
+// back is shared memory: S and dP read two operands of 4 KB per 64 cycles, all that
+// it gives, the tiles come in through it, and so do the keys' kernel's statistics.
+// Tried and slower (8192 tokens): in the queries' kernel dP(j + 1) as soon as dP(j) is in
+// registers 580, Q and dO in tensor memory with one buffer of scores 610, the next
+// scores in registers before dS is reported 606.  One kernel that adds dQ in memory
+// would save two products in seven, but not keep the sums' order.
 #include "attention_tc.cuh"
 
 namespace gdn {
@@ -452,7 +457,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       if (!ok) break;
       tc_fence_after();
       // half of the columns at a time: one half's loads and stores pass while the
-      // other is computed
+      // other is computed (2 x 8192 tokens, heads of 64: 946 -> 864 us; of 128 the same)
       uint32_t s[2][32], g[2][32];
       tmem_ld32(s_at, s[0]);
       tmem_ld_wait_regs(s[0]);

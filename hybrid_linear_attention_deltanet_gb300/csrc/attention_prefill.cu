@@ -17,10 +17,11 @@
 // came from, and are the A operand of the second product there.
 //
 // 16 query and 4 kv heads of 128: 4 x 8192 tokens 620 us (1774 TFLOP/s), 8192
-// 162 us, 1024 21 us; heads of 64, whose products are half as long as their
-// exponentials: 2 x 8192 tokens 280 us (980 TFLOP/s).  Tried and slower: a pair of CTAs
-// on one tile of keys (979 us), four warpgroups of exponentials (fewer registers
-// a row than its scores).
+// 162 us, 1024 20 us; heads of 64, whose exponentials take as long as their products:
+// 2 x 8192 tokens 251 us (1090 TFLOP/s; 258 with the probabilities over the scores).
+// Tried and slower: a pair of CTAs on one tile of keys (979 us where one CTA with one
+// multiplying warp took 736), four warpgroups of exponentials (fewer registers than a
+// row's scores).
 #include "attention_tc.cuh"
 
 namespace gdn {
