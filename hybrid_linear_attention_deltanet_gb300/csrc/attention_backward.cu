@@ -193,11 +193,20 @@ __device__ __forceinline__ void keep_columns(uint32_t (&x)[32], int lo, int hi) 
   for (int i = 0; i < 32; ++i)
     if (i < lo || i >= hi) x[i] = 0;
 }
+// (In two terms: what the rounding leaves, rounded, 32 columns further.)
+template <bool kTwo>
 __device__ __forceinline__ void put_bf16(uint32_t at, const uint32_t (&x)[32]) {
   uint32_t p[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
   tmem_st16(at, p);
+  if constexpr (kTwo) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      p[i] = pack(__uint_as_float(x[2 * i]) - __uint_as_float(p[i] << 16),
+                  __uint_as_float(x[2 * i + 1]) - __uint_as_float(p[i] & 0xffff0000u));
+    tmem_st16(at + 32, p);
+  }
 }
 
 // A row's statistic as it stands in L2 (the queries' kernel may start beside the
@@ -280,7 +289,8 @@ __device__ __forceinline__ void finish(bool ok, uint32_t tmem, unsigned* status)
 // A tile of 128 keys of a kv head: dK and dV.  Rows of all products are keys,
 // so P^T and dS^T are A operands as they come; a column is a packed query row,
 // whose statistics are read from shared memory.
-template <int D>
+// kTwo: P and dS as two bf16 terms each.
+template <int D, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
 keys_kernel(const __grid_constant__ BwdArgs a) {
   using C = Bwd<D>;
@@ -401,6 +411,11 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
             for (int s = 0; s < 8; ++s)
               mma_bf16_ts(g_at, s_at + (s >> 2) * 64 + (s & 3) * 8,
                           gd + (uint64_t)((g_slot * C::kTile + s * 2048) >> 4), kGrad, i > 1 || s > 0);
+            if (kTwo)
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                mma_bf16_ts(g_at, s_at + 32 + (s >> 2) * 64 + (s & 3) * 8,
+                            gd + (uint64_t)((g_slot * C::kTile + s * 2048) >> 4), kGrad, 1);
             if (w) mma_commit(&b.a_empty[ga]);
             else mma_commit(&b.b_empty[gb]);
           }
@@ -462,6 +477,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       tmem_ld32(s_at, s[0]);
       tmem_ld_wait_regs(s[0]);
       tmem_ld32(s_at + 32, s[1]);
+      if (kTwo) tmem_ld_wait_regs(s[1]);   // (its place is written with the first half)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h) tmem_ld_wait_regs(s[1]);
@@ -472,7 +488,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
           exp_pair(s[h][x + 2], s[h][x + 3], cc, f2(l4.z, l4.w));
         }
         if (masked) keep_columns(s[h], lo - 32 * h, hi - 32 * h);
-        put_bf16(s_at + 16 * h, s[h]);
+        put_bf16<kTwo>(s_at + 16 * h, s[h]);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -484,6 +500,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       tmem_ld32(dp_at, g[0]);
       tmem_ld_wait_regs(g[0]);
       tmem_ld32(dp_at + 32, g[1]);
+      if (kTwo) tmem_ld_wait_regs(g[1]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h) tmem_ld_wait_regs(g[1]);
@@ -494,7 +511,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
           times_less(g[h][x + 2], g[h][x + 3], f2(d4.z, d4.w), s[h][x + 2], s[h][x + 3]);
         }
         if (masked) keep_columns(g[h], lo - 32 * h, hi - 32 * h);
-        put_bf16(dp_at + 16 * h, g[h]);
+        put_bf16<kTwo>(dp_at + 16 * h, g[h]);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -520,7 +537,7 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
 }
 
 // A tile of packed query rows: dQ.
-template <int D>
+template <int D, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
 queries_kernel(const __grid_constant__ BwdArgs a) {
   using C = Bwd<D>;
@@ -631,6 +648,11 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
               for (int s = 0; s < 8; ++s)
                 mma_bf16_ts(tmem + kDQ, tmem + kS + 128 * (j & 1) + (s >> 2) * 64 + (s & 3) * 8,
                             an + (uint64_t)((ga * C::kTile + s * 2048) >> 4), kGrad, j > 2 || s > 0);
+              if (kTwo)
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                  mma_bf16_ts(tmem + kDQ, tmem + kS + 32 + 128 * (j & 1) + (s >> 2) * 64 + (s & 3) * 8,
+                              an + (uint64_t)((ga * C::kTile + s * 2048) >> 4), kGrad, 1);
               mma_commit(&b.a_empty[ga]);
               if (j == n + 1) mma_commit(&b.done);
             }
@@ -705,7 +727,7 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
         keep_columns(g[1], 0, see - 31);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) put_bf16(s_at + 16 * h, g[h]);
+      for (int h = 0; h < 2; ++h) put_bf16<kTwo>(s_at + 16 * h, g[h]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -772,6 +794,13 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ B
                                                pack(sum[4] * f, sum[5] * f), pack(sum[6] * f, sum[7] * f));
   }
 }
+
+// Fewer rows than this: P and dS enter their products as two bf16 terms each.  Their
+// rounding to one is as large as that of the results, which makes the error 1.43 times
+// that (1.47 at most in 200 batches of 700 to 12000 rows); over few rows it can be more
+// than 1.5 times, and there the products are not what takes the time (16/4 heads of 128,
+// 17 tokens behind 1183: 17.4 us with one term, 21.5 with two; 300 tokens 25 and 30).
+constexpr int64_t kTwoTerms = 4096;
 
 // How a call is launched, and its scratch.
 struct Plan {
@@ -928,14 +957,16 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
                  0, st, a);
     count_launches(1);
   };
-  static std::atomic<uint64_t> on[4];
-  if (s.d == 128) {
-    run(Bwd<128>{}, keys_kernel<128>, plan.key_tiles, plan.parts, on[0]);
-    run(Bwd<128>{}, queries_kernel<128>, plan.query_tiles, plan.q_parts, on[1]);
-  } else {
-    run(Bwd<64>{}, keys_kernel<64>, plan.key_tiles, plan.parts, on[2]);
-    run(Bwd<64>{}, queries_kernel<64>, plan.query_tiles, plan.q_parts, on[3]);
-  }
+  static std::atomic<uint64_t> on[8];
+  auto both = [&](auto shape, auto keys, auto queries, int i) {
+    run(shape, keys, plan.key_tiles, plan.parts, on[i]);
+    run(shape, queries, plan.query_tiles, plan.q_parts, on[i + 1]);
+  };
+  const bool two = (int64_t)s.rows() < kTwoTerms;
+  if (s.d == 128 && two) both(Bwd<128>{}, keys_kernel<128, true>, queries_kernel<128, true>, 0);
+  else if (s.d == 128) both(Bwd<128>{}, keys_kernel<128, false>, queries_kernel<128, false>, 2);
+  else if (two) both(Bwd<64>{}, keys_kernel<64, true>, queries_kernel<64, true>, 4);
+  else both(Bwd<64>{}, keys_kernel<64, false>, queries_kernel<64, false>, 6);
   auto join = [&](bool on_, auto kern, int64_t tiles) {
     if (!on_ || e != cudaSuccess) return;
     e = launch(true, kern, dim3((unsigned)(tiles * s.kv_heads), 4), kThreads, 0, 0, st, a);

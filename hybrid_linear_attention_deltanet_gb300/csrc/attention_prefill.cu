@@ -33,7 +33,11 @@ using namespace sm100;
 // two warpgroups of softmax; a third with a warp to multiply and one to load
 constexpr int kThreads = 384;
 constexpr uint32_t kTileBytes = 16384;   // 128 rows x 64 columns bf16
-constexpr float kGrow = 8.f;         // a row's probabilities stay below 2^8
+// A row's maximum is replaced where it grows by more than 2^8.  With few rows (below
+// kFewRows) wherever it grows, so that the largest probability is 1, which bf16 holds:
+// over many rows the largest ones' roundings average, over a few they do not.
+constexpr float kGrow = 8.f;
+constexpr int64_t kFewRows = 512;
 constexpr float kLowest = -3.402823466e38f;
 
 struct FwdArgs {
@@ -42,6 +46,7 @@ struct FwdArgs {
   __nv_bfloat16* out;
   float* lse;
   float c;                 // scale log2 e
+  float grow;
   int32_t q_heads, per;    // per: queries of a 128-row tile
   // kListed: the jobs
   const int32_t* count;
@@ -442,10 +447,10 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
         }
         if (j == 0) {
           m = fmaxf(top, kLowest);   // (all -inf: the first finite score replaces it)
-        } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+        } else if (__any_sync(0xffffffffu, top > m + a.grow)) {
           // (one place for both: the scores' commit covers the products before them)
           // a row's bits depend on no other row of its warp: the others get a factor of 1
-          const bool grows = top > m + kGrow;
+          const bool grows = top > m + a.grow;
           const float f = grows ? ex2_sfu(m - top) : 1.f;
           l *= f;
           m = grows ? top : m;
@@ -587,14 +592,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
       ml[p][lane] = make_float2(ld_waited(from), ld_waited(from + 1));
     }
   }
-  __syncthreads();
-  if (r < 0) return;
-  float top = -INFINITY;
-  for (int p = 0; p < a.parts; ++p) top = ml[p][lane].y == 0.f ? top : fmaxf(top, ml[p][lane].x);
-  float all = 0.f, acc[kV][4] = {};
-  bool some = false;
-  for (int p0 = 0; p0 < a.parts; p0 += 4) {
-    float4 x[4][kV];
+  // (the first four parts' sums are on their way while the statistics arrive)
+  float4 x[4][kV];
+  auto read = [&](int p0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -602,6 +602,16 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
         const int p = p0 + i < a.parts ? p0 + i : p0;
         x[i][v] = ld_waited(reinterpret_cast<const float4*>(o + (int64_t)p * 256 * D + v * 1024));
       }
+  };
+  read(0);
+  __syncthreads();
+  if (r < 0) return;
+  float top = -INFINITY;
+  for (int p = 0; p < a.parts; ++p) top = ml[p][lane].y == 0.f ? top : fmaxf(top, ml[p][lane].x);
+  float all = 0.f, acc[kV][4] = {};
+  bool some = false;
+  for (int p0 = 0; p0 < a.parts; p0 += 4) {
+    if (p0) read(p0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (p0 + i >= a.parts) break;
@@ -673,6 +683,7 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   a.out = (__nv_bfloat16*)out;
   a.lse = lse;
   a.c = scale * kLog2e;
+  a.grow = (int64_t)s.rows() < kFewRows ? 0.f : kGrow;
   a.q_heads = s.q_heads;
   a.per = kRows / group;
   const void* kk = tk ? k : q;   // (no keys: nothing is loaded through these)

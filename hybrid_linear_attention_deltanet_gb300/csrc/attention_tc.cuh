@@ -58,6 +58,35 @@ __device__ bool locate(const Seqs& s, int64_t job, int per, bool keys, bool down
     return true;
   }
   const int tid = threadIdx.x;
+  if (s.n <= 32) {
+    // a lane for each sequence, in every warp: no barriers
+    const int lane = tid & 31;
+    const bool mine = lane < s.n;
+    const int32_t a = mine ? s.cu_q[lane] : 0, b = mine ? s.cu_k[lane] : 0;
+    const int32_t lq = mine ? s.cu_q[lane + 1] - a : 0, lk = mine ? s.cu_k[lane + 1] - b : 0;
+    bool bad = a < 0 || b < 0 || lq < 0 || lk < 0 || (lane == 0 && (a != 0 || b != 0)) ||
+               (lane == s.n - 1 && (a + (int64_t)lq != s.len_q || b + (int64_t)lk != s.len_k));
+    if (__any_sync(0xffffffffu, bad)) {
+      if (tid == 0 && blockIdx.x == 0) flag_status(status, GDN_ERR_BAD_SEQLENS);
+      return false;
+    }
+    const int64_t t = ((int64_t)(keys ? lk : lq) + per - 1) / per;
+    int64_t end = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, job < end);
+    if (!here) return false;
+    const int l = __ffs(here) - 1;
+    const int64_t at = job - (__shfl_sync(0xffffffffu, end, l) - __shfl_sync(0xffffffffu, t, l));
+    const int64_t of = __shfl_sync(0xffffffffu, t, l);
+    out = {__shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l),
+           __shfl_sync(0xffffffffu, lq, l), __shfl_sync(0xffffffffu, lk, l),
+           (int32_t)(down ? of - 1 - at : at)};
+    return true;
+  }
   const int64_t chunk = ((int64_t)s.n + kThreads - 1) / kThreads;
   const int64_t i0 = tid * chunk, i1 = i0 + chunk < s.n ? i0 + chunk : s.n;
   int64_t mine = 0;

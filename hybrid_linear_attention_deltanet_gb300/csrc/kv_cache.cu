@@ -56,20 +56,25 @@ __device__ __forceinline__ int64_t scan(int64_t x, ScanMem& sm, int64_t& total) 
   return (warp ? sm.warp[warp - 1] : 0) + y - x;
 }
 
+// The reference counts of pages [p, p + 4), 1 behind the last.
+__device__ __forceinline__ int4 counts_at(const int32_t* refs, int32_t pages, int64_t p) {
+  if (p + 4 <= pages) return *reinterpret_cast<const int4*>(refs + p);
+  int4 r = make_int4(1, 1, 1, 1);
+  if (p < pages) r.x = refs[p];
+  if (p + 1 < pages) r.y = refs[p + 1];
+  if (p + 2 < pages) r.z = refs[p + 2];
+  return r;
+}
 // The first `want` free pages to list, in order; how many there are (at most want).
+// `near` are this thread's counts of the first step, read while the CTA found out
+// what it wants.
 __device__ int64_t find_free(const int32_t* refs, int32_t pages, int64_t want, int32_t* list,
-                             ScanMem& sm) {
+                             int4 near, ScanMem& sm) {
   int64_t found = 0;
   for (int64_t base = 0; base < pages && found < want; base += 4 * kPlan) {
     const int64_t p = base + 4 * (int64_t)threadIdx.x;
-    int32_t r[4] = {1, 1, 1, 1};
-    if (p + 4 <= pages) {
-      const int4 t = *reinterpret_cast<const int4*>(refs + p);
-      r[0] = t.x; r[1] = t.y; r[2] = t.z; r[3] = t.w;
-    } else {
-      for (int i = 0; i < 4; ++i)
-        if (p + i < pages) r[i] = refs[p + i];
-    }
+    const int4 t = base == 0 ? near : counts_at(refs, pages, p);
+    const int32_t r[4] = {t.x, t.y, t.z, t.w};
     int n = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) n += r[i] == 0;
@@ -86,15 +91,18 @@ __device__ int64_t find_free(const int32_t* refs, int32_t pages, int64_t want, i
   __syncthreads();   // the list is there for the CTA
   return found < want ? found : want;
 }
+constexpr int kNear = 2048;   // pages whose list stays in shared memory
 
 // ------------------------------------------------------------- reserving
 __global__ void __launch_bounds__(kPlan)
 reserve_kernel(gdn_kv_cache c, const int32_t* counts, int32_t* start, int32_t* list,
                unsigned* status) {
   __shared__ ScanMem sm;
+  __shared__ int32_t near_list[kNear];
   const int lane = threadIdx.x & 31;
   grid_release_next();
   grid_wait();
+  const int4 near = counts_at(c.refs, c.pages, 4 * (int64_t)threadIdx.x);
   // pages a row holds and will hold; what is asked of it in bad: 1 out of range, 2 no room
   auto ask = [&](int row, int64_t& old, int64_t& now, int64_t& len) {
     if (row >= c.rows) {
@@ -122,7 +130,8 @@ reserve_kernel(gdn_kv_cache c, const int32_t* counts, int32_t* start, int32_t* l
     want += step;
   }
   if (want > c.pages) want = c.pages;
-  const int64_t found = want ? find_free(c.refs, c.pages, want, list, sm) : 0;
+  if (want <= kNear) list = near_list;
+  const int64_t found = want ? find_free(c.refs, c.pages, want, list, near, sm) : 0;
   int64_t before = 0;
   for (int base = 0; base < c.rows; base += kPlan) {
     const int row = base + threadIdx.x;
@@ -301,8 +310,9 @@ __device__ __forceinline__ void copy_vectors(const uint4* src, uint4* dst, int64
 }
 
 // --------------------------------------------------------------- forking
+constexpr int32_t kNoSource = -3;
 struct Pair {
-  int32_t len, page, old;   // tokens of the row (-1: the pair is skipped), the new page and the one
+  int32_t len, page, old;   // tokens of the row (negative: the pair is skipped), the new page and the one
                             // that it copies, or -1
 };
 
@@ -312,38 +322,46 @@ __global__ void __launch_bounds__(kPlan)
 fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t n, Pair* plan,
                  int32_t* list, unsigned* status) {
   __shared__ ScanMem sm;
+  __shared__ int32_t near_list[kNear];
   grid_release_next();
   grid_wait();
+  const int4 near = counts_at(c.refs, c.pages, 4 * (int64_t)threadIdx.x);
   for (int i = threadIdx.x; i < n; i += kPlan) {
     const int32_t s = src[i], d = dst[i];
     const bool in = s >= 0 && s < c.rows && d >= 0 && d < c.rows;
     // (others mark at the same time: their marks are negative)
-    if (in && atomicAdd(c.lengths + d, 0) <= 0) atomicMin(c.lengths + d, i - n);
+    if (in && __ldcg(c.lengths + d) <= 0) atomicMin(c.lengths + d, i - n);
   }
   __syncthreads();
-  // a pair's tokens, -1 where it is skipped
-  auto tokens = [&](int i) {
+  // a pair's tokens, -1 where it is skipped, kNoSource where it has marked dst all the
+  // same; and the page that it copies, or -1
+  auto tokens = [&](int i, int32_t& old) {
+    old = -1;
     if (i >= n) return -1;
     const int32_t s = src[i], d = dst[i];
     if (s < 0 || s >= c.rows || d < 0 || d >= c.rows) return -1;
-    if (__ldcg(c.lengths + d) != i - n) return -1;
-    const int32_t t = __ldcg(c.lengths + s);
-    return t <= 0 ? 0 : t > c.max_pages * c.page ? -1 : t;
+    const int32_t mark = __ldcg(c.lengths + d), t = __ldcg(c.lengths + s);
+    if (mark != i - n) return -1;
+    if (t > c.max_pages * c.page) return kNoSource;
+    if (t <= 0) return 0;
+    if (t % c.page) old = c.table[(int64_t)s * c.max_pages + t / c.page];
+    return t;
   };
   int64_t want = 0, step, at = 0;
-  int32_t t = 0;
+  int32_t t = 0, old = -1;
   const bool one = n <= kPlan;   // then what the first round found is kept
   for (int base = 0; base < n; base += kPlan) {
-    t = tokens(base + threadIdx.x);
+    t = tokens(base + threadIdx.x, old);
     at = scan(t > 0 && t % c.page != 0, sm, step);
     want += step;
   }
-  const int64_t found = want ? find_free(c.refs, c.pages, want, list, sm) : 0;
+  if (want <= kNear) list = near_list;
+  const int64_t found = want ? find_free(c.refs, c.pages, want, list, near, sm) : 0;
   int64_t before = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + threadIdx.x;
     if (!one) {
-      t = tokens(i);
+      t = tokens(i, old);
       at = before + scan(t > 0 && t % c.page != 0, sm, step);
       before += step;
     }
@@ -354,17 +372,19 @@ fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t
     if (need) {
       if (at < found) {
         p.page = list[at];
-        p.old = c.table[(int64_t)src[i] * c.max_pages + t / c.page];
+        p.old = old;
         c.refs[p.page] = 1;
       } else {
-        p.len = -2;   // no page: the mark is taken off below
+        p.len = -2;   // no page: the mark is taken off
         flag_status(status, GDN_ERR_CACHE_FULL);
       }
     }
     plan[i] = p;
+    // the marks become lengths, once no thread reads any more
+    if (one && t != -1) c.lengths[dst[i]] = p.len > 0 ? p.len : 0;
   }
+  if (one) return;
   __syncthreads();
-  // the marks become lengths
   for (int i = threadIdx.x; i < n; i += kPlan) {
     const Pair p = plan[i];
     const int32_t d = dst[i];

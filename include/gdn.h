@@ -650,7 +650,8 @@ int gdn_attention_prefill(const void* q, const void* k, const void* v, const int
  *
  * out, dout and dq [T_q, q_heads, d], dk and dv [T_k, kv_heads, d], bf16 and
  * contiguous; q, k, v with strides as above; the rest as above.  P and dS
- * enter the products rounded to bf16, all sums are fp32 and their order is
+ * enter the products rounded to bf16 (as two bf16 terms each where there are
+ * fewer than 4096 rows T_q * q_heads), all sums are fp32 and their order is
  * fixed.  What is not finite reaches, besides the gradients that it belongs
  * to, those of its own sequence whose 128-row tiles meet its tile.  No output
  * may overlap an input or another output.  Scratch (8 bytes

@@ -198,6 +198,20 @@ def test_fork_skips_what_it_cannot_do(gdn_lib, n):
         assert torch.equal(bits(old), bits(t))
 
 
+@pytest.mark.parametrize("n", [4, 1030])
+def test_fork_of_a_row_with_a_bad_length(gdn_lib, n):
+    """The pair is skipped and its target stays empty; the others are made."""
+    gdn = gdn_lib
+    cache = gdn.kv_cache(1, 8 + n, 1, 2 + n, 3, 16, 64)
+    gdn.cache_reserve(cache, ints([20, 20] + [0] * n))
+    cache.lengths[1] = 3 * 16 + 1
+    src = [i % 2 for i in range(n)]
+    gdn.cache_fork(cache, ints(src), ints(list(range(2, 2 + n))))
+    assert gdn.device_status() == BAD
+    assert cache.lengths[2:].tolist() == [0 if i else 20 for i in src]
+    assert ((cache.table[2:, 0] >= 0).long().tolist() == [1 - i for i in src])
+
+
 def test_fork_without_a_page_left(gdn_lib):
     gdn = gdn_lib
     model = Model(5, 3, 4, 16)
