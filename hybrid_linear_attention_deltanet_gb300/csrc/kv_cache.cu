@@ -8,10 +8,14 @@
 // step is one load, two warp scans and two barriers, about 1 us), that ends as
 // soon as it has found enough.  The kernels are short and come in chains (free,
 // reserve; free, fork), so they are programmatic dependents: each waits for the
-// one before it first, but is on the GPU by then.  (append_kernel is not: a
-// decoding step's is over before the attribute has cost the host its 1.5 us.)
-// Copies are split over the GPU, 64 KB a CTA, 16
-// bytes a lane; they are bound by HBM.
+// one before it first, but is on the GPU by then.  (append_kernel for
+// single tokens is not: it is over before the attribute has cost the host its 1.5 us.)
+// Copies are split over the GPU, 64 KB a CTA, 16 bytes a lane; they are bound by HBM.
+//
+// (free, reserve and append of 4 prompts of up to 8192 tokens into 8 bits, 4 kv heads of
+// 128: 12.9 us, of which 7 are the append's 37 MB; 256 tokens' append 2.7; free and fork
+// of 3 rows 10.5, of 72 16.5, 7 layers; compacting 256 pages of 8 bits 8.6, 922 pages of
+// 7 layers 245.)
 #include "fp8_codes.cuh"
 #include "gdn_internal.cuh"
 #include "hostcheck.cuh"
@@ -183,6 +187,7 @@ template <int D, bool kFp8>
 __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 16;
   grid_release_next();
+  grid_wait();
   const gdn_kv_cache& c = a.c;
   const int64_t units = a.tokens * c.kv_heads;
   const int64_t unit = ((int64_t)blockIdx.x * kCopy + threadIdx.x) / kLanes;
@@ -194,10 +199,10 @@ __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
   if (there) {
     const uint4* k = reinterpret_cast<const uint4*>(a.k + t * a.k_stride + h * D + l * 16);
     const uint4* v = reinterpret_cast<const uint4*>(a.v + t * a.v_stride + h * D + l * 16);
-    x[0][0] = k[0];
-    x[0][1] = k[1];
-    x[1][0] = v[0];
-    x[1][1] = v[1];
+    x[0][0] = ld_waited(k);
+    x[0][1] = ld_waited(k + 1);
+    x[1][0] = ld_waited(v);
+    x[1][1] = ld_waited(v + 1);
   }
   // the token's row and place
   int64_t at = -1;   // first element of its head in the pool, -1: nowhere
@@ -208,18 +213,19 @@ __global__ void __launch_bounds__(kCopy) append_kernel(AppendArgs a) {
       int lo = 0, hi = c.rows - 1;   // last row with cu[row] <= t
       while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
-        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+        if (ld_waited(a.cu + mid) <= t) lo = mid; else hi = mid - 1;
       }
       row = lo;
-      i = t - a.cu[lo];
-      ok = i >= 0 && t < a.cu[lo + 1];
+      i = t - ld_waited(a.cu + lo);
+      ok = i >= 0 && t < ld_waited(a.cu + lo + 1);
       if (!ok) flag_status(a.status, GDN_ERR_BAD_SEQLENS);
     }
-    const int64_t s = ok ? a.start[row] : -1;
-    if (ok && s >= 0 && s + i < c.lengths[row]) {
+    const int64_t s = ok ? ld_waited(a.start + row) : -1;
+    const int64_t len = ok ? ld_waited(c.lengths + row) : 0;
+    if (ok && s >= 0 && s + i < len) {
       const int64_t pos = s + i, n = pos >> a.page_log2;
       int32_t p = -1;
-      if (n < c.max_pages) p = c.table[row * c.max_pages + n];
+      if (n < c.max_pages) p = ld_waited(c.table + row * c.max_pages + n);
       if (p >= 0 && p < c.pages)
         at = ((((int64_t)a.layer * c.pages + p) * c.kv_heads + h) << a.page_log2) + (pos & (c.page - 1));
       else
@@ -599,7 +605,7 @@ int gdn_cache_append(const gdn_kv_cache* cache, int32_t layer, const void* k, co
   auto* kern = c.d == 128 ? (fp8 ? append_kernel<128, true> : append_kernel<128, false>)
                           : (fp8 ? append_kernel<64, true> : append_kernel<64, false>);
   count_launches(1);
-  return launch(false, kern, dim3((unsigned)ctas), kCopy, 0, 0, (cudaStream_t)stream, a) ==
+  return launch(cu_seqlens != nullptr, kern, dim3((unsigned)ctas), kCopy, 0, 0, (cudaStream_t)stream, a) ==
                  cudaSuccess
              ? GDN_OK
              : GDN_ERR_CUDA;
