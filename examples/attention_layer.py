@@ -52,6 +52,15 @@ class AttentionLayer:
         out, _ = gdn.attention_prefill(q, k, v, cu_seqlens)
         return self.output(out), res
 
+    def prefill_on(self, x, cu_seqlens, cache, start, cu_all, tokens, residual=None):
+        """Prompts that go on behind what their rows hold: x are the new tokens, cu_all and
+        tokens the rows' lengths with them."""
+        q, k, v, res = self.project(x, residual)
+        gdn.cache_append(cache, k, v, start, cu_seqlens, self.layer)
+        k, v = gdn.cache_gather(cache, cu_all, tokens, self.layer)
+        out, _ = gdn.attention_prefill(q, k, v, cu_seqlens, cu_all)
+        return self.output(out), res
+
     def decode(self, x, cache, start, residual=None):
         """One token a row, x [rows, dim]; its place was reserved for all layers at once."""
         q, k, v, res = self.project(x, residual)
@@ -94,6 +103,18 @@ def main():
         last = [sum(m + more for m in lens[:i + 1]) - 1 for i in range(n)]
         want = whole[last + [last[0]] * 3].float()
         off = (out[:n + 3].float() - want).norm() / want.norm()
+        # the same tokens as a next turn of whole prompts
+        again = gdn.kv_cache(1, 32, layer.kv, n, 4, page=64, d=layer.d, dtype=dtype)
+        layer.prefill(torch.cat([t[:m] for t, m in zip(x, lens)]), cu[:n + 1].contiguous(), again,
+                      gdn.cache_reserve(again, ints(lens)))
+        turn, _ = layer.prefill_on(torch.cat([t[m:] for t, m in zip(x, lens)]),
+                                   ints([more * i for i in range(n + 1)]), again,
+                                   gdn.cache_reserve(again, ints([more] * n)),
+                                   ints([sum(m + more for m in lens[:i]) for i in range(n + 1)]),
+                                   sum(lens) + n * more)
+        turn = turn[[more * (i + 1) - 1 for i in range(n)]].float()
+        print(f"{str(dtype)[6:]} cache: a next turn's last tokens, relative "
+              f"{(turn - want[:n]).norm() / want[:n].norm():.1e}")
         print(f"{str(dtype)[6:]} cache: decoded outputs against the prefill's, relative {off:.1e}; "
               f"{int((cache.refs > 0).sum())} pages held")
 

@@ -20,6 +20,7 @@ raise when the compiled library is missing.
     cache = kv_cache(layers, pages, kv_heads, rows, max_pages)        # and their paged cache:
     start = cache_reserve(cache, counts); cache_append(cache, k, v, start, layer=i)
     out = attention_decode_step(q, cache, layer=i)
+    k, v = cache_gather(cache, cu_seqlens_k, tokens, layer=i)         # (prompts that go on)
 
 Recurrence (Appendix A.3, Eq. 16-19 of "Long-Context Aware Upcycling"):
 S_t = alpha_t S_{t-1}(I - beta_t k_t k_t^T) + beta_t v_t k_t^T,
@@ -157,6 +158,8 @@ def load():
     lib.gdn_cache_reserve.restype = ctypes.c_int
     lib.gdn_cache_append.argtypes = [vp, i32, vp, vp, vp, vp, i64, i64, i64, vp]
     lib.gdn_cache_append.restype = ctypes.c_int
+    lib.gdn_cache_gather.argtypes = [vp, i32, vp, i64, vp, vp, vp]
+    lib.gdn_cache_gather.restype = ctypes.c_int
     lib.gdn_cache_free.argtypes = [vp, vp, i32, vp]
     lib.gdn_cache_free.restype = ctypes.c_int
     lib.gdn_cache_fork.argtypes = [vp, vp, vp, i32, vp]
@@ -1202,6 +1205,24 @@ def cache_append(cache, k, v, start, cu_seqlens=None, layer=0, stream=None):
         raise ValueError(f"k and v must have a token for each of the {rows} rows (or cu_seqlens)")
     _call("gdn_cache_append", index, stream, at, layer, k.data_ptr(), v.data_ptr(),
           start.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), k.shape[0], ks, vs)
+
+
+def cache_gather(cache, cu_seqlens, tokens, layer=0, stream=None):
+    """One layer's stored keys and values as :func:`attention_prefill` reads them
+    (``gdn_cache_gather``): row r's first cu_seqlens[r+1] - cu_seqlens[r]
+    tokens, packed; tokens = cu_seqlens[-1], which stays on the device.
+    Returns (k, v) [tokens, kv_heads, d] bf16."""
+    index, at = _cache(cache)
+    if stream is None:
+        done = _direct_calls().cache_gather(at, index, cu_seqlens, tokens, layer)
+        if done is not None:
+            return done
+    _out(cu_seqlens, "cu_seqlens", (cache.lengths.shape[0] + 1,), torch.int32, index)
+    k, v = (torch.empty((tokens, cache.k.shape[2], cache.k.shape[4]), dtype=torch.bfloat16,
+                        device=cache.k.device) for _ in range(2))
+    _call("gdn_cache_gather", index, stream, at, layer, cu_seqlens.data_ptr(), tokens, k.data_ptr(),
+          v.data_ptr())
+    return k, v
 
 
 def cache_free(cache, rows, stream=None):

@@ -34,6 +34,7 @@ struct Library {
   decltype(&gdn_attention_decode_step) attention_decode_step = nullptr;
   decltype(&gdn_cache_reserve) cache_reserve = nullptr;
   decltype(&gdn_cache_append) cache_append = nullptr;
+  decltype(&gdn_cache_gather) cache_gather = nullptr;
   decltype(&gdn_cache_free) cache_free = nullptr;
   decltype(&gdn_cache_fork) cache_fork = nullptr;
   decltype(&gdn_cache_compact) cache_compact = nullptr;
@@ -528,6 +529,27 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (cache, device, cu_seqlens, tokens, layer) -> (k, v)
+PyObject* cache_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  c10::DeviceIndex index;
+  const gdn_kv_cache* c = n == 5 ? cache_in(a[0], a[1], index) : nullptr;
+  const int32_t* cu = c ? row_ints(a[2], index, (int64_t)c->rows + 1) : nullptr;
+  const long tokens = int_arg(a[3], -1), layer = int_arg(a[4], -1);
+  if (!cu || tokens < 1 || tokens > INT32_MAX || layer < 0 || layer >= c->layers) return none();
+  const int64_t shape[] = {tokens, c->kv_heads, c->d};
+  const at::Tensor& like_cu = THPVariable_Unpack(a[2]);
+  at::Tensor k = make(like_cu, shape, at::kBFloat16);
+  at::Tensor v = make(like_cu, shape, at::kBFloat16);
+  const gdn_stream_t st = stream_of(index);
+  if (!call([&] {
+        return lib.cache_gather(c, (int32_t)layer, cu, tokens, k.data_ptr(), v.data_ptr(), st);
+      }))
+    return none();
+  return pack({wrap(k), wrap(v)});
+  END_HANDLE_TH_ERRORS
+}
+
 // (cache, device, rows) -> True
 PyObject* cache_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -600,6 +622,7 @@ PyObject* bind(PyObject*, PyObject* path) {
   find(lib.attention_decode_step, "gdn_attention_decode_step");
   find(lib.cache_reserve, "gdn_cache_reserve");
   find(lib.cache_append, "gdn_cache_append");
+  find(lib.cache_gather, "gdn_cache_gather");
   find(lib.cache_free, "gdn_cache_free");
   find(lib.cache_fork, "gdn_cache_fork");
   find(lib.cache_compact, "gdn_cache_compact");
@@ -627,6 +650,7 @@ PyMethodDef methods[] = {
     GDN_CALL(attention_decode_step),
     GDN_CALL(cache_reserve),
     GDN_CALL(cache_append),
+    GDN_CALL(cache_gather),
     GDN_CALL(cache_free),
     GDN_CALL(cache_fork),
     GDN_CALL(cache_compact),

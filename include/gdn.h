@@ -729,6 +729,20 @@ int gdn_cache_append(const gdn_kv_cache* cache, int32_t layer, const void* k, co
                      int64_t k_stride, int64_t v_stride, gdn_stream_t stream);
 
 /*
+ * gdn_cache_gather -- a layer's stored keys and values as gdn_attention_prefill
+ * reads them, for prompts that go on behind a stored context: row r's first
+ * cu_seqlens[r+1] - cu_seqlens[r] tokens to those places of k and v.
+ *   k, v [tokens, kv_heads, d] bf16, contiguous (8 bits: the codes times their
+ *   scales, rounded to bf16)
+ *   cu_seqlens [rows + 1] with cu_seqlens[rows] = tokens
+ * A token at or behind lengths[row], or outside its cu_seqlens
+ * (GDN_ERR_BAD_SEQLENS), or whose page is none (GDN_ERR_BAD_CACHE) is left as it
+ * was.  k and v may overlap neither the cache nor each other.
+ */
+int gdn_cache_gather(const gdn_kv_cache* cache, int32_t layer, const int32_t* cu_seqlens,
+                     int64_t tokens, void* k, void* v, gdn_stream_t stream);
+
+/*
  * gdn_cache_free -- empties rows[0 .. n): their pages lose a reference, their
  * table entries become -1, their lengths 0.  A row named twice is emptied
  * once; an empty row stays so; a number outside [0, cache rows) is skipped

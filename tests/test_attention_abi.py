@@ -98,6 +98,7 @@ def test_a_malformed_cache_is_refused_by_every_call(lib, change, code):  # noqa:
     c, good = ctypes.byref(cache(**change)), ctypes.byref(cache(5))
     assert lib.gdn_cache_reserve(c, A[11], A[12], None) == code
     assert lib.gdn_cache_append(c, 0, A[11], A[12], A[13], None, 4, 128, 128, None) == code
+    assert lib.gdn_cache_gather(c, 0, A[11], 4, A[12], A[13], None) == code
     assert lib.gdn_cache_free(c, A[11], 1, None) == code
     assert lib.gdn_cache_fork(c, A[11], A[12], 1, None) == code
     assert lib.gdn_cache_compact(c, good, None) == code
@@ -121,6 +122,14 @@ def test_cache_calls_refuse(lib):  # noqa: F811
     assert append(k=None) == 1 and append(start=None) == 1 and append(ks=120) == 1
     assert append(ks=132) == 3 and append(k=P(A[5].value + 8)) == 3 and append(start=P(A[7].value + 1)) == 3
     assert append(k=A[0]) == 1 and append(start=A[3]) == 1
+
+    def gather(layer=0, cu=A[5], n=4, k=A[6], v=A[7]):
+        return lib.gdn_cache_gather(c, layer, cu, n, k, v, None)
+    assert gather(n=0) == 0 and gather(n=0, k=None, v=None) == 0
+    assert gather(layer=2) == 1 and gather(layer=-1) == 1 and gather(n=-1) == 1 and gather(n=2 ** 31) == 1
+    assert gather(cu=None) == 1 and gather(k=None) == 1 and gather(v=None) == 1
+    assert gather(cu=P(A[5].value + 2)) == 3 and gather(k=P(A[6].value + 8)) == 3
+    assert gather(k=A[0]) == 1 and gather(v=A[6]) == 1 and gather(v=A[5]) == 1 and gather(k=A[3]) == 1
     assert lib.gdn_cache_free(c, None, 0, None) == 0
     assert lib.gdn_cache_free(c, A[5], -1, None) == 1 and lib.gdn_cache_free(c, None, 1, None) == 1
     assert lib.gdn_cache_free(c, P(A[5].value + 2), 1, None) == 3 and lib.gdn_cache_free(c, A[2], 1, None) == 1

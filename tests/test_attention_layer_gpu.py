@@ -85,6 +85,34 @@ def test_prompts_in_pieces_match_the_whole(gdn_lib):
         assert (s - whole[name].float()).norm() <= 2.0 ** -6 * s.norm(), name
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+def test_a_next_turn_behind_the_stored_context(gdn_lib, dtype):
+    """New tokens of rows that hold a context: appended to the pages, and attended with the gathered
+    context as their keys.  In bf16 these are the bits that the whole prompts' tails have as
+    queries of their own; in 8 bits the keys and values are off by 2^-4 of themselves at most."""
+    kv, G, d = 2, 3, 64
+    g = torch.Generator(device="cuda").manual_seed(13)
+    lens, new = [70, 0, 200, 33], [5, 9, 0, 64]
+    full = [a + b for a, b in zip(lens, new)]
+    x = [[torch.randn(n, h, d, generator=g, device="cuda").to(BF16) for h in (kv * G, kv, kv)]
+         for n in full]
+    cache = gdn.kv_cache(2, 40, kv, 4, 8, 32, d, dtype)
+    for counts, part in ((lens, lambda t, n: t[:n]), (new, lambda t, n: t[n:])):
+        start = gdn.cache_reserve(cache, ints(counts))
+        gdn.cache_append(cache, *(torch.cat([part(t[j], n) for t, n in zip(x, lens)]) for j in (1, 2)),
+                         start, cu_of(counts), 1)
+    k, v = gdn.cache_gather(cache, cu_of(full), sum(full), 1)
+    q = torch.cat([t[0][n:] for t, n in zip(x, lens)])
+    got, lse = gdn.attention_prefill(q, k, v, cu_of(new), cu_of(full))
+    want, sums = gdn.attention_prefill(q, *(torch.cat([t[j] for t in x]) for j in (1, 2)), cu_of(new),
+                                       cu_of(full))
+    if dtype == BF16:
+        assert torch.equal(got, want) and torch.equal(lse, sums)
+    else:
+        assert (got.float() - want.float()).norm() <= 2.0 ** -3 * want.float().norm()
+    assert gdn.device_status() == 0
+
+
 def test_a_captured_decoding_step(gdn_lib):
     """Reserve, append and attention of two layers in one graph, replayed with new inputs; the same
     from calls outside it, bit for bit."""
@@ -137,7 +165,7 @@ def arguments():
 
 
 @pytest.mark.parametrize("name", ["attention_prefill", "attention_prefill_backward",
-                                  "attention_decode_step", "cache_reserve", "cache_append", "cache_free",
+                                  "attention_decode_step", "cache_reserve", "cache_append", "cache_gather", "cache_free",
                                   "cache_fork", "cache_compact"])
 def test_the_direct_call_answers(gdn_lib, name, monkeypatch):
     """Each direct call takes ordinary arguments itself, with the general path's bits."""
@@ -155,6 +183,8 @@ def test_the_direct_call_answers(gdn_lib, name, monkeypatch):
                               lambda: gdn.cache_reserve(cache, ints([1, 2, 3]))),
             "cache_append": ((cache.address, cache.index, k[:3], v[:3], ints([19, 0, -1]), None, 1),
                              lambda: gdn.cache_append(cache, k[:3], v[:3], ints([19, 0, -1]), layer=1)),
+            "cache_gather": ((cache.address, cache.index, cu_of([20, 1, 0]), 21, 1),
+                             lambda: gdn.cache_gather(cache, cu_of([20, 1, 0]), 21, 1)),
             "cache_free": ((cache.address, cache.index, ints([1])), lambda: gdn.cache_free(cache, ints([1]))),
             "cache_fork": ((cache.address, cache.index, ints([0]), ints([2])),
                            lambda: gdn.cache_fork(cache, ints([0]), ints([2]))),

@@ -354,3 +354,41 @@ def test_a_pool_of_more_than_2_31_elements(gdn_lib):
     gdn.cache_compact(cache, into)
     assert torch.equal(stored(into, 0, 1, counts[0])[0], bits(q)[:counts[0]])
     assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("d,page,kv", [(64, 16, 3), (128, 64, 2), (128, 256, 1)])
+def test_gather(gdn_lib, dtype, d, page, kv):
+    """The stored tokens in order; codes times their scales rounded to bf16; fewer than a row holds;
+    what a row does not hold is flagged and left."""
+    gdn = gdn_lib
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lens = [0, 1, 130, 16, 0, 257, 64]
+    need = sum(-(-n // page) for n in lens)
+    cache = gdn.kv_cache(2, need + 2, kv, len(lens), 20, page, d, dtype)
+    x = [torch.randn(sum(lens), kv, d, generator=g, device="cuda").to(BF16) for _ in range(2)]
+    starts = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    gdn.cache_append(cache, *x, gdn.cache_reserve(cache, ints(lens)), ints(starts), 1)
+    if dtype == FP8:
+        x = [(c.float().unflatten(-1, (-1, d)) * s[..., None]).flatten(-2).to(BF16)
+             for c, s in (gdn.quantize_fp8(t.reshape(-1, d)) for t in x)]
+        x = [t.view(-1, kv, d) for t in x]
+    for counts in (lens, [0, 1, 100, 0, 0, 256, 64], [0] * 6 + [3]):
+        cu = [sum(counts[:i]) for i in range(len(counts) + 1)]
+        at = [starts[r] + i for r, n in enumerate(counts) for i in range(n)]
+        got = gdn.cache_gather(cache, ints(cu), cu[-1], 1)
+        assert all(torch.equal(a, b[at]) for a, b in zip(got, x))
+    none = gdn.cache_gather(cache, ints([0] * 8), 0, 1)
+    assert none[0].shape == (0, kv, d) and gdn.device_status() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = gdn.cache_gather(cache, ints(starts), starts[-1], 1, stream=side)
+    side.synchronize()
+    assert torch.equal(got[1], x[1])
+    gdn.cache_gather(cache, ints([0, 0, 2, 2, 2, 2, 2, 2]), 2, 1)
+    assert gdn.device_status() == 6
+    gdn.cache_gather(cache, ints([0, 0, 1, 1, 1, 1, 1, 1]), 2, 1)
+    assert gdn.device_status() == 6
+    cache.table[1, 0] = need + 2
+    gdn.cache_gather(cache, ints([0, 0, 1, 1, 1, 1, 1, 1]), 1, 1)
+    assert gdn.device_status() == BAD
