@@ -263,3 +263,17 @@ def test_tensors_of_more_than_2_31_elements(gdn_lib):
     for a, b in ((0, 64), (64 * 4100, 64 * 4101), (T - 200, T)):
         verify(q[a:b], k[a:b], v[a:b], out[a:b], lse[a:b], [b - a], [b - a])
     assert gdn_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ql,kl", [([20], [9000]), ([1], [1000]), ([64, 3], [700, 40]), ([130], [130]),
+                                   ([200, 0, 90], [3000, 5, 2000]), ([1000], [1000])])
+def test_keys_in_parts(gdn_lib, ql, kl, d):
+    """Few tiles behind many keys: the parts of a tile's keys are joined; the same bits every time."""
+    q, k, v = inputs(sum(ql), sum(kl), 6, 2, d, seed=sum(kl))
+    out, lse = gdn_lib.attention_prefill(q, k, v, cu(ql), cu(kl))
+    verify(q, k, v, out, lse, ql, kl)
+    for _ in range(3):
+        again = gdn_lib.attention_prefill(q, k, v, cu(ql), cu(kl))
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert gdn_lib.device_status() == 0
