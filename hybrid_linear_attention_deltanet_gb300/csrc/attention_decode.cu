@@ -58,7 +58,7 @@ struct Shape {
   static constexpr int kStages = kRow == 64 ? 5 : 3;
   static constexpr int kPitch = D + 8;                      // floats of a row of the join
   static constexpr uint32_t kSmall = kStages * kStage;      // where Small lies
-  static constexpr uint32_t kSmem = kSmall + 768;
+  static constexpr uint32_t kSmem = kSmall + 1024;
   static_assert(kWarps * kHeads * kPitch * 4 <= kStage, "the join uses a consumed stage");
   static_assert(2 * kScales <= 1024 && kStage % 1024 == 0, "");
 };
@@ -72,9 +72,9 @@ struct Tile {
 struct Small {
   uint64_t full[5], empty[5];
   Tile meta[5];
-  float ml[kWarps][kHeads][2];
+  float ml[kWarps][kHeads][3];   // a warp's maximum and sum, 8 bits: and its weights' maximum
 };
-static_assert(sizeof(Small) <= 768, "");
+static_assert(sizeof(Small) <= 1024, "");
 
 // What is left of a cut (row, head)'s parts: slot 2c of CTA c if the part
 // continues one, 2c + 1 if it begins one.
@@ -624,35 +624,32 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         if (t4 == 0) {
           ml[warp][g + 8 * x][0] = m[x];
           ml[warp][g + 8 * x][1] = l[x];
+          if constexpr (kFp8) ml[warp][g + 8 * x][2] = wm[x];
         }
       }
+      // (the stage's other readers are done at the next barrier but one: every warp's own
+      // rows of the join lie behind its tokens' bytes only after this one)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      const int h = tile.hh / a.parts, part = tile.hh - h * a.parts;
+      const int heads = a.group - part * kHeads < kHeads ? a.group - part * kHeads : kHeads;
       float* js = reinterpret_cast<float*>(bytes);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][g + 8 * x][0]);
-        const float f = m[x] == -INFINITY ? 0.f
-                        : !kFp8           ? ex2_sfu(m[x] - top)
-                        : wm[x] == -INFINITY ? 0.f
-                                             : ex2_sfu(wm[x] - kRoom - top);
+        if (g + 8 * x >= heads) break;
         float* r = js + (warp * kHeads + g + 8 * x) * S::kPitch;
         if constexpr (!kFp8) {
 #pragma unroll
           for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<float2*>(r + j * 8 + 2 * t4) =
-                make_float2(o[j][2 * x] * f, o[j][2 * x + 1] * f);
+            *reinterpret_cast<float2*>(r + j * 8 + 2 * t4) = make_float2(o[j][2 * x], o[j][2 * x + 1]);
         } else {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
             *reinterpret_cast<float4*>(r + j * 16 + 4 * t4) =
-                make_float4(o[2 * j][2 * x] * f, o[2 * j + 1][2 * x] * f, o[2 * j][2 * x + 1] * f,
-                            o[2 * j + 1][2 * x + 1] * f);
+                make_float4(o[2 * j][2 * x], o[2 * j + 1][2 * x], o[2 * j][2 * x + 1],
+                            o[2 * j + 1][2 * x + 1]);
         }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-      const int h = tile.hh / a.parts, part = tile.hh - h * a.parts;
       const int64_t item_begin = i - tile.at;
       const bool from_begin = first_of_part == item_begin, whole = from_begin && item_ends;
       const int64_t item = (int64_t)tile.row * HH + tile.hh;
@@ -661,7 +658,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         a.w.cut[item] = make_int2(
             blockIdx.x, whole ? 0 : (int)(owner_of(total, item_begin + tile.n - 1, ctas) - blockIdx.x + 1));
       }
-      const int heads = a.group - part * kHeads < kHeads ? a.group - part * kHeads : kHeads;
 #pragma unroll
       for (int v = 0; v < kHeads * D / 4 / (32 * kWarps); ++v) {
         const int e = v * 32 * kWarps + tid, row = e / (D / 4), col = e % (D / 4) * 4;
@@ -673,9 +669,16 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float4 y = *reinterpret_cast<const float4*>(js + (w * kHeads + row) * S::kPitch + col);
-          sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
           const float mw = ml[w][row][0];
-          all += mw == -INFINITY ? 0.f : ml[w][row][1] * ex2_sfu(mw - top);
+          const float fl = mw == -INFINITY ? 0.f : ex2_sfu(mw - top);
+          float f = fl;
+          if constexpr (kFp8) {
+            const float ww = ml[w][row][2];
+            f = mw == -INFINITY || ww == -INFINITY ? 0.f : ex2_sfu(ww - kRoom - top);
+          }
+          sum.x = fmaf(y.x, f, sum.x); sum.y = fmaf(y.y, f, sum.y);
+          sum.z = fmaf(y.z, f, sum.z); sum.w = fmaf(y.w, f, sum.w);
+          all += mw == -INFINITY ? 0.f : ml[w][row][1] * fl;
         }
         // (a warp whose scores were all NaN kept the maximum -inf: its sum is NaN)
 #pragma unroll
