@@ -5,9 +5,8 @@
 //
 // Every key and value is used once by each of a group's query heads, so the
 // cache's bytes through HBM bound it, whatever the rows' lengths.  The tiles of
-// all rows and kv heads (64 tokens of 256 bytes, 128 of fewer) form one list; CTA
-// c of n takes the c-th n-th of it, so that no CTA has more than a tile more than
-// another.  One warp walks the CTA's part and has TMA bring the tiles, page by
+// all rows and kv heads (64 tokens of 256 bytes, 128 of fewer) form one list, with a slot
+// for each (row, head)'s end; CTA c of n takes the c-th n-th of it.  One warp walks the CTA's part and has TMA bring the tiles, page by
 // page, into a ring; four warps take a quarter of a tile each, with softmax
 // statistics of their own.  (With the loads' addresses computed by all threads
 // these took more instructions than the attention: heads of 64 ran at 3.8 TB/s,
@@ -17,10 +16,11 @@
 // several CTAs is joined from their partial sums by a second kernel, in the order
 // of the CTAs.
 //
-// 20 query and 4 kv heads of 128: 256 rows of up to 8192 tokens 319 us (6.6 TB/s), in
-// 8 bits 209 (5.2; widening the codes); one row of 32768 tokens in 8 bits 17 us, of which
-// the bytes are 5.  Heads of 64 in 8 bits: 3.2 TB/s, a tile's 128 tokens of 64 bytes
-// being too little for the steps that follow one another in it.
+// 16 query and 4 kv heads of 128: 256 rows of up to 8192 tokens 306 us (6.9 TB/s), in
+// 8 bits 194 (5.6; widening the codes); of up to 512 tokens 32 and 29; one row of 32768
+// tokens in 8 bits 17 us, of which the bytes are 5.  Heads of 64 in 8 bits: 3.8 TB/s, a
+// tile's 128 tokens of 64 bytes being too little for the steps that follow one another
+// in it.  Tiles of 64 tokens in 8 bits: 18.9 us for the one row, 9 % more for 256.
 #include "attention_tc.cuh"
 #include "gdn_internal.cuh"
 #include "hostcheck.cuh"
@@ -79,8 +79,8 @@ static_assert(sizeof(Small) <= 1024, "");
 // What is left of a cut (row, head)'s parts: slot 2c of CTA c if the part
 // continues one, 2c + 1 if it begins one.
 struct Work {
-  int2* cut;          // [items] the first CTA that has a part of it, and its parts (0: one CTA
-                      // has all of it)
+  int4* cut;          // [CTAs] the cut (row, kv head and part of the group) that begins in it, and its
+                      // parts (0: none does)
   float* ml;          // [slots][16][2] maximum (of scores in powers of two), sum
   float* o;           // [slots][16][D]
 };
@@ -182,6 +182,22 @@ __device__ __forceinline__ int32_t row_tokens(const gdn_kv_cache& c, int64_t row
   return 0;
 }
 
+// Slots of the list that a (row, head) of n tiles takes: one more than its tiles, for its
+// end and beginning (the join of its warps' sums, the next one's first tile) cost about a
+// tile.  (By tiles alone, 256 rows of up to 512 tokens: the CTAs with short rows ran 33 us where
+// the median one ran 25, 38 us in all instead of 29.)
+__device__ __forceinline__ int32_t slots_of(int32_t n) { return n > 0 ? n + 1 : 0; }
+
+// Zeros for the rows without tokens, by one warp of every CTA.
+template <int D>
+__device__ __forceinline__ void zero_empty_rows(const Args& a, int lane) {
+  for (int64_t r = blockIdx.x; r < a.c.rows; r += gridDim.x) {
+    if (row_tokens(a.c, r, nullptr) > 0) continue;
+    uint4* to = reinterpret_cast<uint4*>(a.out + r * a.q_heads * D);
+    for (int64_t i = lane; i < (int64_t)a.q_heads * D / 8; i += 32) to[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ Args a) {
   using S = Shape<D, kFp8>;
@@ -202,7 +218,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   const int HH = a.items_per_row;
   grid_release_next();
   if (smem_u32(smem) & 1023u) {
-    if (tid == 0) flag_status(a.status, GDN_ERR_UNSUPPORTED);
+    grid_wait();
+    if (tid == 0) {
+      flag_status(a.status, GDN_ERR_UNSUPPORTED);
+      a.w.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
     return;
   }
   if (tid == 0) {
@@ -227,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   if (few) {
     const int32_t n = row_tokens(c, tid, a.status);
     lens[tid] = n;
-    mine = (n + S::kTile - 1) / S::kTile;
+    mine = slots_of((n + S::kTile - 1) / S::kTile);
   } else {
     for (int64_t r = r0; r < r1; ++r)
-      mine += (row_tokens(c, r, a.status) + S::kTile - 1) / S::kTile;
+      mine += slots_of((row_tokens(c, r, a.status) + S::kTile - 1) / S::kTile);
   }
   {
     int64_t x = mine;
@@ -248,9 +268,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   }
   const int64_t total = sums[kThreads] * HH;
   // (the table that fits the GPU's memory bounds total below 2^50: 64 bits do)
-  const int64_t ctas = total < gridDim.x ? total : gridDim.x;   // none has no tile
-  if (blockIdx.x >= ctas) return;
-  const int64_t lo = begin_of(total, blockIdx.x, ctas), hi = begin_of(total, blockIdx.x + 1, ctas);
+  const int64_t ctas = total < gridDim.x ? total : gridDim.x;   // none has no slot
+  if (blockIdx.x >= ctas) {
+    if (tid == 0) a.w.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (warp == kWarps) zero_empty_rows<D>(a, lane);
+    return;
+  }
+  int64_t lo = begin_of(total, blockIdx.x, ctas);
+  const int64_t hi = begin_of(total, blockIdx.x + 1, ctas);
   if (lo >= sums[tid] * HH && lo < sums[tid + 1] * HH) {
     int64_t left = lo - sums[tid] * HH;
     if (few) {
@@ -258,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       where[1] = left;
     }
     for (int64_t r = few ? r1 : r0; r < r1; ++r) {
-      const int64_t n = (int64_t)((row_tokens(c, r, nullptr) + S::kTile - 1) / S::kTile) * HH;
+      const int64_t n = (int64_t)slots_of((row_tokens(c, r, nullptr) + S::kTile - 1) / S::kTile) * HH;
       if (left < n) {
         where[0] = r;
         where[1] = left;
@@ -274,6 +299,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   fence_proxy_async_smem();
   __syncthreads();
   bool ok = true;
+  // the first tile, if the first slot is not a (row, head)'s last, which has none
+  const int32_t slots0 = slots_of((len0 + S::kTile - 1) / S::kTile);
+  const int32_t hh0 = (int32_t)(in_row / slots0), at0 = (int32_t)(in_row - (int64_t)hh0 * slots0);
+  const bool skip = at0 == slots0 - 1;
+  if (skip) ++lo;
 
   if (warp == kWarps) {
     // --------------------------------------------------------------- load
@@ -286,8 +316,27 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     t.len = len0;
     int32_t next_len = len1;
     t.n = (t.len + S::kTile - 1) / S::kTile;
-    t.hh = (int32_t)(in_row / t.n);
-    t.at = (int32_t)(in_row - (int64_t)t.hh * t.n);
+    t.hh = hh0;
+    t.at = at0;
+    // on to the next tile of the list: true where another (row, head) begins
+    auto advance = [&]() {
+      if (++t.at < t.n) return false;
+      t.at = 0;
+      if (++t.hh == HH) {
+        t.hh = 0;
+        do {
+          ++t.row;
+          t.len = next_len;
+          t.n = (t.len + S::kTile - 1) / S::kTile;
+          next_len = row_tokens(c, (int64_t)t.row + 1, nullptr);
+        } while (t.n == 0 && t.row < c.rows);
+      }
+      return true;
+    };
+    if (skip) {
+      t.at = t.n - 1;
+      advance();
+    }
     // lane i reads the page of the tile's i-th copy, one tile ahead
     auto read_id = [&]() {
       const int64_t pos = (int64_t)t.at * S::kTile + lane * box;
@@ -296,10 +345,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         id = c.table[(int64_t)t.row * c.max_pages + (pos >> lg)];
       return id;
     };
-    int32_t id = read_id();
+    int32_t id = lo < hi ? read_id() : 0;
     bool fresh = true;                                       // the first tile of its part
-    for (int64_t i = lo; i < hi; ++i) {
-      const int stage = (int)((i - lo) % S::kStages);
+    int64_t step = 1;                                        // slots to the next tile
+    int64_t k = 0;
+    for (int64_t i = lo; i < hi; i += step, ++k) {
+      const int stage = (int)(k % S::kStages);
       const Tile now = t;
       const bool first = fresh;
       if (id < 0 || id >= c.pages) {                         // some page of the pool in its place
@@ -307,23 +358,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         id = 0;
       }
       const int32_t ids = id;
-      // on to the next tile
-      fresh = false;
-      if (++t.at == t.n) {
-        t.at = 0;
-        fresh = true;
-        if (++t.hh == HH) {
-          t.hh = 0;
-          do {
-            ++t.row;
-            t.len = next_len;
-            t.n = (t.len + S::kTile - 1) / S::kTile;
-            next_len = row_tokens(c, (int64_t)t.row + 1, nullptr);
-          } while (t.n == 0 && t.row < c.rows);
-        }
-      }
-      if (i + 1 < hi) id = read_id();
-      ok = mbar_wait_warp_cycles(&empty[stage], (uint32_t)(((i - lo) / S::kStages) & 1) ^ 1u, kWaitCycles);
+      fresh = advance();
+      step = fresh ? 2 : 1;
+      if (i + step < hi) id = read_id();
+      ok = mbar_wait_warp_cycles(&empty[stage], (uint32_t)((k / S::kStages) & 1) ^ 1u, kWaitCycles);
       if (!ok) break;
       const int64_t pos = (int64_t)now.at * S::kTile;
       const int64_t tokens = now.len - pos < S::kTile ? now.len - pos : S::kTile;
@@ -360,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       }
       __syncwarp();
     }
+    zero_empty_rows<D>(a, lane);
   } else {
     // ---------------------------------------------------------- attention
     const int g = lane >> 2, t4 = lane & 3;
@@ -377,10 +416,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     float unit[2];        // scores' factor of rows g and g + 8
     float wm[2];          // 8 bits: the weights' running maxima
     bool start = true;
-    int64_t first_of_part = lo;
-    for (int64_t i = lo; i < hi; ++i) {
-      const int stage = (int)((i - lo) % S::kStages);
-      ok = mbar_wait_warp_cycles(&full[stage], (uint32_t)(((i - lo) / S::kStages) & 1), kWaitCycles);
+    int64_t first_of_part = lo, k = 0;
+    bool begins = false;         // a (row, head) that is cut begins here
+    for (int64_t i = lo, step; i < hi; i += step, ++k) {
+      const int stage = (int)(k % S::kStages);
+      ok = mbar_wait_warp_cycles(&full[stage], (uint32_t)((k / S::kStages) & 1), kWaitCycles);
       if (!ok) break;
       const Tile tile = meta[stage];
       uint8_t* bytes = smem + stage * S::kStage;
@@ -609,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         }
       }
       const bool item_ends = tile.at == tile.n - 1;
+      step = item_ends ? 2 : 1;                          // (behind its last tile a slot without one)
       if (!item_ends && i + 1 < hi) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
@@ -652,11 +693,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
       const int64_t item_begin = i - tile.at;
       const bool from_begin = first_of_part == item_begin, whole = from_begin && item_ends;
-      const int64_t item = (int64_t)tile.row * HH + tile.hh;
       const int64_t slot = 2 * (int64_t)blockIdx.x + from_begin;
-      if (tid == 0 && from_begin) {
-        a.w.cut[item] = make_int2(
-            blockIdx.x, whole ? 0 : (int)(owner_of(total, item_begin + tile.n - 1, ctas) - blockIdx.x + 1));
+      if (from_begin && !whole) {
+        begins = true;
+        if (tid == 0)
+          a.w.cut[blockIdx.x] = make_int4(
+              tile.row, tile.hh, (int)(owner_of(total, item_begin + tile.n - 1, ctas) - blockIdx.x + 1), 0);
       }
 #pragma unroll
       for (int v = 0; v < kHeads * D / 4 / (32 * kWarps); ++v) {
@@ -704,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
+    if (tid == 0 && !begins) a.w.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (!ok) {
     // copies in flight end within microseconds; give them longer
@@ -713,113 +756,102 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   }
 }
 
-// The cut (row, head)s: a CTA takes one query head at a time, its warps every
-// eighth part, then the warps' sums in order.  (Every load of a step in flight at
-// once: parts one after another took 11 us for the 76 of a row of 32768 tokens.)
-// Rows without tokens get zeros.
+// The cut (row, head)s: blockIdx.x's is the one that begins in that CTA of the kernel before,
+// if one does; a CTA takes one of its query heads, its warps every eighth part, then the
+// warps' sums in order.  (Every load of a step in flight at once: parts one after another
+// took 11 us for the 76 of a row of 32768 tokens.)
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
   constexpr int kN = kJoinThreads / 32, kV = D / 32;
   __shared__ float sm[kN][D + 2], weight[kCtas], sum[kCtas];
-  const gdn_kv_cache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_release_next();
   grid_wait();
-  const int64_t jobs = (int64_t)c.rows * a.q_heads;
-  for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-    const int64_t row = job / a.q_heads;
-    const int head = (int)(job - row * a.q_heads);
-    const int h = head / a.group, in = head - h * a.group, part = in / kHeads, r = in % kHeads;
-    __nv_bfloat16* out = a.out + job * D;
-    const int32_t* cut = reinterpret_cast<const int32_t*>(a.w.cut + row * a.items_per_row + h * a.parts + part);
-    const int32_t first = ld_waited(cut), parts = ld_waited(cut + 1);   // (unset for empty rows)
-    if (row_tokens(c, row, nullptr) == 0) {
-      for (int i = threadIdx.x; i < D; i += kJoinThreads) out[i] = __float2bfloat16_rn(0.f);
-      continue;
-    }
-    if (parts == 0) continue;
-    auto slot = [&](int p) { return (int64_t)((2 * (first + p) + (p == 0)) * kHeads + r); };
-    // the parts' maxima and sums, then every part's factor; a warp's first four
-    // parts are on their way by then
-    float x[4][kV];
-    auto read = [&](int p) {
+  const int first = blockIdx.x, r = blockIdx.y;
+  const uint4 cut = ld_waited(reinterpret_cast<const uint4*>(a.w.cut + first));
+  const int row = (int)cut.x, hh = (int)cut.y, parts = (int)cut.z;
+  const int h = hh / a.parts, part = hh - h * a.parts, in = part * kHeads + r;
+  if (parts == 0 || in >= a.group) return;
+  __nv_bfloat16* out = a.out + ((int64_t)row * a.q_heads + (int64_t)h * a.group + in) * D;
+  auto slot = [&](int p) { return (int64_t)((2 * (first + p) + (p == 0)) * kHeads + r); };
+  // the parts' maxima and sums, then every part's factor; a warp's first four
+  // parts are on their way by then
+  float x[4][kV];
+  auto read = [&](int p) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* src = a.w.o + slot(p + i * kN) * D + lane * kV;
-        if (p + i * kN >= parts) continue;
-        if constexpr (kV == 4) {
-          const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
-          x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
-        } else {
-          x[i][0] = ld_waited(src);
-          x[i][1] = ld_waited(src + 1);
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float* src = a.w.o + slot(p + i * kN) * D + lane * kV;
+      if (p + i * kN >= parts) continue;
+      if constexpr (kV == 4) {
+        const float4 t = ld_waited(reinterpret_cast<const float4*>(src));
+        x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+      } else {
+        x[i][0] = ld_waited(src);
+        x[i][1] = ld_waited(src + 1);
       }
-    };
-    read(warp);
-    float m = -INFINITY;
-    for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
-      const float mp = ld_waited(a.w.ml + slot(p) * 2);
-      weight[p] = mp;
-      sum[p] = ld_waited(a.w.ml + slot(p) * 2 + 1);
-      m = fmaxf(m, mp);
     }
+  };
+  read(warp);
+  float m = -INFINITY;
+  for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
+    const float mp = ld_waited(a.w.ml + slot(p) * 2);
+    weight[p] = mp;
+    sum[p] = ld_waited(a.w.ml + slot(p) * 2 + 1);
+    m = fmaxf(m, mp);
+  }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) sm[warp][D] = m;
-    __syncthreads();
-    m = sm[0][D];
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sm[warp][D] = m;
+  __syncthreads();
+  m = sm[0][D];
 #pragma unroll
-    for (int w = 1; w < kN; ++w) m = fmaxf(m, sm[w][D]);
-    float l = 0.f;
-    for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
-      const float mp = weight[p], lp = sum[p];
-      // (scores that are all NaN leave the maximum -inf and a NaN sum)
-      const float f = mp == -INFINITY ? (isnan(lp) ? 1.f : 0.f) : ex2_sfu(mp - m);
-      weight[p] = f;
-      l += lp * f;
-    }
+  for (int w = 1; w < kN; ++w) m = fmaxf(m, sm[w][D]);
+  float l = 0.f;
+  for (int p = threadIdx.x; p < parts; p += kJoinThreads) {
+    const float mp = weight[p], lp = sum[p];
+    // (scores that are all NaN leave the maximum -inf and a NaN sum)
+    const float f = mp == -INFINITY ? (isnan(lp) ? 1.f : 0.f) : ex2_sfu(mp - m);
+    weight[p] = f;
+    l += lp * f;
+  }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) sm[warp][D + 1] = l;
-    __syncthreads();
-    // a warp adds every eighth part, four in flight
-    float o[kV] = {};
-    for (int p = warp; p < parts; p += 4 * kN) {
-      if (p != warp) read(p);
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) sm[warp][D + 1] = l;
+  __syncthreads();
+  // a warp adds every eighth part, four in flight
+  float o[kV] = {};
+  for (int p = warp; p < parts; p += 4 * kN) {
+    if (p != warp) read(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p + i * kN < parts) {
-          const float f = weight[p + i * kN];
+    for (int i = 0; i < 4; ++i)
+      if (p + i * kN < parts) {
+        const float f = weight[p + i * kN];
 #pragma unroll
-          for (int j = 0; j < kV; ++j) o[j] = f == 0.f ? o[j] : fmaf(x[i][j], f, o[j]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kV; ++i) sm[warp][lane * kV + i] = o[i];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float all = 0.f, x = 0.f;
-#pragma unroll
-      for (int w = 0; w < kN; ++w) {
-        all += sm[w][D + 1];
-        x += sm[w][threadIdx.x];
+        for (int j = 0; j < kV; ++j) o[j] = f == 0.f ? o[j] : fmaf(x[i][j], f, o[j]);
       }
-      out[threadIdx.x] = __float2bfloat16_rn(x / all);
+  }
+#pragma unroll
+  for (int i = 0; i < kV; ++i) sm[warp][lane * kV + i] = o[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float all = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kN; ++w) {
+      all += sm[w][D + 1];
+      x += sm[w][threadIdx.x];
     }
-    __syncthreads();
+    out[threadIdx.x] = __float2bfloat16_rn(x / all);
   }
 }
 
 struct Layout {
   size_t cut, ml, o, bytes;
 };
-Layout layout_of(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t d) {
-  const int32_t group = q_heads / kv_heads, parts = (group + kHeads - 1) / kHeads;
-  const size_t items = (size_t)rows * kv_heads * parts, slots = 2 * (size_t)kCtas;
+Layout layout_of(int32_t d) {
+  const size_t slots = 2 * (size_t)kCtas;
   Layout l;
   l.cut = 0;
-  l.ml = align_up(items * sizeof(int2), 256);
+  l.ml = align_up(kCtas * sizeof(int4), 256);
   l.o = l.ml + slots * kHeads * 2 * 4;
   l.bytes = l.o + slots * kHeads * d * 4;
   return l;
@@ -859,7 +891,7 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
   if (!q || !out || layer < 0 || layer >= c.layers || !(scale > 0.f) || scale > 3e38f)
     return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return GDN_ERR_ALIGNMENT;
-  const Layout lay = layout_of(c.rows, q_heads, c.kv_heads, c.d);
+  const Layout lay = layout_of(c.d);
   if (use_ws) {
     if (!ws || ws_bytes < lay.bytes) return GDN_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return GDN_ERR_ALIGNMENT;
@@ -894,7 +926,7 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
     return GDN_ERR_CUDA;
   }
   char* p = (char*)scratch;
-  a.w.cut = (int2*)(p + lay.cut);
+  a.w.cut = (int4*)(p + lay.cut);
   a.w.ml = (float*)(p + lay.ml);
   a.w.o = (float*)(p + lay.o);
   cudaError_t e;
@@ -911,9 +943,8 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
     fp8 ? run(Shape<64, true>{}, decode_kernel<64, true>, on[2])
         : run(Shape<64, false>{}, decode_kernel<64, false>, on[3]);
   if (e == cudaSuccess) {
-    const int64_t jobs = (int64_t)c.rows * q_heads, most = 8 * kSms;
     e = launch(true, c.d == 128 ? join_kernel<128> : join_kernel<64>,
-               dim3((unsigned)(jobs < most ? jobs : most)), kJoinThreads, 0, 0, st, a);
+               dim3(kCtas, (unsigned)(a.group < kHeads ? a.group : kHeads)), kJoinThreads, 0, 0, st, a);
   }
   count_launches(2);
   if (e != cudaSuccess) (void)cudaGetLastError();
@@ -936,7 +967,7 @@ int gdn_attention_decode_step(const void* q, const gdn_kv_cache* cache, int32_t 
 size_t gdn_attention_decode_step_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads,
                                                 int32_t d) {
   if (heads_check(rows, q_heads, kv_heads, d)) return SIZE_MAX;
-  return layout_of(rows, q_heads, kv_heads, d).bytes;
+  return layout_of(d).bytes;
 }
 
 int gdn_attention_decode_step_ws(const void* q, const gdn_kv_cache* cache, int32_t layer,
