@@ -17,7 +17,7 @@
 // came from, and are the A operand of the second product there.
 //
 // 16 query and 4 kv heads of 128: 4 x 8192 tokens 620 us (1774 TFLOP/s), 8192
-// 162 us, 1024 20 us; heads of 64, whose exponentials take as long as their products:
+// 157 us, 1024 14 us; heads of 64, whose exponentials take as long as their products:
 // 2 x 8192 tokens 251 us (1090 TFLOP/s; 258 with the probabilities over the scores).
 // Tried and slower: a pair of CTAs on one tile of keys (979 us where one CTA with one
 // multiplying warp took 736), four warpgroups of exponentials (fewer registers than a
@@ -48,6 +48,7 @@ struct FwdArgs {
   float c;                 // scale log2 e
   float grow;
   int32_t q_heads, per;    // per: queries of a 128-row tile
+  int32_t tiles;           // of a job: 2, or 1 where there are few
   // kListed: the jobs
   const int32_t* count;
   uint32_t* next;
@@ -81,7 +82,7 @@ struct Fwd {
 // 128 rows x 64 columns a half, K-major: 16 columns a step
 __device__ __forceinline__ uint32_t kstep(int s) { return (s >> 2) * kTileBytes + (s & 3) * 32; }
 
-// What every warp derives from a job: two tiles' first queries, their numbers,
+// What every warp derives from a job: its tiles' first queries, their numbers,
 // and the blocks of 128 keys [begin, end) that this CTA goes over.
 struct Place {
   int64_t q0, k0;
@@ -90,7 +91,8 @@ struct Place {
   __device__ __forceinline__ int32_t first_of(int w) const { return w ? first[1] : first[0]; }
   __device__ __forceinline__ int32_t rows_of(int w) const { return w ? rows[1] : rows[0]; }
   __device__ __forceinline__ int32_t blocks_of(int w) const { return w ? blocks[1] : blocks[0]; }
-  __device__ __forceinline__ Place(const Seq& s, int per, int part, int parts) {
+  __device__ __forceinline__ Place(const Seq& s, const FwdArgs& a, int part, int parts) {
+    const int per = a.per;
     q0 = s.q0;
     k0 = s.k0;
     lk = s.lk;
@@ -98,8 +100,8 @@ struct Place {
     int32_t n[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      first[w] = s.tile * 2 * per + w * per;
-      const int32_t left = s.lq - first[w];
+      first[w] = (s.tile * a.tiles + w) * per;
+      const int32_t left = w < a.tiles ? s.lq - first[w] : 0;
       rows[w] = left < 0 ? 0 : left < per ? left : per;
       const int32_t seen = rows[w] ? first[w] + rows[w] + shift : 0;   // keys that the last row sees
       n[w] = seen > 0 ? (seen + kRows - 1) / kRows : 0;
@@ -161,7 +163,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
   bool here = true;
   if constexpr (kMode != kListed) {
     Seq seq;
-    here = locate<kThreads>(sq, blockIdx.x / sq.kv_heads, 2 * a.per, false, true, scratch, a.status, seq);
+    here = locate<kThreads>(sq, blockIdx.x / sq.kv_heads, a.tiles * a.per, false, true, scratch, a.status, seq);
     if (here && tid == 0) {
       slots[0] = seq;
       slot_head[0] = blockIdx.x % sq.kv_heads;
@@ -240,20 +242,20 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
           if (!take(n, seq)) break;
           head = slot_head[0];
         }
-        const Place pl(seq, a.per, part, parts);
+        const Place pl(seq, a, part, parts);
         if (pl.most == 0) continue;
         ok = mbar_wait_warp_cycles(&q_empty, (jobs_done & 1) ^ 1u, kWaitCycles);
         if (!ok) break;
         ++jobs_done;
         if (lead) {
           const uint32_t box = (uint32_t)(a.per * sq.group) * 128 * C::kHalves;
-          mbar_arrive_expect_tx(&q_full, 2 * box);
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
+          const int tiles = pl.rows[1] > 0 ? 2 : 1;
+          mbar_arrive_expect_tx(&q_full, tiles * box);
+          for (int w = 0; w < tiles; ++w)
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
               tma_load_3d(sm + w * C::kTile + h * kTileBytes, &a.q, 64 * h, head * sq.group,
-                          (int32_t)(pl.q0 + pl.first[w]), &q_full);
+                          (int32_t)(pl.q0 + pl.first_of(w)), &q_full);
         }
         for (int32_t j = 0; ok && j < pl.most; ++j) {
 #pragma unroll
@@ -294,7 +296,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       for (uint32_t n = 0; ok && take(n, seq); ++n) {
         int32_t most, blocks, last;      // last: keys of the last block
         {
-          const Place pl(seq, a.per, part, parts);
+          const Place pl(seq, a, part, parts);
           most = pl.most;
           blocks = pl.blocks_of(w);
           const int64_t valid = pl.lk - (int64_t)(pl.begin + most - 1) * kRows;
@@ -399,7 +401,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     for (uint32_t job = 0; ok && take(job, seq); ++job) {
       int32_t n, first, begin;
       {
-        const Place pl(seq, a.per, part, parts);
+        const Place pl(seq, a, part, parts);
         n = pl.blocks_of(w);
         first = pl.first_of(w) + pl.shift;                   // the last key that the first row sees
         begin = pl.begin;
@@ -497,7 +499,7 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       tc_fence_after();
       if (!ok) break;
       const int slot = kMode == kListed ? job & 1 : 0;
-      const Place pl(slots[slot], a.per, part, parts);       // (again: it took registers)
+      const Place pl(slots[slot], a, part, parts);       // (again: it took registers)
       const bool live = qi < pl.rows_of(w);
       const int64_t r = (pl.q0 + pl.first_of(w) + qi) * a.q_heads +
                         (int64_t)slot_head[slot] * sq.group + row % sq.group;
@@ -692,11 +694,25 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
       !heads_map(&a.v, tk ? v : q, tk, s.kv_heads, s.d, tk ? s.v_stride : (int64_t)s.kv_heads * s.d, 1, kRows))
     return GDN_ERR_CUDA;
   // packed: an upper bound, sum_n ceil(len_n / per) <= T / per + N
-  const int64_t per = 2 * a.per;
-  const int64_t tiles = s.packed ? tq / per + s.batch : (s.seqlen_q + per - 1) / per * s.batch;
-  const int64_t jobs = tiles * s.kv_heads, blocks = (s.seqlen_k + kRows - 1) / kRows;
+  auto tiles_of = [&](int64_t per) {
+    return s.packed ? tq / per + s.batch : (s.seqlen_q + per - 1) / per * s.batch;
+  };
+  const int64_t blocks = (s.seqlen_k + kRows - 1) / kRows;
+  // One tile a job or two, whichever takes the longest job less time: a block takes one
+  // tile 1.1 us, two 1.7, a join 3.  (1024 tokens, 16/4 heads of 128: one 14.5 us, two in
+  // two parts 18.5; 2000 tokens, 4/1: 18.8 in two parts, 16.2 in four.)
+  int32_t one_parts, two_parts;
+  const int64_t ones = tiles_of(a.per) * s.kv_heads, twos = tiles_of(2 * a.per) * s.kv_heads;
+  const Mode one = mode_of(ones, blocks, sms, one_parts), two = mode_of(twos, blocks, sms, two_parts);
+  auto takes = [&](int32_t parts, float block) {
+    return (float)((blocks + parts - 1) / parts) * block + (parts > 1 ? 3.f : 0.f);
+  };
+  const bool single = ones <= sms && takes(one_parts, 1.1f) <= takes(two_parts, 1.7f);
+  const Mode mode = single ? one : two;
+  a.tiles = single ? 1 : 2;
+  a.parts = single ? one_parts : two_parts;
+  const int64_t per = (int64_t)a.tiles * a.per, tiles = tiles_of(per), jobs = tiles * s.kv_heads;
   if (jobs > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
-  const Mode mode = mode_of(jobs, blocks, sms, a.parts);
   size_t need = 0, at_jobs = 256, at_ml = 0, at_o = 0;
   if (mode == kListed) need = at_jobs + (size_t)tiles * sizeof(Job);
   if (mode == kParts) {
