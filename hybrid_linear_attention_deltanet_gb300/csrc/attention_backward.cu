@@ -453,7 +453,8 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
     float nl, nd;
     read(0, nl, nd);
     const F2 cc = f2(a.c, a.c);
-    for (int32_t i = 0; i < n; ++i) {
+    int32_t i = 0;
+    for (; i < n; ++i) {
       float* st = stats + 256 * (i & 1);
       if (fetch) {
         st[row] = nl;
@@ -518,6 +519,12 @@ keys_kernel(const __grid_constant__ BwdArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.ds_ready[0]);
     }
+    // A wait of step i ran out: the warp goes on to meet the others of its warpgroup, whose waits
+    // may have ended in time, at the barriers of the steps that are left, or they would wait
+    // for ever.  (They get no further than their next waits, as the products want all warps'
+    // P and dS.  Asking all of them in every step, bar_agree, took 4 % of the ragged batch.)
+    if (!ok)
+      while (++i < n) bar_sync(1 + w, 128);
     if (ok && n > 0) ok = mbar_wait_warp_cycles(&b.done, 0, kWaitCycles);
     tc_fence_after();
     if (ok) {

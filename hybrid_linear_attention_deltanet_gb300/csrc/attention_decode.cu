@@ -421,7 +421,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     for (int64_t i = lo, step; i < hi; i += step, ++k) {
       const int stage = (int)(k % S::kStages);
       ok = mbar_wait_warp_cycles(&full[stage], (uint32_t)((k / S::kStages) & 1), kWaitCycles);
-      if (!ok) break;
+      if (!ok) {
+        // the others meet where their part ends, which is at this tile or behind it
+        attn::bar_agree(2, 32 * kWarps, false);
+        break;
+      }
       const Tile tile = meta[stage];
       uint8_t* bytes = smem + stage * S::kStage;
       const uint32_t base = smem_u32(bytes);
@@ -670,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       }
       // (the stage's other readers are done at the next barrier but one: every warp's own
       // rows of the join lie behind its tokens' bytes only after this one)
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      ok = attn::bar_agree(2, 32 * kWarps, true);
+      if (!ok) break;
       const int h = tile.hh / a.parts, part = tile.hh - h * a.parts;
       const int heads = a.group - part * kHeads < kHeads ? a.group - part * kHeads : kHeads;
       float* js = reinterpret_cast<float*>(bytes);

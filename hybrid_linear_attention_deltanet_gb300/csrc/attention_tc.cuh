@@ -26,6 +26,19 @@ constexpr float kLn2 = 0.693147180559945309f;
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same, true where all of them say so: warps whose waits run out one by one leave together.
+// One that leaves says false at the barrier at which the others, whose waits ended in time,
+// meet next, and they leave there; a barrier without an answer would hold them for ever.
+__device__ __forceinline__ bool bar_agree(int id, int threads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.and.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
 
 // The call's sequences; dense batches are cu == nullptr.
 struct Seqs {

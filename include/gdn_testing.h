@@ -161,6 +161,23 @@ int32_t gdn_testing_last_prefill_form(void);
 int gdn_testing_bounded_wait(int32_t which, int64_t limit_ns, gdn_stream_t stream);
 
 /*
+ * gdn_testing_group_wait -- fault test of warps that meet at barriers between
+ * bounded waits, in the forms of the attention kernels: asks = 0, a barrier
+ * and then a wait in each of `steps` steps (1 .. 1000); asks = 1, a wait in
+ * each and, behind that of every `part`-th step and of the last, a barrier
+ * that asks all whether theirs ended in time.  In step `step` the waits of the
+ * warps whose bits are set in `late` (of 4) run out, after limit_cycles SM
+ * cycles (0 .. 2e9), and they leave.  left[warp] (int32 [4], device) is the
+ * step in which a warp left, or `steps`: with asks = 1 the others leave at the
+ * barrier where they would next have met those, with asks = 0 they end.  The
+ * device status is GDN_ERR_TIMEOUT where a wait ran out.  Returns
+ * GDN_ERR_INVALID_ARG for other arguments.
+ */
+int gdn_testing_group_wait(int32_t asks, uint32_t late, int32_t step, int32_t steps,
+                           int32_t part, int64_t limit_cycles, int32_t* left,
+                           gdn_stream_t stream);
+
+/*
  * gdn_testing_scratch_reserved -- bytes the library's scratch pool on the
  * current device holds mapped right now (cudaMemPoolAttrReservedMemCurrent;
  * 0 when no call has created the pool).  GDN_ERR_INVALID_ARG for a null
