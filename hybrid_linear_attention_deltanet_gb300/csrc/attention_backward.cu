@@ -555,7 +555,10 @@ queries_kernel(const __grid_constant__ BwdArgs a) {
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   Seq seq;
   int head;
-  if (!begin<D>(a, sm, false, seq, head)) return;
+  if (!begin<D>(a, sm, false, seq, head)) {
+    grid_wait();   // as below: with no job at all, the keys' kernel may still read the sequences
+    return;
+  }
   const int32_t group = a.s.group, shift = seq.lk - seq.lq;
   const int32_t used = a.per * group;
   const int32_t first = seq.tile * a.per;                    // the tile's first query

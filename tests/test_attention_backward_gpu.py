@@ -281,3 +281,26 @@ def test_few_rows_keep_the_results_rounding(gdn_lib):
         for (grad, _), name in zip(want, ("dq", "dk", "dv")):
             off = (got[name].double() - grad).norm()
             assert off <= 1.125 * (grad.to(BF16).double() - grad).norm(), (n, name)
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("T,H,kv", [(300, 2, 1), (4096, 16, 16)])      # jobs from the sequences; a list
+def test_malformed_sequences_write_nothing(gdn_lib, T, H, kv, which):
+    """Through the C call, whose results are the caller's; the call behind it finds its scratch and
+    its inputs as they belong."""
+    gdn = gdn_lib
+    d, half = 64, T // 2
+    q, k, v = inputs(T, T, H, kv, d)
+    good = cu([half, T - half])
+    out, lse, dout, want = step(gdn, q, k, v, good)
+    for bad in ([0, T + 1, T], [1, half, T], [0, half, T - 1], [0, -1, T]):
+        wrong = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        got = [torch.full_like(t, 7) for t in (q, k, v)]
+        c = (wrong, good) if which == "q" else (good, wrong)
+        gdn._call("gdn_attention_prefill_backward", q.get_device(), None,
+                  *(t.data_ptr() for t in (q, k, v, out, lse, dout, *c)), d ** -0.5,
+                  *(t.data_ptr() for t in got), 2, T, T, H, kv, d, H * d, kv * d, kv * d)
+        again = gdn.attention_prefill_backward(q, k, v, out, lse, dout, good)
+        assert gdn.device_status() == BAD_SEQLENS
+        assert all((t == 7).all() for t in got)
+        assert all(torch.equal(want[n], again[n]) for n in want)

@@ -55,6 +55,17 @@ def test_a_warp_whose_wait_ran_out_meets_the_others(name, body, behind):
             assert BARRIER.search(body).start() < min(waits) and "continue" not in body
 
 
+def test_every_way_out_waits_for_the_kernel_beside():
+    """The queries' kernel of the gradients starts beside the keys' one, and its end stands for the
+    end of both: whichever way a CTA leaves, it has waited for the grid before."""
+    code = re.sub(r"//[^\n]*", "", KERNELS["queries_kernel"])
+    assert "return;" in code
+    ways = [code[:m.start()] for m in re.finditer(r"\breturn;", code)] + [code.rstrip()[:-1]]
+    for way in ways:
+        last = [x.strip() for x in way.rstrip().rstrip(";").split(";")][-1]
+        assert last.split("{")[-1].strip() == "grid_wait()", way[-120:]
+
+
 @fake_addresses
 def test_the_hook_refuses(lib):  # noqa: F811
     f = hook(lib)
