@@ -1052,8 +1052,9 @@ def attention_prefill(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None, o
 
 def attention_prefill_backward_workspace_size(batch, seqlen, q_heads, kv_heads, d, varlen=False,
                                               seqlen_k=None) -> int:
-    """Bytes of ``attention_prefill_backward``'s workspace for batch sequences of
-    seqlen queries (varlen: seqlen in all) and seqlen_k keys (as many when None)."""
+    """Bytes of ``attention_prefill_backward``'s workspace on the current device for batch
+    sequences of seqlen queries (varlen: seqlen in all) and seqlen_k keys (as many when
+    None).  It serves calls with fewer of each, too."""
     n = load().gdn_attention_prefill_backward_workspace_size(
         batch, seqlen, seqlen if seqlen_k is None else seqlen_k, int(bool(varlen)), q_heads,
         kv_heads, d)

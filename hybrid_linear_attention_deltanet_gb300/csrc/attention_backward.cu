@@ -819,17 +819,18 @@ struct Plan {
   int32_t parts, q_parts;
   size_t stat, key_jobs, query_jobs, part, q_part, bytes;   // statistics, then where the others lie
 };
+constexpr int kLeastSteps = 6, kMostParts = 16;   // steps of a part, parts of a loop
 // Parts of a loop of `iters` steps (about 1.2 us each) for `jobs` of them: as many
 // as minimise the longest's time and that of the parts' sums, of `bytes` each, out
 // and in again (at about 4 TB/s), where that is not less than what the SMs have to do
 // meanwhile anyway.
-int32_t parts_of(int64_t jobs, int64_t iters, int least, int sms, int64_t bytes) {
-  if (jobs == 0 || iters < 2 * least) return 1;
+int32_t parts_of(int64_t jobs, int64_t iters, int sms, int64_t bytes) {
+  if (jobs == 0 || iters < 2 * kLeastSteps) return 1;
   const float sums = (float)jobs * (float)bytes * 2.f / 4e6f, loop = (float)iters * 1.2f;
   const float share = (float)jobs * (float)iters * 0.9f / (float)sms;   // of both kernels, us
   int32_t best = 1;
   float least_time = fmaxf(loop, share);
-  for (int32_t p = 2; p <= 16 && p * least <= iters; ++p) {
+  for (int32_t p = 2; p <= kMostParts && p * kLeastSteps <= iters; ++p) {
     const float t = fmaxf(loop / (float)p, share) + (float)p * sums + 4.f;
     if (t < least_time) {
       least_time = t;
@@ -851,8 +852,8 @@ Plan plan_of(const Shape& s, int sms) {
   const int64_t tile = (int64_t)kRows * s.d * 4;
   // (packed: no sequence is taken to be longer than four average ones)
   const int64_t few = s.packed && s.batch > 4 ? s.batch : 4;
-  p.parts = parts_of(key_jobs, s.packed ? iters * 4 / few : iters, 6, sms, 2 * tile);
-  p.q_parts = parts_of(query_jobs, s.packed ? blocks * 4 / few : blocks, 6, sms, tile);
+  p.parts = parts_of(key_jobs, s.packed ? iters * 4 / few : iters, sms, 2 * tile);
+  p.q_parts = parts_of(query_jobs, s.packed ? blocks * 4 / few : blocks, sms, tile);
   p.stat = align_up(s.rows() * 4, 256);
   p.bytes = 2 * p.stat;
   if (p.listed) {
@@ -865,6 +866,31 @@ Plan plan_of(const Shape& s, int sms) {
   p.q_part = p.bytes;
   if (p.q_parts > 1) p.bytes += (size_t)query_jobs * p.q_parts * tile;
   return p;
+}
+
+// What gdn_attention_prefill_backward_workspace_size answers: at least plan_of()'s bytes of this
+// problem and of every one with no more sequences, queries and keys, so that a workspace for
+// the largest serves all.  (plan_of()'s own are no such bound: one sequence of 8192 tokens, 16/4
+// heads of 128, has enough jobs without parts, one of 4096 needs 33 MB for their sums.)
+// parts_of() makes parts only where a loop is longer than its share of the work, J 0.9 / sms < 1.2
+// for J jobs, and no more of them than bring it below that: J p < 4/3 sms + J < 3 sms.
+size_t workspace_bound(const Shape& s, int sms) {
+  const int32_t per = kRows / (s.q_heads / s.kv_heads);
+  const int64_t tq = s.tq(), tk = s.tk();
+  const int64_t key_tiles = tk ? tk / kRows + s.batch : 0, query_tiles = tq / per + s.batch;
+  const int64_t key_jobs = key_tiles * s.kv_heads, query_jobs = query_tiles * s.kv_heads;
+  size_t bytes = 2 * align_up(s.rows() * 4, 256);
+  if (key_jobs > 2 * sms || query_jobs > 2 * sms)
+    bytes += 256 + align_up((size_t)key_tiles * sizeof(Job), 256) +
+             align_up((size_t)query_tiles * sizeof(Job), 256);
+  auto sums = [&](int64_t jobs, int64_t tokens, int64_t step, int64_t each) {
+    const int64_t most = (tokens + step - 1) / step / kLeastSteps;   // parts of the longest loop
+    if (most < 2) return (int64_t)0;
+    const int64_t parts = jobs * (most < kMostParts ? most : kMostParts);
+    return (parts < 3 * sms ? parts : 3 * sms) * each;
+  };
+  const int64_t tile = (int64_t)kRows * s.d * 4;
+  return bytes + (size_t)sums(key_jobs, tq, per, 2 * tile) + (size_t)sums(query_jobs, tk, kRows, tile);
 }
 
 int backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -1018,7 +1044,7 @@ size_t gdn_attention_prefill_backward_workspace_size(int32_t batch, int64_t seql
                          varlen != 0};
   if (attn::check_shape(s, varlen ? &some : nullptr, varlen ? &some : nullptr, 1.f)) return SIZE_MAX;
   const int sms = hostcheck::sm_count();
-  return s.tq() ? plan_of(s, sms > 0 ? sms : 152).bytes : 0;
+  return s.tq() ? workspace_bound(s, sms > 0 ? sms : 152) : 0;
 }
 
 int gdn_attention_prefill_backward_ws(const void* q, const void* k, const void* v,

@@ -655,10 +655,12 @@ int gdn_attention_prefill(const void* q, const void* k, const void* v, const int
  * fixed.  What is not finite reaches, besides the gradients that it belongs
  * to, those of its own sequence whose 128-row tiles meet its tile.  No output
  * may overlap an input or another output.  Scratch (8 bytes
- * a token and query head, 32 bytes a tile, up to 192 MB of partial sums where
+ * a token and query head, 32 bytes a tile, up to 90 MB of partial sums where
  * there are few long tiles) from the library's pool, or a caller's 256-byte
  * aligned workspace of at least gdn_attention_prefill_backward_workspace_size
- * bytes (rules as gdn_prefill_ws).
+ * bytes (rules as gdn_prefill_ws).  That size is the current device's; it is
+ * enough for all calls with the same heads and d, dense or packed as asked,
+ * that have no more sequences, queries (seqlen_q) and keys (seqlen_k).
  */
 int gdn_attention_prefill_backward(const void* q, const void* k, const void* v, const void* out,
                                    const float* lse, const void* dout, const int32_t* cu_q,
