@@ -54,7 +54,8 @@ class AttentionLayer:
 
     def prefill_on(self, x, cu_seqlens, cache, start, cu_all, tokens, residual=None):
         """Prompts that go on behind what their rows hold: x are the new tokens, cu_all and
-        tokens the rows' lengths with them."""
+        tokens the rows' lengths with them.  A row whose reservation failed (start -1) attends to
+        zeros in the place of its new tokens; gdn.device_status() tells the caller."""
         q, k, v, res = self.project(x, residual)
         gdn.cache_append(cache, k, v, start, cu_seqlens, self.layer)
         k, v = gdn.cache_gather(cache, cu_all, tokens, self.layer)

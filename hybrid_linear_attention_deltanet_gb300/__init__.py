@@ -1212,7 +1212,8 @@ def cache_gather(cache, cu_seqlens, tokens, layer=0, stream=None):
     """One layer's stored keys and values as :func:`attention_prefill` reads them
     (``gdn_cache_gather``): row r's first cu_seqlens[r+1] - cu_seqlens[r]
     tokens, packed; tokens = cu_seqlens[-1], which stays on the device.
-    Returns (k, v) [tokens, kv_heads, d] bf16."""
+    Returns (k, v) [tokens, kv_heads, d] bf16; zeros for tokens that the row
+    does not hold (its reservation failed; :func:`device_status` then says so)."""
     index, at = _cache(cache)
     if stream is None:
         done = _direct_calls().cache_gather(at, index, cu_seqlens, tokens, layer)

@@ -310,19 +310,23 @@ __global__ void __launch_bounds__(kCopy) gather_kernel(GatherArgs a) {
   const int64_t t = unit >> 32 ? unit / c.kv_heads : (int64_t)((uint32_t)unit / (uint32_t)c.kv_heads);
   const int h = (int)(unit - t * c.kv_heads);
   int64_t row, i;
-  if (!find_row(a.cu, c.rows, t, row, i) || i >= ld_waited(c.lengths + row)) {
+  if (!find_row(a.cu, c.rows, t, row, i)) {
     flag_status(a.status, GDN_ERR_BAD_SEQLENS);
     return;
   }
-  const int64_t at = element_of(c, a.layer, a.page_log2, row, i, h);
-  if (at < 0) {
-    flag_status(a.status, GDN_ERR_BAD_CACHE);
-    return;
+  int64_t at = -1;   // (what the row does not hold becomes zeros: k and v may be new memory)
+  if (i >= ld_waited(c.lengths + row)) {
+    flag_status(a.status, GDN_ERR_BAD_SEQLENS);
+  } else {
+    at = element_of(c, a.layer, a.page_log2, row, i, h);
+    if (at < 0) flag_status(a.status, GDN_ERR_BAD_CACHE);
   }
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     uint4* to = reinterpret_cast<uint4*>((x ? a.v : a.k) + unit * D + l * 16);
-    if constexpr (!kFp8) {
+    if (at < 0) {
+      to[0] = to[1] = make_uint4(0, 0, 0, 0);
+    } else if constexpr (!kFp8) {
       const uint4* from =
           reinterpret_cast<const uint4*>((const __nv_bfloat16*)(x ? c.v : c.k) + at * D + l * 16);
       const uint4 y0 = ld_waited(from), y1 = ld_waited(from + 1);

@@ -737,9 +737,10 @@ int gdn_cache_append(const gdn_kv_cache* cache, int32_t layer, const void* k, co
  *   k, v [tokens, kv_heads, d] bf16, contiguous (8 bits: the codes times their
  *   scales, rounded to bf16)
  *   cu_seqlens [rows + 1] with cu_seqlens[rows] = tokens
- * A token at or behind lengths[row], or outside its cu_seqlens
- * (GDN_ERR_BAD_SEQLENS), or whose page is none (GDN_ERR_BAD_CACHE) is left as it
- * was.  k and v may overlap neither the cache nor each other.
+ * A token at or behind lengths[row] (GDN_ERR_BAD_SEQLENS), as where the row's
+ * reservation failed, or whose page is none (GDN_ERR_BAD_CACHE) becomes zeros;
+ * one outside its cu_seqlens (GDN_ERR_BAD_SEQLENS) is left as it was.  k and v
+ * may overlap neither the cache nor each other.
  */
 int gdn_cache_gather(const gdn_kv_cache* cache, int32_t layer, const int32_t* cu_seqlens,
                      int64_t tokens, void* k, void* v, gdn_stream_t stream);

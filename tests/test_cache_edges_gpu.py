@@ -1,0 +1,55 @@
+"""What the attention cache's calls leave behind where something is wrong: defined contents, and a
+cache that goes on."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF16, FP8 = torch.bfloat16, torch.float8_e4m3fn
+FULL, BAD_SEQLENS, BAD = 8, 6, 9
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cu_of(lens):
+    return ints([sum(lens[:i]) for i in range(len(lens) + 1)])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("d,kv", [(64, 3), (128, 2)])
+def test_gather_of_what_a_row_does_not_hold(gdn_lib, dtype, d, kv):
+    """Zeros, also where the memory held something; what no sequence has is left; the rest arrives."""
+    gdn = gdn_lib
+    lens, more = [20, 3, 0, 17], [0, 40, 0, 1]
+    cache = gdn.kv_cache(1, 6, kv, 4, 4, 16, d, dtype)
+    x = torch.randn(sum(lens), kv, d, device="cuda").to(BF16)
+    gdn.cache_append(cache, x, x, gdn.cache_reserve(cache, ints(lens)), cu_of(lens))
+    start = gdn.cache_reserve(cache, ints(more))           # two pages are left, row 1 wants three
+    assert start.tolist() == [20, -1, 0, 17] and gdn.device_status() == FULL
+    y = torch.randn(sum(more), kv, d, device="cuda").to(BF16)
+    gdn.cache_append(cache, y, y, start, cu_of(more))
+    assert gdn.device_status() == 0
+    full = [a + b for a, b in zip(lens, more)]
+    held = [20, 3, 0, 18]
+    want = gdn.cache_gather(cache, cu_of(held), sum(held))
+    assert gdn.device_status() == 0
+    room = [torch.full((sum(full) + 5, kv, d), 7.0, dtype=BF16, device="cuda") for _ in range(2)]
+    gdn._call("gdn_cache_gather", cache.index, None, cache.address, 0, cu_of(full).data_ptr(),
+              sum(full) + 5, *(t.data_ptr() for t in room))
+    assert gdn.device_status() == BAD_SEQLENS
+    for t, w in zip(room, want):
+        assert (t[sum(full):] == 7).all()                  # behind the last sequence
+        for a, n, b, m in zip(cu_of(full).tolist(), full, cu_of(held).tolist(), held):
+            assert torch.equal(t[a:a + m], w[b:b + m]) and (t[a + m:a + n] == 0).all()
+    # the binding's own results, in memory that has just held something
+    room = [torch.full((sum(full), kv, d), float("nan"), dtype=BF16, device="cuda") for _ in range(2)]
+    del room
+    k, v = gdn.cache_gather(cache, cu_of(full), sum(full))
+    assert gdn.device_status() == BAD_SEQLENS
+    assert (k[23:60] == 0).all() and (v[23:60] == 0).all()
+    cache.table[0, 1] = 6
+    k, v = gdn.cache_gather(cache, cu_of(held), sum(held))
+    assert gdn.device_status() == BAD
+    assert torch.equal(k[:16], want[0][:16]) and torch.equal(v[20:], want[1][20:])
+    assert (k[16:20] == 0).all() and (v[16:20] == 0).all()
