@@ -364,17 +364,18 @@ free_kernel(gdn_kv_cache c, const int32_t* rows, unsigned* status) {
   // of the CTAs that name a row, the first empties it
   if (threadIdx.x == 0) len = atomicExch(c.lengths + r, 0);
   __syncthreads();
-  const int64_t held = ((int64_t)len + c.page - 1) / c.page;
-  if (len < 0 || held > c.max_pages) {
-    if (threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_CACHE);
-    return;
-  }
+  // (entries behind the last page are -1: of a row of bad length all are gone through, or the
+  // pages that it holds would never be free again)
+  const int64_t pages = ((int64_t)len + c.page - 1) / c.page;
+  const bool bad = len < 0 || pages > c.max_pages;
+  const int64_t held = bad ? c.max_pages : pages;
+  if (bad && threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_CACHE);
   for (int64_t i = threadIdx.x; i < held; i += blockDim.x) {
     int32_t* e = c.table + (int64_t)r * c.max_pages + i;
     const int32_t p = *e;
     *e = -1;
     if (p >= 0 && p < c.pages) atomicSub(c.refs + p, 1);
-    else flag_status(status, GDN_ERR_BAD_CACHE);
+    else if (!bad) flag_status(status, GDN_ERR_BAD_CACHE);
   }
 }
 

@@ -749,7 +749,8 @@ int gdn_cache_gather(const gdn_kv_cache* cache, int32_t layer, const int32_t* cu
  * gdn_cache_free -- empties rows[0 .. n): their pages lose a reference, their
  * table entries become -1, their lengths 0.  A row named twice is emptied
  * once; an empty row stays so; a number outside [0, cache rows) is skipped
- * (GDN_ERR_BAD_CACHE).
+ * (GDN_ERR_BAD_CACHE).  A row whose length is out of range gives back every
+ * page that its table names (GDN_ERR_BAD_CACHE).
  */
 int gdn_cache_free(const gdn_kv_cache* cache, const int32_t* rows, int32_t n,
                    gdn_stream_t stream);

@@ -53,3 +53,25 @@ def test_gather_of_what_a_row_does_not_hold(gdn_lib, dtype, d, kv):
     assert gdn.device_status() == BAD
     assert torch.equal(k[:16], want[0][:16]) and torch.equal(v[20:], want[1][20:])
     assert (k[16:20] == 0).all() and (v[16:20] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [-1, -(2 ** 31), 65, 2 ** 31 - 1])
+def test_freeing_a_row_of_bad_length_gives_its_pages_back(gdn_lib, bad):
+    """Once, however often it is named; pages that another row shares lose one reference; the pool
+    serves the next rows as if the length had been right."""
+    gdn = gdn_lib
+    cache = gdn.kv_cache(1, 9, 1, 4, 4, 16, 64)
+    gdn.cache_reserve(cache, ints([50, 17, 0, 0]))
+    gdn.cache_fork(cache, ints([0]), ints([2]))            # three pages shared, a fourth of its own
+    assert cache.refs.tolist() == [2, 2, 2, 1, 1, 1, 1, 0, 0] and gdn.device_status() == 0
+    cache.lengths[0] = bad
+    gdn.cache_free(cache, ints([0, 3, 0, 0]))
+    assert gdn.device_status() == BAD
+    assert cache.lengths.tolist() == [0, 17, 50, 0]
+    assert (cache.table[0] == -1).all()
+    assert cache.refs.tolist() == [1, 1, 1, 0, 1, 1, 1, 0, 0]
+    gdn.cache_free(cache, ints([0, 2]))
+    assert gdn.device_status() == 0
+    assert cache.refs.tolist() == [0, 0, 0, 0, 1, 1, 0, 0, 0]
+    assert gdn.cache_reserve(cache, ints([64, 0, 0, 0])).tolist() == [0, 17, 0, 0]
+    assert cache.table[0].tolist() == [0, 1, 2, 3] and gdn.device_status() == 0
