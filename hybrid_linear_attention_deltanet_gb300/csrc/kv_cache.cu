@@ -400,14 +400,15 @@ __device__ __forceinline__ void copy_vectors(const uint4* src, uint4* dst, int64
 }
 
 // --------------------------------------------------------------- forking
-constexpr int32_t kNoSource = -3;
+constexpr int32_t kSkip = -1, kNoSource = -3;
 struct Pair {
   int32_t len, page, old;   // tokens of the row (negative: the pair is skipped), the new page and the one
                             // that it copies, or -1
 };
 
-// Which pairs are valid is decided by marking dst's length (0) with i - n < 0:
-// the smallest pair wins whatever the order.  The second kernel's CTAs copy.
+// The rows' lengths are read before any is changed.  Which of the pairs that name a dst is
+// valid is decided by marking its length (0) with i - n < 0: the smallest pair wins whatever
+// the order.  The second kernel's CTAs copy.
 __global__ void __launch_bounds__(kPlan)
 fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t n, Pair* plan,
                  int32_t* list, unsigned* status) {
@@ -416,30 +417,35 @@ fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t
   grid_release_next();
   grid_wait();
   const int4 near = counts_at(c.refs, c.pages, 4 * (int64_t)threadIdx.x);
-  for (int i = threadIdx.x; i < n; i += kPlan) {
+  // a pair's tokens: kSkip where a number is out of range or dst not empty, kNoSource where
+  // src's length is bad
+  auto read = [&](int i) {
     const int32_t s = src[i], d = dst[i];
-    const bool in = s >= 0 && s < c.rows && d >= 0 && d < c.rows;
-    // (others mark at the same time: their marks are negative)
-    if (in && __ldcg(c.lengths + d) <= 0) atomicMin(c.lengths + d, i - n);
+    if (s < 0 || s >= c.rows || d < 0 || d >= c.rows || c.lengths[d] != 0) return kSkip;
+    const int32_t t = c.lengths[s];
+    return t < 0 || t > c.max_pages * c.page ? kNoSource : t;
+  };
+  const bool one = n <= kPlan;   // then what a thread finds is kept in registers
+  int32_t own = kSkip;
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    own = read(i);
+    if (!one) plan[i].len = own;
   }
   __syncthreads();
-  // a pair's tokens, -1 where it is skipped, kNoSource where it has marked dst all the
-  // same; and the page that it copies, or -1
+  for (int i = threadIdx.x; i < n; i += kPlan)
+    if ((one ? own : plan[i].len) != kSkip) atomicMin(c.lengths + dst[i], i - n);
+  __syncthreads();
+  // the same, kSkip where an earlier pair names dst; and the page that it copies, or -1
   auto tokens = [&](int i, int32_t& old) {
     old = -1;
-    if (i >= n) return -1;
-    const int32_t s = src[i], d = dst[i];
-    if (s < 0 || s >= c.rows || d < 0 || d >= c.rows) return -1;
-    const int32_t mark = __ldcg(c.lengths + d), t = __ldcg(c.lengths + s);
-    if (mark != i - n) return -1;
-    if (t > c.max_pages * c.page) return kNoSource;
-    if (t <= 0) return 0;
-    if (t % c.page) old = c.table[(int64_t)s * c.max_pages + t / c.page];
+    if (i >= n) return kSkip;
+    const int32_t t = one ? own : plan[i].len;
+    if (t == kSkip || __ldcg(c.lengths + dst[i]) != i - n) return kSkip;
+    if (t > 0 && t % c.page) old = c.table[(int64_t)src[i] * c.max_pages + t / c.page];
     return t;
   };
   int64_t want = 0, step, at = 0;
   int32_t t = 0, old = -1;
-  const bool one = n <= kPlan;   // then what the first round found is kept
   for (int base = 0; base < n; base += kPlan) {
     t = tokens(base + threadIdx.x, old);
     at = scan(t > 0 && t % c.page != 0, sm, step);
@@ -471,15 +477,13 @@ fork_plan_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, int32_t
     }
     plan[i] = p;
     // the marks become lengths, once no thread reads any more
-    if (one && t != -1) c.lengths[dst[i]] = p.len > 0 ? p.len : 0;
+    if (one && t != kSkip) c.lengths[dst[i]] = p.len > 0 ? p.len : 0;
   }
   if (one) return;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kPlan) {
-    const Pair p = plan[i];
-    const int32_t d = dst[i];
-    if (d >= 0 && d < c.rows && __ldcg(c.lengths + d) == i - n)
-      c.lengths[d] = p.len > 0 ? p.len : 0;
+    const int32_t len = plan[i].len;
+    if (len != kSkip) c.lengths[dst[i]] = len > 0 ? len : 0;
   }
 }
 

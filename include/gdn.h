@@ -761,8 +761,9 @@ int gdn_cache_free(const gdn_kv_cache* cache, const int32_t* rows, int32_t n,
  * gdn_cache_reserve takes them in the order of the pairs, for the tokens on
  * the last page if that is not full; those tokens are copied in every layer.
  * All pairs read the rows as they were before the call.  A pair is skipped,
- * with GDN_ERR_BAD_CACHE, where a number is outside [0, rows), dst[i] is not
- * empty, or an earlier pair names the same dst; with GDN_ERR_CACHE_FULL where
+ * with GDN_ERR_BAD_CACHE, where a number is outside [0, rows), the length of
+ * src[i] is out of range, that of dst[i] is not 0, or an earlier pair names
+ * the same dst; with GDN_ERR_CACHE_FULL where
  * its page, together with those of the pairs before it, is more than the
  * free pages.
  */

@@ -75,3 +75,31 @@ def test_freeing_a_row_of_bad_length_gives_its_pages_back(gdn_lib, bad):
     assert cache.refs.tolist() == [0, 0, 0, 0, 1, 1, 0, 0, 0]
     assert gdn.cache_reserve(cache, ints([64, 0, 0, 0])).tolist() == [0, 17, 0, 0]
     assert cache.table[0].tolist() == [0, 1, 2, 3] and gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [8, 1030])
+@pytest.mark.parametrize("bad", [-1, -3, -8, -(2 ** 31)])
+def test_fork_with_lengths_below_zero(gdn_lib, bad, n):
+    """Of a target: it is not empty, the pair is skipped and the row left as it is.  Of a source:
+    the target stays empty.  Both are flagged, whatever the number of pairs."""
+    gdn = gdn_lib
+    rows = n + 2
+    for which in ("target", "source"):
+        cache = gdn.kv_cache(1, n + 8, 1, rows, 3, 16, 64)
+        gdn.cache_reserve(cache, ints([20, 33] + [0] * n))
+        # (a target whose length is the mark of its own pair, where there is such a pair)
+        at = n + bad if 0 <= n + bad < n else n // 2
+        broken = 2 + at if which == "target" else 1
+        if which == "target":
+            cache.table[broken, 0] = 1                     # (what it still holds)
+        cache.lengths[broken] = bad
+        src = [0 if which == "target" else i % 2 for i in range(n)]
+        gdn.cache_fork(cache, ints(src), ints(list(range(2, rows))))
+        assert gdn.device_status() == BAD
+        lengths, first = cache.lengths.tolist(), cache.table[:, 0].tolist()
+        for i in range(n):
+            skipped = 2 + i == broken or src[i] == 1
+            assert lengths[2 + i] == (bad if 2 + i == broken else 0 if skipped else 20), i
+            assert first[2 + i] == (1 if 2 + i == broken else -1 if skipped else 0), i
+        made = sum(s == 0 for s in src) - (which == "target")
+        assert cache.refs[0] == 1 + made and int(cache.refs.clamp(max=1).sum()) == 5 + made
