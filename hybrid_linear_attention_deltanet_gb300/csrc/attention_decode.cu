@@ -198,6 +198,19 @@ __device__ __forceinline__ void zero_empty_rows(const Args& a, int lane) {
   }
 }
 
+// Zeros in the place of a stage's tokens [from, from + n), by one warp.
+template <typename S, bool kFp8>
+__device__ __forceinline__ void zero_tokens(uint8_t* base, int from, int n, int lane) {
+  for (int half = 0; half < 2 * S::kHalves; ++half) {      // of the keys, then of the values
+    uint4* z = reinterpret_cast<uint4*>(base + half * S::kImage + from * S::kSub);
+    for (int i = lane; i < n * S::kSub / 16; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (kFp8)
+    for (int i = lane; i < 2 * n; i += 32)
+      *reinterpret_cast<float*>(base + S::kScaleAt + (i < n ? 0 : S::kScales) +
+                                (from + (i < n ? i : i - n)) * 4) = 0.f;
+}
+
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ Args a) {
   using S = Shape<D, kFp8>;
@@ -353,10 +366,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       const int stage = (int)(k % S::kStages);
       const Tile now = t;
       const bool first = fresh;
-      if (id < 0 || id >= c.pages) {                         // some page of the pool in its place
-        flag_status(a.status, GDN_ERR_BAD_CACHE);
-        id = 0;
-      }
       const int32_t ids = id;
       fresh = advance();
       step = fresh ? 2 : 1;
@@ -368,20 +377,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       const int copies = (int)((tokens + box - 1) / box);
       const int h = now.hh / a.parts, part = now.hh - h * a.parts;
       uint8_t* base = smem + stage * S::kStage;
-      if (lead) {
+      const int32_t off = (int32_t)(pos & (c.page - 1));     // (pages longer than a tile)
+      auto begin = [&](int from_pages) {
+        if (!lead) return;
         meta[stage] = now;
-        mbar_arrive_expect_tx(&full[stage], copies * box * (2 * S::kRow + (kFp8 ? 8 : 0)) +
+        mbar_arrive_expect_tx(&full[stage], from_pages * box * (2 * S::kRow + (kFp8 ? 8 : 0)) +
                                                 (first ? S::kQBytes : 0));
         if (first)
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
             tma_load_2d(base + S::kQ + x * kHeads * 128, &a.q, 64 * x,
                         now.row * a.q_heads + h * a.group + part * kHeads, &full[stage]);
-      }
-      const int32_t off = (int32_t)(pos & (c.page - 1));     // (pages longer than a tile)
-      for (int x = 0; x < copies; ++x) {
+      };
+      auto copy = [&](int x) {
         const int32_t p = __shfl_sync(0xffffffffu, ids, x);
-        if (!lead) continue;
+        if (!lead) return;
 #pragma unroll
         for (int y = 0; y < S::kHalves; ++y) {
           uint8_t* to = base + y * S::kImage + x * box * S::kSub;
@@ -395,6 +405,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
           tma_load_1d(to, c.k_scale + e, box * 4, &full[stage]);
           tma_load_1d(to + S::kScales, c.v_scale + e, box * 4, &full[stage]);
         }
+      };
+      const bool gone = ids < 0 || ids >= c.pages;
+      if (!__any_sync(0xffffffffu, gone)) {
+        begin(copies);
+        for (int x = 0; x < copies; ++x) copy(x);
+      } else {                                               // zeros in the place of pages that are none
+        const unsigned none = __ballot_sync(0xffffffffu, gone);
+        flag_status(a.status, GDN_ERR_BAD_CACHE);
+        for (int x = 0; x < copies; ++x)
+          if (none >> x & 1u) zero_tokens<S, kFp8>(base, x * box, box, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        begin(copies - __popc(none));
+        for (int x = 0; x < copies; ++x)
+          if (!(none >> x & 1u)) copy(x);
       }
       __syncwarp();
     }

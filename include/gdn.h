@@ -794,10 +794,9 @@ int gdn_cache_compact(const gdn_kv_cache* cache, const gdn_kv_cache* into, gdn_s
  * a fixed order.  Scores, sums and the join are fp32; probabilities enter the
  * second product rounded to bf16 (8-bit cache: times the value's scale and
  * rounded to fp16, in units of a running maximum).
- * A length outside [0, max_pages * page] counts as 0; in the place of a page
- * number outside the pool some page of it is read; both with
- * GDN_ERR_BAD_CACHE.  out may not overlap
- * q or the cache.  Scratch from the library's pool, or a caller's 256-byte
+ * A length outside [0, max_pages * page] counts as 0, the keys and values on a
+ * page whose number is outside the pool as zeros; both with GDN_ERR_BAD_CACHE.
+ * out may not overlap q or the cache.  Scratch from the library's pool, or a caller's 256-byte
  * aligned workspace of at least gdn_attention_decode_step_workspace_size
  * bytes (rules as gdn_prefill_ws).
  */

@@ -103,3 +103,46 @@ def test_fork_with_lengths_below_zero(gdn_lib, bad, n):
             assert first[2 + i] == (1 if 2 + i == broken else -1 if skipped else 0), i
         made = sum(s == 0 for s in src) - (which == "target")
         assert cache.refs[0] == 1 + made and int(cache.refs.clamp(max=1).sum()) == 5 + made
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32), (128, 64), (64, 128), (128, 256)])
+def test_decoding_over_a_page_that_is_none(gdn_lib, dtype, d, page):
+    """Its keys and values are zeros, bit for bit what a page of zeros gives, whatever the pool's
+    pages hold; other rows do not change."""
+    gdn = gdn_lib
+    lens = [5 * page + 3, 40, 3 * page, 1]
+    g = torch.Generator(device="cuda").manual_seed(page)
+    cache = gdn.kv_cache(1, 5 + sum(-(-n // page) for n in lens), 2, 4, 6, page, d, dtype)
+    x = [torch.randn(sum(lens), 2, d, generator=g, device="cuda").to(BF16) for _ in range(2)]
+    gdn.cache_append(cache, *x, gdn.cache_reserve(cache, ints(lens)), cu_of(lens))
+    q = torch.randn(4, 6, d, generator=g, device="cuda").to(BF16)
+    whole = gdn.attention_decode_step(q, cache)
+    pages = cache.k.shape[1]
+    free = int((cache.refs == 0).nonzero()[-1])
+    assert (cache.k[0, free].float() == 0).all() and (cache.v[0, free].float() == 0).all()
+    places = [[(0, 0)], [(0, 5)], [(0, 1), (0, 2), (2, 2)], [(2, i) for i in range(3)], [(3, 0)]]
+    table = cache.table.clone()
+    for at in places:
+        for r, i in at:
+            cache.table[r, i] = free
+        want = gdn.attention_decode_step(q, cache)
+        assert gdn.device_status() == 0
+        for number in (-1, pages, 2 ** 31 - 1, -(2 ** 31)):
+            for r, i in at:
+                cache.table[r, i] = number
+            # what the pages that are none might be taken for
+            pools = [t.view(torch.uint8) for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)
+                     if t is not None]
+            kept = [t.clone() for t in pools]
+            used = set(cache.table.flatten().tolist()) | {free}
+            for t in pools:
+                t[0, [p for p in range(pages) if p not in used]] = 0x7f
+            got = gdn.attention_decode_step(q, cache)
+            assert gdn.device_status() == BAD
+            assert torch.equal(got, want), (at, number)
+            for r in set(range(4)) - {r for r, _ in at}:
+                assert torch.equal(got[r], whole[r])
+            for t, was in zip(pools, kept):
+                t.copy_(was)
+        cache.table.copy_(table)
