@@ -512,10 +512,6 @@ fork_copy_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, const P
     return;
   }
   if (!tail) return;
-  if (old < 0 || old >= c.pages) {
-    if (threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_CACHE);
-    return;
-  }
   const int layer = (blockIdx.y - 1) >> 1;
   const bool values = (blockIdx.y - 1) & 1;
   // the two pages; a head is `page` tokens further than the one before, and its
@@ -526,15 +522,23 @@ fork_copy_kernel(gdn_kv_cache c, const int32_t* src, const int32_t* dst, const P
   const int vecs = c.d * (kFp8 ? 1 : 2) / 16;   // of a token
   uint4* pool = (uint4*)(values ? c.v : c.k);
   const int mine = tail * vecs, whole = c.page * vecs;
-  copy_vectors(pool + a * vecs, pool + b * vecs, (int64_t)c.kv_heads * mine, [&](int64_t x) {
+  auto place = [&](int64_t x) {
     const int h = (int)x / mine;
     return (int64_t)h * whole + (int)x - h * mine;
-  });
+  };
+  const bool none = old < 0 || old >= c.pages;   // then zeros: the new page holds what another row left
+  if (none) {
+    if (threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_CACHE);
+    for (int64_t x = threadIdx.x; x < (int64_t)c.kv_heads * mine; x += kCopy)
+      pool[b * vecs + place(x)] = make_uint4(0, 0, 0, 0);
+  } else {
+    copy_vectors(pool + a * vecs, pool + b * vecs, (int64_t)c.kv_heads * mine, place);
+  }
   if constexpr (kFp8) {
     float* scale = values ? c.v_scale : c.k_scale;
     for (int x = threadIdx.x; x < c.kv_heads * tail; x += kCopy) {
       const int h = x / tail, t = x - h * tail;
-      scale[b + h * c.page + t] = ld_waited(scale + a + h * c.page + t);
+      scale[b + h * c.page + t] = none ? 0.f : ld_waited(scale + a + h * c.page + t);
     }
   }
 }

@@ -765,7 +765,8 @@ int gdn_cache_free(const gdn_kv_cache* cache, const int32_t* rows, int32_t n,
  * src[i] is out of range, that of dst[i] is not 0, or an earlier pair names
  * the same dst; with GDN_ERR_CACHE_FULL where
  * its page, together with those of the pairs before it, is more than the
- * free pages.
+ * free pages.  Tokens of a last page whose number is outside the pool are
+ * zeros in the copy (GDN_ERR_BAD_CACHE).
  */
 int gdn_cache_fork(const gdn_kv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
                    gdn_stream_t stream);

@@ -146,3 +146,25 @@ def test_decoding_over_a_page_that_is_none(gdn_lib, dtype, d, page):
             for t, was in zip(pools, kept):
                 t.copy_(was)
         cache.table.copy_(table)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("number", [-1, 8])
+def test_fork_of_a_last_page_that_is_none(gdn_lib, dtype, number):
+    """The copy's own page holds zeros there, not what its last owner left; nothing else changes."""
+    gdn = gdn_lib
+    cache = gdn.kv_cache(2, 8, 3, 3, 4, 16, 64, dtype)
+    pools = [t.view(torch.uint8) for t in (cache.k, cache.v, cache.k_scale, cache.v_scale) if t is not None]
+    for t in pools:
+        t.random_(0, 100)
+    gdn.cache_reserve(cache, ints([21, 0, 5]))             # pages 0, 1; 2
+    cache.table[0, 1] = number
+    was = [t.clone() for t in pools]
+    gdn.cache_fork(cache, ints([0, 2]), ints([1, 1]))
+    assert gdn.device_status() == BAD
+    assert cache.lengths.tolist() == [21, 21, 5] and cache.table[1].tolist() == [0, 3, -1, -1]
+    assert cache.refs.tolist() == [2, 1, 1, 1, 0, 0, 0, 0]
+    for t, w in zip(pools, was):
+        width = t.shape[3] // 16 if t.dim() == 4 else 1    # (scales: four bytes a token)
+        w[:, 3, :, :5 * width] = 0
+        assert torch.equal(t, w)
