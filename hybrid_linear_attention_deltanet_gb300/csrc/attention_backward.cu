@@ -921,17 +921,24 @@ int backward(const void* q, const void* k, const void* v, const void* out, const
   const Span outs[] = {span_of(dq, io), span_of(dk, kio), span_of(dv, kio),
                        span_of(use_ws ? ws : nullptr, need)};
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
-  if (tq == 0 && tk == 0) return GDN_OK;
-  if (tq == 0)   // keys that no query sees
-    return cudaMemsetAsync(dk, 0, kio, st) == cudaSuccess && cudaMemsetAsync(dv, 0, kio, st) == cudaSuccess
-               ? GDN_OK
-               : GDN_ERR_CUDA;
+  if (tq == 0 && tk == 0 && !s.packed) return GDN_OK;
   BwdArgs a;
   memset(&a, 0, sizeof a);
   a.status = status_ptr();
   if (!a.status || sms < 1) return GDN_ERR_CUDA;
   const int32_t group = s.q_heads / s.kv_heads;
   a.s = {cu_q, cu_k, s.batch, s.seqlen_q, s.seqlen_k, group, s.kv_heads};
+  if (tq == 0) {   // keys that no query sees
+    cudaError_t e;
+    if (s.packed) {
+      e = no_queries(a.s, dk, dv, kio, a.status, st);
+    } else {
+      e = cudaMemsetAsync(dk, 0, kio, st);
+      if (e == cudaSuccess) e = cudaMemsetAsync(dv, 0, kio, st);
+    }
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  }
   a.dq = (__nv_bfloat16*)dq;
   a.dk = (__nv_bfloat16*)dk;
   a.dv = (__nv_bfloat16*)dv;

@@ -674,7 +674,7 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
                       span_of(cu_k, cu_bytes)};
   const Span outs[] = {span_of(out, s.rows() * s.d * 2), span_of(lse, s.rows() * 4)};
   if (any_overlap(ins, outs)) return GDN_ERR_INVALID_ARG;
-  if (tq == 0) return GDN_OK;
+  if (tq == 0 && !s.packed) return GDN_OK;
   FwdArgs a;
   memset(&a, 0, sizeof a);
   a.status = status_ptr();
@@ -682,6 +682,11 @@ int prefill(const void* q, const void* k, const void* v, const int32_t* cu_q, co
   if (!a.status || sms < 1) return GDN_ERR_CUDA;
   const int32_t group = s.q_heads / s.kv_heads;
   a.s = {cu_q, cu_k, s.batch, s.seqlen_q, s.seqlen_k, group, s.kv_heads};
+  if (tq == 0) {
+    const bool done = no_queries(a.s, nullptr, nullptr, 0, a.status, st) == cudaSuccess;
+    if (!done) (void)cudaGetLastError();
+    return done ? GDN_OK : GDN_ERR_CUDA;
+  }
   a.out = (__nv_bfloat16*)out;
   a.lse = lse;
   a.c = scale * kLog2e;

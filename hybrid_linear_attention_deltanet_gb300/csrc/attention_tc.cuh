@@ -174,16 +174,20 @@ struct ListArgs {
   Job* jobs;
   unsigned* status;
 };
+// Are packed sequences malformed?  A thread's share of the answer, `threads` of them in all.
+__device__ __forceinline__ bool malformed(const Seqs& s, int tid, int threads) {
+  bool bad = tid == 0 && (s.cu_q[0] != 0 || s.cu_k[0] != 0 || s.cu_q[s.n] != s.len_q ||
+                          s.cu_k[s.n] != s.len_k);
+  for (int i = tid; i < s.n; i += threads)
+    bad |= s.cu_q[i] < 0 || s.cu_k[i] < 0 || s.cu_q[i + 1] < s.cu_q[i] || s.cu_k[i + 1] < s.cu_k[i];
+  return bad;
+}
 inline __device__ void list_jobs(const ListArgs& a) {
   __shared__ int32_t level[kLevels];
   __shared__ int32_t warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Seqs& s = a.s;
-  bool bad = tid == 0 && s.cu_q && (s.cu_q[0] != 0 || s.cu_k[0] != 0 || s.cu_q[s.n] != s.len_q ||
-                                    s.cu_k[s.n] != s.len_k);
-  if (s.cu_q)
-    for (int i = tid; i < s.n; i += kListThreads)
-      bad |= s.cu_q[i] < 0 || s.cu_k[i] < 0 || s.cu_q[i + 1] < s.cu_q[i] || s.cu_k[i + 1] < s.cu_k[i];
+  const bool bad = s.cu_q && malformed(s, tid, kListThreads);
   for (int i = tid; i < kLevels; i += kListThreads) level[i] = 0;
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
@@ -265,7 +269,29 @@ inline __device__ void list_jobs(const ListArgs& a) {
   }
 }
 
+// Packed sequences without any query: their check, and zeros for the n 16-byte vectors at
+// each of x and y (keys' gradients; n 0 without).
+static __global__ void __launch_bounds__(kListThreads)
+no_queries_kernel(Seqs s, uint4* x, uint4* y, int64_t n, unsigned* status) {
+  grid_release_next();
+  grid_wait();
+  if (__syncthreads_or(malformed(s, threadIdx.x, kListThreads))) {
+    if (threadIdx.x == 0) flag_status(status, GDN_ERR_BAD_SEQLENS);
+    return;
+  }
+  for (int64_t i = (int64_t)blockIdx.x * kListThreads + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * kListThreads)
+    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+}
+
 // ---------------------------------------------------------------- host side
+inline cudaError_t no_queries(const Seqs& s, void* x, void* y, size_t bytes, unsigned* status,
+                              cudaStream_t st) {
+  const int64_t n = (int64_t)(bytes / 16), ctas = (n + kListThreads - 1) / kListThreads;
+  count_launches(1);
+  return launch(true, no_queries_kernel, dim3((unsigned)(ctas < 1 ? 1 : ctas < 256 ? ctas : 256)),
+                kListThreads, 0, 0, st, s, (uint4*)x, (uint4*)y, n, status);
+}
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
