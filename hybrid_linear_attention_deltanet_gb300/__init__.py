@@ -194,11 +194,13 @@ def _direct_calls():
     return _direct
 
 
-def _ws_args(workspace):
-    """(pointer, bytes) of a caller workspace: a uint8 CUDA tensor."""
+def _ws_args(workspace, index):
+    """(pointer, bytes) of a caller workspace: a uint8 tensor on CUDA device `index`."""
     if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 \
             or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous torch.uint8 tensor")
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{index}")
     return ctypes.c_void_p(workspace.data_ptr()), workspace.numel()
 
 
@@ -363,7 +365,7 @@ def _prefill_call(q, k, v, alpha, beta, S0, cu_seqlens, out, S_final, return_fin
             rc = getattr(lib, name)(*args, _stream_handle(stream))
         else:
             name += "_ws"
-            rc = getattr(lib, name)(*args, *_ws_args(workspace), _stream_handle(stream))
+            rc = getattr(lib, name)(*args, *_ws_args(workspace, q.get_device()), _stream_handle(stream))
     if rc != 0:
         raise GDNError(name, rc)
     return out, S_final
@@ -411,7 +413,8 @@ def prefill_backward(q, k, v, alpha, beta, dout, S0=None, dS_final=None, cu_seql
         if workspace is None:
             rc = lib.gdn_prefill_backward(*args, _stream_handle(stream))
         else:
-            rc = lib.gdn_prefill_backward_ws(*args, *_ws_args(workspace), _stream_handle(stream))
+            rc = lib.gdn_prefill_backward_ws(*args, *_ws_args(workspace, q.get_device()),
+                                             _stream_handle(stream))
     if rc != 0:
         raise GDNError("gdn_prefill_backward", rc)
     return g
@@ -730,9 +733,9 @@ def _call(name, index, stream, *args):
         raise GDNError(name, rc)
 
 
-def _ws(workspace):
+def _ws(workspace, index):
     """(address, bytes) of a caller workspace as integers."""
-    p, n = _ws_args(workspace)
+    p, n = _ws_args(workspace, index)
     return p.value, n
 
 
@@ -832,7 +835,7 @@ def residual_norm_backward(dy, s, w, ds=None, eps=1e-5, stream=None, workspace=N
     if workspace is None:
         _call("gdn_residual_norm_backward", index, stream, *args)
     else:
-        _call("gdn_residual_norm_backward_ws", index, stream, *args, *_ws(workspace))
+        _call("gdn_residual_norm_backward_ws", index, stream, *args, *_ws(workspace, index))
     return g
 
 
@@ -959,7 +962,7 @@ def gated_ffn_backward(x, w_gate, w_up, dh, act="silu", stream=None, workspace=N
     if workspace is None:
         _call("gdn_gated_ffn_backward", index, stream, *args)
     else:
-        _call("gdn_gated_ffn_backward_ws", index, stream, *args, *_ws(workspace))
+        _call("gdn_gated_ffn_backward_ws", index, stream, *args, *_ws(workspace, index))
     return g
 
 
@@ -1085,7 +1088,7 @@ def attention_prefill_backward(q, k, v, out, lse, dout, cu_seqlens=None, cu_seql
     if workspace is None:
         _call("gdn_attention_prefill_backward", index, stream, *args)
     else:
-        _call("gdn_attention_prefill_backward_ws", index, stream, *args, *_ws(workspace))
+        _call("gdn_attention_prefill_backward_ws", index, stream, *args, *_ws(workspace, index))
     return g
 
 
@@ -1290,7 +1293,7 @@ def attention_decode_step(q, cache, layer=0, scale=None, out=None, stream=None, 
     if workspace is None:
         _call("gdn_attention_decode_step", index, stream, *args)
     else:
-        _call("gdn_attention_decode_step_ws", index, stream, *args, *_ws(workspace))
+        _call("gdn_attention_decode_step_ws", index, stream, *args, *_ws(workspace, index))
     return out
 
 
