@@ -733,6 +733,13 @@ def _call(name, index, stream, *args):
         raise GDNError(name, rc)
 
 
+def _i32(**sizes):
+    """Refuses what ctypes would cut to 32 bits in silence."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name} {n} is out of range")
+
+
 def _ws(workspace, index):
     """(address, bytes) of a caller workspace as integers."""
     p, n = _ws_args(workspace, index)
@@ -1058,6 +1065,7 @@ def attention_prefill_backward_workspace_size(batch, seqlen, q_heads, kv_heads, 
     """Bytes of ``attention_prefill_backward``'s workspace on the current device for batch
     sequences of seqlen queries (varlen: seqlen in all) and seqlen_k keys (as many when
     None).  It serves calls with fewer of each, too."""
+    _i32(batch=batch, q_heads=q_heads, kv_heads=kv_heads, d=d)
     n = load().gdn_attention_prefill_backward_workspace_size(
         batch, seqlen, seqlen if seqlen_k is None else seqlen_k, int(bool(varlen)), q_heads,
         kv_heads, d)
@@ -1122,6 +1130,8 @@ class KVCache:
         index, eight = k.get_device(), k.dtype == FP8
         if (k_scale is not None) != eight or (v_scale is not None) != eight:
             raise ValueError("k_scale and v_scale go with an 8-bit cache")
+        _i32(layers=layers, pages=pages, kv_heads=kv_heads, page=page, d=d, rows=rows,
+             max_pages=max_pages)
         shapes = dict(k=k.shape, v=k.shape, table=(rows, max_pages), lengths=(rows,),
                       refs=(pages,), k_scale=k.shape[:-1], v_scale=k.shape[:-1])
         given = dict(k=k, v=v, table=table, lengths=lengths, refs=refs, k_scale=k_scale,
@@ -1207,6 +1217,7 @@ def cache_append(cache, k, v, start, cu_seqlens=None, layer=0, stream=None):
         _out(cu_seqlens, "cu_seqlens", (rows + 1,), torch.int32, index)
     elif k.shape[0] != rows:
         raise ValueError(f"k and v must have a token for each of the {rows} rows (or cu_seqlens)")
+    _i32(layer=layer)
     _call("gdn_cache_append", index, stream, at, layer, k.data_ptr(), v.data_ptr(),
           start.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), k.shape[0], ks, vs)
 
@@ -1225,6 +1236,7 @@ def cache_gather(cache, cu_seqlens, tokens, layer=0, stream=None):
     _out(cu_seqlens, "cu_seqlens", (cache.lengths.shape[0] + 1,), torch.int32, index)
     k, v = (torch.empty((tokens, cache.k.shape[2], cache.k.shape[4]), dtype=torch.bfloat16,
                         device=cache.k.device) for _ in range(2))
+    _i32(layer=layer)
     _call("gdn_cache_gather", index, stream, at, layer, cu_seqlens.data_ptr(), tokens, k.data_ptr(),
           v.data_ptr())
     return k, v
@@ -1268,6 +1280,7 @@ def cache_compact(cache, into, stream=None):
 
 
 def attention_decode_step_workspace_size(rows, q_heads, kv_heads, d) -> int:
+    _i32(rows=rows, q_heads=q_heads, kv_heads=kv_heads, d=d)
     n = load().gdn_attention_decode_step_workspace_size(rows, q_heads, kv_heads, d)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("unsupported attention_decode_step arguments")
@@ -1287,6 +1300,7 @@ def attention_decode_step(q, cache, layer=0, scale=None, out=None, stream=None, 
     rows, d = cache.lengths.shape[0], cache.k.shape[4]
     if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d:
         raise ValueError(f"q must be [{rows}, q_heads, {d}]")
+    _i32(layer=layer)
     out = torch.empty_like(q) if out is None else _out(out, "out", q.shape, q.dtype, index)
     args = (q.data_ptr(), at, layer, q.shape[1], d ** -0.5 if scale is None else float(scale),
             out.data_ptr())
