@@ -918,7 +918,7 @@ int decode(const void* q, const gdn_kv_cache* cache, int32_t layer, int32_t q_he
   if (const int rc = heads_check(c.rows, q_heads, c.kv_heads, c.d)) return rc;
   if ((int64_t)c.layers * c.pages > kLongestAxis || (int64_t)c.kv_heads * c.page > kLongestAxis)
     return GDN_ERR_UNSUPPORTED;
-  if (!q || !out || layer < 0 || layer >= c.layers || !(scale > 0.f) || scale > 3e38f)
+  if (!q || !out || layer < 0 || layer >= c.layers || !attn::scale_ok(scale))
     return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return GDN_ERR_ALIGNMENT;
   const Layout lay = layout_of(c.d);

@@ -338,6 +338,9 @@ inline bool heads_map(CUtensorMap* m, const void* x, int64_t rows, int32_t d, ui
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Its product with log2 e is finite too.
+inline bool scale_ok(float scale) { return scale > 0.f && scale <= 0x1p127f; }
+
 // The checks that the prompt kernels share: sizes, strides, alignment.
 struct Shape {
   int32_t batch;
@@ -357,7 +360,7 @@ inline int check_shape(const Shape& s, const int32_t* cu_q, const int32_t* cu_k,
   if (s.batch < 1 || s.seqlen_q < 0 || s.seqlen_k < 0 || s.q_heads < 1 || s.kv_heads < 1)
     return GDN_ERR_INVALID_ARG;
   if ((cu_q == nullptr) != (cu_k == nullptr)) return GDN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || scale > 3e38f) return GDN_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return GDN_ERR_INVALID_ARG;
   if ((s.d != 64 && s.d != 128) || s.q_heads % s.kv_heads || s.q_heads / s.kv_heads > kRows)
     return GDN_ERR_UNSUPPORTED;
   // 32-bit token coordinates, with room for a tile; sequences counted in 32 bits

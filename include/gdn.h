@@ -631,8 +631,8 @@ int gdn_gated_ffn_backward_ws(const void* x, const void* w_gate, const void* w_u
  * probabilities enter the second product rounded to bf16.  A key or value
  * that is not finite reaches, besides the rows that see it, the rows of its
  * own sequence whose 128-key tile holds it.
- * Strides are multiples of 8; tensors 16-byte aligned, lse and cu 4; scale
- * finite and > 0.  out and lse may overlap no input or each other.
+ * Strides are multiples of 8; tensors 16-byte aligned, lse and cu 4;
+ * 0 < scale <= 2^127.  out and lse may overlap no input or each other.
  */
 int gdn_attention_prefill(const void* q, const void* k, const void* v, const int32_t* cu_q,
                           const int32_t* cu_k, float scale, void* out, float* lse, int32_t batch,
