@@ -396,6 +396,13 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     const uint32_t p_at = tmem + lanes + C::kP + C::kPStep * w;
     const int qi = row / sq.group;                         // the row's query in its tile
     const float c = a.c;
+    if (kMode == kParts && part == 0) {
+      // before any wait: the join writes where this says, also when a wait has run out
+      const Place pl(slots[0], a, part, parts);
+      const int64_t r = (pl.q0 + pl.first_of(w) + qi) * a.q_heads + (int64_t)slot_head[0] * sq.group +
+                        row % sq.group;
+      a.dest[(int64_t)blockIdx.x * 256 + 128 * w + row] = qi < pl.rows_of(w) ? r : -1;
+    }
     uint32_t scores = 0, outs = 0;       // blocks of this tile so far, and outputs waited for
     Seq seq;
     for (uint32_t job = 0; ok && take(job, seq); ++job) {
@@ -506,7 +513,6 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
       release(job);
       if constexpr (kMode == kParts) {
         const int64_t at = ((int64_t)blockIdx.x * parts + part) * 256 + 128 * w + row;
-        if (part == 0) a.dest[(int64_t)blockIdx.x * 256 + 128 * w + row] = live ? r : -1;
         if (live) a.ml[at] = make_float2(m, n > 0 ? l : 0.f);
         if (n > 0) {
 #pragma unroll

@@ -66,6 +66,16 @@ def test_every_way_out_waits_for_the_kernel_beside():
         assert last.split("{")[-1].strip() == "grid_wait()", way[-120:]
 
 
+def test_the_join_knows_its_rows_before_any_wait():
+    """The kernel that joins a prompt's parts writes to the rows that the first part names.  They are
+    named before the first wait that could run out, or the join would go by unset memory."""
+    code = re.sub(r"//[^\n]*", "", KERNELS["prefill_kernel"])
+    softmax = code[code.index("setmaxnreg.inc"):]
+    assert len(re.findall(r"a\.dest\[", softmax)) == 1
+    assert softmax.index("a.dest[") < softmax.index("mbar_wait") and softmax.index("a.dest[") < \
+        softmax.index("take(")
+
+
 @fake_addresses
 def test_the_hook_refuses(lib):  # noqa: F811
     f = hook(lib)
