@@ -805,11 +805,13 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ B
   }
 }
 
-// Fewer rows than this: P and dS enter their products as two bf16 terms each.  Their
-// rounding to one is as large as that of the results, which makes the error 1.43 times
-// that (1.47 at most in 200 batches of 700 to 12000 rows); over few rows it can be more
-// than 1.5 times, and there the products are not what takes the time (16/4 heads of 128,
-// 17 tokens behind 1183: 17.4 us with one term, 21.5 with two; 300 tokens 25 and 30).
+// Fewer rows than this: P and dS enter their products as two bf16 terms each, which loses
+// 2^-16 of them, and a gradient carries its own rounding alone.  With one term each of them
+// carries theirs too, as large, together about sqrt(2) times its own (1.39 to 1.43 over 2000
+// tokens; in 200 batches of 700 to 12000 rows 1.49 at most, over fewer rows more, as few
+// terms need not average).  Both are within the bound of one rounding of P and dS; the
+// second terms are two products more in seven, which few rows hide best (16/4 heads of 128, one term
+// and two: 17 tokens behind 1183 17.4 and 21.5 us, 300 tokens, above, 25 and 30, 8192 550 and 750).
 constexpr int64_t kTwoTerms = 4096;
 
 // How a call is launched, and its scratch.

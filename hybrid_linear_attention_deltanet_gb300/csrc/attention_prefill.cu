@@ -33,9 +33,12 @@ using namespace sm100;
 // two warpgroups of softmax; a third with a warp to multiply and one to load
 constexpr int kThreads = 384;
 constexpr uint32_t kTileBytes = 16384;   // 128 rows x 64 columns bf16
-// A row's maximum is replaced where it grows by more than 2^8.  With few rows (below
-// kFewRows) wherever it grows, so that the largest probability is 1, which bf16 holds:
-// over many rows the largest ones' roundings average, over a few they do not.
+// A row's maximum is replaced where it grows by more than 2^8: the probabilities then reach
+// 2^8, and their rounding to bf16, which is relative, has the same bound.  In a call of few
+// rows (below kFewRows) it is replaced wherever it grows, so that the largest probability is
+// 1, which bf16 holds exactly: a result carries 1.25 instead of 1.26 times its own rounding,
+// and that costs nothing there (17 tokens behind 1183 10 us both ways; 300 tokens, above,
+// 8.5 -> 8.8, 8192 156 -> 175).
 constexpr float kGrow = 8.f;
 constexpr int64_t kFewRows = 512;
 constexpr float kLowest = -3.402823466e38f;

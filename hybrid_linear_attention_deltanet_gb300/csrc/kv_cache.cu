@@ -296,7 +296,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half(uint32_t w) {
   return r;
 }
 // The way back, split as the append is: a token's 16 columns of a head a lane.  A code
-// times its scale is rounded once, to bf16.  Bound by HBM: 32 rows of 4096 tokens, 4 kv
+// times its scale is an fp32 product, rounded to bf16.  Bound by HBM: 32 rows of 4096 tokens, 4 kv
 // heads of 128, 80 us (6.7 TB/s), from 8 bits 69 (5.9); one of 1183 tokens 2.9.
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kCopy) gather_kernel(GatherArgs a) {

@@ -628,9 +628,13 @@ int gdn_gated_ffn_backward_ws(const void* x, const void* w_gate, const void* w_u
  * gdn_prefill; where either is malformed nothing is written and the device
  * status is GDN_ERR_BAD_SEQLENS.
  * Scores, the softmax's sums and the sum over keys are fp32; the
- * probabilities enter the second product rounded to bf16.  A key or value
- * that is not finite reaches, besides the rows that see it, the rows of its
- * own sequence whose 128-key tile holds it.
+ * probabilities enter the second product as exp(s_ij - m) rounded to bf16,
+ * where m lags the row's maximum by a factor of 2^8 at most (by none in a call
+ * of fewer than 512 rows T_q * q_heads).  Calls are split by their sizes as a
+ * whole, so a sequence's results may differ in their roundings with what it is
+ * packed with; the same call has the same bits every time.  A key or value that
+ * is not finite reaches, besides the rows that see it, the rows of its own
+ * sequence whose 128-key tile holds it.
  * Strides are multiples of 8; tensors 16-byte aligned, lse and cu 4;
  * 0 < scale <= 2^127.  out and lse may overlap no input or each other.
  */
@@ -652,13 +656,14 @@ int gdn_attention_prefill(const void* q, const void* k, const void* v, const int
  * contiguous; q, k, v with strides as above; the rest as above.  P and dS
  * enter the products rounded to bf16 (as two bf16 terms each where there are
  * fewer than 4096 rows T_q * q_heads), all sums are fp32 and their order is
- * fixed.  What is not finite reaches, besides the gradients that it belongs
- * to, those of its own sequence whose 128-row tiles meet its tile.  No output
- * may overlap an input or another output.  Scratch (8 bytes
- * a token and query head, 32 bytes a tile, up to 90 MB of partial sums where
- * there are few long tiles) from the library's pool, or a caller's 256-byte
- * aligned workspace of at least gdn_attention_prefill_backward_workspace_size
- * bytes (rules as gdn_prefill_ws).  That size is the current device's; it is
+ * fixed for a call's sizes (so a sequence's gradients may differ in their
+ * roundings with what it is packed with).  What is not finite reaches, besides
+ * the gradients that it belongs to, those of its own sequence whose 128-row
+ * tiles meet its tile.  No output may overlap an input or another output.
+ * Scratch (8 bytes a token and query head, 32 bytes a tile, up to 90 MB of
+ * partial sums where there are few long tiles) from the library's pool, or a
+ * caller's 256-byte aligned workspace of at least
+ * gdn_attention_prefill_backward_workspace_size bytes (rules as gdn_prefill_ws).  That size is the current device's; it is
  * enough for all calls with the same heads and d, dense or packed as asked,
  * that have no more sequences, queries (seqlen_q) and keys (seqlen_k).
  */
@@ -792,9 +797,10 @@ int gdn_cache_compact(const gdn_kv_cache* cache, const gdn_kv_cache* into, gdn_s
  *   q, out [rows, q_heads, d] bf16, contiguous; an empty row's out is 0
  * The rows' lengths are read on the device; the work is cut into equal parts
  * over all rows and heads whatever they are, and parts of a row are joined in
- * a fixed order.  Scores, sums and the join are fp32; probabilities enter the
- * second product rounded to bf16 (8-bit cache: times the value's scale and
- * rounded to fp16, in units of a running maximum).
+ * a fixed order (where a row is cut, and so how its sum is rounded, depends on
+ * the other rows' lengths).  Scores, sums and the join are fp32; probabilities
+ * enter the second product rounded to bf16 (8-bit cache: times the value's
+ * scale and rounded to fp16, in units of a running maximum).
  * A length outside [0, max_pages * page] counts as 0, the keys and values on a
  * page whose number is outside the pool as zeros; both with GDN_ERR_BAD_CACHE.
  * out may not overlap q or the cache.  Scratch from the library's pool, or a caller's 256-byte
