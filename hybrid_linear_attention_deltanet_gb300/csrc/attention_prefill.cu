@@ -161,6 +161,9 @@ prefill_kernel(const __grid_constant__ FwdArgs a) {
     prefetch_tensormap(&a.k);
     prefetch_tensormap(&a.v);
   }
+  // (behind the allocation: a dependent that took this SM's columns first would wait for this
+  // grid's end, and this grid for the columns)
+  __syncthreads();
   grid_release_next();
   grid_wait();
   bool here = true;

@@ -76,6 +76,21 @@ def test_the_join_knows_its_rows_before_any_wait():
         softmax.index("take(")
 
 
+ALLOCATING = [(name, code) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))
+              for name, code in kernels(open(os.path.join(CSRC, f)).read())
+              if "tmem_alloc" in code and "grid_release_next()" in code]
+
+
+def test_dependents_start_behind_the_allocation_of_tensor_memory():
+    """A dependent may take an SM's tensor memory and then wait for this grid's end, so no kernel lets
+    it start before all of its own CTA's columns are there."""
+    assert {n for n, _ in ALLOCATING} >= {"prefill_kernel", "pair_gemm_kernel", "split_gemm_kernel"}
+    for name, code in ALLOCATING:
+        code = re.sub(r"//[^\n]*", "", code)
+        at, release = code.index("tmem_alloc"), code.index("grid_release_next()")
+        assert "__syncthreads();" in code[at:release], name
+
+
 @fake_addresses
 def test_the_hook_refuses(lib):  # noqa: F811
     f = hook(lib)
