@@ -16,8 +16,9 @@
 // P and dS go back to tensor memory as bf16, over the scores that they came
 // from, and are the A operand there.
 //
-// 16 query and 4 kv heads of 128: 2 x 8192 tokens 1125 us (580 and 509 in the two
-// kernels), 8192 550, 4096 179; heads of 64: 2 x 8192 864.  What holds the products
+// 16 query and 4 kv heads of 128: 2 x 8192 tokens 1195 to 1213 us call after call (at the
+// 1400 W limit), 1105 to 1135 in a run too short for that limit (580 and 509 in the two kernels); in
+// such runs 8192 550, 4096 179; heads of 64: 2 x 8192 874.  What holds the products
 // back is shared memory: S and dP read two operands of 4 KB per 64 cycles, all that
 // it gives, the tiles come in through it, and so do the keys' kernel's statistics.
 // Tried and slower (8192 tokens): in the queries' kernel dP(j + 1) as soon as dP(j) is in

@@ -16,8 +16,8 @@
 // several CTAs is joined from their partial sums by a second kernel, in the order
 // of the CTAs.
 //
-// 16 query and 4 kv heads of 128: 256 rows of up to 8192 tokens 306 us (6.9 TB/s), in
-// 8 bits 194 (5.6; widening the codes); of up to 512 tokens 32 and 29; one row of 32768
+// 16 query and 4 kv heads of 128: 256 rows of up to 8192 tokens 314 us (6.7 TB/s), in
+// 8 bits 195 (5.6; widening the codes); of up to 512 tokens 33 and 29; one row of 32768
 // tokens in 8 bits 17 us, of which the bytes are 5.  Heads of 64 in 8 bits: 3.8 TB/s, a
 // tile's 128 tokens of 64 bytes being too little for the steps that follow one another
 // in it.  Tiles of 64 tokens in 8 bits: 18.9 us for the one row, 9 % more for 256.

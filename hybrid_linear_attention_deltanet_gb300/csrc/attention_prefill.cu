@@ -16,9 +16,10 @@
 // The probabilities go back to tensor memory as bf16, over the scores that they
 // came from, and are the A operand of the second product there.
 //
-// 16 query and 4 kv heads of 128: 4 x 8192 tokens 620 us (1774 TFLOP/s), 8192
-// 157 us, 1024 14 us; heads of 64, whose exponentials take as long as their products:
-// 2 x 8192 tokens 251 us (1090 TFLOP/s; 258 with the probabilities over the scores).
+// 16 query and 4 kv heads of 128: 4 x 8192 tokens 690 us call after call (1594 TFLOP/s, at the
+// 1400 W limit), 600 to 625 in a run too short for that limit; in such runs 8192 156, 1024 14;
+// heads of 64, whose exponentials take as long as their products: 2 x 8192 tokens 245 to 274
+// (258 where 251 is now with the probabilities over the scores).
 // Tried and slower: a pair of CTAs on one tile of keys (979 us where one CTA with one
 // multiplying warp took 736), four warpgroups of exponentials (fewer registers than a
 // row's scores).

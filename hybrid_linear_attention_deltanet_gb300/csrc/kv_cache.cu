@@ -13,8 +13,8 @@
 // Copies are split over the GPU, 64 KB a CTA, 16 bytes a lane; they are bound by HBM.
 //
 // (free, reserve and append of 4 prompts of up to 8192 tokens into 8 bits, 4 kv heads of
-// 128: 12.9 us, of which 7 are the append's 37 MB; 256 tokens' append 2.7; free and fork
-// of 3 rows 10.5, of 72 16.5, 7 layers; compacting 256 pages of 8 bits 8.6, 922 pages of
+// 128: 12.4 us, of which 7 are the append's 37 MB; 256 tokens' append 2.6; free and fork
+// of 3 rows 11.2, of 72 16.3, 7 layers; compacting 256 pages of 8 bits 8.5, 922 pages of
 // 7 layers 245.)
 #include <cuda_fp16.h>
 
