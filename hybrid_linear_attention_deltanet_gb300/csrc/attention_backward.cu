@@ -811,8 +811,8 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ B
 // carries theirs too, as large, together about sqrt(2) times its own (1.39 to 1.43 over 2000
 // tokens; in 200 batches of 700 to 12000 rows 1.49 at most, over fewer rows more, as few
 // terms need not average).  Both are within the bound of one rounding of P and dS; the
-// second terms are two products more in seven, which few rows hide best (16/4 heads of 128, one term
-// and two: 17 tokens behind 1183 17.4 and 21.5 us, 300 tokens, above, 25 and 30, 8192 550 and 750).
+// second terms are three products more than seven, which few rows hide best (16/4 heads of 128, one
+// term and two: 17 tokens behind 1183 17.4 and 21.5 us, 300 tokens, above, 25 and 30, 8192 550 and 750).
 constexpr int64_t kTwoTerms = 4096;
 
 // How a call is launched, and its scratch.
